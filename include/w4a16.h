@@ -1,6 +1,8 @@
 /*
  * w4a16.h -- C ABI of libw4a16.so: fp16-activation x int4-weight group-quantized
- * GEMM for NVIDIA GB300 (sm_103a).
+ * GEMM for NVIDIA GB300 (sm_103a), and the operators that stand between one such
+ * GEMM and the next in a decoder layer (paged key-value cache, rotary positions,
+ * attention of one new token, residual norm: second half of this file).
  *
  * Operation (github.com/justinchuby/onnx-genai pull 960, "What's landed" and
  * "Validation": fp16 x int4 MatMulNBits with per-group scales, group sizes
@@ -298,6 +300,191 @@ w4a16_status w4a16_set_wait_limit_ns(unsigned long long limit_ns);
  * Synchronises `stream`. Returns W4A16_OK when no kernel reported an error.
  */
 w4a16_status w4a16_device_error(void *stream);
+
+/* ------------------------------------------------------------------------
+ * Operators between the int4 projections of a decoder layer.
+ *
+ * The conventions above hold (host validation first, no allocation, no
+ * synchronisation, everything enqueued on `stream`), with these of their own:
+ *   - Zero rows (rows, batch or M = 0) is a valid call that enqueues nothing.
+ *   - Strides are counted in elements of the tensor and may be larger than the
+ *     row they step over; the innermost dimension is contiguous. Offsets are
+ *     computed in 64 bits.
+ *   - Values that only the GPU sees (lengths, page numbers, slots) are checked
+ *     by the kernels: one that is out of range is never used as an address, is
+ *     treated as the call's comment says, and leaves W4A16_ERR_INVALID_ARG in
+ *     the device error word (w4a16_device_error), unless that comment gives it
+ *     a status of its own.
+ *   - With w4a16_set_launch_overlap(1) the calls are programmatic dependents of
+ *     the work before them on the stream, as the small-M GEMM is; they read
+ *     nothing before that work has completed, so they have no further rule.
+ *   - Sums, softmax statistics and norms are held in fp32; every output element
+ *     is rounded once, to nearest even.
+ * ------------------------------------------------------------------------ */
+typedef enum {
+    W4A16_TYPE_F16 = 0,
+    W4A16_TYPE_BF16 = 1,
+    W4A16_TYPE_E4M3 = 2,         /* 8-bit float, 4 exponent bits, largest 448 (cache only) */
+    W4A16_TYPE_F32 = 3           /* residual stream only */
+} w4a16_type;
+
+/*
+ * A paged key-value cache. Keys and values are two pools of `pages` pages of
+ * `page_size` tokens of kv_heads x head_dim elements; element d of head h of
+ * token t of page p is at p*page + t*token + h*head + d of its pool, so pages
+ * laid out tokens first, heads first, or both pools in one allocation are all
+ * described by the strides. Slot s is token s % page_size of page s / page_size.
+ *   type      F16, BF16 or E4M3. E4M3 stores e4m3(x / scale[h]) and stands for
+ *             that times scale[h], with one fp32 scale for each kv head
+ *   k_scale, v_scale  device fp32 [kv_heads], E4M3 only; NULL means 1
+ * Rules: pages, page_size, kv_heads > 0; head_dim a multiple of 8 (E4M3: 16), at
+ * most 256; pools 16-byte aligned and strides multiples of 16 bytes.
+ */
+typedef struct {
+    void *k, *v;
+    const float *k_scale, *v_scale;
+    long long k_page, k_token, k_head;
+    long long v_page, v_token, v_head;
+    int type;
+    int pages, page_size, kv_heads, head_dim;
+} w4a16_kv_cache;
+
+/*
+ * Places for a step's new tokens, from the requests' lengths: one call takes
+ * pages from a free list, grows the block table and names every token's slot.
+ *   lens        device [batch]: tokens that each request holds now
+ *   new_tokens  device [batch]: tokens that it gets in this step (0: none);
+ *               negative: the request has ended and gives its pages back
+ *   table       device [batch][max_pages] (rows table_stride apart): entry j of
+ *               request b is the page of its tokens j*page_size...; read and written
+ *   free_pages  device [pool]: the free list, a stack of page numbers, of which
+ *   free_count  device [1]: the first free_count are free
+ * In this order:
+ *   1. ended requests' pages go onto the stack, in the order of (request, j);
+ *   2. the requests are served in their order: one that needs pages gets them
+ *      from the top of the stack if the needs of all requests up to it, itself
+ *      included, can be met; otherwise it is refused (refused[b] = 1). One whose
+ *      tokens do not fit its table row or the slots buffer, or whose length is
+ *      negative, is refused too (refused[b] = 2) and counts as needing none.
+ *      The n-th page handed out is the n-th from the top.
+ * Outputs:
+ *   lens_out    [batch]: the new lengths (0 for ended, unchanged for refused)
+ *   free_count_out [1]
+ *   refused     [batch]: 0, 1 or 2 as above
+ *   slots       int64 [n_slots], positions int32 [n_slots]: the step's tokens,
+ *               request after request, refused ones included: slot and position
+ *               in the request; -1 and 0 for refused requests' tokens and for
+ *               the entries behind the last token
+ * lens_out may be lens and free_count_out may be free_count. Table entries of
+ * ended requests stay as they are. batch <= 8192; free_count is clamped to
+ * [0, pool], and pages given back beyond the pool's size are dropped.
+ */
+w4a16_status w4a16_kv_extend(const int32_t *lens, const int32_t *new_tokens, int32_t *table,
+                             long long table_stride, int batch, int max_pages, int page_size,
+                             int32_t *free_pages, int pool, const int32_t *free_count,
+                             int32_t *lens_out, int32_t *free_count_out, int64_t *slots,
+                             int32_t *positions, int n_slots, int32_t *refused, void *stream);
+
+/*
+ * Host helper: the rot_dim/2 inverse frequencies base^(-2i/rot_dim) in fp32,
+ * scaled for contexts longer than `context`, the one that a model was made for.
+ *   scaling  0 as they are
+ *            1 all divided by factor (positions squeezed)
+ *            2 base * factor^(rot_dim/(rot_dim-2)) in place of base: the lowest
+ *              frequency is divided by factor, the highest stays
+ *            3 by bands: with t = context * f / (2 pi) turns in the context, f stays
+ *              for t >= high, is divided by factor for t <= low, and goes linearly
+ *              in t from one to the other between
+ * rot_dim positive and even (at least 4 for scaling 2), base > 0, factor >= 1,
+ * for scaling 3 context > 0 and high > low. Computed in fp64.
+ */
+w4a16_status w4a16_rope_frequencies(float *inv_freq, int rot_dim, double base, int scaling,
+                                    double factor, double context, double low, double high);
+
+/*
+ * Rotary positions for a step's queries and keys, and its keys and values into
+ * the cache. For each row r and each head of q and k, on the first rot_dim
+ * elements, with x = input + bias and angle = positions[r] * inv_freq[i]:
+ *     (x_a, x_b) -> m * (x_a cos - x_b sin, x_b cos + x_a sin)
+ * interleaved = 0: a = i, b = i + rot_dim/2; interleaved = 1: a = 2i, b = 2i+1.
+ * The other elements of q and k, and v, only get their bias.
+ *   q, k, v   device, `type` (F16 or BF16), [rows][heads or kv_heads][head_dim]
+ *             with row and head strides (the joined QKV projection's output is
+ *             three such views); kv_heads and head_dim are the cache's
+ *   bias      device, `type`, [(heads + 2*kv_heads) * head_dim] in the order q,
+ *             k, v, or NULL
+ *   positions device int32 [rows]; inv_freq device fp32 [rot_dim/2]
+ *   mscale    the m above (1 unless the frequencies are scaled with one)
+ *   q_out     device, `type`, [rows][heads][head_dim], may be q itself
+ *   slots     device int64 [rows]: where k and v go; a negative slot is not
+ *             written, one beyond the cache is an error and not written. Two
+ *             rows with one slot leave either row's values there.
+ * The product of position and frequency is reduced to a part of one turn in
+ * 64-bit fixed point before it is rounded to fp32, so the angle is as exact at
+ * far positions as at near ones.
+ * rot_dim: 0 <= rot_dim <= head_dim, a multiple of 4. Pointers 4-byte aligned,
+ * strides even; 16-byte alignment throughout and rot_dim % 16 == 0 are faster.
+ * The cache's type is `type` or E4M3.
+ */
+w4a16_status w4a16_rope_append(const void *q, const void *k, const void *v, w4a16_type type,
+                               long long q_row, long long q_head, long long k_row, long long k_head,
+                               long long v_row, long long v_head, const void *bias,
+                               const int32_t *positions, const float *inv_freq, int rot_dim,
+                               int interleaved, float mscale, void *q_out, long long qo_row,
+                               long long qo_head, const w4a16_kv_cache *cache, const int64_t *slots,
+                               int rows, int heads, void *stream);
+
+/*
+ * Attention of one new token of each request over its pages:
+ *     s_j = scale * q . K_j,  s_j = softcap * tanh(s_j / softcap) if softcap > 0,
+ *     out = sum_j exp(s_j - m) V_j / sum_j exp(s_j - m),  lse = m + log sum_j exp(s_j - m)
+ * over the tokens j < lens[b] (the new one is already in the cache), and of these
+ * only the last `window` if window > 0. Query head h reads kv head
+ * h / (heads/kv_heads). A request with no token gets out = 0 and lse = -inf.
+ * What the cache holds behind lens[b] is not used, whatever it is.
+ *   q, out    device, `type` (F16 or BF16), [batch][heads][head_dim], 16-byte
+ *             aligned rows and heads; out may be q
+ *   cache     of `type` or E4M3; heads a multiple of its kv_heads
+ *   table     device int32 [batch][max_pages], rows table_stride apart
+ *   lens      device int32 [batch]. A length beyond max_pages*page_size is an
+ *             error and counts as that; a page number out of range is an error,
+ *             and its tokens are left out
+ *   lse       device fp32 [batch][heads], or NULL
+ *   ws        device scratch of w4a16_paged_attention_workspace_bytes(), 256-byte
+ *             aligned. It has to be zero before its first use; every call leaves
+ *             it ready for the next. Calls that can overlap on the GPU need one
+ *             each.
+ */
+size_t w4a16_paged_attention_workspace_bytes(int batch, int heads, int kv_heads, int head_dim);
+w4a16_status w4a16_paged_attention(const void *q, w4a16_type type, long long q_row, long long q_head,
+                                   const w4a16_kv_cache *cache, const int32_t *table,
+                                   long long table_stride, int max_pages, const int32_t *lens,
+                                   int batch, int heads, float scale, int window, float softcap,
+                                   void *out, long long o_row, long long o_head, float *lse, void *ws,
+                                   size_t ws_bytes, void *stream);
+
+/*
+ * A block's output into the residual stream, and the norm that the next block
+ * begins with, in one pass over M rows of K elements:
+ *     t = y,  t = t / sqrt(mean_k t^2 + eps) * post_gamma if post_gamma,
+ *     t = t * gate if gate,
+ *     h_out = h + alpha * t,
+ *     n_out = h_out / sqrt(mean_k h_out^2 + eps) * gamma     (of the unrounded h_out)
+ *   h, h_out  device, h_type (F16, BF16 or F32), rows h_row and ho_row apart;
+ *             h_out may be h
+ *   y, n_out  device, `type` (F16 or BF16); n_out may be y. gamma and n_out are
+ *             both NULL where only the residual stream is wanted
+ *   post_gamma, gamma  device, `type`, [K], or NULL
+ *   gate      device, `type`: [K] for all rows (gate_row = 0) or [M][K] with rows
+ *             gate_row apart; or NULL
+ *   eps       >= 0, finite
+ * K % 8 == 0, K <= 32768; all rows 16-byte aligned.
+ */
+w4a16_status w4a16_residual_rmsnorm(const void *h, w4a16_type h_type, long long h_row, const void *y,
+                                    w4a16_type type, long long y_row, const void *post_gamma,
+                                    const void *gate, long long gate_row, float alpha,
+                                    const void *gamma, float eps, void *h_out, long long ho_row,
+                                    void *n_out, long long no_row, int M, int K, void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,4 +1,5 @@
-"""Python binding of libw4a16.so (fp16 x int4 group-quantized GEMM for GB300).
+"""Python binding of libw4a16.so (fp16 x int4 group-quantized GEMM for GB300, and
+the operators between two such GEMMs of a decoder layer).
 
 Argument marshalling only: every step of the computation runs in the CUDA
 library. PyTorch supplies device memory and the current stream. The functions
@@ -37,6 +38,10 @@ W4A16_SCALE_F16 = 0
 W4A16_SCALE_F32 = 1
 W4A16_PATH_SMALL_M = 0
 W4A16_PATH_TCGEN05 = 1
+W4A16_TYPE_F16 = 0
+W4A16_TYPE_BF16 = 1
+W4A16_TYPE_E4M3 = 2
+W4A16_TYPE_F32 = 3
 
 EXPORTS = (
     "w4a16_status_string", "w4a16_repacked_bytes", "w4a16_repack", "w4a16_unpack_host",
@@ -45,9 +50,12 @@ EXPORTS = (
     "w4a16_device_error", "w4a16_swiglu_static_scratch_bytes", "w4a16_gemm_swiglu_unfused_static",
     "w4a16_set_wait_limit_ns", "w4a16_rmsnorm_workspace_bytes", "w4a16_gemm_rmsnorm",
     "w4a16_gemm_swiglu_rmsnorm", "w4a16_gemm_launch_info", "w4a16_gemm_host_io",
+    "w4a16_kv_extend", "w4a16_rope_frequencies", "w4a16_rope_append",
+    "w4a16_paged_attention_workspace_bytes", "w4a16_paged_attention", "w4a16_residual_rmsnorm",
 )
 
 _vp, _ci, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_ll, _cf, _cd = ctypes.c_longlong, ctypes.c_float, ctypes.c_double
 
 
 class LaunchInfo(ctypes.Structure):
@@ -58,6 +66,45 @@ class LaunchInfo(ctypes.Structure):
     def as_dict(self):
         return {k: getattr(self, k) for k, _ in self._fields_}
 
+
+_TYPES = {torch.float16: W4A16_TYPE_F16, torch.bfloat16: W4A16_TYPE_BF16,
+          torch.float8_e4m3fn: W4A16_TYPE_E4M3, torch.float32: W4A16_TYPE_F32}
+
+
+class KVCache(ctypes.Structure):
+    """w4a16_kv_cache over two pools of pages, CUDA tensors [pages, page_size, kv_heads,
+    head_dim] of float16, bfloat16 or float8_e4m3fn. Any order of the first three
+    dimensions will do (pass a transposed view of pools that are laid out heads first);
+    head_dim is contiguous. k_scale, v_scale: float32 [kv_heads], float8_e4m3fn only.
+    Made once for a cache and passed to every call; holds on to its tensors."""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp),
+                ("k_page", _ll), ("k_token", _ll), ("k_head", _ll),
+                ("v_page", _ll), ("v_token", _ll), ("v_head", _ll),
+                ("type", _ci), ("pages", _ci), ("page_size", _ci), ("kv_heads", _ci), ("head_dim", _ci)]
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k and v are two pools [pages, page_size, kv_heads, head_dim] of one type")
+        if k.dtype not in _TYPES or k.dtype == torch.float32:
+            raise TypeError("a cache is float16, bfloat16 or float8_e4m3fn")
+        if k.stride(3) != 1 or v.stride(3) != 1:
+            raise ValueError("head_dim must be contiguous")
+        for s in (k_scale, v_scale):
+            if s is not None:
+                _expect(s, torch.float32, "k_scale, v_scale")
+                if s.numel() != k.shape[2]:
+                    raise ValueError("one scale for each kv head")
+        super().__init__(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), *k.stride()[:3],
+                         *v.stride()[:3], _TYPES[k.dtype], *k.shape)
+        self.tensors = (k, v, k_scale, v_scale)
+
+
+def _expect(t, dtype, what):
+    if t.dtype is not dtype or not t.is_contiguous():
+        raise TypeError(f"{what}: contiguous {dtype} expected")
+
+
+_kv = ctypes.POINTER(KVCache)
 
 _sig = {
     "w4a16_status_string": (ctypes.c_char_p, [_ci]),
@@ -84,6 +131,16 @@ _sig = {
     "w4a16_swiglu_static_scratch_bytes": (_sz, []),
     "w4a16_gemm_swiglu_unfused_static": (_ci, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _ci, _vp,
                                                _ci, _ci, _ci, _ci, _vp]),
+    "w4a16_kv_extend": (_ci, [_vp, _vp, _vp, _ll, _ci, _ci, _ci, _vp, _ci, _vp, _vp, _vp, _vp, _vp, _ci, _vp,
+                              _vp]),
+    "w4a16_rope_frequencies": (_ci, [_vp, _ci, _cd, _ci, _cd, _cd, _cd, _cd]),
+    "w4a16_rope_append": (_ci, [_vp, _vp, _vp, _ci, _ll, _ll, _ll, _ll, _ll, _ll, _vp, _vp, _vp, _ci, _ci, _cf,
+                                _vp, _ll, _ll, _kv, _vp, _ci, _ci, _vp]),
+    "w4a16_paged_attention_workspace_bytes": (_sz, [_ci, _ci, _ci, _ci]),
+    "w4a16_paged_attention": (_ci, [_vp, _ci, _ll, _ll, _kv, _vp, _ll, _ci, _vp, _ci, _ci, _cf, _ci, _cf, _vp,
+                                    _ll, _ll, _vp, _vp, _sz, _vp]),
+    "w4a16_residual_rmsnorm": (_ci, [_vp, _ci, _ll, _vp, _ci, _ll, _vp, _vp, _ll, _cf, _vp, _cf, _vp, _ll, _vp,
+                                     _ll, _ci, _ci, _vp]),
 }
 for _name, (_res, _args) in _sig.items():
     _f = getattr(lib, _name)
@@ -282,6 +339,149 @@ def w4a16_gemm_swiglu_unfused_static(A, qg_rep, sg, zg, qu_rep, su, zu, group: i
                                                 _stream(stream)),
            "w4a16_gemm_swiglu_unfused_static")
     return out
+
+
+def w4a16_kv_extend(lens, new_tokens, table, free_pages, free_count, page_size: int, slots, positions, refused,
+                    lens_out=None, count_out=None, stream=None):
+    """Places for a step's new tokens: pages taken from (and, where new_tokens is negative,
+    given back to) the free list, the block table grown, a slot and a position for every
+    token. All int32 CUDA tensors but slots (int64); see include/w4a16.h. lens and
+    free_count are updated in place unless lens_out / count_out are given. Returns lens."""
+    lens_out = lens if lens_out is None else lens_out
+    count_out = free_count if count_out is None else count_out
+    batch, max_pages = table.shape
+    for t in (lens, new_tokens, free_pages, free_count, positions, refused, lens_out, count_out):
+        _expect(t, torch.int32, "w4a16_kv_extend")
+    _expect(slots, torch.int64, "slots")
+    n_slots = slots.numel()
+    if (table.dtype is not torch.int32 or (max_pages > 1 and table.stride(1) != 1)
+            or not lens.numel() == new_tokens.numel() == refused.numel() == lens_out.numel() == batch
+            or positions.numel() != n_slots):
+        raise ValueError("w4a16_kv_extend: table is int32 [batch, max_pages], the others have one entry for each "
+                         "request or slot")
+    _check(lib.w4a16_kv_extend(lens.data_ptr(), new_tokens.data_ptr(), table.data_ptr(),
+                               table.stride(0) if batch > 1 else max_pages, batch,
+                               max_pages, page_size, free_pages.data_ptr(), free_pages.numel(),
+                               free_count.data_ptr(), lens_out.data_ptr(), count_out.data_ptr(), slots.data_ptr(),
+                               positions.data_ptr(), n_slots, refused.data_ptr(), _stream(stream)),
+           "w4a16_kv_extend")
+    return lens_out
+
+
+def w4a16_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = 0, factor: float = 1.0,
+                           context: float = 0.0, low: float = 1.0, high: float = 32.0):
+    """The rot_dim/2 inverse frequencies as a CPU float32 tensor; scaling 0..3 as in include/w4a16.h."""
+    out = torch.empty(max(0, rot_dim) // 2, dtype=torch.float32)
+    _check(lib.w4a16_rope_frequencies(out.data_ptr() or None, rot_dim, base, scaling, factor, context, low, high),
+           "w4a16_rope_frequencies")
+    return out
+
+
+def w4a16_rope_append(q, k, v, positions, inv_freq, cache, slots, interleaved: bool = False, mscale: float = 1.0,
+                      bias=None, out=None, stream=None):
+    """Rotary positions for q [rows, heads, D] and k [rows, kv_heads, D] (their first
+    2*len(inv_freq) elements), k and v into the cache at `slots`; returns the turned q.
+    q, k, v may be views of one joined projection; out may be q."""
+    rows, heads, D = q.shape
+    if out is None:
+        out = torch.empty((rows, heads, D), dtype=q.dtype, device=q.device)
+    _expect(positions, torch.int32, "positions")
+    _expect(inv_freq, torch.float32, "inv_freq")
+    _expect(slots, torch.int64, "slots")
+    sq, sk, sv, so = q.stride(), k.stride(), v.stride(), out.stride()
+    if (k.shape != (rows, cache.kv_heads, D) or v.shape != k.shape or out.shape != q.shape or D != cache.head_dim
+            or positions.numel() != rows or slots.numel() != rows or sq[2] != 1 or sk[2] != 1 or sv[2] != 1
+            or so[2] != 1):
+        raise ValueError("w4a16_rope_append: q, out [rows, heads, D], k, v [rows, kv_heads, D], positions and slots "
+                         "[rows], D contiguous and the cache's")
+    if not q.dtype is k.dtype is v.dtype is out.dtype:
+        raise TypeError("w4a16_rope_append: q, k, v and out have one type")
+    if bias is not None:
+        _expect(bias, q.dtype, "bias")
+        if bias.numel() != (heads + 2 * cache.kv_heads) * D:
+            raise ValueError("bias: (heads + 2*kv_heads) * head_dim elements")
+    _check(lib.w4a16_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), _TYPES.get(q.dtype, -1), sq[0], sq[1],
+                                 sk[0], sk[1], sv[0], sv[1], None if bias is None else bias.data_ptr(),
+                                 positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.numel(), int(interleaved),
+                                 mscale, out.data_ptr(), so[0], so[1], cache, slots.data_ptr(), rows, heads,
+                                 _stream(stream)), "w4a16_rope_append")
+    return out
+
+
+def w4a16_paged_attention_workspace_bytes(batch: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib.w4a16_paged_attention_workspace_bytes(batch, heads, kv_heads, head_dim))
+
+
+def w4a16_paged_attention(q, cache, table, lens, scale: Optional[float] = None, window: int = 0,
+                          softcap: float = 0.0, out=None, lse=None, workspace=None, stream=None):
+    """Attention of one new token of each request, q [batch, heads, D], over its pages of
+    the cache (table int32 [batch, max_pages], lens int32 [batch], the new token counted).
+    scale defaults to D ** -0.5; lse (float32 [batch, heads]) is written if given.
+    workspace: w4a16_paged_attention_workspace_bytes() of uint8, zeroed once before its
+    first use and then kept for further calls; made here if it is not given."""
+    batch, heads, D = q.shape
+    max_pages = table.shape[1]
+    if out is None:
+        out = torch.empty((batch, heads, D), dtype=q.dtype, device=q.device)
+    if workspace is None:
+        need = w4a16_paged_attention_workspace_bytes(batch, heads, cache.kv_heads, D)
+        workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
+    _expect(lens, torch.int32, "lens")
+    sq, so = q.stride(), out.stride()
+    if (D != cache.head_dim or table.shape[0] != batch or lens.numel() != batch or out.shape != q.shape
+            or sq[2] != 1 or so[2] != 1 or (max_pages > 1 and table.stride(1) != 1)):
+        raise ValueError("w4a16_paged_attention: q, out [batch, heads, D], table [batch, max_pages], lens [batch], D "
+                         "contiguous and the cache's")
+    if q.dtype is not out.dtype or table.dtype is not torch.int32:
+        raise TypeError("w4a16_paged_attention: q and out have one type, table is int32")
+    if lse is not None:
+        _expect(lse, torch.float32, "lse")
+        if lse.numel() != batch * heads:
+            raise ValueError("lse: [batch, heads]")
+    _check(lib.w4a16_paged_attention(q.data_ptr(), _TYPES.get(q.dtype, -1), sq[0], sq[1], cache, table.data_ptr(),
+                                     table.stride(0) if batch > 1 else max_pages, max_pages, lens.data_ptr(), batch,
+                                     heads, D ** -0.5 if scale is None else scale, window, softcap, out.data_ptr(),
+                                     so[0], so[1], None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), _stream(stream)),
+           "w4a16_paged_attention")
+    return out
+
+
+def w4a16_residual_rmsnorm(h, y, gamma=None, eps: float = 1e-5, post_gamma=None, gate=None, alpha: float = 1.0,
+                           h_out=None, n_out=None, stream=None):
+    """h + alpha * [gate *] [rmsnorm(y; post_gamma) | y], and its rmsnorm with gamma: returns
+    (h_out, n_out), n_out None without gamma. h [M, K] is y's type or float32; gate is [K]
+    or [M, K]; h_out may be h."""
+    M, K = h.shape
+    if h_out is None:
+        h_out = torch.empty((M, K), dtype=h.dtype, device=h.device)
+    if gamma is not None and n_out is None:
+        n_out = torch.empty((M, K), dtype=y.dtype, device=y.device)
+    if (y.shape != h.shape or h_out.shape != h.shape or (n_out is not None and n_out.shape != h.shape)
+            or (gate is not None and gate.shape != h.shape and gate.shape != (K,))):
+        raise ValueError("w4a16_residual_rmsnorm: h, y, h_out, n_out [M, K], gate [K] or [M, K]")
+    if K > 1:
+        for t in (h, y, h_out, n_out, gate):
+            if t is not None and t.stride(-1) != 1:
+                raise ValueError("w4a16_residual_rmsnorm: rows must be contiguous")
+    for t in (gamma, post_gamma):
+        if t is not None:
+            _expect(t, y.dtype, "gamma, post_gamma")
+            if t.numel() != K:
+                raise ValueError("gamma, post_gamma: [K]")
+    if h_out.dtype is not h.dtype or (n_out is not None and n_out.dtype is not y.dtype) or (
+            gate is not None and gate.dtype is not y.dtype):
+        raise TypeError("w4a16_residual_rmsnorm: h_out has h's type, n_out and gate have y's")
+    gate_row = 0 if gate is None or gate.dim() == 1 else gate.stride(0) if M > 1 else K
+    _check(lib.w4a16_residual_rmsnorm(h.data_ptr(), _TYPES.get(h.dtype, -1), h.stride(0) if M > 1 else K,
+                                      y.data_ptr(), _TYPES.get(y.dtype, -1), y.stride(0) if M > 1 else K,
+                                      None if post_gamma is None else post_gamma.data_ptr(),
+                                      None if gate is None else gate.data_ptr(), gate_row, alpha,
+                                      None if gamma is None else gamma.data_ptr(), eps, h_out.data_ptr(),
+                                      h_out.stride(0) if M > 1 else K, None if n_out is None else n_out.data_ptr(),
+                                      0 if n_out is None else n_out.stride(0) if M > 1 else K, M, K,
+                                      _stream(stream)), "w4a16_residual_rmsnorm")
+    return h_out, n_out
 
 
 def w4a16_set_tuning(smallm_max: int) -> None:

@@ -1,0 +1,149 @@
+// Residual stream and norms between two blocks of a decoder layer:
+//     t = [rms(y) * post_gamma | y] * [gate],  h' = h + alpha * t,  n = rms(h') * gamma
+// with rms(x) = x / sqrt(mean x^2 + eps). Streaming work, bound by HBM: every
+// element of h, y (and a full gate) is read once and every element of h' and n
+// written once; the row between the passes stays in registers.
+#include <cmath>
+
+#include "elem.cuh"
+#include "ptx.cuh"
+#include "w4a16_internal.h"
+
+namespace w4a16 {
+namespace {
+
+struct NormParams {
+    const void *h, *y, *post, *gate, *gamma;
+    void *h_out, *n_out;
+    long long h_row, y_row, gate_row, ho_row, no_row;
+    int K;
+    float alpha, eps;
+};
+
+constexpr int kThreads = 512;
+constexpr int kMaxK = 32768;
+
+// Sum over the CTA, the same in every thread and in the same order on every run.
+__device__ __forceinline__ float cta_sum(float x, float *red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+    __syncthreads();
+    float s = 0.f;
+    for (int w = 0; w < kThreads / 32; ++w) s += red[w];
+    return s;
+}
+
+// One CTA per row; thread t holds the 8-element groups t, t + 512, ...
+template <typename T, typename H, int V>
+__global__ void __launch_bounds__(kThreads) residual_norm_kernel(const NormParams p) {
+    using VT = elem::Vec<T, 8>;
+    using VH = elem::Vec<H, 8>;
+    __shared__ float red[2][kThreads / 32];
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const long long row = blockIdx.x;
+    const int groups = p.K / 8;
+    const T *y = static_cast<const T *>(p.y) + row * p.y_row;
+    const H *h = static_cast<const H *>(p.h) + row * p.h_row;
+    float x[V][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int g = threadIdx.x + v * kThreads;
+        if (g >= groups) break;
+        VT::load(y + 8 * g, x[v]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(x[v][e], x[v][e], ss);
+    }
+    float r = 1.f;
+    if (p.post) r = 1.0f / sqrtf(cta_sum(ss, red[0]) / (float)p.K + p.eps);
+    ss = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int g = threadIdx.x + v * kThreads;
+        if (g >= groups) break;
+        float f[8];
+        if (p.post) {
+            VT::load(static_cast<const T *>(p.post) + 8 * g, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[v][e] *= r * f[e];
+        }
+        if (p.gate) {
+            VT::load(static_cast<const T *>(p.gate) + row * p.gate_row + 8 * g, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[v][e] *= f[e];
+        }
+        VH::load(h + 8 * g, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[v][e] = fmaf(p.alpha, x[v][e], f[e]);
+            ss = fmaf(x[v][e], x[v][e], ss);
+        }
+        VH::store(static_cast<H *>(p.h_out) + row * p.ho_row + 8 * g, x[v]);
+    }
+    if (!p.gamma) return;
+    r = 1.0f / sqrtf(cta_sum(ss, red[1]) / (float)p.K + p.eps);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int g = threadIdx.x + v * kThreads;
+        if (g >= groups) break;
+        float f[8];
+        VT::load(static_cast<const T *>(p.gamma) + 8 * g, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[v][e] *= r * f[e];
+        VT::store(static_cast<T *>(p.n_out) + row * p.no_row + 8 * g, x[v]);
+    }
+}
+
+template <typename T, typename H>
+cudaError_t launch(const NormParams &p, int M, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)M, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = launch_overlap() ? 1 : 0;
+    const int v = (p.K / 8 + kThreads - 1) / kThreads;
+    if (v <= 1) return cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, H, 1>, p);
+    if (v <= 2) return cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, H, 2>, p);
+    if (v <= 4) return cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, H, 4>, p);
+    return cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, H, 8>, p);
+}
+
+}  // namespace
+}  // namespace w4a16
+
+using namespace w4a16;
+
+extern "C" w4a16_status w4a16_residual_rmsnorm(const void *h, w4a16_type h_type, long long h_row, const void *y,
+                                               w4a16_type type, long long y_row, const void *post_gamma,
+                                               const void *gate, long long gate_row, float alpha, const void *gamma,
+                                               float eps, void *h_out, long long ho_row, void *n_out,
+                                               long long no_row, int M, int K, void *stream) {
+    if (M < 0 || K <= 0) return W4A16_ERR_INVALID_ARG;
+    if (type != W4A16_TYPE_F16 && type != W4A16_TYPE_BF16) return W4A16_ERR_INVALID_ARG;
+    if (h_type != type && h_type != W4A16_TYPE_F32)
+        return h_type == W4A16_TYPE_F16 || h_type == W4A16_TYPE_BF16 ? W4A16_ERR_UNSUPPORTED : W4A16_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f) || std::isinf(eps) || std::isnan(alpha)) return W4A16_ERR_INVALID_ARG;
+    if (K % 8 != 0 || K > kMaxK) return W4A16_ERR_UNSUPPORTED;
+    if (M == 0) return W4A16_OK;
+    if ((gamma == nullptr) != (n_out == nullptr)) return W4A16_ERR_INVALID_ARG;
+    if (!h || !y || !h_out) return W4A16_ERR_INVALID_ARG;
+    const int hv = h_type == W4A16_TYPE_F32 ? 4 : 8;  // elements of 16 bytes
+    for (const void *p : {h, y, (const void *)h_out, (const void *)n_out, post_gamma, gate, gamma})
+        if (!aligned(p, 16)) return W4A16_ERR_INVALID_ARG;
+    if (M > 1 && (h_row < K || ho_row < K || y_row < K || (n_out && no_row < K) || (gate && gate_row && gate_row < K)))
+        return W4A16_ERR_INVALID_ARG;
+    if (h_row % hv || ho_row % hv || y_row % 8 || (n_out && no_row % 8) || (gate && gate_row % 8))
+        return W4A16_ERR_INVALID_ARG;
+    NormParams p{h, y, post_gamma, gate, gamma, h_out, n_out, h_row, y_row, gate_row, ho_row, no_row, K, alpha, eps};
+    cudaStream_t s = (cudaStream_t)stream;
+    if (type == W4A16_TYPE_F16)
+        return from_cuda(h_type == W4A16_TYPE_F32 ? launch<__half, float>(p, M, s) : launch<__half, __half>(p, M, s));
+    return from_cuda(h_type == W4A16_TYPE_F32 ? launch<__nv_bfloat16, float>(p, M, s)
+                                              : launch<__nv_bfloat16, __nv_bfloat16>(p, M, s));
+}

@@ -19,14 +19,14 @@ unsigned long long g_wait_ns = 2000000000ull;  // limit of every bounded device-
 
 __device__ unsigned int g_device_error;  // set by bounded waits that expire
 
-bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
 // Per-device caches below are filled on first use under this lock, so that
 // concurrent first calls from several host threads are well defined.
 std::mutex g_cache_mu;
 
+}  // namespace
+
 // Device address of the error word on the current device (looked up once per device).
-unsigned int *device_error_ptr() {
+unsigned int *w4a16::device_error_ptr() {
     static unsigned int *cached[64] = {nullptr};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
@@ -39,7 +39,7 @@ unsigned int *device_error_ptr() {
     return cached[dev];
 }
 
-}  // namespace
+bool w4a16::launch_overlap() { return g_launch_overlap != 0; }
 
 cudaError_t w4a16::ensure_max_dyn_smem(const void *func, int bytes) {
     static std::set<std::pair<const void *, int>> done;
@@ -132,8 +132,6 @@ w4a16_status make_plan(int M, int N, int K, int group, int split_k, bool swiglu,
     *out = p;
     return W4A16_OK;
 }
-
-w4a16_status from_cuda(cudaError_t e) { return e == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA; }
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
