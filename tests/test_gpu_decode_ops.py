@@ -51,7 +51,8 @@ def within(got, want, bound, label):
     both = np.isfinite(want)
     assert np.array_equal(got[~both], want[~both], equal_nan=True), label
     off = np.abs(got[both] - want[both]) - np.broadcast_to(bound, want.shape)[both]
-    assert off.size == 0 or off.max() <= 0, f"{label}: {off.max()} over the bound"
+    worst = off.max() if off.size else 0.0
+    assert worst <= 0, f"{label}: {worst} over the bound"
 
 
 # ------------------------------------------------------------------ kv_extend
