@@ -138,46 +138,56 @@ __device__ __forceinline__ long long tiles_of(const Range &r) {
     return r.hi > r.lo ? (r.hi + kTile - 1) / kTile - r.lo / kTile : 0;
 }
 
-// One warp's copies of the slice that begins at token t0 into ring stage `dst`.
-// Returns the mask of its rows that hold visible tokens of valid pages.
+// Where the 16 tokens of a slice are: lane l (and l + 16) knows that of token l. The
+// page number is loaded a slice ahead of its use, so its latency is not waited for.
+struct Places {
+    int page;          // -1: not a visible token
+    unsigned int at;   // the token's place in its page
+};
+__device__ __forceinline__ Places look_up(const Params &p, const int32_t *table, long long t0, const Range &r, int lane) {
+    const long long tok = t0 + (lane & 15);
+    Places x{-1, 0u};
+    if (tok >= r.lo && tok < r.hi) {  // lengths fit 31 bits
+        const unsigned int j = (unsigned int)tok / (unsigned int)p.c.page_size;
+        x.page = __ldg(table + j);
+        x.at = (unsigned int)tok - j * (unsigned int)p.c.page_size;
+    }
+    return x;
+}
+
+// One warp's copies of a slice into ring stage `dst`. Returns the mask of its rows
+// that hold visible tokens of valid pages; the others become zeros.
 template <typename K, typename C>
-__device__ __forceinline__ uint32_t load_slice(const Params &p, const int32_t *table, int kvh, long long t0,
-                                               const Range &r, uint32_t dst, int lane) {
+__device__ __forceinline__ uint32_t load_slice(const Params &p, const Places &x, const Range &r, long long t0, int kvh,
+                                               uint32_t dst, int lane) {
     constexpr int kLanes = K::kChunks < 8 ? K::kChunks : 8;  // lanes on a row
     constexpr int kRowsAt = 32 / kLanes;
     const int chunks = p.c.head_dim * K::kBytes / 16;
     const int sub = lane % kLanes;
-    uint32_t mask = 0;
+    const long long tok = t0 + (lane & 15);
+    const bool good = x.page >= 0 && x.page < p.c.pages;
+    if (!good && tok >= r.lo && tok < r.hi) atomicExch(p.err, (unsigned int)W4A16_ERR_INVALID_ARG);
+    const uint32_t mask = __ballot_sync(0xffffffffu, good) & 0xffffu;
+    const int page_ok = good ? x.page : 0;
+    const C *kh = static_cast<const C *>(p.c.k) + kvh * p.c.k_head + sub * (16 / K::kBytes);
+    const C *vh = static_cast<const C *>(p.c.v) + kvh * p.c.v_head + sub * (16 / K::kBytes);
 #pragma unroll
     for (int i = 0; i < kSlice / kRowsAt; ++i) {
         const int row = i * kRowsAt + lane / kLanes;
-        const long long tok = t0 + row;
-        bool ok = tok >= r.lo && tok < r.hi;
-        long long page = 0, at = 0;
-        if (ok) {
-            const unsigned int j = (unsigned int)tok / (unsigned int)p.c.page_size;  // lengths fit 31 bits
-            page = table[j];
-            at = (unsigned int)tok - j * (unsigned int)p.c.page_size;
-            if (page < 0 || page >= p.c.pages) {
-                atomicExch(p.err, (unsigned int)W4A16_ERR_INVALID_ARG);
-                page = 0;
-                ok = false;
-            }
-        }
-        const C *k = static_cast<const C *>(p.c.k) + page * p.c.k_page + at * p.c.k_token + kvh * p.c.k_head;
-        const C *v = static_cast<const C *>(p.c.v) + page * p.c.v_page + at * p.c.v_token + kvh * p.c.v_head;
+        const bool ok = (mask >> row) & 1u;
+        const long long page = __shfl_sync(0xffffffffu, page_ok, row);
+        const long long at = __shfl_sync(0xffffffffu, x.at, row);
+        const C *k = kh + page * p.c.k_page + at * p.c.k_token;
+        const C *v = vh + page * p.c.v_page + at * p.c.v_token;
 #pragma unroll
         for (int c = 0; c < K::kChunks / kLanes; ++c) {
             const int chunk = c * kLanes + sub;
             if (chunk < chunks) {
                 const uint32_t o = place<K::kChunks>(row, chunk);
-                copy16(dst + o, k + chunk * (16 / K::kBytes), ok);
-                copy16(dst + K::kSliceBytes + o, v + chunk * (16 / K::kBytes), ok);
+                copy16(dst + o, k + c * kLanes * (16 / K::kBytes), ok);
+                copy16(dst + K::kSliceBytes + o, v + c * kLanes * (16 / K::kBytes), ok);
             }
         }
-        const uint32_t votes = __ballot_sync(0xffffffffu, ok);
-#pragma unroll
-        for (int x = 0; x < kRowsAt; ++x) mask |= ((votes >> (x * kLanes)) & 1u) << (i * kRowsAt + x);
     }
     return mask;
 }
@@ -335,11 +345,14 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, 1) paged_atten
 
         // Fill the ring, then one slice out and one in.
         const int fill = min(count, K::kStages - 1);
+        Places ahead = look_up(p, table, tok0, r, lane);
 #pragma unroll 1
         for (int i = 0; i < K::kStages - 1; ++i) {
             if (i < fill) {
-                const uint32_t mask = load_slice<K, C>(p, table, kvh, tok0 + (long long)i * K::kTile, r,
-                                                       ring + i * 2 * K::kSliceBytes, lane);
+                const Places now = ahead;
+                const long long t0 = tok0 + (long long)i * K::kTile;
+                ahead = look_up(p, table, t0 + K::kTile, r, lane);
+                const uint32_t mask = load_slice<K, C>(p, now, r, t0, kvh, ring + i * 2 * K::kSliceBytes, lane);
                 if (lane == 0) masks[warp][i] = mask;
             }
             copies_commit();
@@ -462,8 +475,10 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, 1) paged_atten
             const int next = i + K::kStages - 1;
             if (next < count) {
                 const int to = stage == 0 ? K::kStages - 1 : stage - 1;
-                const uint32_t got = load_slice<K, C>(p, table, kvh, tok0 + (long long)next * K::kTile, r,
-                                                      ring + to * 2 * K::kSliceBytes, lane);
+                const Places now = ahead;
+                const long long t0 = tok0 + (long long)next * K::kTile;
+                ahead = look_up(p, table, t0 + K::kTile, r, lane);
+                const uint32_t got = load_slice<K, C>(p, now, r, t0, kvh, ring + to * 2 * K::kSliceBytes, lane);
                 if (lane == 0) masks[warp][to] = got;
             }
             copies_commit();
