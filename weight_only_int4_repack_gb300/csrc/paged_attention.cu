@@ -6,13 +6,9 @@ using namespace w4a16;
 
 namespace {
 
-// Workspace: a counter for each CTA, then two partial results for each CTA, of the
-// size of the largest (16 heads x 128 + 2, a little more than 8 x 256 + 2), so that one
-// workspace serves calls of every shape.
-constexpr size_t kCounterBytes = 4096;
-constexpr size_t kPartialBytes = 16 * (128 + 2) * 4;
-
-int max_ctas() { return sm_count() < (int)(kCounterBytes / 4) ? sm_count() : (int)(kCounterBytes / 4); }
+// Workspace: the counters, then two partial results for each CTA, of the size of the
+// largest, so that one workspace serves calls of every shape.
+constexpr size_t kCounterBytes = 3 * attn::kMaxCtas * 4;
 
 }  // namespace
 
@@ -20,7 +16,7 @@ extern "C" {
 
 size_t w4a16_paged_attention_workspace_bytes(int batch, int heads, int kv_heads, int head_dim) {
     if (batch <= 0 || heads <= 0 || kv_heads <= 0 || head_dim <= 0 || heads % kv_heads) return 0;
-    return kCounterBytes + (size_t)max_ctas() * 2 * kPartialBytes;
+    return kCounterBytes + (size_t)sm_count() * attn::kPerSm * 2 * attn::kMaxPartial * 4;
 }
 
 w4a16_status w4a16_paged_attention(const void *q, w4a16_type type, long long q_row, long long q_head,
@@ -57,7 +53,7 @@ w4a16_status w4a16_paged_attention(const void *q, w4a16_type type, long long q_r
     p.err = device_error_ptr();
     if (!p.err) return W4A16_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
-    return from_cuda(type == W4A16_TYPE_F16 ? attn::launch_f16(p, max_ctas(), s) : attn::launch_bf16(p, max_ctas(), s));
+    return from_cuda(type == W4A16_TYPE_F16 ? attn::launch_f16(p, sm_count(), s) : attn::launch_bf16(p, sm_count(), s));
 }
 
 }  // extern "C"

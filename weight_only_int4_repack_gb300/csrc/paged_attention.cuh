@@ -3,15 +3,16 @@
 // Bound by HBM: each visible key and value is read once, for all query heads that
 // share it.
 //
-// Work. A tile is kWarps * 16 tokens of one request, kv head and block of 8 * NT
-// query heads. All tiles, request after request and head after head, form one line
+// Work. A tile is kWarps slices of 16 or 32 tokens of one request, kv head and block
+// of 8 * NT query heads. All tiles, request after request and head after head, form one line
 // that is cut into equal parts, one for each CTA, so lengths may differ as they
 // like and a single long request still fills the GPU. What a CTA has of a head's
 // tokens is a segment; a head whose tokens lie in several CTAs leaves one partial
 // result (maximum, sum, unnormalised output) for each, and the CTA that finishes
 // last joins them in the order of the tokens, so results do not depend on timing.
+// Many partial results are joined in two rounds, groups first.
 //
-// A segment. Warp w takes the w-th 16 tokens of each tile and keeps its own running
+// A segment. Warp w takes the w-th slice of each tile and keeps its own running
 // maximum, sum and output; the warps meet once, at the segment's end. Each warp
 // feeds a ring of its own with 16-byte asynchronous copies (no CTA barrier in the
 // loop). Tokens are the rows of the matrix instruction and query heads its columns
@@ -37,14 +38,16 @@ struct Params {
     w4a16_kv_cache c;
     const int32_t *table, *lens;
     float *lse;
-    unsigned int *counters;  // [CTAs], zero between calls
-    float *partial;          // [CTAs][2][rows * (kDim + 2)]
+    unsigned int *counters;  // [3][kMaxCtas], zero between calls
+    float *partial;          // [CTAs][2][kMaxPartial]
     int max_pages, batch, heads, group, head_blocks, window;
     float scale, softcap;
     unsigned int *err;
 };
 
-constexpr int kSlice = 16;  // tokens that a warp takes at a time
+constexpr int kMaxCtas = 1024;
+constexpr int kMaxPartial = 16 * (128 + 4);  // floats of the largest partial result (8 * (256 + 4) is less)
+constexpr int kPerSm = 2;                    // CTAs on an SM: one streams while the other begins or ends a segment
 
 template <typename T, typename C, int DT, int NT>
 struct Config {
@@ -53,17 +56,20 @@ struct Config {
     static constexpr int kBytes = sizeof(C);
     static constexpr int kRowBytes = DT * kBytes;          // a token's keys (or values) in the ring
     static constexpr int kChunks = kRowBytes / 16;
-    static constexpr int kSliceBytes = kSlice * kRowBytes; // keys or values of a slice
-    static constexpr int kWarps = kSliceBytes > 4096 ? 4 : 8;
+    static constexpr int kTok = kRowBytes <= 128 ? 32 : 16;  // tokens of a slice
+    static constexpr int kTiles = kTok / 16;
+    static constexpr int kSliceBytes = kTok * kRowBytes;   // keys or values of a slice
+    static constexpr int kWarps = kSliceBytes > 4096 ? 2 : 4;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kTile = kWarps * kSlice;
-    static constexpr int kStagesFit = 196608 / (kWarps * 2 * kSliceBytes);
+    static constexpr int kTile = kWarps * kTok;
+    static constexpr int kStagesFit = 98304 / (kWarps * 2 * kSliceBytes);
     static constexpr int kStages = kStagesFit > 6 ? 6 : kStagesFit;
     static constexpr int kRing = kStages * 2 * kSliceBytes;  // one warp's
     static constexpr int kMerge = kWarps * kRows * (DT + 2) * 4;
     static constexpr int kSmem = kWarps * kRing > kMerge ? kWarps * kRing : kMerge;
-    static constexpr int kPartial = kRows * (DT + 2);        // floats of a partial result
-    static_assert(kPartial <= 16 * (128 + 2), "the workspace holds partial results of this size");
+    // A partial result: outputs, then maxima and sums, then room for those of a joined group.
+    static constexpr int kPartial = kRows * (DT + 4);
+    static_assert(kPartial <= kMaxPartial, "the workspace holds partial results of this size");
 };
 
 // ------------------------------------------------------------------ instructions
@@ -138,16 +144,18 @@ __device__ __forceinline__ long long tiles_of(const Range &r) {
     return r.hi > r.lo ? (r.hi + kTile - 1) / kTile - r.lo / kTile : 0;
 }
 
-// Where the 16 tokens of a slice are: lane l (and l + 16) knows that of token l. The
-// page number is loaded a slice ahead of its use, so its latency is not waited for.
+// Where a slice's tokens are: lane l knows that of token l (with 16 tokens, so does
+// lane l + 16). The page number is loaded a slice ahead of its use, so that its
+// latency is not waited for.
 struct Places {
     int page;          // -1: not a visible token
     unsigned int at;   // the token's place in its page
 };
-__device__ __forceinline__ Places look_up(const Params &p, const int32_t *table, long long t0, const Range &r, int lane) {
-    const long long tok = t0 + (lane & 15);
+template <int kTok>
+__device__ __forceinline__ Places look_up(const Params &p, const int32_t *table, int t0, int lo, int hi, int lane) {
+    const int tok = t0 + lane % kTok;
     Places x{-1, 0u};
-    if (tok >= r.lo && tok < r.hi) {  // lengths fit 31 bits
+    if (tok >= lo && tok < hi) {
         const unsigned int j = (unsigned int)tok / (unsigned int)p.c.page_size;
         x.page = __ldg(table + j);
         x.at = (unsigned int)tok - j * (unsigned int)p.c.page_size;
@@ -156,48 +164,53 @@ __device__ __forceinline__ Places look_up(const Params &p, const int32_t *table,
 }
 
 // One warp's copies of a slice into ring stage `dst`. Returns the mask of its rows
-// that hold visible tokens of valid pages; the others become zeros.
+// that hold visible tokens of valid pages; the others become zeros. k, v: the lane's
+// 16 bytes of the kv head's first token.
 template <typename K, typename C>
-__device__ __forceinline__ uint32_t load_slice(const Params &p, const Places &x, const Range &r, long long t0, int kvh,
+__device__ __forceinline__ uint32_t load_slice(const Params &p, const Places &x, bool in_range, const C *k, const C *v,
                                                uint32_t dst, int lane) {
     constexpr int kLanes = K::kChunks < 8 ? K::kChunks : 8;  // lanes on a row
     constexpr int kRowsAt = 32 / kLanes;
     const int chunks = p.c.head_dim * K::kBytes / 16;
     const int sub = lane % kLanes;
-    const long long tok = t0 + (lane & 15);
     const bool good = x.page >= 0 && x.page < p.c.pages;
-    if (!good && tok >= r.lo && tok < r.hi) atomicExch(p.err, (unsigned int)W4A16_ERR_INVALID_ARG);
-    const uint32_t mask = __ballot_sync(0xffffffffu, good) & 0xffffu;
+    if (!good && in_range) atomicExch(p.err, (unsigned int)W4A16_ERR_INVALID_ARG);
+    const uint32_t mask = __ballot_sync(0xffffffffu, good) & (K::kTok == 32 ? 0xffffffffu : 0xffffu);
     const int page_ok = good ? x.page : 0;
-    const C *kh = static_cast<const C *>(p.c.k) + kvh * p.c.k_head + sub * (16 / K::kBytes);
-    const C *vh = static_cast<const C *>(p.c.v) + kvh * p.c.v_head + sub * (16 / K::kBytes);
 #pragma unroll
-    for (int i = 0; i < kSlice / kRowsAt; ++i) {
+    for (int i = 0; i < K::kTok / kRowsAt; ++i) {
         const int row = i * kRowsAt + lane / kLanes;
         const bool ok = (mask >> row) & 1u;
         const long long page = __shfl_sync(0xffffffffu, page_ok, row);
         const long long at = __shfl_sync(0xffffffffu, x.at, row);
-        const C *k = kh + page * p.c.k_page + at * p.c.k_token;
-        const C *v = vh + page * p.c.v_page + at * p.c.v_token;
+        const C *kr = k + page * p.c.k_page + at * p.c.k_token;
+        const C *vr = v + page * p.c.v_page + at * p.c.v_token;
 #pragma unroll
         for (int c = 0; c < K::kChunks / kLanes; ++c) {
             const int chunk = c * kLanes + sub;
             if (chunk < chunks) {
                 const uint32_t o = place<K::kChunks>(row, chunk);
-                copy16(dst + o, k + c * kLanes * (16 / K::kBytes), ok);
-                copy16(dst + K::kSliceBytes + o, v + c * kLanes * (16 / K::kBytes), ok);
+                copy16(dst + o, kr + c * kLanes * (16 / K::kBytes), ok);
+                copy16(dst + K::kSliceBytes + o, vr + c * kLanes * (16 / K::kBytes), ok);
             }
         }
     }
     return mask;
 }
 
-// Running state of a warp over its slices of a segment. M is the operand type.
-template <typename K, typename M, int NT>
-struct State {
-    uint32_t q[K::kDim / 16][NT][2];
-    float o[K::kDim / 16][NT][4];
-    float m[NT][2], l[NT][2];  // maximum and sum of the thread's two heads (l: of its own rows)
+// A running maximum, sum and unnormalised output of 4 elements, and another one
+// taken in. Maxima are in units of log2.
+struct Joined {
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    __device__ __forceinline__ void take(float m2, float l2, const float4 &y) {
+        const float mx = fmaxf(m, m2), top = mx == -INFINITY ? 0.f : mx;
+        const float f1 = exp2_approx(m - top), f2 = exp2_approx(m2 - top);
+        l = l * f1 + l2 * f2;
+        o.x = o.x * f1 + y.x * f2, o.y = o.y * f1 + y.y * f2;
+        o.z = o.z * f1 + y.z * f2, o.w = o.w * f1 + y.w * f2;
+        m = mx;
+    }
 };
 
 // Weights are drawn up by 2^kUp before they become operands of 16 bits, so that
@@ -205,13 +218,17 @@ struct State {
 constexpr float kUp = 12.f;
 
 template <typename T, typename C, int DT, int NT>
-__global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, 1) paged_attention_kernel(const Params p) {
+__global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, kPerSm) paged_attention_kernel(const Params p) {
     using K = Config<T, C, DT, NT>;
     constexpr bool k8 = sizeof(C) == 1;
     using M = typename std::conditional<k8, __half, T>::type;  // operand type
-    constexpr int kSteps = DT / 16;
+    // Weights become one operand of 16 bits and, with 16-bit caches, a second one for what the first's rounding
+    // left: alone it would be as coarse as the output's own rounding. With 8-bit values, whose own rounding is
+    // 2^-4, that second product is not spent.
+    constexpr bool kTwo = !k8;
+    constexpr int kSteps = DT / 16, MT = K::kTiles;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ long long sums[32];
+    __shared__ long long sums[K::kWarps];
     __shared__ long long first_base;
     __shared__ int first_request;
     __shared__ uint32_t masks[K::kWarps][K::kStages];
@@ -237,6 +254,7 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, 1) paged_atten
     if (lane == 31) sums[warp] = upto;
     __syncthreads();
     long long total = 0;
+#pragma unroll
     for (int w = 0; w < K::kWarps; ++w) {
         if (w == warp) upto += total;
         total += sums[w];
@@ -273,6 +291,7 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, 1) paged_atten
     __syncthreads();
 
     const uint32_t ring = ptx::smem_u32(smem) + warp * K::kRing;
+    constexpr int kLanes = K::kChunks < 8 ? K::kChunks : 8;
     long long t = t_begin, base = first_base;
     int b = first_request;
     while (t < t_end) {
@@ -289,28 +308,56 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, 1) paged_atten
         const int count = (int)(seg_end - t);  // tiles of the segment
         const int kvh = item / p.head_blocks, h0 = kvh * p.group + (item % p.head_blocks) * K::kRows;
         const int rows = min(K::kRows, (kvh + 1) * p.group - h0);
-        const long long tok0 = (r.lo / K::kTile + (t - item_begin)) * K::kTile + warp * kSlice;
+        const int lo = (int)r.lo, hi = (int)r.hi;  // lengths fit 31 bits
+        // The warp's first token. Slices behind the last one may begin beyond 31 bits: taken modulo 2^32 they
+        // turn negative and so lie outside [lo, hi).
+        int tok = (int)((unsigned int)(r.lo / K::kTile + (t - item_begin)) * K::kTile + warp * K::kTok);
         const int32_t *table = p.table + b * p.table_stride;
+        const C *kp = static_cast<const C *>(p.c.k) + kvh * p.c.k_head + lane % kLanes * (16 / K::kBytes);
+        const C *vp = static_cast<const C *>(p.c.v) + kvh * p.c.v_head + lane % kLanes * (16 / K::kBytes);
 
-        State<K, M, NT> st;
+        // Fill the ring.
+        Places ahead = look_up<K::kTok>(p, table, tok, lo, hi, lane);
+        int loaded = 0;
+        auto load_next = [&](int stage) {
+            if (loaded < count) {
+                const Places now = ahead;
+                const int mine = tok + lane % K::kTok;
+                const bool in = mine >= lo && mine < hi;
+                tok = (int)((unsigned int)tok + K::kTile);
+                ahead = look_up<K::kTok>(p, table, tok, lo, hi, lane);
+                const uint32_t mask = load_slice<K, C>(p, now, in, kp, vp, ring + stage * 2 * K::kSliceBytes, lane);
+                if (lane == 0) masks[warp][stage] = mask;
+                ++loaded;
+            }
+            copies_commit();
+        };
+#pragma unroll 1
+        for (int i = 0; i < K::kStages - 1; ++i) load_next(i);
+
         // Queries as the B operand: column n = head lane/4, two k of each half. With 8-bit keys the k of a
         // step are taken in the order in which four consecutive bytes of a row come out of the ring.
+        uint32_t q[kSteps][NT][2];
+        float o[kSteps][NT][4];
+        float m[NT][2], l[NT][2];  // maximum and sum of the thread's two heads (l: of its own rows)
         float q_scale = 1.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int head = nt * 8 + lane / 4;
-            const T *q = static_cast<const T *>(p.q) + b * p.q_row + (h0 + head) * p.q_head;
+            const T *qh = static_cast<const T *>(p.q) + b * p.q_row + (h0 + head) * p.q_head;
+            // A scale of 0 or below turns into queries that are 0 or negated, and a positive scale.
+            const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
             for (int ks = 0; ks < kSteps; ++ks) {
                 const int k0 = ks * 16 + (k8 ? 4 : 2) * (lane % 4);
-                const bool in = head < rows && ks * 16 < D;
+                const bool in = head < rows && ks * 16 < D && p.scale != 0.f;
                 const bool in2 = in && (k8 || ks * 16 + 8 < D);
-                st.q[ks][nt][0] = in ? *reinterpret_cast<const uint32_t *>(q + k0) : 0u;
-                st.q[ks][nt][1] = in2 ? *reinterpret_cast<const uint32_t *>(q + k0 + (k8 ? 2 : 8)) : 0u;
-                st.o[ks][nt][0] = st.o[ks][nt][1] = st.o[ks][nt][2] = st.o[ks][nt][3] = 0.f;
+                q[ks][nt][0] = in ? *reinterpret_cast<const uint32_t *>(qh + k0) ^ flip : 0u;
+                q[ks][nt][1] = in2 ? *reinterpret_cast<const uint32_t *>(qh + k0 + (k8 ? 2 : 8)) ^ flip : 0u;
+                o[ks][nt][0] = o[ks][nt][1] = o[ks][nt][2] = o[ks][nt][3] = 0.f;
             }
-            st.m[nt][0] = st.m[nt][1] = -INFINITY;
-            st.l[nt][0] = st.l[nt][1] = 0.f;
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
         }
         if constexpr (k8 && !std::is_same<T, __half>::value) {
             // bf16 queries against 8-bit keys: keys become fp16 (exact), queries fp16 after a power of two that
@@ -322,41 +369,29 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, 1) paged_atten
                 for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const float2 f = elem::pair_to_f32<T>(st.q[ks][nt][x]);
+                        const float2 f = elem::pair_to_f32<T>(q[ks][nt][x]);
                         big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
                     }
 #pragma unroll
             for (int x = 16; x > 0; x >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
-            const int e = big > 0.f && big < INFINITY ? ilogbf(big) : 0;
-            const float down = ldexpf(1.f, -max(e, -120));
-            q_scale = ldexpf(1.f, max(e, -120));
+            const int e = big > 0.f && big < INFINITY ? max(ilogbf(big), -120) : 0;
+            const float down = ldexpf(1.f, -e);
+            q_scale = ldexpf(1.f, e);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const float2 f = elem::pair_to_f32<T>(st.q[ks][nt][x]);
-                        st.q[ks][nt][x] = elem::pair_from_f32<__half>(f.x * down, f.y * down);
+                        const float2 f = elem::pair_to_f32<T>(q[ks][nt][x]);
+                        q[ks][nt][x] = elem::pair_from_f32<__half>(f.x * down, f.y * down);
                     }
         }
-        const float k_scale = p.scale * q_scale * (k8 && p.c.k_scale ? p.c.k_scale[kvh] : 1.f);
+        // Scores in units of log2 are the products times `unit`.
         constexpr float kLog2e = 1.4426950408889634f;
+        const float to_score = (p.scale != 0.f ? fabsf(p.scale) : 1.f) * q_scale * (k8 && p.c.k_scale ? p.c.k_scale[kvh] : 1.f);
+        const float unit = p.softcap > 0.f ? 1.f : to_score * kLog2e;
 
-        // Fill the ring, then one slice out and one in.
-        const int fill = min(count, K::kStages - 1);
-        Places ahead = look_up(p, table, tok0, r, lane);
-#pragma unroll 1
-        for (int i = 0; i < K::kStages - 1; ++i) {
-            if (i < fill) {
-                const Places now = ahead;
-                const long long t0 = tok0 + (long long)i * K::kTile;
-                ahead = look_up(p, table, t0 + K::kTile, r, lane);
-                const uint32_t mask = load_slice<K, C>(p, now, r, t0, kvh, ring + i * 2 * K::kSliceBytes, lane);
-                if (lane == 0) masks[warp][i] = mask;
-            }
-            copies_commit();
-        }
         int stage = 0;
 #pragma unroll 1
         for (int i = 0; i < count; ++i) {
@@ -364,124 +399,133 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, 1) paged_atten
             __syncwarp();
             const uint32_t sk = ring + stage * 2 * K::kSliceBytes, sv = sk + K::kSliceBytes;
             const uint32_t mask = masks[warp][stage];
-            // Scores: 16 tokens x 8 NT heads.
-            float s[NT][4];
+            // Products: MT * 16 tokens x 8 NT heads; rows lane/4 and lane/4 + 8, heads 2*(lane%4) and the next.
+            float s[MT][NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-            if constexpr (!k8) {
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int ks = 0; ks < kSteps; ++ks) {
-                    if (ks * 16 >= D) break;
-                    uint32_t a[4];
-                    ldsm4(a, sk + place<K::kChunks>(lane & 15, ks * 2 + (lane >> 4)));
+                for (int nt = 0; nt < NT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma<M>(s[nt], a, st.q[ks][nt][0], st.q[ks][nt][1]);
-                }
-            } else {
+            for (int ks = 0; ks < kSteps; ks += k8 ? 2 : 1) {
+                if (ks * 16 >= D) break;
 #pragma unroll
-                for (int k2 = 0; k2 < kSteps / 2; ++k2) {  // two steps for each four matrices
-                    if (k2 * 32 >= D) break;
+                for (int mt = 0; mt < MT; ++mt) {
                     uint32_t w[4];
-                    ldsm4(w, sk + place<K::kChunks>(lane & 15, k2 * 2 + (lane >> 4)));
+                    if constexpr (!k8) {
+                        ldsm4(w, sk + place<K::kChunks>(mt * 16 + (lane & 15), ks * 2 + (lane >> 4)));
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const uint32_t a[4] = {elem::e4m3_to_half2((uint16_t)w[2 * x]), elem::e4m3_to_half2((uint16_t)w[2 * x + 1]),
-                                               elem::e4m3_to_half2((uint16_t)(w[2 * x] >> 16)),
-                                               elem::e4m3_to_half2((uint16_t)(w[2 * x + 1] >> 16))};
+                        for (int nt = 0; nt < NT; ++nt) mma<M>(s[mt][nt], w, q[ks][nt][0], q[ks][nt][1]);
+                    } else {
+                        ldsm4(w, sk + place<K::kChunks>(mt * 16 + (lane & 15), ks + (lane >> 4)));
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma<M>(s[nt], a, st.q[2 * k2 + x][nt][0], st.q[2 * k2 + x][nt][1]);
+                        for (int x = 0; x < 2; ++x) {  // two steps for each four matrices
+                            const uint32_t a[4] = {elem::e4m3_to_half2((uint16_t)w[2 * x]),
+                                                   elem::e4m3_to_half2((uint16_t)w[2 * x + 1]),
+                                                   elem::e4m3_to_half2((uint16_t)(w[2 * x] >> 16)),
+                                                   elem::e4m3_to_half2((uint16_t)(w[2 * x + 1] >> 16))};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma<M>(s[mt][nt], a, q[ks + x][nt][0], q[ks + x][nt][1]);
+                        }
                     }
                 }
             }
-            // Scores in units of log2: rows lane/4 and lane/4 + 8, heads 2*(lane%4) and the next.
-            const bool up = (mask >> (lane / 4)) & 1u, low = (mask >> (lane / 4 + 8)) & 1u;
-            uint32_t ph[NT][2], pl[NT][2];
+            if (p.softcap > 0.f) {
+                const float in = to_score / p.softcap, out = p.softcap * kLog2e;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    float y = s[nt][x] * k_scale;
-                    if (p.softcap > 0.f) y = p.softcap * tanhf(y / p.softcap);
-                    s[nt][x] = (x < 2 ? up : low) ? y * kLog2e : -INFINITY;
-                }
-                float top[2], keep[2];
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) s[mt][nt][x] = out * tanhf(s[mt][nt][x] * in);
+            }
+            if (mask != (K::kTok == 32 ? 0xffffffffu : 0xffffu)) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        if (!((mask >> (mt * 16 + lane / 4 + (x < 2 ? 0 : 8))) & 1u))
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) s[mt][nt][x] = -INFINITY;
+            }
+            // Maxima over the slice's tokens, and what the past is worth under the new ones.
+            float keep[NT][2], off[NT][2];
+            bool moved = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    float y = fmaxf(s[nt][x], s[nt][x + 2]);
+                    float y = fmaxf(s[0][nt][x], s[0][nt][x + 2]);
+#pragma unroll
+                    for (int mt = 1; mt < MT; ++mt) y = fmaxf(y, fmaxf(s[mt][nt][x], s[mt][nt][x + 2]));
                     y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
                     y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
                     y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
-                    y = fmaxf(y, st.m[nt][x]);
-                    top[x] = y == -INFINITY ? 0.f : y;  // no token so far: all weights are 0
-                    keep[x] = exp2_approx(st.m[nt][x] - top[x]);
-                    st.m[nt][x] = y;
+                    y = fmaxf(y, m[nt][x]);
+                    const float top = y == -INFINITY ? 0.f : y;  // no token so far: all weights are 0
+                    keep[nt][x] = exp2_approx((m[nt][x] - top) * unit);
+                    off[nt][x] = kUp - top * unit;
+                    moved |= m[nt][x] != y;
+                    m[nt][x] = y;
                 }
-                float w[4];
+            if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x) w[x] = exp2_approx(s[nt][x] - top[x & 1] + kUp);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) st.l[nt][x] = st.l[nt][x] * keep[x] + (w[x] + w[x + 2]);
-                if (__any_sync(0xffffffffu, keep[0] != 1.f || keep[1] != 1.f)) {
+                for (int nt = 0; nt < NT; ++nt) {
+                    l[nt][0] *= keep[nt][0], l[nt][1] *= keep[nt][1];
 #pragma unroll
                     for (int dt = 0; dt < kSteps; ++dt)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) st.o[dt][nt][x] *= keep[x & 1];
-                }
-                // Weights as two operands, the value and what its rounding left: one of 16 bits would be as
-                // coarse as the output's own rounding.
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const uint32_t h = elem::pair_from_f32<M>(w[2 * x], w[2 * x + 1]);
-                    const float2 f = elem::pair_to_f32<M>(h);
-                    ph[nt][x] = transpose8x8(h);
-                    pl[nt][x] = transpose8x8(elem::pair_from_f32<M>(w[2 * x] - f.x, w[2 * x + 1] - f.y));
+                        for (int x = 0; x < 4; ++x) o[dt][nt][x] *= keep[nt][x & 1];
                 }
             }
-            // Outputs: 16 elements of the head at a time.
-            if constexpr (!k8) {
+            uint32_t ph[MT][NT][2], pl[kTwo ? MT : 1][kTwo ? NT : 1][2];
 #pragma unroll
-                for (int dt = 0; dt < kSteps; ++dt) {
-                    if (dt * 16 >= D) break;
-                    uint32_t a[4];
-                    ldsm4_t(a, sv + place<K::kChunks>((lane & 7) + ((lane >> 4) << 3), dt * 2 + ((lane >> 3) & 1)));
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma<M>(st.o[dt][nt], a, ph[nt][0], ph[nt][1]);
-                        mma<M>(st.o[dt][nt], a, pl[nt][0], pl[nt][1]);
-                    }
-                }
-            } else {
+                for (int nt = 0; nt < NT; ++nt) {
+                    float w[4];
 #pragma unroll
-                for (int d2 = 0; d2 < kSteps / 2; ++d2) {
-                    if (d2 * 32 >= D) break;
-                    uint32_t w[4];
-                    ldsm4_t(w, sv + place<K::kChunks>(lane & 15, d2 * 2 + (lane >> 4)));
+                    for (int x = 0; x < 4; ++x) w[x] = exp2_approx(fmaf(s[mt][nt][x], unit, off[nt][x & 1]));
+                    l[nt][0] += w[0] + w[2], l[nt][1] += w[1] + w[3];
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        // Bytes: (d, d+1) of one token, (d, d+1) of the next; rows r and r + 8 become d = 2r, 2r + 1.
-                        const uint32_t e0 = __byte_perm(w[2 * x], 0, 0x3120), e1 = __byte_perm(w[2 * x + 1], 0, 0x3120);
-                        const uint32_t a[4] = {elem::e4m3_to_half2((uint16_t)e0), elem::e4m3_to_half2((uint16_t)(e0 >> 16)),
-                                               elem::e4m3_to_half2((uint16_t)e1), elem::e4m3_to_half2((uint16_t)(e1 >> 16))};
+                        const uint32_t h = elem::pair_from_f32<M>(w[2 * x], w[2 * x + 1]);
+                        ph[mt][nt][x] = transpose8x8(h);
+                        if constexpr (kTwo) {
+                            const float2 f = elem::pair_to_f32<M>(h);
+                            pl[mt][nt][x] = transpose8x8(elem::pair_from_f32<M>(w[2 * x] - f.x, w[2 * x + 1] - f.y));
+                        }
+                    }
+                }
+            // Outputs: 16 elements of the head at a time.
+#pragma unroll
+            for (int dt = 0; dt < kSteps; dt += k8 ? 2 : 1) {
+                if (dt * 16 >= D) break;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    uint32_t w[4];
+                    if constexpr (!k8) {
+                        ldsm4_t(w, sv + place<K::kChunks>(mt * 16 + (lane & 7) + ((lane >> 4) << 3), dt * 2 + ((lane >> 3) & 1)));
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma<M>(st.o[2 * d2 + x][nt], a, ph[nt][0], ph[nt][1]);
-                            mma<M>(st.o[2 * d2 + x][nt], a, pl[nt][0], pl[nt][1]);
+                            mma<M>(o[dt][nt], w, ph[mt][nt][0], ph[mt][nt][1]);
+                            mma<M>(o[dt][nt], w, pl[mt][nt][0], pl[mt][nt][1]);
+                        }
+                    } else {
+                        ldsm4_t(w, sv + place<K::kChunks>(mt * 16 + (lane & 15), dt + (lane >> 4)));
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            // Bytes: (d, d+1) of one token, (d, d+1) of the next; rows r, r + 8 become d = 2r, 2r + 1.
+                            const uint32_t e0 = __byte_perm(w[2 * x], 0, 0x3120), e1 = __byte_perm(w[2 * x + 1], 0, 0x3120);
+                            const uint32_t a[4] = {elem::e4m3_to_half2((uint16_t)e0), elem::e4m3_to_half2((uint16_t)(e0 >> 16)),
+                                                   elem::e4m3_to_half2((uint16_t)e1), elem::e4m3_to_half2((uint16_t)(e1 >> 16))};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma<M>(o[dt + x][nt], a, ph[mt][nt][0], ph[mt][nt][1]);
                         }
                     }
                 }
             }
             __syncwarp();  // all lanes have read the stage that is filled next time
-            const int next = i + K::kStages - 1;
-            if (next < count) {
-                const int to = stage == 0 ? K::kStages - 1 : stage - 1;
-                const Places now = ahead;
-                const long long t0 = tok0 + (long long)next * K::kTile;
-                ahead = look_up(p, table, t0 + K::kTile, r, lane);
-                const uint32_t got = load_slice<K, C>(p, now, r, t0, kvh, ring + to * 2 * K::kSliceBytes, lane);
-                if (lane == 0) masks[warp][to] = got;
-            }
-            copies_commit();
+            load_next(stage == 0 ? K::kStages - 1 : stage - 1);
             stage = stage + 1 == K::kStages ? 0 : stage + 1;
         }
         copies_wait<0>();
@@ -495,86 +539,97 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, 1) paged_atten
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int row = nt * 8 + 2 * (lane % 4) + x;
-                float l = st.l[nt][x];
-                l += __shfl_xor_sync(0xffffffffu, l, 4);
-                l += __shfl_xor_sync(0xffffffffu, l, 8);
-                l += __shfl_xor_sync(0xffffffffu, l, 16);
-                if (lane < 4) mm[warp * K::kRows + row] = st.m[nt][x], ml[warp * K::kRows + row] = l;
+                float sum = l[nt][x];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                if (lane < 4) mm[warp * K::kRows + row] = m[nt][x] * unit, ml[warp * K::kRows + row] = sum;
 #pragma unroll
                 for (int dt = 0; dt < kSteps; ++dt) {
-                    float *o = mo + (warp * K::kRows + row) * DT + dt * 16;
-                    o[k8 ? 2 * (lane / 4) : lane / 4] = st.o[dt][nt][x];
-                    o[k8 ? 2 * (lane / 4) + 1 : lane / 4 + 8] = st.o[dt][nt][x + 2];
+                    float *to = mo + (warp * K::kRows + row) * DT + dt * 16;
+                    to[k8 ? 2 * (lane / 4) : lane / 4] = o[dt][nt][x];
+                    to[k8 ? 2 * (lane / 4) + 1 : lane / 4 + 8] = o[dt][nt][x + 2];
                 }
             }
         __syncthreads();
         const int c_first = (int)(((item_begin + 1) * active - 1) / total), c_last = (int)((item_end * active - 1) / total);
-        const bool whole = c_first == c_last;
-        float *part = p.partial + ((long long)cta * 2 + (cta == c_first)) * K::kPartial;
+        const int parts = c_last - c_first + 1;
         const float v_scale = k8 && p.c.v_scale ? p.c.v_scale[kvh] : 1.f;
         constexpr float kLn2 = 0.6931471805599453f;
         // A joined row: o / l, and its lse.
-        auto finish = [&](int row, int d, float4 o, float m, float l) {
-            const float f = l > 0.f || l != l ? v_scale / l : 0.f;
+        auto finish = [&](int row, int d, const Joined &j) {
+            const bool any = j.l > 0.f || j.l != j.l;
+            const float f = any ? v_scale / j.l : 0.f;
             T *out = static_cast<T *>(p.out) + b * p.o_row + (h0 + row) * p.o_head + d;
             *reinterpret_cast<uint2 *>(out) =
-                make_uint2(elem::pair_from_f32<T>(o.x * f, o.y * f), elem::pair_from_f32<T>(o.z * f, o.w * f));
+                make_uint2(elem::pair_from_f32<T>(j.o.x * f, j.o.y * f), elem::pair_from_f32<T>(j.o.z * f, j.o.w * f));
             if (p.lse && d == 0)
-                p.lse[(long long)b * p.heads + h0 + row] = l > 0.f || l != l ? (m + log2f(l) - kUp) * kLn2 : -INFINITY;
+                p.lse[(long long)b * p.heads + h0 + row] = any ? (j.m + log2f(j.l) - kUp) * kLn2 : -INFINITY;
+        };
+        // The place of the i-th partial result of this item.
+        auto part = [&](int i) { return p.partial + ((long long)(c_first + i) * 2 + (i == 0)) * kMaxPartial; };
+        auto leave = [&](float *to, int row, int d, const Joined &j, int joined) {
+            __stcg(reinterpret_cast<float4 *>(to + row * DT + d), j.o);
+            if (d == 0)
+                __stcg(reinterpret_cast<float2 *>(to + K::kRows * (DT + 2 * joined) + 2 * row), make_float2(j.m, j.l));
         };
         for (int i = tid; i < rows * (DT / 4); i += K::kThreads) {
             const int row = i / (DT / 4), d = i % (DT / 4) * 4;
             if (d >= D) continue;
-            float m = -INFINITY, l = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            Joined j;
 #pragma unroll
-            for (int w = 0; w < K::kWarps; ++w) m = fmaxf(m, mm[w * K::kRows + row]);
-            const float top = m == -INFINITY ? 0.f : m;
-#pragma unroll
-            for (int w = 0; w < K::kWarps; ++w) {
-                const float f = exp2_approx(mm[w * K::kRows + row] - top);
-                const float4 x = *reinterpret_cast<const float4 *>(mo + (w * K::kRows + row) * DT + d);
-                l += f * ml[w * K::kRows + row];
-                o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
-            }
-            if (whole) {
-                finish(row, d, o, m, l);
-            } else {
-                __stcg(reinterpret_cast<float4 *>(part + row * DT + d), o);
-                if (d == 0) __stcg(part + K::kRows * DT + 2 * row, m), __stcg(part + K::kRows * DT + 2 * row + 1, l);
-            }
+            for (int w = 0; w < K::kWarps; ++w)
+                j.take(mm[w * K::kRows + row], ml[w * K::kRows + row],
+                       *reinterpret_cast<const float4 *>(mo + (w * K::kRows + row) * DT + d));
+            if (parts == 1) finish(row, d, j);
+            else leave(part(cta - c_first), row, d, j, 0);
         }
-        if (!whole) {
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const unsigned int parts = (unsigned int)(c_last - c_first + 1);
-                const bool last = atomicAdd(p.counters + c_first, 1u) == parts - 1;
-                if (last) p.counters[c_first] = 0u;  // ready for the next call
-                is_last = last;
-            }
-            __syncthreads();
-            if (is_last) {
+        if (parts > 1) {
+            // Joined by the last CTA to arrive: first in groups of consecutive CTAs (when there are many), then
+            // over the groups. A CTA is in front of the end of one item only, so counters at its number, one for
+            // items that begin in it and one for the item that does not, are not shared.
+            int group = 8;
+            while (group * group < parts) ++group;
+            const int of = (cta - c_first) / group, in_group = min(group, parts - of * group);
+            const int groups = (parts + group - 1) / group;
+            auto last_of = [&](unsigned int *counter, int n) {
                 __threadfence();
-                const float *first = p.partial + ((long long)c_first * 2 + 1) * K::kPartial;
+                __syncthreads();
+                if (tid == 0) {
+                    is_last = atomicAdd(counter, 1u) == (unsigned int)n - 1u;
+                    if (is_last) *counter = 0u;  // ready for the next call
+                }
+                __syncthreads();
+                const bool yes = is_last;
+                if (yes) __threadfence();
+                return yes;
+            };
+            auto join = [&](int from, int step, int n, int joined, bool end) {
                 for (int i = tid; i < rows * (DT / 4); i += K::kThreads) {
                     const int row = i / (DT / 4), d = i % (DT / 4) * 4;
                     if (d >= D) continue;
-                    float m = -INFINITY, l = 0.f;
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int c = c_first; c <= c_last; ++c) {
-                        const float *x = c == c_first ? first : p.partial + (long long)c * 2 * K::kPartial;
-                        const float m2 = __ldcg(x + K::kRows * DT + 2 * row), l2 = __ldcg(x + K::kRows * DT + 2 * row + 1);
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(x + row * DT + d));
-                        const float mx = fmaxf(m, m2), top = mx == -INFINITY ? 0.f : mx;
-                        const float f1 = exp2_approx(m - top), f2 = exp2_approx(m2 - top);
-                        l = l * f1 + l2 * f2;
-                        o.x = o.x * f1 + y.x * f2, o.y = o.y * f1 + y.y * f2;
-                        o.z = o.z * f1 + y.z * f2, o.w = o.w * f1 + y.w * f2;
-                        m = mx;
+                    Joined j;
+                    for (int c = 0; c < n; c += 8) {
+                        float2 ml2[8];
+                        float4 y[8];
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            const float *x = part(from + min(c + u, n - 1) * step);
+                            ml2[u] = __ldcg(reinterpret_cast<const float2 *>(x + K::kRows * (DT + 2 * joined) + 2 * row));
+                            y[u] = __ldcg(reinterpret_cast<const float4 *>(x + row * DT + d));
+                        }
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            if (c + u < n) j.take(ml2[u].x, ml2[u].y, y[u]);
                     }
-                    finish(row, d, o, m, l);
+                    if (end) finish(row, d, j);
+                    else leave(part(from), row, d, j, 1);
                 }
+            };
+            unsigned int *counter = of == 0 ? p.counters + c_first : p.counters + kMaxCtas + c_first + of * group;
+            if (last_of(counter, in_group)) {
+                join(of * group, 1, in_group, 0, groups == 1);
+                if (groups > 1 && last_of(p.counters + 2 * kMaxCtas + c_first, groups)) join(0, group, groups, 1, true);
             }
         }
         t = seg_end;
@@ -588,7 +643,7 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, 1) paged_atten
 }
 
 template <typename T, typename C, int DT, int NT>
-cudaError_t launch(Params p, int ctas, cudaStream_t s) {
+cudaError_t launch(Params p, int sms, cudaStream_t s) {
     using K = Config<T, C, DT, NT>;
     auto kernel = paged_attention_kernel<T, C, DT, NT>;
     cudaError_t e = ensure_max_dyn_smem((const void *)kernel, K::kSmem);
@@ -596,6 +651,7 @@ cudaError_t launch(Params p, int ctas, cudaStream_t s) {
     p.head_blocks = (p.group + K::kRows - 1) / K::kRows;
     const long long tiles = ((long long)p.max_pages * p.c.page_size + K::kTile - 1) / K::kTile * p.batch *
                             p.c.kv_heads * p.head_blocks;
+    const int ctas = sms * kPerSm < kMaxCtas ? sms * kPerSm : kMaxCtas;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles < ctas ? tiles : ctas), 1, 1);
     cfg.blockDim = dim3(K::kThreads, 1, 1);
@@ -610,16 +666,16 @@ cudaError_t launch(Params p, int ctas, cudaStream_t s) {
 }
 
 template <typename T, typename C>
-cudaError_t launch_dims(const Params &p, int ctas, cudaStream_t s) {
+cudaError_t launch_dims(const Params &p, int sms, cudaStream_t s) {
     const bool two = p.group > 8;
-    if (p.c.head_dim <= 64) return two ? launch<T, C, 64, 2>(p, ctas, s) : launch<T, C, 64, 1>(p, ctas, s);
-    if (p.c.head_dim <= 128) return two ? launch<T, C, 128, 2>(p, ctas, s) : launch<T, C, 128, 1>(p, ctas, s);
-    return launch<T, C, 256, 1>(p, ctas, s);
+    if (p.c.head_dim <= 64) return two ? launch<T, C, 64, 2>(p, sms, s) : launch<T, C, 64, 1>(p, sms, s);
+    if (p.c.head_dim <= 128) return two ? launch<T, C, 128, 2>(p, sms, s) : launch<T, C, 128, 1>(p, sms, s);
+    return launch<T, C, 256, 1>(p, sms, s);
 }
 
 // Defined in paged_attention_f16.cu and paged_attention_bf16.cu.
-cudaError_t launch_f16(const Params &p, int ctas, cudaStream_t s);
-cudaError_t launch_bf16(const Params &p, int ctas, cudaStream_t s);
+cudaError_t launch_f16(const Params &p, int sms, cudaStream_t s);
+cudaError_t launch_bf16(const Params &p, int sms, cudaStream_t s);
 
 }  // namespace attn
 }  // namespace w4a16

@@ -4,8 +4,8 @@
 namespace w4a16 {
 namespace attn {
 
-cudaError_t launch_bf16(const Params &p, int ctas, cudaStream_t s) {
-    return p.c.type == W4A16_TYPE_E4M3 ? launch_dims<__nv_bfloat16, E4M3>(p, ctas, s) : launch_dims<__nv_bfloat16, __nv_bfloat16>(p, ctas, s);
+cudaError_t launch_bf16(const Params &p, int sms, cudaStream_t s) {
+    return p.c.type == W4A16_TYPE_E4M3 ? launch_dims<__nv_bfloat16, E4M3>(p, sms, s) : launch_dims<__nv_bfloat16, __nv_bfloat16>(p, sms, s);
 }
 
 }  // namespace attn
