@@ -338,7 +338,7 @@ typedef enum {
  *             that times scale[h], with one fp32 scale for each kv head
  *   k_scale, v_scale  device fp32 [kv_heads], E4M3 only; NULL means 1
  * Rules: pages, page_size, kv_heads > 0; head_dim a multiple of 8 (E4M3: 16), at
- * most 256; pools 16-byte aligned and strides multiples of 16 bytes.
+ * most 256; pools 16-byte aligned; strides multiples of 16 bytes, below 2^31 elements.
  */
 typedef struct {
     void *k, *v;

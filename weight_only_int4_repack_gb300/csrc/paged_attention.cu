@@ -16,7 +16,7 @@ extern "C" {
 
 size_t w4a16_paged_attention_workspace_bytes(int batch, int heads, int kv_heads, int head_dim) {
     if (batch <= 0 || heads <= 0 || kv_heads <= 0 || head_dim <= 0 || heads % kv_heads) return 0;
-    return kCounterBytes + (size_t)sm_count() * attn::kPerSm * 2 * attn::kMaxPartial * 4;
+    return kCounterBytes + (size_t)sm_count() * attn::kMostPerSm * 2 * attn::kMaxPartial * 4;
 }
 
 w4a16_status w4a16_paged_attention(const void *q, w4a16_type type, long long q_row, long long q_head,
@@ -49,6 +49,7 @@ w4a16_status w4a16_paged_attention(const void *q, w4a16_type type, long long q_r
     p.counters = static_cast<unsigned int *>(ws);
     p.partial = reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + kCounterBytes);
     p.max_pages = max_pages, p.batch = batch, p.heads = heads, p.group = heads / cache->kv_heads;
+    p.one_page = cache->page_size % 16 == 0;
     p.window = window, p.scale = scale, p.softcap = softcap;
     p.err = device_error_ptr();
     if (!p.err) return W4A16_ERR_CUDA;

@@ -15,7 +15,7 @@
 // A segment. Warp w takes the w-th slice of each tile and keeps its own running
 // maximum, sum and output; the warps meet once, at the segment's end. Each warp
 // feeds a ring of its own with 16-byte asynchronous copies (no CTA barrier in the
-// loop). Tokens are the rows of the matrix instruction and query heads its columns
+// loop), and begins to fill it for the next segment before the warps meet. Tokens are the rows of the matrix instruction and query heads its columns
 // (m16n8k16: S^T = K Q^T, O^T = V^T P^T), so heads are padded to 8, not to 16, and
 // scores and outputs of one head stay in the same threads.
 #pragma once
@@ -41,13 +41,15 @@ struct Params {
     unsigned int *counters;  // [3][kMaxCtas], zero between calls
     float *partial;          // [CTAs][2][kMaxPartial]
     int max_pages, batch, heads, group, head_blocks, window;
+    int one_page;  // page_size is a multiple of 16
+    unsigned int k_page, k_token, v_page, v_token;  // strides below 2^31
     float scale, softcap;
     unsigned int *err;
 };
 
 constexpr int kMaxCtas = 1024;
 constexpr int kMaxPartial = 16 * (128 + 4);  // floats of the largest partial result (8 * (256 + 4) is less)
-constexpr int kPerSm = 2;                    // CTAs on an SM: one streams while the other begins or ends a segment
+constexpr int kMostPerSm = 3;                // CTAs on an SM at most
 
 template <typename T, typename C, int DT, int NT>
 struct Config {
@@ -56,19 +58,25 @@ struct Config {
     static constexpr int kBytes = sizeof(C);
     static constexpr int kRowBytes = DT * kBytes;          // a token's keys (or values) in the ring
     static constexpr int kChunks = kRowBytes / 16;
-    static constexpr int kTok = kRowBytes <= 128 ? 32 : 16;  // tokens of a slice
-    static constexpr int kTiles = kTok / 16;
+    static constexpr int kTok = DT == 64 ? 32 : 16;  // tokens of a slice
+    static constexpr uint32_t kAll = kTok == 32 ? 0xffffffffu : 0xffffu;
+    // CTAs on an SM: one streams while another begins or ends a segment. 8-bit slices cost more instructions for
+    // each byte, so a third CTA's warps are needed.
+    static constexpr int kPerSm = kBytes == 1 && DT <= 128 ? 3 : 2;
     static constexpr int kSliceBytes = kTok * kRowBytes;   // keys or values of a slice
     static constexpr int kWarps = kSliceBytes > 4096 ? 2 : 4;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kTile = kWarps * kTok;
-    static constexpr int kStagesFit = 98304 / (kWarps * 2 * kSliceBytes);
+    static constexpr int kStagesFit = (kPerSm == 3 ? 49152 : 98304) / (kWarps * 2 * kSliceBytes);
     static constexpr int kStages = kStagesFit > 6 ? 6 : kStagesFit;
     static constexpr int kRing = kStages * 2 * kSliceBytes;  // one warp's
-    static constexpr int kMerge = kWarps * kRows * (DT + 2) * 4;
-    static constexpr int kSmem = kWarps * kRing > kMerge ? kWarps * kRing : kMerge;
+    static constexpr int kPitch = DT + 4;                    // of a row in the merge area: no bank conflicts
+    static constexpr int kMerge = kWarps * 8 * kPitch * 4;   // 8 heads of every warp
+    static_assert(kMerge >= kRows * DT * 2, "the queries lie in the merge area");
+    static constexpr int kSmem = kWarps * kRing + kMerge;
     // A partial result: outputs, then maxima and sums, then room for those of a joined group.
     static constexpr int kPartial = kRows * (DT + 4);
+    static_assert(kStages >= 3, "one slice is computed on while two are on their way");
     static_assert(kPartial <= kMaxPartial, "the workspace holds partial results of this size");
 };
 
@@ -151,52 +159,68 @@ struct Places {
     int page;          // -1: not a visible token
     unsigned int at;   // the token's place in its page
 };
-template <int kTok>
-__device__ __forceinline__ Places look_up(const Params &p, const int32_t *table, int t0, int lo, int hi, int lane) {
-    const int tok = t0 + lane % kTok;
-    Places x{-1, 0u};
-    if (tok >= lo && tok < hi) {
-        const unsigned int j = (unsigned int)tok / (unsigned int)p.c.page_size;
-        x.page = __ldg(table + j);
-        x.at = (unsigned int)tok - j * (unsigned int)p.c.page_size;
-    }
-    return x;
-}
+// The lane's token of the slice that is looked up next: its number, and page and place
+// as the division gives them once and every step of a tile moves them on.
+struct Cursor {
+    int tok;
+    unsigned int j, at;
+};
 
 // One warp's copies of a slice into ring stage `dst`. Returns the mask of its rows
 // that hold visible tokens of valid pages; the others become zeros. k, v: the lane's
-// 16 bytes of the kv head's first token.
+// 16 bytes of the kv head in the lane's first row, row lane/kLanes of a page.
 template <typename K, typename C>
 __device__ __forceinline__ uint32_t load_slice(const Params &p, const Places &x, bool in_range, const C *k, const C *v,
                                                uint32_t dst, int lane) {
     constexpr int kLanes = K::kChunks < 8 ? K::kChunks : 8;  // lanes on a row
     constexpr int kRowsAt = 32 / kLanes;
     const int chunks = p.c.head_dim * K::kBytes / 16;
-    const int sub = lane % kLanes;
+    const int sub = lane % kLanes, row0 = lane / kLanes;
     const bool good = x.page >= 0 && x.page < p.c.pages;
     if (!good && in_range) atomicExch(p.err, (unsigned int)W4A16_ERR_INVALID_ARG);
-    const uint32_t mask = __ballot_sync(0xffffffffu, good) & (K::kTok == 32 ? 0xffffffffu : 0xffffu);
-    const int page_ok = good ? x.page : 0;
+    const uint32_t mask = __ballot_sync(0xffffffffu, good) & K::kAll;
+    // The offset of the lane's token from the pool's first (a slice begins at a multiple of 16 tokens).
+    const unsigned int page = good ? x.page : 0, at = good ? x.at : 0;
+    const unsigned long long k_at = (unsigned long long)page * p.k_page + (unsigned long long)at * p.k_token;
+    const unsigned long long v_at = (unsigned long long)page * p.v_page + (unsigned long long)at * p.v_token;
+    auto copy_row = [&](int i, const C *kr, const C *vr) {
+        const bool ok = (mask >> (i * kRowsAt + row0)) & 1u;
 #pragma unroll
-    for (int i = 0; i < K::kTok / kRowsAt; ++i) {
-        const int row = i * kRowsAt + lane / kLanes;
-        const bool ok = (mask >> row) & 1u;
-        const long long page = __shfl_sync(0xffffffffu, page_ok, row);
-        const long long at = __shfl_sync(0xffffffffu, x.at, row);
-        const C *kr = k + page * p.c.k_page + at * p.c.k_token;
-        const C *vr = v + page * p.c.v_page + at * p.c.v_token;
-#pragma unroll
-        for (int c = 0; c < K::kChunks / kLanes; ++c) {
-            const int chunk = c * kLanes + sub;
-            if (chunk < chunks) {
-                const uint32_t o = place<K::kChunks>(row, chunk);
+        for (int c = 0; c < K::kChunks / kLanes; ++c)
+            if (c * kLanes + sub < chunks) {
+                const uint32_t o = place<K::kChunks>(i * kRowsAt + row0, c * kLanes + sub);
                 copy16(dst + o, kr + c * kLanes * (16 / K::kBytes), ok);
                 copy16(dst + K::kSliceBytes + o, vr + c * kLanes * (16 / K::kBytes), ok);
             }
+    };
+    if (p.one_page) {  // pages of a multiple of 16 tokens: 16 tokens lie in one, that of the first visible one
+#pragma unroll
+        for (int g = 0; g < K::kTok / 16; ++g) {
+            const uint32_t here = (mask >> (16 * g)) & 0xffffu;
+            const int from = here ? __ffs(here) - 1 : 0;
+            const C *kr = k + (__shfl_sync(0xffffffffu, k_at, 16 * g + from) - from * p.k_token);
+            const C *vr = v + (__shfl_sync(0xffffffffu, v_at, 16 * g + from) - from * p.v_token);
+#pragma unroll
+            for (int i = 0; i < 16 / kRowsAt; ++i)
+                copy_row(g * (16 / kRowsAt) + i, kr + i * kRowsAt * p.k_token, vr + i * kRowsAt * p.v_token);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < K::kTok / kRowsAt; ++i) {
+            const int row = i * kRowsAt + row0;
+            copy_row(i, k + (__shfl_sync(0xffffffffu, k_at, row) - row0 * p.k_token),
+                     v + (__shfl_sync(0xffffffffu, v_at, row) - row0 * p.v_token));
         }
     }
     return mask;
 }
+
+// What a CTA has of one item of the line (a request, kv head and block of heads).
+struct Segment {
+    int b, kvh, h0, rows, count;  // first query head, heads, tiles
+    int c_first, parts;           // the first CTA with tokens of the item, and how many have some
+    int t, base;                  // the line's tile behind the segment, and the request's first
+};
 
 // A running maximum, sum and unnormalised output of 4 elements, and another one
 // taken in. Maxima are in units of log2.
@@ -213,12 +237,98 @@ struct Joined {
     }
 };
 
-// Weights are drawn up by 2^kUp before they become operands of 16 bits, so that
-// fp16 holds those down to 2^-(kUp + 14) of the largest with full precision.
-constexpr float kUp = 12.f;
+// The reference that scores are taken relative to is moved (and everything summed so
+// far rescaled) only when a score passes it by more than kSlack powers of two: then
+// weights reach 2^(kUp + kSlack) = 2^14, within fp16's range, and fp16 holds those
+// down to 2^-18 of the reference with full precision (and smaller ones to 2^-28).
+constexpr float kUp = 4.f, kSlack = 10.f;
+
+// Where a segment's results go.
+template <typename K, typename T>
+struct Ends {
+    const Params &p;
+    const Segment seg;
+    const float v_scale;
+
+    // A joined row: o / l, and its lse.
+    __device__ __forceinline__ void finish(int row, int d, const Joined &j) const {
+        constexpr float kLn2 = 0.6931471805599453f;
+        const bool any = j.l > 0.f || j.l != j.l;
+        const float f = any ? v_scale / j.l : 0.f;
+        T *out = static_cast<T *>(p.out) + seg.b * p.o_row + (seg.h0 + row) * p.o_head + d;
+        *reinterpret_cast<uint2 *>(out) =
+            make_uint2(elem::pair_from_f32<T>(j.o.x * f, j.o.y * f), elem::pair_from_f32<T>(j.o.z * f, j.o.w * f));
+        if (p.lse && d == 0)
+            p.lse[(long long)seg.b * p.heads + seg.h0 + row] = any ? (j.m + log2f(j.l) - kUp) * kLn2 : -INFINITY;
+    }
+    // The place of the i-th partial result of these heads.
+    __device__ __forceinline__ float *part(int i) const {
+        return p.partial + ((long long)(seg.c_first + i) * 2 + (i == 0)) * kMaxPartial;
+    }
+    __device__ __forceinline__ void leave(float *to, int row, int d, const Joined &j, int joined) const {
+        __stcg(reinterpret_cast<float4 *>(to + row * K::kDim + d), j.o);
+        if (d == 0)
+            __stcg(reinterpret_cast<float2 *>(to + K::kRows * (K::kDim + 2 * joined) + 2 * row), make_float2(j.m, j.l));
+    }
+    __device__ __forceinline__ void join(int from, int step, int n, int joined, bool end) const {
+        constexpr int kDeep = 8;  // partial results that a thread asks for at a time
+        const int cols = seg.rows * (K::kDim / 4);
+        for (int i = threadIdx.x; i < cols; i += K::kThreads) {
+            const int row = i / (K::kDim / 4), d = i % (K::kDim / 4) * 4;
+            if (d >= p.c.head_dim) continue;
+            Joined j;
+            for (int c = 0; c < n; c += kDeep) {
+                float2 ml[kDeep];
+                float4 y[kDeep];
+#pragma unroll
+                for (int u = 0; u < kDeep; ++u)
+                    if (c + u < n) {
+                        const float *x = part(from + (c + u) * step);
+                        ml[u] = __ldcg(reinterpret_cast<const float2 *>(x + K::kRows * (K::kDim + 2 * joined) + 2 * row));
+                        y[u] = __ldcg(reinterpret_cast<const float4 *>(x + row * K::kDim + d));
+                    }
+#pragma unroll
+                for (int u = 0; u < kDeep; ++u)
+                    if (c + u < n) j.take(ml[u].x, ml[u].y, y[u]);
+            }
+            if (end) finish(row, d, j);
+            else leave(part(from), row, d, j, 1);
+        }
+    }
+};
+
+// Partial results are joined by the last CTA to arrive: first in groups of consecutive
+// CTAs (when there are many), then over the groups. A CTA is in front of the end of one
+// item only, so counters at its number, one for items that begin in it and one for the
+// item that does not, are not shared.
+template <typename K, typename T>
+__device__ __forceinline__ void join_parts(const Ends<K, T> &ends, int *is_last) {
+    const Segment &seg = ends.seg;
+    unsigned int *counters = ends.p.counters;
+    int group = 8;
+    while (group * group < seg.parts) ++group;
+    const int of = ((int)blockIdx.x - seg.c_first) / group, in_group = min(group, seg.parts - of * group);
+    const int groups = (seg.parts + group - 1) / group;
+    // The barrier in front of the atomic puts every thread's partial result before it.
+    auto last_of = [&](unsigned int *counter, int n) {
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            unsigned int old;
+            asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+            *is_last = old == (unsigned int)n - 1u;
+            if (*is_last) *counter = 0u;  // ready for the next call
+        }
+        __syncthreads();
+        return *is_last != 0;
+    };
+    if (last_of(of == 0 ? counters + seg.c_first : counters + kMaxCtas + seg.c_first + of * group, in_group)) {
+        ends.join(of * group, 1, in_group, 0, groups == 1);
+        if (groups > 1 && last_of(counters + 2 * kMaxCtas + seg.c_first, groups)) ends.join(0, group, groups, 1, true);
+    }
+}
 
 template <typename T, typename C, int DT, int NT>
-__global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, kPerSm) paged_attention_kernel(const Params p) {
+__global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, DT, NT>::kPerSm) paged_attention_kernel(const __grid_constant__ Params p) {
     using K = Config<T, C, DT, NT>;
     constexpr bool k8 = sizeof(C) == 1;
     using M = typename std::conditional<k8, __half, T>::type;  // operand type
@@ -226,12 +336,13 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, kPerSm) paged_
     // left: alone it would be as coarse as the output's own rounding. With 8-bit values, whose own rounding is
     // 2^-4, that second product is not spent.
     constexpr bool kTwo = !k8;
-    constexpr int kSteps = DT / 16, MT = K::kTiles;
+    constexpr int kSteps = DT / 16, MT = K::kTok / 16;
+    constexpr int kAsk = kSteps / K::kWarps;  // steps whose queries a warp brings
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ long long sums[K::kWarps];
-    __shared__ long long first_base;
-    __shared__ int first_request;
+    __shared__ Segment segs[2], open[2];  // this segment and the next; those that begin before the CTA or end behind it
     __shared__ uint32_t masks[K::kWarps][K::kStages];
+    __shared__ float2 meet[K::kWarps][8];  // maxima and sums
     __shared__ int is_last;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
@@ -259,21 +370,22 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, kPerSm) paged_
         if (w == warp) upto += total;
         total += sums[w];
     }
-    total *= items;
+    total *= items;  // below 2^31: the host has seen to that
     const int active = (int)min((long long)ctas, total);  // CTAs with work: each has a tile at least
-    const long long t_begin = cta < active ? total * cta / active : 0, t_end = cta < active ? total * (cta + 1) / active : 0;
-    long long before = (upto - mine) * items;
+    const int t_begin = cta < active ? (int)(total * cta / active) : 0;
+    const int t_end = cta < active ? (int)(total * (cta + 1) / active) : 0;
+    int before = (int)((upto - mine) * items);
     if (t_begin < t_end && before <= t_begin && t_begin < upto * items) {
         for (int b = b0; b < b1; ++b) {
-            const long long n = tiles_of<K::kTile>(visible(p, b)) * items;
+            const int n = (int)tiles_of<K::kTile>(visible(p, b)) * items;
             if (t_begin < before + n) {
-                first_request = b;
-                first_base = before;
+                segs[1].b = b, segs[1].base = before, segs[1].t = t_begin;
                 break;
             }
             before += n;
         }
     }
+    if (tid < 2) open[tid].parts = 0;
     // Requests without tokens, and lengths out of range.
     for (int b = cta; b < p.batch; b += ctas) {
         const Range r = visible(p, b);
@@ -291,108 +403,191 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, kPerSm) paged_
     __syncthreads();
 
     const uint32_t ring = ptx::smem_u32(smem) + warp * K::kRing;
+    float *mo = reinterpret_cast<float *>(smem + K::kWarps * K::kRing);  // [warp][8][kPitch]
     constexpr int kLanes = K::kChunks < 8 ? K::kChunks : 8;
-    long long t = t_begin, base = first_base;
-    int b = first_request;
-    while (t < t_end) {
-        Range r = visible(p, b);
-        long long n = tiles_of<K::kTile>(r);
-        while (t >= base + n * items) {
-            base += n * items;
-            r = visible(p, ++b);
-            n = tiles_of<K::kTile>(r);
+
+    // Of the segment whose slices are being loaded: the visible range, slices left, the lane's token of the next
+    // slice and where it is, its token of the one after.
+    int lo = 0, hi = 0, left = 0;
+    const int32_t *table = nullptr;
+    const C *kp = nullptr, *vp = nullptr;
+    Places ahead{-1, 0u};
+    Cursor cur{0, 0u, 0u};
+    const unsigned int page_size = (unsigned int)p.c.page_size;
+    const unsigned int tile_pages = K::kTile / page_size, tile_rest = K::kTile % page_size;
+    uint32_t asked[kAsk][NT][2];
+
+    auto visible_token = [&](int tok) { return tok >= lo && tok < hi; };
+    auto look_ahead = [&] {
+        ahead.page = visible_token(cur.tok) ? __ldg(table + cur.j) : -1;
+        ahead.at = cur.at;
+        cur.tok = (int)((unsigned int)cur.tok + K::kTile);
+        cur.j += tile_pages, cur.at += tile_rest;
+        if (cur.at >= page_size) cur.at -= page_size, ++cur.j;
+    };
+    auto load_next = [&](int stage) {
+        if (left > 0) {
+            const Places now = ahead;
+            const bool in = visible_token((int)((unsigned int)cur.tok - K::kTile));
+            look_ahead();
+            const uint32_t mask = load_slice<K, C>(p, now, in, kp, vp, ring + stage * 2 * K::kSliceBytes, lane);
+            if (lane == 0) masks[warp][stage] = mask;
+            --left;
         }
-        const int item = (int)((t - base) / n);
-        const long long item_begin = base + item * n, item_end = item_begin + n;
-        const long long seg_end = min(t_end, item_end);
-        const int count = (int)(seg_end - t);  // tiles of the segment
-        const int kvh = item / p.head_blocks, h0 = kvh * p.group + (item % p.head_blocks) * K::kRows;
-        const int rows = min(K::kRows, (kvh + 1) * p.group - h0);
-        const int lo = (int)r.lo, hi = (int)r.hi;  // lengths fit 31 bits
-        // The warp's first token. Slices behind the last one may begin beyond 31 bits: taken modulo 2^32 they
-        // turn negative and so lie outside [lo, hi).
-        int tok = (int)((unsigned int)(r.lo / K::kTile + (t - item_begin)) * K::kTile + warp * K::kTok);
-        const int32_t *table = p.table + b * p.table_stride;
-        const C *kp = static_cast<const C *>(p.c.k) + kvh * p.c.k_head + lane % kLanes * (16 / K::kBytes);
-        const C *vp = static_cast<const C *>(p.c.v) + kvh * p.c.v_head + lane % kLanes * (16 / K::kBytes);
-
-        // Fill the ring.
-        Places ahead = look_up<K::kTok>(p, table, tok, lo, hi, lane);
-        int loaded = 0;
-        auto load_next = [&](int stage) {
-            if (loaded < count) {
-                const Places now = ahead;
-                const int mine = tok + lane % K::kTok;
-                const bool in = mine >= lo && mine < hi;
-                tok = (int)((unsigned int)tok + K::kTile);
-                ahead = look_up<K::kTok>(p, table, tok, lo, hi, lane);
-                const uint32_t mask = load_slice<K, C>(p, now, in, kp, vp, ring + stage * 2 * K::kSliceBytes, lane);
-                if (lane == 0) masks[warp][stage] = mask;
-                ++loaded;
-            }
-            copies_commit();
-        };
-#pragma unroll 1
-        for (int i = 0; i < K::kStages - 1; ++i) load_next(i);
-
-        // Queries as the B operand: column n = head lane/4, two k of each half. With 8-bit keys the k of a
-        // step are taken in the order in which four consecutive bytes of a row come out of the ring.
-        uint32_t q[kSteps][NT][2];
-        float o[kSteps][NT][4];
-        float m[NT][2], l[NT][2];  // maximum and sum of the thread's two heads (l: of its own rows)
-        float q_scale = 1.f;
+        copies_commit();
+    };
+    // Finds the segment after segs[turn ^ 1], which every thread notes in segs[turn] (the same values).
+    auto find_segment = [&](int turn) {
+        Segment s = segs[turn ^ 1];
+        Range r = visible(p, s.b);
+        int n = (int)tiles_of<K::kTile>(r);
+        while (s.t >= s.base + n * items) {
+            s.base += n * items;
+            r = visible(p, ++s.b);
+            n = (int)tiles_of<K::kTile>(r);
+        }
+        const int item = (s.t - s.base) / n;
+        const int item_begin = s.base + item * n, item_end = item_begin + n;
+        const int seg_end = min(t_end, item_end);
+        s.kvh = item / p.head_blocks;
+        s.h0 = s.kvh * p.group + (item % p.head_blocks) * K::kRows;
+        s.rows = min(K::kRows, (s.kvh + 1) * p.group - s.h0);
+        s.count = seg_end - s.t;
+        s.c_first = (int)((((long long)item_begin + 1) * active - 1) / total);
+        s.parts = (int)(((long long)item_end * active - 1) / total) - s.c_first + 1;
+        lo = (int)r.lo, hi = (int)r.hi;  // lengths fit 31 bits
+        left = s.count;
+        // The lane's first token. Tokens behind the last one may lie beyond 31 bits: taken modulo 2^32 they turn
+        // negative and so are outside [lo, hi).
+        const unsigned int tok =
+            (unsigned int)((int)(r.lo / K::kTile) + (s.t - item_begin)) * K::kTile + warp * K::kTok + lane % K::kTok;
+        cur.tok = (int)tok;
+        cur.j = tok / page_size;
+        cur.at = tok - cur.j * page_size;
+        table = p.table + s.b * p.table_stride;
+        kp = static_cast<const C *>(p.c.k) + s.kvh * p.c.k_head + lane / kLanes * p.c.k_token + lane % kLanes * (16 / K::kBytes);
+        vp = static_cast<const C *>(p.c.v) + s.kvh * p.c.v_head + lane / kLanes * p.c.v_token + lane % kLanes * (16 / K::kBytes);
+        s.t = seg_end;
+        segs[turn] = s;
+        look_ahead();
+    };
+    // Queries as the B operand (column n = head lane/4, two k of each half), in shared memory in the order of the
+    // lanes: [step][lane][NT][2]. With 8-bit keys the k of a step are taken in the order in which four consecutive
+    // bytes of a row come out of the ring. Each warp brings some of the steps: ask_queries() loads them, in front
+    // of the keys, so that they do not queue behind them; put_queries() writes them when the area is free.
+    auto ask_queries = [&](int turn) {
+        const int rows = segs[turn].rows;
+        const T *qs = static_cast<const T *>(p.q) + segs[turn].b * p.q_row + segs[turn].h0 * p.q_head;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int head = nt * 8 + lane / 4;
-            const T *qh = static_cast<const T *>(p.q) + b * p.q_row + (h0 + head) * p.q_head;
-            // A scale of 0 or below turns into queries that are 0 or negated, and a positive scale.
-            const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
+            const T *qh = qs + head * p.q_head;
 #pragma unroll
-            for (int ks = 0; ks < kSteps; ++ks) {
-                const int k0 = ks * 16 + (k8 ? 4 : 2) * (lane % 4);
+            for (int x = 0; x < kAsk; ++x) {
+                const int ks = warp * kAsk + x, k0 = ks * 16 + (k8 ? 4 : 2) * (lane % 4);
                 const bool in = head < rows && ks * 16 < D && p.scale != 0.f;
                 const bool in2 = in && (k8 || ks * 16 + 8 < D);
-                q[ks][nt][0] = in ? *reinterpret_cast<const uint32_t *>(qh + k0) ^ flip : 0u;
-                q[ks][nt][1] = in2 ? *reinterpret_cast<const uint32_t *>(qh + k0 + (k8 ? 2 : 8)) ^ flip : 0u;
-                o[ks][nt][0] = o[ks][nt][1] = o[ks][nt][2] = o[ks][nt][3] = 0.f;
+                asked[x][nt][0] = in ? *reinterpret_cast<const uint32_t *>(qh + k0) : 0u;
+                asked[x][nt][1] = in2 ? *reinterpret_cast<const uint32_t *>(qh + k0 + (k8 ? 2 : 8)) : 0u;
             }
-            m[nt][0] = m[nt][1] = -INFINITY;
-            l[nt][0] = l[nt][1] = 0.f;
         }
+    };
+    uint32_t *q_area = reinterpret_cast<uint32_t *>(mo);
+    auto put_queries = [&] {
+        // A scale of 0 or below turns into queries that are 0 (above) or negated, and a positive scale.
+        const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
+        float result = 1.f, down = 1.f;
         if constexpr (k8 && !std::is_same<T, __half>::value) {
             // bf16 queries against 8-bit keys: keys become fp16 (exact), queries fp16 after a power of two that
             // brings the block's largest below 2; what that loses is 2^-25 of the largest.
             float big = 0.f;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int x = 0; x < kAsk; ++x)
 #pragma unroll
-                for (int ks = 0; ks < kSteps; ++ks)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const float2 f = elem::pair_to_f32<T>(q[ks][nt][x]);
+                    for (int y = 0; y < 2; ++y) {
+                        const float2 f = elem::pair_to_f32<T>(asked[x][nt][y]);
                         big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
                     }
 #pragma unroll
             for (int x = 16; x > 0; x >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
+            if (lane == 0) meet[warp][0].x = big;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < K::kWarps; ++w) big = fmaxf(big, meet[w][0].x);
             const int e = big > 0.f && big < INFINITY ? max(ilogbf(big), -120) : 0;
-            const float down = ldexpf(1.f, -e);
-            q_scale = ldexpf(1.f, e);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int ks = 0; ks < kSteps; ++ks)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const float2 f = elem::pair_to_f32<T>(q[ks][nt][x]);
-                        q[ks][nt][x] = elem::pair_from_f32<__half>(f.x * down, f.y * down);
-                    }
+            down = ldexpf(1.f, -e);
+            result = ldexpf(1.f, e);
         }
+#pragma unroll
+        for (int x = 0; x < kAsk; ++x)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    asked[x][nt][y] ^= flip;
+                    if constexpr (k8 && !std::is_same<T, __half>::value) {
+                        const float2 f = elem::pair_to_f32<T>(asked[x][nt][y]);
+                        asked[x][nt][y] = elem::pair_from_f32<__half>(f.x * down, f.y * down);
+                    }
+                }
+                *reinterpret_cast<uint2 *>(q_area + ((warp * kAsk + x) * 32 + lane) * (2 * NT) + 2 * nt) =
+                    make_uint2(asked[x][nt][0], asked[x][nt][1]);
+            }
+        __syncthreads();
+        return result;
+    };
+    auto queries = [&](int ks, uint32_t (&q)[NT][2]) {
+        const uint32_t *at = q_area + (ks * 32 + lane) * (2 * NT);
+        if constexpr (NT == 1) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(at);
+            q[0][0] = x.x, q[0][1] = x.y;
+        } else {
+#pragma unroll
+            for (int nt = 0; nt < NT; nt += 2) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(at + 2 * nt);
+                q[nt][0] = x.x, q[nt][1] = x.y, q[nt + 1][0] = x.z, q[nt + 1][1] = x.w;
+            }
+        }
+    };
+    auto fill = [&](int stage) {
+#pragma unroll 1
+        for (int i = 0; i < K::kStages - 1; ++i) {
+            load_next(stage);
+            stage = stage + 1 == K::kStages ? 0 : stage + 1;
+        }
+    };
+
+    int stage = 0, turn = 0;
+    bool more = t_begin < t_end;
+    if (more) {
+        find_segment(turn);
+        ask_queries(turn);
+        fill(0);
+    }
+    while (more) {
+        float o[kSteps][NT][4];
+        // Of the thread's two heads: the reference, the score that moves it, what is added to a score's power of
+        // two, and the sum of the weights (of the thread's own rows).
+        float m[NT][2], limit[NT][2], off[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int ks = 0; ks < kSteps; ++ks) o[ks][nt][0] = o[ks][nt][1] = o[ks][nt][2] = o[ks][nt][3] = 0.f;
+            m[nt][0] = m[nt][1] = limit[nt][0] = limit[nt][1] = -INFINITY;
+            off[nt][0] = off[nt][1] = kUp;  // no token so far: all weights are 0 against any reference
+            l[nt][0] = l[nt][1] = 0.f;
+        }
+        const float q_scale = put_queries();
         // Scores in units of log2 are the products times `unit`.
         constexpr float kLog2e = 1.4426950408889634f;
-        const float to_score = (p.scale != 0.f ? fabsf(p.scale) : 1.f) * q_scale * (k8 && p.c.k_scale ? p.c.k_scale[kvh] : 1.f);
+        const float to_score =
+            (p.scale != 0.f ? fabsf(p.scale) : 1.f) * q_scale * (k8 && p.c.k_scale ? p.c.k_scale[segs[turn].kvh] : 1.f);
         const float unit = p.softcap > 0.f ? 1.f : to_score * kLog2e;
+        const float slack = kSlack / unit;
 
-        int stage = 0;
+        const int count = segs[turn].count;
 #pragma unroll 1
         for (int i = 0; i < count; ++i) {
             copies_wait<K::kStages - 2>();
@@ -407,16 +602,17 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, kPerSm) paged_
                 for (int nt = 0; nt < NT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
 #pragma unroll
             for (int ks = 0; ks < kSteps; ks += k8 ? 2 : 1) {
-                if (ks * 16 >= D) break;
+                uint32_t q[k8 ? 2 : 1][NT][2];
+#pragma unroll
+                for (int x = 0; x < (k8 ? 2 : 1); ++x) queries(ks + x, q[x]);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     uint32_t w[4];
+                    ldsm4(w, sk + place<K::kChunks>(mt * 16 + (lane & 15), (k8 ? ks : 2 * ks) + (lane >> 4)));
                     if constexpr (!k8) {
-                        ldsm4(w, sk + place<K::kChunks>(mt * 16 + (lane & 15), ks * 2 + (lane >> 4)));
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma<M>(s[mt][nt], w, q[ks][nt][0], q[ks][nt][1]);
+                        for (int nt = 0; nt < NT; ++nt) mma<M>(s[mt][nt], w, q[0][nt][0], q[0][nt][1]);
                     } else {
-                        ldsm4(w, sk + place<K::kChunks>(mt * 16 + (lane & 15), ks + (lane >> 4)));
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {  // two steps for each four matrices
                             const uint32_t a[4] = {elem::e4m3_to_half2((uint16_t)w[2 * x]),
@@ -424,7 +620,7 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, kPerSm) paged_
                                                    elem::e4m3_to_half2((uint16_t)(w[2 * x] >> 16)),
                                                    elem::e4m3_to_half2((uint16_t)(w[2 * x + 1] >> 16))};
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma<M>(s[mt][nt], a, q[ks + x][nt][0], q[ks + x][nt][1]);
+                            for (int nt = 0; nt < NT; ++nt) mma<M>(s[mt][nt], a, q[x][nt][0], q[x][nt][1]);
                         }
                     }
                 }
@@ -438,7 +634,7 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, kPerSm) paged_
 #pragma unroll
                         for (int x = 0; x < 4; ++x) s[mt][nt][x] = out * tanhf(s[mt][nt][x] * in);
             }
-            if (mask != (K::kTok == 32 ? 0xffffffffu : 0xffffu)) {
+            if (mask != K::kAll) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -447,9 +643,8 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, kPerSm) paged_
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) s[mt][nt][x] = -INFINITY;
             }
-            // Maxima over the slice's tokens, and what the past is worth under the new ones.
-            float keep[NT][2], off[NT][2];
-            bool moved = false;
+            // Where a score has left the reference far behind, the slice's maximum becomes the new one.
+            bool move = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -457,24 +652,31 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, kPerSm) paged_
                     float y = fmaxf(s[0][nt][x], s[0][nt][x + 2]);
 #pragma unroll
                     for (int mt = 1; mt < MT; ++mt) y = fmaxf(y, fmaxf(s[mt][nt][x], s[mt][nt][x + 2]));
-                    y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
-                    y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
-                    y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
-                    y = fmaxf(y, m[nt][x]);
-                    const float top = y == -INFINITY ? 0.f : y;  // no token so far: all weights are 0
-                    keep[nt][x] = exp2_approx((m[nt][x] - top) * unit);
-                    off[nt][x] = kUp - top * unit;
-                    moved |= m[nt][x] != y;
-                    m[nt][x] = y;
+                    move |= y > limit[nt][x];
                 }
-            if (__any_sync(0xffffffffu, moved)) {
+            if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    l[nt][0] *= keep[nt][0], l[nt][1] *= keep[nt][1];
+                    float keep[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float y = fmaxf(s[0][nt][x], s[0][nt][x + 2]);
+#pragma unroll
+                        for (int mt = 1; mt < MT; ++mt) y = fmaxf(y, fmaxf(s[mt][nt][x], s[mt][nt][x + 2]));
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+                        y = fmaxf(y, m[nt][x]);
+                        keep[x] = y == -INFINITY ? 1.f : exp2_approx((m[nt][x] - y) * unit);
+                        m[nt][x] = y;
+                        limit[nt][x] = y + slack;
+                        off[nt][x] = kUp - (y == -INFINITY ? 0.f : y * unit);
+                        l[nt][x] *= keep[x];
+                    }
 #pragma unroll
                     for (int dt = 0; dt < kSteps; ++dt)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) o[dt][nt][x] *= keep[nt][x & 1];
+                        for (int x = 0; x < 4; ++x) o[dt][nt][x] *= keep[x & 1];
                 }
             }
             uint32_t ph[MT][NT][2], pl[kTwo ? MT : 1][kTwo ? NT : 1][2];
@@ -498,8 +700,7 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, kPerSm) paged_
                 }
             // Outputs: 16 elements of the head at a time.
 #pragma unroll
-            for (int dt = 0; dt < kSteps; dt += k8 ? 2 : 1) {
-                if (dt * 16 >= D) break;
+            for (int dt = 0; dt < kSteps; dt += k8 ? 2 : 1)
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     uint32_t w[4];
@@ -523,122 +724,66 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, kPerSm) paged_
                         }
                     }
                 }
-            }
             __syncwarp();  // all lanes have read the stage that is filled next time
             load_next(stage == 0 ? K::kStages - 1 : stage - 1);
             stage = stage + 1 == K::kStages ? 0 : stage + 1;
         }
-        copies_wait<0>();
-        __syncthreads();
+        // Copied before the warps meet: a warp that has met the others may write segs[turn] again.
+        const Segment seg = segs[turn];
+        if (seg.parts > 1 && tid == 0) open[cta == seg.c_first] = seg;
+        // What is loaded from here on belongs to the next segment.
+        turn ^= 1;
+        more = seg.t < t_end;
+        if (more) {
+            find_segment(turn);
+            ask_queries(turn);
+            fill(stage);
+        }
+        __syncthreads();  // all warps are done with the queries
 
-        // The warps' results meet in shared memory (the ring is empty): [warp][row][DT], then maxima, sums.
-        float *mo = reinterpret_cast<float *>(smem);
-        float *mm = mo + K::kWarps * K::kRows * DT, *ml = mm + K::kWarps * K::kRows;
+        // The warps' results meet in shared memory, 8 heads at a time.
+        const Ends<K, T> ends{p, seg, k8 && p.c.v_scale ? p.c.v_scale[seg.kvh] : 1.f};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const int row = nt * 8 + 2 * (lane % 4) + x;
+                const int row = 2 * (lane % 4) + x;
                 float sum = l[nt][x];
                 sum += __shfl_xor_sync(0xffffffffu, sum, 4);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-                if (lane < 4) mm[warp * K::kRows + row] = m[nt][x] * unit, ml[warp * K::kRows + row] = sum;
+                if (lane < 4) meet[warp][row] = make_float2(m[nt][x] * unit, sum);
 #pragma unroll
                 for (int dt = 0; dt < kSteps; ++dt) {
-                    float *to = mo + (warp * K::kRows + row) * DT + dt * 16;
+                    float *to = mo + (warp * 8 + row) * K::kPitch + dt * 16;
                     to[k8 ? 2 * (lane / 4) : lane / 4] = o[dt][nt][x];
                     to[k8 ? 2 * (lane / 4) + 1 : lane / 4 + 8] = o[dt][nt][x + 2];
                 }
             }
-        __syncthreads();
-        const int c_first = (int)(((item_begin + 1) * active - 1) / total), c_last = (int)((item_end * active - 1) / total);
-        const int parts = c_last - c_first + 1;
-        const float v_scale = k8 && p.c.v_scale ? p.c.v_scale[kvh] : 1.f;
-        constexpr float kLn2 = 0.6931471805599453f;
-        // A joined row: o / l, and its lse.
-        auto finish = [&](int row, int d, const Joined &j) {
-            const bool any = j.l > 0.f || j.l != j.l;
-            const float f = any ? v_scale / j.l : 0.f;
-            T *out = static_cast<T *>(p.out) + b * p.o_row + (h0 + row) * p.o_head + d;
-            *reinterpret_cast<uint2 *>(out) =
-                make_uint2(elem::pair_from_f32<T>(j.o.x * f, j.o.y * f), elem::pair_from_f32<T>(j.o.z * f, j.o.w * f));
-            if (p.lse && d == 0)
-                p.lse[(long long)b * p.heads + h0 + row] = any ? (j.m + log2f(j.l) - kUp) * kLn2 : -INFINITY;
-        };
-        // The place of the i-th partial result of this item.
-        auto part = [&](int i) { return p.partial + ((long long)(c_first + i) * 2 + (i == 0)) * kMaxPartial; };
-        auto leave = [&](float *to, int row, int d, const Joined &j, int joined) {
-            __stcg(reinterpret_cast<float4 *>(to + row * DT + d), j.o);
-            if (d == 0)
-                __stcg(reinterpret_cast<float2 *>(to + K::kRows * (DT + 2 * joined) + 2 * row), make_float2(j.m, j.l));
-        };
-        for (int i = tid; i < rows * (DT / 4); i += K::kThreads) {
-            const int row = i / (DT / 4), d = i % (DT / 4) * 4;
-            if (d >= D) continue;
-            Joined j;
+            __syncthreads();
+            for (int i = tid; i < 8 * (DT / 4); i += K::kThreads) {
+                const int row = i / (DT / 4), d = i % (DT / 4) * 4;
+                if (nt * 8 + row >= seg.rows || d >= D) continue;
+                Joined j;
 #pragma unroll
-            for (int w = 0; w < K::kWarps; ++w)
-                j.take(mm[w * K::kRows + row], ml[w * K::kRows + row],
-                       *reinterpret_cast<const float4 *>(mo + (w * K::kRows + row) * DT + d));
-            if (parts == 1) finish(row, d, j);
-            else leave(part(cta - c_first), row, d, j, 0);
-        }
-        if (parts > 1) {
-            // Joined by the last CTA to arrive: first in groups of consecutive CTAs (when there are many), then
-            // over the groups. A CTA is in front of the end of one item only, so counters at its number, one for
-            // items that begin in it and one for the item that does not, are not shared.
-            int group = 8;
-            while (group * group < parts) ++group;
-            const int of = (cta - c_first) / group, in_group = min(group, parts - of * group);
-            const int groups = (parts + group - 1) / group;
-            auto last_of = [&](unsigned int *counter, int n) {
-                __threadfence();
-                __syncthreads();
-                if (tid == 0) {
-                    is_last = atomicAdd(counter, 1u) == (unsigned int)n - 1u;
-                    if (is_last) *counter = 0u;  // ready for the next call
-                }
-                __syncthreads();
-                const bool yes = is_last;
-                if (yes) __threadfence();
-                return yes;
-            };
-            auto join = [&](int from, int step, int n, int joined, bool end) {
-                for (int i = tid; i < rows * (DT / 4); i += K::kThreads) {
-                    const int row = i / (DT / 4), d = i % (DT / 4) * 4;
-                    if (d >= D) continue;
-                    Joined j;
-                    for (int c = 0; c < n; c += 8) {
-                        float2 ml2[8];
-                        float4 y[8];
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            const float *x = part(from + min(c + u, n - 1) * step);
-                            ml2[u] = __ldcg(reinterpret_cast<const float2 *>(x + K::kRows * (DT + 2 * joined) + 2 * row));
-                            y[u] = __ldcg(reinterpret_cast<const float4 *>(x + row * DT + d));
-                        }
-#pragma unroll
-                        for (int u = 0; u < 8; ++u)
-                            if (c + u < n) j.take(ml2[u].x, ml2[u].y, y[u]);
-                    }
-                    if (end) finish(row, d, j);
-                    else leave(part(from), row, d, j, 1);
-                }
-            };
-            unsigned int *counter = of == 0 ? p.counters + c_first : p.counters + kMaxCtas + c_first + of * group;
-            if (last_of(counter, in_group)) {
-                join(of * group, 1, in_group, 0, groups == 1);
-                if (groups > 1 && last_of(p.counters + 2 * kMaxCtas + c_first, groups)) join(0, group, groups, 1, true);
+                for (int w = 0; w < K::kWarps; ++w)
+                    j.take(meet[w][row].x, meet[w][row].y,
+                           *reinterpret_cast<const float4 *>(mo + (w * 8 + row) * K::kPitch + d));
+                if (seg.parts == 1) ends.finish(nt * 8 + row, d, j);
+                else ends.leave(ends.part(cta - seg.c_first), nt * 8 + row, d, j, 0);
             }
-        }
-        t = seg_end;
-        __syncthreads();  // the merge area becomes the ring again
-        if (D < DT && t < t_end) {
-            for (int i = tid; i < K::kWarps * K::kRing / 16; i += K::kThreads)
-                reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
             __syncthreads();
         }
+    }
+    copies_wait<0>();
+    // The parts that are not whole (the first segment and the last at most) are joined behind the loop, where
+    // nothing of it holds registers.
+    __syncthreads();
+#pragma unroll 1
+    for (int x = 0; x < 2; ++x) {
+        const Segment seg = open[x];
+        if (seg.parts < 2) continue;
+        join_parts<K, T>(Ends<K, T>{p, seg, k8 && p.c.v_scale ? p.c.v_scale[seg.kvh] : 1.f}, &is_last);
     }
 }
 
@@ -648,10 +793,13 @@ cudaError_t launch(Params p, int sms, cudaStream_t s) {
     auto kernel = paged_attention_kernel<T, C, DT, NT>;
     cudaError_t e = ensure_max_dyn_smem((const void *)kernel, K::kSmem);
     if (e != cudaSuccess) return e;
+    p.k_page = (unsigned int)p.c.k_page, p.k_token = (unsigned int)p.c.k_token;
+    p.v_page = (unsigned int)p.c.v_page, p.v_token = (unsigned int)p.c.v_token;
     p.head_blocks = (p.group + K::kRows - 1) / K::kRows;
     const long long tiles = ((long long)p.max_pages * p.c.page_size + K::kTile - 1) / K::kTile * p.batch *
                             p.c.kv_heads * p.head_blocks;
-    const int ctas = sms * kPerSm < kMaxCtas ? sms * kPerSm : kMaxCtas;
+    if (tiles >= (1ll << 31)) return cudaErrorInvalidValue;
+    const int ctas = sms * K::kPerSm < kMaxCtas ? sms * K::kPerSm : kMaxCtas;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles < ctas ? tiles : ctas), 1, 1);
     cfg.blockDim = dim3(K::kThreads, 1, 1);

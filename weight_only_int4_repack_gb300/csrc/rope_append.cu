@@ -181,6 +181,8 @@ w4a16_status check_cache(const w4a16_kv_cache *c) {
         return W4A16_ERR_INVALID_ARG;
     for (long long stride : {c->k_page, c->k_token, c->k_head, c->v_page, c->v_token, c->v_head})
         if (stride < 0 || stride % per16) return W4A16_ERR_INVALID_ARG;
+    for (long long stride : {c->k_page, c->k_token, c->k_head, c->v_page, c->v_token, c->v_head})
+        if (stride >= (1LL << 31)) return W4A16_ERR_UNSUPPORTED;
     if (c->head_dim % per16 || c->head_dim > 256) return W4A16_ERR_UNSUPPORTED;
     if ((long long)c->pages * c->page_size > (1LL << 40)) return W4A16_ERR_UNSUPPORTED;
     return W4A16_OK;
