@@ -25,55 +25,66 @@ struct ExtendParams {
     int batch, max_pages, page_size, pool, n_slots;
 };
 
-constexpr int kThreads = 1024;
+constexpr int kMostThreads = 1024;
 constexpr int kMaxBatch = 8192;
 
-// A request's figures, kept in shared memory.
+// A request's figures, kept in shared memory (besides its first token in the step, at
+// most n_slots, in an array of its own: the searches go through that).
 struct Request {
-    int start;   // its first token in the step, at most n_slots
     int len;     // tokens before the step; negative: it gets none (kRefused..., kEnded)
     int held;    // pages before the step
     int page0;   // pages handed out before its first; ended: pages given back before its first
 };
+constexpr int kRequestBytes = sizeof(Request) + sizeof(int);
 constexpr int kRefusedPages = -1, kRefusedRoom = -2, kEnded = -3;
 
-// Inclusive prefix sum over the CTA's threads; *total is the sum of all.
-__device__ __forceinline__ long long scan(long long x, long long *warp_sums, long long *total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Inclusive prefix sums of N values over the CTA's threads; totals are the sums of all.
+template <int N>
+__device__ __forceinline__ void scan(long long (&x)[N], long long (*sums)[32], long long (&totals)[N]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    __syncthreads();  // the last scan's sums have been read
-    if (lane == 31) warp_sums[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        long long s = lane < kThreads / 32 ? warp_sums[lane] : 0;
+    for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += y;
+        for (int n = 0; n < N; ++n) {
+            const long long y = __shfl_up_sync(0xffffffffu, x[n], o);
+            if (lane >= o) x[n] += y;
         }
-        warp_sums[lane] = s;
-    }
+    if (lane == 31)
+#pragma unroll
+        for (int n = 0; n < N; ++n) sums[n][warp] = x[n];
     __syncthreads();
-    *total = warp_sums[kThreads / 32 - 1];
-    return x + (warp ? warp_sums[warp - 1] : 0);
+    long long s[N];  // every warp sums the warps' sums for itself
+#pragma unroll
+    for (int n = 0; n < N; ++n) s[n] = lane < warps ? sums[n][lane] : 0;
+    for (int o = 1; o < warps; o <<= 1)
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const long long y = __shfl_up_sync(0xffffffffu, s[n], o);
+            if (lane >= o) s[n] += y;
+        }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        totals[n] = __shfl_sync(0xffffffffu, s[n], warps - 1);
+        const long long in_front = __shfl_sync(0xffffffffu, s[n], max(warp - 1, 0));
+        if (warp) x[n] += in_front;
+    }
 }
 
-__global__ void __launch_bounds__(kThreads) kv_extend_kernel(const ExtendParams p) {
-    extern __shared__ Request req[];
-    __shared__ long long warp_sums[32];
+__global__ void __launch_bounds__(kMostThreads) kv_extend_kernel(const ExtendParams p) {
+    extern __shared__ int starts[];  // [batch], then the requests
+    Request *req = reinterpret_cast<Request *>(starts + p.batch);
+    __shared__ long long warp_sums[3][32];
     __shared__ long long taken;
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
-    const int ctas = gridDim.x, cta = blockIdx.x, tid = threadIdx.x;
-    const int per = (p.batch + kThreads - 1) / kThreads;  // consecutive requests of a thread
+    const int ctas = gridDim.x, cta = blockIdx.x, tid = threadIdx.x, threads = blockDim.x;
+    if (tid == 0) taken = 0;
+    const int per = (p.batch + threads - 1) / threads;  // consecutive requests of a thread
     const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
-    const long long ps = p.page_size, room = min((long long)p.max_pages * ps, (long long)INT_MAX);
+    const unsigned int ps = (unsigned int)p.page_size;
+    const long long room = min((long long)p.max_pages * ps, (long long)INT_MAX);
     const long long count0 = min(max(p.free_count[0], 0), p.pool);
-    auto pages = [&](long long n) { return (n + ps - 1) / ps; };
+    auto pages = [&](long long n) { return (long long)(((unsigned int)n + ps - 1) / ps); };  // 0 <= n < 2^31
 
     // Tokens and pages given back, in front of each request.
     long long tokens = 0, given = 0;
@@ -82,9 +93,10 @@ __global__ void __launch_bounds__(kThreads) kv_extend_kernel(const ExtendParams 
         if (add > 0) tokens += add;
         if (add < 0) given += min(pages(max(len, 0)), (long long)p.max_pages);
     }
-    long long all_tokens, all_given, all_need;
-    long long start = scan(tokens, warp_sums, &all_tokens) - tokens;
-    long long give = scan(given, warp_sums, &all_given) - given;
+    long long upto2[2] = {tokens, given}, all2[2];
+    scan<2>(upto2, warp_sums, all2);
+    const long long start = upto2[0] - tokens, all_tokens = all2[0], all_given = all2[1];
+    long long give = upto2[1] - given;
     const long long count = min(count0 + all_given, (long long)p.pool);
 
     // What each request needs.
@@ -95,8 +107,9 @@ __global__ void __launch_bounds__(kThreads) kv_extend_kernel(const ExtendParams 
         if (fits) need += pages((long long)len + add) - pages(len);
         if (add > 0) at += add;
     }
-    if (tid == 0) taken = 0;
-    long long upto = scan(need, warp_sums, &all_need) - need;
+    long long upto1[1] = {need}, all1[1];
+    scan<1>(upto1, warp_sums + 2, all1);
+    long long upto = upto1[0] - need, last = 0;
     at = start;
     for (int b = b0; b < b1; ++b) {
         const int len = p.lens[b], add = p.new_tokens[b];
@@ -104,68 +117,115 @@ __global__ void __launch_bounds__(kThreads) kv_extend_kernel(const ExtendParams 
         const long long n = fits ? pages((long long)len + add) - pages(len) : 0;
         const bool got = fits && (n == 0 || upto + n <= count);
         Request r;
-        r.start = (int)min(at, (long long)p.n_slots);
+        starts[b] = (int)min(at, (long long)p.n_slots);
         r.held = (int)min(pages(max(len, 0)), (long long)p.max_pages);
         r.len = got ? len : add < 0 ? kEnded : fits ? kRefusedPages : kRefusedRoom;
         r.page0 = (int)min(add < 0 ? give : upto, (long long)p.pool);
         req[b] = r;
-        if (got && n > 0) atomicMax(&taken, upto + n);
+        if (got && n > 0) last = upto + n;
         if (add < 0) give += r.held;
         if (add > 0) at += add;
         upto += n;
     }
+    // Pages handed out in all: what all need, if that is there.
+    if (all1[0] <= count) {
+        if (tid == 0) taken = all1[0];
+    } else {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
+        if ((tid & 31) == 0 && last) atomicMax(&taken, last);
+    }
     __syncthreads();
 
-    // Pages given back: one warp per ended request.
-    const int lane = tid & 31, gwarp = (tid >> 5) * ctas + cta, gwarps = ctas * (kThreads / 32);
-    for (int b = gwarp; b < p.batch; b += gwarps) {
-        const Request r = req[b];
-        if (r.len != kEnded) continue;
-        const long long to = count0 + r.page0;
-        for (int j = lane; j < r.held; j += 32)
-            if (to + j < p.pool) p.free_pages[to + j] = p.table[(long long)b * p.table_stride + j];
+    // A lane moves the pages of its request, unless they are many: then the warp does.
+    const int lane = tid & 31, gwarp = (tid >> 5) * ctas + cta, gwarps = ctas * (threads / 32);
+    constexpr int kFew = 2;
+    const int share = min(32, max(1, (p.batch + gwarps - 1) / gwarps));  // requests of a warp at a time
+    auto move_pages = [&](int b, int n, auto &&move) {
+        if (n <= kFew)
+            for (int j = 0; j < n; ++j) move(b, j);
+        for (unsigned int many = __ballot_sync(0xffffffffu, n > kFew); many; many &= many - 1) {
+            const int from = __ffs(many) - 1;
+            const int b2 = __shfl_sync(0xffffffffu, b, from), n2 = __shfl_sync(0xffffffffu, n, from);
+            for (int j = lane; j < n2; j += 32) move(b2, j);
+        }
+    };
+    // Pages given back.
+    for (int b0 = gwarp * share; b0 < p.batch; b0 += gwarps * share) {
+        const int b = b0 + lane;
+        move_pages(b, lane < share && b < p.batch && req[b].len == kEnded ? req[b].held : 0, [&](int b2, int j) {
+            const long long to = count0 + req[b2].page0 + j;
+            if (to < p.pool) p.free_pages[to] = p.table[(long long)b2 * p.table_stride + j];
+        });
     }
     __syncwarp();
     ptx::cluster_sync();
 
-    // Pages handed out: the n-th from the top of the list.
+    // Pages handed out: the n-th from the top of the list. Lengths and refusals.
     const long long top = count - 1;
-    for (int b = gwarp; b < p.batch; b += gwarps) {
-        const Request r = req[b];
-        const int add = p.new_tokens[b];
-        if (lane == 0) {
+    for (int b0 = gwarp * share; b0 < p.batch; b0 += gwarps * share) {
+        const int b = b0 + lane;
+        int n = 0;
+        if (lane < share && b < p.batch) {
+            const Request r = req[b];
+            const int add = p.new_tokens[b];
+            if (r.len >= 0) n = (int)pages((long long)r.len + add) - r.held;
             p.lens_out[b] = r.len == kEnded ? 0 : r.len >= 0 ? r.len + add : p.lens[b];
             p.refused[b] = r.len == kRefusedPages ? 1 : r.len == kRefusedRoom ? 2 : 0;
         }
-        if (r.len < 0) continue;
-        const int last = (int)pages((long long)r.len + add);
-        for (int j = r.held + lane; j < last; j += 32)
-            p.table[(long long)b * p.table_stride + j] = __ldcg(p.free_pages + (top - (r.page0 + j - r.held)));
+        move_pages(b, n, [&](int b2, int j) {
+            p.table[(long long)b2 * p.table_stride + req[b2].held + j] = __ldcg(p.free_pages + (top - (req[b2].page0 + j)));
+        });
     }
     if (cta == 0 && tid == 0) p.free_count_out[0] = (int)(count - taken);
 
-    // Every token's place.
-    for (long long t = (long long)cta * kThreads + tid; t < p.n_slots; t += (long long)ctas * kThreads) {
-        long long slot = -1;
-        int pos = 0;
-        if (t < all_tokens) {
-            int lo = 0, hi = p.batch - 1;  // the last request that starts at or before t
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) / 2;
-                if (req[mid].start <= t) lo = mid;
-                else hi = mid - 1;
-            }
+    // Every token's place. A warp takes consecutive groups of 32 tokens: it searches for the first one's request,
+    // and from there on a group's requests are among the next 32, one to a lane. The looks at the table of kAt
+    // groups are on their way together.
+    constexpr int kAt = 4;
+    const int all_groups = (int)(((long long)p.n_slots + 31) / 32), groups = (all_groups + gwarps - 1) / gwarps;
+    const int g_begin = min((int)min((long long)gwarp * groups, (long long)INT_MAX), all_groups), g_end = min(g_begin + groups, all_groups);
+    auto search = [&](int t) {  // the last request that starts at or before t
+        int lo = 0, hi = p.batch - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (starts[mid] <= t) lo = mid;
+            else hi = mid - 1;
+        }
+        return lo;
+    };
+    int first = g_begin < g_end ? search(g_begin * 32) : 0;
+    for (int g = g_begin; g < g_end; g += kAt) {
+        int page[kAt], pos[kAt];
+#pragma unroll
+        for (int x = 0; x < kAt; ++x) {
+            pos[x] = -1, page[x] = 0;
+            if (g + x >= g_end) continue;
+            const int t = (g + x) * 32 + lane;  // below 2^31: a group behind n_slots does not exist
+            const int start = first + 1 + lane < p.batch ? starts[first + 1 + lane] : INT_MAX;
+            int c = 0;  // how many of the 32 start at or before t
+#pragma unroll
+            for (int step = 16; step; step >>= 1)
+                if (__shfl_sync(0xffffffffu, start, c + step - 1) <= t) c += step;
+            if (__shfl_sync(0xffffffffu, start, c) <= t) ++c;
+            int lo = first + c;
+            if (c == 32) lo = search(t);  // many requests without tokens
+            first = __shfl_sync(0xffffffffu, lo, 31);
             const Request r = req[lo];
-            if (r.len >= 0) {
-                pos = r.len + (int)(t - r.start);
-                const int j = (int)(pos / ps);
-                const int page = j < r.held ? p.table[(long long)lo * p.table_stride + j]
-                                            : __ldcg(p.free_pages + (top - (r.page0 + j - r.held)));
-                slot = (long long)page * ps + pos % ps;
+            if (t < all_tokens && t < p.n_slots && r.len >= 0) {
+                pos[x] = r.len + (t - starts[lo]);
+                const int j = (int)((unsigned int)pos[x] / ps);
+                page[x] = j < r.held ? p.table[(long long)lo * p.table_stride + j]
+                                     : __ldcg(p.free_pages + (top - (r.page0 + j - r.held)));
             }
         }
-        p.slots[t] = slot;
-        p.positions[t] = pos;
+#pragma unroll
+        for (int x = 0; x < kAt; ++x) {
+            const int t = (g + x) * 32 + lane;
+            if (g + x >= g_end || t >= p.n_slots || t < 0) continue;
+            p.slots[t] = pos[x] < 0 ? -1ll : (long long)page[x] * ps + (unsigned int)pos[x] % ps;
+            p.positions[t] = max(pos[x], 0);
+        }
     }
 }
 
@@ -181,7 +241,7 @@ extern "C" w4a16_status w4a16_kv_extend(const int32_t *lens, const int32_t *new_
                                         int32_t *refused, void *stream) {
     if (batch < 0 || max_pages <= 0 || page_size <= 0 || pool <= 0 || n_slots < 0 || table_stride < max_pages)
         return W4A16_ERR_INVALID_ARG;
-    if (batch > kMaxBatch) return W4A16_ERR_UNSUPPORTED;
+    if (batch > kMaxBatch || n_slots > INT_MAX - 63) return W4A16_ERR_UNSUPPORTED;
     if (batch == 0) return W4A16_OK;
     if (!lens || !new_tokens || !table || !free_pages || !free_count || !lens_out || !free_count_out || !refused ||
         (n_slots && (!slots || !positions)))
@@ -194,13 +254,15 @@ extern "C" w4a16_status w4a16_kv_extend(const int32_t *lens, const int32_t *new_
     const ExtendParams p{lens,      new_tokens, free_count, table,        free_pages, lens_out,  free_count_out,
                          positions, refused,    slots,      table_stride, batch,      max_pages, page_size,
                          pool,      n_slots};
-    cudaError_t e = ensure_max_dyn_smem((const void *)kv_extend_kernel, kMaxBatch * (int)sizeof(Request));
+    cudaError_t e = ensure_max_dyn_smem((const void *)kv_extend_kernel, kMaxBatch * kRequestBytes);
     if (e != cudaSuccess) return from_cuda(e);
+    // A step of running requests fits one CTA, and a small one is done sooner with fewer warps to wait for.
     const int ctas = batch <= 1024 && n_slots <= 4096 ? 1 : 8;
+    const int threads = batch <= 128 && n_slots <= 1024 ? 256 : batch <= 512 && n_slots <= 4096 ? 512 : kMostThreads;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = (size_t)batch * sizeof(Request);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)batch * kRequestBytes;
     cfg.stream = (cudaStream_t)stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;

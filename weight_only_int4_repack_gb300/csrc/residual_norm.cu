@@ -20,7 +20,6 @@ struct NormParams {
     float alpha, eps;
 };
 
-constexpr int kThreads = 512;
 constexpr int kMaxK = 32768;
 
 // Sum over the CTA, the same in every thread and in the same order on every run.
@@ -29,52 +28,81 @@ __device__ __forceinline__ float cta_sum(float x, float *red) {
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
     __syncthreads();
-    float s = 0.f;
-    for (int w = 0; w < kThreads / 32; ++w) s += red[w];
-    return s;
+    x = threadIdx.x % 32 < blockDim.x / 32 ? red[threadIdx.x % 32] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
 }
 
-// One CTA per row; thread t holds the 8-element groups t, t + 512, ...
-template <typename T, typename H, int V>
-__global__ void __launch_bounds__(kThreads) residual_norm_kernel(const NormParams p) {
+// Eight elements as they are in memory.
+template <typename T>
+struct Raw {
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) w[i] = reinterpret_cast<const uint4 *>(p)[i];
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        elem::Vec<T, 8>::load(reinterpret_cast<const T *>(w), f);
+    }
+};
+
+// One CTA per row; thread t holds the 8-element groups t, t + blockDim, ... All that
+// the row needs from HBM is asked for before the first sum.
+template <typename T, typename H, int V, int kMost>
+__global__ void __launch_bounds__(kMost) residual_norm_kernel(const NormParams p) {
     using VT = elem::Vec<T, 8>;
     using VH = elem::Vec<H, 8>;
-    __shared__ float red[2][kThreads / 32];
+    __shared__ float red[2][32];
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     const long long row = blockIdx.x;
-    const int groups = p.K / 8;
+    const int groups = p.K / 8, threads = blockDim.x;
     const T *y = static_cast<const T *>(p.y) + row * p.y_row;
     const H *h = static_cast<const H *>(p.h) + row * p.h_row;
-    float x[V][8];
-    float ss = 0.f;
+    const T *gate = static_cast<const T *>(p.gate) + row * p.gate_row;
+    Raw<T> ry[V], rg[V];
+    Raw<H> rh[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int g = threadIdx.x + v * kThreads;
-        if (g >= groups) break;
-        VT::load(y + 8 * g, x[v]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[v][e], x[v][e], ss);
+        const int g = threadIdx.x + v * threads;
+        if (g < groups) {
+            ry[v].load(y + 8 * g);
+            rh[v].load(h + 8 * g);
+            if (p.gate) rg[v].load(gate + 8 * g);
+        }
     }
     float r = 1.f;
-    if (p.post) r = 1.0f / sqrtf(cta_sum(ss, red[0]) / (float)p.K + p.eps);
-    ss = 0.f;
+    if (p.post) {
+        float ss = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (threadIdx.x + v * threads < groups) {
+                float f[8];
+                ry[v].get(f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
+            }
+        r = 1.0f / sqrtf(cta_sum(ss, red[0]) / (float)p.K + p.eps);
+    }
+    float x[V][8], ss = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int g = threadIdx.x + v * kThreads;
+        const int g = threadIdx.x + v * threads;
         if (g >= groups) break;
         float f[8];
+        ry[v].get(x[v]);
         if (p.post) {
             VT::load(static_cast<const T *>(p.post) + 8 * g, f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[v][e] *= r * f[e];
         }
         if (p.gate) {
-            VT::load(static_cast<const T *>(p.gate) + row * p.gate_row + 8 * g, f);
+            rg[v].get(f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[v][e] *= f[e];
         }
-        VH::load(h + 8 * g, f);
+        rh[v].get(f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             x[v][e] = fmaf(p.alpha, x[v][e], f[e]);
@@ -86,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) residual_norm_kernel(const NormParam
     r = 1.0f / sqrtf(cta_sum(ss, red[1]) / (float)p.K + p.eps);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int g = threadIdx.x + v * kThreads;
+        const int g = threadIdx.x + v * threads;
         if (g >= groups) break;
         float f[8];
         VT::load(static_cast<const T *>(p.gamma) + 8 * g, f);
@@ -98,20 +126,26 @@ __global__ void __launch_bounds__(kThreads) residual_norm_kernel(const NormParam
 
 template <typename T, typename H>
 cudaError_t launch(const NormParams &p, int M, cudaStream_t s) {
+    // Few rows: as many threads as there are groups, for the shortest way through a row. Many rows: fewer
+    // threads with more loads in flight each, and more rows on an SM at different stages.
+    const int groups = p.K / 8;
+    const bool many = M > 2 * sm_count() && groups > 256 && groups <= 1024;
+    const int v = many ? (groups > 512 ? 4 : 2) : groups <= 1024 ? 1 : groups <= 2048 ? 2 : 4;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)M, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3((unsigned)((groups + v - 1) / v + 31) / 32 * 32, 1, 1);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = launch_overlap() ? 1 : 0;
-    const int v = (p.K / 8 + kThreads - 1) / kThreads;
-    if (v <= 1) return cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, H, 1>, p);
-    if (v <= 2) return cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, H, 2>, p);
-    if (v <= 4) return cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, H, 4>, p);
-    return cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, H, 8>, p);
+    if (many)
+        return v == 4 ? cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, H, 4, 256>, p)
+                      : cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, H, 2, 256>, p);
+    if (v == 1) return cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, H, 1, 1024>, p);
+    if (v == 2) return cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, H, 2, 1024>, p);
+    return cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, H, 4, 1024>, p);
 }
 
 }  // namespace

@@ -7,9 +7,10 @@
 //
 // The angle: a position times a frequency passes 2^24 times the spacing that fp32
 // has near it, so the product is taken modulo one turn in 64-bit fixed point.
-// F = frac(inv_freq / 2 pi) * 2^64 (fp64, once per frequency); position * F modulo
-// 2^64 is one integer multiplication and drops whole turns exactly; its upper 32
-// bits, signed, are the angle in units of 2^-32 turns.
+// F = inv_freq / (2 pi) * 2^64 modulo 2^64, one integer product of the frequency's
+// 24-bit mantissa and the first 64 bits of 1 / (2 pi); position * F modulo 2^64 is
+// another one and drops whole turns exactly; its upper 32 bits, signed, are the angle
+// in units of 2^-32 turns. No fp64, of which the GPU has little.
 #include <cmath>
 
 #include "elem.cuh"
@@ -29,32 +30,201 @@ struct RopeParams {
     const float *inv_freq;
     const int64_t *slots;
     w4a16_kv_cache c;
-    int rows, heads, rot;
+    int rows, heads, rot, split;
     float mscale;
     unsigned int *err;
 };
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kMaxHalf = 128;  // rot_dim / 2 at most
 
-// cos and sin of frequency i at `pos`, times mscale.
+// cos and sin of frequency `inv_freq` at `pos`, times mscale.
 __device__ __forceinline__ float2 rotation(float inv_freq, int pos, float mscale) {
-    double turns = (double)inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
-    turns -= floor(turns);
-    const unsigned long long F = __double2ull_rd(turns * 18446744073709551616.0);
+    const uint32_t bits = __float_as_uint(inv_freq), exponent = (bits >> 23) & 0xffu;
+    const unsigned long long mant = (bits & 0x7fffffu) | (exponent ? 0x800000u : 0u);
+    const unsigned long long kTurn = 0x28BE60DB9391054Aull;  // 2^64 / (2 pi)
+    // mant * kTurn * 2^(exponent - 150), modulo 2^64
+    const unsigned long long lo = mant * kTurn, hi = __umul64hi(mant, kTurn);
+    const int s = 150 - (int)(exponent ? exponent : 1u);
+    unsigned long long F = s <= 0 ? (s > -64 ? lo << -s : 0ull)
+                         : s < 64 ? (lo >> s) | (hi << (64 - s)) : s < 128 ? hi >> (s - 64) : 0ull;
+    if (bits >> 31) F = 0ull - F;
     const unsigned long long part = (unsigned long long)(long long)pos * F;
     const float half_turns = (float)(int)(part >> 32) * 4.656612873077393e-10f;  // 2^-31
-    float s, c;
-    sincospif(half_turns, &s, &c);
-    return make_float2(c * mscale, s * mscale);
+    float s1, c1;
+    sincospif(half_turns, &s1, &c1);
+    return make_float2(c1 * mscale, s1 * mscale);
 }
 
-// One CTA per row. A head's work is cut into units: rot/2/VEC units that each turn
-// VEC pairs, then units that copy VEC elements.
-template <typename T, typename C, int VEC, bool kPairs>
+// The row's place in the cache: false where its keys and values are not written.
+struct Place {
+    long long page, token;
+};
+__device__ __forceinline__ bool place_of(const RopeParams &p, long long slot, Place &at) {
+    if (slot < 0) return false;
+    if (slot >= (long long)p.c.pages * p.c.page_size) {
+        atomicExch(p.err, (unsigned int)W4A16_ERR_INVALID_ARG);
+        return false;
+    }
+    if (slot < (1ll << 31)) {
+        const unsigned int page = (unsigned int)slot / (unsigned int)p.c.page_size;
+        at.page = page, at.token = (unsigned int)slot - page * (unsigned int)p.c.page_size;
+    } else {
+        at.page = slot / p.c.page_size, at.token = slot % p.c.page_size;
+    }
+    return true;
+}
+
+// rot_dim a multiple of 16, everything 16-byte aligned. p.split warps share a row. A
+// unit is 16 elements of a head as two groups a and b of 8, a lane's: eight pairs
+// between a and b (halves), or four in each (neighbours), always those of frequencies
+// 8u..8u+7; or elements behind rot_dim, and of v, which only get their bias. So a lane
+// has the same frequencies for every head, in registers; a warp's lanes cover several
+// heads at once, and the next heads are loaded while these are turned.
+template <typename T, typename C, bool kPairs>
+__global__ void __launch_bounds__(kThreads, 6) rope_append_wide_kernel(const RopeParams p) {
+    using VT = elem::Vec<T, 8>;
+    using VC = elem::Vec<C, 8>;
+    __shared__ float2 cs[kThreads / 32][kMaxHalf];
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long id = (long long)blockIdx.x * (kThreads / 32) + warp;
+    const int row = (int)(id / p.split), part = (int)(id - (long long)row * p.split);
+    if (row >= p.rows) return;
+    const int D = p.c.head_dim, half = p.rot / 2, kv = p.c.kv_heads;
+    const int units = (D + 15) / 16, at_once = 32 / units;  // units of a head, heads of a warp
+    const int sub = lane / units, u = lane - sub * units;
+    const bool active = sub < at_once;
+    const int pos = p.positions[row];
+    const long long slot = p.slots[row];
+
+    // Passes: at_once heads of q each, then of k, then of v. Elements that the lane's groups begin at: of q and k
+    // heads, and 16u, 16u + 8 of v heads; b may lie behind the head.
+    const int q_passes = (p.heads + at_once - 1) / at_once, kv_passes = (kv + at_once - 1) / at_once;
+    const int passes = q_passes + 2 * kv_passes;
+    const bool turns = 16 * u < p.rot;
+    const int qa = kPairs || !turns ? 16 * u : 8 * u, qb = kPairs || !turns ? qa + 8 : qa + half;
+    uint4 ra[2], rb[2];  // two passes on their way
+    auto load = [&](int x, int pass) {
+        if (pass >= passes) return;
+        const T *src;
+        int left, a = qa, b = qb;  // heads from the pass's first on
+        if (pass < q_passes) {
+            left = p.heads - pass * at_once;
+            src = static_cast<const T *>(p.q) + row * p.q_row + pass * at_once * p.q_head + sub * p.q_head;
+        } else if (pass < q_passes + kv_passes) {
+            const int first = (pass - q_passes) * at_once;
+            left = kv - first;
+            src = static_cast<const T *>(p.k) + row * p.k_row + first * p.k_head + sub * p.k_head;
+        } else {
+            const int first = (pass - q_passes - kv_passes) * at_once;
+            left = kv - first;
+            src = static_cast<const T *>(p.v) + row * p.v_row + first * p.v_head + sub * p.v_head;
+            a = 16 * u, b = a + 8;
+        }
+        if (!active || sub >= left) return;
+        ra[x] = *reinterpret_cast<const uint4 *>(src + a);
+        if (b < D) rb[x] = *reinterpret_cast<const uint4 *>(src + b);
+    };
+    load(0, part);
+    load(1, part + p.split);
+
+    for (int i = lane; i < half; i += 32) cs[warp][i] = rotation(p.inv_freq[i], pos, p.mscale);
+    Place at{0, 0};
+    const bool writes = place_of(p, slot, at);
+    __syncwarp();
+    float co[8], si[8];
+    if (turns) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) co[e] = cs[warp][8 * u + e].x, si[e] = cs[warp][8 * u + e].y;
+    }
+
+    auto add_bias = [&](int head, int ia, int ib, float (&a)[8], float (&b)[8]) {
+        if (!p.bias) return;
+        float f[8];
+        const T *bias = static_cast<const T *>(p.bias) + head * D;
+        VT::load(bias + ia, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] += f[e];
+        if (ib < D) {
+            VT::load(bias + ib, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) b[e] += f[e];
+        }
+    };
+    auto turn = [&](float (&a)[8], float (&b)[8]) {
+        if (!turns) return;
+        if (kPairs) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float xa = a[2 * e], xb = b[2 * e];
+                a[2 * e] = xa * co[e] - a[2 * e + 1] * si[e];
+                a[2 * e + 1] = a[2 * e + 1] * co[e] + xa * si[e];
+                b[2 * e] = xb * co[4 + e] - b[2 * e + 1] * si[4 + e];
+                b[2 * e + 1] = b[2 * e + 1] * co[4 + e] + xb * si[4 + e];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float xa = a[e];
+                a[e] = xa * co[e] - b[e] * si[e];
+                b[e] = b[e] * co[e] + xa * si[e];
+            }
+        }
+    };
+    auto to_cache = [&](void *pool, long long page_stride, long long token_stride, long long head_stride, const float *scale,
+                        int head, int ia, int ib, float (&a)[8], float (&b)[8]) {
+        C *dst = static_cast<C *>(pool) + at.page * page_stride + at.token * token_stride + head * head_stride;
+        if (scale) {
+            const float r = 1.0f / scale[head];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) a[e] *= r, b[e] *= r;
+        }
+        VC::store(dst + ia, a);
+        if (ib < D) VC::store(dst + ib, b);
+    };
+    for (int pass0 = part; pass0 < passes; pass0 += 2 * p.split) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int pass = pass0 + x * p.split;
+            if (pass >= passes) break;
+            float a[8], b[8];
+            VT::load(reinterpret_cast<const T *>(&ra[x]), a);
+            VT::load(reinterpret_cast<const T *>(&rb[x]), b);
+            load(x, pass + 2 * p.split);
+            if (!active) continue;
+            if (pass < q_passes) {
+                const int head = pass * at_once + sub;
+                if (head >= p.heads) continue;
+                add_bias(head, qa, qb, a, b);
+                turn(a, b);
+                T *dst = static_cast<T *>(p.q_out) + row * p.qo_row + pass * at_once * p.qo_head + sub * p.qo_head;
+                VT::store(dst + qa, a);
+                if (qb < D) VT::store(dst + qb, b);
+            } else if (pass < q_passes + kv_passes) {
+                const int head = (pass - q_passes) * at_once + sub;
+                if (head >= kv || !writes) continue;
+                add_bias(p.heads + head, qa, qb, a, b);
+                turn(a, b);
+                to_cache(p.c.k, p.c.k_page, p.c.k_token, p.c.k_head, p.c.k_scale, head, qa, qb, a, b);
+            } else {
+                const int head = (pass - q_passes - kv_passes) * at_once + sub;
+                if (head >= kv || !writes) continue;
+                add_bias(p.heads + kv + head, 16 * u, 16 * u + 8, a, b);
+                to_cache(p.c.v, p.c.v_page, p.c.v_token, p.c.v_head, p.c.v_scale, head, 16 * u, 16 * u + 8, a, b);
+            }
+        }
+    }
+}
+
+// Any alignment of 4 bytes and rot_dim a multiple of 4: two elements at a time, one CTA
+// per row. A head's work is rot/4 units that turn two pairs each, then units that copy
+// two elements.
+template <typename T, typename C, bool kPairs>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams p) {
-    using VT = elem::Vec<T, VEC>;
-    using VC = elem::Vec<C, VEC>;
+    using VT = elem::Vec<T, 2>;
+    using VC = elem::Vec<C, 2>;
     __shared__ float2 cs[kMaxHalf];
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
@@ -62,65 +232,49 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
     const int half = p.rot / 2, D = p.c.head_dim;
     const int pos = p.positions[row];
     for (int i = threadIdx.x; i < half; i += kThreads) cs[i] = rotation(p.inv_freq[i], pos, p.mscale);
-    long long slot = p.slots[row];
-    if (slot >= (long long)p.c.pages * p.c.page_size) {
-        if (threadIdx.x == 0) atomicExch(p.err, (unsigned int)W4A16_ERR_INVALID_ARG);
-        slot = -1;
-    }
-    const long long page = slot < 0 ? 0 : slot / p.c.page_size;
-    const long long token = slot < 0 ? 0 : slot % p.c.page_size;
+    Place at{0, 0};
+    const bool writes = place_of(p, p.slots[row], at);
     __syncthreads();
 
-    const int turn_units = half / VEC, units = turn_units + (D - p.rot) / VEC;
-    const int v_units = D / VEC;
+    const int turn_units = half / 2, units = turn_units + (D - p.rot) / 2, v_units = D / 2;
     const int nq = p.heads * units, nk = p.c.kv_heads * units, nv = p.c.kv_heads * v_units;
     for (int j = threadIdx.x; j < nq + nk + nv; j += kThreads) {
         const bool is_q = j < nq, is_v = j >= nq + nk;
         const int i = is_q ? j : is_v ? j - nq - nk : j - nq;
         const int per = is_v ? v_units : units;
         const int head = i / per, u = i - head * per;
-        if (!is_q && slot < 0) continue;
+        if (!is_q && !writes) continue;
         const T *src = is_q ? static_cast<const T *>(p.q) + row * p.q_row + head * p.q_head
                      : is_v ? static_cast<const T *>(p.v) + row * p.v_row + head * p.v_head
                             : static_cast<const T *>(p.k) + row * p.k_row + head * p.k_head;
         const int bias_head = is_q ? head : is_v ? p.heads + p.c.kv_heads + head : p.heads + head;
         const T *bias = p.bias ? static_cast<const T *>(p.bias) + bias_head * D : nullptr;
         const bool turn = !is_v && u < turn_units;
-        // The unit's two groups of VEC elements (copies have one).
-        const int lo = is_v ? u * VEC : turn ? (kPairs ? 2 * VEC * u : VEC * u) : p.rot + (u - turn_units) * VEC;
-        const int hi = kPairs ? lo + VEC : lo + half;
-        float a[VEC], b[VEC];
+        // The unit's two groups of two elements (copies have one).
+        const int lo = is_v ? 2 * u : turn ? (kPairs ? 4 * u : 2 * u) : p.rot + (u - turn_units) * 2;
+        const int hi = kPairs ? lo + 2 : lo + half;
+        float a[2], b[2] = {0.f, 0.f};
         VT::load(src + lo, a);
         if (turn) VT::load(src + hi, b);
         if (bias) {
-            float f[VEC];
+            float f[2];
             VT::load(bias + lo, f);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) a[e] += f[e];
+            a[0] += f[0], a[1] += f[1];
             if (turn) {
                 VT::load(bias + hi, f);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) b[e] += f[e];
+                b[0] += f[0], b[1] += f[1];
             }
         }
         if (turn) {
-            const float2 *w = cs + u * VEC;
+            const float2 w0 = cs[2 * u], w1 = cs[2 * u + 1];
             if (kPairs) {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {  // pair e of the 2*VEC elements a, b
-                    float &x = (2 * e < VEC) ? a[2 * e % VEC] : b[2 * e % VEC];
-                    float &y = (2 * e < VEC) ? a[2 * e % VEC + 1] : b[2 * e % VEC + 1];
-                    const float x1 = x * w[e].x - y * w[e].y;
-                    y = y * w[e].x + x * w[e].y;
-                    x = x1;
-                }
+                const float xa = a[0], xb = b[0];
+                a[0] = xa * w0.x - a[1] * w0.y, a[1] = a[1] * w0.x + xa * w0.y;
+                b[0] = xb * w1.x - b[1] * w1.y, b[1] = b[1] * w1.x + xb * w1.y;
             } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float x1 = a[e] * w[e].x - b[e] * w[e].y;
-                    b[e] = b[e] * w[e].x + a[e] * w[e].y;
-                    a[e] = x1;
-                }
+                const float x0 = a[0], x1 = a[1];
+                a[0] = x0 * w0.x - b[0] * w0.y, a[1] = x1 * w1.x - b[1] * w1.y;
+                b[0] = b[0] * w0.x + x0 * w0.y, b[1] = b[1] * w1.x + x1 * w1.y;
             }
         }
         if (is_q) {
@@ -128,16 +282,12 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
             VT::store(dst + lo, a);
             if (turn) VT::store(dst + hi, b);
         } else {
-            C *dst = is_v ? static_cast<C *>(p.c.v) + page * p.c.v_page + token * p.c.v_token + head * p.c.v_head
-                          : static_cast<C *>(p.c.k) + page * p.c.k_page + token * p.c.k_token + head * p.c.k_head;
+            C *dst = is_v ? static_cast<C *>(p.c.v) + at.page * p.c.v_page + at.token * p.c.v_token + head * p.c.v_head
+                          : static_cast<C *>(p.c.k) + at.page * p.c.k_page + at.token * p.c.k_token + head * p.c.k_head;
             const float *scale = is_v ? p.c.v_scale : p.c.k_scale;
             if (scale) {
-                const float s = scale[head];
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    a[e] = a[e] / s;
-                    if (turn) b[e] = b[e] / s;
-                }
+                const float r = 1.0f / scale[head];
+                a[0] *= r, a[1] *= r, b[0] *= r, b[1] *= r;
             }
             VC::store(dst + lo, a);
             if (turn) VC::store(dst + hi, b);
@@ -145,10 +295,9 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
     }
 }
 
-template <typename T, typename C, int VEC>
-cudaError_t launch(const RopeParams &p, bool pairs, cudaStream_t s) {
+template <typename T, typename C>
+cudaError_t launch(RopeParams p, bool pairs, bool wide, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.rows, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -156,15 +305,27 @@ cudaError_t launch(const RopeParams &p, bool pairs, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = launch_overlap() ? 1 : 0;
-    return pairs ? cudaLaunchKernelEx(&cfg, rope_append_kernel<T, C, VEC, true>, p)
-                 : cudaLaunchKernelEx(&cfg, rope_append_kernel<T, C, VEC, false>, p);
+    if (!wide) {
+        cfg.gridDim = dim3((unsigned)p.rows, 1, 1);
+        return pairs ? cudaLaunchKernelEx(&cfg, rope_append_kernel<T, C, true>, p)
+                     : cudaLaunchKernelEx(&cfg, rope_append_kernel<T, C, false>, p);
+    }
+    // Rows are split over warps until there are 48 warps for an SM, two rounds of the 28 that it holds, so that
+    // the last round does not leave it half empty; down to one pass of a row for each warp.
+    const int at_once = 32 / ((p.c.head_dim + 15) / 16);
+    const int passes = (p.heads + at_once - 1) / at_once + 2 * ((p.c.kv_heads + at_once - 1) / at_once);
+    p.split = 1;
+    while (p.split < passes && (long long)p.rows * p.split < 48ll * sm_count()) p.split *= 2;
+    if (p.split > passes) p.split = passes;
+    const long long warps = (long long)p.rows * p.split;
+    cfg.gridDim = dim3((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)), 1, 1);
+    return pairs ? cudaLaunchKernelEx(&cfg, rope_append_wide_kernel<T, C, true>, p)
+                 : cudaLaunchKernelEx(&cfg, rope_append_wide_kernel<T, C, false>, p);
 }
 
 template <typename T>
 cudaError_t launch_type(const RopeParams &p, bool pairs, bool wide, cudaStream_t s) {
-    if (p.c.type == W4A16_TYPE_E4M3)
-        return wide ? launch<T, E4M3, 8>(p, pairs, s) : launch<T, E4M3, 2>(p, pairs, s);
-    return wide ? launch<T, T, 8>(p, pairs, s) : launch<T, T, 2>(p, pairs, s);
+    return p.c.type == W4A16_TYPE_E4M3 ? launch<T, E4M3>(p, pairs, wide, s) : launch<T, T>(p, pairs, wide, s);
 }
 
 }  // namespace
@@ -240,7 +401,7 @@ w4a16_status w4a16_rope_append(const void *q, const void *k, const void *v, w4a1
         wide = wide && s % 8 == 0;
     }
     RopeParams p{q, k, v, bias, q_out, q_row, q_head, k_row, k_head, v_row, v_head, qo_row, qo_head,
-                 positions, inv_freq, slots, *cache, rows, heads, rot_dim, mscale, device_error_ptr()};
+                 positions, inv_freq, slots, *cache, rows, heads, rot_dim, 1, mscale, device_error_ptr()};
     if (!p.err) return W4A16_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
     return from_cuda(type == W4A16_TYPE_F16 ? launch_type<__half>(p, interleaved != 0, wide, s)
