@@ -67,6 +67,7 @@ class LaunchInfo(ctypes.Structure):
         return {k: getattr(self, k) for k, _ in self._fields_}
 
 
+_int32, _int64, _float32 = torch.int32, torch.int64, torch.float32
 _TYPES = {torch.float16: W4A16_TYPE_F16, torch.bfloat16: W4A16_TYPE_BF16,
           torch.float8_e4m3fn: W4A16_TYPE_E4M3, torch.float32: W4A16_TYPE_F32}
 
@@ -167,9 +168,16 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+# The current stream as a number. torch.cuda.current_stream() builds a Stream object for it, about 3 us a call on the
+# host, as long as a small kernel runs; the getter behind it takes 0.1.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
+        if _raw_stream is not None and _current_device is not None:
+            return _raw_stream(_current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
@@ -350,15 +358,17 @@ def w4a16_kv_extend(lens, new_tokens, table, free_pages, free_count, page_size: 
     lens_out = lens if lens_out is None else lens_out
     count_out = free_count if count_out is None else count_out
     batch, max_pages = table.shape
-    for t in (lens, new_tokens, free_pages, free_count, positions, refused, lens_out, count_out):
-        _expect(t, torch.int32, "w4a16_kv_extend")
-    _expect(slots, torch.int64, "slots")
+    if not (lens.dtype is new_tokens.dtype is free_pages.dtype is free_count.dtype is positions.dtype is refused.dtype
+            is lens_out.dtype is count_out.dtype is table.dtype is _int32) or slots.dtype is not _int64:
+        raise TypeError("w4a16_kv_extend: slots is int64, everything else int32")
     n_slots = slots.numel()
-    if (table.dtype is not torch.int32 or (max_pages > 1 and table.stride(1) != 1)
+    if (not (lens.is_contiguous() and new_tokens.is_contiguous() and free_pages.is_contiguous() and slots.is_contiguous()
+             and positions.is_contiguous() and refused.is_contiguous() and lens_out.is_contiguous())
+            or (max_pages > 1 and table.stride(1) != 1)
             or not lens.numel() == new_tokens.numel() == refused.numel() == lens_out.numel() == batch
             or positions.numel() != n_slots):
-        raise ValueError("w4a16_kv_extend: table is int32 [batch, max_pages], the others have one entry for each "
-                         "request or slot")
+        raise ValueError("w4a16_kv_extend: table is [batch, max_pages], the others are contiguous with one entry for "
+                         "each request or slot")
     _check(lib.w4a16_kv_extend(lens.data_ptr(), new_tokens.data_ptr(), table.data_ptr(),
                                table.stride(0) if batch > 1 else max_pages, batch,
                                max_pages, page_size, free_pages.data_ptr(), free_pages.numel(),
@@ -385,9 +395,9 @@ def w4a16_rope_append(q, k, v, positions, inv_freq, cache, slots, interleaved: b
     rows, heads, D = q.shape
     if out is None:
         out = torch.empty((rows, heads, D), dtype=q.dtype, device=q.device)
-    _expect(positions, torch.int32, "positions")
-    _expect(inv_freq, torch.float32, "inv_freq")
-    _expect(slots, torch.int64, "slots")
+    if (positions.dtype is not _int32 or slots.dtype is not _int64 or inv_freq.dtype is not _float32
+            or not (positions.is_contiguous() and slots.is_contiguous() and inv_freq.is_contiguous())):
+        raise TypeError("w4a16_rope_append: positions int32, slots int64, inv_freq float32, contiguous")
     sq, sk, sv, so = q.stride(), k.stride(), v.stride(), out.stride()
     if (k.shape != (rows, cache.kv_heads, D) or v.shape != k.shape or out.shape != q.shape or D != cache.head_dim
             or positions.numel() != rows or slots.numel() != rows or sq[2] != 1 or sk[2] != 1 or sv[2] != 1
@@ -426,14 +436,13 @@ def w4a16_paged_attention(q, cache, table, lens, scale: Optional[float] = None, 
     if workspace is None:
         need = w4a16_paged_attention_workspace_bytes(batch, heads, cache.kv_heads, D)
         workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
-    _expect(lens, torch.int32, "lens")
     sq, so = q.stride(), out.stride()
     if (D != cache.head_dim or table.shape[0] != batch or lens.numel() != batch or out.shape != q.shape
             or sq[2] != 1 or so[2] != 1 or (max_pages > 1 and table.stride(1) != 1)):
         raise ValueError("w4a16_paged_attention: q, out [batch, heads, D], table [batch, max_pages], lens [batch], D "
                          "contiguous and the cache's")
-    if q.dtype is not out.dtype or table.dtype is not torch.int32:
-        raise TypeError("w4a16_paged_attention: q and out have one type, table is int32")
+    if (q.dtype is not out.dtype or not table.dtype is lens.dtype is _int32 or not lens.is_contiguous()):
+        raise TypeError("w4a16_paged_attention: q and out have one type, table and lens are int32, lens contiguous")
     if lse is not None:
         _expect(lse, torch.float32, "lse")
         if lse.numel() != batch * heads:
@@ -457,18 +466,19 @@ def w4a16_residual_rmsnorm(h, y, gamma=None, eps: float = 1e-5, post_gamma=None,
         h_out = torch.empty((M, K), dtype=h.dtype, device=h.device)
     if gamma is not None and n_out is None:
         n_out = torch.empty((M, K), dtype=y.dtype, device=y.device)
-    if (y.shape != h.shape or h_out.shape != h.shape or (n_out is not None and n_out.shape != h.shape)
-            or (gate is not None and gate.shape != h.shape and gate.shape != (K,))):
+    shape = h.shape
+    if (y.shape != shape or h_out.shape != shape or (n_out is not None and n_out.shape != shape)
+            or (gate is not None and gate.shape != shape and gate.shape != (K,))):
         raise ValueError("w4a16_residual_rmsnorm: h, y, h_out, n_out [M, K], gate [K] or [M, K]")
-    if K > 1:
-        for t in (h, y, h_out, n_out, gate):
-            if t is not None and t.stride(-1) != 1:
-                raise ValueError("w4a16_residual_rmsnorm: rows must be contiguous")
+    if K > 1 and (h.stride(1) != 1 or y.stride(1) != 1 or h_out.stride(1) != 1
+                  or (n_out is not None and n_out.stride(1) != 1) or (gate is not None and gate.stride(-1) != 1)):
+        raise ValueError("w4a16_residual_rmsnorm: rows must be contiguous")
     for t in (gamma, post_gamma):
         if t is not None:
-            _expect(t, y.dtype, "gamma, post_gamma")
-            if t.numel() != K:
-                raise ValueError("gamma, post_gamma: [K]")
+            if t.dtype is not y.dtype:
+                raise TypeError("gamma and post_gamma have y's type")
+            if t.numel() != K or not t.is_contiguous():
+                raise ValueError("gamma, post_gamma: [K], contiguous")
     if h_out.dtype is not h.dtype or (n_out is not None and n_out.dtype is not y.dtype) or (
             gate is not None and gate.dtype is not y.dtype):
         raise TypeError("w4a16_residual_rmsnorm: h_out has h's type, n_out and gate have y's")

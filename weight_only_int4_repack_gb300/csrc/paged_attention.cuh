@@ -76,6 +76,8 @@ struct Config {
     static constexpr int kSmem = kWarps * kRing + kMerge;
     // A partial result: outputs, then maxima and sums, then room for those of a joined group.
     static constexpr int kPartial = kRows * (DT + 4);
+    static constexpr int kStaged = kRows * (DT + 2);         // floats of one of them while they are joined
+    static constexpr int kJoin = kWarps * kRing / (kStaged * 4) < 24 ? kWarps * kRing / (kStaged * 4) : 24;
     static_assert(kStages >= 3, "one slice is computed on while two are on their way");
     static_assert(kPartial <= kMaxPartial, "the workspace holds partial results of this size");
 };
@@ -270,29 +272,42 @@ struct Ends {
         if (d == 0)
             __stcg(reinterpret_cast<float2 *>(to + K::kRows * (K::kDim + 2 * joined) + 2 * row), make_float2(j.m, j.l));
     }
-    __device__ __forceinline__ void join(int from, int step, int n, int joined, bool end) const {
-        constexpr int kDeep = 8;  // partial results that a thread asks for at a time
+    // Joins n partial results, `step` apart from `from` on, into the output or the first one's place. They come
+    // through shared memory (the ring, which is idle by then), so that all their loads are on their way together.
+    __device__ __forceinline__ void join(float *area, int from, int step, int n, int joined, bool end) const {
+        constexpr int kCols = K::kRows * K::kDim / 4, kEach = (kCols + K::kThreads - 1) / K::kThreads;
         const int cols = seg.rows * (K::kDim / 4);
-        for (int i = threadIdx.x; i < cols; i += K::kThreads) {
-            const int row = i / (K::kDim / 4), d = i % (K::kDim / 4) * 4;
-            if (d >= p.c.head_dim) continue;
-            Joined j;
-            for (int c = 0; c < n; c += kDeep) {
-                float2 ml[kDeep];
-                float4 y[kDeep];
-#pragma unroll
-                for (int u = 0; u < kDeep; ++u)
-                    if (c + u < n) {
-                        const float *x = part(from + (c + u) * step);
-                        ml[u] = __ldcg(reinterpret_cast<const float2 *>(x + K::kRows * (K::kDim + 2 * joined) + 2 * row));
-                        y[u] = __ldcg(reinterpret_cast<const float4 *>(x + row * K::kDim + d));
-                    }
-#pragma unroll
-                for (int u = 0; u < kDeep; ++u)
-                    if (c + u < n) j.take(ml[u].x, ml[u].y, y[u]);
+        Joined j[kEach];
+        for (int c = 0; c < n; c += K::kJoin) {
+            const int here = min(K::kJoin, n - c);
+            for (int u = 0; u < here; ++u) {
+                const float *x = part(from + (c + u) * step);
+                const uint32_t to = ptx::smem_u32(area + u * K::kStaged);
+                for (int i = threadIdx.x; i < cols; i += K::kThreads) copy16(to + i * 16, x + i * 4, true);
+                if (threadIdx.x < K::kRows / 2)
+                    copy16(to + kCols * 16 + threadIdx.x * 16, x + K::kRows * (K::kDim + 2 * joined) + threadIdx.x * 4, true);
             }
-            if (end) finish(row, d, j);
-            else leave(part(from), row, d, j, 1);
+            copies_commit();
+            copies_wait<0>();
+            __syncthreads();
+#pragma unroll
+            for (int y = 0; y < kEach; ++y) {
+                const int i = threadIdx.x + y * K::kThreads, row = i / (K::kDim / 4);
+                if (i >= cols) break;
+                for (int u = 0; u < here; ++u) {
+                    const float *x = area + u * K::kStaged;
+                    const float2 ml = reinterpret_cast<const float2 *>(x + kCols * 4)[row];
+                    j[y].take(ml.x, ml.y, reinterpret_cast<const float4 *>(x)[i]);
+                }
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int y = 0; y < kEach; ++y) {
+            const int i = threadIdx.x + y * K::kThreads, row = i / (K::kDim / 4), d = i % (K::kDim / 4) * 4;
+            if (i >= cols || d >= p.c.head_dim) continue;
+            if (end) finish(row, d, j[y]);
+            else leave(part(from), row, d, j[y], 1);
         }
     }
 };
@@ -302,11 +317,14 @@ struct Ends {
 // item only, so counters at its number, one for items that begin in it and one for the
 // item that does not, are not shared.
 template <typename K, typename T>
-__device__ __forceinline__ void join_parts(const Ends<K, T> &ends, int *is_last) {
+__device__ __forceinline__ void join_parts(const Ends<K, T> &ends, float *area, int *is_last) {
     const Segment &seg = ends.seg;
     unsigned int *counters = ends.p.counters;
-    int group = 8;
-    while (group * group < seg.parts) ++group;
+    int group = seg.parts;  // one round, if shared memory holds them all
+    if (group > K::kJoin) {
+        group = min(8, K::kJoin);
+        while (group * group < seg.parts) ++group;
+    }
     const int of = ((int)blockIdx.x - seg.c_first) / group, in_group = min(group, seg.parts - of * group);
     const int groups = (seg.parts + group - 1) / group;
     // The barrier in front of the atomic puts every thread's partial result before it.
@@ -322,8 +340,8 @@ __device__ __forceinline__ void join_parts(const Ends<K, T> &ends, int *is_last)
         return *is_last != 0;
     };
     if (last_of(of == 0 ? counters + seg.c_first : counters + kMaxCtas + seg.c_first + of * group, in_group)) {
-        ends.join(of * group, 1, in_group, 0, groups == 1);
-        if (groups > 1 && last_of(counters + 2 * kMaxCtas + seg.c_first, groups)) ends.join(0, group, groups, 1, true);
+        ends.join(area, of * group, 1, in_group, 0, groups == 1);
+        if (groups > 1 && last_of(counters + 2 * kMaxCtas + seg.c_first, groups)) ends.join(area, 0, group, groups, 1, true);
     }
 }
 
@@ -783,7 +801,8 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
     for (int x = 0; x < 2; ++x) {
         const Segment seg = open[x];
         if (seg.parts < 2) continue;
-        join_parts<K, T>(Ends<K, T>{p, seg, k8 && p.c.v_scale ? p.c.v_scale[seg.kvh] : 1.f}, &is_last);
+        join_parts<K, T>(Ends<K, T>{p, seg, k8 && p.c.v_scale ? p.c.v_scale[seg.kvh] : 1.f},
+                         reinterpret_cast<float *>(smem), &is_last);
     }
 }
 

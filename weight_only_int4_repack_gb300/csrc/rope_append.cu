@@ -12,6 +12,7 @@
 // another one and drops whole turns exactly; its upper 32 bits, signed, are the angle
 // in units of 2^-32 turns. No fp64, of which the GPU has little.
 #include <cmath>
+#include <type_traits>
 
 #include "elem.cuh"
 #include "ptx.cuh"
@@ -30,7 +31,7 @@ struct RopeParams {
     const float *inv_freq;
     const int64_t *slots;
     w4a16_kv_cache c;
-    int rows, heads, rot, split;
+    int rows, heads, rot, at_once;
     float mscale;
     unsigned int *err;
 };
@@ -75,146 +76,145 @@ __device__ __forceinline__ bool place_of(const RopeParams &p, long long slot, Pl
     return true;
 }
 
-// rot_dim a multiple of 16, everything 16-byte aligned. p.split warps share a row. A
-// unit is 16 elements of a head as two groups a and b of 8, a lane's: eight pairs
+// rot_dim a multiple of 16, everything 16-byte aligned. A CTA takes p.at_once rows.
+//
+// A unit is 16 elements of a head as two groups a and b of 8, a lane's: eight pairs
 // between a and b (halves), or four in each (neighbours), always those of frequencies
-// 8u..8u+7; or elements behind rot_dim, and of v, which only get their bias. So a lane
-// has the same frequencies for every head, in registers; a warp's lanes cover several
-// heads at once, and the next heads are loaded while these are turned.
+// 8u..8u+7; or elements behind rot_dim, and of v, which only get their bias. A warp's
+// lanes cover several heads, a pass, and go through the CTA's rows with it: which
+// heads, where they lie and their bias are found once for all rows. The rows' angles
+// and cache places are worked out once for all heads, in shared memory. (A warp for
+// each row, which finds the heads anew for every one, took 60.7 us for 16384 rows of
+// 36 heads of 128 with an 8-bit cache, where this takes ROPE16384.)
+constexpr int kWideWarps = 16, kRowsAtOnce = 8;
+
 template <typename T, typename C, bool kPairs>
-__global__ void __launch_bounds__(kThreads, 6) rope_append_wide_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(32 * kWideWarps, 2) rope_append_wide_kernel(const RopeParams p) {
     using VT = elem::Vec<T, 8>;
     using VC = elem::Vec<C, 8>;
-    __shared__ float2 cs[kThreads / 32][kMaxHalf];
+    // Row r's cos and sin of frequencies 8u + 2e, 8u + 2e + 1 at [r][e * turning units + u]: lanes side by side.
+    __shared__ float4 cs[kRowsAtOnce][kMaxHalf / 2];
+    __shared__ long long k_at[kRowsAtOnce], v_at[kRowsAtOnce];  // offsets in the pools; k_at < 0: not written
     ptx::grid_dep_launch();
     ptx::grid_dep_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long id = (long long)blockIdx.x * (kThreads / 32) + warp;
-    const int row = (int)(id / p.split), part = (int)(id - (long long)row * p.split);
-    if (row >= p.rows) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int row0 = blockIdx.x * p.at_once, rows = min(p.at_once, p.rows - row0);
     const int D = p.c.head_dim, half = p.rot / 2, kv = p.c.kv_heads;
-    const int units = (D + 15) / 16, at_once = 32 / units;  // units of a head, heads of a warp
+    const int units = (D + 15) / 16, heads_at = 32 / units, turning = p.rot / 16;
     const int sub = lane / units, u = lane - sub * units;
-    const bool active = sub < at_once;
-    const int pos = p.positions[row];
-    const long long slot = p.slots[row];
+    const int q_passes = (p.heads + heads_at - 1) / heads_at, kv_passes = (kv + heads_at - 1) / heads_at;
 
-    // Passes: at_once heads of q each, then of k, then of v. Elements that the lane's groups begin at: of q and k
-    // heads, and 16u, 16u + 8 of v heads; b may lie behind the head.
-    const int q_passes = (p.heads + at_once - 1) / at_once, kv_passes = (kv + at_once - 1) / at_once;
-    const int passes = q_passes + 2 * kv_passes;
-    const bool turns = 16 * u < p.rot;
-    const int qa = kPairs || !turns ? 16 * u : 8 * u, qb = kPairs || !turns ? qa + 8 : qa + half;
-    uint4 ra[2], rb[2];  // two passes on their way
-    auto load = [&](int x, int pass) {
-        if (pass >= passes) return;
-        const T *src;
-        int left, a = qa, b = qb;  // heads from the pass's first on
-        if (pass < q_passes) {
-            left = p.heads - pass * at_once;
-            src = static_cast<const T *>(p.q) + row * p.q_row + pass * at_once * p.q_head + sub * p.q_head;
-        } else if (pass < q_passes + kv_passes) {
-            const int first = (pass - q_passes) * at_once;
-            left = kv - first;
-            src = static_cast<const T *>(p.k) + row * p.k_row + first * p.k_head + sub * p.k_head;
-        } else {
-            const int first = (pass - q_passes - kv_passes) * at_once;
-            left = kv - first;
-            src = static_cast<const T *>(p.v) + row * p.v_row + first * p.v_head + sub * p.v_head;
-            a = 16 * u, b = a + 8;
+    for (int pass = warp; pass < q_passes + 2 * kv_passes; pass += warps) {  // one at least: warps <= passes
+        // Which heads, and where the lane's groups lie in them (b may lie behind the head).
+        const bool q = pass < q_passes, v = pass >= q_passes + kv_passes;
+        const int head = (pass - (q ? 0 : v ? q_passes + kv_passes : q_passes)) * heads_at + sub;
+        const bool in = sub < heads_at && head < (q ? p.heads : kv);
+        const bool turns = !v && u < turning;
+        const int a_at = kPairs || !turns ? 16 * u : 8 * u, b_at = kPairs || !turns ? a_at + 8 : a_at + half;
+        const bool two = b_at < D;
+        const long long src_row = q ? p.q_row : v ? p.v_row : p.k_row;
+        const T *src = (q ? static_cast<const T *>(p.q) + head * p.q_head
+                          : v ? static_cast<const T *>(p.v) + head * p.v_head : static_cast<const T *>(p.k) + head * p.k_head) +
+                       row0 * src_row + a_at;
+        const int ab = b_at - a_at;
+        uint4 ra[2], rb[2];  // two rows on their way
+        auto load = [&](int x) {
+            if (!in) return;
+            ra[x] = *reinterpret_cast<const uint4 *>(src);
+            if (two) rb[x] = *reinterpret_cast<const uint4 *>(src + ab);
+            src += src_row;
+        };
+        load(0);
+        if (rows > 1) load(1);
+        uint4 fa = make_uint4(0, 0, 0, 0), fb = fa;
+        if (p.bias && in) {
+            const T *bias = static_cast<const T *>(p.bias) + (head + (q ? 0 : v ? p.heads + kv : p.heads)) * D;
+            fa = *reinterpret_cast<const uint4 *>(bias + a_at);
+            if (two) fb = *reinterpret_cast<const uint4 *>(bias + b_at);
         }
-        if (!active || sub >= left) return;
-        ra[x] = *reinterpret_cast<const uint4 *>(src + a);
-        if (b < D) rb[x] = *reinterpret_cast<const uint4 *>(src + b);
-    };
-    load(0, part);
-    load(1, part + p.split);
+        T *q_out = static_cast<T *>(p.q_out) + row0 * p.qo_row + head * p.qo_head + a_at;
+        C *pool = v ? static_cast<C *>(p.c.v) + head * p.c.v_head + a_at : static_cast<C *>(p.c.k) + head * p.c.k_head + a_at;
+        const float *scales = v ? p.c.v_scale : p.c.k_scale;
+        const float to_stored = !q && scales && in ? 1.0f / scales[head] : 1.0f;
 
-    for (int i = lane; i < half; i += 32) cs[warp][i] = rotation(p.inv_freq[i], pos, p.mscale);
-    Place at{0, 0};
-    const bool writes = place_of(p, slot, at);
-    __syncwarp();
-    float co[8], si[8];
-    if (turns) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) co[e] = cs[warp][8 * u + e].x, si[e] = cs[warp][8 * u + e].y;
-    }
-
-    auto add_bias = [&](int head, int ia, int ib, float (&a)[8], float (&b)[8]) {
-        if (!p.bias) return;
-        float f[8];
-        const T *bias = static_cast<const T *>(p.bias) + head * D;
-        VT::load(bias + ia, f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] += f[e];
-        if (ib < D) {
-            VT::load(bias + ib, f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) b[e] += f[e];
-        }
-    };
-    auto turn = [&](float (&a)[8], float (&b)[8]) {
-        if (!turns) return;
-        if (kPairs) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float xa = a[2 * e], xb = b[2 * e];
-                a[2 * e] = xa * co[e] - a[2 * e + 1] * si[e];
-                a[2 * e + 1] = a[2 * e + 1] * co[e] + xa * si[e];
-                b[2 * e] = xb * co[4 + e] - b[2 * e + 1] * si[4 + e];
-                b[2 * e + 1] = b[2 * e + 1] * co[4 + e] + xb * si[4 + e];
+        if (pass == warp) {  // the first loads are on their way
+            for (int i = threadIdx.x; i < rows * half; i += blockDim.x) {
+                const int r = i / half, f = i - r * half, e = f & 7;
+                reinterpret_cast<float2 *>(cs[r])[((e >> 1) * turning + (f >> 3)) * 2 + (e & 1)] =
+                    rotation(p.inv_freq[f], p.positions[row0 + r], p.mscale);
             }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float xa = a[e];
-                a[e] = xa * co[e] - b[e] * si[e];
-                b[e] = b[e] * co[e] + xa * si[e];
+            if (threadIdx.x < rows) {
+                Place at{0, 0};
+                const bool writes = place_of(p, p.slots[row0 + threadIdx.x], at);
+                k_at[threadIdx.x] = writes ? at.page * p.c.k_page + at.token * p.c.k_token : -1;
+                v_at[threadIdx.x] = at.page * p.c.v_page + at.token * p.c.v_token;
             }
+            __syncthreads();
         }
-    };
-    auto to_cache = [&](void *pool, long long page_stride, long long token_stride, long long head_stride, const float *scale,
-                        int head, int ia, int ib, float (&a)[8], float (&b)[8]) {
-        C *dst = static_cast<C *>(pool) + at.page * page_stride + at.token * token_stride + head * head_stride;
-        if (scale) {
-            const float r = 1.0f / scale[head];
+        // The lane's rows, for queries (0), keys (1) or values (2).
+        auto go = [&](auto kind) {
+            constexpr int kKind = decltype(kind)::value;
+            const T *from = src;
+            const long long *at = kKind == 2 ? v_at : k_at;
+            for (int r0 = 0; r0 < rows; r0 += 2) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) a[e] *= r, b[e] *= r;
-        }
-        VC::store(dst + ia, a);
-        if (ib < D) VC::store(dst + ib, b);
-    };
-    for (int pass0 = part; pass0 < passes; pass0 += 2 * p.split) {
+                for (int y = 0; y < 2; ++y) {
+                    const int r = r0 + y;
+                    if (r >= rows) break;
+                    float a[8], b[8];
+                    VT::load(reinterpret_cast<const T *>(&ra[y]), a);
+                    VT::load(reinterpret_cast<const T *>(&rb[y]), b);
+                    if (r + 2 < rows) {
+                        ra[y] = *reinterpret_cast<const uint4 *>(from);
+                        if (two) rb[y] = *reinterpret_cast<const uint4 *>(from + ab);
+                        from += src_row;
+                    }
+                    if (p.bias) {
+                        float f[8];
+                        VT::load(reinterpret_cast<const T *>(&fa), f);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int pass = pass0 + x * p.split;
-            if (pass >= passes) break;
-            float a[8], b[8];
-            VT::load(reinterpret_cast<const T *>(&ra[x]), a);
-            VT::load(reinterpret_cast<const T *>(&rb[x]), b);
-            load(x, pass + 2 * p.split);
-            if (!active) continue;
-            if (pass < q_passes) {
-                const int head = pass * at_once + sub;
-                if (head >= p.heads) continue;
-                add_bias(head, qa, qb, a, b);
-                turn(a, b);
-                T *dst = static_cast<T *>(p.q_out) + row * p.qo_row + pass * at_once * p.qo_head + sub * p.qo_head;
-                VT::store(dst + qa, a);
-                if (qb < D) VT::store(dst + qb, b);
-            } else if (pass < q_passes + kv_passes) {
-                const int head = (pass - q_passes) * at_once + sub;
-                if (head >= kv || !writes) continue;
-                add_bias(p.heads + head, qa, qb, a, b);
-                turn(a, b);
-                to_cache(p.c.k, p.c.k_page, p.c.k_token, p.c.k_head, p.c.k_scale, head, qa, qb, a, b);
-            } else {
-                const int head = (pass - q_passes - kv_passes) * at_once + sub;
-                if (head >= kv || !writes) continue;
-                add_bias(p.heads + kv + head, 16 * u, 16 * u + 8, a, b);
-                to_cache(p.c.v, p.c.v_page, p.c.v_token, p.c.v_head, p.c.v_scale, head, 16 * u, 16 * u + 8, a, b);
+                        for (int e = 0; e < 8; ++e) a[e] += f[e];
+                        VT::load(reinterpret_cast<const T *>(&fb), f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) b[e] += f[e];
+                    }
+                    if (kKind < 2 && turns) {
+                        const float4 *w = cs[r] + u;
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) {
+                            const float4 x = w[(e >> 1) * turning];  // cos, sin of two frequencies
+                            if (kPairs) {
+                                float *g = e < 4 ? a : b;
+                                const int i = 2 * e & 7;
+                                const float y0 = g[i], y2 = g[i + 2];
+                                g[i] = y0 * x.x - g[i + 1] * x.y, g[i + 1] = g[i + 1] * x.x + y0 * x.y;
+                                g[i + 2] = y2 * x.z - g[i + 3] * x.w, g[i + 3] = g[i + 3] * x.z + y2 * x.w;
+                            } else {
+                                const float y0 = a[e], y1 = a[e + 1];
+                                a[e] = y0 * x.x - b[e] * x.y, b[e] = b[e] * x.x + y0 * x.y;
+                                a[e + 1] = y1 * x.z - b[e + 1] * x.w, b[e + 1] = b[e + 1] * x.z + y1 * x.w;
+                            }
+                        }
+                    }
+                    if (kKind == 0) {
+                        VT::store(q_out, a);
+                        if (two) VT::store(q_out + ab, b);
+                        q_out += p.qo_row;
+                    } else if (k_at[r] >= 0) {
+                        if (sizeof(C) == 1) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) a[e] *= to_stored, b[e] *= to_stored;
+                        }
+                        VC::store(pool + at[r], a);
+                        if (two) VC::store(pool + at[r] + ab, b);
+                    }
+                }
             }
-        }
+        };
+        if (!in) continue;
+        if (q) go(std::integral_constant<int, 0>());
+        else if (!v) go(std::integral_constant<int, 1>());
+        else go(std::integral_constant<int, 2>());
     }
 }
 
@@ -310,15 +310,19 @@ cudaError_t launch(RopeParams p, bool pairs, bool wide, cudaStream_t s) {
         return pairs ? cudaLaunchKernelEx(&cfg, rope_append_kernel<T, C, true>, p)
                      : cudaLaunchKernelEx(&cfg, rope_append_kernel<T, C, false>, p);
     }
-    // Rows are split over warps until there are 48 warps for an SM, two rounds of the 28 that it holds, so that
-    // the last round does not leave it half empty; down to one pass of a row for each warp.
-    const int at_once = 32 / ((p.c.head_dim + 15) / 16);
-    const int passes = (p.heads + at_once - 1) / at_once + 2 * ((p.c.kv_heads + at_once - 1) / at_once);
-    p.split = 1;
-    while (p.split < passes && (long long)p.rows * p.split < 48ll * sm_count()) p.split *= 2;
-    if (p.split > passes) p.split = passes;
-    const long long warps = (long long)p.rows * p.split;
-    cfg.gridDim = dim3((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)), 1, 1);
+    // A warp for each pass. As many rows at once as take the fewest rounds of the CTAs that the SMs hold (64
+    // registers a thread), where what a CTA does once costs about as much as one and a half rows.
+    const int heads_at = 32 / ((p.c.head_dim + 15) / 16);
+    const int passes = (p.heads + heads_at - 1) / heads_at + 2 * ((p.c.kv_heads + heads_at - 1) / heads_at);
+    const int threads = 32 * (passes < kWideWarps ? passes : kWideWarps);
+    const long long held = (long long)sm_count() * (1024 / threads);
+    double least = 0.;
+    for (int n = 1; n <= kRowsAtOnce; ++n) {
+        const long long ctas = ((long long)p.rows + n - 1) / n, rounds = (ctas + held - 1) / held;
+        if (n == 1 || rounds * (n + 1.5) < least) least = rounds * (n + 1.5), p.at_once = n;
+    }
+    cfg.gridDim = dim3((unsigned)((p.rows + p.at_once - 1) / p.at_once), 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
     return pairs ? cudaLaunchKernelEx(&cfg, rope_append_wide_kernel<T, C, true>, p)
                  : cudaLaunchKernelEx(&cfg, rope_append_wide_kernel<T, C, false>, p);
 }
