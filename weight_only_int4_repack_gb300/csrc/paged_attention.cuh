@@ -78,6 +78,7 @@ struct Config {
     static constexpr int kPartial = kRows * (DT + 4);
     static constexpr int kStaged = kRows * (DT + 2);         // floats of one of them while they are joined
     static constexpr int kJoin = kWarps * kRing / (kStaged * 4) < 24 ? kWarps * kRing / (kStaged * 4) : 24;
+    static_assert(kWarps * 8 >= kRows, "a joined row's maximum and sum lie where the warps' were");
     static_assert(kStages >= 3, "one slice is computed on while two are on their way");
     static_assert(kPartial <= kMaxPartial, "the workspace holds partial results of this size");
 };
@@ -274,31 +275,61 @@ struct Ends {
     }
     // Joins n partial results, `step` apart from `from` on, into the output or the first one's place. They come
     // through shared memory (the ring, which is idle by then), so that all their loads are on their way together.
-    __device__ __forceinline__ void join(float *area, int from, int step, int n, int joined, bool end) const {
+    // rows: room for kRows pairs.
+    __device__ __forceinline__ void join(float *area, float2 *rows, int from, int step, int n, int joined, bool end) const {
         constexpr int kCols = K::kRows * K::kDim / 4, kEach = (kCols + K::kThreads - 1) / K::kThreads;
         const int cols = seg.rows * (K::kDim / 4);
         Joined j[kEach];
         for (int c = 0; c < n; c += K::kJoin) {
             const int here = min(K::kJoin, n - c);
+            const uint32_t to = ptx::smem_u32(area) + threadIdx.x * 16;
+#pragma unroll 4
             for (int u = 0; u < here; ++u) {
-                const float *x = part(from + (c + u) * step);
-                const uint32_t to = ptx::smem_u32(area + u * K::kStaged);
-                for (int i = threadIdx.x; i < cols; i += K::kThreads) copy16(to + i * 16, x + i * 4, true);
+                const float *x = part(from + (c + u) * step) + threadIdx.x * 4;
+#pragma unroll
+                for (int y = 0; y < kEach; ++y)
+                    if ((int)threadIdx.x + y * K::kThreads < cols)
+                        copy16(to + u * (K::kStaged * 4) + y * (K::kThreads * 16), x + y * (K::kThreads * 4), true);
                 if (threadIdx.x < K::kRows / 2)
-                    copy16(to + kCols * 16 + threadIdx.x * 16, x + K::kRows * (K::kDim + 2 * joined) + threadIdx.x * 4, true);
+                    copy16(to + u * (K::kStaged * 4) + kCols * 16, x + K::kRows * (K::kDim + 2 * joined), true);
             }
             copies_commit();
             copies_wait<0>();
             __syncthreads();
+            // A warp takes a row: the maximum, each part's factor (in the place of its maximum) and the sum.
+            const int lane = threadIdx.x & 31;
+            for (int row = threadIdx.x >> 5; row < seg.rows; row += K::kWarps) {
+                float2 *at = reinterpret_cast<float2 *>(area + lane * K::kStaged + kCols * 4) + row;
+                const float2 ml = lane < here ? *at : make_float2(-INFINITY, 0.f);
+                float top = ml.x;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float f = exp2_approx(ml.x - (top == -INFINITY ? 0.f : top));
+                float sum = f * ml.y;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (lane < here) at->x = f;
+                if (lane == 0) rows[row] = make_float2(top, sum);
+            }
+            __syncthreads();
+            float4 o[kEach];
+#pragma unroll
+            for (int y = 0; y < kEach; ++y) o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int u = 0; u < here; ++u) {
+                const float *x = area + u * K::kStaged;
+#pragma unroll
+                for (int y = 0; y < kEach; ++y) {
+                    const int i = min((int)threadIdx.x + y * K::kThreads, cols - 1);
+                    const float f = reinterpret_cast<const float2 *>(x + kCols * 4)[i / (K::kDim / 4)].x;
+                    const float4 v = reinterpret_cast<const float4 *>(x)[i];
+                    o[y].x += f * v.x, o[y].y += f * v.y, o[y].z += f * v.z, o[y].w += f * v.w;
+                }
+            }
 #pragma unroll
             for (int y = 0; y < kEach; ++y) {
-                const int i = threadIdx.x + y * K::kThreads, row = i / (K::kDim / 4);
-                if (i >= cols) break;
-                for (int u = 0; u < here; ++u) {
-                    const float *x = area + u * K::kStaged;
-                    const float2 ml = reinterpret_cast<const float2 *>(x + kCols * 4)[row];
-                    j[y].take(ml.x, ml.y, reinterpret_cast<const float4 *>(x)[i]);
-                }
+                const float2 r = rows[min((int)threadIdx.x + y * K::kThreads, cols - 1) / (K::kDim / 4)];
+                j[y].take(r.x, r.y, o[y]);
             }
             __syncthreads();
         }
@@ -317,7 +348,7 @@ struct Ends {
 // item only, so counters at its number, one for items that begin in it and one for the
 // item that does not, are not shared.
 template <typename K, typename T>
-__device__ __forceinline__ void join_parts(const Ends<K, T> &ends, float *area, int *is_last) {
+__device__ __forceinline__ void join_parts(const Ends<K, T> &ends, float *area, float2 *rows, int *is_last) {
     const Segment &seg = ends.seg;
     unsigned int *counters = ends.p.counters;
     int group = seg.parts;  // one round, if shared memory holds them all
@@ -327,8 +358,13 @@ __device__ __forceinline__ void join_parts(const Ends<K, T> &ends, float *area, 
     }
     const int of = ((int)blockIdx.x - seg.c_first) / group, in_group = min(group, seg.parts - of * group);
     const int groups = (seg.parts + group - 1) / group;
-    // The barrier in front of the atomic puts every thread's partial result before it.
-    auto last_of = [&](unsigned int *counter, int n) {
+    // Both rounds go through the same instructions: those of a second copy would come from far away.
+#pragma unroll 1
+    for (int round = 0; round < 2; ++round) {
+        unsigned int *counter = round ? counters + 2 * kMaxCtas + seg.c_first
+                                : of == 0 ? counters + seg.c_first : counters + kMaxCtas + seg.c_first + of * group;
+        const int n = round ? groups : in_group;
+        // The barrier in front of the atomic puts every thread's partial result before it.
         __syncthreads();
         if (threadIdx.x == 0) {
             unsigned int old;
@@ -337,11 +373,10 @@ __device__ __forceinline__ void join_parts(const Ends<K, T> &ends, float *area, 
             if (*is_last) *counter = 0u;  // ready for the next call
         }
         __syncthreads();
-        return *is_last != 0;
-    };
-    if (last_of(of == 0 ? counters + seg.c_first : counters + kMaxCtas + seg.c_first + of * group, in_group)) {
-        ends.join(area, of * group, 1, in_group, 0, groups == 1);
-        if (groups > 1 && last_of(counters + 2 * kMaxCtas + seg.c_first, groups)) ends.join(area, 0, group, groups, 1, true);
+        if (!*is_last) return;
+        const bool end = round || groups == 1;
+        ends.join(area, rows, round ? 0 : of * group, round ? group : 1, n, round, end);
+        if (end) return;
     }
 }
 
@@ -802,7 +837,7 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
         const Segment seg = open[x];
         if (seg.parts < 2) continue;
         join_parts<K, T>(Ends<K, T>{p, seg, k8 && p.c.v_scale ? p.c.v_scale[seg.kvh] : 1.f},
-                         reinterpret_cast<float *>(smem), &is_last);
+                         reinterpret_cast<float *>(smem), meet[0], &is_last);
     }
 }
 
