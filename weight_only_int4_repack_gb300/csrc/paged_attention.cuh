@@ -64,10 +64,10 @@ struct Config {
     // each byte, so a third CTA's warps are needed.
     static constexpr int kPerSm = kBytes == 1 && DT <= 128 ? 3 : 2;
     static constexpr int kSliceBytes = kTok * kRowBytes;   // keys or values of a slice
-    static constexpr int kWarps = kSliceBytes > 4096 ? 2 : 4;
+    static constexpr int kWarps = (DT == 256 ? (kBytes == 1 ? 6 : 4) : kBytes == 1 ? 12 : 8) / kPerSm;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kTile = kWarps * kTok;
-    static constexpr int kStagesFit = (kPerSm == 3 ? 49152 : 98304) / (kWarps * 2 * kSliceBytes);
+    static constexpr int kStagesFit = (kBytes == 1 ? 147456 : 196608) / kPerSm / (kWarps * 2 * kSliceBytes);
     static constexpr int kStages = kStagesFit > 6 ? 6 : kStagesFit;
     static constexpr int kRing = kStages * 2 * kSliceBytes;  // one warp's
     static constexpr int kPitch = DT + 4;                    // of a row in the merge area: no bank conflicts
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
     // 2^-4, that second product is not spent.
     constexpr bool kTwo = !k8;
     constexpr int kSteps = DT / 16, MT = K::kTok / 16;
-    constexpr int kAsk = kSteps / K::kWarps;  // steps whose queries a warp brings
+    constexpr int kAsk = (kSteps + K::kWarps - 1) / K::kWarps;  // steps whose queries a warp brings
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ long long sums[K::kWarps];
     __shared__ Segment segs[2], open[2];  // this segment and the next; those that begin before the CTA or end behind it
@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
 #pragma unroll
             for (int x = 0; x < kAsk; ++x) {
                 const int ks = warp * kAsk + x, k0 = ks * 16 + (k8 ? 4 : 2) * (lane % 4);
-                const bool in = head < rows && ks * 16 < D && p.scale != 0.f;
+                const bool in = ks < kSteps && head < rows && ks * 16 < D && p.scale != 0.f;
                 const bool in2 = in && (k8 || ks * 16 + 8 < D);
                 asked[x][nt][0] = in ? *reinterpret_cast<const uint32_t *>(qh + k0) : 0u;
                 asked[x][nt][1] = in2 ? *reinterpret_cast<const uint32_t *>(qh + k0 + (k8 ? 2 : 8)) : 0u;
@@ -585,8 +585,9 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
                         asked[x][nt][y] = elem::pair_from_f32<__half>(f.x * down, f.y * down);
                     }
                 }
-                *reinterpret_cast<uint2 *>(q_area + ((warp * kAsk + x) * 32 + lane) * (2 * NT) + 2 * nt) =
-                    make_uint2(asked[x][nt][0], asked[x][nt][1]);
+                if (warp * kAsk + x < kSteps)
+                    *reinterpret_cast<uint2 *>(q_area + ((warp * kAsk + x) * 32 + lane) * (2 * NT) + 2 * nt) =
+                        make_uint2(asked[x][nt][0], asked[x][nt][1]);
             }
         __syncthreads();
         return result;
