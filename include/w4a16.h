@@ -371,10 +371,13 @@ typedef struct {
  *   lens_out    [batch]: the new lengths (0 for ended, unchanged for refused)
  *   free_count_out [1]
  *   refused     [batch]: 0, 1 or 2 as above
- *   slots       int64 [n_slots], positions int32 [n_slots]: the step's tokens,
- *               request after request, refused ones included: slot and position
- *               in the request; -1 and 0 for refused requests' tokens and for
- *               the entries behind the last token
+ *   slots       int64 [n_slots], positions int32 [n_slots]: slot and position in
+ *               the request of the step's tokens; -1 and 0 for refused requests'
+ *               tokens and where there is no token
+ *   spacing     0: the tokens follow each other, request after request, refused
+ *               ones included (prompts packed into a step); > 0: request b's
+ *               begin at entry b*spacing, and more than spacing of them do not
+ *               fit (a batch whose rows stay with their requests: 1)
  * lens_out may be lens and free_count_out may be free_count. Table entries of
  * ended requests stay as they are. batch <= 8192; free_count is clamped to
  * [0, pool], and pages given back beyond the pool's size are dropped.
@@ -383,7 +386,7 @@ w4a16_status w4a16_kv_extend(const int32_t *lens, const int32_t *new_tokens, int
                              long long table_stride, int batch, int max_pages, int page_size,
                              int32_t *free_pages, int pool, const int32_t *free_count,
                              int32_t *lens_out, int32_t *free_count_out, int64_t *slots,
-                             int32_t *positions, int n_slots, int32_t *refused, void *stream);
+                             int32_t *positions, int n_slots, int32_t *refused, int spacing, void *stream);
 
 /*
  * Host helper: the rot_dim/2 inverse frequencies base^(-2i/rot_dim) in fp32,

@@ -12,7 +12,7 @@ import numpy as np
 E4M3_MAX = 448.0
 
 
-def kv_extend(lens, new_tokens, table, free_pages, free_count, page_size, n_slots):
+def kv_extend(lens, new_tokens, table, free_pages, free_count, page_size, n_slots, spacing=0):
     """The step's places, one request and one token after the other. Returns a dict
     with the names of the call's outputs (table and free_pages as they are left)."""
     lens, new = [int(x) for x in lens], [int(x) for x in new_tokens]
@@ -36,9 +36,9 @@ def kv_extend(lens, new_tokens, table, free_pages, free_count, page_size, n_slot
         if n < 0:
             lens_out[b] = 0
             continue
-        start = at
-        at += n
-        if lens[b] < 0 or lens[b] + n > room or (n > 0 and at > n_slots):
+        start = b * spacing if spacing else at
+        at = start + n
+        if lens[b] < 0 or lens[b] + n > room or (n > 0 and (at > n_slots or (spacing and n > spacing))):
             refused[b] = 2
             continue
         held, need = pages(lens[b]), pages(lens[b] + n) - pages(lens[b])

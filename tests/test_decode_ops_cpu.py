@@ -34,22 +34,22 @@ CACHE_REFUSALS = [
     (dict(page_size=-1), INVALID), (dict(kv_heads=0), INVALID), (dict(head_dim=0), INVALID), (dict(type=3), INVALID),
     (dict(type=9), INVALID), (dict(k_token=1028), INVALID), (dict(v_page=-8), INVALID), (dict(k_scale=A), INVALID),
     (dict(type=2, k_head=136), INVALID), (dict(type=2, k_scale=BAD4), INVALID), (dict(head_dim=132), UNSUPPORTED),
-    (dict(head_dim=264), UNSUPPORTED), (dict(type=2, head_dim=72), UNSUPPORTED),
+    (dict(head_dim=264), UNSUPPORTED), (dict(type=2, head_dim=72), UNSUPPORTED), (dict(v_page=2**31), UNSUPPORTED),
 ]
 
 
 def extend(w4, **kw):
     a = dict(lens=A, new=A, table=A, stride=64, batch=4, max_pages=64, page=16, free=A, pool=100, count=A, lens_out=A,
-             count_out=A, slots=A, positions=A, n=64, refused=A)
+             count_out=A, slots=A, positions=A, n=64, refused=A, spacing=0)
     a.update(kw)
     return w4.lib.w4a16_kv_extend(a["lens"], a["new"], a["table"], a["stride"], a["batch"], a["max_pages"], a["page"],
                                   a["free"], a["pool"], a["count"], a["lens_out"], a["count_out"], a["slots"],
-                                  a["positions"], a["n"], a["refused"], None)
+                                  a["positions"], a["n"], a["refused"], a["spacing"], None)
 
 
 @pytest.mark.parametrize("kw,status", [
     (dict(batch=-1), INVALID), (dict(max_pages=0), INVALID), (dict(page=0), INVALID), (dict(pool=0), INVALID),
-    (dict(n=-1), INVALID), (dict(stride=63), INVALID), (dict(batch=8193), UNSUPPORTED), (dict(lens=None), INVALID),
+    (dict(n=-1), INVALID), (dict(spacing=-1), INVALID), (dict(n=2**31 - 1), UNSUPPORTED), (dict(stride=63), INVALID), (dict(batch=8193), UNSUPPORTED), (dict(lens=None), INVALID),
     (dict(new=None), INVALID), (dict(table=None), INVALID), (dict(free=None), INVALID), (dict(count=None), INVALID),
     (dict(lens_out=None), INVALID), (dict(count_out=None), INVALID), (dict(slots=None), INVALID),
     (dict(positions=None), INVALID), (dict(refused=None), INVALID), (dict(lens=BAD4), INVALID),
@@ -225,6 +225,12 @@ def test_oracle_kv_extend_worked_example():
     assert got["lens_out"].tolist() == [0, 9, 3, 0] and got["refused"].tolist() == [0, 0, 0, 1]
     assert got["slots"][:8].tolist() == [9, 10, 11, 32, 28, 29, 30, -1]
     assert got["positions"][:8].tolist() == [5, 6, 7, 8, 0, 1, 2, 0]
+
+
+def test_oracle_kv_extend_spacing():
+    table = np.array([[7, 8], [3, 2], [4, 5]])
+    got = ref.kv_extend([6, 5, 2], [0, 2, 3], table, np.array([1]), 0, 4, 6, spacing=2)
+    assert got["slots"].tolist() == [-1, -1, 9, 10, -1, -1] and got["refused"].tolist() == [0, 0, 2]
 
 
 def test_oracle_rope_quarter_turn():

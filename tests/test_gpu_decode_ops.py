@@ -56,22 +56,22 @@ def within(got, want, bound, label):
 
 
 # ------------------------------------------------------------------ kv_extend
-def run_extend(w4, lens, new, table, free, count, page, n_slots, in_place=False):
+def run_extend(w4, lens, new, table, free, count, page, n_slots, in_place=False, spacing=0):
     t = dict(lens=i32(lens), new=i32(new), table=i32(table), free=i32(free), count=i32([count]))
     batch = len(lens)
     slots = torch.full((n_slots,), 77, dtype=torch.int64, device="cuda")
     positions, refused = i32(np.full(n_slots, 77)), i32(np.full(batch, 77))
     lens_out, count_out = (t["lens"], t["count"]) if in_place else (i32(np.full(batch, 77)), i32([77]))
     w4.w4a16_kv_extend(t["lens"], t["new"], t["table"], t["free"], t["count"], page, slots, positions, refused,
-                       lens_out=lens_out, count_out=count_out)
+                       lens_out=lens_out, count_out=count_out, spacing=spacing)
     torch.cuda.synchronize()
     return dict(table=t["table"], free_pages=t["free"], free_count_out=count_out[0], lens_out=lens_out, refused=refused,
                 slots=slots, positions=positions)
 
 
-def check_extend(w4, lens, new, table, free, count, page, n_slots, in_place=False):
-    want = ref.kv_extend(lens, new, table, free, count, page, n_slots)
-    got = run_extend(w4, lens, new, table, free, count, page, n_slots, in_place)
+def check_extend(w4, lens, new, table, free, count, page, n_slots, in_place=False, spacing=0):
+    want = ref.kv_extend(lens, new, table, free, count, page, n_slots, spacing)
+    got = run_extend(w4, lens, new, table, free, count, page, n_slots, in_place, spacing)
     for name, x in want.items():
         np.testing.assert_array_equal(got[name].cpu().numpy(), x, err_msg=name)
     return want
@@ -112,6 +112,14 @@ def test_kv_extend(w4, batch, page, max_pages, share, tight, in_place):
     want = check_extend(w4, *a, page, n + 5, in_place)
     if tight:
         assert (want["refused"] == 1).any()
+
+
+@pytest.mark.parametrize("batch,spacing,short", [(1, 1, 0), (50, 1, 0), (50, 3, 7), (700, 64, 0), (8192, 2, 100)])
+def test_kv_extend_with_spacing(w4, batch, spacing, short):
+    rng = np.random.default_rng(batch + spacing)
+    a = draw_extend(rng, batch, 16, 5, 0.7)
+    want = check_extend(w4, *a, 16, batch * spacing - short, spacing=spacing)
+    assert spacing < 2 or (want["refused"] == 2).any()
 
 
 def test_kv_extend_refuses_what_does_not_fit(w4):

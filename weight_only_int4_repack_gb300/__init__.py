@@ -133,7 +133,7 @@ _sig = {
     "w4a16_gemm_swiglu_unfused_static": (_ci, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _ci, _vp,
                                                _ci, _ci, _ci, _ci, _vp]),
     "w4a16_kv_extend": (_ci, [_vp, _vp, _vp, _ll, _ci, _ci, _ci, _vp, _ci, _vp, _vp, _vp, _vp, _vp, _ci, _vp,
-                              _vp]),
+                              _ci, _vp]),
     "w4a16_rope_frequencies": (_ci, [_vp, _ci, _cd, _ci, _cd, _cd, _cd, _cd]),
     "w4a16_rope_append": (_ci, [_vp, _vp, _vp, _ci, _ll, _ll, _ll, _ll, _ll, _ll, _vp, _vp, _vp, _ci, _ci, _cf,
                                 _vp, _ll, _ll, _kv, _vp, _ci, _ci, _vp]),
@@ -350,10 +350,11 @@ def w4a16_gemm_swiglu_unfused_static(A, qg_rep, sg, zg, qu_rep, su, zu, group: i
 
 
 def w4a16_kv_extend(lens, new_tokens, table, free_pages, free_count, page_size: int, slots, positions, refused,
-                    lens_out=None, count_out=None, stream=None):
+                    lens_out=None, count_out=None, spacing: int = 0, stream=None):
     """Places for a step's new tokens: pages taken from (and, where new_tokens is negative,
     given back to) the free list, the block table grown, a slot and a position for every
-    token. All int32 CUDA tensors but slots (int64); see include/w4a16.h. lens and
+    token (packed, or request b's from entry b*spacing on). All int32 CUDA tensors but
+    slots (int64); see include/w4a16.h. lens and
     free_count are updated in place unless lens_out / count_out are given. Returns lens."""
     lens_out = lens if lens_out is None else lens_out
     count_out = free_count if count_out is None else count_out
@@ -373,7 +374,7 @@ def w4a16_kv_extend(lens, new_tokens, table, free_pages, free_count, page_size: 
                                table.stride(0) if batch > 1 else max_pages, batch,
                                max_pages, page_size, free_pages.data_ptr(), free_pages.numel(),
                                free_count.data_ptr(), lens_out.data_ptr(), count_out.data_ptr(), slots.data_ptr(),
-                               positions.data_ptr(), n_slots, refused.data_ptr(), _stream(stream)),
+                               positions.data_ptr(), n_slots, refused.data_ptr(), spacing, _stream(stream)),
            "w4a16_kv_extend")
     return lens_out
 

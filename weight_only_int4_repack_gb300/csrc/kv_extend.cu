@@ -23,6 +23,7 @@ struct ExtendParams {
     int64_t *slots;
     long long table_stride;
     int batch, max_pages, page_size, pool, n_slots;
+    int spacing;  // slots from one request's first token to the next one's; 0: they follow each other
 };
 
 constexpr int kMostThreads = 1024;
@@ -86,6 +87,12 @@ __global__ void __launch_bounds__(kMostThreads) kv_extend_kernel(const ExtendPar
     const long long count0 = min(max(p.free_count[0], 0), p.pool);
     auto pages = [&](long long n) { return (long long)(((unsigned int)n + ps - 1) / ps); };  // 0 <= n < 2^31
 
+    auto first_slot = [&](int b, long long at) { return p.spacing ? (long long)b * p.spacing : at; };
+    auto fits = [&](int b, int len, int add, long long at) {
+        return add >= 0 && len >= 0 && (long long)len + add <= room &&
+               (add == 0 || (first_slot(b, at) + add <= p.n_slots && (!p.spacing || add <= p.spacing)));
+    };
+
     // Tokens and pages given back, in front of each request.
     long long tokens = 0, given = 0;
     for (int b = b0; b < b1; ++b) {
@@ -103,8 +110,7 @@ __global__ void __launch_bounds__(kMostThreads) kv_extend_kernel(const ExtendPar
     long long need = 0, at = start;
     for (int b = b0; b < b1; ++b) {
         const int len = p.lens[b], add = p.new_tokens[b];
-        const bool fits = add >= 0 && len >= 0 && (long long)len + add <= room && (add == 0 || at + add <= p.n_slots);
-        if (fits) need += pages((long long)len + add) - pages(len);
+        if (fits(b, len, add, at)) need += pages((long long)len + add) - pages(len);
         if (add > 0) at += add;
     }
     long long upto1[1] = {need}, all1[1];
@@ -113,13 +119,13 @@ __global__ void __launch_bounds__(kMostThreads) kv_extend_kernel(const ExtendPar
     at = start;
     for (int b = b0; b < b1; ++b) {
         const int len = p.lens[b], add = p.new_tokens[b];
-        const bool fits = add >= 0 && len >= 0 && (long long)len + add <= room && (add == 0 || at + add <= p.n_slots);
-        const long long n = fits ? pages((long long)len + add) - pages(len) : 0;
-        const bool got = fits && (n == 0 || upto + n <= count);
+        const bool fit = fits(b, len, add, at);
+        const long long n = fit ? pages((long long)len + add) - pages(len) : 0;
+        const bool got = fit && (n == 0 || upto + n <= count);
         Request r;
-        starts[b] = (int)min(at, (long long)p.n_slots);
+        starts[b] = (int)min(first_slot(b, at), (long long)p.n_slots);
         r.held = (int)min(pages(max(len, 0)), (long long)p.max_pages);
-        r.len = got ? len : add < 0 ? kEnded : fits ? kRefusedPages : kRefusedRoom;
+        r.len = got ? len : add < 0 ? kEnded : fit ? kRefusedPages : kRefusedRoom;
         r.page0 = (int)min(add < 0 ? give : upto, (long long)p.pool);
         req[b] = r;
         if (got && n > 0) last = upto + n;
@@ -212,7 +218,7 @@ __global__ void __launch_bounds__(kMostThreads) kv_extend_kernel(const ExtendPar
             if (c == 32) lo = search(t);  // many requests without tokens
             first = __shfl_sync(0xffffffffu, lo, 31);
             const Request r = req[lo];
-            if (t < all_tokens && t < p.n_slots && r.len >= 0) {
+            if (t < p.n_slots && r.len >= 0 && (p.spacing ? t - starts[lo] < p.new_tokens[lo] : t < all_tokens)) {
                 pos[x] = r.len + (t - starts[lo]);
                 const int j = (int)((unsigned int)pos[x] / ps);
                 page[x] = j < r.held ? p.table[(long long)lo * p.table_stride + j]
@@ -238,8 +244,8 @@ extern "C" w4a16_status w4a16_kv_extend(const int32_t *lens, const int32_t *new_
                                         long long table_stride, int batch, int max_pages, int page_size,
                                         int32_t *free_pages, int pool, const int32_t *free_count, int32_t *lens_out,
                                         int32_t *free_count_out, int64_t *slots, int32_t *positions, int n_slots,
-                                        int32_t *refused, void *stream) {
-    if (batch < 0 || max_pages <= 0 || page_size <= 0 || pool <= 0 || n_slots < 0 || table_stride < max_pages)
+                                        int32_t *refused, int spacing, void *stream) {
+    if (batch < 0 || spacing < 0 || max_pages <= 0 || page_size <= 0 || pool <= 0 || n_slots < 0 || table_stride < max_pages)
         return W4A16_ERR_INVALID_ARG;
     if (batch > kMaxBatch || n_slots > INT_MAX - 63) return W4A16_ERR_UNSUPPORTED;
     if (batch == 0) return W4A16_OK;
@@ -253,7 +259,7 @@ extern "C" w4a16_status w4a16_kv_extend(const int32_t *lens, const int32_t *new_
     if (!aligned(slots, 8)) return W4A16_ERR_INVALID_ARG;
     const ExtendParams p{lens,      new_tokens, free_count, table,        free_pages, lens_out,  free_count_out,
                          positions, refused,    slots,      table_stride, batch,      max_pages, page_size,
-                         pool,      n_slots};
+                         pool,      n_slots,    spacing};
     cudaError_t e = ensure_max_dyn_smem((const void *)kv_extend_kernel, kMaxBatch * kRequestBytes);
     if (e != cudaSuccess) return from_cuda(e);
     // A step of running requests fits one CTA, and a small one is done sooner with fewer warps to wait for.

@@ -64,7 +64,7 @@ struct Config {
     // each byte, so a third CTA's warps are needed.
     static constexpr int kPerSm = kBytes == 1 && DT <= 128 ? 3 : 2;
     static constexpr int kSliceBytes = kTok * kRowBytes;   // keys or values of a slice
-    static constexpr int kWarps = (DT == 256 ? (kBytes == 1 ? 6 : 4) : kBytes == 1 ? 12 : 8) / kPerSm;
+    static constexpr int kWarps = DT == 256 ? (kBytes == 1 ? 3 : 2) : 4;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kTile = kWarps * kTok;
     static constexpr int kStagesFit = (kBytes == 1 ? 147456 : 196608) / kPerSm / (kWarps * 2 * kSliceBytes);
