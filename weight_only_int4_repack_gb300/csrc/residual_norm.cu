@@ -40,7 +40,7 @@ struct Raw {
     uint4 w[sizeof(T) / 2];
     __device__ __forceinline__ void load(const T *p) {
 #pragma unroll
-        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) w[i] = reinterpret_cast<const uint4 *>(p)[i];
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) w[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
     }
     __device__ __forceinline__ void get(float (&f)[8]) const {
         elem::Vec<T, 8>::load(reinterpret_cast<const T *>(w), f);

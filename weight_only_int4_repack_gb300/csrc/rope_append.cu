@@ -120,8 +120,8 @@ __global__ void __launch_bounds__(32 * kWideWarps, 2) rope_append_wide_kernel(co
         uint4 ra[2], rb[2];  // two rows on their way
         auto load = [&](int x) {
             if (!in) return;
-            ra[x] = *reinterpret_cast<const uint4 *>(src);
-            if (two) rb[x] = *reinterpret_cast<const uint4 *>(src + ab);
+            ra[x] = __ldcs(reinterpret_cast<const uint4 *>(src));
+            if (two) rb[x] = __ldcs(reinterpret_cast<const uint4 *>(src + ab));
             src += src_row;
         };
         load(0);
@@ -165,8 +165,8 @@ __global__ void __launch_bounds__(32 * kWideWarps, 2) rope_append_wide_kernel(co
                     VT::load(reinterpret_cast<const T *>(&ra[y]), a);
                     VT::load(reinterpret_cast<const T *>(&rb[y]), b);
                     if (r + 2 < rows) {
-                        ra[y] = *reinterpret_cast<const uint4 *>(from);
-                        if (two) rb[y] = *reinterpret_cast<const uint4 *>(from + ab);
+                        ra[y] = __ldcs(reinterpret_cast<const uint4 *>(from));
+                        if (two) rb[y] = __ldcs(reinterpret_cast<const uint4 *>(from + ab));
                         from += src_row;
                     }
                     if (p.bias) {
