@@ -50,6 +50,13 @@ __device__ __forceinline__ uint32_t e4m3_to_half2(uint16_t x) {
     return r;
 }
 
+// The lower and the upper two of four e4m3 values as fp16.
+__device__ __forceinline__ void e4m3x4_to_half2(uint32_t x, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
+}
+
 // N consecutive elements to fp32 and back (the address is aligned to their size in
 // bytes). Stores of 8 are marked as streaming: what these operators write is read by
 // another kernel once. Together with streaming loads that takes residual_rmsnorm from

@@ -671,10 +671,9 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
                     } else {
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {  // two steps for each four matrices
-                            const uint32_t a[4] = {elem::e4m3_to_half2((uint16_t)w[2 * x]),
-                                                   elem::e4m3_to_half2((uint16_t)w[2 * x + 1]),
-                                                   elem::e4m3_to_half2((uint16_t)(w[2 * x] >> 16)),
-                                                   elem::e4m3_to_half2((uint16_t)(w[2 * x + 1] >> 16))};
+                            uint32_t a[4];
+                            elem::e4m3x4_to_half2(w[2 * x], a[0], a[2]);
+                            elem::e4m3x4_to_half2(w[2 * x + 1], a[1], a[3]);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) mma<M>(s[mt][nt], a, q[x][nt][0], q[x][nt][1]);
                         }
@@ -772,9 +771,9 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             // Bytes: (d, d+1) of one token, (d, d+1) of the next; rows r, r + 8 become d = 2r, 2r + 1.
-                            const uint32_t e0 = __byte_perm(w[2 * x], 0, 0x3120), e1 = __byte_perm(w[2 * x + 1], 0, 0x3120);
-                            const uint32_t a[4] = {elem::e4m3_to_half2((uint16_t)e0), elem::e4m3_to_half2((uint16_t)(e0 >> 16)),
-                                                   elem::e4m3_to_half2((uint16_t)e1), elem::e4m3_to_half2((uint16_t)(e1 >> 16))};
+                            uint32_t a[4];
+                            elem::e4m3x4_to_half2(__byte_perm(w[2 * x], 0, 0x3120), a[0], a[1]);
+                            elem::e4m3x4_to_half2(__byte_perm(w[2 * x + 1], 0, 0x3120), a[2], a[3]);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) mma<M>(o[dt + x][nt], a, ph[mt][nt][0], ph[mt][nt][1]);
                         }
