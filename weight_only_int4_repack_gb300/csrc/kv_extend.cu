@@ -23,6 +23,7 @@ struct ExtendParams {
     int64_t *slots;
     long long table_stride;
     int batch, max_pages, page_size, pool, n_slots;
+    unsigned int magic, shift;  // n / page_size = n * magic >> shift for 0 <= n < 2^31
     int spacing;  // slots from one request's first token to the next one's; 0: they follow each other
 };
 
@@ -85,7 +86,11 @@ __global__ void __launch_bounds__(kMostThreads) kv_extend_kernel(const ExtendPar
     const unsigned int ps = (unsigned int)p.page_size;
     const long long room = min((long long)p.max_pages * ps, (long long)INT_MAX);
     const long long count0 = min(max(p.free_count[0], 0), p.pool);
-    auto pages = [&](long long n) { return (long long)(((unsigned int)n + ps - 1) / ps); };  // 0 <= n < 2^31
+    auto by_page = [&](int n) { return (int)(((unsigned long long)(unsigned int)n * p.magic) >> p.shift); };  // n / ps
+    auto pages = [&](int n) {  // n / ps, rounded up
+        const int whole = by_page(n);
+        return whole + (n > whole * p.page_size);
+    };
 
     auto first_slot = [&](int b, long long at) { return p.spacing ? (long long)b * p.spacing : at; };
     auto fits = [&](int b, int len, int add, long long at) {
@@ -98,7 +103,7 @@ __global__ void __launch_bounds__(kMostThreads) kv_extend_kernel(const ExtendPar
     for (int b = b0; b < b1; ++b) {
         const int len = p.lens[b], add = p.new_tokens[b];
         if (add > 0) tokens += add;
-        if (add < 0) given += min(pages(max(len, 0)), (long long)p.max_pages);
+        if (add < 0) given += min(pages(max(len, 0)), p.max_pages);
     }
     long long upto2[2] = {tokens, given}, all2[2];
     scan<2>(upto2, warp_sums, all2);
@@ -110,27 +115,27 @@ __global__ void __launch_bounds__(kMostThreads) kv_extend_kernel(const ExtendPar
     long long need = 0, at = start;
     for (int b = b0; b < b1; ++b) {
         const int len = p.lens[b], add = p.new_tokens[b];
-        if (fits(b, len, add, at)) need += pages((long long)len + add) - pages(len);
+        // Kept for the next loop: whether it fits, its pages and how many it needs.
+        const bool fit = fits(b, len, add, at);
+        const int held = min(pages(max(len, 0)), p.max_pages), more = fit ? pages(len + add) - held : 0;
+        req[b].len = fit ? len : add < 0 ? kEnded : kRefusedRoom;
+        req[b].held = held, req[b].page0 = more;
+        starts[b] = (int)min(first_slot(b, at), (long long)p.n_slots);
+        need += more;
         if (add > 0) at += add;
     }
     long long upto1[1] = {need}, all1[1];
     scan<1>(upto1, warp_sums + 2, all1);
     long long upto = upto1[0] - need, last = 0;
-    at = start;
     for (int b = b0; b < b1; ++b) {
-        const int len = p.lens[b], add = p.new_tokens[b];
-        const bool fit = fits(b, len, add, at);
-        const long long n = fit ? pages((long long)len + add) - pages(len) : 0;
-        const bool got = fit && (n == 0 || upto + n <= count);
-        Request r;
-        starts[b] = (int)min(first_slot(b, at), (long long)p.n_slots);
-        r.held = (int)min(pages(max(len, 0)), (long long)p.max_pages);
-        r.len = got ? len : add < 0 ? kEnded : fit ? kRefusedPages : kRefusedRoom;
-        r.page0 = (int)min(add < 0 ? give : upto, (long long)p.pool);
+        Request r = req[b];
+        const int n = r.page0;
+        const bool there = n == 0 || upto + n <= count;
+        if (n > 0 && there) last = upto + n;
+        r.page0 = (int)min(r.len == kEnded ? give : upto, (long long)p.pool);
+        if (r.len >= 0 && !there) r.len = kRefusedPages;
         req[b] = r;
-        if (got && n > 0) last = upto + n;
-        if (add < 0) give += r.held;
-        if (add > 0) at += add;
+        if (r.len == kEnded) give += r.held;
         upto += n;
     }
     // Pages handed out in all: what all need, if that is there.
@@ -175,7 +180,7 @@ __global__ void __launch_bounds__(kMostThreads) kv_extend_kernel(const ExtendPar
         if (lane < share && b < p.batch) {
             const Request r = req[b];
             const int add = p.new_tokens[b];
-            if (r.len >= 0) n = (int)pages((long long)r.len + add) - r.held;
+            if (r.len >= 0) n = pages(r.len + add) - r.held;
             p.lens_out[b] = r.len == kEnded ? 0 : r.len >= 0 ? r.len + add : p.lens[b];
             p.refused[b] = r.len == kRefusedPages ? 1 : r.len == kRefusedRoom ? 2 : 0;
         }
@@ -220,7 +225,7 @@ __global__ void __launch_bounds__(kMostThreads) kv_extend_kernel(const ExtendPar
             const Request r = req[lo];
             if (t < p.n_slots && r.len >= 0 && (p.spacing ? t - starts[lo] < p.new_tokens[lo] : t < all_tokens)) {
                 pos[x] = r.len + (t - starts[lo]);
-                const int j = (int)((unsigned int)pos[x] / ps);
+                const int j = by_page(pos[x]);
                 page[x] = j < r.held ? p.table[(long long)lo * p.table_stride + j]
                                      : __ldcg(p.free_pages + (top - (r.page0 + j - r.held)));
             }
@@ -229,7 +234,7 @@ __global__ void __launch_bounds__(kMostThreads) kv_extend_kernel(const ExtendPar
         for (int x = 0; x < kAt; ++x) {
             const int t = (g + x) * 32 + lane;
             if (g + x >= g_end || t >= p.n_slots || t < 0) continue;
-            p.slots[t] = pos[x] < 0 ? -1ll : (long long)page[x] * ps + (unsigned int)pos[x] % ps;
+            p.slots[t] = pos[x] < 0 ? -1ll : (long long)page[x] * ps + (pos[x] - by_page(pos[x]) * p.page_size);
             p.positions[t] = max(pos[x], 0);
         }
     }
@@ -257,9 +262,15 @@ extern "C" w4a16_status w4a16_kv_extend(const int32_t *lens, const int32_t *new_
                           (const void *)positions, (const void *)refused})
         if (!aligned(q, 4)) return W4A16_ERR_INVALID_ARG;
     if (!aligned(slots, 8)) return W4A16_ERR_INVALID_ARG;
+    // Division by page_size as a product: with 2^l the first power of two not below it, 2^(31 + l) / page_size rounded
+    // up is below 2^32, and what the rounding adds stays below one for every n below 2^31.
+    unsigned int l = 0;
+    while ((1ull << l) < (unsigned int)page_size) ++l;
+    const unsigned long long whole = ((1ull << (31 + l)) + page_size - 1) / page_size;
+    const unsigned int magic = (unsigned int)whole, shift = 31 + l;
     const ExtendParams p{lens,      new_tokens, free_count, table,        free_pages, lens_out,  free_count_out,
                          positions, refused,    slots,      table_stride, batch,      max_pages, page_size,
-                         pool,      n_slots,    spacing};
+                         pool,      n_slots,    magic,        shift,      spacing};
     cudaError_t e = ensure_max_dyn_smem((const void *)kv_extend_kernel, kMaxBatch * kRequestBytes);
     if (e != cudaSuccess) return from_cuda(e);
     // A step of running requests fits one CTA, and a small one is done sooner with fewer warps to wait for.
