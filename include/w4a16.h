@@ -296,7 +296,9 @@ w4a16_status w4a16_set_wait_limit_ns(unsigned long long limit_ns);
 
 /*
  * Read and clear the device-side error word that bounded waits set when they
- * expire (W4A16_ERR_TIMEOUT) on the device current for the calling thread.
+ * expire (W4A16_ERR_TIMEOUT), and the operators between the projections when a
+ * value on the GPU is out of range (W4A16_ERR_INVALID_ARG), on the device current
+ * for the calling thread.
  * Synchronises `stream`. Returns W4A16_OK when no kernel reported an error.
  */
 w4a16_status w4a16_device_error(void *stream);
@@ -455,8 +457,12 @@ w4a16_status w4a16_rope_append(const void *q, const void *k, const void *v, w4a1
  *   lse       device fp32 [batch][heads], or NULL
  *   ws        device scratch of w4a16_paged_attention_workspace_bytes(), 256-byte
  *             aligned. It has to be zero before its first use; every call leaves
- *             it ready for the next. Calls that can overlap on the GPU need one
- *             each.
+ *             it ready for the next, of whatever shape (its size is the same for
+ *             all). Calls that can overlap on the GPU need one each.
+ * The result does not depend on timing: how a request's tokens are divided among
+ * the SMs follows from all lengths of the call, and the parts are joined in the
+ * tokens' order. batch * (32-token tiles of a table row) * kv_heads * (blocks of 8
+ * query heads) below 2^31.
  */
 size_t w4a16_paged_attention_workspace_bytes(int batch, int heads, int kv_heads, int head_dim);
 w4a16_status w4a16_paged_attention(const void *q, w4a16_type type, long long q_row, long long q_head,

@@ -99,6 +99,7 @@ def attention(w4, c=None, **kw):
     (dict(lens=None), INVALID), (dict(q=BAD16), INVALID), (dict(out=BAD16), INVALID), (dict(lens=BAD4), INVALID),
     (dict(lse=BAD4), INVALID), (dict(q_row=5124), INVALID), (dict(o_head=-128), INVALID), (dict(ws=None), WORKSPACE),
     (dict(ws=A * 16 + 16), WORKSPACE), (dict(ws_bytes=0), WORKSPACE), (dict(batch=1 << 20), UNSUPPORTED),
+    (dict(batch=100, max_pages=1 << 27, stride=1 << 27), UNSUPPORTED),
     (dict(batch=0), 0),
 ])
 def test_paged_attention_refusals(w4, kw, status):

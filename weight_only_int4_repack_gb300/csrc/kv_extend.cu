@@ -12,7 +12,7 @@
 #include <climits>
 
 #include "ptx.cuh"
-#include "w4a16_internal.h"
+#include "decode_ops.h"
 
 namespace w4a16 {
 namespace {

@@ -1,5 +1,7 @@
 // Entry point of paged attention: argument checks and the workspace's layout. The
 // kernel is in paged_attention.cuh.
+#include <climits>
+
 #include "paged_attention.cuh"
 
 using namespace w4a16;
@@ -32,6 +34,10 @@ w4a16_status w4a16_paged_attention(const void *q, w4a16_type type, long long q_r
         return W4A16_ERR_INVALID_ARG;
     if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f) return W4A16_ERR_INVALID_ARG;
     if ((long long)batch * heads > (1 << 24)) return W4A16_ERR_UNSUPPORTED;
+    // Tiles (of 32 tokens at least, 8 heads at least) are numbered in 31 bits.
+    const long long room = (long long)max_pages * cache->page_size, most = room < INT_MAX ? room : INT_MAX;
+    if ((most + 31) / 32 * batch * ((heads / cache->kv_heads + 7) / 8 * cache->kv_heads) > INT_MAX)
+        return W4A16_ERR_UNSUPPORTED;
     if (batch == 0) return W4A16_OK;
     if (!q || !out || !table || !lens) return W4A16_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(lse, 4))

@@ -24,7 +24,7 @@
 
 #include "elem.cuh"
 #include "ptx.cuh"
-#include "w4a16_internal.h"
+#include "decode_ops.h"
 
 namespace w4a16 {
 namespace attn {
@@ -854,7 +854,6 @@ cudaError_t launch(Params p, int sms, cudaStream_t s) {
     p.head_blocks = (p.group + K::kRows - 1) / K::kRows;
     const long long tiles = ((long long)p.max_pages * p.c.page_size + K::kTile - 1) / K::kTile * p.batch *
                             p.c.kv_heads * p.head_blocks;
-    if (tiles >= (1ll << 31)) return cudaErrorInvalidValue;
     const int ctas = sms * K::kPerSm < kMaxCtas ? sms * K::kPerSm : kMaxCtas;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles < ctas ? tiles : ctas), 1, 1);

@@ -16,7 +16,7 @@
 
 #include "elem.cuh"
 #include "ptx.cuh"
-#include "w4a16_internal.h"
+#include "decode_ops.h"
 
 namespace w4a16 {
 namespace {

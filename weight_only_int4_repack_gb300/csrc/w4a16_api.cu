@@ -7,7 +7,7 @@
 #include <set>
 #include <utility>
 
-#include "w4a16_internal.h"
+#include "decode_ops.h"
 
 using namespace w4a16;
 

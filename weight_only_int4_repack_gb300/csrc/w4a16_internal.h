@@ -109,15 +109,4 @@ cudaError_t launch_silu_mul(const __half *G, const __half *U, __half *Y, size_t 
 
 constexpr int kSmallMMaxM = 64;      // 8 token tiles of 8
 
-// Device address of the error word on the current device (nullptr: no device).
-unsigned int *device_error_ptr();
-// Whether calls are launched as programmatic dependents (w4a16_set_launch_overlap).
-bool launch_overlap();
-
-inline bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
-inline w4a16_status from_cuda(cudaError_t e) { return e == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA; }
-
-// What w4a16_kv_cache promises (include/w4a16.h), checked on the host.
-w4a16_status check_cache(const w4a16_kv_cache *c);
-
 }  // namespace w4a16
