@@ -30,14 +30,14 @@ struct ExtendParams {
 constexpr int kMostThreads = 1024;
 constexpr int kMaxBatch = 8192;
 
-// A request's figures, kept in shared memory (besides its first token in the step, at
-// most n_slots, in an array of its own: the searches go through that).
+// A request's figures, kept in shared memory. What it has of the step's tokens, of the
+// pages handed out and of those given back begins where three more arrays say (never
+// less than for the request before it, so they can be searched).
 struct Request {
-    int len;     // tokens before the step; negative: it gets none (kRefused..., kEnded)
-    int held;    // pages before the step
-    int page0;   // pages handed out before its first; ended: pages given back before its first
+    int len;   // tokens before the step; negative: it gets none (kRefused..., kEnded)
+    int held;  // pages before the step
 };
-constexpr int kRequestBytes = sizeof(Request) + sizeof(int);
+constexpr int kRequestBytes = sizeof(Request) + 3 * sizeof(int);
 constexpr int kRefusedPages = -1, kRefusedRoom = -2, kEnded = -3;
 
 // Inclusive prefix sums of N values over the CTA's threads; totals are the sums of all.
@@ -73,8 +73,8 @@ __device__ __forceinline__ void scan(long long (&x)[N], long long (*sums)[32], l
 }
 
 __global__ void __launch_bounds__(kMostThreads) kv_extend_kernel(const ExtendParams p) {
-    extern __shared__ int starts[];  // [batch], then the requests
-    Request *req = reinterpret_cast<Request *>(starts + p.batch);
+    extern __shared__ Request req[];  // [batch], then first token, page handed out and page given back of each
+    int *starts = reinterpret_cast<int *>(req + p.batch), *first_page = starts + p.batch, *first_given = first_page + p.batch;
     __shared__ long long warp_sums[3][32];
     __shared__ long long taken;
     ptx::grid_dep_launch();
@@ -119,7 +119,8 @@ __global__ void __launch_bounds__(kMostThreads) kv_extend_kernel(const ExtendPar
         const bool fit = fits(b, len, add, at);
         const int held = min(pages(max(len, 0)), p.max_pages), more = fit ? pages(len + add) - held : 0;
         req[b].len = fit ? len : add < 0 ? kEnded : kRefusedRoom;
-        req[b].held = held, req[b].page0 = more;
+        req[b].held = held;
+        first_page[b] = more;
         starts[b] = (int)min(first_slot(b, at), (long long)p.n_slots);
         need += more;
         if (add > 0) at += add;
@@ -128,14 +129,13 @@ __global__ void __launch_bounds__(kMostThreads) kv_extend_kernel(const ExtendPar
     scan<1>(upto1, warp_sums + 2, all1);
     long long upto = upto1[0] - need, last = 0;
     for (int b = b0; b < b1; ++b) {
-        Request r = req[b];
-        const int n = r.page0;
+        const int n = first_page[b];
         const bool there = n == 0 || upto + n <= count;
         if (n > 0 && there) last = upto + n;
-        r.page0 = (int)min(r.len == kEnded ? give : upto, (long long)p.pool);
-        if (r.len >= 0 && !there) r.len = kRefusedPages;
-        req[b] = r;
-        if (r.len == kEnded) give += r.held;
+        first_page[b] = (int)min(upto, (long long)INT_MAX);
+        first_given[b] = (int)min(give, (long long)p.pool);
+        if (req[b].len >= 0 && !there) req[b].len = kRefusedPages;
+        if (req[b].len == kEnded) give += req[b].held;
         upto += n;
     }
     // Pages handed out in all: what all need, if that is there.
@@ -148,96 +148,90 @@ __global__ void __launch_bounds__(kMostThreads) kv_extend_kernel(const ExtendPar
     }
     __syncthreads();
 
-    // A lane moves the pages of its request, unless they are many: then the warp does.
+    // Goes through `total` things (tokens, pages) that belong to the requests as `first` says: asks for a value for
+    // each of them, then does something with it. A warp takes consecutive groups of 32; it searches for the first
+    // one's request, and from there on a group's requests are among the next 32, one to a lane. What is asked for
+    // kAt groups is on its way together.
     const int lane = tid & 31, gwarp = (tid >> 5) * ctas + cta, gwarps = ctas * (threads / 32);
-    constexpr int kFew = 2;
-    const int share = min(32, max(1, (p.batch + gwarps - 1) / gwarps));  // requests of a warp at a time
-    auto move_pages = [&](int b, int n, auto &&move) {
-        if (n <= kFew)
-            for (int j = 0; j < n; ++j) move(b, j);
-        for (unsigned int many = __ballot_sync(0xffffffffu, n > kFew); many; many &= many - 1) {
-            const int from = __ffs(many) - 1;
-            const int b2 = __shfl_sync(0xffffffffu, b, from), n2 = __shfl_sync(0xffffffffu, n, from);
-            for (int j = lane; j < n2; j += 32) move(b2, j);
+    auto go_through = [&](int by, const int *first, int total, auto &&ask, auto &&take) {  // by: the warp's number
+        constexpr int kAt = 4;
+        const int all = (int)(((long long)total + 31) / 32), groups = (all + gwarps - 1) / gwarps;
+        const int g_begin = (int)min((long long)by * groups, (long long)all), g_end = min(g_begin + groups, all);
+        auto search = [&](int t) {  // the last request that begins at or before t
+            int lo = 0, hi = p.batch - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (first[mid] <= t) lo = mid;
+                else hi = mid - 1;
+            }
+            return lo;
+        };
+        int at = g_begin > 0 && g_begin < g_end ? search(g_begin * 32) : 0;
+        for (int g = g_begin; g < g_end; g += kAt) {
+            int lo[kAt], got[kAt];
+#pragma unroll
+            for (int x = 0; x < kAt; ++x) {
+                lo[x] = got[x] = 0;
+                if (g + x >= g_end) continue;
+                const int t = (g + x) * 32 + lane;
+                const int next = at + 1 + lane < p.batch ? first[at + 1 + lane] : INT_MAX;
+                int c = 0;  // how many of the 32 begin at or before t
+#pragma unroll
+                for (int step = 16; step; step >>= 1)
+                    if (__shfl_sync(0xffffffffu, next, c + step - 1) <= t) c += step;
+                if (__shfl_sync(0xffffffffu, next, c) <= t) ++c;
+                lo[x] = c < 32 ? at + c : search(t);  // 32: many requests without any
+                at = __shfl_sync(0xffffffffu, lo[x], 31);
+                if (t < total) got[x] = ask(t, lo[x]);
+            }
+#pragma unroll
+            for (int x = 0; x < kAt; ++x) {
+                const int t = (g + x) * 32 + lane;
+                if (g + x < g_end && t < total) take(t, lo[x], got[x]);
+            }
         }
     };
-    // Pages given back.
-    for (int b0 = gwarp * share; b0 < p.batch; b0 += gwarps * share) {
-        const int b = b0 + lane;
-        move_pages(b, lane < share && b < p.batch && req[b].len == kEnded ? req[b].held : 0, [&](int b2, int j) {
-            const long long to = count0 + req[b2].page0 + j;
-            if (to < p.pool) p.free_pages[to] = p.table[(long long)b2 * p.table_stride + j];
-        });
-    }
+
+    // Pages given back, behind those that are free.
+    go_through(gwarp, first_given, (int)min(all_given, (long long)p.pool - count0),
+               [&](int n, int b) { return p.table[(long long)b * p.table_stride + (n - first_given[b])]; },
+               [&](int n, int, int page) { p.free_pages[count0 + n] = page; });
     __syncwarp();
     ptx::cluster_sync();
 
-    // Pages handed out: the n-th from the top of the list. Lengths and refusals.
-    const long long top = count - 1;
-    for (int b0 = gwarp * share; b0 < p.batch; b0 += gwarps * share) {
-        const int b = b0 + lane;
-        int n = 0;
-        if (lane < share && b < p.batch) {
-            const Request r = req[b];
-            const int add = p.new_tokens[b];
-            if (r.len >= 0) n = pages(r.len + add) - r.held;
-            p.lens_out[b] = r.len == kEnded ? 0 : r.len >= 0 ? r.len + add : p.lens[b];
-            p.refused[b] = r.len == kRefusedPages ? 1 : r.len == kRefusedRoom ? 2 : 0;
-        }
-        move_pages(b, n, [&](int b2, int j) {
-            p.table[(long long)b2 * p.table_stride + req[b2].held + j] = __ldcg(p.free_pages + (top - (req[b2].page0 + j)));
-        });
+    // Lengths and refusals, in place perhaps: from here on nobody reads the old ones.
+    for (int b = cta * threads + (threads - 1 - tid); b < p.batch; b += ctas * threads) {
+        const int len = req[b].len;
+        p.lens_out[b] = len == kEnded ? 0 : len >= 0 ? len + p.new_tokens[b] : p.lens[b];
+        p.refused[b] = len == kRefusedPages ? 1 : len == kRefusedRoom ? 2 : 0;
     }
-    if (cta == 0 && tid == 0) p.free_count_out[0] = (int)(count - taken);
 
-    // Every token's place. A warp takes consecutive groups of 32 tokens: it searches for the first one's request,
-    // and from there on a group's requests are among the next 32, one to a lane. The looks at the table of kAt
-    // groups are on their way together.
-    constexpr int kAt = 4;
-    const int all_groups = (int)(((long long)p.n_slots + 31) / 32), groups = (all_groups + gwarps - 1) / gwarps;
-    const int g_begin = min((int)min((long long)gwarp * groups, (long long)INT_MAX), all_groups), g_end = min(g_begin + groups, all_groups);
-    auto search = [&](int t) {  // the last request that starts at or before t
-        int lo = 0, hi = p.batch - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (starts[mid] <= t) lo = mid;
-            else hi = mid - 1;
-        }
-        return lo;
+    // Pages handed out: the n-th from the top of the list. Few are the last warps', few tokens the first ones'.
+    const long long top = count - 1;
+    go_through(gwarps - 1 - gwarp, first_page, (int)taken, [&](int n, int) { return __ldcg(p.free_pages + (top - n)); },
+               [&](int n, int b, int page) {
+                   p.table[(long long)b * p.table_stride + req[b].held + (n - first_page[b])] = page;
+               });
+
+    // Every token's place.
+    auto position = [&](int t, int b) {  // -1: no slot
+        const int nth = t - starts[b], len = req[b].len;
+        return len >= 0 && (p.spacing ? nth < p.new_tokens[b] : t < all_tokens) ? len + nth : -1;
     };
-    int first = g_begin < g_end ? search(g_begin * 32) : 0;
-    for (int g = g_begin; g < g_end; g += kAt) {
-        int page[kAt], pos[kAt];
-#pragma unroll
-        for (int x = 0; x < kAt; ++x) {
-            pos[x] = -1, page[x] = 0;
-            if (g + x >= g_end) continue;
-            const int t = (g + x) * 32 + lane;  // below 2^31: a group behind n_slots does not exist
-            const int start = first + 1 + lane < p.batch ? starts[first + 1 + lane] : INT_MAX;
-            int c = 0;  // how many of the 32 start at or before t
-#pragma unroll
-            for (int step = 16; step; step >>= 1)
-                if (__shfl_sync(0xffffffffu, start, c + step - 1) <= t) c += step;
-            if (__shfl_sync(0xffffffffu, start, c) <= t) ++c;
-            int lo = first + c;
-            if (c == 32) lo = search(t);  // many requests without tokens
-            first = __shfl_sync(0xffffffffu, lo, 31);
-            const Request r = req[lo];
-            if (t < p.n_slots && r.len >= 0 && (p.spacing ? t - starts[lo] < p.new_tokens[lo] : t < all_tokens)) {
-                pos[x] = r.len + (t - starts[lo]);
-                const int j = by_page(pos[x]);
-                page[x] = j < r.held ? p.table[(long long)lo * p.table_stride + j]
-                                     : __ldcg(p.free_pages + (top - (r.page0 + j - r.held)));
-            }
-        }
-#pragma unroll
-        for (int x = 0; x < kAt; ++x) {
-            const int t = (g + x) * 32 + lane;
-            if (g + x >= g_end || t >= p.n_slots || t < 0) continue;
-            p.slots[t] = pos[x] < 0 ? -1ll : (long long)page[x] * ps + (pos[x] - by_page(pos[x]) * p.page_size);
-            p.positions[t] = max(pos[x], 0);
-        }
-    }
+    go_through(gwarp, starts, p.n_slots,
+               [&](int t, int b) {
+                   const int pos = position(t, b), j = by_page(max(pos, 0)), held = req[b].held;
+                   return pos < 0    ? 0
+                          : j < held ? p.table[(long long)b * p.table_stride + j]
+                                     : __ldcg(p.free_pages + (top - (first_page[b] + j - held)));
+               },
+               [&](int t, int b, int page) {
+                   const int pos = position(t, b);
+                   p.slots[t] = pos < 0 ? -1ll : (long long)page * ps + (pos - by_page(pos) * p.page_size);
+                   p.positions[t] = max(pos, 0);
+               });
+
+    if (cta == 0 && tid == 0) p.free_count_out[0] = (int)(count - taken);
 }
 
 }  // namespace
