@@ -337,7 +337,7 @@ typedef enum {
  * laid out tokens first, heads first, or both pools in one allocation are all
  * described by the strides. Slot s is token s % page_size of page s / page_size.
  *   type      F16, BF16 or E4M3. E4M3 stores e4m3(x / scale[h]) and stands for
- *             that times scale[h], with one fp32 scale for each kv head
+ *             that times scale[h], with one positive fp32 scale for each kv head
  *   k_scale, v_scale  device fp32 [kv_heads], E4M3 only; NULL means 1
  * Rules: pages, page_size, kv_heads > 0; head_dim a multiple of 8 (E4M3: 16), at
  * most 256; pools 16-byte aligned; strides multiples of 16 bytes, below 2^31 elements.

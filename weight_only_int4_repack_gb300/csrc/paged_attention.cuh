@@ -4,9 +4,9 @@
 // share it.
 //
 // Work. A tile is kWarps slices of 16 or 32 tokens of one request, kv head and block
-// of 8 * NT query heads. All tiles, request after request and head after head, form one line
-// that is cut into equal parts, one for each CTA, so lengths may differ as they
-// like and a single long request still fills the GPU. What a CTA has of a head's
+// of 8 * NT query heads. All tiles, request after request and head after head, form
+// one line that is cut into equal parts, one for each CTA, so lengths may differ as
+// they like and a single long request still fills the GPU. What a CTA has of a head's
 // tokens is a segment; a head whose tokens lie in several CTAs leaves one partial
 // result (maximum, sum, unnormalised output) for each, and the CTA that finishes
 // last joins them in the order of the tokens, so results do not depend on timing.
@@ -15,16 +15,25 @@
 // A segment. Warp w takes the w-th slice of each tile and keeps its own running
 // maximum, sum and output; the warps meet once, at the segment's end. Each warp
 // feeds a ring of its own with 16-byte asynchronous copies (no CTA barrier in the
-// loop), and begins to fill it for the next segment before the warps meet. Tokens are the rows of the matrix instruction and query heads its columns
-// (m16n8k16: S^T = K Q^T, O^T = V^T P^T), so heads are padded to 8, not to 16, and
-// scores and outputs of one head stay in the same threads.
+// loop), and begins to fill it for the next segment before the warps meet. Tokens
+// are the rows of the matrix instruction and query heads its columns (m16n8k16:
+// S^T = K Q^T, O^T = V^T P^T), so heads are padded to 8, not to 16, and scores and
+// outputs of one head stay in the same threads.
+//
+// Measured (GB300, in a CUDA graph): 64 requests of 0 to 8191 tokens, 40 query and 8
+// kv heads of 128 in fp16 (1.16 GB) 177 to 181 us, 6.4 to 6.6 TB/s, the rate of a plain
+// copy; 121 requests of up to 16001 tokens, 32 and 2 heads, 8-bit cache (0.59 GB) 104
+// to 107 us, bound by instructions (about 520 for each 16 tokens of 16 heads, of which
+// 64 convert e4m3 to fp16). A call that is not long, or has few heads, pays about 4 us
+// until the first keys arrive (lengths, then the table, then keys) and 5 to 12 us for
+// joins: one request of 1000 tokens 7.8 us, two of up to 200003 with 2 kv heads 55 us.
 #pragma once
 
 #include <cmath>
 
+#include "decode_ops.h"
 #include "elem.cuh"
 #include "ptx.cuh"
-#include "decode_ops.h"
 
 namespace w4a16 {
 namespace attn {

@@ -14,9 +14,9 @@
 #include <cmath>
 #include <type_traits>
 
+#include "decode_ops.h"
 #include "elem.cuh"
 #include "ptx.cuh"
-#include "decode_ops.h"
 
 namespace w4a16 {
 namespace {
@@ -85,7 +85,10 @@ __device__ __forceinline__ bool place_of(const RopeParams &p, long long slot, Pl
 // heads, where they lie and their bias are found once for all rows. The rows' angles
 // and cache places are worked out once for all heads, in shared memory. (A warp for
 // each row, which finds the heads anew for every one, took 60.7 us for 16384 rows of
-// 36 heads of 128 with an 8-bit cache, where this takes ROPE16384.)
+// 36 heads of 128 with an 8-bit cache, where this takes 52.2.)
+// Measured (GB300, in a CUDA graph): that case (294 MB) 52.2 us, 5.6 TB/s, 84% of the
+// copy rate; 4099 rows of 56 heads in bf16 (118 MB) 22.6 us, 78%: what a CTA does before
+// its first row and the last round of CTAs weigh more there; one row 3.1 us.
 constexpr int kWideWarps = 16, kRowsAtOnce = 8;
 
 template <typename T, typename C, bool kPairs>
