@@ -150,18 +150,18 @@ __device__ __forceinline__ uint32_t place(int row, int chunk) {
 
 // A request's visible tokens [lo, hi).
 struct Range {
-    long long lo, hi;
+    int lo, hi;
 };
 __device__ __forceinline__ Range visible(const Params &p, int b) {
     const long long most = (long long)p.max_pages * p.c.page_size;
     Range r;
-    r.hi = min(max((long long)p.lens[b], 0ll), most);
+    r.hi = (int)min((long long)max(p.lens[b], 0), most);
     r.lo = p.window > 0 && r.hi > p.window ? r.hi - p.window : 0;
     return r;
 }
 template <int kTile>
-__device__ __forceinline__ long long tiles_of(const Range &r) {
-    return r.hi > r.lo ? (r.hi + kTile - 1) / kTile - r.lo / kTile : 0;
+__device__ __forceinline__ int tiles_of(const Range &r) {
+    return r.hi > r.lo ? (r.hi - 1) / kTile + 1 - r.lo / kTile : 0;
 }
 
 // Where a slice's tokens are: lane l knows that of token l (with 16 tokens, so does
@@ -230,8 +230,9 @@ __device__ __forceinline__ uint32_t load_slice(const Params &p, const Places &x,
 // What a CTA has of one item of the line (a request, kv head and block of heads).
 struct Segment {
     int b, kvh, h0, rows, count;  // first query head, heads, tiles
-    int c_first, parts;           // the first CTA with tokens of the item, and how many have some
+    int begin, end;               // the item's tiles in the line
     int t, base;                  // the line's tile behind the segment, and the request's first
+    int c_first, parts;           // the first CTA with tokens of the item, and how many have some (set at its end)
 };
 
 // A running maximum, sum and unnormalised output of 4 elements, and another one
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
     constexpr int kSteps = DT / 16, MT = K::kTok / 16;
     constexpr int kAsk = (kSteps + K::kWarps - 1) / K::kWarps;  // steps whose queries a warp brings
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ long long sums[K::kWarps];
+    __shared__ int sums[K::kWarps];
     __shared__ Segment segs[2], open[2];  // this segment and the next; those that begin before the CTA or end behind it
     __shared__ uint32_t masks[K::kWarps][K::kStages];
     __shared__ float2 meet[K::kWarps][8];  // maxima and sums
@@ -418,30 +419,34 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
     // Where this CTA's part of the line begins.
     const int per = (p.batch + K::kThreads - 1) / K::kThreads;
     const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
-    long long mine = 0;
+    int mine = 0;  // all tiles are below 2^31: the host has seen to that
     for (int b = b0; b < b1; ++b) mine += tiles_of<K::kTile>(visible(p, b));
-    long long upto = mine;
+    int upto = mine;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, upto, x);
+        const int y = __shfl_up_sync(0xffffffffu, upto, x);
         if (lane >= x) upto += y;
     }
     if (lane == 31) sums[warp] = upto;
     __syncthreads();
-    long long total = 0;
+    int total = 0;
 #pragma unroll
     for (int w = 0; w < K::kWarps; ++w) {
         if (w == warp) upto += total;
         total += sums[w];
     }
-    total *= items;  // below 2^31: the host has seen to that
-    const int active = (int)min((long long)ctas, total);  // CTAs with work: each has a tile at least
-    const int t_begin = cta < active ? (int)(total * cta / active) : 0;
-    const int t_end = cta < active ? (int)(total * (cta + 1) / active) : 0;
-    int before = (int)((upto - mine) * items);
+    total *= items;
+    const int active = min(ctas, total);  // CTAs with work: each has a tile at least
+    int t_begin = 0, t_end = 0;           // total * cta / active, in 32 bits
+    if (cta < active) {
+        const int each = total / active, over = total - each * active;
+        t_begin = each * cta + over * cta / active;
+        t_end = each * (cta + 1) + over * (cta + 1) / active;
+    }
+    int before = (upto - mine) * items;
     if (t_begin < t_end && before <= t_begin && t_begin < upto * items) {
         for (int b = b0; b < b1; ++b) {
-            const int n = (int)tiles_of<K::kTile>(visible(p, b)) * items;
+            const int n = tiles_of<K::kTile>(visible(p, b)) * items;
             if (t_begin < before + n) {
                 segs[1].b = b, segs[1].base = before, segs[1].t = t_begin;
                 break;
@@ -504,27 +509,25 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
     auto find_segment = [&](int turn) {
         Segment s = segs[turn ^ 1];
         Range r = visible(p, s.b);
-        int n = (int)tiles_of<K::kTile>(r);
+        int n = tiles_of<K::kTile>(r);
         while (s.t >= s.base + n * items) {
             s.base += n * items;
             r = visible(p, ++s.b);
-            n = (int)tiles_of<K::kTile>(r);
+            n = tiles_of<K::kTile>(r);
         }
         const int item = (s.t - s.base) / n;
-        const int item_begin = s.base + item * n, item_end = item_begin + n;
-        const int seg_end = min(t_end, item_end);
+        s.begin = s.base + item * n, s.end = s.begin + n;
+        const int seg_end = min(t_end, s.end);
         s.kvh = item / p.head_blocks;
         s.h0 = s.kvh * p.group + (item % p.head_blocks) * K::kRows;
         s.rows = min(K::kRows, (s.kvh + 1) * p.group - s.h0);
         s.count = seg_end - s.t;
-        s.c_first = (int)((((long long)item_begin + 1) * active - 1) / total);
-        s.parts = (int)(((long long)item_end * active - 1) / total) - s.c_first + 1;
-        lo = (int)r.lo, hi = (int)r.hi;  // lengths fit 31 bits
+        lo = r.lo, hi = r.hi;
         left = s.count;
         // The lane's first token. Tokens behind the last one may lie beyond 31 bits: taken modulo 2^32 they turn
         // negative and so are outside [lo, hi).
         const unsigned int tok =
-            (unsigned int)((int)(r.lo / K::kTile) + (s.t - item_begin)) * K::kTile + warp * K::kTok + lane % K::kTok;
+            (unsigned int)(r.lo / K::kTile + (s.t - s.begin)) * K::kTile + warp * K::kTok + lane % K::kTok;
         cur.tok = (int)tok;
         cur.j = tok / page_size;
         cur.at = tok - cur.j * page_size;
@@ -793,7 +796,12 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
             stage = stage + 1 == K::kStages ? 0 : stage + 1;
         }
         // Copied before the warps meet: a warp that has met the others may write segs[turn] again.
-        const Segment seg = segs[turn];
+        Segment seg = segs[turn];
+        seg.c_first = cta, seg.parts = 1;
+        if (seg.begin < t_begin || seg.end > t_end) {  // tile x lies with CTA ((x + 1) * active - 1) / total
+            seg.c_first = (int)((((long long)seg.begin + 1) * active - 1) / total);
+            seg.parts = (int)(((long long)seg.end * active - 1) / total) - seg.c_first + 1;
+        }
         if (seg.parts > 1 && tid == 0) open[cta == seg.c_first] = seg;
         // What is loaded from here on belongs to the next segment.
         turn ^= 1;
@@ -825,14 +833,20 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
                 }
             }
             __syncthreads();
-            for (int i = tid; i < 8 * (DT / 4); i += K::kThreads) {
-                const int row = i / (DT / 4), d = i % (DT / 4) * 4;
-                if (nt * 8 + row >= seg.rows || d >= D) continue;
+#pragma unroll
+            for (int i0 = 0; i0 < 8 * (DT / 4); i0 += K::kThreads) {
+                const int i = i0 + tid, row = i / (DT / 4), d = i % (DT / 4) * 4;
+                if (i >= 8 * (DT / 4) || nt * 8 + row >= seg.rows || d >= D) continue;
                 Joined j;
 #pragma unroll
-                for (int w = 0; w < K::kWarps; ++w)
-                    j.take(meet[w][row].x, meet[w][row].y,
-                           *reinterpret_cast<const float4 *>(mo + (w * 8 + row) * K::kPitch + d));
+                for (int w = 0; w < K::kWarps; ++w) j.m = fmaxf(j.m, meet[w][row].x);
+#pragma unroll
+                for (int w = 0; w < K::kWarps; ++w) {
+                    const float f = exp2_approx(meet[w][row].x - (j.m == -INFINITY ? 0.f : j.m));
+                    const float4 x = *reinterpret_cast<const float4 *>(mo + (w * 8 + row) * K::kPitch + d);
+                    j.l += f * meet[w][row].y;
+                    j.o.x += f * x.x, j.o.y += f * x.y, j.o.z += f * x.z, j.o.w += f * x.w;
+                }
                 if (seg.parts == 1) ends.finish(nt * 8 + row, d, j);
                 else ends.leave(ends.part(cta - seg.c_first), nt * 8 + row, d, j, 0);
             }
