@@ -495,6 +495,89 @@ w4a16_status w4a16_residual_rmsnorm(const void *h, w4a16_type h_type, long long 
                                     const void *gamma, float eps, void *h_out, long long ho_row,
                                     void *n_out, long long no_row, int M, int K, void *stream);
 
+/*
+ * The four calls above with their arguments in one block, in the order of the
+ * parameters: for callers to whom every argument of a foreign call costs time (a
+ * Python program spends more of it on 24 arguments than on the launch). Same
+ * checks, same results; a NULL block is W4A16_ERR_INVALID_ARG. The block is read
+ * before the call returns.
+ */
+typedef struct {
+    const int32_t *lens, *new_tokens;
+    int32_t *table;
+    long long table_stride;
+    int batch, max_pages, page_size;
+    int32_t *free_pages;
+    int pool;
+    const int32_t *free_count;
+    int32_t *lens_out, *free_count_out;
+    int64_t *slots;
+    int32_t *positions;
+    int n_slots;
+    int32_t *refused;
+    int spacing;
+    void *stream;
+} w4a16_kv_extend_args;
+typedef struct {
+    const void *q, *k, *v;
+    int type;
+    long long q_row, q_head, k_row, k_head, v_row, v_head;
+    const void *bias;
+    const int32_t *positions;
+    const float *inv_freq;
+    int rot_dim, interleaved;
+    float mscale;
+    void *q_out;
+    long long qo_row, qo_head;
+    const w4a16_kv_cache *cache;
+    const int64_t *slots;
+    int rows, heads;
+    void *stream;
+} w4a16_rope_append_args;
+typedef struct {
+    const void *q;
+    int type;
+    long long q_row, q_head;
+    const w4a16_kv_cache *cache;
+    const int32_t *table;
+    long long table_stride;
+    int max_pages;
+    const int32_t *lens;
+    int batch, heads;
+    float scale;
+    int window;
+    float softcap;
+    void *out;
+    long long o_row, o_head;
+    float *lse;
+    void *ws;
+    size_t ws_bytes;
+    void *stream;
+} w4a16_paged_attention_args;
+typedef struct {
+    const void *h;
+    int h_type;
+    long long h_row;
+    const void *y;
+    int type;
+    long long y_row;
+    const void *post_gamma, *gate;
+    long long gate_row;
+    float alpha;
+    const void *gamma;
+    float eps;
+    void *h_out;
+    long long ho_row;
+    void *n_out;
+    long long no_row;
+    int M, K;
+    void *stream;
+} w4a16_residual_rmsnorm_args;
+w4a16_status w4a16_kv_extend_block(const w4a16_kv_extend_args *args);
+w4a16_status w4a16_rope_append_block(const w4a16_rope_append_args *args);
+w4a16_status w4a16_paged_attention_block(const w4a16_paged_attention_args *args);
+w4a16_status w4a16_residual_rmsnorm_block(const w4a16_residual_rmsnorm_args *args);
+
 #ifdef __cplusplus
 }
 #endif

@@ -2,6 +2,7 @@
 (fake addresses, nothing is launched) and of the binding, the frequency helper
 against its formulas, and the oracle on worked examples."""
 import ctypes
+import struct
 
 import numpy as np
 import pytest
@@ -139,6 +140,38 @@ def norm(w4, **kw):
 ])
 def test_residual_rmsnorm_refusals(w4, kw, status):
     assert norm(w4, **kw) == status
+
+
+# ------------------------------------------------------------------ the calls with their arguments in one block
+class Blocks:
+    """Stands for the library where a call's arguments go as the block of its parameters, in their order."""
+
+    def __init__(self, w4):
+        self.w4, self.lib, self.KVCache = w4, self, w4.KVCache
+
+    def __getattr__(self, name):
+        def call(*args):
+            flat = [0 if a is None else ctypes.addressof(a) if isinstance(a, ctypes.Structure) else a for a in args]
+            return getattr(self.w4.lib, name + "_block")(struct.pack(self.w4._blocks[name], *flat))
+        return call
+
+
+@pytest.mark.parametrize("call,kw,status", [
+    (extend, dict(batch=8193), UNSUPPORTED), (extend, dict(refused=None), INVALID), (extend, dict(spacing=-1), INVALID),
+    (extend, dict(slots=0x10004), INVALID), (extend, dict(n=-1), INVALID), (extend, dict(batch=0), 0),
+    (rope, dict(rot=6), UNSUPPORTED), (rope, dict(bias=BAD4), INVALID), (rope, dict(v_head=-128), INVALID),
+    (rope, dict(slots=0x10004), INVALID), (rope, dict(heads=0), INVALID), (rope, dict(rows=0), 0),
+    (attention, dict(heads=41), INVALID), (attention, dict(cap=-1.0), INVALID), (attention, dict(lse=BAD4), INVALID),
+    (attention, dict(ws_bytes=0), WORKSPACE), (attention, dict(type=1), UNSUPPORTED), (attention, dict(batch=0), 0),
+    (norm, dict(K=5124), UNSUPPORTED), (norm, dict(eps=-1.0), INVALID), (norm, dict(no_row=5112), INVALID),
+    (norm, dict(h_type=2), INVALID), (norm, dict(gate=A, gate_row=8), INVALID), (norm, dict(M=0), 0)])
+def test_blocks_are_read_in_order(w4, call, kw, status):
+    assert call(w4, **kw) == status and call(Blocks(w4), **kw) == status
+
+
+def test_blocks_refuse_none(w4):
+    for name in w4._blocks:
+        assert getattr(w4.lib, name + "_block")(None) == INVALID
 
 
 # ------------------------------------------------------------------ binding

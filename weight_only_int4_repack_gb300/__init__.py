@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Tuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -52,6 +53,8 @@ EXPORTS = (
     "w4a16_gemm_swiglu_rmsnorm", "w4a16_gemm_launch_info", "w4a16_gemm_host_io",
     "w4a16_kv_extend", "w4a16_rope_frequencies", "w4a16_rope_append",
     "w4a16_paged_attention_workspace_bytes", "w4a16_paged_attention", "w4a16_residual_rmsnorm",
+    "w4a16_kv_extend_block", "w4a16_rope_append_block", "w4a16_paged_attention_block",
+    "w4a16_residual_rmsnorm_block",
 )
 
 _vp, _ci, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
@@ -98,6 +101,7 @@ class KVCache(ctypes.Structure):
         super().__init__(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), *k.stride()[:3],
                          *v.stride()[:3], _TYPES[k.dtype], *k.shape)
         self.tensors = (k, v, k_scale, v_scale)
+        self.address = ctypes.addressof(self)
 
 
 def _expect(t, dtype, what):
@@ -143,10 +147,21 @@ _sig = {
     "w4a16_residual_rmsnorm": (_ci, [_vp, _ci, _ll, _vp, _ci, _ll, _vp, _vp, _ll, _cf, _vp, _cf, _vp, _ll, _vp,
                                      _ll, _ci, _ci, _vp]),
 }
+# The same calls with their arguments in one block: packed by `struct` in the parameters' order (native alignment, as
+# the C structs of include/w4a16.h), which costs a fifth of what ctypes takes to convert them one by one.
+_blocks = {
+    "w4a16_kv_extend": "PPPqiiiPiPPPPPiPiP",
+    "w4a16_rope_append": "PPPiqqqqqqPPPiifPqqPPiiP",
+    "w4a16_paged_attention": "PiqqPPqiPiififPqqPPNP",
+    "w4a16_residual_rmsnorm": "PiqPiqPPqfPfPqPqiiP",
+}
+_sig.update({_name + "_block": (_ci, [ctypes.c_char_p]) for _name in _blocks})
 for _name, (_res, _args) in _sig.items():
     _f = getattr(lib, _name)
     _f.restype = _res
     _f.argtypes = _args
+_pack_extend, _pack_rope, _pack_attention, _pack_norm = (struct.Struct(_blocks[_name]).pack for _name in _blocks)
+_extend, _rope, _attention, _norm = (getattr(lib, _name + "_block") for _name in _blocks)
 
 
 class W4A16Error(RuntimeError):
@@ -364,18 +379,19 @@ def w4a16_kv_extend(lens, new_tokens, table, free_pages, free_count, page_size: 
         raise TypeError("w4a16_kv_extend: slots is int64, everything else int32")
     n_slots = slots.numel()
     if (not (lens.is_contiguous() and new_tokens.is_contiguous() and free_pages.is_contiguous() and slots.is_contiguous()
-             and positions.is_contiguous() and refused.is_contiguous() and lens_out.is_contiguous())
+             and positions.is_contiguous() and refused.is_contiguous() and (lens_out is lens or lens_out.is_contiguous()))
             or (max_pages > 1 and table.stride(1) != 1)
             or not lens.numel() == new_tokens.numel() == refused.numel() == lens_out.numel() == batch
             or positions.numel() != n_slots):
         raise ValueError("w4a16_kv_extend: table is [batch, max_pages], the others are contiguous with one entry for "
                          "each request or slot")
-    _check(lib.w4a16_kv_extend(lens.data_ptr(), new_tokens.data_ptr(), table.data_ptr(),
-                               table.stride(0) if batch > 1 else max_pages, batch,
-                               max_pages, page_size, free_pages.data_ptr(), free_pages.numel(),
-                               free_count.data_ptr(), lens_out.data_ptr(), count_out.data_ptr(), slots.data_ptr(),
-                               positions.data_ptr(), n_slots, refused.data_ptr(), spacing, _stream(stream)),
-           "w4a16_kv_extend")
+    status = _extend(_pack_extend(
+        lens.data_ptr(), new_tokens.data_ptr(), table.data_ptr(), table.stride(0) if batch > 1 else max_pages, batch,
+        max_pages, page_size, free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(), lens_out.data_ptr(),
+        count_out.data_ptr(), slots.data_ptr(), positions.data_ptr(), n_slots, refused.data_ptr(), spacing,
+        _stream(stream)))
+    if status:
+        raise W4A16Error(status, "w4a16_kv_extend")
     return lens_out
 
 
@@ -411,11 +427,13 @@ def w4a16_rope_append(q, k, v, positions, inv_freq, cache, slots, interleaved: b
         _expect(bias, q.dtype, "bias")
         if bias.numel() != (heads + 2 * cache.kv_heads) * D:
             raise ValueError("bias: (heads + 2*kv_heads) * head_dim elements")
-    _check(lib.w4a16_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), _TYPES.get(q.dtype, -1), sq[0], sq[1],
-                                 sk[0], sk[1], sv[0], sv[1], None if bias is None else bias.data_ptr(),
-                                 positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.numel(), int(interleaved),
-                                 mscale, out.data_ptr(), so[0], so[1], cache, slots.data_ptr(), rows, heads,
-                                 _stream(stream)), "w4a16_rope_append")
+    status = _rope(_pack_rope(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _TYPES.get(q.dtype, -1), sq[0], sq[1], sk[0], sk[1], sv[0], sv[1],
+        0 if bias is None else bias.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.numel(),
+        interleaved, mscale, out.data_ptr(), so[0], so[1], cache.address, slots.data_ptr(), rows, heads,
+        _stream(stream)))
+    if status:
+        raise W4A16Error(status, "w4a16_rope_append")
     return out
 
 
@@ -448,12 +466,14 @@ def w4a16_paged_attention(q, cache, table, lens, scale: Optional[float] = None, 
         _expect(lse, torch.float32, "lse")
         if lse.numel() != batch * heads:
             raise ValueError("lse: [batch, heads]")
-    _check(lib.w4a16_paged_attention(q.data_ptr(), _TYPES.get(q.dtype, -1), sq[0], sq[1], cache, table.data_ptr(),
-                                     table.stride(0) if batch > 1 else max_pages, max_pages, lens.data_ptr(), batch,
-                                     heads, D ** -0.5 if scale is None else scale, window, softcap, out.data_ptr(),
-                                     so[0], so[1], None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), _stream(stream)),
-           "w4a16_paged_attention")
+    status = _attention(_pack_attention(
+        q.data_ptr(), _TYPES.get(q.dtype, -1), sq[0], sq[1], cache.address, table.data_ptr(),
+        table.stride(0) if batch > 1 else max_pages, max_pages, lens.data_ptr(), batch, heads,
+        D ** -0.5 if scale is None else scale, window, softcap, out.data_ptr(), so[0], so[1],
+        0 if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream(stream)))
+    if status:
+        raise W4A16Error(status, "w4a16_paged_attention")
     return out
 
 
@@ -484,14 +504,14 @@ def w4a16_residual_rmsnorm(h, y, gamma=None, eps: float = 1e-5, post_gamma=None,
             gate is not None and gate.dtype is not y.dtype):
         raise TypeError("w4a16_residual_rmsnorm: h_out has h's type, n_out and gate have y's")
     gate_row = 0 if gate is None or gate.dim() == 1 else gate.stride(0) if M > 1 else K
-    _check(lib.w4a16_residual_rmsnorm(h.data_ptr(), _TYPES.get(h.dtype, -1), h.stride(0) if M > 1 else K,
-                                      y.data_ptr(), _TYPES.get(y.dtype, -1), y.stride(0) if M > 1 else K,
-                                      None if post_gamma is None else post_gamma.data_ptr(),
-                                      None if gate is None else gate.data_ptr(), gate_row, alpha,
-                                      None if gamma is None else gamma.data_ptr(), eps, h_out.data_ptr(),
-                                      h_out.stride(0) if M > 1 else K, None if n_out is None else n_out.data_ptr(),
-                                      0 if n_out is None else n_out.stride(0) if M > 1 else K, M, K,
-                                      _stream(stream)), "w4a16_residual_rmsnorm")
+    status = _norm(_pack_norm(
+        h.data_ptr(), _TYPES.get(h.dtype, -1), h.stride(0) if M > 1 else K, y.data_ptr(), _TYPES.get(y.dtype, -1),
+        y.stride(0) if M > 1 else K, 0 if post_gamma is None else post_gamma.data_ptr(),
+        0 if gate is None else gate.data_ptr(), gate_row, alpha, 0 if gamma is None else gamma.data_ptr(), eps,
+        h_out.data_ptr(), h_out.stride(0) if M > 1 else K, 0 if n_out is None else n_out.data_ptr(),
+        0 if n_out is None else n_out.stride(0) if M > 1 else K, M, K, _stream(stream)))
+    if status:
+        raise W4A16Error(status, "w4a16_residual_rmsnorm")
     return h_out, n_out
 
 

@@ -290,3 +290,11 @@ extern "C" w4a16_status w4a16_kv_extend(const int32_t *lens, const int32_t *new_
     cfg.numAttrs = launch_overlap() ? 2 : 1;
     return from_cuda(cudaLaunchKernelEx(&cfg, kv_extend_kernel, p));
 }
+
+extern "C" w4a16_status w4a16_kv_extend_block(const w4a16_kv_extend_args *args) {
+    if (!args) return W4A16_ERR_INVALID_ARG;
+    const w4a16_kv_extend_args &a = *args;
+    return w4a16_kv_extend(a.lens, a.new_tokens, a.table, a.table_stride, a.batch, a.max_pages, a.page_size, a.free_pages,
+                           a.pool, a.free_count, a.lens_out, a.free_count_out, a.slots, a.positions, a.n_slots,
+                           a.refused, a.spacing, a.stream);
+}

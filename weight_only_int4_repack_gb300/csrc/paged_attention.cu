@@ -63,4 +63,12 @@ w4a16_status w4a16_paged_attention(const void *q, w4a16_type type, long long q_r
     return from_cuda(type == W4A16_TYPE_F16 ? attn::launch_f16(p, sm_count(), s) : attn::launch_bf16(p, sm_count(), s));
 }
 
+w4a16_status w4a16_paged_attention_block(const w4a16_paged_attention_args *args) {
+    if (!args) return W4A16_ERR_INVALID_ARG;
+    const w4a16_paged_attention_args &a = *args;
+    return w4a16_paged_attention(a.q, (w4a16_type)a.type, a.q_row, a.q_head, a.cache, a.table, a.table_stride,
+                                 a.max_pages, a.lens, a.batch, a.heads, a.scale, a.window, a.softcap, a.out, a.o_row,
+                                 a.o_head, a.lse, a.ws, a.ws_bytes, a.stream);
+}
+
 }  // extern "C"

@@ -183,3 +183,11 @@ extern "C" w4a16_status w4a16_residual_rmsnorm(const void *h, w4a16_type h_type,
     return from_cuda(h_type == W4A16_TYPE_F32 ? launch<__nv_bfloat16, float>(p, M, s)
                                               : launch<__nv_bfloat16, __nv_bfloat16>(p, M, s));
 }
+
+extern "C" w4a16_status w4a16_residual_rmsnorm_block(const w4a16_residual_rmsnorm_args *args) {
+    if (!args) return W4A16_ERR_INVALID_ARG;
+    const w4a16_residual_rmsnorm_args &a = *args;
+    return w4a16_residual_rmsnorm(a.h, (w4a16_type)a.h_type, a.h_row, a.y, (w4a16_type)a.type, a.y_row, a.post_gamma,
+                                  a.gate, a.gate_row, a.alpha, a.gamma, a.eps, a.h_out, a.ho_row, a.n_out, a.no_row,
+                                  a.M, a.K, a.stream);
+}

@@ -415,4 +415,12 @@ w4a16_status w4a16_rope_append(const void *q, const void *k, const void *v, w4a1
                                             : launch_type<__nv_bfloat16>(p, interleaved != 0, wide, s));
 }
 
+w4a16_status w4a16_rope_append_block(const w4a16_rope_append_args *args) {
+    if (!args) return W4A16_ERR_INVALID_ARG;
+    const w4a16_rope_append_args &a = *args;
+    return w4a16_rope_append(a.q, a.k, a.v, (w4a16_type)a.type, a.q_row, a.q_head, a.k_row, a.k_head, a.v_row, a.v_head,
+                             a.bias, a.positions, a.inv_freq, a.rot_dim, a.interleaved, a.mscale, a.q_out, a.qo_row,
+                             a.qo_head, a.cache, a.slots, a.rows, a.heads, a.stream);
+}
+
 }  // extern "C"
