@@ -357,36 +357,60 @@ struct Ends {
 // CTAs (when there are many), then over the groups. A CTA is in front of the end of one
 // item only, so counters at its number, one for items that begin in it and one for the
 // item that does not, are not shared.
-template <typename K, typename T>
-__device__ __forceinline__ void join_parts(const Ends<K, T> &ends, float *area, float2 *rows, int *is_last) {
-    const Segment &seg = ends.seg;
-    unsigned int *counters = ends.p.counters;
-    int group = seg.parts;  // one round, if shared memory holds them all
-    if (group > K::kJoin) {
-        group = min(8, K::kJoin);
-        while (group * group < seg.parts) ++group;
-    }
-    const int of = ((int)blockIdx.x - seg.c_first) / group, in_group = min(group, seg.parts - of * group);
-    const int groups = (seg.parts + group - 1) / group;
-    // Both rounds go through the same instructions: those of a second copy would come from far away.
-#pragma unroll 1
-    for (int round = 0; round < 2; ++round) {
-        unsigned int *counter = round ? counters + 2 * kMaxCtas + seg.c_first
-                                : of == 0 ? counters + seg.c_first : counters + kMaxCtas + seg.c_first + of * group;
-        const int n = round ? groups : in_group;
-        // The barrier in front of the atomic puts every thread's partial result before it.
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            unsigned int old;
-            asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
-            *is_last = old == (unsigned int)n - 1u;
-            if (*is_last) *counter = 0u;  // ready for the next call
+template <typename K>
+struct Groups {
+    int group, of, here, all;  // CTAs of a group, this CTA's group, its CTAs, groups
+    __device__ __forceinline__ Groups(const Segment &seg) {
+        group = seg.parts;  // one round, if shared memory holds them all
+        if (group > K::kJoin) {
+            group = min(8, K::kJoin);
+            while (group * group < seg.parts) ++group;
         }
-        __syncthreads();
-        if (!*is_last) return;
-        const bool end = round || groups == 1;
-        ends.join(area, rows, round ? 0 : of * group, round ? group : 1, n, round, end);
-        if (end) return;
+        of = ((int)blockIdx.x - seg.c_first) / group;
+        here = min(group, seg.parts - of * group);
+        all = (seg.parts + group - 1) / group;
+    }
+};
+// Whether this is the last of `n` arrivals. What the CTA's other threads have written
+// before a barrier in front of this counts as written before it.
+__device__ __forceinline__ bool arrive(unsigned int *counter, int n) {
+    unsigned int old;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+    const bool last = old == (unsigned int)n - 1u;
+    if (last) *counter = 0u;  // ready for the next call
+    return last;
+}
+// Joins the CTA's segments that are not whole (two at most). It arrives for both before
+// it joins either: a join takes as long as others would wait for the second arrival.
+template <typename K, typename T>
+__device__ __forceinline__ void join_parts(const Params &p, const Segment *open, bool k8, float *area, float2 *rows, int *last) {
+    if (threadIdx.x < 2) {
+        const Segment seg = open[threadIdx.x];
+        bool mine = false;
+        if (seg.parts > 1) {
+            const Groups<K> g(seg);
+            mine = arrive(g.of == 0 ? p.counters + seg.c_first : p.counters + kMaxCtas + seg.c_first + g.of * g.group, g.here);
+        }
+        last[threadIdx.x] = mine;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int x = 0; x < 2; ++x) {
+        if (!last[x]) continue;
+        const Segment seg = open[x];
+        const Groups<K> g(seg);
+        const Ends<K, T> ends{p, seg, k8 && p.c.v_scale ? p.c.v_scale[seg.kvh] : 1.f};
+        // Both rounds go through the same instructions: those of a second copy would come from far away.
+#pragma unroll 1
+        for (int round = 0; round < 2; ++round) {
+            const bool end = round || g.all == 1;
+            ends.join(area, rows, round ? 0 : g.of * g.group, round ? g.group : 1, round ? g.all : g.here, round, end);
+            if (end) break;
+            __syncthreads();
+            if (threadIdx.x == 0) last[2] = arrive(p.counters + 2 * kMaxCtas + seg.c_first, g.all);
+            __syncthreads();
+            if (!last[2]) break;
+        }
     }
 }
 
@@ -406,7 +430,7 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
     __shared__ Segment segs[2], open[2];  // this segment and the next; those that begin before the CTA or end behind it
     __shared__ uint32_t masks[K::kWarps][K::kStages];
     __shared__ float2 meet[K::kWarps][8];  // maxima and sums
-    __shared__ int is_last;
+    __shared__ int last[3];
     // With launch overlap the next kernel's CTAs come when this one's leave, not earlier: beside these, which fill the
     // SMs' shared memory, they only took SMs in an uneven way (a decoding step of four layers of width 5120: 333 us
     // against 339 with an early signal for 8 requests, 295 against 314 for one).
@@ -857,13 +881,7 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
     // The parts that are not whole (the first segment and the last at most) are joined behind the loop, where
     // nothing of it holds registers.
     __syncthreads();
-#pragma unroll 1
-    for (int x = 0; x < 2; ++x) {
-        const Segment seg = open[x];
-        if (seg.parts < 2) continue;
-        join_parts<K, T>(Ends<K, T>{p, seg, k8 && p.c.v_scale ? p.c.v_scale[seg.kvh] : 1.f},
-                         reinterpret_cast<float *>(smem), meet[0], &is_last);
-    }
+    join_parts<K, T>(p, open, k8, reinterpret_cast<float *>(smem), meet[0], last);
 }
 
 template <typename T, typename C, int DT, int NT>
