@@ -317,9 +317,10 @@ w4a16_status w4a16_device_error(void *stream);
  *     treated as the call's comment says, and leaves W4A16_ERR_INVALID_ARG in
  *     the device error word (w4a16_device_error), unless that comment gives it
  *     a status of its own.
- *   - With w4a16_set_launch_overlap(1) the calls are programmatic dependents of
- *     the work before them on the stream, as the small-M GEMM is; they read
- *     nothing before that work has completed, so they have no further rule.
+ *   - The calls may be launched as programmatic dependents of the work before
+ *     them on the stream; they touch no memory before that work has completed, so
+ *     they have no rule to keep. With w4a16_set_launch_overlap(1) captured calls
+ *     are too, and all but paged_attention let the work behind them begin early.
  *   - Sums, softmax statistics and norms are held in fp32; every output element
  *     is rounded once, to nearest even.
  * ------------------------------------------------------------------------ */

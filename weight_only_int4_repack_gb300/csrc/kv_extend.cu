@@ -30,6 +30,7 @@ struct ExtendParams {
     int batch, max_pages, page_size, pool, n_slots;
     unsigned int magic, shift;  // n / page_size = n * magic >> shift for 0 <= n < 2^31
     int spacing;  // slots from one request's first token to the next one's; 0: they follow each other
+    bool overlap;
 };
 
 constexpr int kMostThreads = 1024;
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(kMostThreads) kv_extend_kernel(const ExtendPar
     int *starts = reinterpret_cast<int *>(req + p.batch), *first_page = starts + p.batch, *first_given = first_page + p.batch;
     __shared__ long long warp_sums[3][32];
     __shared__ long long taken;
-    ptx::grid_dep_launch();
+    if (p.overlap) ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     const int ctas = gridDim.x, cta = blockIdx.x, tid = threadIdx.x, threads = blockDim.x;
     if (tid == 0) taken = 0;
@@ -269,7 +270,7 @@ extern "C" w4a16_status w4a16_kv_extend(const int32_t *lens, const int32_t *new_
     const unsigned int magic = (unsigned int)whole, shift = 31 + l;
     const ExtendParams p{lens,      new_tokens, free_count, table,        free_pages, lens_out,  free_count_out,
                          positions, refused,    slots,      table_stride, batch,      max_pages, page_size,
-                         pool,      n_slots,    magic,        shift,      spacing};
+                         pool,      n_slots,    magic,        shift,      spacing,   launch_overlap()};
     cudaError_t e = ensure_max_dyn_smem((const void *)kv_extend_kernel, kMaxBatch * kRequestBytes);
     if (e != cudaSuccess) return from_cuda(e);
     // A step of running requests fits one CTA, and a small one is done sooner with fewer warps to wait for.
@@ -287,7 +288,7 @@ extern "C" w4a16_status w4a16_kv_extend(const int32_t *lens, const int32_t *new_
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = launch_overlap() ? 2 : 1;
+    cfg.numAttrs = as_dependent(cfg.stream) ? 2 : 1;
     return from_cuda(cudaLaunchKernelEx(&cfg, kv_extend_kernel, p));
 }
 

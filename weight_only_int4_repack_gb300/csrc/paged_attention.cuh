@@ -913,7 +913,7 @@ cudaError_t launch(Params p, int sms, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = launch_overlap() ? 1 : 0;
+    cfg.numAttrs = as_dependent(s) ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 

@@ -20,6 +20,7 @@ struct NormParams {
     long long h_row, y_row, gate_row, ho_row, no_row;
     int K;
     float alpha, eps;
+    bool overlap;
 };
 
 constexpr int kMaxK = 32768;
@@ -56,7 +57,7 @@ __global__ void __launch_bounds__(kMost) residual_norm_kernel(const NormParams p
     using VT = elem::Vec<T, 8>;
     using VH = elem::Vec<H, 8>;
     __shared__ float red[2][32];
-    ptx::grid_dep_launch();
+    if (p.overlap) ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     const long long row = blockIdx.x;
     const int groups = p.K / 8, threads = blockDim.x;
@@ -141,7 +142,7 @@ cudaError_t launch(const NormParams &p, int M, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = launch_overlap() ? 1 : 0;
+    cfg.numAttrs = as_dependent(s) ? 1 : 0;
     if (many)
         return v == 4 ? cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, H, 4, 256>, p)
                       : cudaLaunchKernelEx(&cfg, residual_norm_kernel<T, H, 2, 256>, p);
@@ -176,7 +177,7 @@ extern "C" w4a16_status w4a16_residual_rmsnorm(const void *h, w4a16_type h_type,
         return W4A16_ERR_INVALID_ARG;
     if (h_row % hv || ho_row % hv || y_row % 8 || (n_out && no_row % 8) || (gate && gate_row % 8))
         return W4A16_ERR_INVALID_ARG;
-    NormParams p{h, y, post_gamma, gate, gamma, h_out, n_out, h_row, y_row, gate_row, ho_row, no_row, K, alpha, eps};
+    NormParams p{h, y, post_gamma, gate, gamma, h_out, n_out, h_row, y_row, gate_row, ho_row, no_row, K, alpha, eps, launch_overlap()};
     cudaStream_t s = (cudaStream_t)stream;
     if (type == W4A16_TYPE_F16)
         return from_cuda(h_type == W4A16_TYPE_F32 ? launch<__half, float>(p, M, s) : launch<__half, __half>(p, M, s));

@@ -34,6 +34,7 @@ struct RopeParams {
     int rows, heads, rot, at_once;
     float mscale;
     unsigned int *err;
+    bool overlap;
 };
 
 constexpr int kThreads = 128;
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(32 * kWideWarps, 2) rope_append_wide_kernel(co
     // Row r's cos and sin of frequencies 8u + 2e, 8u + 2e + 1 at [r][e * turning units + u]: lanes side by side.
     __shared__ float4 cs[kRowsAtOnce][kMaxHalf / 2];
     __shared__ long long k_at[kRowsAtOnce], v_at[kRowsAtOnce];  // offsets in the pools; k_at < 0: not written
-    ptx::grid_dep_launch();
+    if (p.overlap) ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int row0 = blockIdx.x * p.at_once, rows = min(p.at_once, p.rows - row0);
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
     using VT = elem::Vec<T, 2>;
     using VC = elem::Vec<C, 2>;
     __shared__ float2 cs[kMaxHalf];
-    ptx::grid_dep_launch();
+    if (p.overlap) ptx::grid_dep_launch();
     ptx::grid_dep_wait();
     const long long row = blockIdx.x;
     const int half = p.rot / 2, D = p.c.head_dim;
@@ -307,7 +308,7 @@ cudaError_t launch(RopeParams p, bool pairs, bool wide, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = launch_overlap() ? 1 : 0;
+    cfg.numAttrs = as_dependent(s) ? 1 : 0;
     if (!wide) {
         cfg.gridDim = dim3((unsigned)p.rows, 1, 1);
         return pairs ? cudaLaunchKernelEx(&cfg, rope_append_kernel<T, C, true>, p)
@@ -408,7 +409,7 @@ w4a16_status w4a16_rope_append(const void *q, const void *k, const void *v, w4a1
         wide = wide && s % 8 == 0;
     }
     RopeParams p{q, k, v, bias, q_out, q_row, q_head, k_row, k_head, v_row, v_head, qo_row, qo_head,
-                 positions, inv_freq, slots, *cache, rows, heads, rot_dim, 1, mscale, device_error_ptr()};
+                 positions, inv_freq, slots, *cache, rows, heads, rot_dim, 1, mscale, device_error_ptr(), launch_overlap()};
     if (!p.err) return W4A16_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
     return from_cuda(type == W4A16_TYPE_F16 ? launch_type<__half>(p, interleaved != 0, wide, s)

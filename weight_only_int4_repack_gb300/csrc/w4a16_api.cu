@@ -41,6 +41,12 @@ unsigned int *w4a16::device_error_ptr() {
 
 bool w4a16::launch_overlap() { return g_launch_overlap != 0; }
 
+bool w4a16::as_dependent(cudaStream_t s) {
+    if (g_launch_overlap) return true;
+    cudaStreamCaptureStatus st;
+    return cudaStreamIsCapturing(s, &st) == cudaSuccess && st == cudaStreamCaptureStatusNone;
+}
+
 cudaError_t w4a16::ensure_max_dyn_smem(const void *func, int bytes) {
     static std::set<std::pair<const void *, int>> done;
     int dev = 0;
