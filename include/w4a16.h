@@ -337,6 +337,8 @@ typedef enum {
  * token t of page p is at p*page + t*token + h*head + d of its pool, so pages
  * laid out tokens first, heads first, or both pools in one allocation are all
  * described by the strides. Slot s is token s % page_size of page s / page_size.
+ * Heads whose rows are no multiple of 128 bytes are read faster from pages laid out
+ * heads first.
  *   type      F16, BF16 or E4M3. E4M3 stores e4m3(x / scale[h]) and stands for
  *             that times scale[h], with one positive fp32 scale for each kv head
  *   k_scale, v_scale  device fp32 [kv_heads], E4M3 only; NULL means 1

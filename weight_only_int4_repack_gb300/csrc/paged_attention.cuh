@@ -21,12 +21,15 @@
 // outputs of one head stay in the same threads.
 //
 // Measured (GB300, in a CUDA graph): 64 requests of 0 to 8191 tokens, 40 query and 8
-// kv heads of 128 in fp16 (1.16 GB) 177 to 181 us, 6.4 to 6.6 TB/s, the rate of a plain
-// copy; 121 requests of up to 16001 tokens, 32 and 2 heads, 8-bit cache (0.59 GB) 104
-// to 107 us, bound by instructions (about 520 for each 16 tokens of 16 heads, of which
+// kv heads of 128 in fp16 (1.16 GB) 173 to 180 us, 6.5 to 6.7 TB/s, the rate of a plain
+// copy; 121 requests of up to 16001 tokens, 32 and 2 heads, 8-bit cache (0.59 GB) 101
+// to 105 us, bound by instructions (about 520 for each 16 tokens of 16 heads, of which
 // 64 convert e4m3 to fp16). A call that is not long, or has few heads, pays about 4 us
-// until the first keys arrive (lengths, then the table, then keys) and 5 to 12 us for
+// until the first keys arrive (lengths, then the table, then keys) and 3 to 12 us for
 // joins: one request of 1000 tokens 7.8 us, two of up to 200003 with 2 kv heads 55 us.
+// Rows of a head that are no multiple of 128 bytes, in a cache laid out tokens first,
+// share memory lines with other heads' that are read at another time: 52% of the copy
+// rate with 64 e4m3 elements, 73% with 96 of fp16; heads first 92% and 100%.
 #pragma once
 
 #include <cmath>
