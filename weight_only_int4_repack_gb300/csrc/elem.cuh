@@ -43,14 +43,7 @@ __device__ __forceinline__ uint16_t pair_to_e4m3(float a, float b) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
     return r;
 }
-// Two e4m3 values as two fp16 values (exact).
-__device__ __forceinline__ uint32_t e4m3_to_half2(uint16_t x) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
-    return r;
-}
-
-// The lower and the upper two of four e4m3 values as fp16.
+// The lower and the upper two of four e4m3 values as fp16 (exact).
 __device__ __forceinline__ void e4m3x4_to_half2(uint32_t x, uint32_t &lo, uint32_t &hi) {
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
         : "=r"(lo), "=r"(hi)
@@ -118,20 +111,6 @@ struct Vec<E4M3, N> {
             __stcs(reinterpret_cast<uint2 *>(p), make_uint2(w[0] | ((uint32_t)w[1] << 16), w[2] | ((uint32_t)w[3] << 16)));
         else
             *reinterpret_cast<uint16_t *>(p) = w[0];
-    }
-    static __device__ __forceinline__ void load(const E4M3 *p, float (&f)[N]) {
-        uint16_t w[N / 2];
-        if constexpr (N == 8) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(p);
-            w[0] = (uint16_t)x.x, w[1] = (uint16_t)(x.x >> 16), w[2] = (uint16_t)x.y, w[3] = (uint16_t)(x.y >> 16);
-        } else {
-            w[0] = *reinterpret_cast<const uint16_t *>(p);
-        }
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-            const float2 v = pair_to_f32<__half>(e4m3_to_half2(w[i]));
-            f[2 * i] = v.x, f[2 * i + 1] = v.y;
-        }
     }
 };
 
