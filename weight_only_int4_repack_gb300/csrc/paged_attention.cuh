@@ -196,8 +196,9 @@ __device__ __forceinline__ uint32_t load_slice(const Params &p, const Places &x,
     const uint32_t mask = __ballot_sync(0xffffffffu, good) & K::kAll;
     // The offset of the lane's token from the pool's first (a slice begins at a multiple of 16 tokens).
     const unsigned int page = good ? x.page : 0, at = good ? x.at : 0;
-    const unsigned long long k_at = (unsigned long long)page * p.k_page + (unsigned long long)at * p.k_token;
-    const unsigned long long v_at = (unsigned long long)page * p.v_page + (unsigned long long)at * p.v_token;
+    const unsigned long long k_token = p.k_token, v_token = p.v_token;  // products below are of 64 bits
+    const unsigned long long k_at = (unsigned long long)page * p.k_page + at * k_token;
+    const unsigned long long v_at = (unsigned long long)page * p.v_page + at * v_token;
     auto copy_row = [&](int i, const C *kr, const C *vr) {
         const bool ok = (mask >> (i * kRowsAt + row0)) & 1u;
 #pragma unroll
@@ -213,18 +214,18 @@ __device__ __forceinline__ uint32_t load_slice(const Params &p, const Places &x,
         for (int g = 0; g < K::kTok / 16; ++g) {
             const uint32_t here = (mask >> (16 * g)) & 0xffffu;
             const int from = here ? __ffs(here) - 1 : 0;
-            const C *kr = k + (__shfl_sync(0xffffffffu, k_at, 16 * g + from) - from * p.k_token);
-            const C *vr = v + (__shfl_sync(0xffffffffu, v_at, 16 * g + from) - from * p.v_token);
+            const C *kr = k + (__shfl_sync(0xffffffffu, k_at, 16 * g + from) - from * k_token);
+            const C *vr = v + (__shfl_sync(0xffffffffu, v_at, 16 * g + from) - from * v_token);
 #pragma unroll
             for (int i = 0; i < 16 / kRowsAt; ++i)
-                copy_row(g * (16 / kRowsAt) + i, kr + i * kRowsAt * p.k_token, vr + i * kRowsAt * p.v_token);
+                copy_row(g * (16 / kRowsAt) + i, kr + i * kRowsAt * k_token, vr + i * kRowsAt * v_token);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < K::kTok / kRowsAt; ++i) {
             const int row = i * kRowsAt + row0;
-            copy_row(i, k + (__shfl_sync(0xffffffffu, k_at, row) - row0 * p.k_token),
-                     v + (__shfl_sync(0xffffffffu, v_at, row) - row0 * p.v_token));
+            copy_row(i, k + (__shfl_sync(0xffffffffu, k_at, row) - row0 * k_token),
+                     v + (__shfl_sync(0xffffffffu, v_at, row) - row0 * v_token));
         }
     }
     return mask;
