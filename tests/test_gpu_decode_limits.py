@@ -36,3 +36,49 @@ def test_attention_token_strides_beyond_32_bits(w4, page, stride, window):
     check_attention(w4, q, cache, pools, scales, table, lens, page, window=window)
     del flat, pools, cache
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ streams of the caller's
+def on_side_stream(call, as_number):
+    """call(stream) while the current stream is busy and its free memory holds ones; the result."""
+    torch.cuda.synchronize()
+    junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (1 << 24, 1 << 23, 1 << 20, 1 << 14)]
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(200_000_000)
+    del junk
+    out = call(side.cuda_stream if as_number else side)
+    side.synchronize()
+    early = not torch.cuda.current_stream().query()
+    torch.cuda.synchronize()
+    assert early, "the current stream was to be busy all the while"
+    return out
+
+
+@pytest.mark.parametrize("as_number", [False, True])
+def test_calls_on_another_stream_than_the_current_one(w4, as_number):
+    lens, page = [3000, 9, 777], 16
+    q, cache, pools, scales, table = build(w4, lens, 8, 2, 64, F16, F16, page, "tokens", 8)
+    t, n = i32(table), i32(lens)
+    want = w4.w4a16_paged_attention(q, cache, t, n)
+    assert torch.equal(on_side_stream(lambda s: w4.w4a16_paged_attention(q, cache, t, n, stream=s), as_number), want)
+    h, y, gm = normal((5, 64), F16, 1), normal((5, 64), F16, 2), normal((64,), F16, 3)
+    want = w4.w4a16_residual_rmsnorm(h, y, gm)
+    got = on_side_stream(lambda s: w4.w4a16_residual_rmsnorm(h, y, gm, stream=s), as_number)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    args = i32([5, 6, 7]), torch.ones(32, device="cuda"), cache, torch.tensor([0, 1, 2], device="cuda")
+    want = w4.w4a16_rope_append(q, q[:, :2], q[:, 2:4], *args)
+    assert torch.equal(on_side_stream(lambda s: w4.w4a16_rope_append(q, q[:, :2], q[:, 2:4], *args, stream=s), as_number), want)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    weight = torch.randint(0, 256, (256, 128), dtype=torch.uint8, device="cuda", generator=g)
+    scale = torch.full((256, 2), 0.01, dtype=F16, device="cuda")
+    rep, a, gm = w4.w4a16_repack(weight), normal((5, 256), F16, 4), normal((256,), F16, 5)
+    side = lambda s: {"stream": s}  # noqa: E731
+    for call in (lambda kw: w4.w4a16_repack(weight, **kw),
+                 lambda kw: w4.w4a16_gemm(a, rep, scale, None, 128, **kw),
+                 lambda kw: w4.w4a16_gemm_swiglu(a, rep, scale, None, rep, scale, None, 128, **kw),
+                 lambda kw: w4.w4a16_gemm_swiglu(a, rep, scale, None, rep, scale, None, 128, fused=False, **kw),
+                 lambda kw: w4.w4a16_gemm_rmsnorm(a, gm, 1e-5, rep, scale, None, 128, **kw),
+                 lambda kw: w4.w4a16_gemm_swiglu_rmsnorm(a, gm, 1e-5, rep, scale, None, rep, scale, None, 128, **kw),
+                 lambda kw: w4.w4a16_gemm_swiglu_unfused_static(a, rep, scale, None, rep, scale, None, 128, **kw)):
+        want = call({})
+        assert torch.equal(on_side_stream(lambda s: call(side(s)), as_number), want)

@@ -3,7 +3,9 @@ the operators between two such GEMMs of a decoder layer).
 
 Argument marshalling only: every step of the computation runs in the CUDA
 library. PyTorch supplies device memory and the current stream. The functions
-carry the C ABI's names (include/w4a16.h); `lib` is the raw ctypes handle.
+carry the C ABI's names (include/w4a16.h); `lib` is the raw ctypes handle. A call with
+`stream` runs there; outputs and workspaces that it makes belong to that stream, inputs
+have to be ready on it.
 
 Importing fails loudly when the compiled library is missing: there is no CPU or
 PyTorch fallback.
@@ -197,6 +199,15 @@ def _stream(stream) -> Optional[int]:
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _new(shape, dtype, like, stream, make=torch.empty):
+    """A tensor on `like`'s device for a call on `stream`. Made under that stream: it is cleared there, if at all, and its
+    memory is not given to work of another stream while the call may still use it."""
+    if stream is None or _stream(stream) == _stream(None):
+        return make(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, like.device) if isinstance(stream, int) else stream):
+        return make(shape, dtype=dtype, device=like.device)
+
+
 def w4a16_repacked_bytes(N: int, K: int) -> int:
     return int(lib.w4a16_repacked_bytes(N, K))
 
@@ -206,7 +217,7 @@ def w4a16_repack(q, out=None, stream=None):
     import torch
     N, K = q.shape[0], 2 * q.shape[1]
     if out is None:
-        out = torch.empty(w4a16_repacked_bytes(N, K), dtype=torch.uint8, device=q.device)
+        out = _new(w4a16_repacked_bytes(N, K), torch.uint8, q, stream)
     _check(lib.w4a16_repack(_ptr(q), _ptr(out), N, K, _stream(stream)), "w4a16_repack")
     return out
 
@@ -258,7 +269,7 @@ def w4a16_gemm(A, q_rep, scales, zp, group: int, out=None, split_k: int = 0, wor
     M, K = A.shape
     N = scales.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=A.device)
+        out = _new((M, N), torch.float16, A, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.w4a16_gemm(_ptr(A), _ptr(q_rep), _ptr(scales), _scale_dtype(scales), _ptr(zp),
                           _ptr(out), M, N, K, group, split_k, _ptr(workspace), ws_bytes,
@@ -290,10 +301,10 @@ def w4a16_gemm_swiglu(A, qg_rep, sg, zg, qu_rep, su, zu, group: int, fused: bool
     M, K = A.shape
     N = sg.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=A.device)
+        out = _new((M, N), torch.float16, A, stream)
     need = w4a16_swiglu_workspace_bytes(M, N, K, group, fused)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=A.device)
+        workspace = _new(need, torch.uint8, A, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.w4a16_gemm_swiglu(_ptr(A), _ptr(qg_rep), _ptr(sg), _ptr(zg), _ptr(qu_rep),
                                  _ptr(su), _ptr(zu), _scale_dtype(sg), _ptr(out), M, N, K, group,
@@ -313,10 +324,9 @@ def w4a16_gemm_rmsnorm(A, gamma, eps: float, q_rep, scales, zp, group: int, out=
     M, K = A.shape
     N = scales.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=A.device)
+        out = _new((M, N), torch.float16, A, stream)
     if workspace is None:
-        workspace = torch.empty(w4a16_rmsnorm_workspace_bytes(M, N, K, group, 0), dtype=torch.uint8,
-                                device=A.device)
+        workspace = _new(w4a16_rmsnorm_workspace_bytes(M, N, K, group, 0), torch.uint8, A, stream)
     ws_bytes = workspace.numel() * workspace.element_size()
     _check(lib.w4a16_gemm_rmsnorm(_ptr(A), _ptr(gamma), float(eps), _ptr(q_rep), _ptr(scales),
                                   _scale_dtype(scales), _ptr(zp), _ptr(out), M, N, K, group, split_k,
@@ -331,10 +341,9 @@ def w4a16_gemm_swiglu_rmsnorm(A, gamma, eps: float, qg_rep, sg, zg, qu_rep, su, 
     M, K = A.shape
     N = sg.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=A.device)
+        out = _new((M, N), torch.float16, A, stream)
     if workspace is None:
-        workspace = torch.empty(w4a16_rmsnorm_workspace_bytes(M, N, K, group, 1 if fused else 2),
-                                dtype=torch.uint8, device=A.device)
+        workspace = _new(w4a16_rmsnorm_workspace_bytes(M, N, K, group, 1 if fused else 2), torch.uint8, A, stream)
     ws_bytes = workspace.numel() * workspace.element_size()
     _check(lib.w4a16_gemm_swiglu_rmsnorm(_ptr(A), _ptr(gamma), float(eps), _ptr(qg_rep), _ptr(sg), _ptr(zg),
                                          _ptr(qu_rep), _ptr(su), _ptr(zu), _scale_dtype(sg), _ptr(out),
@@ -355,7 +364,7 @@ def w4a16_gemm_swiglu_unfused_static(A, qg_rep, sg, zg, qu_rep, su, zu, group: i
     M, K = A.shape
     N = sg.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=A.device)
+        out = _new((M, N), torch.float16, A, stream)
     _check(lib.w4a16_gemm_swiglu_unfused_static(_ptr(A), _ptr(qg_rep), _ptr(sg), _ptr(zg),
                                                 _ptr(qu_rep), _ptr(su), _ptr(zu),
                                                 _scale_dtype(sg), _ptr(out), M, N, K, group,
@@ -411,7 +420,7 @@ def w4a16_rope_append(q, k, v, positions, inv_freq, cache, slots, interleaved: b
     q, k, v may be views of one joined projection; out may be q."""
     rows, heads, D = q.shape
     if out is None:
-        out = torch.empty((rows, heads, D), dtype=q.dtype, device=q.device)
+        out = _new((rows, heads, D), q.dtype, q, stream)
     if (positions.dtype is not _int32 or slots.dtype is not _int64 or inv_freq.dtype is not _float32
             or not (positions.is_contiguous() and slots.is_contiguous() and inv_freq.is_contiguous())):
         raise TypeError("w4a16_rope_append: positions int32, slots int64, inv_freq float32, contiguous")
@@ -451,10 +460,10 @@ def w4a16_paged_attention(q, cache, table, lens, scale: Optional[float] = None, 
     batch, heads, D = q.shape
     max_pages = table.shape[1]
     if out is None:
-        out = torch.empty((batch, heads, D), dtype=q.dtype, device=q.device)
+        out = _new((batch, heads, D), q.dtype, q, stream)
     if workspace is None:
         need = w4a16_paged_attention_workspace_bytes(batch, heads, cache.kv_heads, D)
-        workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
+        workspace = _new(need, torch.uint8, q, stream, torch.zeros)
     sq, so = q.stride(), out.stride()
     if (D != cache.head_dim or table.shape[0] != batch or lens.numel() != batch or out.shape != q.shape
             or sq[2] != 1 or so[2] != 1 or (max_pages > 1 and table.stride(1) != 1)):
@@ -484,9 +493,9 @@ def w4a16_residual_rmsnorm(h, y, gamma=None, eps: float = 1e-5, post_gamma=None,
     or [M, K]; h_out may be h."""
     M, K = h.shape
     if h_out is None:
-        h_out = torch.empty((M, K), dtype=h.dtype, device=h.device)
+        h_out = _new((M, K), h.dtype, h, stream)
     if gamma is not None and n_out is None:
-        n_out = torch.empty((M, K), dtype=y.dtype, device=y.device)
+        n_out = _new((M, K), y.dtype, y, stream)
     shape = h.shape
     if (y.shape != shape or h_out.shape != shape or (n_out is not None and n_out.shape != shape)
             or (gate is not None and gate.shape != shape and gate.shape != (K,))):
