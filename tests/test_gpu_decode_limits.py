@@ -38,6 +38,39 @@ def test_attention_token_strides_beyond_32_bits(w4, page, stride, window):
     torch.cuda.empty_cache()
 
 
+# ------------------------------------------------------------------ paged_attention: the softmax's weights
+def few_large(w4, dtype, cdtype, score, large, small, requests=912, n=640, page=16):
+    """Requests over the same pages: keys 0, 16, .. 112 have a score of `score` and the value `large`, the others a score
+    of 0 and the values `small` [kv_heads, D] (8-bit caches: one value for each head). So many requests that a CTA has
+    some from end to end: its weights are relative to the largest, which comes first. Returns outputs [requests, kv_heads,
+    D] and the part that the others have of the sum of weights."""
+    kv, D = small.shape
+    cache, pools, scales = make_cache(w4, n // page, page, kv, D, cdtype, 5)
+    first = (torch.arange(n, device="cuda").view(n // page, page, 1, 1) % 16 == 0)
+    first &= torch.arange(n, device="cuda").view(n // page, page, 1, 1) < 128
+    one = torch.ones(n // page, page, kv, D, device="cuda")
+    unit = small if cdtype != E4M3 else torch.ones_like(small)
+    pools[0].copy_(torch.where(first, one * (score / math.sqrt(D)), one * 0).to(cdtype))
+    pools[1].copy_(torch.where(first, one * large, one * unit.cuda()).to(cdtype))
+    if cdtype == E4M3:
+        scales[0].fill_(1.0)
+        scales[1].copy_(small[:, 0])
+    table = np.arange(n // page)[None].repeat(requests, 0)
+    q = torch.ones(requests, kv, D, dtype=dtype, device="cuda")
+    out = w4.w4a16_paged_attention(q, cache, i32(table), i32([n] * requests))
+    w = (n - 8) * math.exp(-score)
+    return f64(out), w / (8 + w)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_attention_over_one_value_returns_it(w4, dtype):
+    # All values of the 8-bit cache stand for 2047/1024. Weights of exp(-3.25) are rounded up by 3.5e-4 each, more than
+    # the output's half step there; the sums of 640 weights and products differ by 704 e = 4.2e-5 at most.
+    small = torch.full((1, 64), 2047 / 1024)
+    got, _ = few_large(w4, dtype, E4M3, 3.25, 1.0, small)
+    assert (got == f64(small.to(dtype))).all()
+
+
 # ------------------------------------------------------------------ streams of the caller's
 def on_side_stream(call, as_number):
     """call(stream) while the current stream is busy and its free memory holds ones; the result."""
