@@ -71,6 +71,18 @@ def test_attention_over_one_value_returns_it(w4, dtype):
     assert (got == f64(small.to(dtype))).all()
 
 
+@pytest.mark.parametrize("score", [14.0, 18.0, 20.0])
+@pytest.mark.parametrize("dtype,cdtype", [(F16, F16), (BF16, BF16), (F16, E4M3), (BF16, E4M3)])
+def test_attention_weights_far_below_the_largest(w4, dtype, cdtype, score):
+    # The largest weights' values are 0, so the output is made of weights of 2^-20 to 2^-29 of them. As fp16 operands
+    # each is off by 2^-35 of the largest, besides their rounding (half a step with 8-bit caches, 2^-16 otherwise).
+    got, share = few_large(w4, dtype, cdtype, score, 0.0, torch.full((2, 64), 28672.0))
+    want = 28672.0 * share
+    rounding = U[F16] if cdtype == E4M3 else 2.0**-16
+    bound = (U[dtype] + rounding + 704 * E) * want + 632 / 8 * 2.0**-35 * 28672.0
+    assert np.abs(got - want).max() <= bound
+
+
 # ------------------------------------------------------------------ streams of the caller's
 def on_side_stream(call, as_number):
     """call(stream) while the current stream is busy and its free memory holds ones; the result."""

@@ -256,9 +256,9 @@ struct Joined {
 
 // The reference that scores are taken relative to is moved (and everything summed so
 // far rescaled) only when a score passes it by more than kSlack powers of two: then
-// weights reach 2^(kUp + kSlack) = 2^14, within fp16's range, and fp16 holds those
-// down to 2^-18 of the reference with full precision (and smaller ones to 2^-28).
-constexpr float kUp = 4.f, kSlack = 10.f;
+// weights reach 2^(kUp + kSlack) = 2^15, within fp16's range, and fp16 holds those
+// down to 2^-25 of the reference with full precision, smaller ones to 2^-36 of it.
+constexpr float kUp = 11.f, kSlack = 4.f;
 
 // Where a segment's results go.
 template <typename K, typename T>
