@@ -83,6 +83,12 @@ def test_attention_weights_far_below_the_largest(w4, dtype, cdtype, score):
     assert np.abs(got - want).max() <= bound
 
 
+def test_attention_sums_values_as_large_as_fp32_does(w4):
+    # 640 values of 2^118 with weights of 1 at most: sums stay below 2^128.
+    got, _ = few_large(w4, BF16, BF16, 0.0, 2.0**118, torch.full((1, 64), 2.0**118))
+    assert (got == 2.0**118).all()
+
+
 # ------------------------------------------------------------------ streams of the caller's
 def on_side_stream(call, as_number):
     """call(stream) while the current stream is busy and its free memory holds ones; the result."""

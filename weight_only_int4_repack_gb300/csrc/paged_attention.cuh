@@ -33,6 +33,7 @@
 #pragma once
 
 #include <cmath>
+#include <type_traits>
 
 #include "decode_ops.h"
 #include "elem.cuh"
@@ -63,8 +64,20 @@ constexpr int kMaxCtas = 1024;
 constexpr int kMaxPartial = 16 * (128 + 4);  // floats of the largest partial result (8 * (256 + 4) is less)
 constexpr int kMostPerSm = 3;                // CTAs on an SM at most
 
+// The reference that scores are taken relative to is moved (and everything summed so
+// far rescaled) only when a score passes it by more than kSlack powers of two. The
+// reference's own weight is 2^kUp. As fp16 operands weights then reach 2^15, within the
+// range, and are held down to 2^-25 of the reference with full precision, smaller ones
+// to 2^-36 of it. bf16 has the range of fp32: there they stay below 1, so that values of
+// any size can be summed.
+constexpr float kSlack = 4.f;
+template <typename M>
+constexpr float kUpOf = std::is_same<M, __half>::value ? 11.f : -kSlack;
+
 template <typename T, typename C, int DT, int NT>
 struct Config {
+    using M = typename std::conditional<sizeof(C) == 1, __half, T>::type;  // operand type
+    static constexpr float kUp = kUpOf<M>;
     static constexpr int kDim = DT;                        // head_dim, rounded up
     static constexpr int kRows = 8 * NT;                   // query heads of a block
     static constexpr int kBytes = sizeof(C);
@@ -254,12 +267,6 @@ struct Joined {
     }
 };
 
-// The reference that scores are taken relative to is moved (and everything summed so
-// far rescaled) only when a score passes it by more than kSlack powers of two: then
-// weights reach 2^(kUp + kSlack) = 2^15, within fp16's range, and fp16 holds those
-// down to 2^-25 of the reference with full precision, smaller ones to 2^-36 of it.
-constexpr float kUp = 11.f, kSlack = 4.f;
-
 // Where a segment's results go.
 template <typename K, typename T>
 struct Ends {
@@ -276,7 +283,7 @@ struct Ends {
         *reinterpret_cast<uint2 *>(out) =
             make_uint2(elem::pair_from_f32<T>(j.o.x * f, j.o.y * f), elem::pair_from_f32<T>(j.o.z * f, j.o.w * f));
         if (p.lse && d == 0)
-            p.lse[(long long)seg.b * p.heads + seg.h0 + row] = any ? (j.m + log2f(j.l) - kUp) * kLn2 : -INFINITY;
+            p.lse[(long long)seg.b * p.heads + seg.h0 + row] = any ? (j.m + log2f(j.l) - K::kUp) * kLn2 : -INFINITY;
     }
     // The place of the i-th partial result of these heads.
     __device__ __forceinline__ float *part(int i) const {
@@ -424,7 +431,8 @@ template <typename T, typename C, int DT, int NT>
 __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, DT, NT>::kPerSm) paged_attention_kernel(const __grid_constant__ Params p) {
     using K = Config<T, C, DT, NT>;
     constexpr bool k8 = sizeof(C) == 1;
-    using M = typename std::conditional<k8, __half, T>::type;  // operand type
+    using M = typename K::M;
+    constexpr float kUp = K::kUp;
     // Weights become one operand of 16 bits and, with 16-bit caches, a second one for what the first's rounding
     // left: alone it would be as coarse as the output's own rounding. With 8-bit values, whose own rounding is
     // 2^-4, that second product is not spent (104 -> 117 us for 121 requests of 32 heads), but the weights are summed
