@@ -89,6 +89,32 @@ def test_attention_sums_values_as_large_as_fp32_does(w4):
     assert (got == 2.0**118).all()
 
 
+@pytest.mark.parametrize("dtype,cdtype", [(F16, F16), (BF16, BF16), (F16, E4M3), (BF16, E4M3)])
+@pytest.mark.parametrize("scale", [3000.0, 7.3e6, -1.9e12, 1.1e20])
+def test_attention_scores_beyond_24_bits(w4, dtype, cdtype, scale):
+    # Exact products far apart: the best key's value is the output, and its score the lse, however large it is.
+    lens, page, heads = [700, 3, 90], 16, 6
+    q, cache, pools, scales, table = build(w4, lens, heads, 2, 64, dtype, cdtype, page, "tokens", 3)
+    for s in scales:
+        if s is not None:
+            s.fill_(1.0)
+    q.fill_(3.0)
+    g = torch.Generator().manual_seed(1)
+    pools[0].copy_(torch.randint(-8, 8, pools[0].shape, generator=g).float().cuda().to(cdtype))
+    lse = torch.empty(3, heads, device="cuda")
+    out = w4.w4a16_paged_attention(q, cache, i32(table), i32(lens), scale=scale, lse=lse)
+    for b, n in enumerate(lens):
+        pages = torch.as_tensor(table[b, :-(-n // page)]).cuda()
+        k, v = (f64(p.float()[pages]).reshape(-1, 2, 64)[:n] for p in pools)
+        score = 3.0 * k.sum(2) * scale
+        for h in range(heads):
+            mine = score[:, h // 3]
+            best = mine == mine.max()
+            want = v[best, h // 3].mean(0)
+            assert np.abs(f64(out[b, h]) - want).max() <= U[dtype] * np.abs(want).max() + 2.0**-16 * np.abs(v).max()
+            assert abs(float(lse[b, h]) - mine.max()) <= 8 * E * abs(mine.max())
+
+
 # ------------------------------------------------------------------ streams of the caller's
 def on_side_stream(call, as_number):
     """call(stream) while the current stream is busy and its free memory holds ones; the result."""

@@ -70,7 +70,7 @@ constexpr int kMostPerSm = 3;                // CTAs on an SM at most
 // range, and are held down to 2^-25 of the reference with full precision, smaller ones
 // to 2^-36 of it. bf16 has the range of fp32: there they stay below 1, so that values of
 // any size can be summed.
-constexpr float kSlack = 4.f;
+constexpr float kSlack = 4.f, kLowest = -3.402823466e38f;
 template <typename M>
 constexpr float kUpOf = std::is_same<M, __half>::value ? 11.f : -kSlack;
 
@@ -676,16 +676,14 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
     }
     while (more) {
         float o[kSteps][NT][4];
-        // Of the thread's two heads: the reference, the score that moves it, what is added to a score's power of
-        // two, the sum of the weights (of the thread's own rows) and, where they are rounded once, that of what they
-        // were rounded to.
-        float m[NT][2], limit[NT][2], off[NT][2], l[NT][2], rounded[kTwo ? 1 : NT][2];
+        // Of the thread's two heads: the reference, the score that moves it, the sum of the weights (of the thread's own
+        // rows) and, where they are rounded once, that of what they were rounded to.
+        float m[NT][2], limit[NT][2], l[NT][2], rounded[kTwo ? 1 : NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int ks = 0; ks < kSteps; ++ks) o[ks][nt][0] = o[ks][nt][1] = o[ks][nt][2] = o[ks][nt][3] = 0.f;
-            m[nt][0] = m[nt][1] = limit[nt][0] = limit[nt][1] = -INFINITY;
-            off[nt][0] = off[nt][1] = kUp;  // no token so far: all weights are 0 against any reference
+            m[nt][0] = m[nt][1] = limit[nt][0] = limit[nt][1] = kLowest;  // no token so far
             l[nt][0] = l[nt][1] = 0.f;
             if constexpr (!kTwo) rounded[nt][0] = rounded[nt][1] = 0.f;
         }
@@ -776,10 +774,9 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
                         y = fmaxf(y, m[nt][x]);
-                        keep[x] = y == -INFINITY ? 1.f : exp2_approx((m[nt][x] - y) * unit);
+                        keep[x] = exp2_approx((m[nt][x] - y) * unit);
                         m[nt][x] = y;
                         limit[nt][x] = y + slack;
-                        off[nt][x] = kUp - (y == -INFINITY ? 0.f : y * unit);
                         l[nt][x] *= keep[x];
                         if constexpr (!kTwo) rounded[nt][x] *= keep[x];
                     }
@@ -796,7 +793,8 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
                 for (int nt = 0; nt < NT; ++nt) {
                     float w[4];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) w[x] = exp2_approx(fmaf(s[mt][nt][x], unit, off[nt][x & 1]));
+                    for (int x = 0; x < 4; ++x)  // differences first: however large both are, the reference's weight is 2^kUp
+                        w[x] = exp2_approx(fmaf(s[mt][nt][x] - m[nt][x & 1], unit, kUp));
                     l[nt][0] += w[0] + w[2], l[nt][1] += w[1] + w[3];
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
