@@ -115,6 +115,43 @@ def test_attention_scores_beyond_24_bits(w4, dtype, cdtype, scale):
             assert abs(float(lse[b, h]) - mine.max()) <= 8 * E * abs(mine.max())
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("lens", [[50, 300, 1], [20000, 3]])
+def test_attention_infinite_values_stay_infinite(w4, dtype, lens):
+    page = 16
+    q, cache, pools, scales, table = build(w4, lens, 8, 2, 64, dtype, dtype, page, "tokens", 8, q_scale=1.0)
+    clean = w4.w4a16_paged_attention(q, cache, i32(table), i32(lens))
+    inf = float("inf")
+    for b, n in enumerate(lens):
+        for j in range(0, n, 7):  # elements 3 and 9: one sign; element 20: one such value; 33: both signs
+            pools[1][int(table[b, j // page]), j % page, 1, 3] = inf
+            pools[1][int(table[b, j // page]), j % page, 1, 9] = -inf
+        at = n // 2
+        pools[1][int(table[b, at // page]), at % page, 1, 20] = inf
+        pools[1][int(table[b, 0]), 0, 1, 33] = -inf
+        pools[1][int(table[b, (n - 1) // page]), (n - 1) % page, 1, 33] = inf
+    out = w4.w4a16_paged_attention(q, cache, i32(table), i32(lens))
+    want = clean.clone()
+    want[:, 4:, 3], want[:, 4:, 9], want[:, 4:, 20] = inf, -inf, inf
+    want[:, 4:, 33] = torch.tensor([inf if n == 1 else math.nan for n in lens], device="cuda")[:, None]
+    np.testing.assert_array_equal(f64(out), f64(want))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_attention_weights_are_not_rounded_to_the_operands_type(w4, dtype):
+    # Weights of exp(-3.25), of which one in 16 bits is 3.5e-4 (fp16) or 1.1e-3 (bf16) too large. As two operands they are
+    # exact to 2^-16, sums of 640 terms to 704 e: all outputs but those near a border have to be the correctly rounded
+    # ones.
+    small = (torch.rand(8, 64, generator=torch.Generator().manual_seed(3)) + 1.0).to(dtype).float()
+    got, share = few_large(w4, dtype, dtype, 3.25, 0.0, small)
+    half = lambda x: f64(torch.as_tensor(x, dtype=torch.float64).to(dtype))  # noqa: E731
+    want, off = f64(small) * share, 2.0**-16 + 704 * E
+    sure = half(want * (1 - off)) == half(want * (1 + off))
+    once = float(torch.tensor(math.exp(-3.25), dtype=torch.float64).to(dtype)) * math.exp(3.25)
+    assert sure.mean() > 0.8 and (half(want * once) != half(want))[sure].mean() > 0.1  # what is asked for is worth asking
+    np.testing.assert_array_equal(got[:, sure], half(want)[None, sure].repeat(len(got), 0))
+
+
 # ------------------------------------------------------------------ streams of the caller's
 def on_side_stream(call, as_number):
     """call(stream) while the current stream is busy and its free memory holds ones; the result."""

@@ -156,6 +156,26 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
+// Two weights as pairs of 16-bit operands: h, and l for what h's rounding left. h is rounded
+// down and l is never 0 where h is not (2^-24 or 2^-126 at least), so that an infinite value
+// times either is that infinity.
+__device__ __forceinline__ void split(float a, float b, uint32_t &h, uint32_t &l, __half) {
+    uint32_t least;
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(b), "f"(a));
+    const float2 f = elem::pair_to_f32<__half>(h);
+    l = elem::pair_from_f32<__half>(a - f.x, b - f.y);
+    asm("min.f16x2 %0, %1, %2;" : "=r"(least) : "r"(h), "r"(0x00010001u));
+    asm("max.f16x2 %0, %1, %2;" : "=r"(l) : "r"(l), "r"(least));
+}
+__device__ __forceinline__ void split(float a, float b, uint32_t &h, uint32_t &l, __nv_bfloat16) {
+    uint32_t least;
+    h = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+    const float2 f = elem::pair_to_f32<__nv_bfloat16>(h);
+    l = elem::pair_from_f32<__nv_bfloat16>(a - f.x, b - f.y);
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(least) : "r"(h), "r"(0x00800080u));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(l) : "r"(l), "r"(least));
+}
+
 // Byte offset of 16-byte chunk `chunk` of ring row `row`: chunks change places so
 // that the eight rows of an 8x8 matrix lie in eight different bank groups.
 template <int kChunks>
@@ -798,13 +818,16 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
                     l[nt][0] += w[0] + w[2], l[nt][1] += w[1] + w[3];
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const uint32_t h = elem::pair_from_f32<M>(w[2 * x], w[2 * x + 1]);
-                        ph[mt][nt][x] = transpose8x8(h);
-                        const float2 f = elem::pair_to_f32<M>(h);
-                        if constexpr (kTwo)
-                            pl[mt][nt][x] = transpose8x8(elem::pair_from_f32<M>(w[2 * x] - f.x, w[2 * x + 1] - f.y));
-                        else
+                        if constexpr (kTwo) {
+                            uint32_t h, lo;
+                            split(w[2 * x], w[2 * x + 1], h, lo, M());
+                            ph[mt][nt][x] = transpose8x8(h), pl[mt][nt][x] = transpose8x8(lo);
+                        } else {
+                            const uint32_t h = elem::pair_from_f32<M>(w[2 * x], w[2 * x + 1]);
+                            ph[mt][nt][x] = transpose8x8(h);
+                            const float2 f = elem::pair_to_f32<M>(h);
                             rounded[nt][0] += f.x, rounded[nt][1] += f.y;
+                        }
                     }
                 }
             // Outputs: 16 elements of the head at a time.
