@@ -152,6 +152,30 @@ def test_attention_weights_are_not_rounded_to_the_operands_type(w4, dtype):
     np.testing.assert_array_equal(got[:, sure], half(want)[None, sure].repeat(len(got), 0))
 
 
+@pytest.mark.parametrize("heads,kv,D", [(8, 1, 128), (32, 2, 64), (8, 1, 256), (5, 1, 48)])
+def test_attention_heads_of_any_size_on_8_bit_keys(w4, heads, kv, D):
+    # Each head's queries are brought to fp16 by a power of two of their own: neighbours 2^30 larger take nothing away.
+    lens, page = [130, 17, 1], 16
+    q, cache, pools, scales, table = build(w4, lens, heads, kv, D, BF16, E4M3, page, "tokens", 8)
+    q.mul_(torch.exp2(torch.arange(heads, device="cuda") % 5 * -30.0 + 30.0).to(BF16)[:, None])
+    check_attention(w4, q, cache, pools, scales, table, lens, page)
+    check_attention(w4, q, cache, pools, scales, table, lens, page, cap=4.0)
+
+
+def test_attention_infinite_and_nan_queries_stay_in_their_head_on_8_bit_keys(w4):
+    lens, page = [50, 130], 16
+    q, cache, pools, scales, table = build(w4, lens, 16, 1, 128, BF16, E4M3, page, "tokens", 8)
+    q[:, 2] *= 2.0**100
+    clean = w4.w4a16_paged_attention(q, cache, i32(table), i32(lens))
+    q[0, 5, 7], q[1, 9, 3] = float("inf"), float("nan")
+    out = w4.w4a16_paged_attention(q, cache, i32(table), i32(lens))
+    nan = torch.isnan(out)
+    assert nan[0, 5].all() and nan[1, 9].all()
+    clean[0, 5], clean[1, 9] = 0, 0
+    out[0, 5], out[1, 9] = 0, 0
+    assert torch.equal(out, clean)
+
+
 # ------------------------------------------------------------------ streams of the caller's
 def on_side_stream(call, as_number):
     """call(stream) while the current stream is busy and its free memory holds ones; the result."""

@@ -467,6 +467,7 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
     __shared__ uint32_t masks[K::kWarps][K::kStages];
     __shared__ float2 meet[K::kWarps][8];  // maxima and sums
     __shared__ int last[3];
+    __shared__ float ups[K::kRows];  // what a head's products have to be multiplied by, where that is not 1 (kOwnPower)
     // With launch overlap the next kernel's CTAs come when this one's leave, not earlier: beside these, which fill the
     // SMs' shared memory, they only took SMs in an uneven way (a decoding step of four layers of width 5120: 333 us
     // against 339 with an early signal for 8 requests, 295 against 314 for one).
@@ -620,14 +621,16 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
         }
     };
     uint32_t *q_area = reinterpret_cast<uint32_t *>(mo);
+    constexpr bool kOwnPower = k8 && !std::is_same<T, __half>::value;
     auto put_queries = [&] {
         // A scale of 0 or below turns into queries that are 0 (above) or negated, and a positive scale.
         const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
-        float result = 1.f, down = 1.f;
-        if constexpr (k8 && !std::is_same<T, __half>::value) {
+        [[maybe_unused]] float down[NT];
+        if constexpr (kOwnPower) {
             // bf16 queries against 8-bit keys: keys become fp16 (exact), queries fp16 after a power of two that
-            // brings the block's largest below 2; what that loses is 2^-25 of the largest.
-            float big = 0.f;
+            // brings their head's largest below 2; what that loses is 2^-25 of the largest.
+            static_assert(NT <= 2, "a warp's maxima of two heads lie in one pair");
+            float big[2] = {0.f, 0.f};  // of heads lane/4 and 8 + lane/4
 #pragma unroll
             for (int x = 0; x < kAsk; ++x)
 #pragma unroll
@@ -635,17 +638,27 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const float2 f = elem::pair_to_f32<T>(asked[x][nt][y]);
-                        big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+                        big[nt] = fmaxf(big[nt], fmaxf(fabsf(f.x), fabsf(f.y)));
                     }
 #pragma unroll
-            for (int x = 16; x > 0; x >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
-            if (lane == 0) meet[warp][0].x = big;
+            for (int nt = 0; nt < NT; ++nt) {
+                big[nt] = fmaxf(big[nt], __shfl_xor_sync(0xffffffffu, big[nt], 1));
+                big[nt] = fmaxf(big[nt], __shfl_xor_sync(0xffffffffu, big[nt], 2));
+            }
+            if (lane % 4 == 0) meet[warp][lane / 4] = make_float2(big[0], big[1]);
             __syncthreads();
+            auto power = [&](int nt, int head) {
+                float most = 0.f;
 #pragma unroll
-            for (int w = 0; w < K::kWarps; ++w) big = fmaxf(big, meet[w][0].x);
-            const int e = big > 0.f && big < INFINITY ? max(ilogbf(big), -120) : 0;
-            down = ldexpf(1.f, -e);
-            result = ldexpf(1.f, e);
+                for (int w = 0; w < K::kWarps; ++w) most = fmaxf(most, nt ? meet[w][head].y : meet[w][head].x);
+                return most > 0.f && most < INFINITY ? max(ilogbf(most), -120) : 0;
+            };
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int e = power(nt, lane / 4);
+                down[nt] = ldexpf(1.f, -e);
+                ups[nt * 8 + lane / 4] = ldexpf(1.f, e);  // every thread of the head writes the same
+            }
         }
 #pragma unroll
         for (int x = 0; x < kAsk; ++x)
@@ -654,9 +667,9 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     asked[x][nt][y] ^= flip;
-                    if constexpr (k8 && !std::is_same<T, __half>::value) {
+                    if constexpr (kOwnPower) {
                         const float2 f = elem::pair_to_f32<T>(asked[x][nt][y]);
-                        asked[x][nt][y] = elem::pair_from_f32<__half>(f.x * down, f.y * down);
+                        asked[x][nt][y] = elem::pair_from_f32<__half>(f.x * down[nt], f.y * down[nt]);
                     }
                 }
                 if (warp * kAsk + x < kSteps)
@@ -664,7 +677,6 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
                         make_uint2(asked[x][nt][0], asked[x][nt][1]);
             }
         __syncthreads();
-        return result;
     };
     auto queries = [&](int ks, uint32_t (&q)[NT][2]) {
         const uint32_t *at = q_area + (ks * 32 + lane) * (2 * NT);
@@ -707,13 +719,20 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
             l[nt][0] = l[nt][1] = 0.f;
             if constexpr (!kTwo) rounded[nt][0] = rounded[nt][1] = 0.f;
         }
-        const float q_scale = put_queries();
-        // Scores in units of log2 are the products times `unit`.
+        put_queries();
+        // Scores in units of log2 are the products times unit().
         constexpr float kLog2e = 1.4426950408889634f;
         const float to_score =
-            (p.scale != 0.f ? fabsf(p.scale) : 1.f) * q_scale * (k8 && p.c.k_scale ? p.c.k_scale[segs[turn].kvh] : 1.f);
-        const float unit = p.softcap > 0.f ? 1.f : to_score * kLog2e;
-        const float slack = kSlack / unit;
+            (p.scale != 0.f ? fabsf(p.scale) : 1.f) * (k8 && p.c.k_scale ? p.c.k_scale[segs[turn].kvh] : 1.f);
+        const float unit_all = p.softcap > 0.f ? 1.f : to_score * kLog2e, slack_all = kSlack / unit_all;
+        float units[kOwnPower ? NT : 1][2];
+        if constexpr (kOwnPower)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) units[nt][x] = p.softcap > 0.f ? 1.f : unit_all * ups[nt * 8 + 2 * (lane % 4) + x];
+        auto unit = [&](int nt, int x) { return kOwnPower ? units[kOwnPower ? nt : 0][x] : unit_all; };
+        auto slack = [&](int nt, int x) { return kOwnPower ? kSlack / unit(nt, x) : slack_all; };
 
         const int count = segs[turn].count;
 #pragma unroll 1
@@ -759,7 +778,8 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) s[mt][nt][x] = out * tanhf(s[mt][nt][x] * in);
+                        for (int x = 0; x < 4; ++x)
+                            s[mt][nt][x] = out * tanhf(s[mt][nt][x] * (kOwnPower ? in * ups[nt * 8 + 2 * (lane % 4) + (x & 1)] : in));
             }
             if (mask != K::kAll) {
 #pragma unroll
@@ -794,9 +814,9 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
                         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
                         y = fmaxf(y, m[nt][x]);
-                        keep[x] = exp2_approx((m[nt][x] - y) * unit);
+                        keep[x] = exp2_approx((m[nt][x] - y) * unit(nt, x));
                         m[nt][x] = y;
-                        limit[nt][x] = y + slack;
+                        limit[nt][x] = y + slack(nt, x);
                         l[nt][x] *= keep[x];
                         if constexpr (!kTwo) rounded[nt][x] *= keep[x];
                     }
@@ -814,7 +834,7 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
                     float w[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x)  // differences first: however large both are, the reference's weight is 2^kUp
-                        w[x] = exp2_approx(fmaf(s[mt][nt][x] - m[nt][x & 1], unit, kUp));
+                        w[x] = exp2_approx(fmaf(s[mt][nt][x] - m[nt][x & 1], unit(nt, x & 1), kUp));
                     l[nt][0] += w[0] + w[2], l[nt][1] += w[1] + w[3];
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
@@ -891,7 +911,7 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
                     return y + __shfl_xor_sync(0xffffffffu, y, 16);
                 };
                 const float sum = over_rows(l[nt][x]);
-                if (lane < 4) meet[warp][row] = make_float2(m[nt][x] * unit, sum);
+                if (lane < 4) meet[warp][row] = make_float2(m[nt][x] * unit(nt, x), sum);
                 if constexpr (!kTwo) {  // from here on outputs belong to the sum of the weights as they were
                     const float of = over_rows(rounded[nt][x]), f = of > 0.f ? sum / of : 1.f;
 #pragma unroll
