@@ -176,6 +176,16 @@ def test_attention_infinite_and_nan_queries_stay_in_their_head_on_8_bit_keys(w4)
     assert torch.equal(out, clean)
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("k_scale,scale,cap", [(0.0, 0.125, 0.0), (1e-10, 1e-40, 0.0), (0.0, 0.125, 5.0)])
+def test_attention_scores_that_vanish_are_all_alike(w4, dtype, k_scale, scale, cap):
+    # Keys that stand for 0 (or next to it): the mean of the visible values, in a slice that is not full too.
+    lens, page = [21, 1, 300], 16
+    q, cache, pools, scales, table = build(w4, lens, 8, 2, 64, dtype, E4M3, page, "tokens", 8)
+    scales[0].fill_(k_scale)
+    check_attention(w4, q, cache, pools, scales, table, lens, page, scale=scale, cap=cap)
+
+
 # ------------------------------------------------------------------ streams of the caller's
 def on_side_stream(call, as_number):
     """call(stream) while the current stream is busy and its free memory holds ones; the result."""

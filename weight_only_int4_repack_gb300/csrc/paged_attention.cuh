@@ -724,13 +724,16 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
         constexpr float kLog2e = 1.4426950408889634f;
         const float to_score =
             (p.scale != 0.f ? fabsf(p.scale) : 1.f) * (k8 && p.c.k_scale ? p.c.k_scale[segs[turn].kvh] : 1.f);
-        const float unit_all = p.softcap > 0.f ? 1.f : to_score * kLog2e, slack_all = kSlack / unit_all;
+        // A unit that is no normal number would be 0 times minus infinity where nothing is visible; the smallest one
+        // makes the same of finite scores: all alike.
+        auto normal = [](float x) { return x < 1.2e-38f ? 1.2e-38f : x; };
+        const float unit_all = p.softcap > 0.f ? 1.f : normal(to_score * kLog2e), slack_all = kSlack / unit_all;
         float units[kOwnPower ? NT : 1][2];
         if constexpr (kOwnPower)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int x = 0; x < 2; ++x) units[nt][x] = p.softcap > 0.f ? 1.f : unit_all * ups[nt * 8 + 2 * (lane % 4) + x];
+                for (int x = 0; x < 2; ++x) units[nt][x] = p.softcap > 0.f ? 1.f : normal(to_score * kLog2e * ups[nt * 8 + 2 * (lane % 4) + x]);
         auto unit = [&](int nt, int x) { return kOwnPower ? units[kOwnPower ? nt : 0][x] : unit_all; };
         auto slack = [&](int nt, int x) { return kOwnPower ? kSlack / unit(nt, x) : slack_all; };
 
