@@ -186,6 +186,44 @@ def test_attention_scores_that_vanish_are_all_alike(w4, dtype, k_scale, scale, c
     check_attention(w4, q, cache, pools, scales, table, lens, page, scale=scale, cap=cap)
 
 
+# ------------------------------------------------------------------ rope_append
+@pytest.mark.parametrize("rot", [16, 12])
+def test_rope_append_divides_by_the_scale(w4, rot):
+    # x / scale lies exactly between two e4m3 values: the even one is stored. A product with the rounded reciprocal
+    # leaves the border, one way or the other, in 38 of these 256.
+    odd = torch.arange(3, 67, 2, dtype=torch.float32)                     # one scale for each head
+    cache, pools, scales = make_cache(w4, 1, 16, odd.numel(), 16, E4M3, 1)
+    ties = torch.arange(17, 33, 2, dtype=torch.float32).repeat(2) * torch.tensor([1.0, -1.0]).repeat_interleave(8)
+    for s in scales:
+        s.copy_(odd * 2.0**-8)
+    kv = (odd[:, None] * 2.0**-8 * ties).to(F16)[None].cuda()
+    assert torch.equal(kv.float().cpu()[0], odd[:, None] * 2.0**-8 * ties)
+    q = torch.zeros(1, 32, 16, dtype=F16, device="cuda")
+    w4.w4a16_rope_append(q, kv, kv, i32([0]), torch.ones(rot // 2, device="cuda"), cache, torch.tensor([3], device="cuda"))
+    want = f64(ties.to(E4M3))[None].repeat(odd.numel(), 0)
+    assert set(np.abs(want[0])) == {16, 20, 24, 28, 32}
+    for pool in pools:
+        np.testing.assert_array_equal(f64(pool)[0, 3], want)
+
+
+@pytest.mark.parametrize("rot", [16, 12])
+def test_rope_append_stores_the_rounded_quotient_of_every_value(w4, rot):
+    # Every finite fp16 value as a value of the cache, over scales of different mantissas and sizes.
+    x = torch.arange(2**16, dtype=torch.int32).to(torch.int16).view(F16)
+    x = x[torch.isfinite(x)]
+    rows = x.numel() // 16
+    scale = torch.tensor([1.0, 1 / 3, 0.0213, 2 - 2.0**-23, 1 + 2.0**-23, 7.7e4, 3.1e-7, 2.0**-60 * 1.7])
+    cache, pools, scales = make_cache(w4, -(-rows // 16), 16, scale.numel(), 16, E4M3, 1)
+    for s in scales:
+        s.copy_(scale)
+    kv = x.view(rows, 1, 16).expand(rows, scale.numel(), 16).contiguous().cuda()
+    q = torch.zeros(rows, 8, 16, dtype=F16, device="cuda")
+    w4.w4a16_rope_append(q, kv, kv, i32(np.zeros(rows)), torch.ones(rot // 2, device="cuda"), cache, torch.arange(rows, device="cuda"))
+    want = f64((kv.float().cpu() / scale[:, None]).clamp(-448, 448).to(E4M3))
+    for pool in pools:
+        np.testing.assert_array_equal(f64(pool).reshape(-1, scale.numel(), 16)[:rows], want)
+
+
 # ------------------------------------------------------------------ streams of the caller's
 def on_side_stream(call, as_number):
     """call(stream) while the current stream is busy and its free memory holds ones; the result."""

@@ -58,6 +58,15 @@ __device__ __forceinline__ float2 rotation(float inv_freq, int pos, float mscale
     return make_float2(c1 * mscale, s1 * mscale);
 }
 
+// x / scale for an 8-bit cache, from the rounded reciprocal: the product's remainder is exact as a fused product, and
+// corrects it to the rounded quotient (Markstein, IBM Journal of Research and Development 34, 1990), as long as it
+// does not underflow (scales from 2^-60 on). Quotients beyond the type's range, infinite ones among them, saturate
+// as they are. A division in its place took 59.1 us for the 16384 rows below, the product alone 53.0.
+__device__ __forceinline__ float quotient(float x, float scale, float inverse) {
+    const float q = x * inverse;
+    return fabsf(q) < 1024.f ? fmaf(fmaf(-q, scale, x), inverse, q) : q;
+}
+
 // The row's place in the cache: false where its keys and values are not written.
 struct Place {
     long long page, token;
@@ -139,7 +148,7 @@ __global__ void __launch_bounds__(32 * kWideWarps, 2) rope_append_wide_kernel(co
         T *q_out = static_cast<T *>(p.q_out) + row0 * p.qo_row + head * p.qo_head + a_at;
         C *pool = v ? static_cast<C *>(p.c.v) + head * p.c.v_head + a_at : static_cast<C *>(p.c.k) + head * p.c.k_head + a_at;
         const float *scales = v ? p.c.v_scale : p.c.k_scale;
-        const float to_stored = !q && scales && in ? 1.0f / scales[head] : 1.0f;
+        const float scale = !q && scales && in ? scales[head] : 1.0f, inverse = 1.0f / scale;
 
         if (pass == warp) {  // the first loads are on their way
             for (int i = threadIdx.x; i < rows * half; i += blockDim.x) {
@@ -207,7 +216,7 @@ __global__ void __launch_bounds__(32 * kWideWarps, 2) rope_append_wide_kernel(co
                     } else if (k_at[r] >= 0) {
                         if (sizeof(C) == 1) {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) a[e] *= to_stored, b[e] *= to_stored;
+                            for (int e = 0; e < 8; ++e) a[e] = quotient(a[e], scale, inverse), b[e] = quotient(b[e], scale, inverse);
                         }
                         VC::store(pool + at[r], a);
                         if (two) VC::store(pool + at[r] + ab, b);
@@ -290,8 +299,9 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
                           : static_cast<C *>(p.c.k) + at.page * p.c.k_page + at.token * p.c.k_token + head * p.c.k_head;
             const float *scale = is_v ? p.c.v_scale : p.c.k_scale;
             if (scale) {
-                const float r = 1.0f / scale[head];
-                a[0] *= r, a[1] *= r, b[0] *= r, b[1] *= r;
+                const float s = scale[head], r = 1.0f / s;
+                a[0] = quotient(a[0], s, r), a[1] = quotient(a[1], s, r);
+                b[0] = quotient(b[0], s, r), b[1] = quotient(b[1], s, r);
             }
             VC::store(dst + lo, a);
             if (turn) VC::store(dst + hi, b);
