@@ -224,6 +224,25 @@ def test_rope_append_stores_the_rounded_quotient_of_every_value(w4, rot):
         np.testing.assert_array_equal(f64(pool).reshape(-1, scale.numel(), 16)[:rows], want)
 
 
+@pytest.mark.parametrize("rot", [32, 28])
+@pytest.mark.parametrize("pairs", [False, True])
+def test_rope_append_frequencies_that_are_no_numbers(w4, rot, pairs):
+    cache, pools, _ = make_cache(w4, 1, 16, 2, 64, F16, 1)
+    qkv = normal((3, 8, 64), F16, 2)
+    freq = w4.w4a16_rope_frequencies(rot, 1e4)
+    args = i32([0, 5, -7]), cache, torch.arange(3, device="cuda")
+    run = lambda f: w4.w4a16_rope_append(qkv[:, :4], qkv[:, 4:6], qkv[:, 6:], args[0], f.cuda(), *args[1:], interleaved=pairs)  # noqa: E731
+    clean = [run(freq)] + [p[0, :3].clone() for p in pools]
+    freq[2], freq[5], freq[6] = float("inf"), float("nan"), -float("inf")
+    got = [run(freq)] + [p[0, :3] for p in pools]
+    gone = [x for i in (2, 5, 6) for x in ((2 * i, 2 * i + 1) if pairs else (i, i + rot // 2))]
+    for x, y in zip(got[:2], clean[:2]):
+        assert torch.isnan(x[..., gone]).all()
+        rest = [i for i in range(64) if i not in gone]
+        assert torch.equal(x[..., rest], y[..., rest])
+    assert torch.equal(got[2], clean[2])
+
+
 # ------------------------------------------------------------------ streams of the caller's
 def on_side_stream(call, as_number):
     """call(stream) while the current stream is busy and its free memory holds ones; the result."""

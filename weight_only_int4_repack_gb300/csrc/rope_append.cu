@@ -43,6 +43,7 @@ constexpr int kMaxHalf = 128;  // rot_dim / 2 at most
 // cos and sin of frequency `inv_freq` at `pos`, times mscale.
 __device__ __forceinline__ float2 rotation(float inv_freq, int pos, float mscale) {
     const uint32_t bits = __float_as_uint(inv_freq), exponent = (bits >> 23) & 0xffu;
+    if (exponent == 0xffu) return make_float2(NAN, NAN);  // an infinite frequency has no angle, and NaN none either
     const unsigned long long mant = (bits & 0x7fffffu) | (exponent ? 0x800000u : 0u);
     const unsigned long long kTurn = 0x28BE60DB9391054Aull;  // 2^64 / (2 pi)
     // mant * kTurn * 2^(exponent - 150), modulo 2^64
