@@ -386,6 +386,11 @@ typedef struct {
  * lens_out may be lens and free_count_out may be free_count. Table entries of
  * ended requests stay as they are. batch <= 8192; free_count is clamped to
  * [0, pool], and pages given back beyond the pool's size are dropped.
+ * In the device error word: an ended request's length that is negative (it gives
+ * nothing back) or beyond its table row (it gives the row back), and a negative page
+ * number that is given back, handed out or gets a token of the step; it goes where a
+ * page would, and its tokens have slot -1. How many pages the cache has is not known
+ * here: numbers beyond it are named by the calls that use the slots and the table.
  */
 w4a16_status w4a16_kv_extend(const int32_t *lens, const int32_t *new_tokens, int32_t *table,
                              long long table_stride, int batch, int max_pages, int page_size,

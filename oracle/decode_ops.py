@@ -54,7 +54,8 @@ def kv_extend(lens, new_tokens, table, free_pages, free_count, page_size, n_slot
         for i in range(n):
             pos = lens[b] + i
             positions[start + i] = pos
-            slots[start + i] = int(table[b, pos // page_size]) * page_size + pos % page_size
+            page = int(table[b, pos // page_size])
+            slots[start + i] = page * page_size + pos % page_size if page >= 0 else -1
     return {"table": table, "free_pages": free, "free_count_out": count - taken, "lens_out": np.array(lens_out),
             "refused": np.array(refused), "slots": slots, "positions": positions}
 

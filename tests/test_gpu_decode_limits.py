@@ -243,6 +243,44 @@ def test_rope_append_frequencies_that_are_no_numbers(w4, rot, pairs):
     assert torch.equal(got[2], clean[2])
 
 
+# ------------------------------------------------------------------ kv_extend
+def extend(w4, lens, new, table, free, count, page=4, n=16, spacing=0):
+    t = [i32(x) for x in (lens, new, table, free, [count])]
+    slots = torch.full((n,), 77, dtype=torch.int64, device="cuda")
+    positions, refused = i32(np.full(n, 77)), i32(np.full(len(lens), 77))
+    w4.w4a16_kv_extend(*t, page, slots, positions, refused, spacing=spacing)
+    return t, slots.tolist(), positions.tolist(), refused.tolist()
+
+
+def test_kv_extend_names_pages_that_are_none(w4):
+    ok, bad = w4.W4A16_OK, w4.W4A16_ERR_INVALID_ARG
+    # A page of -1 in a running request's row, which its next token would go to.
+    t, slots, positions, refused = extend(w4, [5, 5], [1, 1], [[0, -1], [2, 3]], [9, 9], 0, n=4)
+    assert w4.w4a16_device_error() == bad
+    assert slots == [-1, 13, -1, -1] and positions[:2] == [5, 5] and refused == [0, 0]
+    # One that an ended request gives back, and that goes on to the next: both calls say so.
+    t, slots, _, _ = extend(w4, [6, 0], [-1, 0], [[1, -3], [0, 0]], [9, 9, 9], 1, n=4)
+    assert w4.w4a16_device_error() == bad and t[3].tolist() == [9, 1, -3] and t[4].tolist() == [3]
+    t, slots, _, refused = extend(w4, [0], [6], [[0, 0]], [9, 1, -3], 3, n=8)
+    assert w4.w4a16_device_error() == bad and refused == [0]
+    assert slots == [-1] * 4 + [4, 5, -1, -1] and t[2].tolist() == [[-3, 1]]
+    # Pages that no token of the step goes to are not looked at.
+    extend(w4, [5, 5], [1, 0], [[-1, 1], [-1, -1]], [-1, -1], 0, n=4)
+    assert w4.w4a16_device_error() == ok
+
+
+def test_kv_extend_names_lengths_of_ended_requests_out_of_range(w4):
+    ok, bad = w4.W4A16_OK, w4.W4A16_ERR_INVALID_ARG
+    for length, status in ((-1, bad), (9, bad), (8, ok), (0, ok), (2**31 - 1, bad)):
+        t, _, _, refused = extend(w4, [length, 3], [-1, 1], [[1, 2], [3, 4]], [9] * 4, 1)
+        assert w4.w4a16_device_error() == status
+        held = 0 if length <= 0 else 2
+        assert t[0].tolist() == [0, 4] and t[4].tolist() == [1 + held] and refused == [0, 0]
+    # Running requests' are answered by `refused` alone.
+    extend(w4, [-1, 9], [1, 1], [[1, 2], [3, 4]], [9] * 4, 1)
+    assert w4.w4a16_device_error() == ok
+
+
 # ------------------------------------------------------------------ streams of the caller's
 def on_side_stream(call, as_number):
     """call(stream) while the current stream is busy and its free memory holds ones; the result."""

@@ -30,6 +30,7 @@ struct ExtendParams {
     int batch, max_pages, page_size, pool, n_slots;
     unsigned int magic, shift;  // n / page_size = n * magic >> shift for 0 <= n < 2^31
     int spacing;  // slots from one request's first token to the next one's; 0: they follow each other
+    unsigned int *err;
     bool overlap;
 };
 
@@ -104,12 +105,17 @@ __global__ void __launch_bounds__(kMostThreads) kv_extend_kernel(const ExtendPar
                (add == 0 || (first_slot(b, at) + add <= p.n_slots && (!p.spacing || add <= p.spacing)));
     };
 
+    auto wrong = [&] { atomicExch(p.err, (unsigned int)W4A16_ERR_INVALID_ARG); };
+
     // Tokens and pages given back, in front of each request.
     long long tokens = 0, given = 0;
     for (int b = b0; b < b1; ++b) {
         const int len = p.lens[b], add = p.new_tokens[b];
         if (add > 0) tokens += add;
-        if (add < 0) given += min(pages(max(len, 0)), p.max_pages);
+        if (add < 0) {
+            given += min(pages(max(len, 0)), p.max_pages);
+            if (cta == 0 && (len < 0 || len > room)) wrong();
+        }
     }
     long long upto2[2] = {tokens, given}, all2[2];
     scan<2>(upto2, warp_sums, all2);
@@ -201,7 +207,10 @@ __global__ void __launch_bounds__(kMostThreads) kv_extend_kernel(const ExtendPar
     // Pages given back, behind those that are free.
     go_through(gwarp, first_given, (int)min(all_given, (long long)p.pool - count0),
                [&](int n, int b) { return p.table[(long long)b * p.table_stride + (n - first_given[b])]; },
-               [&](int n, int, int page) { p.free_pages[count0 + n] = page; });
+               [&](int n, int, int page) {
+                   p.free_pages[count0 + n] = page;
+                   if (page < 0) wrong();
+               });
     __syncwarp();
     ptx::cluster_sync();
 
@@ -217,6 +226,7 @@ __global__ void __launch_bounds__(kMostThreads) kv_extend_kernel(const ExtendPar
     go_through(gwarps - 1 - gwarp, first_page, (int)taken, [&](int n, int) { return __ldcg(p.free_pages + (top - n)); },
                [&](int n, int b, int page) {
                    p.table[(long long)b * p.table_stride + req[b].held + (n - first_page[b])] = page;
+                   if (page < 0) wrong();
                });
 
     // Every token's place.
@@ -233,7 +243,8 @@ __global__ void __launch_bounds__(kMostThreads) kv_extend_kernel(const ExtendPar
                },
                [&](int t, int b, int page) {
                    const int pos = position(t, b);
-                   p.slots[t] = pos < 0 ? -1ll : (long long)page * ps + (pos - by_page(pos) * p.page_size);
+                   p.slots[t] = pos < 0 || page < 0 ? -1ll : (long long)page * ps + (pos - by_page(pos) * p.page_size);
+                   if (page < 0) wrong();
                    p.positions[t] = max(pos, 0);
                });
 
@@ -270,7 +281,8 @@ extern "C" w4a16_status w4a16_kv_extend(const int32_t *lens, const int32_t *new_
     const unsigned int magic = (unsigned int)whole, shift = 31 + l;
     const ExtendParams p{lens,      new_tokens, free_count, table,        free_pages, lens_out,  free_count_out,
                          positions, refused,    slots,      table_stride, batch,      max_pages, page_size,
-                         pool,      n_slots,    magic,        shift,      spacing,   launch_overlap()};
+                         pool,      n_slots,    magic,        shift,      spacing,   device_error_ptr(), launch_overlap()};
+    if (!p.err) return W4A16_ERR_CUDA;
     cudaError_t e = ensure_max_dyn_smem((const void *)kv_extend_kernel, kMaxBatch * kRequestBytes);
     if (e != cudaSuccess) return from_cuda(e);
     // A step of running requests fits one CTA, and a small one is done sooner with fewer warps to wait for.
