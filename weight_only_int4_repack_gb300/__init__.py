@@ -208,6 +208,14 @@ def _new(shape, dtype, like, stream, make=torch.empty):
         return make(shape, dtype=dtype, device=like.device)
 
 
+def _expect_half(*tensors):
+    """The projections read and write contiguous float16 and are handed addresses only."""
+    for t in tensors:
+        if t is not None and (t.dtype is not torch.float16 or not t.is_contiguous()):
+            raise TypeError(f"activations, gamma and out: contiguous torch.float16 expected, got {t.dtype}"
+                            f"{'' if t.is_contiguous() else ' with gaps'}")
+
+
 def w4a16_repacked_bytes(N: int, K: int) -> int:
     return int(lib.w4a16_repacked_bytes(N, K))
 
@@ -265,7 +273,7 @@ def _scale_dtype(scales) -> int:
 def w4a16_gemm(A, q_rep, scales, zp, group: int, out=None, split_k: int = 0, workspace=None,
                stream=None):
     """Y[M, N] = A[M, K] . dequant(q_rep)^T (all CUDA tensors; zp may be None)."""
-    import torch
+    _expect_half(A, out)
     M, K = A.shape
     N = scales.shape[0]
     if out is None:
@@ -282,6 +290,7 @@ def w4a16_gemm_host_io(A_host, A_dev, q_rep, scales, zp, group: int, Y_dev, Y_ho
     """Copy A_host (pinned CPU fp16 [M, K]) into A_dev, run the GEMM into Y_dev and
     copy it into Y_host (pinned CPU fp16 [M, N]), all enqueued on the stream; no
     synchronisation (Y_host is valid once the stream has passed the call)."""
+    _expect_half(A_host, A_dev, Y_dev, Y_host)
     M, K = A_host.shape
     N = scales.shape[0]
     _check(lib.w4a16_gemm_host_io(_ptr(A_host), _ptr(A_dev), _ptr(q_rep), _ptr(scales), _scale_dtype(scales),
@@ -297,7 +306,7 @@ def w4a16_swiglu_workspace_bytes(M, N, K, group, fused) -> int:
 def w4a16_gemm_swiglu(A, qg_rep, sg, zg, qu_rep, su, zu, group: int, fused: bool = True,
                       out=None, workspace=None, stream=None):
     """Y = silu(A . Wg^T) * (A . Wu^T); fused or the unfused three-kernel chain."""
-    import torch
+    _expect_half(A, out)
     M, K = A.shape
     N = sg.shape[0]
     if out is None:
@@ -320,7 +329,7 @@ def w4a16_rmsnorm_workspace_bytes(M, N, K, group, mode) -> int:
 def w4a16_gemm_rmsnorm(A, gamma, eps: float, q_rep, scales, zp, group: int, out=None, split_k: int = 0,
                        workspace=None, stream=None):
     """Y = rmsnorm(A; gamma, eps) . dequant(q_rep)^T (normalised A staged in the workspace)."""
-    import torch
+    _expect_half(A, gamma, out)
     M, K = A.shape
     N = scales.shape[0]
     if out is None:
@@ -337,7 +346,7 @@ def w4a16_gemm_rmsnorm(A, gamma, eps: float, q_rep, scales, zp, group: int, out=
 def w4a16_gemm_swiglu_rmsnorm(A, gamma, eps: float, qg_rep, sg, zg, qu_rep, su, zu, group: int,
                               fused: bool = True, out=None, workspace=None, stream=None):
     """Y = silu(An . Wg^T) * (An . Wu^T), An = rmsnorm(A; gamma, eps)."""
-    import torch
+    _expect_half(A, gamma, out)
     M, K = A.shape
     N = sg.shape[0]
     if out is None:
@@ -360,7 +369,7 @@ def w4a16_gemm_swiglu_unfused_static(A, qg_rep, sg, zg, qu_rep, su, zu, group: i
                                      stream=None):
     """Unfused SwiGLU whose intermediates live in the library's fixed device
     array: for callers that cannot allocate device memory (see include/w4a16.h)."""
-    import torch
+    _expect_half(A, out)
     M, K = A.shape
     N = sg.shape[0]
     if out is None:
