@@ -281,6 +281,26 @@ def test_kv_extend_names_lengths_of_ended_requests_out_of_range(w4):
     assert w4.w4a16_device_error() == ok
 
 
+# ------------------------------------------------------------------ strides that step over nothing
+def test_strides_of_single_entries_say_nothing(w4):
+    # One request, one head, a cache of one page: strides between entries that there are none of may be anything.
+    odd = lambda t, *steps: torch.as_strided(t, t.shape, (*steps, 1))  # noqa: E731
+    pools = [normal((1, 16, 1, 64), F16, s) for s in (1, 2)]
+    cache, same = w4.KVCache(*[odd(p, 1027, 64, 13) for p in pools]), w4.KVCache(*pools)
+    q, k, v = (normal((1, 1, 64), F16, s) for s in (3, 4, 5))
+    args = i32([7]), torch.ones(32, device="cuda")
+    slot = torch.tensor([9], device="cuda")
+    out = torch.zeros(1, 1, 64, dtype=F16, device="cuda")
+    want = w4.w4a16_rope_append(q, k, v, *args, same, slot)
+    kept = [p.clone() for p in pools]
+    w4.w4a16_rope_append(odd(q, 77, 3), odd(k, 5, 9), odd(v, 1, 1), *args, cache, slot, out=odd(out, 65, 67))
+    assert torch.equal(out, want) and all(torch.equal(a, b) for a, b in zip(pools, kept))
+    table, lens = i32([[0]]), i32([10])
+    want = w4.w4a16_paged_attention(q, same, table, lens)
+    w4.w4a16_paged_attention(odd(q, 77, 3), cache, table, lens, out=odd(out, 65, 67))
+    assert torch.equal(out, want)
+
+
 # ------------------------------------------------------------------ streams of the caller's
 def on_side_stream(call, as_number):
     """call(stream) while the current stream is busy and its free memory holds ones; the result."""

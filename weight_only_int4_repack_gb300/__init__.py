@@ -100,10 +100,16 @@ class KVCache(ctypes.Structure):
                 _expect(s, torch.float32, "k_scale, v_scale")
                 if s.numel() != k.shape[2]:
                     raise ValueError("one scale for each kv head")
-        super().__init__(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), *k.stride()[:3],
-                         *v.stride()[:3], _TYPES[k.dtype], *k.shape)
+        super().__init__(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), *_steps(k), *_steps(v),
+                         _TYPES[k.dtype], *k.shape)
         self.tensors = (k, v, k_scale, v_scale)
         self.address = ctypes.addressof(self)
+
+
+def _steps(t):
+    """Strides of all dimensions but the last; 0 where there is one entry only, whose stride says nothing."""
+    n, step = t.shape, t.stride()
+    return [step[i] if n[i] > 1 else 0 for i in range(len(n) - 1)]
 
 
 def _expect(t, dtype, what):
@@ -445,11 +451,13 @@ def w4a16_rope_append(q, k, v, positions, inv_freq, cache, slots, interleaved: b
         _expect(bias, q.dtype, "bias")
         if bias.numel() != (heads + 2 * cache.kv_heads) * D:
             raise ValueError("bias: (heads + 2*kv_heads) * head_dim elements")
+    many, kv = rows > 1, cache.kv_heads > 1  # strides over one entry say nothing
     status = _rope(_pack_rope(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), _TYPES.get(q.dtype, -1), sq[0], sq[1], sk[0], sk[1], sv[0], sv[1],
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _TYPES.get(q.dtype, -1), sq[0] if many else 0,
+        sq[1] if heads > 1 else 0, sk[0] if many else 0, sk[1] if kv else 0, sv[0] if many else 0, sv[1] if kv else 0,
         0 if bias is None else bias.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.numel(),
-        interleaved, mscale, out.data_ptr(), so[0], so[1], cache.address, slots.data_ptr(), rows, heads,
-        _stream(stream)))
+        interleaved, mscale, out.data_ptr(), so[0] if many else 0, so[1] if heads > 1 else 0, cache.address,
+        slots.data_ptr(), rows, heads, _stream(stream)))
     if status:
         raise W4A16Error(status, "w4a16_rope_append")
     return out
@@ -484,10 +492,12 @@ def w4a16_paged_attention(q, cache, table, lens, scale: Optional[float] = None, 
         _expect(lse, torch.float32, "lse")
         if lse.numel() != batch * heads:
             raise ValueError("lse: [batch, heads]")
+    many = batch > 1  # strides over one entry say nothing
     status = _attention(_pack_attention(
-        q.data_ptr(), _TYPES.get(q.dtype, -1), sq[0], sq[1], cache.address, table.data_ptr(),
-        table.stride(0) if batch > 1 else max_pages, max_pages, lens.data_ptr(), batch, heads,
-        D ** -0.5 if scale is None else scale, window, softcap, out.data_ptr(), so[0], so[1],
+        q.data_ptr(), _TYPES.get(q.dtype, -1), sq[0] if many else 0, sq[1] if heads > 1 else 0, cache.address,
+        table.data_ptr(), table.stride(0) if many else max_pages, max_pages, lens.data_ptr(), batch, heads,
+        D ** -0.5 if scale is None else scale, window, softcap, out.data_ptr(), so[0] if many else 0,
+        so[1] if heads > 1 else 0,
         0 if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         _stream(stream)))
     if status:
