@@ -1,5 +1,9 @@
 """CPU checks of what the Python binding refuses before it hands addresses to the library, and of the argument blocks'
 layout."""
+import ctypes
+import os
+import re
+
 import pytest
 import torch
 
@@ -40,3 +44,32 @@ def test_rmsnorm_projections_take_fp16_gamma_only(w4):
     for call in projections(w4, good, good, torch.ones(256, dtype=torch.bfloat16))[2:4]:
         with pytest.raises(TypeError):
             call()
+
+
+# ------------------------------------------------------------------ the argument blocks against the header
+def header_struct(name):
+    """(field, type) of a struct of include/w4a16.h, in its order; "*" for every pointer."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "include", "w4a16.h")) as f:
+        text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+    body = re.search(r"typedef struct \{([^{}]*)\} %s;" % name, text).group(1)
+    fields = []
+    for line in filter(None, (part.strip() for part in body.split(";"))):
+        kind, names = re.match(r"((?:const )?(?:long long|\w+))\s+(.*)", line, flags=re.S).groups()
+        for n in names.split(","):
+            fields.append((n.strip().lstrip("*").strip(), "*" if "*" in n else kind))
+    return fields
+
+
+LETTERS = {"*": "P", "int": "i", "long long": "q", "float": "f", "size_t": "N"}
+
+
+def test_blocks_are_laid_out_as_in_the_header(w4):
+    assert len(w4._blocks) == 4
+    for name, letters in w4._blocks.items():
+        assert "".join(LETTERS[kind] for _, kind in header_struct(name + "_args")) == letters, name
+
+
+def test_cache_is_laid_out_as_in_the_header(w4):
+    kinds = {ctypes.c_void_p: "*", ctypes.c_longlong: "long long", ctypes.c_int: "int"}
+    assert [(n, kinds[t]) for n, t in w4.KVCache._fields_] == header_struct("w4a16_kv_cache")
