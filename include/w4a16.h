@@ -322,7 +322,8 @@ w4a16_status w4a16_device_error(void *stream);
  *     they have no rule to keep. With w4a16_set_launch_overlap(1) captured calls
  *     are too, and all but paged_attention let the work behind them begin early.
  *   - Sums, softmax statistics and norms are held in fp32; every output element
- *     is rounded once, to nearest even.
+ *     is rounded once, to nearest even. Softmax weights are matrix operands of 16
+ *     bits: w4a16_paged_attention says what that leaves of them.
  * ------------------------------------------------------------------------ */
 typedef enum {
     W4A16_TYPE_F16 = 0,
@@ -339,8 +340,9 @@ typedef enum {
  * described by the strides. Slot s is token s % page_size of page s / page_size.
  * Heads whose rows are no multiple of 128 bytes are read faster from pages laid out
  * heads first.
- *   type      F16, BF16 or E4M3. E4M3 stores e4m3(x / scale[h]) and stands for
- *             that times scale[h], with one positive fp32 scale for each kv head
+ *   type      F16, BF16 or E4M3. E4M3 stores e4m3(x / scale[h]), the quotient in
+ *             fp32 first, and stands for that times scale[h], with one positive fp32
+ *             scale for each kv head. Beyond 448 it saturates
  *   k_scale, v_scale  device fp32 [kv_heads], E4M3 only; NULL means 1
  * Rules: pages, page_size, kv_heads > 0; head_dim a multiple of 8 (E4M3: 16), at
  * most 256; pools 16-byte aligned; strides multiples of 16 bytes, below 2^31 elements.
@@ -408,6 +410,7 @@ w4a16_status w4a16_kv_extend(const int32_t *lens, const int32_t *new_tokens, int
  *            3 by bands: with t = context * f / (2 pi) turns in the context, f stays
  *              for t >= high, is divided by factor for t <= low, and goes linearly
  *              in t from one to the other between
+ * (The ramp of 3 is over turns, not over the pair's index i.)
  * rot_dim positive and even (at least 4 for scaling 2), base > 0, factor >= 1,
  * for scaling 3 context > 0 and high > low. Computed in fp64.
  */
@@ -434,7 +437,7 @@ w4a16_status w4a16_rope_frequencies(float *inv_freq, int rot_dim, double base, i
  *             rows with one slot leave either row's values there.
  * The product of position and frequency is reduced to a part of one turn in
  * 64-bit fixed point before it is rounded to fp32, so the angle is as exact at
- * far positions as at near ones.
+ * far positions as at near ones. A frequency that is infinite or NaN gives NaN.
  * rot_dim: 0 <= rot_dim <= head_dim, a multiple of 4. Pointers 4-byte aligned,
  * strides even; 16-byte alignment throughout and rot_dim % 16 == 0 are faster.
  * The cache's type is `type` or E4M3.
@@ -469,8 +472,16 @@ w4a16_status w4a16_rope_append(const void *q, const void *k, const void *v, w4a1
  *             all). Calls that can overlap on the GPU need one each.
  * The result does not depend on timing: how a request's tokens are divided among
  * the SMs follows from all lengths of the call, and the parts are joined in the
- * tokens' order. batch * (32-token tiles of a table row) * kv_heads * (blocks of 8
- * query heads) below 2^31.
+ * tokens' order.
+ * Scores, their maximum and the sums are fp32. Weights are rounded as operands: with a
+ * 16-bit cache to two of them (2^-21 of a weight in fp16, 2^-16 in bf16), with E4M3 to
+ * one of fp16 (2^-11), whose sum is also what the output is divided by. In fp16 they
+ * end at 2^-35 of the largest: smaller ones count in lse, not in out. bf16 queries of
+ * an E4M3 cache lose what is below 2^-25 of their head's largest. A visible infinity of
+ * a 16-bit cache gives that infinity (NaN beside one of the other sign), as long as its
+ * weight is not below 2^-35 of the largest.
+ * Refused as unsupported: batch * heads above 2^24; batch * (32-token tiles of a table
+ * row) * kv_heads * (blocks of 8 query heads) of 2^31 and more.
  */
 size_t w4a16_paged_attention_workspace_bytes(int batch, int heads, int kv_heads, int head_dim);
 w4a16_status w4a16_paged_attention(const void *q, w4a16_type type, long long q_row, long long q_head,

@@ -421,7 +421,8 @@ def w4a16_kv_extend(lens, new_tokens, table, free_pages, free_count, page_size: 
 
 def w4a16_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = 0, factor: float = 1.0,
                            context: float = 0.0, low: float = 1.0, high: float = 32.0):
-    """The rot_dim/2 inverse frequencies as a CPU float32 tensor; scaling 0..3 as in include/w4a16.h."""
+    """The rot_dim/2 inverse frequencies as a CPU float32 tensor; scaling 0..3 as in include/w4a16.h (3 goes from one
+    to the other linearly in turns within the context, from `low` to `high` of them)."""
     out = torch.empty(max(0, rot_dim) // 2, dtype=torch.float32)
     _check(lib.w4a16_rope_frequencies(out.data_ptr() or None, rot_dim, base, scaling, factor, context, low, high),
            "w4a16_rope_frequencies")

@@ -1,7 +1,7 @@
 // Attention of one new token of each request over its pages of the cache.
 //     s_j = scale * q . K_j (capped),  out = sum_j exp(s_j - m) V_j / sum_j exp(s_j - m)
-// Bound by HBM: each visible key and value is read once, for all query heads that
-// share it.
+// Bound by HBM: each visible key and value is read once for each block of 16 query
+// heads (8 where heads are wider than 128) that share it.
 //
 // Work. A tile is kWarps slices of 16 or 32 tokens of one request, kv head and block
 // of 8 * NT query heads. All tiles, request after request and head after head, form
@@ -22,11 +22,14 @@
 //
 // Measured (GB300, in a CUDA graph): 64 requests of 0 to 8191 tokens, 40 query and 8
 // kv heads of 128 in fp16 (1.16 GB) 173 to 180 us, 6.5 to 6.7 TB/s, the rate of a plain
-// copy; 121 requests of up to 16001 tokens, 32 and 2 heads, 8-bit cache (0.59 GB) 101
-// to 105 us, bound by instructions (about 520 for each 16 tokens of 16 heads, of which
-// 64 convert e4m3 to fp16). A call that is not long, or has few heads, pays about 4 us
-// until the first keys arrive (lengths, then the table, then keys) and 3 to 12 us for
-// joins: one request of 1000 tokens 7.8 us, two of up to 200003 with 2 kv heads 55 us.
+// copy; 121 requests of up to 16001 tokens, 32 and 2 heads, 8-bit cache (0.59 GB) 105
+// to 107 us with fp16 queries, 107 to 108 with bf16 ones, bound by instructions (about
+// 560 for each 16 tokens of 16 heads, of which 64 convert e4m3 to fp16). A call that is
+// not long, or has few heads, pays about 4 us until the first keys arrive (lengths, then
+// the table, then keys) and 3 to 12 us for joins: one request of 1000 tokens 7.8 us, two
+// of up to 200003 with 2 kv heads 56 us. 32 query heads on one key head are two blocks,
+// so everything is read twice: 128 requests of up to 8000 tokens (0.32 GB) 95 us, 32 of
+// them 32 us.
 // Rows of a head that are no multiple of 128 bytes, in a cache laid out tokens first,
 // share memory lines with other heads' that are read at another time: 52% of the copy
 // rate with 64 e4m3 elements, 73% with 96 of fp16; heads first 92% and 100%.
@@ -454,7 +457,7 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
     using M = typename K::M;
     constexpr float kUp = K::kUp;
     // Weights become one operand of 16 bits and, with 16-bit caches, a second one for what the first's rounding
-    // left: alone it would be as coarse as the output's own rounding. With 8-bit values, whose own rounding is
+    // left (together 22 bits of fp16, 16 of bf16): alone it would be as coarse as the output's own rounding. With 8-bit values, whose own rounding is
     // 2^-4, that second product is not spent (104 -> 117 us for 121 requests of 32 heads), but the weights are summed
     // as they are rounded too, so that the output is a mean of the values (104 -> 105 us; error against 64 bits
     // 2.1e-4 in place of 2.6e-4).
