@@ -457,10 +457,10 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
     using M = typename K::M;
     constexpr float kUp = K::kUp;
     // Weights become one operand of 16 bits and, with 16-bit caches, a second one for what the first's rounding
-    // left (together 22 bits of fp16, 16 of bf16): alone it would be as coarse as the output's own rounding. With 8-bit values, whose own rounding is
-    // 2^-4, that second product is not spent (104 -> 117 us for 121 requests of 32 heads), but the weights are summed
-    // as they are rounded too, so that the output is a mean of the values (104 -> 105 us; error against 64 bits
-    // 2.1e-4 in place of 2.6e-4).
+    // left (together 22 bits of fp16, 16 of bf16): alone it would be as coarse as the output's own rounding. With
+    // 8-bit values, whose own rounding is 2^-4, that second product is not spent (104 -> 117 us for 121 requests of
+    // 32 heads), but the weights are summed as they are rounded too, so that the output is a mean of the values
+    // (104 -> 105 us; error against 64 bits 2.1e-4 in place of 2.6e-4).
     constexpr bool kTwo = !k8;
     constexpr int kSteps = DT / 16, MT = K::kTok / 16;
     constexpr int kAsk = (kSteps + K::kWarps - 1) / K::kWarps;  // steps whose queries a warp brings
@@ -736,7 +736,8 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int x = 0; x < 2; ++x) units[nt][x] = p.softcap > 0.f ? 1.f : normal(to_score * kLog2e * ups[nt * 8 + 2 * (lane % 4) + x]);
+                for (int x = 0; x < 2; ++x)
+                    units[nt][x] = p.softcap > 0.f ? 1.f : normal(to_score * kLog2e * ups[nt * 8 + 2 * (lane % 4) + x]);
         auto unit = [&](int nt, int x) { return kOwnPower ? units[kOwnPower ? nt : 0][x] : unit_all; };
         auto slack = [&](int nt, int x) { return kOwnPower ? kSlack / unit(nt, x) : slack_all; };
 
