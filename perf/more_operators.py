@@ -233,7 +233,7 @@ def _prepare_attention(c, g, r):
         if c["op"] == "prompt":
             need = w4.w4a16_prompt_attention_workspace_bytes(rows, c["heads"], c["kv_heads"], c["dim"])
         else:
-            need = w4.w4a16_prefix_attention_workspace_bytes(rows, c["heads"], c["kv_heads"], c["dim"], c["prefixes"])
+            need = w4.w4a16_prefix_attention_workspace_bytes(rows, c["heads"], c["kv_heads"], c["dim"])
         s["workspace"] = torch.zeros(need, dtype=torch.uint8, device=DEVICE)
     return s
 
