@@ -597,6 +597,134 @@ w4a16_status w4a16_rope_append_block(const w4a16_rope_append_args *args);
 w4a16_status w4a16_paged_attention_block(const w4a16_paged_attention_args *args);
 w4a16_status w4a16_residual_rmsnorm_block(const w4a16_residual_rmsnorm_args *args);
 
+/*
+ * Attention of several new tokens of each request over its pages: prompts, parts of
+ * prompts, drafts to be checked. Request b has the rows starts[b] <= r < starts[b+1] of
+ * q, its newest tokens, whose keys and values are in the cache already. With P the length
+ * of its prefix (0 without one) its keys are the prefix's, then its own; row r of n is at
+ * position t = P + lens[b] - n + (r - starts[b]) and sees the keys j <= t, with a window
+ * the last `window` of these:
+ *     s_j = scale * q . K_j,  s_j = softcap * tanh(s_j / softcap) if softcap > 0,
+ *     out = sum_j exp(s_j - m) V_j / sum_j exp(s_j - m),  lse = m + log sum_j exp(s_j - m)
+ *   q, out    device, `type` (F16 or BF16), [rows][heads][head_dim], 16-byte aligned
+ *             rows and heads; out must not overlap q. Rows that belong to no request
+ *             stay as they are
+ *   cache, table, heads, scale, window, softcap  as for w4a16_paged_attention
+ *   starts    device int32 [batch + 1], never falling, from 0 to `rows` at most
+ *   lens      device int32 [batch]: the request's own tokens, the new ones counted
+ *   prefix_table  device int32 [prefixes][prefix_pages], rows prefix_stride apart:
+ *             pages of the same cache that requests share; read only
+ *   prefix_lens   device int32 [prefixes]
+ *   prefix_of device int32 [batch]: the request's prefix, negative: none. The three are
+ *             looked at if prefixes > 0 only
+ *   lse       device fp32 [rows][heads], or NULL
+ *   ws        device scratch of w4a16_prompt_attention_workspace_bytes(), 256-byte
+ *             aligned; nothing is kept in it from call to call. Calls that can overlap
+ *             on the GPU need one each
+ * Errors in the device error word: a pair of starts that falls or leaves [0, rows] (the
+ * request has no rows), a length below the request's rows or beyond its table row (it
+ * counts as its row), a prefix number of `prefixes` or more (no prefix) and a prefix length
+ * beyond its row; a page number out of range, whose tokens are left out. A row that sees
+ * no key gets out = 0 and lse = -inf.
+ * The result does not depend on timing. Scores, their maximum and the sums are fp32.
+ * Weights are rounded once to `type`, as operands (2^-11 of a weight in fp16, down to
+ * 2^-25 of the largest; 2^-8 in bf16), and outputs are divided by the sum of the rounded
+ * ones; lse is that of the unrounded ones. Values that a row does not see do not reach it,
+ * whatever they are.
+ * Refused as unsupported: rows * heads above 2^24, batch above 8192, prefixes above 2048,
+ * table rows of 2^31 tokens together.
+ */
+size_t w4a16_prompt_attention_workspace_bytes(int rows, int heads, int kv_heads, int head_dim);
+w4a16_status w4a16_prompt_attention(const void *q, w4a16_type type, long long q_row, long long q_head,
+                                    const w4a16_kv_cache *cache, const int32_t *table,
+                                    long long table_stride, int max_pages, const int32_t *starts,
+                                    const int32_t *lens, int rows, int batch, int heads,
+                                    const int32_t *prefix_table, long long prefix_stride,
+                                    int prefix_pages, const int32_t *prefix_lens,
+                                    const int32_t *prefix_of, int prefixes, float scale, int window,
+                                    float softcap, void *out, long long o_row, long long o_head,
+                                    float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Attention of one new token of each request, as w4a16_paged_attention, in a batch whose
+ * requests share prefixes: request b sees the tokens of prefix prefix_of[b] and then its
+ * own lens[b] (the new one counted). What the requests of a prefix see of it is computed
+ * for all of them together, so a prefix's keys and values are read once for up to 256
+ * query heads that share them, not once a request.
+ * Arguments as above, with one row of q and out for each request; prefixes > 0. A request
+ * without a token of its own (lens[b] <= 0) gets out = 0 and lse = -inf; one without a
+ * prefix is as in w4a16_paged_attention. A window counts over prefix and own tokens.
+ *   ws        of w4a16_prefix_attention_workspace_bytes(), 256-byte aligned. It has to be
+ *             zero before its first use; every call leaves it ready for the next of the
+ *             same heads, kv_heads and head_dim and no larger a batch
+ * Numerics: the prefix's part as in w4a16_prompt_attention, the own tokens' part as in
+ * w4a16_paged_attention; the two are joined in fp32 and rounded once.
+ */
+size_t w4a16_prefix_attention_workspace_bytes(int batch, int heads, int kv_heads, int head_dim);
+w4a16_status w4a16_prefix_attention(const void *q, w4a16_type type, long long q_row, long long q_head,
+                                    const w4a16_kv_cache *cache, const int32_t *table,
+                                    long long table_stride, int max_pages, const int32_t *lens,
+                                    int batch, int heads, const int32_t *prefix_table,
+                                    long long prefix_stride, int prefix_pages,
+                                    const int32_t *prefix_lens, const int32_t *prefix_of, int prefixes,
+                                    float scale, int window, float softcap, void *out, long long o_row,
+                                    long long o_head, float *lse, void *ws, size_t ws_bytes,
+                                    void *stream);
+
+/* The two calls above with their arguments in one block (see the blocks above). */
+typedef struct {
+    const void *q;
+    int type;
+    long long q_row, q_head;
+    const w4a16_kv_cache *cache;
+    const int32_t *table;
+    long long table_stride;
+    int max_pages;
+    const int32_t *starts, *lens;
+    int rows, batch, heads;
+    const int32_t *prefix_table;
+    long long prefix_stride;
+    int prefix_pages;
+    const int32_t *prefix_lens, *prefix_of;
+    int prefixes;
+    float scale;
+    int window;
+    float softcap;
+    void *out;
+    long long o_row, o_head;
+    float *lse;
+    void *ws;
+    size_t ws_bytes;
+    void *stream;
+} w4a16_prompt_attention_args;
+typedef struct {
+    const void *q;
+    int type;
+    long long q_row, q_head;
+    const w4a16_kv_cache *cache;
+    const int32_t *table;
+    long long table_stride;
+    int max_pages;
+    const int32_t *lens;
+    int batch, heads;
+    const int32_t *prefix_table;
+    long long prefix_stride;
+    int prefix_pages;
+    const int32_t *prefix_lens, *prefix_of;
+    int prefixes;
+    float scale;
+    int window;
+    float softcap;
+    void *out;
+    long long o_row, o_head;
+    float *lse;
+    void *ws;
+    size_t ws_bytes;
+    void *stream;
+} w4a16_prefix_attention_args;
+w4a16_status w4a16_prompt_attention_block(const w4a16_prompt_attention_args *args);
+w4a16_status w4a16_prefix_attention_block(const w4a16_prefix_attention_args *args);
+
 #ifdef __cplusplus
 }
 #endif

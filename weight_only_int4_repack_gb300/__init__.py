@@ -57,6 +57,8 @@ EXPORTS = (
     "w4a16_paged_attention_workspace_bytes", "w4a16_paged_attention", "w4a16_residual_rmsnorm",
     "w4a16_kv_extend_block", "w4a16_rope_append_block", "w4a16_paged_attention_block",
     "w4a16_residual_rmsnorm_block",
+    "w4a16_prompt_attention_workspace_bytes", "w4a16_prompt_attention", "w4a16_prompt_attention_block",
+    "w4a16_prefix_attention_workspace_bytes", "w4a16_prefix_attention", "w4a16_prefix_attention_block",
 )
 
 _vp, _ci, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
@@ -163,13 +165,28 @@ _blocks = {
     "w4a16_paged_attention": "PiqqPPqiPiififPqqPPNP",
     "w4a16_residual_rmsnorm": "PiqPiqPPqfPfPqPqiiP",
 }
-_sig.update({_name + "_block": (_ci, [ctypes.c_char_p]) for _name in _blocks})
+# Those of the attention of many rows.
+_wide_blocks = {
+    "w4a16_prompt_attention": "PiqqPPqiPPiiiPqiPPififPqqPPNP",
+    "w4a16_prefix_attention": "PiqqPPqiPiiPqiPPififPqqPPNP",
+}
+_sig.update({
+    "w4a16_prompt_attention_workspace_bytes": (_sz, [_ci, _ci, _ci, _ci]),
+    "w4a16_prompt_attention": (_ci, [_vp, _ci, _ll, _ll, _kv, _vp, _ll, _ci, _vp, _vp, _ci, _ci, _ci, _vp, _ll, _ci, _vp,
+                                     _vp, _ci, _cf, _ci, _cf, _vp, _ll, _ll, _vp, _vp, _sz, _vp]),
+    "w4a16_prefix_attention_workspace_bytes": (_sz, [_ci, _ci, _ci, _ci]),
+    "w4a16_prefix_attention": (_ci, [_vp, _ci, _ll, _ll, _kv, _vp, _ll, _ci, _vp, _ci, _ci, _vp, _ll, _ci, _vp, _vp, _ci,
+                                     _cf, _ci, _cf, _vp, _ll, _ll, _vp, _vp, _sz, _vp]),
+})
+_sig.update({_name + "_block": (_ci, [ctypes.c_char_p]) for _name in (*_blocks, *_wide_blocks)})
 for _name, (_res, _args) in _sig.items():
     _f = getattr(lib, _name)
     _f.restype = _res
     _f.argtypes = _args
 _pack_extend, _pack_rope, _pack_attention, _pack_norm = (struct.Struct(_blocks[_name]).pack for _name in _blocks)
 _extend, _rope, _attention, _norm = (getattr(lib, _name + "_block") for _name in _blocks)
+_pack_prompt, _pack_prefix = (struct.Struct(_wide_blocks[_name]).pack for _name in _wide_blocks)
+_prompt, _prefix = (getattr(lib, _name + "_block") for _name in _wide_blocks)
 
 
 class W4A16Error(RuntimeError):
@@ -503,6 +520,110 @@ def w4a16_paged_attention(q, cache, table, lens, scale: Optional[float] = None, 
         _stream(stream)))
     if status:
         raise W4A16Error(status, "w4a16_paged_attention")
+    return out
+
+
+def _prefixes(where, batch, prefix_table, prefix_lens, prefix_of):
+    """The arguments of shared prefixes as they go into a block: (table, stride, pages, lens, of, prefixes)."""
+    if prefix_table is None:
+        if prefix_lens is not None or prefix_of is not None:
+            raise ValueError(f"{where}: prefix_lens and prefix_of come with prefix_table")
+        return 0, 0, 0, 0, 0, 0
+    if prefix_lens is None or prefix_of is None or prefix_table.dim() != 2:
+        raise ValueError(f"{where}: prefix_table [prefixes, pages] comes with prefix_lens and prefix_of")
+    n, pages = prefix_table.shape
+    if not (prefix_table.dtype is prefix_lens.dtype is prefix_of.dtype is _int32):
+        raise TypeError(f"{where}: prefix_table, prefix_lens and prefix_of are int32")
+    if (prefix_lens.numel() != n or prefix_of.numel() != batch or not prefix_lens.is_contiguous()
+            or not prefix_of.is_contiguous() or (pages > 1 and prefix_table.stride(1) != 1)):
+        raise ValueError(f"{where}: prefix_table [prefixes, pages], prefix_lens [prefixes], prefix_of [batch]")
+    return (prefix_table.data_ptr(), prefix_table.stride(0) if n > 1 else pages, pages, prefix_lens.data_ptr(),
+            prefix_of.data_ptr(), n)
+
+
+def _attention_tensors(where, q, cache, table, out, lse, *ints):
+    """What prompt and prefix attention expect alike of their tensors. Returns q's and out's strides."""
+    if q.dim() != 3 or table.dim() != 2 or out.shape != q.shape or q.shape[2] != cache.head_dim:
+        raise ValueError(f"{where}: q, out [rows, heads, D], D the cache's, table [batch, max_pages]")
+    if q.dtype is not out.dtype or table.dtype is not _int32:
+        raise TypeError(f"{where}: q and out have one type, table is int32")
+    sq, so = q.stride(), out.stride()
+    if sq[2] != 1 or so[2] != 1 or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"{where}: D and the table's rows are contiguous")
+    for t in ints:
+        _expect(t, _int32, f"{where}: starts, lens")
+    if lse is not None:
+        _expect(lse, _float32, "lse")
+        if lse.numel() != q.shape[0] * q.shape[1]:
+            raise ValueError("lse: [rows, heads]")
+    rows, heads = q.shape[0] > 1, q.shape[1] > 1  # strides over one entry say nothing
+    return sq[0] if rows else 0, sq[1] if heads else 0, so[0] if rows else 0, so[1] if heads else 0
+
+
+def w4a16_prompt_attention_workspace_bytes(rows: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib.w4a16_prompt_attention_workspace_bytes(rows, heads, kv_heads, head_dim))
+
+
+def w4a16_prompt_attention(q, cache, table, starts, lens, scale: Optional[float] = None, window: int = 0,
+                           softcap: float = 0.0, prefix_table=None, prefix_lens=None, prefix_of=None, out=None, lse=None,
+                           workspace=None, stream=None):
+    """Attention of several new tokens of each request, q [rows, heads, D]: request b's are the rows from starts[b] up
+    to starts[b + 1] (int32 [batch + 1]), the newest of its lens[b] tokens in the cache; each sees the keys up to its
+    own. With prefix_table (int32 [prefixes, pages]), prefix_lens and prefix_of (int32 [batch], negative: none) the
+    tokens of a shared prefix come in front of the request's own. Rows of no request are left as they are in `out` (and
+    as torch.empty gives them where it is made here). lse: float32 [rows, heads], written if given.
+    workspace: w4a16_prompt_attention_workspace_bytes() of uint8; made here if it is not given."""
+    if out is None:
+        out = _new(q.shape, q.dtype, q, stream)
+    q_row, q_head, o_row, o_head = _attention_tensors("w4a16_prompt_attention", q, cache, table, out, lse, starts, lens)
+    rows, heads, D = q.shape
+    batch, max_pages = table.shape
+    if starts.numel() != batch + 1 or lens.numel() != batch:
+        raise ValueError("w4a16_prompt_attention: starts [batch + 1], lens [batch]")
+    prefixes = _prefixes("w4a16_prompt_attention", batch, prefix_table, prefix_lens, prefix_of)
+    if workspace is None:
+        workspace = _new(w4a16_prompt_attention_workspace_bytes(rows, heads, cache.kv_heads, D), torch.uint8, q, stream)
+    status = _prompt(_pack_prompt(
+        q.data_ptr(), _TYPES.get(q.dtype, -1), q_row, q_head, cache.address, table.data_ptr(),
+        table.stride(0) if batch > 1 else max_pages, max_pages, starts.data_ptr(), lens.data_ptr(), rows, batch, heads,
+        *prefixes, D ** -0.5 if scale is None else scale, window, softcap, out.data_ptr(), o_row, o_head,
+        0 if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream(stream)))
+    if status:
+        raise W4A16Error(status, "w4a16_prompt_attention")
+    return out
+
+
+def w4a16_prefix_attention_workspace_bytes(batch: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib.w4a16_prefix_attention_workspace_bytes(batch, heads, kv_heads, head_dim))
+
+
+def w4a16_prefix_attention(q, cache, table, lens, prefix_table, prefix_lens, prefix_of, scale: Optional[float] = None,
+                           window: int = 0, softcap: float = 0.0, out=None, lse=None, workspace=None, stream=None):
+    """Attention of one new token of each request, q [batch, heads, D], as w4a16_paged_attention, where request b's own
+    tokens (table, lens) come behind those of prefix prefix_of[b] (int32 [batch], negative: none; prefix_table int32
+    [prefixes, pages], prefix_lens int32 [prefixes]). What is shared is computed once for all requests of a prefix.
+    workspace: w4a16_prefix_attention_workspace_bytes() of uint8, zeroed once before its first use and then kept for
+    further calls; made here if it is not given."""
+    if out is None:
+        out = _new(q.shape, q.dtype, q, stream)
+    q_row, q_head, o_row, o_head = _attention_tensors("w4a16_prefix_attention", q, cache, table, out, lse, lens)
+    batch, heads, D = q.shape
+    max_pages = table.shape[1]
+    if table.shape[0] != batch or lens.numel() != batch:
+        raise ValueError("w4a16_prefix_attention: table [batch, max_pages], lens [batch]")
+    prefixes = _prefixes("w4a16_prefix_attention", batch, prefix_table, prefix_lens, prefix_of)
+    if workspace is None:
+        workspace = _new(w4a16_prefix_attention_workspace_bytes(batch, heads, cache.kv_heads, D), torch.uint8, q, stream,
+                         torch.zeros)
+    status = _prefix(_pack_prefix(
+        q.data_ptr(), _TYPES.get(q.dtype, -1), q_row, q_head, cache.address, table.data_ptr(),
+        table.stride(0) if batch > 1 else max_pages, max_pages, lens.data_ptr(), batch, heads, *prefixes,
+        D ** -0.5 if scale is None else scale, window, softcap, out.data_ptr(), o_row, o_head,
+        0 if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream(stream)))
+    if status:
+        raise W4A16Error(status, "w4a16_prefix_attention")
     return out
 
 

@@ -11,6 +11,9 @@ unsigned int *device_error_ptr();
 // Whether calls are launched as programmatic dependents (w4a16_set_launch_overlap).
 bool launch_overlap();
 
+// Limit of a bounded wait (w4a16_set_wait_limit_ns).
+unsigned long long wait_limit_ns();
+
 // Whether an operator between the projections is launched as a programmatic dependent
 // of the work before it. These kernels wait for that work before they touch memory, so
 // all that overlaps is the launch: about 2 us less between two calls on a stream (a

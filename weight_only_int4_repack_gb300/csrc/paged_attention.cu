@@ -14,18 +14,11 @@ constexpr size_t kCounterBytes = 3 * attn::kMaxCtas * 4;
 
 }  // namespace
 
-extern "C" {
-
-size_t w4a16_paged_attention_workspace_bytes(int batch, int heads, int kv_heads, int head_dim) {
-    if (batch <= 0 || heads <= 0 || kv_heads <= 0 || head_dim <= 0 || heads % kv_heads) return 0;
-    return kCounterBytes + (size_t)sm_count() * attn::kMostPerSm * 2 * attn::kMaxPartial * 4;
-}
-
-w4a16_status w4a16_paged_attention(const void *q, w4a16_type type, long long q_row, long long q_head,
-                                   const w4a16_kv_cache *cache, const int32_t *table, long long table_stride,
-                                   int max_pages, const int32_t *lens, int batch, int heads, float scale, int window,
-                                   float softcap, void *out, long long o_row, long long o_head, float *lse, void *ws,
-                                   size_t ws_bytes, void *stream) {
+// Of a call without requests only the host's values are looked at.
+w4a16_status w4a16::attn::fill(Params &p, const void *q, w4a16_type type, long long q_row, long long q_head,
+                               const w4a16_kv_cache *cache, const int32_t *table, long long table_stride, int max_pages,
+                               const int32_t *lens, int batch, int heads, float scale, int window, float softcap, void *out,
+                               long long o_row, long long o_head, float *lse, void *ws, size_t ws_bytes) {
     w4a16_status st = check_cache(cache);
     if (st != W4A16_OK) return st;
     if (type != W4A16_TYPE_F16 && type != W4A16_TYPE_BF16) return W4A16_ERR_INVALID_ARG;
@@ -47,7 +40,6 @@ w4a16_status w4a16_paged_attention(const void *q, w4a16_type type, long long q_r
     if (!ws || !aligned(ws, 256) ||
         ws_bytes < w4a16_paged_attention_workspace_bytes(batch, heads, cache->kv_heads, cache->head_dim))
         return W4A16_ERR_WORKSPACE;
-    attn::Params p{};
     p.q = q, p.out = out;
     p.q_row = q_row, p.q_head = q_head, p.o_row = o_row, p.o_head = o_head, p.table_stride = table_stride;
     p.c = *cache;
@@ -59,6 +51,25 @@ w4a16_status w4a16_paged_attention(const void *q, w4a16_type type, long long q_r
     p.window = window, p.scale = scale, p.softcap = softcap;
     p.err = device_error_ptr();
     if (!p.err) return W4A16_ERR_CUDA;
+    return W4A16_OK;
+}
+
+extern "C" {
+
+size_t w4a16_paged_attention_workspace_bytes(int batch, int heads, int kv_heads, int head_dim) {
+    if (batch <= 0 || heads <= 0 || kv_heads <= 0 || head_dim <= 0 || heads % kv_heads) return 0;
+    return kCounterBytes + (size_t)sm_count() * attn::kMostPerSm * 2 * attn::kMaxPartial * 4;
+}
+
+w4a16_status w4a16_paged_attention(const void *q, w4a16_type type, long long q_row, long long q_head,
+                                   const w4a16_kv_cache *cache, const int32_t *table, long long table_stride,
+                                   int max_pages, const int32_t *lens, int batch, int heads, float scale, int window,
+                                   float softcap, void *out, long long o_row, long long o_head, float *lse, void *ws,
+                                   size_t ws_bytes, void *stream) {
+    attn::Params p{};
+    const w4a16_status st = attn::fill(p, q, type, q_row, q_head, cache, table, table_stride, max_pages, lens, batch, heads,
+                                       scale, window, softcap, out, o_row, o_head, lse, ws, ws_bytes);
+    if (st != W4A16_OK || batch == 0) return st;
     cudaStream_t s = (cudaStream_t)stream;
     return from_cuda(type == W4A16_TYPE_F16 ? attn::launch_f16(p, sm_count(), s) : attn::launch_bf16(p, sm_count(), s));
 }

@@ -56,6 +56,9 @@ struct Params {
     float *lse;
     unsigned int *counters;  // [3][kMaxCtas], zero between calls
     float *partial;          // [CTAs][2][kMaxPartial]
+    // Where another kernel joins the results with more tokens of the requests (prefix attention): outputs in fp32,
+    // [batch * heads][head_dim], and log2 of the sums of weights, in place of out and lse; nullptr otherwise.
+    float *raw, *raw_lse;
     int max_pages, batch, heads, group, head_blocks, window;
     int one_page;  // page_size is a multiple of 16
     unsigned int k_page, k_token, v_page, v_token;  // strides below 2^31
@@ -302,6 +305,12 @@ struct Ends {
         constexpr float kLn2 = 0.6931471805599453f;
         const bool any = j.l > 0.f || j.l != j.l;
         const float f = any ? v_scale / j.l : 0.f;
+        if (p.raw) {
+            const long long at = (long long)seg.b * p.heads + seg.h0 + row;
+            *reinterpret_cast<float4 *>(p.raw + at * p.c.head_dim + d) = make_float4(j.o.x * f, j.o.y * f, j.o.z * f, j.o.w * f);
+            if (d == 0) p.raw_lse[at] = any ? j.m + log2f(j.l) - K::kUp : -INFINITY;
+            return;
+        }
         T *out = static_cast<T *>(p.out) + seg.b * p.o_row + (seg.h0 + row) * p.o_head + d;
         *reinterpret_cast<uint2 *>(out) =
             make_uint2(elem::pair_from_f32<T>(j.o.x * f, j.o.y * f), elem::pair_from_f32<T>(j.o.z * f, j.o.w * f));
@@ -525,6 +534,10 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
         if (tid == 0 && (p.lens[b] < 0 || p.lens[b] > (long long)p.max_pages * p.c.page_size))
             atomicExch(p.err, (unsigned int)W4A16_ERR_INVALID_ARG);
         if (r.hi > r.lo) continue;
+        if (p.raw) {
+            for (int i = tid; i < p.heads; i += K::kThreads) p.raw_lse[(long long)b * p.heads + i] = -INFINITY;
+            continue;
+        }
         for (int i = tid; i < p.heads * D; i += K::kThreads)
             static_cast<T *>(p.out)[b * p.o_row + (i / D) * p.o_head + i % D] = T(0.f);
         if (p.lse)
@@ -997,6 +1010,12 @@ cudaError_t launch_dims(const Params &p, int sms, cudaStream_t s) {
     if (p.c.head_dim <= 128) return two ? launch<T, C, 128, 2>(p, sms, s) : launch<T, C, 128, 1>(p, sms, s);
     return launch<T, C, 256, 1>(p, sms, s);
 }
+
+// Checks a call's arguments as w4a16_paged_attention does, and fills `p` with them. Defined in paged_attention.cu.
+w4a16_status fill(Params &p, const void *q, w4a16_type type, long long q_row, long long q_head, const w4a16_kv_cache *cache,
+                  const int32_t *table, long long table_stride, int max_pages, const int32_t *lens, int batch, int heads,
+                  float scale, int window, float softcap, void *out, long long o_row, long long o_head, float *lse, void *ws,
+                  size_t ws_bytes);
 
 // Defined in paged_attention_f16.cu and paged_attention_bf16.cu.
 cudaError_t launch_f16(const Params &p, int sms, cudaStream_t s);

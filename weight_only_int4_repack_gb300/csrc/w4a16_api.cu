@@ -41,6 +41,8 @@ unsigned int *w4a16::device_error_ptr() {
 
 bool w4a16::launch_overlap() { return g_launch_overlap != 0; }
 
+unsigned long long w4a16::wait_limit_ns() { return g_wait_ns; }
+
 bool w4a16::as_dependent(cudaStream_t s) {
     if (g_launch_overlap) return true;
     cudaStreamCaptureStatus st;

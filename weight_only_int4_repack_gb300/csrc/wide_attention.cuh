@@ -1,0 +1,1200 @@
+// Attention of many query rows over the pages of a cache: several new tokens of each
+// request (prompt_attention.cu), or one new token of every request behind a shared
+// prefix (prefix_attention.cu).
+//     s_j = scale * q . K_j (capped),  out = sum_j exp(s_j - m) V_j / sum_j exp(s_j - m)
+//
+// Rows. What reads the same keys is a sequence: a request (its new tokens, each of which
+// sees the keys up to its own), or a prefix (the requests behind it, which all see all of
+// it). The rows of a sequence and kv head are its tokens times the heads of the group;
+// they are taken in tiles of kRows rows, whole tokens each, so that a key that has been
+// brought serves the heads of the group and up to kRows / group tokens.
+//
+// Work. A unit is a tile of rows against kKeys keys. The units of all tiles, kv head after
+// kv head, form one line that is cut into equal parts, one for each CTA (one on an SM).
+// What a CTA has of a tile is a segment; a tile that lies in several CTAs leaves its sums in
+// the workspace, and a second kernel joins them in the order of the keys. Results do not
+// depend on timing.
+//
+// A CTA. Four warps bring queries, keys and values with 16-byte copies, page by page, into
+// the layout of the 128-byte swizzle (any page size and order; e4m3 becomes the queries'
+// type on the way, which is exact). One thread issues the matrix products (tcgen05, both
+// operands of Q K^T in shared memory, the weights of P V in tensor memory). Two groups of
+// four warps have 128 rows each, a row to a thread: maximum, weights, sum, and at the end
+// the output. While the tensor cores work for one group the other has its softmax. Heads
+// wider than 128 leave tensor memory for one group.
+#pragma once
+
+#include <cmath>
+#include <type_traits>
+
+#include "decode_ops.h"
+#include "elem.cuh"
+#include "ptx.cuh"
+#include "tc5.cuh"
+
+namespace w4a16 {
+namespace wide {
+
+using elem::E4M3;
+
+constexpr int kMaxSeqs = 8192;      // requests of a call
+constexpr int kMaxPrefixes = 2048;  // prefixes of a call
+constexpr int kMaxCtas = 256;
+
+// What a CTA's last tile leaves for the kernel that joins (prompts): the parts lie with
+// the CTAs from this one on.
+struct Cut {
+    int parts, rows, q0, h0, kvh, heads, seq, first;
+};
+// Where a request's sums over its prefix are (prefixes): parts from CTA `first` on, in
+// row `row` of each; first < 0: whole, in its own row.
+struct Found {
+    int first, parts, row, pad;
+};
+
+struct Params {
+    const void *q;
+    void *out;
+    long long q_row, q_head, o_row, o_head;
+    w4a16_kv_cache c;
+    const int32_t *table, *lens, *starts;  // starts: nullptr where the sequences are prefixes
+    const int32_t *ptable, *plens, *pof;   // nullptr without prefixes
+    long long table_stride, ptable_stride;
+    int max_pages, pmax_pages, prefixes;
+    int rows, batch, heads, group, window;
+    float scale, softcap;
+    float *lse;
+    Cut *cuts;          // [CTAs]
+    Found *found;       // [kv heads * head blocks][batch]
+    float *slots;       // [2 * CTAs][kRows][kPitch]
+    float *whole;       // [batch * heads][kPitch]
+    const float *raw, *raw_lse;  // prefixes: the requests' own tokens, [batch * heads][head_dim] and log2 of the sums
+    int *odd;           // [CTAs]: whether a CTA has written something that is no finite number
+    int ctas;
+    unsigned int *err;
+    unsigned long long wait_ns;
+};
+
+// The reference that weights are taken relative to is moved when a score passes it by more
+// than kSlack powers of two. As fp16 operands weights are 2^11 at the reference, so that
+// they keep 11 bits down to 2^-25 of it; bf16 has the range of fp32.
+constexpr float kSlack = 4.f, kLowest = -3.402823466e38f, kLog2e = 1.4426950408889634f;
+
+template <typename T, typename C, int DT>
+struct Config {
+    static constexpr bool kB16 = std::is_same<T, __nv_bfloat16>::value;
+    static constexpr bool k8 = sizeof(C) == 1;
+    static constexpr float kUp = kB16 ? -kSlack : 11.f;
+    static constexpr int kDim = DT;                       // head_dim, rounded up
+    static constexpr int kTiles = DT > 128 ? 1 : 2;       // groups of 128 rows
+    static constexpr int kRows = 128 * kTiles;
+    static constexpr int kKeys = DT > 128 ? 64 : 128;     // of a unit
+    static constexpr int kStageBytes = kKeys * DT * 2;    // keys or values of a unit
+    static constexpr int kStages = DT == 64 ? 8 : 4;
+    static constexpr int kQBytes = 128 * DT * 2;          // queries of a group
+    static constexpr int kRing = kTiles * kQBytes;        // offset of the ring
+    static constexpr int kAfter = kRing + kStages * kStageBytes;
+    static constexpr int kPitch = DT + 8;                 // floats of a row of sums: outputs, then m, l, l as rounded
+    static constexpr int kSlot = kRows * kPitch;
+    // Tensor memory: a group's scores (its weights take their place) and outputs.
+    static constexpr int kO = DT > 128 ? 256 : 256, kOStep = DT > 128 ? 0 : 128, kSStep = 128;
+    static constexpr int kWarps = 4 * kTiles + 5, kThreads = 32 * kWarps;
+    static constexpr int kLoader = 4 * kTiles, kMma = kLoader + 4;  // first warps of the roles
+};
+
+constexpr int kQueue = 4;
+// A segment, as the loaders describe it to the other warps.
+struct Segment {
+    int rows;        // of the tile that are real
+    int q0;          // row of q of the tile's first token (requests)
+    int first;       // visible keys of the tile's first token; each further token sees one more (requests)
+    int total;       // keys of the sequence
+    int kvh, h0;     // kv head, first query head
+    int key0, count; // first key, units
+    int slot;        // where the sums go; -1: the tile is whole
+    int last;        // no segment follows
+};
+
+template <int kRows>
+struct Shared {
+    int counts[kMaxPrefixes], least[kMaxPrefixes];  // of each prefix: requests, shortest own length
+    int members[kQueue][kRows];                     // requests of a tile (prefixes)
+    uint32_t bad[8][4];                             // keys of a unit whose page is none
+    Segment segs[kQueue];
+    uint64_t full[8], empty[8], seg_full[kQueue], seg_empty[kQueue], s_full[2], p_full[2], o_full[2], q_full, q_empty, drain;
+    long long sums[32];
+    long long units;
+    int start_s, start_t, start_hd, tiles;
+    long long start_base;
+    uint32_t tmem;
+    int abort, odd;
+};
+
+// ------------------------------------------------------------------ sequences and tiles
+struct Seq {
+    int n;       // tokens (requests: new ones; prefixes: requests behind it)
+    int total;   // keys
+    int q0;      // first row of q (requests)
+    int own0;    // requests: tokens in front of the own ones
+    int pre;     // requests: the prefix, -1: none
+};
+__device__ __forceinline__ int clamp_len(int len, int pages, int page_size) {
+    const long long most = (long long)pages * page_size;
+    return (int)min((long long)max(len, 0), most);
+}
+// The prefix of request b, or -1; *none: the number was neither a prefix nor negative.
+__device__ __forceinline__ int prefix_of(const Params &p, int b, bool *none) {
+    if (!p.pof) return -1;
+    const int x = p.pof[b];
+    if (x >= p.prefixes) *none = true;
+    return x >= 0 && x < p.prefixes ? x : -1;
+}
+__device__ __forceinline__ Seq request(const Params &p, int b, bool report) {
+    Seq s;
+    const int from = p.starts[b], to = p.starts[b + 1], len = p.lens[b];
+    bool bad = from < 0 || to < from || to > p.rows;
+    s.n = bad ? 0 : to - from;
+    s.q0 = from;
+    const int own = clamp_len(len, p.max_pages, p.c.page_size);
+    bad |= own != len || own < s.n;
+    s.pre = prefix_of(p, b, &bad);
+    s.own0 = 0;
+    if (s.pre >= 0) {
+        s.own0 = clamp_len(p.plens[s.pre], p.pmax_pages, p.c.page_size);
+        bad |= s.own0 != p.plens[s.pre];
+    }
+    s.total = s.own0 + own;
+    if (bad && report) atomicExch(p.err, (unsigned int)W4A16_ERR_INVALID_ARG);
+    return s;
+}
+// Whether request b is one of a prefix's (has a prefix and a token of its own).
+__device__ __forceinline__ bool behind(const Params &p, int b, int prefix) {
+    return p.pof[b] == prefix && p.lens[b] > 0;
+}
+
+// A tile of a sequence: its tokens, the keys that any of them sees, its units.
+struct Tile {
+    int tok0, toks, first, lo, hi, key0, count;
+};
+template <typename K>
+__device__ __forceinline__ Tile tile_of(const Params &p, const Seq &s, int least, int tt, int t) {
+    Tile x;
+    x.tok0 = t * tt;
+    x.toks = min(tt, s.n - x.tok0);
+    if (p.starts) {
+        x.first = s.total - s.n + x.tok0 + 1;
+        x.hi = max(x.first + x.toks - 1, 0);
+        x.lo = p.window > 0 ? max(0, x.first - p.window) : 0;
+    } else {
+        x.first = 0;
+        x.hi = s.total;
+        x.lo = p.window > 0 ? (int)max(0ll, (long long)s.total + least - p.window) : 0;
+    }
+    x.key0 = 0, x.count = 1;
+    if (x.lo < x.hi) {
+        x.key0 = x.lo / K::kKeys * K::kKeys;
+        x.count = (x.hi - 1) / K::kKeys + 1 - x.lo / K::kKeys;
+    }
+    return x;
+}
+
+// Sum over the threads in front of this one, and over all.
+template <int kWarps>
+__device__ __forceinline__ long long scan(long long mine, long long *sums, long long *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    long long before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += sums[w];
+        all += sums[w];
+    }
+    *total = all;
+    return before + upto - mine;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real) {
+    const int n = real ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(ptx::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// 32 bytes, 32-byte aligned.
+__device__ __forceinline__ void store8(float *to, const float *x) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+                 "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+}
+
+// How a raw product becomes a score, in units of log2.
+struct Scores {
+    float unit;            // without a cap: score * log2(e) of a product
+    float in, cap;         // with one: 2 * log2(e) / softcap * scale, softcap * log2(e)
+    float slack;           // kSlack powers of two, as a difference of products
+    bool capped;
+    __device__ __forceinline__ Scores(const Params &p, float k_scale) {
+        // A scale of 0 or below is in the queries (none, or negated); a unit that is no normal number would be 0 times
+        // minus infinity where nothing is visible.
+        const float to_score = (p.scale != 0.f ? fabsf(p.scale) : 1.f) * k_scale;
+        unit = fmaxf(to_score * kLog2e, 1.2e-38f);
+        capped = p.softcap > 0.f;
+        in = capped ? 2.f * kLog2e * to_score / p.softcap : 0.f;
+        cap = p.softcap * kLog2e;
+        slack = kSlack / unit;
+    }
+    // cap * tanh(x): 1 - 2 / (1 + e^2x), off by a few 2^-24 of the cap.
+    __device__ __forceinline__ float squeezed(float s) const { return fmaf(rcp(1.f + ex2(s * in)), -2.f * cap, cap); }
+    // What a reference m is as a score.
+    __device__ __forceinline__ float of(float m) const { return capped ? squeezed(m) : m * unit; }
+};
+
+// ------------------------------------------------------------------ the kernel
+template <typename T, typename C, int DT>
+__global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(const __grid_constant__ Params p) {
+    using K = Config<T, C, DT>;
+    using Sh = Shared<K::kRows>;
+    constexpr int kTiles = K::kTiles, kKeys = K::kKeys, kStages = K::kStages;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    Sh &sh = *reinterpret_cast<Sh *>(smem + K::kAfter);
+    volatile int *abort_flag = &sh.abort;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int cta = blockIdx.x;
+    const int D = p.c.head_dim;
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) ptx::mbar_init(&sh.full[i], 4), ptx::mbar_init(&sh.empty[i], 1);
+        for (int i = 0; i < kQueue; ++i) ptx::mbar_init(&sh.seg_full[i], 1), ptx::mbar_init(&sh.seg_empty[i], 4 * kTiles + 1);
+        for (int i = 0; i < 2; ++i)
+            ptx::mbar_init(&sh.s_full[i], 1), ptx::mbar_init(&sh.p_full[i], 4), ptx::mbar_init(&sh.o_full[i], 1);
+        ptx::mbar_init(&sh.q_full, 4), ptx::mbar_init(&sh.q_empty, 1), ptx::mbar_init(&sh.drain, 1);
+        sh.abort = 0, sh.odd = 0, sh.start_s = -1;
+        ptx::mbar_init_fence();
+    }
+    if (warp == K::kMma) tc5::alloc(&sh.tmem, 512);
+    ptx::grid_dep_wait();
+
+    // ---------------------------------------------------------------- plan
+    const int gb = min(p.group, K::kRows), head_blocks = (p.group + gb - 1) / gb, tt = K::kRows / gb;
+    const int hds = p.c.kv_heads * head_blocks;
+    const int seqs = p.starts ? p.batch : p.prefixes;
+    int *plan_off = reinterpret_cast<int *>(smem), *plan_n = plan_off + seqs + 1, *plan_total = plan_n + seqs;
+    if (!p.starts) {
+        for (int i = tid; i < seqs; i += K::kThreads) sh.counts[i] = 0, sh.least[i] = 0x7fffffff;
+        __syncthreads();
+        for (int b = tid; b < p.batch; b += K::kThreads) {
+            bool bad = false;
+            const int x = prefix_of(p, b, &bad), len = p.lens[b], own = clamp_len(len, p.max_pages, p.c.page_size);
+            if (x >= 0 && len > 0) atomicAdd(&sh.counts[x], 1), atomicMin(&sh.least[x], own);
+            if (bad && cta == 0) atomicExch(p.err, (unsigned int)W4A16_ERR_INVALID_ARG);
+        }
+        __syncthreads();
+    }
+    auto seq_of = [&](int i, bool report) {
+        if (p.starts) return request(p, i, report);
+        Seq s{sh.counts[i], clamp_len(p.plens[i], p.pmax_pages, p.c.page_size), 0, 0, i};
+        if (report && s.total != p.plens[i]) atomicExch(p.err, (unsigned int)W4A16_ERR_INVALID_ARG);
+        return s;
+    };
+    {
+        const int per = (seqs + K::kThreads - 1) / K::kThreads, s0 = min(tid * per, seqs), s1 = min(s0 + per, seqs);
+        long long mine = 0, all = 0;
+        for (int i = s0; i < s1; ++i) {
+            const Seq s = seq_of(i, cta == 0);
+            plan_n[i] = s.n, plan_total[i] = s.total;
+            mine += (s.n + tt - 1) / tt;
+        }
+        long long at = scan<K::kWarps>(mine, sh.sums, &all);
+        for (int i = s0; i < s1; ++i) {
+            plan_off[i] = (int)at;
+            at += (plan_n[i] + tt - 1) / tt;
+        }
+        if (tid == 0) plan_off[seqs] = (int)all, sh.tiles = (int)all;
+    }
+    __syncthreads();
+    long long total_units = 0, t_begin = 0, t_end = 0;
+    int active;
+    {
+        const int tiles = sh.tiles;
+        const int per = (tiles + K::kThreads - 1) / K::kThreads, i0 = min(tid * per, tiles), i1 = min(i0 + per, tiles);
+        int s_first = 0;
+        if (i0 < i1) {  // the sequence of the thread's first tile: the last one that begins at or in front of it
+            int lo = 0, hi = seqs - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (plan_off[mid] <= i0) lo = mid;
+                else hi = mid - 1;
+            }
+            s_first = lo;
+        }
+        auto units_of = [&](int s, int i) {
+            const Seq q{plan_n[s], plan_total[s], 0, 0, 0};
+            return tile_of<K>(p, q, p.starts ? 0 : sh.least[s], tt, i - plan_off[s]).count;
+        };
+        long long mine = 0, per_hd = 0;
+        for (int i = i0, s = s_first; i < i1; ++i) {
+            while (i >= plan_off[s + 1]) ++s;
+            mine += units_of(s, i);
+        }
+        const long long before = scan<K::kWarps>(mine, sh.sums, &per_hd);
+        total_units = per_hd * hds;
+        active = (int)min((long long)gridDim.x, total_units);
+        if (cta < active) {
+            const long long each = total_units / active, over = total_units - each * active;
+            t_begin = each * cta + over * cta / active;
+            t_end = each * (cta + 1) + over * (cta + 1) / active;
+            const long long rem = t_begin % per_hd;
+            if (rem >= before && rem < before + mine) {
+                long long at = before;
+                for (int i = i0, s = s_first; i < i1; ++i) {
+                    while (i >= plan_off[s + 1]) ++s;
+                    const int n = units_of(s, i);
+                    if (rem < at + n) {
+                        sh.start_s = s, sh.start_t = i - plan_off[s], sh.start_hd = (int)(t_begin / per_hd);
+                        sh.start_base = t_begin - rem + at;
+                        break;
+                    }
+                    at += n;
+                }
+            }
+        }
+    }
+    tc5::fence_before();
+    __syncthreads();
+    tc5::fence_after();
+    const uint32_t tmem = sh.tmem;
+    const bool has_work = cta < active && sh.start_s >= 0;
+    const uint32_t q_base = ptx::smem_u32(smem), ring = q_base + K::kRing;
+    const int k_steps = (D + 15) / 16;
+
+    if (warp >= K::kLoader && warp < K::kMma) {
+        // ------------------------------------------------------------ loaders
+        const int w = warp - K::kLoader;
+        if (w == 0 && lane == 0 && p.cuts) p.cuts[cta].parts = 0;
+        bool ok = has_work;
+        int s = sh.start_s, t = sh.start_t, hd = sh.start_hd;
+        long long x = t_begin, base = sh.start_base;
+        int stage = 0, seg_n = 0, unit_n = 0;
+        uint32_t ring_phase = 1;  // of the empty barriers
+        // Copies on their way, oldest first: the barriers that wait for them.
+        constexpr int kLag = 2;
+        uint64_t *pend[kLag + 1];
+        int pending = 0;
+        auto signal = [&](uint64_t *bar) {
+            fence_async();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar);
+        };
+        auto drain = [&] {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < kLag + 1; ++i)
+                if (i < pending) signal(pend[i]);
+            pending = 0;
+        };
+        auto queue = [&](uint64_t *bar) {
+            asm volatile("cp.async.commit_group;" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < kLag + 1; ++i)
+                if (i == pending) pend[i] = bar;
+            if (++pending == kLag + 1) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
+                signal(pend[0]);
+#pragma unroll
+                for (int i = 0; i < kLag; ++i) pend[i] = pend[i + 1];
+                pending = kLag;
+            }
+        };
+        // Waits; what is on its way is signalled first, as others may need it to come to an end.
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            if (!__all_sync(0xffffffffu, mbar_test(bar, parity))) {
+                drain();
+                if (!__all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort_flag, p.err, p.wait_ns))) ok = false;
+            }
+            return ok;
+        };
+        while (ok && x < t_end) {
+            const Seq seq = seq_of(s, false);
+            const Tile tile = tile_of<K>(p, seq, p.starts ? 0 : sh.least[s], tt, t);
+            const int from = (int)(x - base), take = (int)min((long long)(tile.count - from), t_end - x);
+            const int kvh = hd / head_blocks, h0 = kvh * p.group + hd % head_blocks * gb;
+            const int heads_here = min(gb, (kvh + 1) * p.group - h0);
+            const bool begins = from == 0, ends = from + take == tile.count;
+            const int qi = seg_n % kQueue;
+            if (!wait(&sh.seg_empty[qi], (uint32_t)(seg_n / kQueue + 1) & 1u)) break;
+            int *members = sh.members[qi];
+            const int rows = tile.toks * gb;
+            if (!p.starts) {  // the requests of these ranks (every loader warp writes the same)
+                int rank = 0;
+                for (int b0 = 0; b0 < p.batch && rank < tile.tok0 + tile.toks; b0 += 32) {
+                    const int b = b0 + lane;
+                    const bool in = b < p.batch && behind(p, b, s);
+                    const uint32_t mask = __ballot_sync(0xffffffffu, in);
+                    const int r = rank + __popc(mask & ((1u << lane) - 1u)) - tile.tok0;
+                    if (in && r >= 0 && r < tile.toks) members[r] = b;
+                    rank += __popc(mask);
+                }
+                __syncwarp();
+            }
+            int parts = 1;
+            if (begins && !ends) parts = (int)(((base + tile.count) * active - 1) / total_units) - cta + 1;
+            if (w == 0) {
+                if (lane == 0) {
+                    Segment g;
+                    g.rows = rows, g.q0 = seq.q0 + tile.tok0, g.first = tile.first, g.total = seq.total;
+                    g.kvh = kvh, g.h0 = h0, g.key0 = tile.key0 + from * kKeys, g.count = take;
+                    g.slot = begins && ends ? -1 : begins ? 2 * cta + 1 : 2 * cta;
+                    g.last = x + take >= t_end;
+                    sh.segs[qi] = g;
+                    if (p.cuts && begins && !ends) p.cuts[cta] = Cut{parts, rows, g.q0, h0, kvh, heads_here, s, tile.first};
+                }
+                if (!p.starts && begins)
+                    for (int i = lane; i < tile.toks; i += 32)
+                        p.found[(long long)hd * p.batch + members[i]] = Found{ends ? -1 : cta, parts, i * gb, 0};
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&sh.seg_full[qi]);
+            }
+            // Queries, in the order of the rows.
+            if (!wait(&sh.q_empty, (uint32_t)(seg_n + 1) & 1u)) break;
+            {
+                constexpr int kChunks = DT / 8, kLanes = kChunks < 32 ? kChunks : 32, kAt = 32 / kLanes;
+                const int c = lane % kLanes;
+                for (int r0 = w * (K::kRows / 4); r0 < (w + 1) * (K::kRows / 4) && r0 < (rows + 127) / 128 * 128; r0 += 32) {
+                    const int r = r0 + lane, tk = r / gb, hh = r - tk * gb;
+                    const bool in = r < rows && hh < heads_here && p.scale != 0.f;
+                    const long long row = !in ? 0 : p.starts ? seq.q0 + tile.tok0 + tk : members[tk];
+                    const long long at = in ? row * p.q_row + (h0 + hh) * p.q_head : -1;
+#pragma unroll 4
+                    for (int i = 0; i < 32; i += kAt) {
+                        const int rr = r0 + i + lane / kLanes;
+                        const long long src = __shfl_sync(0xffffffffu, at, i + lane / kLanes);
+                        if (c * 8 < 16 * k_steps) {
+                            const bool real = src >= 0 && c * 8 < D;
+                            copy16(q_base + (rr >> 7) * K::kQBytes + (c >> 3) * 16384 + (rr & 127) * 128 + (((c & 7) ^ (rr & 7)) << 4),
+                                   static_cast<const T *>(p.q) + (real ? src + c * 8 : 0), real);
+                        }
+                    }
+                }
+                queue(&sh.q_full);
+            }
+            // Keys and values, unit after unit.
+            const int32_t *own_pages = p.starts ? p.table + (long long)s * p.table_stride : nullptr;
+            const int32_t *pre_pages = seq.pre >= 0 ? p.ptable + (long long)seq.pre * p.ptable_stride : nullptr;
+            const int own0 = p.starts ? seq.own0 : seq.total;  // keys of the prefix
+            constexpr int kMine = kKeys / 4;  // rows of a warp
+            const int key_end = tile.hi;
+            auto look_up = [&](int u, int &page, int &at, bool &in) {
+                const int j = tile.key0 + (from + u) * kKeys + w * kMine + lane % kMine;
+                in = j >= tile.lo && j < key_end;
+                page = -1, at = 0;
+                if (in) {
+                    const bool pre = j < own0;
+                    const unsigned int y = pre ? j : j - own0, n = y / (unsigned int)p.c.page_size;
+                    at = (int)(y - n * (unsigned int)p.c.page_size);
+                    page = __ldg((pre ? pre_pages : own_pages) + n);
+                }
+            };
+            int page, at;
+            bool in;
+            look_up(0, page, at, in);
+            for (int u = 0; u < take; ++u) {
+                const bool good = in && page >= 0 && page < p.c.pages;
+                const uint32_t bad = __ballot_sync(0xffffffffu, in && !good);
+                if (bad && in && !good) atomicExch(p.err, (unsigned int)W4A16_ERR_INVALID_ARG);
+                const uint32_t real = __ballot_sync(0xffffffffu, good);
+                const unsigned long long pg = good ? page : 0, tk = good ? at : 0;
+                const unsigned long long k_at = pg * (unsigned long long)p.c.k_page + tk * (unsigned long long)p.c.k_token;
+                const unsigned long long v_at = pg * (unsigned long long)p.c.v_page + tk * (unsigned long long)p.c.v_token;
+                if (u + 1 < take) look_up(u + 1, page, at, in);
+#pragma unroll
+                for (int side = 0; side < 2; ++side) {
+                    if (!wait(&sh.empty[stage], ring_phase)) break;
+                    if (side == 0 && lane == 0) {
+                        if (kMine == 32) sh.bad[unit_n & 7][w] = bad;
+                        else sh.bad[unit_n & 7][w] = bad & 0xffffu;
+                    }
+                    const C *pool = static_cast<const C *>(side ? p.c.v : p.c.k) + kvh * (side ? p.c.v_head : p.c.k_head);
+                    const unsigned long long off = side ? v_at : k_at;
+                    const uint32_t dst = ring + stage * K::kStageBytes;
+                    if constexpr (!K::k8) {
+                        constexpr int kChunks = DT / 8, kLanes = kChunks < 32 ? kChunks : 32, kAt = 32 / kLanes;
+                        const int c = lane % kLanes;
+#pragma unroll
+                        for (int i = 0; i < kMine; i += kAt) {
+                            const int r = i + lane / kLanes, row = w * kMine + r;
+                            const unsigned long long src = __shfl_sync(0xffffffffu, off, r);
+                            if (c * 8 < 16 * k_steps) {
+                                const bool there = ((real >> r) & 1u) && c * 8 < D;
+                                copy16(dst + (c >> 3) * (kKeys * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                                       pool + (there ? src + c * 8 : 0), there);
+                            }
+                        }
+                        queue(&sh.full[stage]);
+                    } else {
+                        constexpr int kChunks = DT / 16, kAt = 32 / kChunks, kSteps = kMine / kAt;
+                        const int c = lane % kChunks;
+                        uint4 y[kSteps];
+#pragma unroll
+                        for (int i = 0; i < kSteps; ++i) {
+                            const int r = i * kAt + lane / kChunks;
+                            const unsigned long long src = __shfl_sync(0xffffffffu, off, r);
+                            const bool there = ((real >> r) & 1u) && c * 16 < D;
+                            y[i] = there ? __ldg(reinterpret_cast<const uint4 *>(pool + src + c * 16)) : make_uint4(0, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int i = 0; i < kSteps; ++i) {
+                            const int row = w * kMine + i * kAt + lane / kChunks;
+                            uint32_t h[8];
+                            elem::e4m3x4_to_half2(y[i].x, h[0], h[1]);
+                            elem::e4m3x4_to_half2(y[i].y, h[2], h[3]);
+                            elem::e4m3x4_to_half2(y[i].z, h[4], h[5]);
+                            elem::e4m3x4_to_half2(y[i].w, h[6], h[7]);
+                            if constexpr (K::kB16)
+#pragma unroll
+                                for (int z = 0; z < 8; ++z) {
+                                    const float2 f = elem::pair_to_f32<__half>(h[z]);
+                                    h[z] = elem::pair_from_f32<__nv_bfloat16>(f.x, f.y);
+                                }
+                            const uint32_t to = dst + (c >> 2) * (kKeys * 128) + row * 128;
+                            const int c0 = (2 * c) & 7;
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((c0 ^ (row & 7)) << 4)), "r"(h[0]),
+                                         "r"(h[1]), "r"(h[2]), "r"(h[3])
+                                         : "memory");
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((c0 + 1) ^ (row & 7)) << 4)),
+                                         "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7])
+                                         : "memory");
+                        }
+                        drain();  // the queries
+                        signal(&sh.full[stage]);
+                    }
+                    if (++stage == kStages) stage = 0, ring_phase ^= 1u;
+                }
+                if (!ok) break;
+                ++unit_n;
+            }
+            if (!ok) break;
+            // The next tile.
+            x += take;
+            base = x;
+            ++seg_n;
+            if (x < t_end && ++t >= (seq.n + tt - 1) / tt) {
+                t = 0;
+                for (;;) {  // the next sequence with a row
+                    if (++s >= seqs) s = 0, ++hd;
+                    const int y = s + lane;
+                    const bool some = y < seqs && (p.starts ? request(p, y, false).n > 0 : sh.counts[y] > 0);
+                    const uint32_t mask = __ballot_sync(0xffffffffu, some);
+                    if (mask) {
+                        s += __ffs(mask) - 1;
+                        break;
+                    }
+                    s += 31;
+                }
+            }
+        }
+        drain();
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == K::kMma) {
+        // ------------------------------------------------------------ matrix products
+        if (lane == 0 && has_work) {
+            const uint32_t id_qk = tc5::idesc(K::kB16, kKeys, p.scale < 0.f, false);
+            const uint32_t id_pv = tc5::idesc(K::kB16, 16 * k_steps, false, true);
+            int stage = 0;
+            uint32_t phase = 0;
+            uint32_t p_phase[2] = {0u, 0u};
+            bool ok = true, last = false;
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                if (!ptx::mbar_wait(bar, parity, abort_flag, p.err, p.wait_ns)) ok = false;
+                return ok;
+            };
+            auto qk = [&](int x, int st) {
+                const uint64_t a = tc5::desc_sw128(q_base + x * K::kQBytes, 16, 1024);
+                const uint64_t b = tc5::desc_sw128(ring + st * K::kStageBytes, 16, 1024);
+                for (int ks = 0; ks < k_steps; ++ks)
+                    tc5::mma_ss(tmem + x * K::kSStep, a + (uint32_t)((ks >> 2) * (16384 >> 4) + (ks & 3) * 2),
+                                b + (uint32_t)((ks >> 2) * (kKeys * 128 >> 4) + (ks & 3) * 2), id_qk, ks > 0);
+                tc5::commit(&sh.s_full[x]);
+            };
+            auto pv = [&](int x, int st, bool more) {
+                const uint64_t b = tc5::desc_sw128(ring + st * K::kStageBytes, kKeys * 128, 1024);
+#pragma unroll
+                for (int ks = 0; ks < kKeys / 16; ++ks)
+                    tc5::mma_ts(tmem + K::kO + x * K::kOStep, tmem + x * K::kSStep + ks * 8, b + (uint32_t)(ks * (2048 >> 4)), id_pv,
+                                more || ks > 0);
+            };
+            for (int n = 0; ok && !last; ++n) {
+                const int qi = n % kQueue;
+                if (!wait(&sh.seg_full[qi], (uint32_t)(n / kQueue) & 1u)) break;
+                const int groups = kTiles == 1 || sh.segs[qi].rows <= 128 ? 1 : 2, count = sh.segs[qi].count;
+                last = sh.segs[qi].last;
+                ptx::mbar_arrive(&sh.seg_empty[qi]);
+                if (!wait(&sh.q_full, (uint32_t)n & 1u)) break;
+                auto next = [&](int &st) {  // the next tile of the ring
+                    st = stage;
+                    if (!wait(&sh.full[stage], phase)) return false;
+                    if (++stage == kStages) stage = 0, phase ^= 1u;
+                    return true;
+                };
+                int k_at, v_at;
+                if (!next(k_at)) break;
+                tc5::fence_after();
+                for (int x = 0; x < groups; ++x) qk(x, k_at);
+                tc5::commit(&sh.empty[k_at]);
+                if (count == 1) tc5::commit(&sh.q_empty);
+                for (int j = 0; j < count; ++j) {
+                    if (!next(v_at)) break;
+                    for (int x = 0; x < groups; ++x) {
+                        if (!wait(&sh.p_full[x], p_phase[x])) break;
+                        p_phase[x] ^= 1u;
+                        tc5::fence_after();
+                        pv(x, v_at, j > 0);
+                        if (x == groups - 1) tc5::commit(&sh.empty[v_at]);
+                        if (j == count - 1) {
+                            tc5::commit(&sh.o_full[x]);
+                        } else {
+                            if (x == 0 && !next(k_at)) break;
+                            tc5::fence_after();
+                            qk(x, k_at);
+                            if (x == groups - 1) {
+                                tc5::commit(&sh.empty[k_at]);
+                                if (j == count - 2) tc5::commit(&sh.q_empty);
+                            }
+                        }
+                    }
+                    if (!ok) break;
+                }
+            }
+            if (!ok) {  // what has been issued comes to an end before tensor memory is given back
+                tc5::commit(&sh.drain);
+                volatile int no_abort = 0;
+                ptx::mbar_wait(&sh.drain, 0u, &no_abort, nullptr, 200000000ull);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax and output
+        const int x = warp >> 2;                                   // group
+        const int row = x * 128 + (warp & 3) * 32 + lane;          // of the tile
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;  // tensor memory lanes of this warp
+        const uint32_t t_s = tmem + lanes + x * K::kSStep, t_o = tmem + lanes + K::kO + x * K::kOStep;
+        uint32_t s_phase = 0, o_phase = 0;
+        int unit_n = 0;
+        bool last = !has_work, ok = true, odd = false;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort_flag, p.err, p.wait_ns))) ok = false;
+            return ok;
+        };
+        for (int n = 0; ok && !last; ++n) {
+            const int qi = n % kQueue;
+            if (!wait(&sh.seg_full[qi], (uint32_t)(n / kQueue) & 1u)) break;
+            const Segment g = sh.segs[qi];
+            last = g.last;
+            const int tk = row / gb, hh = row - tk * gb, head = g.h0 + hh;
+            const bool in = row < g.rows && head < (g.kvh + 1) * p.group;
+            const bool some = x * 128 + (warp & 3) * 32 < g.rows;  // the warp has a row
+            int b = 0, lo = 0, hi = 0;
+            if (in) {
+                if (p.starts) {
+                    b = g.q0 + tk;
+                    hi = max(g.first + tk, 0);
+                    lo = p.window > 0 ? max(0, hi - p.window) : 0;
+                } else {
+                    b = sh.members[qi][tk];
+                    hi = g.total;
+                    if (p.window > 0)
+                        lo = (int)max(0ll, (long long)hi + clamp_len(p.lens[b], p.max_pages, p.c.page_size) - p.window);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sh.seg_empty[qi]);
+            if (x * 128 >= g.rows) {  // nothing for this group
+                unit_n += g.count;
+                continue;
+            }
+            const float k_scale = K::k8 && p.c.k_scale ? p.c.k_scale[g.kvh] : 1.f;
+            const Scores sc(p, k_scale);
+            float m = kLowest, limit = kLowest, m_score = 0.f, l = 0.f, lr = 0.f;
+            for (int j = 0; j < g.count; ++j, ++unit_n) {
+                if (!wait(&sh.s_full[x], s_phase)) break;
+                s_phase ^= 1u;
+                tc5::fence_after();
+                if (some) {
+                    const int key0 = g.key0 + j * kKeys;
+                    uint32_t bad[kKeys / 32];
+#pragma unroll
+                    for (int i = 0; i < kKeys / 32; ++i)
+                        bad[i] = kKeys == 128 ? sh.bad[unit_n & 7][i] : sh.bad[unit_n & 7][2 * i] | (sh.bad[unit_n & 7][2 * i + 1] << 16);
+                    uint32_t any_bad = 0;
+#pragma unroll
+                    for (int i = 0; i < kKeys / 32; ++i) any_bad |= bad[i];
+                    const bool masked = __any_sync(0xffffffffu, lo > key0 || hi < key0 + kKeys) || any_bad;
+                    const unsigned int rel = (unsigned int)(key0 - lo), span = (unsigned int)max(hi - lo, 0);
+                    auto hide = [&](float (&f)[32], int c) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (rel + (unsigned int)(c * 32 + i) >= span || ((bad[c] >> i) & 1u)) f[i] = -INFINITY;
+                    };
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < kKeys / 32; ++c) {
+                        uint32_t v[32];
+                        float f[32];
+                        tc5::ld32(t_s + c * 32, v);
+                        tc5::wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+                        if (masked) hide(f, c);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, f[i]);
+                    }
+                    if (__any_sync(0xffffffffu, mx > limit)) {
+                        const float y = fmaxf(m, mx), y_score = sc.of(y);
+                        const float keep = sc.capped ? ex2(m_score - y_score) : ex2((m - y) * sc.unit);
+                        if (j > 0) {
+                            for (int c = 0; c < (D + 31) / 32; ++c) {
+                                uint32_t v[32];
+                                tc5::ld32(t_o + c * 32, v);
+                                tc5::wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * keep);
+                                tc5::st32(t_o + c * 32, v);
+                            }
+                        }
+                        l *= keep, lr *= keep;
+                        m = y, m_score = y_score, limit = y + sc.slack;
+                    }
+                    const float shift = K::kUp + sc.cap - m_score;
+#pragma unroll
+                    for (int c = 0; c < kKeys / 32; ++c) {
+                        uint32_t v[32], h[16];
+                        float f[32];
+                        tc5::ld32(t_s + c * 32, v);
+                        tc5::wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+                        if (masked) hide(f, c);
+                        if (!sc.capped) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) f[i] = ex2(fmaf(f[i] - m, sc.unit, K::kUp));
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const float y = ex2(fmaf(rcp(1.f + ex2(f[i] * sc.in)), -2.f * sc.cap, shift));
+                                f[i] = f[i] == -INFINITY ? 0.f : y;
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            l += f[2 * i] + f[2 * i + 1];
+                            h[i] = elem::pair_from_f32<T>(f[2 * i], f[2 * i + 1]);
+                            const float2 r = elem::pair_to_f32<T>(h[i]);
+                            lr += r.x + r.y;
+                        }
+                        tc5::st16(t_s + c * 16, h);
+                    }
+                    tc5::wait_st();
+                }
+                tc5::fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&sh.p_full[x]);
+            }
+            if (!ok) break;
+            if (!wait(&sh.o_full[x], o_phase)) break;
+            o_phase ^= 1u;
+            tc5::fence_after();
+            if (!some) continue;
+            const float v_scale = K::k8 && p.c.v_scale ? p.c.v_scale[g.kvh] : 1.f;
+            const bool any = l > 0.f || l != l;
+            const bool direct = g.slot < 0 && p.starts;
+            const float f = !direct ? 1.f : any ? v_scale / lr : 0.f;
+            float *sums = nullptr;
+            if (!direct)
+                sums = g.slot >= 0 ? p.slots + (long long)g.slot * K::kSlot + row * K::kPitch
+                                   : p.whole + ((long long)b * p.heads + head) * K::kPitch;
+            T *out = static_cast<T *>(p.out) + (long long)b * p.o_row + head * p.o_head;
+            float check = 0.f;
+            for (int c = 0; c < (D + 31) / 32; ++c) {
+                uint32_t v[32];
+                float o[32];
+                tc5::ld32(t_o + c * 32, v);
+                tc5::wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = any ? __uint_as_float(v[i]) * f : 0.f;
+                if (direct) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        if (c * 32 + i < D) {
+#pragma unroll
+                            for (int z = 0; z < 8; ++z) check = fmaf(o[i + z], 0.f, check);
+                            if (in)
+                                *reinterpret_cast<uint4 *>(out + c * 32 + i) =
+                                    make_uint4(elem::pair_from_f32<T>(o[i], o[i + 1]), elem::pair_from_f32<T>(o[i + 2], o[i + 3]),
+                                               elem::pair_from_f32<T>(o[i + 4], o[i + 5]), elem::pair_from_f32<T>(o[i + 6], o[i + 7]));
+                        }
+                    }
+                } else if (in) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+                        if (c * 32 + i < D) store8(sums + c * 32 + i, o + i);
+                }
+            }
+            if (in) {
+                if (direct) {
+                    odd |= check != check;
+                    if (p.lse)
+                        p.lse[(long long)b * p.heads + head] = any ? (sc.of(m) + log2f(l) - K::kUp) / kLog2e : -INFINITY;
+                } else {
+                    *reinterpret_cast<float4 *>(sums + DT) = make_float4(any ? sc.of(m) : -INFINITY, l, lr, 0.f);
+                }
+            }
+        }
+        if (odd) sh.odd = 1;  // every thread writes the same
+    }
+    tc5::fence_before();
+    __syncthreads();
+    tc5::fence_after();
+    if (warp == K::kMma) tc5::dealloc(tmem, 512);
+    if (tid == 0) p.odd[cta] = sh.odd;
+}
+
+// ------------------------------------------------------------------ joins
+// Sums over some keys of a row: a lane holds the elements 4 * (lane + 32 i).
+template <int DT>
+struct Sums {
+    static constexpr int kEach = DT > 128 ? 2 : 1;
+    float m = -INFINITY, l = 0.f, lr = 0.f;
+    float4 o[kEach];
+};
+// Joins a row's parts, which lie with the CTAs from `first` on.
+template <typename K>
+__device__ __forceinline__ Sums<K::kDim> join_parts(const Params &p, int first, int parts, int row, int D) {
+    constexpr int DT = K::kDim;
+    Sums<DT> r;
+    const int lane = threadIdx.x & 31;
+    auto part = [&](int i) { return p.slots + (long long)(2 * (first + i) + (i == 0)) * K::kSlot + row * K::kPitch; };
+#pragma unroll
+    for (int e = 0; e < r.kEach; ++e) r.o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = lane; i < parts; i += 32) r.m = fmaxf(r.m, __ldcg(part(i) + DT));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) r.m = fmaxf(r.m, __shfl_xor_sync(0xffffffffu, r.m, o));
+    const float top = r.m == -INFINITY ? 0.f : r.m;
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+        float4 s = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        if (i0 + lane < parts) s = __ldcg(reinterpret_cast<const float4 *>(part(i0 + lane) + DT));
+        const float f = ex2(s.x - top);
+        r.l += f * s.y, r.lr += f * s.z;
+        const int here = min(32, parts - i0);
+#pragma unroll 8
+        for (int i = 0; i < here; ++i) {
+            const float g = __shfl_sync(0xffffffffu, f, i);
+            const float *from = part(i0 + i);
+#pragma unroll
+            for (int e = 0; e < r.kEach; ++e) {
+                const int d = 4 * (lane + 32 * e);
+                if (d < D) {
+                    const float4 y = __ldcg(reinterpret_cast<const float4 *>(from + d));
+                    r.o[e].x += g * y.x, r.o[e].y += g * y.y, r.o[e].z += g * y.z, r.o[e].w += g * y.w;
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        r.l += __shfl_xor_sync(0xffffffffu, r.l, o);
+        r.lr += __shfl_xor_sync(0xffffffffu, r.lr, o);
+    }
+    return r;
+}
+
+// One row (a warp) from its definition: what a weight of 0 times an infinity, or a value that
+// this row does not see but others of its tile do, has spoilt. Keys [lo, hi) of a prefix of
+// `own0` keys and the request's own; only the tokens with a weight are looked at.
+template <typename T, typename C, int DT>
+__device__ __noinline__ void one_row(const Params &p, const T *q, T *out, float *lse, int kvh, const int32_t *pre_pages,
+                                     const int32_t *own_pages, int own0, int lo, int hi) {
+    constexpr int kEach = (DT + 31) / 32;
+    const int lane = threadIdx.x & 31, D = p.c.head_dim;
+    const float k_scale = sizeof(C) == 1 && p.c.k_scale ? p.c.k_scale[kvh] : 1.f;
+    const float v_scale = sizeof(C) == 1 && p.c.v_scale ? p.c.v_scale[kvh] : 1.f;
+    const Scores sc(p, k_scale);
+    float qv[kEach], o[kEach], m = kLowest, m_score = 0.f, l = 0.f;
+    auto number = [](C x) {
+        if constexpr (sizeof(C) == 1) {
+            uint32_t a, b;
+            elem::e4m3x4_to_half2(x.bits, a, b);
+            return elem::pair_to_f32<__half>(a).x;
+        } else {
+            return (float)x;
+        }
+    };
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const int d = lane + 32 * e;
+        qv[e] = d < D && p.scale != 0.f ? (float)q[d] : 0.f;
+        if (p.scale < 0.f) qv[e] = -qv[e];
+        o[e] = 0.f;
+    }
+    for (int j = lo; j < hi; ++j) {
+        const bool pre = j < own0;
+        const unsigned int y = pre ? j : j - own0, n = y / (unsigned int)p.c.page_size;
+        const int page = (pre ? pre_pages : own_pages)[n];
+        if (page < 0 || page >= p.c.pages) continue;
+        const unsigned long long at = y - n * (unsigned int)p.c.page_size, pg = page;
+        const C *k = static_cast<const C *>(p.c.k) + pg * p.c.k_page + at * p.c.k_token + kvh * p.c.k_head;
+        const C *v = static_cast<const C *>(p.c.v) + pg * p.c.v_page + at * p.c.v_token + kvh * p.c.v_head;
+        float s = 0.f;
+        if (p.scale != 0.f)
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                const int d = lane + 32 * e;
+                if (d < D) s = fmaf(qv[e], number(k[d]), s);
+            }
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+        const float top = fmaxf(m, s);
+        if (top > m) {
+            const float top_score = sc.of(top);
+            const float keep = sc.capped ? ex2(m_score - top_score) : ex2((m - top) * sc.unit);
+            const bool none = l == 0.f;
+            l = none ? 0.f : l * keep;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) o[e] = none || keep == 0.f ? 0.f : o[e] * keep;
+            m = top, m_score = top_score;
+        }
+        const float w = sc.capped ? ex2(sc.of(s) - m_score) : ex2((s - m) * sc.unit);
+        l += w;
+        if (w != 0.f)
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                const int d = lane + 32 * e;
+                if (d < D) o[e] = fmaf(w, number(v[d]), o[e]);
+            }
+    }
+    const bool any = l > 0.f || l != l;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const int d = lane + 32 * e;
+        if (d < D) out[d] = any ? (T)(o[e] / l * v_scale) : (T)0.f;
+    }
+    if (lse && lane == 0) *lse = any ? (sc.of(m) + log2f(l)) / kLog2e : -INFINITY;
+}
+
+// The largest magnitude of what a lane holds is no finite number in some lane.
+__device__ __forceinline__ bool spoilt(float check) { return __any_sync(0xffffffffu, check != check); }
+
+// Four elements of a row; *check becomes NaN where one is no finite number.
+template <typename T>
+__device__ __forceinline__ void store4(T *to, const float4 &y, float *check) {
+    *check = fmaf(y.x, 0.f, fmaf(y.y, 0.f, fmaf(y.z, 0.f, fmaf(y.w, 0.f, *check))));
+    *reinterpret_cast<uint2 *>(to) = make_uint2(elem::pair_from_f32<T>(y.x, y.y), elem::pair_from_f32<T>(y.z, y.w));
+}
+
+constexpr int kJoinWarps = 8, kJoinRows = 16;  // of a block
+
+// Requests: the tiles that were cut are joined, and rows that are no finite numbers looked at again.
+template <typename T, typename C, int DT>
+__global__ void __launch_bounds__(32 * kJoinWarps) finish_kernel(const __grid_constant__ Params p) {
+    using K = Config<T, C, DT>;
+    ptx::grid_dep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = p.c.head_dim;
+    constexpr int kBlocks = K::kRows / kJoinRows;  // of a tile
+    const int gb = min(p.group, K::kRows), cta = blockIdx.x / kBlocks, r0 = blockIdx.x % kBlocks * kJoinRows;
+    auto again = [&](int b, int row, int head, int hi) {
+        const Seq s = request(p, b, false);
+        const int lo = p.window > 0 ? max(0, hi - p.window) : 0, kvh = head / p.group;
+        one_row<T, C, DT>(p, static_cast<const T *>(p.q) + (long long)row * p.q_row + head * p.q_head,
+                          static_cast<T *>(p.out) + (long long)row * p.o_row + head * p.o_head,
+                          p.lse ? p.lse + (long long)row * p.heads + head : nullptr, kvh,
+                          s.pre >= 0 ? p.ptable + s.pre * p.ptable_stride : nullptr, p.table + b * p.table_stride, s.own0, lo, hi);
+    };
+    const Cut c = p.cuts[cta];
+    if (c.parts > 1 && cta + c.parts <= p.ctas)
+        for (int i = 0; i < kJoinRows / kJoinWarps; ++i) {
+            const int r = r0 + i * kJoinWarps + warp, tk = r / gb, hh = r - tk * gb;
+            if (r >= c.rows || hh >= c.heads) continue;
+            const Sums<DT> x = join_parts<K>(p, cta, c.parts, r, D);
+            const bool any = x.l > 0.f || x.l != x.l;
+            const float f = any ? (K::k8 && p.c.v_scale ? p.c.v_scale[c.kvh] : 1.f) / x.lr : 0.f;
+            const int row = c.q0 + tk, head = c.h0 + hh;
+            T *out = static_cast<T *>(p.out) + (long long)row * p.o_row + head * p.o_head;
+            float check = 0.f;
+#pragma unroll
+            for (int e = 0; e < x.kEach; ++e) {
+                const int d = 4 * (lane + 32 * e);
+                if (d < D) store4(out + d, make_float4(x.o[e].x * f, x.o[e].y * f, x.o[e].z * f, x.o[e].w * f), &check);
+            }
+            if (p.lse && lane == 0)
+                p.lse[(long long)row * p.heads + head] = any ? (x.m + log2f(x.l) - K::kUp) / kLog2e : -INFINITY;
+            if (spoilt(check)) again(c.seq, row, head, max(c.first + tk, 0));
+        }
+    if (!__syncthreads_or((int)threadIdx.x < p.ctas && p.odd[threadIdx.x])) return;
+    for (long long i = (long long)blockIdx.x * kJoinWarps + warp; i < (long long)p.rows * p.heads; i += (long long)gridDim.x * kJoinWarps) {
+        const int row = (int)(i / p.heads), head = (int)(i % p.heads);
+        const T *out = static_cast<const T *>(p.out) + (long long)row * p.o_row + head * p.o_head;
+        float check = 0.f;
+        for (int d = lane; d < D; d += 32) check = fmaf((float)out[d], 0.f, check);
+        if (!spoilt(check)) continue;
+        bool cut = false;  // joined above, or being joined
+        for (int x = lane; x < p.ctas; x += 32) {
+            const Cut y = p.cuts[x];
+            cut |= y.parts > 1 && row >= y.q0 && row < y.q0 + y.rows / gb && head >= y.h0 && head < y.h0 + y.heads;
+        }
+        if (__any_sync(0xffffffffu, cut)) continue;
+        for (int b0 = 0; b0 < p.batch; b0 += 32) {
+            Seq s{0, 0, 0, 0, 0};
+            if (b0 + lane < p.batch) s = request(p, b0 + lane, false);
+            const uint32_t mask = __ballot_sync(0xffffffffu, row >= s.q0 && row - s.q0 < s.n);
+            if (!mask) continue;
+            const int from = __ffs(mask) - 1;
+            const int hi = __shfl_sync(0xffffffffu, max(s.total - s.n + (row - s.q0) + 1, 0), from);
+            again(b0 + from, row, head, hi);
+            break;
+        }
+    }
+}
+
+// Prefixes: what a request sees of its prefix is joined with its own tokens.
+template <typename T, typename C, int DT>
+__global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __grid_constant__ Params p) {
+    using K = Config<T, C, DT>;
+    ptx::grid_dep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = p.c.head_dim;
+    const long long i = (long long)blockIdx.x * kJoinWarps + warp;
+    if (i >= (long long)p.batch * p.heads) return;
+    const int b = (int)(i / p.heads), head = (int)(i % p.heads), kvh = head / p.group, in_group = head % p.group;
+    const int gb = min(p.group, K::kRows), head_blocks = (p.group + gb - 1) / gb;
+    const int own = clamp_len(p.lens[b], p.max_pages, p.c.page_size);
+    T *out = static_cast<T *>(p.out) + b * p.o_row + head * p.o_head;
+    bool none = false;
+    const int pre = own > 0 ? prefix_of(p, b, &none) : -1;
+    Sums<DT> x;
+#pragma unroll
+    for (int e = 0; e < x.kEach; ++e) x.o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (pre >= 0) {
+        const Found f = p.found[(long long)(kvh * head_blocks + in_group / gb) * p.batch + b];
+        const int row = f.row + in_group % gb;
+        if (f.first < 0) {
+            const float *from = p.whole + i * K::kPitch;
+            const float4 s = __ldcg(reinterpret_cast<const float4 *>(from + DT));
+            x.m = s.x, x.l = s.y, x.lr = s.z;
+#pragma unroll
+            for (int e = 0; e < x.kEach; ++e) {
+                const int d = 4 * (lane + 32 * e);
+                if (d < D) x.o[e] = __ldcg(reinterpret_cast<const float4 *>(from + d));
+            }
+        } else if (f.parts > 0 && f.first + f.parts <= p.ctas && row >= 0 && row < K::kRows) {
+            x = join_parts<K>(p, f.first, f.parts, row, D);
+        }
+    }
+    const float own_lse = own > 0 ? p.raw_lse[i] : -INFINITY;
+    const bool any = x.l > 0.f || x.l != x.l, any_own = !(own_lse == -INFINITY);
+    const float a = any ? x.m + log2f(x.l) - K::kUp : -INFINITY;
+    const float top = fmaxf(a, own_lse), from = top == -INFINITY ? 0.f : top;
+    const float wa = any ? ex2(a - from) : 0.f, wo = any_own ? ex2(own_lse - from) : 0.f;
+    const float sum = wa + wo, f = any ? wa / sum * (K::k8 && p.c.v_scale ? p.c.v_scale[kvh] : 1.f) / x.lr : 0.f;
+    const float fo = any_own ? wo / sum : 0.f;
+    float check = 0.f;
+#pragma unroll
+    for (int e = 0; e < x.kEach; ++e) {
+        const int d = 4 * (lane + 32 * e);
+        if (d >= D) continue;
+        float4 y = make_float4(x.o[e].x * f, x.o[e].y * f, x.o[e].z * f, x.o[e].w * f);
+        if (any_own) {
+            const float4 z = __ldcg(reinterpret_cast<const float4 *>(p.raw + i * D + d));
+            y.x = fmaf(z.x, fo, y.x), y.y = fmaf(z.y, fo, y.y), y.z = fmaf(z.z, fo, y.z), y.w = fmaf(z.w, fo, y.w);
+        }
+        store4(out + d, y, &check);
+    }
+    if (p.lse && lane == 0) p.lse[i] = any || any_own ? (from + log2f(sum)) / kLog2e : -INFINITY;
+    if (spoilt(check)) {
+        const int shared = pre >= 0 ? clamp_len(p.plens[pre], p.pmax_pages, p.c.page_size) : 0;
+        const long long hi = (long long)shared + own;
+        one_row<T, C, DT>(p, static_cast<const T *>(p.q) + b * p.q_row + head * p.q_head, out, p.lse ? p.lse + i : nullptr, kvh,
+                          pre >= 0 ? p.ptable + pre * p.ptable_stride : nullptr, p.table + b * p.table_stride, shared,
+                          p.window > 0 ? (int)max(0ll, hi - p.window) : 0, (int)hi);
+    }
+}
+
+// ------------------------------------------------------------------ launches
+// Grid and block of a launch on `s`, as a programmatic dependent where that is wanted.
+struct Launch {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    Launch(unsigned blocks, int threads, int smem, cudaStream_t s) {
+        cfg.gridDim = dim3(blocks, 1, 1);
+        cfg.blockDim = dim3((unsigned)threads, 1, 1);
+        cfg.dynamicSmemBytes = (size_t)smem;
+        cfg.stream = s;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = as_dependent(s) ? 1 : 0;
+    }
+};
+
+// The kernels of a call, chosen by the types and the head's width.
+enum Which { kWide, kFinish, kPrefixJoin };
+template <typename T, typename C, int DT>
+cudaError_t launch(Which which, const Params &p, cudaStream_t s) {
+    using K = Config<T, C, DT>;
+    constexpr int kSmem = K::kAfter + (int)sizeof(Shared<K::kRows>) + 1024;
+    static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+    static_assert((3 * kMaxSeqs + 1) * 4 <= K::kAfter, "the plan lies where queries, keys and values come later");
+    static_assert(K::kAfter % 1024 == 0, "alignment");
+    if (which == kWide) {
+        auto kernel = wide_kernel<T, C, DT>;
+        const cudaError_t e = ensure_max_dyn_smem((const void *)kernel, kSmem);
+        if (e != cudaSuccess) return e;
+        Launch l((unsigned)p.ctas, K::kThreads, kSmem, s);
+        return cudaLaunchKernelEx(&l.cfg, kernel, p);
+    }
+    if (which == kFinish) {
+        Launch l((unsigned)(p.ctas * (K::kRows / kJoinRows)), 32 * kJoinWarps, 0, s);
+        return cudaLaunchKernelEx(&l.cfg, finish_kernel<T, C, DT>, p);
+    }
+    Launch l((unsigned)(((long long)p.batch * p.heads + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, 0, s);
+    return cudaLaunchKernelEx(&l.cfg, prefix_join_kernel<T, C, DT>, p);
+}
+template <typename T, typename C>
+cudaError_t launch_dims(Which which, const Params &p, cudaStream_t s) {
+    if (p.c.head_dim <= 64) return launch<T, C, 64>(which, p, s);
+    if (p.c.head_dim <= 128) return launch<T, C, 128>(which, p, s);
+    return launch<T, C, 256>(which, p, s);
+}
+
+// A head's width as the kernels have it, and the rows of a tile.
+inline int dim_of(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
+inline int rows_of(int head_dim) { return head_dim > 128 ? 128 : 256; }
+
+// Defined in wide_attention_f16.cu and wide_attention_bf16.cu.
+cudaError_t launch_f16(Which which, const Params &p, cudaStream_t s);
+cudaError_t launch_bf16(Which which, const Params &p, cudaStream_t s);
+
+}  // namespace wide
+}  // namespace w4a16
