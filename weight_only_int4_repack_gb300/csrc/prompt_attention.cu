@@ -52,7 +52,7 @@ w4a16_status check(const void *q, w4a16_type type, long long q_row, long long q_
                    const int32_t *table, long long table_stride, int max_pages, const int32_t *lens, int rows, int batch,
                    int heads, const int32_t *ptable, long long ptable_stride, int pmax_pages, const int32_t *plens,
                    const int32_t *pof, int prefixes, float scale, int window, float softcap, const void *out, long long o_row,
-                   long long o_head, const float *lse, bool *nothing) {
+                   long long o_head, const float *lse, bool prefixes_only, bool *nothing) {
     const w4a16_status st = check_cache(cache);
     if (st != W4A16_OK) return st;
     if (type != W4A16_TYPE_F16 && type != W4A16_TYPE_BF16) return W4A16_ERR_INVALID_ARG;
@@ -65,6 +65,11 @@ w4a16_status check(const void *q, w4a16_type type, long long q_row, long long q_
     // Keys of a sequence are numbered in 31 bits.
     const long long keys = ((long long)max_pages + (prefixes > 0 ? pmax_pages : 0)) * cache->page_size;
     if (keys > INT_MAX - 1024) return W4A16_ERR_UNSUPPORTED;
+    // Units of work are numbered in 31 bits: tiles of rows, at most one a sequence besides the full ones, times keys.
+    const int group = heads / cache->kv_heads, most = wide::rows_of(cache->head_dim), block = group < most ? group : most;
+    const long long seqs = prefixes_only ? prefixes : batch;
+    const long long tiles = rows / (most / block) + seqs, hds = (long long)(group + block - 1) / block * cache->kv_heads;
+    if (tiles * hds > INT_MAX / (keys / wide::keys_of(cache->head_dim) + 2)) return W4A16_ERR_UNSUPPORTED;
     *nothing = rows == 0 || batch == 0;
     if (*nothing) return W4A16_OK;
     if (!q || !out || !table || !lens || (prefixes > 0 && (!ptable || !plens || !pof))) return W4A16_ERR_INVALID_ARG;
@@ -95,7 +100,7 @@ w4a16_status w4a16_prompt_attention(const void *q, w4a16_type type, long long q_
     bool nothing = false;
     const w4a16_status st = check(q, type, q_row, q_head, cache, table, table_stride, max_pages, lens, rows, batch, heads,
                                   prefix_table, prefix_stride, prefix_pages, prefix_lens, prefix_of, prefixes, scale, window,
-                                  softcap, out, o_row, o_head, lse, &nothing);
+                                  softcap, out, o_row, o_head, lse, false, &nothing);
     if (st != W4A16_OK || nothing) return st;
     if (!starts || !aligned(starts, 4) || q == out) return W4A16_ERR_INVALID_ARG;
     const Layout l(0, cache->head_dim);
@@ -134,7 +139,7 @@ w4a16_status w4a16_prefix_attention(const void *q, w4a16_type type, long long q_
     bool nothing = false;
     w4a16_status st = check(q, type, q_row, q_head, cache, table, table_stride, max_pages, lens, batch, batch, heads,
                             prefix_table, prefix_stride, prefix_pages, prefix_lens, prefix_of, prefixes, scale, window, softcap,
-                            out, o_row, o_head, lse, &nothing);
+                            out, o_row, o_head, lse, true, &nothing);
     if (st != W4A16_OK) return st;
     if (prefixes == 0) return W4A16_ERR_INVALID_ARG;
     if (nothing) return W4A16_OK;

@@ -82,8 +82,10 @@ constexpr float kSlack = 4.f, kLowest = -3.402823466e38f, kLog2e = 1.44269504088
 
 template <typename T, typename C, int DT>
 struct Config {
-    static constexpr bool kB16 = std::is_same<T, __nv_bfloat16>::value;
     static constexpr bool k8 = sizeof(C) == 1;
+    using M = typename std::conditional<k8, __half, T>::type;  // operands
+    static constexpr bool kB16 = std::is_same<M, __nv_bfloat16>::value;
+    static constexpr bool kOwnPower = k8 && std::is_same<T, __nv_bfloat16>::value;  // queries brought to fp16
     static constexpr float kUp = kB16 ? -kSlack : 11.f;
     static constexpr int kDim = DT;                       // head_dim, rounded up
     static constexpr int kTiles = DT > 128 ? 1 : 2;       // groups of 128 rows
@@ -97,9 +99,14 @@ struct Config {
     static constexpr int kPitch = DT + 8;                 // floats of a row of sums: outputs, then m, l, l as rounded
     static constexpr int kSlot = kRows * kPitch;
     // Tensor memory: a group's scores (its weights take their place) and outputs.
-    static constexpr int kO = DT > 128 ? 256 : 256, kOStep = DT > 128 ? 0 : 128, kSStep = 128;
-    static constexpr int kWarps = 4 * kTiles + 5, kThreads = 32 * kWarps;
+    static constexpr int kO = 256, kOStep = 128, kSStep = 128;
+    static constexpr int kWarps = 4 * kTiles + 8, kThreads = 32 * kWarps;
     static constexpr int kLoader = 4 * kTiles, kMma = kLoader + 4;  // first warps of the roles
+    // Registers: with two groups of rows the loaders and the issuing warps leave some of theirs to them
+    // (256 threads at 184 and 256 at 72 are the 65536 that 512 threads get at 128).
+    static constexpr bool kSplit = kTiles == 2;
+    static constexpr int kMore = 184, kLess = 72;
+    static_assert(kMore + kLess == 256, "as many registers as there are");
 };
 
 constexpr int kQueue = 4;
@@ -119,13 +126,12 @@ template <int kRows>
 struct Shared {
     int counts[kMaxPrefixes], least[kMaxPrefixes];  // of each prefix: requests, shortest own length
     int members[kQueue][kRows];                     // requests of a tile (prefixes)
+    float powers[kQueue][kRows];                    // what a row's scores have to be multiplied by (kOwnPower)
     uint32_t bad[8][4];                             // keys of a unit whose page is none
     Segment segs[kQueue];
     uint64_t full[8], empty[8], seg_full[kQueue], seg_empty[kQueue], s_full[2], p_full[2], o_full[2], q_full, q_empty, drain;
-    long long sums[32];
-    long long units;
-    int start_s, start_t, start_hd, tiles;
-    long long start_base;
+    int sums[32];
+    int start_s, start_t, start_hd, start_base, tiles;
     uint32_t tmem;
     int abort, odd;
 };
@@ -200,18 +206,18 @@ __device__ __forceinline__ Tile tile_of(const Params &p, const Seq &s, int least
 
 // Sum over the threads in front of this one, and over all.
 template <int kWarps>
-__device__ __forceinline__ long long scan(long long mine, long long *sums, long long *total) {
+__device__ __forceinline__ int scan(int mine, int *sums, int *total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long upto = mine;
+    int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += y;
     }
     __syncthreads();
     if (lane == 31) sums[warp] = upto;
     __syncthreads();
-    long long before = 0, all = 0;
+    int before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) before += sums[w];
@@ -235,6 +241,9 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real)
     const int n = real ? 16 : 0;
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+__device__ __forceinline__ void copy16_all(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
@@ -250,6 +259,23 @@ __device__ __forceinline__ void store8(float *to, const float *x) {
     asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "f"(x[0]), "f"(x[1]), "f"(x[2]),
                  "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
                  : "memory");
+}
+
+// Two at a time.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
 }
 
 // How a raw product becomes a score, in units of log2.
@@ -324,21 +350,21 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
     };
     {
         const int per = (seqs + K::kThreads - 1) / K::kThreads, s0 = min(tid * per, seqs), s1 = min(s0 + per, seqs);
-        long long mine = 0, all = 0;
+        int mine = 0, all = 0;
         for (int i = s0; i < s1; ++i) {
             const Seq s = seq_of(i, cta == 0);
             plan_n[i] = s.n, plan_total[i] = s.total;
             mine += (s.n + tt - 1) / tt;
         }
-        long long at = scan<K::kWarps>(mine, sh.sums, &all);
+        int at = scan<K::kWarps>(mine, sh.sums, &all);
         for (int i = s0; i < s1; ++i) {
-            plan_off[i] = (int)at;
+            plan_off[i] = at;
             at += (plan_n[i] + tt - 1) / tt;
         }
-        if (tid == 0) plan_off[seqs] = (int)all, sh.tiles = (int)all;
+        if (tid == 0) plan_off[seqs] = all, sh.tiles = all;
     }
     __syncthreads();
-    long long total_units = 0, t_begin = 0, t_end = 0;
+    int total_units = 0, t_begin = 0, t_end = 0;  // below 2^31: the host has seen to that
     int active;
     {
         const int tiles = sh.tiles;
@@ -357,26 +383,26 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             const Seq q{plan_n[s], plan_total[s], 0, 0, 0};
             return tile_of<K>(p, q, p.starts ? 0 : sh.least[s], tt, i - plan_off[s]).count;
         };
-        long long mine = 0, per_hd = 0;
+        int mine = 0, per_hd = 0;
         for (int i = i0, s = s_first; i < i1; ++i) {
             while (i >= plan_off[s + 1]) ++s;
             mine += units_of(s, i);
         }
-        const long long before = scan<K::kWarps>(mine, sh.sums, &per_hd);
+        const int before = scan<K::kWarps>(mine, sh.sums, &per_hd);
         total_units = per_hd * hds;
-        active = (int)min((long long)gridDim.x, total_units);
+        active = min((int)gridDim.x, total_units);
         if (cta < active) {
-            const long long each = total_units / active, over = total_units - each * active;
+            const int each = total_units / active, over = total_units - each * active;
             t_begin = each * cta + over * cta / active;
             t_end = each * (cta + 1) + over * (cta + 1) / active;
-            const long long rem = t_begin % per_hd;
+            const int hd = t_begin / per_hd, rem = t_begin - hd * per_hd;
             if (rem >= before && rem < before + mine) {
-                long long at = before;
+                int at = before;
                 for (int i = i0, s = s_first; i < i1; ++i) {
                     while (i >= plan_off[s + 1]) ++s;
                     const int n = units_of(s, i);
                     if (rem < at + n) {
-                        sh.start_s = s, sh.start_t = i - plan_off[s], sh.start_hd = (int)(t_begin / per_hd);
+                        sh.start_s = s, sh.start_t = i - plan_off[s], sh.start_hd = hd;
                         sh.start_base = t_begin - rem + at;
                         break;
                     }
@@ -395,11 +421,12 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
 
     if (warp >= K::kLoader && warp < K::kMma) {
         // ------------------------------------------------------------ loaders
+        if constexpr (K::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(K::kLess));
         const int w = warp - K::kLoader;
         if (w == 0 && lane == 0 && p.cuts) p.cuts[cta].parts = 0;
         bool ok = has_work;
         int s = sh.start_s, t = sh.start_t, hd = sh.start_hd;
-        long long x = t_begin, base = sh.start_base;
+        int x = t_begin, base = sh.start_base;
         int stage = 0, seg_n = 0, unit_n = 0;
         uint32_t ring_phase = 1;  // of the empty barriers
         // Copies on their way, oldest first: the barriers that wait for them.
@@ -442,7 +469,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
         while (ok && x < t_end) {
             const Seq seq = seq_of(s, false);
             const Tile tile = tile_of<K>(p, seq, p.starts ? 0 : sh.least[s], tt, t);
-            const int from = (int)(x - base), take = (int)min((long long)(tile.count - from), t_end - x);
+            const int from = x - base, take = min(tile.count - from, t_end - x);
             const int kvh = hd / head_blocks, h0 = kvh * p.group + hd % head_blocks * gb;
             const int heads_here = min(gb, (kvh + 1) * p.group - h0);
             const bool begins = from == 0, ends = from + take == tile.count;
@@ -463,7 +490,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                 __syncwarp();
             }
             int parts = 1;
-            if (begins && !ends) parts = (int)(((base + tile.count) * active - 1) / total_units) - cta + 1;
+            if (begins && !ends) parts = (int)(((long long)(base + tile.count) * active - 1) / total_units) - cta + 1;
             if (w == 0) {
                 if (lane == 0) {
                     Segment g;
@@ -494,14 +521,41 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                     for (int i = 0; i < 32; i += kAt) {
                         const int rr = r0 + i + lane / kLanes;
                         const long long src = __shfl_sync(0xffffffffu, at, i + lane / kLanes);
-                        if (c * 8 < 16 * k_steps) {
-                            const bool real = src >= 0 && c * 8 < D;
-                            copy16(q_base + (rr >> 7) * K::kQBytes + (c >> 3) * 16384 + (rr & 127) * 128 + (((c & 7) ^ (rr & 7)) << 4),
-                                   static_cast<const T *>(p.q) + (real ? src + c * 8 : 0), real);
+                        const bool real = src >= 0 && c * 8 < D;
+                        const T *from = static_cast<const T *>(p.q) + (real ? src + c * 8 : 0);
+                        const uint32_t to = q_base + (rr >> 7) * K::kQBytes + (c >> 3) * 16384 + (rr & 127) * 128 + (((c & 7) ^ (rr & 7)) << 4);
+                        if constexpr (!K::kOwnPower) {
+                            if (c * 8 < 16 * k_steps) copy16(to, from, real);
+                        } else {
+                            // To fp16, after a power of two that brings the row's largest below 2: what that loses is 2^-25
+                            // of the largest.
+                            const uint4 y = real ? *reinterpret_cast<const uint4 *>(from) : make_uint4(0, 0, 0, 0);
+                            const uint32_t z[4] = {y.x, y.y, y.z, y.w};
+                            float big = 0.f;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float2 f = elem::pair_to_f32<T>(z[e]);
+                                big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+                            }
+#pragma unroll
+                            for (int o = 1; o < kLanes; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+                            const int e2 = big > 0.f && big < INFINITY ? max(ilogbf(big), -120) : 0;
+                            const float down = ldexpf(1.f, -e2);
+                            uint32_t h[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float2 f = elem::pair_to_f32<T>(z[e]);
+                                h[e] = elem::pair_from_f32<__half>(f.x * down, f.y * down);
+                            }
+                            if (c == 0) sh.powers[qi][rr] = ldexpf(1.f, e2);
+                            if (c * 8 < 16 * k_steps)
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                                             : "memory");
                         }
                     }
                 }
-                queue(&sh.q_full);
+                if constexpr (K::kOwnPower) signal(&sh.q_full);
+                else queue(&sh.q_full);
             }
             // Keys and values, unit after unit.
             const int32_t *own_pages = p.starts ? p.table + (long long)s * p.table_stride : nullptr;
@@ -544,15 +598,22 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                     const uint32_t dst = ring + stage * K::kStageBytes;
                     if constexpr (!K::k8) {
                         constexpr int kChunks = DT / 8, kLanes = kChunks < 32 ? kChunks : 32, kAt = 32 / kLanes;
-                        const int c = lane % kLanes;
-#pragma unroll
-                        for (int i = 0; i < kMine; i += kAt) {
-                            const int r = i + lane / kLanes, row = w * kMine + r;
-                            const unsigned long long src = __shfl_sync(0xffffffffu, off, r);
-                            if (c * 8 < 16 * k_steps) {
-                                const bool there = ((real >> r) & 1u) && c * 8 < D;
-                                copy16(dst + (c >> 3) * (kKeys * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-                                       pool + (there ? src + c * 8 : 0), there);
+                        const int c = lane % kLanes, r0 = lane / kLanes;
+                        const C *from = pool + c * 8;
+                        const uint32_t to = dst + (c >> 3) * (kKeys * 128) + (w * kMine + r0) * 128;
+                        const uint32_t all = kMine == 32 ? 0xffffffffu : 0xffffu;
+                        if ((real & all) == all && D == DT) {  // as a rule
+#pragma unroll 8
+                            for (int i = 0; i < kMine; i += kAt)
+                                copy16_all(to + i * 128 + (((c & 7) ^ ((i + r0) & 7)) << 4),
+                                           from + __shfl_sync(0xffffffffu, off, i + r0));
+                        } else {
+#pragma unroll 1
+                            for (int i = 0; i < kMine; i += kAt) {
+                                const unsigned long long src = __shfl_sync(0xffffffffu, off, i + r0);
+                                const bool there = ((real >> (i + r0)) & 1u) && c * 8 < D;
+                                if (c * 8 < 16 * k_steps)
+                                    copy16(to + i * 128 + (((c & 7) ^ ((i + r0) & 7)) << 4), there ? from + src : pool, there);
                             }
                         }
                         queue(&sh.full[stage]);
@@ -575,12 +636,6 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                             elem::e4m3x4_to_half2(y[i].y, h[2], h[3]);
                             elem::e4m3x4_to_half2(y[i].z, h[4], h[5]);
                             elem::e4m3x4_to_half2(y[i].w, h[6], h[7]);
-                            if constexpr (K::kB16)
-#pragma unroll
-                                for (int z = 0; z < 8; ++z) {
-                                    const float2 f = elem::pair_to_f32<__half>(h[z]);
-                                    h[z] = elem::pair_from_f32<__nv_bfloat16>(f.x, f.y);
-                                }
                             const uint32_t to = dst + (c >> 2) * (kKeys * 128) + row * 128;
                             const int c0 = (2 * c) & 7;
                             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((c0 ^ (row & 7)) << 4)), "r"(h[0]),
@@ -590,7 +645,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                                          "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7])
                                          : "memory");
                         }
-                        drain();  // the queries
+                        if (!K::kOwnPower) drain();  // the queries
                         signal(&sh.full[stage]);
                     }
                     if (++stage == kStages) stage = 0, ring_phase ^= 1u;
@@ -620,9 +675,10 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
         }
         drain();
         asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp == K::kMma) {
+    } else if (warp >= K::kMma) {
         // ------------------------------------------------------------ matrix products
-        if (lane == 0 && has_work) {
+        if constexpr (K::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(K::kLess));
+        if (warp == K::kMma && lane == 0 && has_work) {
             const uint32_t id_qk = tc5::idesc(K::kB16, kKeys, p.scale < 0.f, false);
             const uint32_t id_pv = tc5::idesc(K::kB16, 16 * k_steps, false, true);
             int stage = 0;
@@ -699,6 +755,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax and output
+        if constexpr (K::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(K::kMore));
         const int x = warp >> 2;                                   // group
         const int row = x * 128 + (warp & 3) * 32 + lane;          // of the tile
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;  // tensor memory lanes of this warp
@@ -731,90 +788,98 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                         lo = (int)max(0ll, (long long)hi + clamp_len(p.lens[b], p.max_pages, p.c.page_size) - p.window);
                 }
             }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&sh.seg_empty[qi]);
+            auto done = [&] {
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&sh.seg_empty[qi]);
+            };
             if (x * 128 >= g.rows) {  // nothing for this group
+                done();
                 unit_n += g.count;
                 continue;
             }
-            const float k_scale = K::k8 && p.c.k_scale ? p.c.k_scale[g.kvh] : 1.f;
-            const Scores sc(p, k_scale);
-            float m = kLowest, limit = kLowest, m_score = 0.f, l = 0.f, lr = 0.f;
+            float k_scale = K::k8 && p.c.k_scale ? p.c.k_scale[g.kvh] : 1.f;
+            float unit = 1.f, slack = 0.f;
+            Scores sc(p, k_scale);
+            float m = kLowest, limit = kLowest;
+            float2 l = make_float2(0.f, 0.f), lr = make_float2(0.f, 0.f);
             for (int j = 0; j < g.count; ++j, ++unit_n) {
                 if (!wait(&sh.s_full[x], s_phase)) break;
                 s_phase ^= 1u;
                 tc5::fence_after();
+                if (j == 0) {
+                    if constexpr (K::kOwnPower) sc = Scores(p, k_scale * sh.powers[qi][row]);
+                    unit = sc.capped ? 1.f : sc.unit;
+                    slack = sc.capped ? kSlack : sc.slack;
+                    done();
+                }
                 if (some) {
                     const int key0 = g.key0 + j * kKeys;
-                    uint32_t bad[kKeys / 32];
+                    const uint32_t *bad = sh.bad[unit_n & 7];
+                    const bool masked = __any_sync(0xffffffffu, lo > key0 || hi < key0 + kKeys) || (bad[0] | bad[1] | bad[2] | bad[3]);
+                    if (masked || sc.capped) {  // what is not a plain product goes back to where the products were
+                        const unsigned int rel = (unsigned int)(key0 - lo), span = (unsigned int)max(hi - lo, 0);
+#pragma unroll 1
+                        for (int c = 0; c < kKeys / 32; ++c) {
+                            uint32_t v[32];
+                            tc5::ld32(t_s + c * 32, v);
+                            const uint32_t none = kKeys == 128 ? bad[c] : bad[2 * c] | (bad[2 * c + 1] << 16);
+                            tc5::wait_ld();
+                            if (sc.capped)
 #pragma unroll
-                    for (int i = 0; i < kKeys / 32; ++i)
-                        bad[i] = kKeys == 128 ? sh.bad[unit_n & 7][i] : sh.bad[unit_n & 7][2 * i] | (sh.bad[unit_n & 7][2 * i + 1] << 16);
-                    uint32_t any_bad = 0;
+                                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(sc.squeezed(__uint_as_float(v[i])));
+                            if (masked)
 #pragma unroll
-                    for (int i = 0; i < kKeys / 32; ++i) any_bad |= bad[i];
-                    const bool masked = __any_sync(0xffffffffu, lo > key0 || hi < key0 + kKeys) || any_bad;
-                    const unsigned int rel = (unsigned int)(key0 - lo), span = (unsigned int)max(hi - lo, 0);
-                    auto hide = [&](float (&f)[32], int c) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (rel + (unsigned int)(c * 32 + i) >= span || ((bad[c] >> i) & 1u)) f[i] = -INFINITY;
-                    };
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < kKeys / 32; ++c) {
-                        uint32_t v[32];
-                        float f[32];
-                        tc5::ld32(t_s + c * 32, v);
-                        tc5::wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-                        if (masked) hide(f, c);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, f[i]);
+                                for (int i = 0; i < 32; ++i)
+                                    if (rel + (unsigned int)(c * 32 + i) >= span || ((none >> i) & 1u)) v[i] = 0xff800000u;
+                            tc5::st32(t_s + c * 32, v);
+                        }
+                        tc5::wait_st();
                     }
+                    uint32_t v[kKeys / 32][32];
+#pragma unroll
+                    for (int c = 0; c < kKeys / 32; ++c) tc5::ld32(t_s + c * 32, v[c]);
+                    tc5::wait_ld();
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < kKeys / 32; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2)
+                            top[i / 2 & 3] = fmaxf(top[i / 2 & 3], fmaxf(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1])));
+                    const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     if (__any_sync(0xffffffffu, mx > limit)) {
-                        const float y = fmaxf(m, mx), y_score = sc.of(y);
-                        const float keep = sc.capped ? ex2(m_score - y_score) : ex2((m - y) * sc.unit);
+                        const float y = fmaxf(m, mx), keep = ex2((m - y) * unit);
                         if (j > 0) {
-                            for (int c = 0; c < (D + 31) / 32; ++c) {
-                                uint32_t v[32];
-                                tc5::ld32(t_o + c * 32, v);
+#pragma unroll 1
+                            for (int c = 0; c < (D + 15) / 16; ++c) {
+                                uint32_t o[16];
+                                tc5::ld16(t_o + c * 16, o);
                                 tc5::wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * keep);
-                                tc5::st32(t_o + c * 32, v);
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                                tc5::st16(t_o + c * 16, o);
                             }
                         }
-                        l *= keep, lr *= keep;
-                        m = y, m_score = y_score, limit = y + sc.slack;
+                        l.x *= keep, l.y *= keep, lr.x *= keep, lr.y *= keep;
+                        m = y, limit = y + slack;
                     }
-                    const float shift = K::kUp + sc.cap - m_score;
+                    // Weights 2^((s - m) unit + kUp): differences first, so that however large scores are the reference's weight is
+                    // right. They are cut to the operands' precision, not rounded to it: what that takes from all of them
+                    // alike cancels in the quotient by the sum of the cut ones, and what is left is as small as after rounding.
+                    const float2 neg = make_float2(-m, -m), by = make_float2(unit, unit), up = make_float2(K::kUp, K::kUp);
+                    constexpr uint32_t kCut = K::kB16 ? 0xffff0000u : 0xffffe000u;
 #pragma unroll
                     for (int c = 0; c < kKeys / 32; ++c) {
-                        uint32_t v[32], h[16];
-                        float f[32];
-                        tc5::ld32(t_s + c * 32, v);
-                        tc5::wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-                        if (masked) hide(f, c);
-                        if (!sc.capped) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) f[i] = ex2(fmaf(f[i] - m, sc.unit, K::kUp));
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const float y = ex2(fmaf(rcp(1.f + ex2(f[i] * sc.in)), -2.f * sc.cap, shift));
-                                f[i] = f[i] == -INFINITY ? 0.f : y;
-                            }
-                        }
+                        uint32_t h[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            l += f[2 * i] + f[2 * i + 1];
-                            h[i] = elem::pair_from_f32<T>(f[2 * i], f[2 * i + 1]);
-                            const float2 r = elem::pair_to_f32<T>(h[i]);
-                            lr += r.x + r.y;
+                            float2 s = make_float2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1]));
+                            s = fma2(add2(s, neg), by, up);
+                            s.x = ex2(s.x), s.y = ex2(s.y);
+                            l = add2(l, s);
+                            s.x = __uint_as_float(__float_as_uint(s.x) & kCut), s.y = __uint_as_float(__float_as_uint(s.y) & kCut);
+                            lr = add2(lr, s);
+                            if constexpr (K::kB16) h[i] = __byte_perm(__float_as_uint(s.x), __float_as_uint(s.y), 0x7632);
+                            else h[i] = elem::pair_from_f32<__half>(s.x, s.y);
                         }
                         tc5::st16(t_s + c * 16, h);
                     }
@@ -830,15 +895,17 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             tc5::fence_after();
             if (!some) continue;
             const float v_scale = K::k8 && p.c.v_scale ? p.c.v_scale[g.kvh] : 1.f;
-            const bool any = l > 0.f || l != l;
+            const float sum = l.x + l.y, cut = lr.x + lr.y;
+            const bool any = sum > 0.f || sum != sum;
             const bool direct = g.slot < 0 && p.starts;
-            const float f = !direct ? 1.f : any ? v_scale / lr : 0.f;
+            const float f = !direct ? 1.f : any ? v_scale / cut : 0.f;
             float *sums = nullptr;
             if (!direct)
                 sums = g.slot >= 0 ? p.slots + (long long)g.slot * K::kSlot + row * K::kPitch
                                    : p.whole + ((long long)b * p.heads + head) * K::kPitch;
             T *out = static_cast<T *>(p.out) + (long long)b * p.o_row + head * p.o_head;
             float check = 0.f;
+#pragma unroll 1
             for (int c = 0; c < (D + 31) / 32; ++c) {
                 uint32_t v[32];
                 float o[32];
@@ -868,9 +935,9 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                 if (direct) {
                     odd |= check != check;
                     if (p.lse)
-                        p.lse[(long long)b * p.heads + head] = any ? (sc.of(m) + log2f(l) - K::kUp) / kLog2e : -INFINITY;
+                        p.lse[(long long)b * p.heads + head] = any ? (m * unit + log2f(sum) - K::kUp) / kLog2e : -INFINITY;
                 } else {
-                    *reinterpret_cast<float4 *>(sums + DT) = make_float4(any ? sc.of(m) : -INFINITY, l, lr, 0.f);
+                    *reinterpret_cast<float4 *>(sums + DT) = make_float4(any ? m * unit : -INFINITY, sum, cut, 0.f);
                 }
             }
         }
@@ -1188,9 +1255,10 @@ cudaError_t launch_dims(Which which, const Params &p, cudaStream_t s) {
     return launch<T, C, 256>(which, p, s);
 }
 
-// A head's width as the kernels have it, and the rows of a tile.
+// A head's width as the kernels have it, the rows of a tile, the keys of a unit.
 inline int dim_of(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
 inline int rows_of(int head_dim) { return head_dim > 128 ? 128 : 256; }
+inline int keys_of(int head_dim) { return head_dim > 128 ? 64 : 128; }
 
 // Defined in wide_attention_f16.cu and wide_attention_bf16.cu.
 cudaError_t launch_f16(Which which, const Params &p, cudaStream_t s);
