@@ -155,7 +155,7 @@ __device__ __forceinline__ int prefix_of(const Params &p, int b, bool *none) {
     if (x >= p.prefixes) *none = true;
     return x >= 0 && x < p.prefixes ? x : -1;
 }
-__device__ __forceinline__ Seq request(const Params &p, int b, bool report) {
+static __device__ __noinline__ Seq request(const Params &p, int b, bool report) {
     Seq s;
     const int from = p.starts[b], to = p.starts[b + 1], len = p.lens[b];
     bool bad = from < 0 || to < from || to > p.rows;
@@ -183,7 +183,7 @@ struct Tile {
     int tok0, toks, first, lo, hi, key0, count;
 };
 template <typename K>
-__device__ __forceinline__ Tile tile_of(const Params &p, const Seq &s, int least, int tt, int t) {
+__device__ __noinline__ Tile tile_of(const Params &p, const Seq &s, int least, int tt, int t) {
     Tile x;
     x.tok0 = t * tt;
     x.toks = min(tt, s.n - x.tok0);
@@ -254,6 +254,27 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// ptx::mbar_wait in fewer instructions, for all lanes of a warp alike.
+__device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *abort_flag, unsigned int *err, uint64_t limit_ns) {
+    uint64_t since = 0;
+#pragma unroll 1
+    for (;;) {
+        if (__all_sync(0xffffffffu, ptx::mbar_try_wait_sleep(bar, parity, 20000u))) return true;
+        const uint64_t now = ptx::globaltimer();
+        if (since == 0) since = now;
+        const bool over = now - since >= limit_ns;
+        if (over && err) atomicExch(err, (unsigned int)W4A16_ERR_TIMEOUT);
+        if (over) *abort_flag = 1;
+        if (__any_sync(0xffffffffu, over || *abort_flag)) return false;
+    }
+}
+
+// One lane of the warp, always the same: matrix instructions are issued by it, and the compiler knows that it is one.
+__device__ __forceinline__ bool elect() {
+    uint32_t x;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(x));
+    return x != 0;
+}
 // 32 bytes, 32-byte aligned.
 __device__ __forceinline__ void store8(float *to, const float *x) {
     asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "f"(x[0]), "f"(x[1]), "f"(x[2]),
@@ -315,8 +336,11 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
     const int D = p.c.head_dim;
 
     if (tid == 0) {
+#pragma unroll 1
         for (int i = 0; i < kStages; ++i) ptx::mbar_init(&sh.full[i], 4), ptx::mbar_init(&sh.empty[i], 1);
+#pragma unroll 1
         for (int i = 0; i < kQueue; ++i) ptx::mbar_init(&sh.seg_full[i], 1), ptx::mbar_init(&sh.seg_empty[i], 4 * kTiles + 1);
+#pragma unroll 1
         for (int i = 0; i < 2; ++i)
             ptx::mbar_init(&sh.s_full[i], 1), ptx::mbar_init(&sh.p_full[i], 4), ptx::mbar_init(&sh.o_full[i], 1);
         ptx::mbar_init(&sh.q_full, 4), ptx::mbar_init(&sh.q_empty, 1), ptx::mbar_init(&sh.drain, 1);
@@ -332,8 +356,10 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
     const int seqs = p.starts ? p.batch : p.prefixes;
     int *plan_off = reinterpret_cast<int *>(smem), *plan_n = plan_off + seqs + 1, *plan_total = plan_n + seqs;
     if (!p.starts) {
+#pragma unroll 1
         for (int i = tid; i < seqs; i += K::kThreads) sh.counts[i] = 0, sh.least[i] = 0x7fffffff;
         __syncthreads();
+#pragma unroll 1
         for (int b = tid; b < p.batch; b += K::kThreads) {
             bool bad = false;
             const int x = prefix_of(p, b, &bad), len = p.lens[b], own = clamp_len(len, p.max_pages, p.c.page_size);
@@ -351,12 +377,14 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
     {
         const int per = (seqs + K::kThreads - 1) / K::kThreads, s0 = min(tid * per, seqs), s1 = min(s0 + per, seqs);
         int mine = 0, all = 0;
+#pragma unroll 1
         for (int i = s0; i < s1; ++i) {
             const Seq s = seq_of(i, cta == 0);
             plan_n[i] = s.n, plan_total[i] = s.total;
             mine += (s.n + tt - 1) / tt;
         }
         int at = scan<K::kWarps>(mine, sh.sums, &all);
+#pragma unroll 1
         for (int i = s0; i < s1; ++i) {
             plan_off[i] = at;
             at += (plan_n[i] + tt - 1) / tt;
@@ -372,6 +400,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
         int s_first = 0;
         if (i0 < i1) {  // the sequence of the thread's first tile: the last one that begins at or in front of it
             int lo = 0, hi = seqs - 1;
+#pragma unroll 1
             while (lo < hi) {
                 const int mid = (lo + hi + 1) / 2;
                 if (plan_off[mid] <= i0) lo = mid;
@@ -384,7 +413,9 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             return tile_of<K>(p, q, p.starts ? 0 : sh.least[s], tt, i - plan_off[s]).count;
         };
         int mine = 0, per_hd = 0;
+#pragma unroll 1
         for (int i = i0, s = s_first; i < i1; ++i) {
+#pragma unroll 1
             while (i >= plan_off[s + 1]) ++s;
             mine += units_of(s, i);
         }
@@ -398,7 +429,9 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             const int hd = t_begin / per_hd, rem = t_begin - hd * per_hd;
             if (rem >= before && rem < before + mine) {
                 int at = before;
+#pragma unroll 1
                 for (int i = i0, s = s_first; i < i1; ++i) {
+#pragma unroll 1
                     while (i >= plan_off[s + 1]) ++s;
                     const int n = units_of(s, i);
                     if (rem < at + n) {
@@ -462,10 +495,11 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             if (!__all_sync(0xffffffffu, mbar_test(bar, parity))) {
                 drain();
-                if (!__all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort_flag, p.err, p.wait_ns))) ok = false;
+                ok = wait_on(bar, parity, abort_flag, p.err, p.wait_ns);
             }
             return ok;
         };
+#pragma unroll 1
         while (ok && x < t_end) {
             const Seq seq = seq_of(s, false);
             const Tile tile = tile_of<K>(p, seq, p.starts ? 0 : sh.least[s], tt, t);
@@ -479,6 +513,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             const int rows = tile.toks * gb;
             if (!p.starts) {  // the requests of these ranks (every loader warp writes the same)
                 int rank = 0;
+#pragma unroll 1
                 for (int b0 = 0; b0 < p.batch && rank < tile.tok0 + tile.toks; b0 += 32) {
                     const int b = b0 + lane;
                     const bool in = b < p.batch && behind(p, b, s);
@@ -502,6 +537,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                     if (p.cuts && begins && !ends) p.cuts[cta] = Cut{parts, rows, g.q0, h0, kvh, heads_here, s, tile.first};
                 }
                 if (!p.starts && begins)
+#pragma unroll 1
                     for (int i = lane; i < tile.toks; i += 32)
                         p.found[(long long)hd * p.batch + members[i]] = Found{ends ? -1 : cta, parts, i * gb, 0};
                 __syncwarp();
@@ -512,6 +548,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             {
                 constexpr int kChunks = DT / 8, kLanes = kChunks < 32 ? kChunks : 32, kAt = 32 / kLanes;
                 const int c = lane % kLanes;
+#pragma unroll 1
                 for (int r0 = w * (K::kRows / 4); r0 < (w + 1) * (K::kRows / 4) && r0 < (rows + 127) / 128 * 128; r0 += 32) {
                     const int r = r0 + lane, tk = r / gb, hh = r - tk * gb;
                     const bool in = r < rows && hh < heads_here && p.scale != 0.f;
@@ -577,6 +614,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             int page, at;
             bool in;
             look_up(0, page, at, in);
+#pragma unroll 1
             for (int u = 0; u < take; ++u) {
                 const bool good = in && page >= 0 && page < p.c.pages;
                 const uint32_t bad = __ballot_sync(0xffffffffu, in && !good);
@@ -586,7 +624,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                 const unsigned long long k_at = pg * (unsigned long long)p.c.k_page + tk * (unsigned long long)p.c.k_token;
                 const unsigned long long v_at = pg * (unsigned long long)p.c.v_page + tk * (unsigned long long)p.c.v_token;
                 if (u + 1 < take) look_up(u + 1, page, at, in);
-#pragma unroll
+#pragma unroll 1
                 for (int side = 0; side < 2; ++side) {
                     if (!wait(&sh.empty[stage], ring_phase)) break;
                     if (side == 0 && lane == 0) {
@@ -660,6 +698,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             ++seg_n;
             if (x < t_end && ++t >= (seq.n + tt - 1) / tt) {
                 t = 0;
+#pragma unroll 1
                 for (;;) {  // the next sequence with a row
                     if (++s >= seqs) s = 0, ++hd;
                     const int y = s + lane;
@@ -678,76 +717,83 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
     } else if (warp >= K::kMma) {
         // ------------------------------------------------------------ matrix products
         if constexpr (K::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(K::kLess));
-        if (warp == K::kMma && lane == 0 && has_work) {
+        if (warp == K::kMma && has_work) {
             const uint32_t id_qk = tc5::idesc(K::kB16, kKeys, p.scale < 0.f, false);
             const uint32_t id_pv = tc5::idesc(K::kB16, 16 * k_steps, false, true);
+            const uint64_t q_desc = tc5::desc_sw128(q_base, 16, 1024), k_desc = tc5::desc_sw128(ring, 16, 1024),
+                           v_desc = tc5::desc_sw128(ring, kKeys * 128, 1024);
             int stage = 0;
-            uint32_t phase = 0;
-            uint32_t p_phase[2] = {0u, 0u};
+            uint32_t phase = 0, p_phase = 0;
             bool ok = true, last = false;
             auto wait = [&](uint64_t *bar, uint32_t parity) {
-                if (!ptx::mbar_wait(bar, parity, abort_flag, p.err, p.wait_ns)) ok = false;
+                if (!__all_sync(0xffffffffu, mbar_test(bar, parity))) ok = wait_on(bar, parity, abort_flag, p.err, p.wait_ns);
                 return ok;
             };
-            auto qk = [&](int x, int st) {
-                const uint64_t a = tc5::desc_sw128(q_base + x * K::kQBytes, 16, 1024);
-                const uint64_t b = tc5::desc_sw128(ring + st * K::kStageBytes, 16, 1024);
-                for (int ks = 0; ks < k_steps; ++ks)
-                    tc5::mma_ss(tmem + x * K::kSStep, a + (uint32_t)((ks >> 2) * (16384 >> 4) + (ks & 3) * 2),
-                                b + (uint32_t)((ks >> 2) * (kKeys * 128 >> 4) + (ks & 3) * 2), id_qk, ks > 0);
-                tc5::commit(&sh.s_full[x]);
-            };
-            auto pv = [&](int x, int st, bool more) {
-                const uint64_t b = tc5::desc_sw128(ring + st * K::kStageBytes, kKeys * 128, 1024);
-#pragma unroll
-                for (int ks = 0; ks < kKeys / 16; ++ks)
-                    tc5::mma_ts(tmem + K::kO + x * K::kOStep, tmem + x * K::kSStep + ks * 8, b + (uint32_t)(ks * (2048 >> 4)), id_pv,
-                                more || ks > 0);
-            };
+#pragma unroll 1
             for (int n = 0; ok && !last; ++n) {
                 const int qi = n % kQueue;
                 if (!wait(&sh.seg_full[qi], (uint32_t)(n / kQueue) & 1u)) break;
                 const int groups = kTiles == 1 || sh.segs[qi].rows <= 128 ? 1 : 2, count = sh.segs[qi].count;
                 last = sh.segs[qi].last;
-                ptx::mbar_arrive(&sh.seg_empty[qi]);
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&sh.seg_empty[qi]);
                 if (!wait(&sh.q_full, (uint32_t)n & 1u)) break;
-                auto next = [&](int &st) {  // the next tile of the ring
-                    st = stage;
-                    if (!wait(&sh.full[stage], phase)) return false;
-                    if (++stage == kStages) stage = 0, phase ^= 1u;
-                    return true;
-                };
-                int k_at, v_at;
-                if (!next(k_at)) break;
-                tc5::fence_after();
-                for (int x = 0; x < groups; ++x) qk(x, k_at);
-                tc5::commit(&sh.empty[k_at]);
-                if (count == 1) tc5::commit(&sh.q_empty);
-                for (int j = 0; j < count; ++j) {
-                    if (!next(v_at)) break;
+                // Step j: the values of unit j, then the keys of the next one, group after group.
+#pragma unroll 1
+                for (int j = -1; ok && j < count; ++j) {
+                    const bool values = j >= 0, keys = j + 1 < count;
+                    int v_at = 0, k_at = 0;
+                    if (values) {
+                        v_at = stage;
+                        if (!wait(&sh.full[stage], phase)) break;
+                        if (++stage == kStages) stage = 0, phase ^= 1u;
+                    }
+#pragma unroll 1
                     for (int x = 0; x < groups; ++x) {
-                        if (!wait(&sh.p_full[x], p_phase[x])) break;
-                        p_phase[x] ^= 1u;
-                        tc5::fence_after();
-                        pv(x, v_at, j > 0);
-                        if (x == groups - 1) tc5::commit(&sh.empty[v_at]);
-                        if (j == count - 1) {
-                            tc5::commit(&sh.o_full[x]);
-                        } else {
-                            if (x == 0 && !next(k_at)) break;
+                        const bool final = x == groups - 1;
+                        if (values) {
+                            if (!wait(&sh.p_full[x], (p_phase >> x) & 1u)) break;
+                            p_phase ^= 1u << x;
                             tc5::fence_after();
-                            qk(x, k_at);
-                            if (x == groups - 1) {
-                                tc5::commit(&sh.empty[k_at]);
-                                if (j == count - 2) tc5::commit(&sh.q_empty);
+                            const uint32_t d = tmem + K::kO + x * K::kOStep, a = tmem + x * K::kSStep;
+                            const uint64_t b = v_desc + (uint32_t)(v_at * (K::kStageBytes >> 4));
+                            if (elect()) {
+#pragma unroll
+                                for (int ks = 0; ks < kKeys / 16; ++ks)
+                                    tc5::mma_ts(d, a + ks * 8, b + (uint32_t)(ks * (2048 >> 4)), id_pv, j > 0 || ks > 0);
+                                if (final) tc5::commit(&sh.empty[v_at]);
+                                if (!keys) tc5::commit(&sh.o_full[x]);
                             }
+                            __syncwarp();
+                        }
+                        if (keys) {
+                            if (x == 0) {
+                                k_at = stage;
+                                if (!wait(&sh.full[stage], phase)) break;
+                                if (++stage == kStages) stage = 0, phase ^= 1u;
+                                tc5::fence_after();
+                            }
+                            const uint32_t d = tmem + x * K::kSStep;
+                            const uint64_t a = q_desc + (uint32_t)(x * (K::kQBytes >> 4)), b = k_desc + (uint32_t)(k_at * (K::kStageBytes >> 4));
+                            if (elect()) {
+#pragma unroll
+                                for (int ks = 0; ks < DT / 16; ++ks)
+                                    if (ks < k_steps)
+                                        tc5::mma_ss(d, a + (uint32_t)((ks >> 2) * (16384 >> 4) + (ks & 3) * 2),
+                                                    b + (uint32_t)((ks >> 2) * (kKeys * 128 >> 4) + (ks & 3) * 2), id_qk, ks > 0);
+                                tc5::commit(&sh.s_full[x]);
+                                if (final) {
+                                    tc5::commit(&sh.empty[k_at]);
+                                    if (j + 2 == count) tc5::commit(&sh.q_empty);
+                                }
+                            }
+                            __syncwarp();
                         }
                     }
-                    if (!ok) break;
                 }
             }
             if (!ok) {  // what has been issued comes to an end before tensor memory is given back
-                tc5::commit(&sh.drain);
+                if (elect()) tc5::commit(&sh.drain);
                 volatile int no_abort = 0;
                 ptx::mbar_wait(&sh.drain, 0u, &no_abort, nullptr, 200000000ull);
             }
@@ -764,9 +810,10 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
         int unit_n = 0;
         bool last = !has_work, ok = true, odd = false;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            if (!__all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort_flag, p.err, p.wait_ns))) ok = false;
+            if (!__all_sync(0xffffffffu, mbar_test(bar, parity))) ok = wait_on(bar, parity, abort_flag, p.err, p.wait_ns);
             return ok;
         };
+#pragma unroll 1
         for (int n = 0; ok && !last; ++n) {
             const int qi = n % kQueue;
             if (!wait(&sh.seg_full[qi], (uint32_t)(n / kQueue) & 1u)) break;
@@ -802,6 +849,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             Scores sc(p, k_scale);
             float m = kLowest, limit = kLowest;
             float2 l = make_float2(0.f, 0.f), lr = make_float2(0.f, 0.f);
+#pragma unroll 1
             for (int j = 0; j < g.count; ++j, ++unit_n) {
                 if (!wait(&sh.s_full[x], s_phase)) break;
                 s_phase ^= 1u;
@@ -967,17 +1015,19 @@ __device__ __forceinline__ Sums<K::kDim> join_parts(const Params &p, int first, 
     auto part = [&](int i) { return p.slots + (long long)(2 * (first + i) + (i == 0)) * K::kSlot + row * K::kPitch; };
 #pragma unroll
     for (int e = 0; e < r.kEach; ++e) r.o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
     for (int i = lane; i < parts; i += 32) r.m = fmaxf(r.m, __ldcg(part(i) + DT));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) r.m = fmaxf(r.m, __shfl_xor_sync(0xffffffffu, r.m, o));
     const float top = r.m == -INFINITY ? 0.f : r.m;
+#pragma unroll 1
     for (int i0 = 0; i0 < parts; i0 += 32) {
         float4 s = make_float4(-INFINITY, 0.f, 0.f, 0.f);
         if (i0 + lane < parts) s = __ldcg(reinterpret_cast<const float4 *>(part(i0 + lane) + DT));
         const float f = ex2(s.x - top);
         r.l += f * s.y, r.lr += f * s.z;
         const int here = min(32, parts - i0);
-#pragma unroll 8
+#pragma unroll 4
         for (int i = 0; i < here; ++i) {
             const float g = __shfl_sync(0xffffffffu, f, i);
             const float *from = part(i0 + i);
@@ -1027,6 +1077,7 @@ __device__ __noinline__ void one_row(const Params &p, const T *q, T *out, float 
         if (p.scale < 0.f) qv[e] = -qv[e];
         o[e] = 0.f;
     }
+#pragma unroll 1
     for (int j = lo; j < hi; ++j) {
         const bool pre = j < own0;
         const unsigned int y = pre ? j : j - own0, n = y / (unsigned int)p.c.page_size;
@@ -1102,6 +1153,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) finish_kernel(const __grid_co
     };
     const Cut c = p.cuts[cta];
     if (c.parts > 1 && cta + c.parts <= p.ctas)
+#pragma unroll 1
         for (int i = 0; i < kJoinRows / kJoinWarps; ++i) {
             const int r = r0 + i * kJoinWarps + warp, tk = r / gb, hh = r - tk * gb;
             if (r >= c.rows || hh >= c.heads) continue;
@@ -1121,18 +1173,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps) finish_kernel(const __grid_co
             if (spoilt(check)) again(c.seq, row, head, max(c.first + tk, 0));
         }
     if (!__syncthreads_or((int)threadIdx.x < p.ctas && p.odd[threadIdx.x])) return;
+#pragma unroll 1
     for (long long i = (long long)blockIdx.x * kJoinWarps + warp; i < (long long)p.rows * p.heads; i += (long long)gridDim.x * kJoinWarps) {
         const int row = (int)(i / p.heads), head = (int)(i % p.heads);
         const T *out = static_cast<const T *>(p.out) + (long long)row * p.o_row + head * p.o_head;
         float check = 0.f;
+#pragma unroll 1
         for (int d = lane; d < D; d += 32) check = fmaf((float)out[d], 0.f, check);
         if (!spoilt(check)) continue;
         bool cut = false;  // joined above, or being joined
+#pragma unroll 1
         for (int x = lane; x < p.ctas; x += 32) {
             const Cut y = p.cuts[x];
             cut |= y.parts > 1 && row >= y.q0 && row < y.q0 + y.rows / gb && head >= y.h0 && head < y.h0 + y.heads;
         }
         if (__any_sync(0xffffffffu, cut)) continue;
+#pragma unroll 1
         for (int b0 = 0; b0 < p.batch; b0 += 32) {
             Seq s{0, 0, 0, 0, 0};
             if (b0 + lane < p.batch) s = request(p, b0 + lane, false);
