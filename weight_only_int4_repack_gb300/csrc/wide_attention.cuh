@@ -110,16 +110,19 @@ struct Config {
 };
 
 constexpr int kQueue = 4;
-// A segment, as the loaders describe it to the other warps.
+// A segment, as the scheduling warp describes it to the others.
 struct Segment {
-    int rows;        // of the tile that are real
-    int q0;          // row of q of the tile's first token (requests)
-    int first;       // visible keys of the tile's first token; each further token sees one more (requests)
-    int total;       // keys of the sequence
-    int kvh, h0;     // kv head, first query head
-    int key0, count; // first key, units
-    int slot;        // where the sums go; -1: the tile is whole
-    int last;        // no segment follows
+    int rows, heads;     // of the tile that are real; heads of a token
+    int q0;              // row of q of the tile's first token (requests)
+    int first;           // visible keys of the tile's first token; each further token sees one more (requests)
+    int total;           // keys of the sequence
+    int kvh, h0;         // kv head, first query head
+    int key0, count;     // first key, units
+    int lo, hi;          // keys that some row sees
+    int own0;            // keys of the prefix in front of the request's own
+    const int32_t *own_pages, *pre_pages;
+    int slot;            // where the sums go; -1: the tile is whole
+    int last;            // no segment follows
 };
 
 template <int kRows>
@@ -258,8 +261,9 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
 __device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *abort_flag, unsigned int *err, uint64_t limit_ns) {
     uint64_t since = 0;
 #pragma unroll 1
-    for (;;) {
-        if (__all_sync(0xffffffffu, ptx::mbar_try_wait_sleep(bar, parity, 20000u))) return true;
+    for (int i = 0;; ++i) {
+        if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+        if ((i & 31) != 0) continue;
         const uint64_t now = ptx::globaltimer();
         if (since == 0) since = now;
         const bool over = now - since >= limit_ns;
@@ -268,6 +272,9 @@ __device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile
         if (__any_sync(0xffffffffu, over || *abort_flag)) return false;
     }
 }
+
+// The same value in all lanes, so that the compiler knows it.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // One lane of the warp, always the same: matrix instructions are issued by it, and the compiler knows that it is one.
 __device__ __forceinline__ bool elect() {
@@ -299,6 +306,12 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return r;
 }
 
+// A score in units of log2 is a raw product times this. A scale of 0 or below is in the queries (none, or negated); a unit
+// that is no normal number would be 0 times minus infinity where nothing is visible.
+__device__ __forceinline__ float unit_of(const Params &p, float k_scale) {
+    return fmaxf((p.scale != 0.f ? fabsf(p.scale) : 1.f) * k_scale * kLog2e, 1.2e-38f);
+}
+
 // How a raw product becomes a score, in units of log2.
 struct Scores {
     float unit;            // without a cap: score * log2(e) of a product
@@ -306,10 +319,8 @@ struct Scores {
     float slack;           // kSlack powers of two, as a difference of products
     bool capped;
     __device__ __forceinline__ Scores(const Params &p, float k_scale) {
-        // A scale of 0 or below is in the queries (none, or negated); a unit that is no normal number would be 0 times
-        // minus infinity where nothing is visible.
         const float to_score = (p.scale != 0.f ? fabsf(p.scale) : 1.f) * k_scale;
-        unit = fmaxf(to_score * kLog2e, 1.2e-38f);
+        unit = unit_of(p, k_scale);
         capped = p.softcap > 0.f;
         in = capped ? 2.f * kLog2e * to_score / p.softcap : 0.f;
         cap = p.softcap * kLog2e;
@@ -331,7 +342,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
     unsigned char *smem = reinterpret_cast<unsigned char *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     Sh &sh = *reinterpret_cast<Sh *>(smem + K::kAfter);
     volatile int *abort_flag = &sh.abort;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
     const int cta = blockIdx.x;
     const int D = p.c.head_dim;
 
@@ -339,7 +350,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
 #pragma unroll 1
         for (int i = 0; i < kStages; ++i) ptx::mbar_init(&sh.full[i], 4), ptx::mbar_init(&sh.empty[i], 1);
 #pragma unroll 1
-        for (int i = 0; i < kQueue; ++i) ptx::mbar_init(&sh.seg_full[i], 1), ptx::mbar_init(&sh.seg_empty[i], 4 * kTiles + 1);
+        for (int i = 0; i < kQueue; ++i) ptx::mbar_init(&sh.seg_full[i], 1), ptx::mbar_init(&sh.seg_empty[i], 4 * kTiles + 5);
 #pragma unroll 1
         for (int i = 0; i < 2; ++i)
             ptx::mbar_init(&sh.s_full[i], 1), ptx::mbar_init(&sh.p_full[i], 4), ptx::mbar_init(&sh.o_full[i], 1);
@@ -447,7 +458,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
     tc5::fence_before();
     __syncthreads();
     tc5::fence_after();
-    const uint32_t tmem = sh.tmem;
+    const uint32_t tmem = uniform(sh.tmem);
     const bool has_work = cta < active && sh.start_s >= 0;
     const uint32_t q_base = ptx::smem_u32(smem), ring = q_base + K::kRing;
     const int k_steps = (D + 15) / 16;
@@ -456,11 +467,8 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
         // ------------------------------------------------------------ loaders
         if constexpr (K::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(K::kLess));
         const int w = warp - K::kLoader;
-        if (w == 0 && lane == 0 && p.cuts) p.cuts[cta].parts = 0;
-        bool ok = has_work;
-        int s = sh.start_s, t = sh.start_t, hd = sh.start_hd;
-        int x = t_begin, base = sh.start_base;
-        int stage = 0, seg_n = 0, unit_n = 0;
+        bool ok = true, last = !has_work;
+        int stage = 0, unit_n = 0;
         uint32_t ring_phase = 1;  // of the empty barriers
         // Copies on their way, oldest first: the barriers that wait for them.
         constexpr int kLag = 2;
@@ -500,60 +508,22 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             return ok;
         };
 #pragma unroll 1
-        while (ok && x < t_end) {
-            const Seq seq = seq_of(s, false);
-            const Tile tile = tile_of<K>(p, seq, p.starts ? 0 : sh.least[s], tt, t);
-            const int from = x - base, take = min(tile.count - from, t_end - x);
-            const int kvh = hd / head_blocks, h0 = kvh * p.group + hd % head_blocks * gb;
-            const int heads_here = min(gb, (kvh + 1) * p.group - h0);
-            const bool begins = from == 0, ends = from + take == tile.count;
-            const int qi = seg_n % kQueue;
-            if (!wait(&sh.seg_empty[qi], (uint32_t)(seg_n / kQueue + 1) & 1u)) break;
-            int *members = sh.members[qi];
-            const int rows = tile.toks * gb;
-            if (!p.starts) {  // the requests of these ranks (every loader warp writes the same)
-                int rank = 0;
-#pragma unroll 1
-                for (int b0 = 0; b0 < p.batch && rank < tile.tok0 + tile.toks; b0 += 32) {
-                    const int b = b0 + lane;
-                    const bool in = b < p.batch && behind(p, b, s);
-                    const uint32_t mask = __ballot_sync(0xffffffffu, in);
-                    const int r = rank + __popc(mask & ((1u << lane) - 1u)) - tile.tok0;
-                    if (in && r >= 0 && r < tile.toks) members[r] = b;
-                    rank += __popc(mask);
-                }
-                __syncwarp();
-            }
-            int parts = 1;
-            if (begins && !ends) parts = (int)(((long long)(base + tile.count) * active - 1) / total_units) - cta + 1;
-            if (w == 0) {
-                if (lane == 0) {
-                    Segment g;
-                    g.rows = rows, g.q0 = seq.q0 + tile.tok0, g.first = tile.first, g.total = seq.total;
-                    g.kvh = kvh, g.h0 = h0, g.key0 = tile.key0 + from * kKeys, g.count = take;
-                    g.slot = begins && ends ? -1 : begins ? 2 * cta + 1 : 2 * cta;
-                    g.last = x + take >= t_end;
-                    sh.segs[qi] = g;
-                    if (p.cuts && begins && !ends) p.cuts[cta] = Cut{parts, rows, g.q0, h0, kvh, heads_here, s, tile.first};
-                }
-                if (!p.starts && begins)
-#pragma unroll 1
-                    for (int i = lane; i < tile.toks; i += 32)
-                        p.found[(long long)hd * p.batch + members[i]] = Found{ends ? -1 : cta, parts, i * gb, 0};
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&sh.seg_full[qi]);
-            }
+        for (int n = 0; ok && !last; ++n) {
+            const int qi = n % kQueue;
+            if (!wait(&sh.seg_full[qi], (uint32_t)(n / kQueue) & 1u)) break;
+            const Segment &g = sh.segs[qi];  // stays as it is until this warp has been counted at the segment's end
+            last = g.last;
             // Queries, in the order of the rows.
-            if (!wait(&sh.q_empty, (uint32_t)(seg_n + 1) & 1u)) break;
+            if (!wait(&sh.q_empty, (uint32_t)(n + 1) & 1u)) break;
             {
                 constexpr int kChunks = DT / 8, kLanes = kChunks < 32 ? kChunks : 32, kAt = 32 / kLanes;
-                const int c = lane % kLanes;
+                const int c = lane % kLanes, rows = g.rows;
 #pragma unroll 1
                 for (int r0 = w * (K::kRows / 4); r0 < (w + 1) * (K::kRows / 4) && r0 < (rows + 127) / 128 * 128; r0 += 32) {
                     const int r = r0 + lane, tk = r / gb, hh = r - tk * gb;
-                    const bool in = r < rows && hh < heads_here && p.scale != 0.f;
-                    const long long row = !in ? 0 : p.starts ? seq.q0 + tile.tok0 + tk : members[tk];
-                    const long long at = in ? row * p.q_row + (h0 + hh) * p.q_head : -1;
+                    const bool in = r < rows && hh < g.heads && p.scale != 0.f;
+                    const long long row = !in ? 0 : p.starts ? g.q0 + tk : sh.members[qi][tk];
+                    const long long at = in ? row * p.q_row + (g.h0 + hh) * p.q_head : -1;
 #pragma unroll 4
                     for (int i = 0; i < 32; i += kAt) {
                         const int rr = r0 + i + lane / kLanes;
@@ -595,20 +565,17 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                 else queue(&sh.q_full);
             }
             // Keys and values, unit after unit.
-            const int32_t *own_pages = p.starts ? p.table + (long long)s * p.table_stride : nullptr;
-            const int32_t *pre_pages = seq.pre >= 0 ? p.ptable + (long long)seq.pre * p.ptable_stride : nullptr;
-            const int own0 = p.starts ? seq.own0 : seq.total;  // keys of the prefix
             constexpr int kMine = kKeys / 4;  // rows of a warp
-            const int key_end = tile.hi;
+            const int take = g.count, kvh = g.kvh;
             auto look_up = [&](int u, int &page, int &at, bool &in) {
-                const int j = tile.key0 + (from + u) * kKeys + w * kMine + lane % kMine;
-                in = j >= tile.lo && j < key_end;
+                const int j = g.key0 + u * kKeys + w * kMine + lane % kMine, own0 = g.own0;
+                in = j >= g.lo && j < g.hi;
                 page = -1, at = 0;
                 if (in) {
                     const bool pre = j < own0;
                     const unsigned int y = pre ? j : j - own0, n = y / (unsigned int)p.c.page_size;
                     at = (int)(y - n * (unsigned int)p.c.page_size);
-                    page = __ldg((pre ? pre_pages : own_pages) + n);
+                    page = __ldg((pre ? g.pre_pages : g.own_pages) + n);
                 }
             };
             int page, at;
@@ -656,32 +623,37 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                         }
                         queue(&sh.full[stage]);
                     } else {
-                        constexpr int kChunks = DT / 16, kAt = 32 / kChunks, kSteps = kMine / kAt;
-                        const int c = lane % kChunks;
-                        uint4 y[kSteps];
+                        constexpr int kChunks = DT / 16, kAt = 32 / kChunks, kSteps = kMine / kAt, kOnce = kSteps < 4 ? kSteps : 4;
+                        const int c = lane % kChunks, r0 = lane / kChunks;
+                        const C *from = pool + c * 16;
+                        const uint32_t to = dst + (c >> 2) * (kKeys * 128) + (w * kMine + r0) * 128;
+                        const int c0 = (2 * c) & 7;
+#pragma unroll 1
+                        for (int i0 = 0; i0 < kSteps; i0 += kOnce) {
+                            uint4 y[kOnce];
 #pragma unroll
-                        for (int i = 0; i < kSteps; ++i) {
-                            const int r = i * kAt + lane / kChunks;
-                            const unsigned long long src = __shfl_sync(0xffffffffu, off, r);
-                            const bool there = ((real >> r) & 1u) && c * 16 < D;
-                            y[i] = there ? __ldg(reinterpret_cast<const uint4 *>(pool + src + c * 16)) : make_uint4(0, 0, 0, 0);
-                        }
+                            for (int i = 0; i < kOnce; ++i) {
+                                const int r = (i0 + i) * kAt + r0;
+                                const unsigned long long src = __shfl_sync(0xffffffffu, off, r);
+                                const bool there = ((real >> r) & 1u) && c * 16 < D;
+                                y[i] = there ? __ldg(reinterpret_cast<const uint4 *>(from + src)) : make_uint4(0, 0, 0, 0);
+                            }
 #pragma unroll
-                        for (int i = 0; i < kSteps; ++i) {
-                            const int row = w * kMine + i * kAt + lane / kChunks;
-                            uint32_t h[8];
-                            elem::e4m3x4_to_half2(y[i].x, h[0], h[1]);
-                            elem::e4m3x4_to_half2(y[i].y, h[2], h[3]);
-                            elem::e4m3x4_to_half2(y[i].z, h[4], h[5]);
-                            elem::e4m3x4_to_half2(y[i].w, h[6], h[7]);
-                            const uint32_t to = dst + (c >> 2) * (kKeys * 128) + row * 128;
-                            const int c0 = (2 * c) & 7;
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((c0 ^ (row & 7)) << 4)), "r"(h[0]),
-                                         "r"(h[1]), "r"(h[2]), "r"(h[3])
-                                         : "memory");
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((c0 + 1) ^ (row & 7)) << 4)),
-                                         "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7])
-                                         : "memory");
+                            for (int i = 0; i < kOnce; ++i) {
+                                const int at_row = (i0 + i) * kAt, turn = (at_row + r0) & 7;
+                                uint32_t h[8];
+                                elem::e4m3x4_to_half2(y[i].x, h[0], h[1]);
+                                elem::e4m3x4_to_half2(y[i].y, h[2], h[3]);
+                                elem::e4m3x4_to_half2(y[i].z, h[4], h[5]);
+                                elem::e4m3x4_to_half2(y[i].w, h[6], h[7]);
+                                const uint32_t row_to = to + at_row * 128;
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_to + ((c0 ^ turn) << 4)), "r"(h[0]),
+                                             "r"(h[1]), "r"(h[2]), "r"(h[3])
+                                             : "memory");
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_to + (((c0 + 1) ^ turn) << 4)), "r"(h[4]),
+                                             "r"(h[5]), "r"(h[6]), "r"(h[7])
+                                             : "memory");
+                            }
                         }
                         if (!K::kOwnPower) drain();  // the queries
                         signal(&sh.full[stage]);
@@ -692,32 +664,82 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                 ++unit_n;
             }
             if (!ok) break;
-            // The next tile.
-            x += take;
-            base = x;
-            ++seg_n;
-            if (x < t_end && ++t >= (seq.n + tt - 1) / tt) {
-                t = 0;
-#pragma unroll 1
-                for (;;) {  // the next sequence with a row
-                    if (++s >= seqs) s = 0, ++hd;
-                    const int y = s + lane;
-                    const bool some = y < seqs && (p.starts ? request(p, y, false).n > 0 : sh.counts[y] > 0);
-                    const uint32_t mask = __ballot_sync(0xffffffffu, some);
-                    if (mask) {
-                        s += __ffs(mask) - 1;
-                        break;
-                    }
-                    s += 31;
-                }
-            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sh.seg_empty[qi]);
         }
         drain();
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp >= K::kMma) {
-        // ------------------------------------------------------------ matrix products
+        // ------------------------------------------------------------ segments and matrix products
         if constexpr (K::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(K::kLess));
+        if (warp == K::kMma + 1) {
+            // -------------------------------------------------------- segments
+            if (lane == 0 && p.cuts) p.cuts[cta].parts = 0;
+            int s = sh.start_s, t = sh.start_t, hd = sh.start_hd, x = t_begin, base = sh.start_base;
+#pragma unroll 1
+            for (int n = 0; has_work && x < t_end; ++n) {
+                const Seq seq = seq_of(s, false);
+                const Tile tile = tile_of<K>(p, seq, p.starts ? 0 : sh.least[s], tt, t);
+                const int from = x - base, take = min(tile.count - from, t_end - x);
+                const int kvh = hd / head_blocks, h0 = kvh * p.group + hd % head_blocks * gb;
+                const bool begins = from == 0, ends = from + take == tile.count;
+                const int qi = n % kQueue;
+                if (!wait_on(&sh.seg_empty[qi], (uint32_t)(n / kQueue + 1) & 1u, abort_flag, p.err, p.wait_ns)) break;
+                int *members = sh.members[qi];
+                if (!p.starts) {  // the requests of these ranks
+                    int rank = 0;
+#pragma unroll 1
+                    for (int b0 = 0; b0 < p.batch && rank < tile.tok0 + tile.toks; b0 += 32) {
+                        const int b = b0 + lane;
+                        const bool in = b < p.batch && behind(p, b, s);
+                        const uint32_t mask = __ballot_sync(0xffffffffu, in);
+                        const int r = rank + __popc(mask & ((1u << lane) - 1u)) - tile.tok0;
+                        if (in && r >= 0 && r < tile.toks) members[r] = b;
+                        rank += __popc(mask);
+                    }
+                    __syncwarp();
+                }
+                int parts = 1;
+                if (begins && !ends) parts = (int)(((long long)(base + tile.count) * active - 1) / total_units) - cta + 1;
+                if (!p.starts && begins)
+#pragma unroll 1
+                    for (int i = lane; i < tile.toks; i += 32)
+                        p.found[(long long)hd * p.batch + members[i]] = Found{ends ? -1 : cta, parts, i * gb, 0};
+                if (lane == 0) {
+                    Segment &g = sh.segs[qi];
+                    g.rows = tile.toks * gb, g.heads = min(gb, (kvh + 1) * p.group - h0);
+                    g.q0 = seq.q0 + tile.tok0, g.first = tile.first, g.total = seq.total;
+                    g.kvh = kvh, g.h0 = h0, g.key0 = tile.key0 + from * kKeys, g.count = take;
+                    g.lo = tile.lo, g.hi = tile.hi, g.own0 = p.starts ? seq.own0 : seq.total;
+                    g.own_pages = p.table + (p.starts ? s * p.table_stride : 0);
+                    g.pre_pages = p.ptable + (seq.pre >= 0 ? seq.pre * p.ptable_stride : 0);
+                    g.slot = begins && ends ? -1 : begins ? 2 * cta + 1 : 2 * cta;
+                    g.last = x + take >= t_end;
+                    if (p.cuts && begins && !ends) p.cuts[cta] = Cut{parts, g.rows, g.q0, h0, kvh, g.heads, s, tile.first};
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&sh.seg_full[qi]);
+                x += take;
+                base = x;
+                if (x < t_end && ++t >= (seq.n + tt - 1) / tt) {
+                    t = 0;
+#pragma unroll 1
+                    for (;;) {  // the next sequence with a row
+                        if (++s >= seqs) s = 0, ++hd;
+                        const int y = s + lane;
+                        const bool some = y < seqs && (p.starts ? request(p, y, false).n > 0 : sh.counts[y] > 0);
+                        const uint32_t mask = __ballot_sync(0xffffffffu, some);
+                        if (mask) {
+                            s += __ffs(mask) - 1;
+                            break;
+                        }
+                        s += 31;
+                    }
+                }
+            }
+        }
         if (warp == K::kMma && has_work) {
+            // -------------------------------------------------------- matrix products
             const uint32_t id_qk = tc5::idesc(K::kB16, kKeys, p.scale < 0.f, false);
             const uint32_t id_pv = tc5::idesc(K::kB16, 16 * k_steps, false, true);
             const uint64_t q_desc = tc5::desc_sw128(q_base, 16, 1024), k_desc = tc5::desc_sw128(ring, 16, 1024),
@@ -733,8 +755,8 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             for (int n = 0; ok && !last; ++n) {
                 const int qi = n % kQueue;
                 if (!wait(&sh.seg_full[qi], (uint32_t)(n / kQueue) & 1u)) break;
-                const int groups = kTiles == 1 || sh.segs[qi].rows <= 128 ? 1 : 2, count = sh.segs[qi].count;
-                last = sh.segs[qi].last;
+                const int groups = kTiles == 1 || uniform(sh.segs[qi].rows) <= 128 ? 1 : 2, count = uniform(sh.segs[qi].count);
+                last = uniform(sh.segs[qi].last);
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&sh.seg_empty[qi]);
                 if (!wait(&sh.q_full, (uint32_t)n & 1u)) break;
@@ -817,12 +839,14 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
         for (int n = 0; ok && !last; ++n) {
             const int qi = n % kQueue;
             if (!wait(&sh.seg_full[qi], (uint32_t)(n / kQueue) & 1u)) break;
-            const Segment g = sh.segs[qi];
+            const Segment &g = sh.segs[qi];
             last = g.last;
+            const int count = g.count, key_first = g.key0, slot = g.slot, kvh = g.kvh;
             const int tk = row / gb, hh = row - tk * gb, head = g.h0 + hh;
-            const bool in = row < g.rows && head < (g.kvh + 1) * p.group;
+            const bool in = row < g.rows && hh < g.heads;
             const bool some = x * 128 + (warp & 3) * 32 < g.rows;  // the warp has a row
-            int b = 0, lo = 0, hi = 0;
+            const bool idle = x * 128 >= g.rows;                     // so has none of the group
+            int b = 0, lo = 0, hi = 0x7fffffff;  // rows that are none see everything, so that nothing has to be hidden for them
             if (in) {
                 if (p.starts) {
                     b = g.q0 + tk;
@@ -839,32 +863,31 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&sh.seg_empty[qi]);
             };
-            if (x * 128 >= g.rows) {  // nothing for this group
+            if (idle) {
                 done();
-                unit_n += g.count;
+                unit_n += count;
                 continue;
             }
-            float k_scale = K::k8 && p.c.k_scale ? p.c.k_scale[g.kvh] : 1.f;
-            float unit = 1.f, slack = 0.f;
-            Scores sc(p, k_scale);
+            float k_scale = K::k8 && p.c.k_scale ? p.c.k_scale[kvh] : 1.f, unit = 1.f, slack = 0.f;
             float m = kLowest, limit = kLowest;
             float2 l = make_float2(0.f, 0.f), lr = make_float2(0.f, 0.f);
 #pragma unroll 1
-            for (int j = 0; j < g.count; ++j, ++unit_n) {
+            for (int j = 0; j < count; ++j, ++unit_n) {
                 if (!wait(&sh.s_full[x], s_phase)) break;
                 s_phase ^= 1u;
                 tc5::fence_after();
                 if (j == 0) {
-                    if constexpr (K::kOwnPower) sc = Scores(p, k_scale * sh.powers[qi][row]);
-                    unit = sc.capped ? 1.f : sc.unit;
-                    slack = sc.capped ? kSlack : sc.slack;
+                    if constexpr (K::kOwnPower) k_scale *= sh.powers[qi][row];
+                    unit = p.softcap > 0.f ? 1.f : unit_of(p, k_scale);
+                    slack = kSlack / unit;
                     done();
                 }
                 if (some) {
-                    const int key0 = g.key0 + j * kKeys;
+                    const int key0 = key_first + j * kKeys;
                     const uint32_t *bad = sh.bad[unit_n & 7];
-                    const bool masked = __any_sync(0xffffffffu, lo > key0 || hi < key0 + kKeys) || (bad[0] | bad[1] | bad[2] | bad[3]);
-                    if (masked || sc.capped) {  // what is not a plain product goes back to where the products were
+                    const bool masked = __any_sync(0xffffffffu, lo > key0 || hi - kKeys < key0) || (bad[0] | bad[1] | bad[2] | bad[3]);
+                    if (masked || p.softcap > 0.f) {  // what is not a plain product goes back to where the products were
+                        const Scores sc(p, k_scale);
                         const unsigned int rel = (unsigned int)(key0 - lo), span = (unsigned int)max(hi - lo, 0);
 #pragma unroll 1
                         for (int c = 0; c < kKeys / 32; ++c) {
@@ -942,14 +965,14 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             o_phase ^= 1u;
             tc5::fence_after();
             if (!some) continue;
-            const float v_scale = K::k8 && p.c.v_scale ? p.c.v_scale[g.kvh] : 1.f;
+            const float v_scale = K::k8 && p.c.v_scale ? p.c.v_scale[kvh] : 1.f;
             const float sum = l.x + l.y, cut = lr.x + lr.y;
             const bool any = sum > 0.f || sum != sum;
-            const bool direct = g.slot < 0 && p.starts;
+            const bool direct = slot < 0 && p.starts;
             const float f = !direct ? 1.f : any ? v_scale / cut : 0.f;
             float *sums = nullptr;
             if (!direct)
-                sums = g.slot >= 0 ? p.slots + (long long)g.slot * K::kSlot + row * K::kPitch
+                sums = slot >= 0 ? p.slots + (long long)slot * K::kSlot + row * K::kPitch
                                    : p.whole + ((long long)b * p.heads + head) * K::kPitch;
             T *out = static_cast<T *>(p.out) + (long long)b * p.o_row + head * p.o_head;
             float check = 0.f;
