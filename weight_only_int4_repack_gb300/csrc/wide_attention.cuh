@@ -132,7 +132,7 @@ struct Shared {
     float powers[kQueue][kRows];                    // what a row's scores have to be multiplied by (kOwnPower)
     uint32_t bad[8][4];                             // keys of a unit whose page is none
     Segment segs[kQueue];
-    uint64_t full[8], empty[8], seg_full[kQueue], seg_empty[kQueue], s_full[2], p_full[2], o_full[2], q_full, q_empty, drain;
+    uint64_t full[8], empty[8], seg_full[kQueue], seg_empty[kQueue], s_full[2], p_half[2], p_full[2], o_full[2], q_full, q_empty, drain;
     int sums[32];
     int start_s, start_t, start_hd, start_base, tiles;
     uint32_t tmem;
@@ -306,6 +306,19 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return r;
 }
 
+// The two halves of a pair of operands added to a pair of sums.
+template <bool kB16>
+__device__ __forceinline__ void add_pair(float2 &sum, uint32_t pair) {
+    if constexpr (kB16)
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.rn.f32.bf16 %0, a, %0;\n\tadd.rn.f32.bf16 %1, b, %1;\n\t}"
+            : "+f"(sum.x), "+f"(sum.y)
+            : "r"(pair));
+    else
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.rn.f32.f16 %0, a, %0;\n\tadd.rn.f32.f16 %1, b, %1;\n\t}"
+            : "+f"(sum.x), "+f"(sum.y)
+            : "r"(pair));
+}
+
 // A score in units of log2 is a raw product times this. A scale of 0 or below is in the queries (none, or negated); a unit
 // that is no normal number would be 0 times minus infinity where nothing is visible.
 __device__ __forceinline__ float unit_of(const Params &p, float k_scale) {
@@ -353,7 +366,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
         for (int i = 0; i < kQueue; ++i) ptx::mbar_init(&sh.seg_full[i], 1), ptx::mbar_init(&sh.seg_empty[i], 4 * kTiles + 5);
 #pragma unroll 1
         for (int i = 0; i < 2; ++i)
-            ptx::mbar_init(&sh.s_full[i], 1), ptx::mbar_init(&sh.p_full[i], 4), ptx::mbar_init(&sh.o_full[i], 1);
+            ptx::mbar_init(&sh.s_full[i], 1), ptx::mbar_init(&sh.p_half[i], 4), ptx::mbar_init(&sh.p_full[i], 4), ptx::mbar_init(&sh.o_full[i], 1);
         ptx::mbar_init(&sh.q_full, 4), ptx::mbar_init(&sh.q_empty, 1), ptx::mbar_init(&sh.drain, 1);
         sh.abort = 0, sh.odd = 0, sh.start_s = -1;
         ptx::mbar_init_fence();
@@ -774,15 +787,23 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                     for (int x = 0; x < groups; ++x) {
                         const bool final = x == groups - 1;
                         if (values) {
-                            if (!wait(&sh.p_full[x], (p_phase >> x) & 1u)) break;
-                            p_phase ^= 1u << x;
+                            if (!wait(&sh.p_half[x], (p_phase >> x) & 1u)) break;
                             tc5::fence_after();
                             const uint32_t d = tmem + K::kO + x * K::kOStep, a = tmem + x * K::kSStep;
                             const uint64_t b = v_desc + (uint32_t)(v_at * (K::kStageBytes >> 4));
                             if (elect()) {
 #pragma unroll
-                                for (int ks = 0; ks < kKeys / 16; ++ks)
+                                for (int ks = 0; ks < kKeys / 32; ++ks)
                                     tc5::mma_ts(d, a + ks * 8, b + (uint32_t)(ks * (2048 >> 4)), id_pv, j > 0 || ks > 0);
+                            }
+                            __syncwarp();
+                            if (!wait(&sh.p_full[x], (p_phase >> x) & 1u)) break;
+                            p_phase ^= 1u << x;
+                            tc5::fence_after();
+                            if (elect()) {
+#pragma unroll
+                                for (int ks = kKeys / 32; ks < kKeys / 16; ++ks)
+                                    tc5::mma_ts(d, a + ks * 8, b + (uint32_t)(ks * (2048 >> 4)), id_pv, 1u);
                                 if (final) tc5::commit(&sh.empty[v_at]);
                                 if (!keys) tc5::commit(&sh.o_full[x]);
                             }
@@ -869,7 +890,8 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                 continue;
             }
             float k_scale = K::k8 && p.c.k_scale ? p.c.k_scale[kvh] : 1.f, unit = 1.f, slack = 0.f;
-            float m = kLowest, limit = kLowest;
+            float m = kLowest, limit = kLowest, shift = 0.f;
+            bool far = false;
             float2 l = make_float2(0.f, 0.f), lr = make_float2(0.f, 0.f);
 #pragma unroll 1
             for (int j = 0; j < count; ++j, ++unit_n) {
@@ -907,18 +929,28 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                         tc5::wait_st();
                     }
                     uint32_t v[kKeys / 32][32];
-#pragma unroll
-                    for (int c = 0; c < kKeys / 32; ++c) tc5::ld32(t_s + c * 32, v[c]);
-                    tc5::wait_ld();
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int c = 0; c < kKeys / 32; ++c)
+                    auto tops = [&](int c) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 2)
                             top[i / 2 & 3] = fmaxf(top[i / 2 & 3], fmaxf(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1])));
+                    };
+                    constexpr int kHalf = kKeys / 64;
+#pragma unroll
+                    for (int c = 0; c < kHalf; ++c) tc5::ld32(t_s + c * 32, v[c]);
+                    tc5::wait_ld();
+#pragma unroll
+                    for (int c = kHalf; c < 2 * kHalf; ++c) tc5::ld32(t_s + c * 32, v[c]);
+#pragma unroll
+                    for (int c = 0; c < kHalf; ++c) tops(c);
+                    tc5::wait_ld();
+#pragma unroll
+                    for (int c = kHalf; c < 2 * kHalf; ++c) tops(c);
                     const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     if (__any_sync(0xffffffffu, mx > limit)) {
-                        const float y = fmaxf(m, mx), keep = ex2((m - y) * unit);
+                        const float y = fmaxf(m, mx), far_y = y * unit, up = fmaf(-y, unit, K::kUp);
+                        far = __any_sync(0xffffffffu, fabsf(far_y) >= 1024.f && y > kLowest);
+                        const float keep = far ? ex2((m - y) * unit) : ex2(up - shift);
                         if (j > 0) {
 #pragma unroll 1
                             for (int c = 0; c < (D + 15) / 16; ++c) {
@@ -931,30 +963,53 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                             }
                         }
                         l.x *= keep, l.y *= keep, lr.x *= keep, lr.y *= keep;
-                        m = y, limit = y + slack;
+                        m = y, limit = y + slack, shift = up;
                     }
-                    // Weights 2^((s - m) unit + kUp): differences first, so that however large scores are the reference's weight is
-                    // right. They are cut to the operands' precision, not rounded to it: what that takes from all of them
-                    // alike cancels in the quotient by the sum of the cut ones, and what is left is as small as after rounding.
-                    const float2 neg = make_float2(-m, -m), by = make_float2(unit, unit), up = make_float2(K::kUp, K::kUp);
-                    constexpr uint32_t kCut = K::kB16 ? 0xffff0000u : 0xffffe000u;
+                    // Weights are 2^(s unit + shift), 2^kUp at the reference; the shift's rounding is in all of them alike and in
+                    // the shift that is kept. Where scores are so large that it could be seen, differences are taken first.
+                    float by = unit, up = shift;
+                    if (far) {
+#pragma unroll 1
+                        for (int c = 0; c < kKeys / 32; ++c) {
+                            uint32_t z[32];
+                            tc5::ld32(t_s + c * 32, z);
+                            tc5::wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) z[i] = __float_as_uint((__uint_as_float(z[i]) - m) * unit);
+                            tc5::st32(t_s + c * 32, z);
+                        }
+                        tc5::wait_st();
+#pragma unroll
+                        for (int c = 0; c < 2 * kHalf; ++c) tc5::ld32(t_s + c * 32, v[c]);
+                        tc5::wait_ld();
+                        by = 1.f, up = K::kUp;
+                    }
+                    // Rounded to the operands' type; outputs are divided by the sum of the rounded ones, so that they are a mean of
+                    // the values.
+                    const float2 by2 = make_float2(by, by), up2 = make_float2(up, up);
 #pragma unroll
                     for (int c = 0; c < kKeys / 32; ++c) {
                         uint32_t h[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             float2 s = make_float2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1]));
-                            s = fma2(add2(s, neg), by, up);
+                            s = fma2(s, by2, up2);
                             s.x = ex2(s.x), s.y = ex2(s.y);
                             l = add2(l, s);
-                            s.x = __uint_as_float(__float_as_uint(s.x) & kCut), s.y = __uint_as_float(__float_as_uint(s.y) & kCut);
-                            lr = add2(lr, s);
-                            if constexpr (K::kB16) h[i] = __byte_perm(__float_as_uint(s.x), __float_as_uint(s.y), 0x7632);
-                            else h[i] = elem::pair_from_f32<__half>(s.x, s.y);
+                            h[i] = elem::pair_from_f32<typename K::M>(s.x, s.y);
+                            add_pair<K::kB16>(lr, h[i]);
                         }
                         tc5::st16(t_s + c * 16, h);
+                        if (c == kHalf - 1) {  // the first half of the product with the values can begin
+                            tc5::wait_st();
+                            tc5::fence_before();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(&sh.p_half[x]);
+                        }
                     }
                     tc5::wait_st();
+                } else if (lane == 0) {
+                    ptx::mbar_arrive(&sh.p_half[x]);
                 }
                 tc5::fence_before();
                 __syncwarp();
@@ -1006,9 +1061,9 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                 if (direct) {
                     odd |= check != check;
                     if (p.lse)
-                        p.lse[(long long)b * p.heads + head] = any ? (m * unit + log2f(sum) - K::kUp) / kLog2e : -INFINITY;
+                        p.lse[(long long)b * p.heads + head] = any ? (log2f(sum) - shift) / kLog2e : -INFINITY;
                 } else {
-                    *reinterpret_cast<float4 *>(sums + DT) = make_float4(any ? m * unit : -INFINITY, sum, cut, 0.f);
+                    *reinterpret_cast<float4 *>(sums + DT) = make_float4(any ? -shift : -INFINITY, sum, cut, 0.f);
                 }
             }
         }
@@ -1192,7 +1247,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) finish_kernel(const __grid_co
                 if (d < D) store4(out + d, make_float4(x.o[e].x * f, x.o[e].y * f, x.o[e].z * f, x.o[e].w * f), &check);
             }
             if (p.lse && lane == 0)
-                p.lse[(long long)row * p.heads + head] = any ? (x.m + log2f(x.l) - K::kUp) / kLog2e : -INFINITY;
+                p.lse[(long long)row * p.heads + head] = any ? (x.m + log2f(x.l)) / kLog2e : -INFINITY;
             if (spoilt(check)) again(c.seq, row, head, max(c.first + tk, 0));
         }
     if (!__syncthreads_or((int)threadIdx.x < p.ctas && p.odd[threadIdx.x])) return;
@@ -1260,7 +1315,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
     }
     const float own_lse = own > 0 ? p.raw_lse[i] : -INFINITY;
     const bool any = x.l > 0.f || x.l != x.l, any_own = !(own_lse == -INFINITY);
-    const float a = any ? x.m + log2f(x.l) - K::kUp : -INFINITY;
+    const float a = any ? x.m + log2f(x.l) : -INFINITY;
     const float top = fmaxf(a, own_lse), from = top == -INFINITY ? 0.f : top;
     const float wa = any ? ex2(a - from) : 0.f, wo = any_own ? ex2(own_lse - from) : 0.f;
     const float sum = wa + wo, f = any ? wa / sum * (K::k8 && p.c.v_scale ? p.c.v_scale[kvh] : 1.f) / x.lr : 0.f;
