@@ -69,7 +69,7 @@ w4a16_status check(const void *q, w4a16_type type, long long q_row, long long q_
     const int group = heads / cache->kv_heads, most = wide::rows_of(cache->head_dim), block = group < most ? group : most;
     const long long seqs = prefixes_only ? prefixes : batch;
     const long long tiles = rows / (most / block) + seqs, hds = (long long)(group + block - 1) / block * cache->kv_heads;
-    if (tiles * hds > INT_MAX / (keys / wide::keys_of(cache->head_dim) + 2)) return W4A16_ERR_UNSUPPORTED;
+    if (tiles * hds > INT_MAX / (keys / wide::keys_of(cache->head_dim) + 2 + wide::kOver)) return W4A16_ERR_UNSUPPORTED;
     *nothing = rows == 0 || batch == 0;
     if (*nothing) return W4A16_OK;
     if (!q || !out || !table || !lens || (prefixes > 0 && (!ptable || !plens || !pof))) return W4A16_ERR_INVALID_ARG;
@@ -118,6 +118,7 @@ w4a16_status w4a16_prompt_attention(const void *q, w4a16_type type, long long q_
     p.cuts = reinterpret_cast<wide::Cut *>(at + l.cuts);
     p.odd = reinterpret_cast<int *>(at + l.odd);
     p.slots = reinterpret_cast<float *>(at + l.slots);
+    p.wide_out = aligned(out, 32) && o_row % 16 == 0 && o_head % 16 == 0;
     p.ctas = ctas(), p.err = device_error_ptr(), p.wait_ns = wait_limit_ns();
     if (!p.err) return W4A16_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
@@ -161,6 +162,7 @@ w4a16_status w4a16_prefix_attention(const void *q, w4a16_type type, long long q_
     p.found = reinterpret_cast<wide::Found *>(at + l.found);
     p.whole = reinterpret_cast<float *>(at + l.whole);
     p.raw = reinterpret_cast<float *>(at + l.raw), p.raw_lse = reinterpret_cast<float *>(at + l.raw_lse);
+    p.wide_out = aligned(out, 32) && o_row % 16 == 0 && o_head % 16 == 0;
     p.ctas = ctas(), p.err = device_error_ptr(), p.wait_ns = wait_limit_ns();
     if (!p.err) return W4A16_ERR_CUDA;
     // The requests' own tokens: paged attention, whose sums go into the workspace.

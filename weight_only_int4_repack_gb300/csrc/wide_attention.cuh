@@ -71,6 +71,7 @@ struct Params {
     const float *raw, *raw_lse;  // prefixes: the requests' own tokens, [batch * heads][head_dim] and log2 of the sums
     int *odd;           // [CTAs]: whether a CTA has written something that is no finite number
     int ctas;
+    int wide_out;       // rows of out are 32-byte aligned
     unsigned int *err;
     unsigned long long wait_ns;
 };
@@ -91,6 +92,7 @@ struct Config {
     static constexpr int kTiles = DT > 128 ? 1 : 2;       // groups of 128 rows
     static constexpr int kRows = 128 * kTiles;
     static constexpr int kKeys = DT > 128 ? 64 : 128;     // of a unit
+    static constexpr int kAhead = DT > 128 ? 2 : 1;       // units whose scores fit beside the outputs
     static constexpr int kStageBytes = kKeys * DT * 2;    // keys or values of a unit
     static constexpr int kStages = DT == 64 ? 8 : 4;
     static constexpr int kQBytes = 128 * DT * 2;          // queries of a group
@@ -98,18 +100,20 @@ struct Config {
     static constexpr int kAfter = kRing + kStages * kStageBytes;
     static constexpr int kPitch = DT + 8;                 // floats of a row of sums: outputs, then m, l, l as rounded
     static constexpr int kSlot = kRows * kPitch;
-    // Tensor memory: a group's scores (its weights take their place) and outputs.
-    static constexpr int kO = 256, kOStep = 128, kSStep = 128;
+    // Tensor memory: kAhead units' scores of each group (weights take their place), and its outputs.
+    static constexpr int kO = 256, kOStep = 128, kSStep = 128, kSBuffer = 64;
+    static_assert(kAhead * kKeys <= kSStep, "scores lie in front of the outputs");
     static constexpr int kWarps = 4 * kTiles + 8, kThreads = 32 * kWarps;
     static constexpr int kLoader = 4 * kTiles, kMma = kLoader + 4;  // first warps of the roles
-    // Registers: with two groups of rows the loaders and the issuing warps leave some of theirs to them
-    // (256 threads at 184 and 256 at 72 are the 65536 that 512 threads get at 128).
+    // Registers: where a row's 128 scores are in them, the loaders and the issuing warps leave some of theirs to the rows'
+    // warps (256 threads at 184 and 256 at 72 are the 65536 that 512 threads get at 128).
     static constexpr bool kSplit = kTiles == 2;
     static constexpr int kMore = 184, kLess = 72;
     static_assert(kMore + kLess == 256, "as many registers as there are");
 };
 
 constexpr int kQueue = 4;
+constexpr int kOver = 2;
 // A segment, as the scheduling warp describes it to the others.
 struct Segment {
     int rows, heads;     // of the tile that are real; heads of a token
@@ -130,11 +134,11 @@ struct Shared {
     int counts[kMaxPrefixes], least[kMaxPrefixes];  // of each prefix: requests, shortest own length
     int members[kQueue][kRows];                     // requests of a tile (prefixes)
     float powers[kQueue][kRows];                    // what a row's scores have to be multiplied by (kOwnPower)
-    uint32_t bad[8][4];                             // keys of a unit whose page is none
+    uint32_t bad[16][4];                            // keys of a unit whose page is none
     Segment segs[kQueue];
-    uint64_t full[8], empty[8], seg_full[kQueue], seg_empty[kQueue], s_full[2], p_half[2], p_full[2], o_full[2], q_full, q_empty, drain;
+    uint64_t full[12], empty[12], seg_full[kQueue], seg_empty[kQueue], s_full[2][2], p_half[2], p_full[2][2], o_step[2], o_full[2], q_full, q_empty, drain;
     int sums[32];
-    int start_s, start_t, start_hd, start_base, tiles;
+    int start_s, start_t, start_hd, start_base, tiles, work;
     uint32_t tmem;
     int abort, odd;
 };
@@ -261,9 +265,7 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
 __device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *abort_flag, unsigned int *err, uint64_t limit_ns) {
     uint64_t since = 0;
 #pragma unroll 1
-    for (int i = 0;; ++i) {
-        if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
-        if ((i & 31) != 0) continue;
+    while (!__all_sync(0xffffffffu, ptx::mbar_try_wait_sleep(bar, parity, 20000u))) {
         const uint64_t now = ptx::globaltimer();
         if (since == 0) since = now;
         const bool over = now - since >= limit_ns;
@@ -271,10 +273,11 @@ __device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile
         if (over) *abort_flag = 1;
         if (__any_sync(0xffffffffu, over || *abort_flag)) return false;
     }
+    return true;
 }
 
 // The same value in all lanes, so that the compiler knows it.
-__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ int uniform(int x) { return (int)__reduce_or_sync(0xffffffffu, (unsigned)x); }
 
 // One lane of the warp, always the same: matrix instructions are issued by it, and the compiler knows that it is one.
 __device__ __forceinline__ bool elect() {
@@ -366,9 +369,11 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
         for (int i = 0; i < kQueue; ++i) ptx::mbar_init(&sh.seg_full[i], 1), ptx::mbar_init(&sh.seg_empty[i], 4 * kTiles + 5);
 #pragma unroll 1
         for (int i = 0; i < 2; ++i)
-            ptx::mbar_init(&sh.s_full[i], 1), ptx::mbar_init(&sh.p_half[i], 4), ptx::mbar_init(&sh.p_full[i], 4), ptx::mbar_init(&sh.o_full[i], 1);
+            ptx::mbar_init(&sh.p_half[i], 4), ptx::mbar_init(&sh.o_step[i], 1), ptx::mbar_init(&sh.o_full[i], 1);
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) ptx::mbar_init(&sh.s_full[i >> 1][i & 1], 1), ptx::mbar_init(&sh.p_full[i >> 1][i & 1], 4);
         ptx::mbar_init(&sh.q_full, 4), ptx::mbar_init(&sh.q_empty, 1), ptx::mbar_init(&sh.drain, 1);
-        sh.abort = 0, sh.odd = 0, sh.start_s = -1;
+        sh.abort = 0, sh.odd = 0, sh.work = 0;
         ptx::mbar_init_fence();
     }
     if (warp == K::kMma) tc5::alloc(&sh.tmem, 512);
@@ -417,7 +422,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
     }
     __syncthreads();
     int total_units = 0, t_begin = 0, t_end = 0;  // below 2^31: the host has seen to that
-    int active;
+    int active, over;
     {
         const int tiles = sh.tiles;
         const int per = (tiles + K::kThreads - 1) / K::kThreads, i0 = min(tid * per, tiles), i1 = min(i0 + per, tiles);
@@ -443,13 +448,17 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             while (i >= plan_off[s + 1]) ++s;
             mine += units_of(s, i);
         }
-        const int before = scan<K::kWarps>(mine, sh.sums, &per_hd);
+        int before = scan<K::kWarps>(mine, sh.sums, &per_hd);
+        // A tile costs about as much as kOver units besides (queries, a first and a last unit that nothing overlaps,
+        // outputs): where CTAs have several tiles the line counts them, in front of the tile's own units.
+        over = per_hd * hds >= 8 * (int)gridDim.x ? kOver : 0;
+        before += over * i0, mine += over * (i1 - i0), per_hd += over * tiles;
         total_units = per_hd * hds;
         active = min((int)gridDim.x, total_units);
         if (cta < active) {
-            const int each = total_units / active, over = total_units - each * active;
-            t_begin = each * cta + over * cta / active;
-            t_end = each * (cta + 1) + over * (cta + 1) / active;
+            const int each = total_units / active, rest = total_units - each * active;
+            t_begin = each * cta + rest * cta / active;
+            t_end = each * (cta + 1) + rest * (cta + 1) / active;
             const int hd = t_begin / per_hd, rem = t_begin - hd * per_hd;
             if (rem >= before && rem < before + mine) {
                 int at = before;
@@ -457,10 +466,11 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                 for (int i = i0, s = s_first; i < i1; ++i) {
 #pragma unroll 1
                     while (i >= plan_off[s + 1]) ++s;
-                    const int n = units_of(s, i);
+                    const int n = units_of(s, i) + over;
                     if (rem < at + n) {
-                        sh.start_s = s, sh.start_t = i - plan_off[s], sh.start_hd = hd;
-                        sh.start_base = t_begin - rem + at;
+                        const int base = t_begin - rem + at, end = min(base + n, t_end);
+                        sh.start_s = s, sh.start_t = i - plan_off[s], sh.start_hd = hd, sh.start_base = base;
+                        sh.work = end > max(t_begin, base + over) || t_end - (base + n) > over;
                         break;
                     }
                     at += n;
@@ -472,7 +482,8 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
     __syncthreads();
     tc5::fence_after();
     const uint32_t tmem = uniform(sh.tmem);
-    const bool has_work = cta < active && sh.start_s >= 0;
+    const int gb_inv = (65535 + gb) / gb;  // x * gb_inv >> 16 is x / gb for all rows of a tile
+    const bool has_work = cta < active && sh.work;
     const uint32_t q_base = ptx::smem_u32(smem), ring = q_base + K::kRing;
     const int k_steps = (D + 15) / 16;
 
@@ -533,14 +544,19 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                 const int c = lane % kLanes, rows = g.rows;
 #pragma unroll 1
                 for (int r0 = w * (K::kRows / 4); r0 < (w + 1) * (K::kRows / 4) && r0 < (rows + 127) / 128 * 128; r0 += 32) {
-                    const int r = r0 + lane, tk = r / gb, hh = r - tk * gb;
+                    const int r = r0 + lane, tk = r * gb_inv >> 16, hh = r - tk * gb;
                     const bool in = r < rows && hh < g.heads && p.scale != 0.f;
                     const long long row = !in ? 0 : p.starts ? g.q0 + tk : sh.members[qi][tk];
                     const long long at = in ? row * p.q_row + (g.h0 + hh) * p.q_head : -1;
-#pragma unroll 4
-                    for (int i = 0; i < 32; i += kAt) {
-                        const int rr = r0 + i + lane / kLanes;
-                        const long long src = __shfl_sync(0xffffffffu, at, i + lane / kLanes);
+#pragma unroll 1
+                    for (int i0 = 0; i0 < 32; i0 += 4 * kAt) {
+                      long long srcs[4];  // the rows' places first: copies and shuffles stay in their order
+#pragma unroll
+                      for (int z = 0; z < 4; ++z) srcs[z] = __shfl_sync(0xffffffffu, at, i0 + z * kAt + lane / kLanes);
+#pragma unroll
+                      for (int z = 0; z < 4; ++z) {
+                        const int rr = r0 + i0 + z * kAt + lane / kLanes;
+                        const long long src = srcs[z];
                         const bool real = src >= 0 && c * 8 < D;
                         const T *from = static_cast<const T *>(p.q) + (real ? src + c * 8 : 0);
                         const uint32_t to = q_base + (rr >> 7) * K::kQBytes + (c >> 3) * 16384 + (rr & 127) * 128 + (((c & 7) ^ (rr & 7)) << 4);
@@ -550,11 +566,11 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                             // To fp16, after a power of two that brings the row's largest below 2: what that loses is 2^-25
                             // of the largest.
                             const uint4 y = real ? *reinterpret_cast<const uint4 *>(from) : make_uint4(0, 0, 0, 0);
-                            const uint32_t z[4] = {y.x, y.y, y.z, y.w};
+                            const uint32_t w4[4] = {y.x, y.y, y.z, y.w};
                             float big = 0.f;
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const float2 f = elem::pair_to_f32<T>(z[e]);
+                                const float2 f = elem::pair_to_f32<T>(w4[e]);
                                 big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
                             }
 #pragma unroll
@@ -564,7 +580,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                             uint32_t h[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const float2 f = elem::pair_to_f32<T>(z[e]);
+                                const float2 f = elem::pair_to_f32<T>(w4[e]);
                                 h[e] = elem::pair_from_f32<__half>(f.x * down, f.y * down);
                             }
                             if (c == 0) sh.powers[qi][rr] = ldexpf(1.f, e2);
@@ -572,6 +588,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                                 asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
                                              : "memory");
                         }
+                      }
                     }
                 }
                 if constexpr (K::kOwnPower) signal(&sh.q_full);
@@ -580,6 +597,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             // Keys and values, unit after unit.
             constexpr int kMine = kKeys / 4;  // rows of a warp
             const int take = g.count, kvh = g.kvh;
+            const bool blocks = p.c.page_size % 16 == 0 && g.own0 % 16 == 0 && D == DT;  // 16 keys lie in one page
             auto look_up = [&](int u, int &page, int &at, bool &in) {
                 const int j = g.key0 + u * kKeys + w * kMine + lane % kMine, own0 = g.own0;
                 in = j >= g.lo && j < g.hi;
@@ -591,28 +609,39 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                     page = __ldg((pre ? g.pre_pages : g.own_pages) + n);
                 }
             };
+            // Keys run kAhead units ahead of the values, as the products that need them do. A unit's places are looked up when its
+            // keys are brought, and kept for its values.
             int page, at;
             bool in;
             look_up(0, page, at, in);
+            unsigned long long v_off[K::kAhead + 1] = {};
+            uint32_t v_rows[K::kAhead + 1] = {};
 #pragma unroll 1
-            for (int u = 0; u < take; ++u) {
-                const bool good = in && page >= 0 && page < p.c.pages;
-                const uint32_t bad = __ballot_sync(0xffffffffu, in && !good);
-                if (bad && in && !good) atomicExch(p.err, (unsigned int)W4A16_ERR_INVALID_ARG);
-                const uint32_t real = __ballot_sync(0xffffffffu, good);
-                const unsigned long long pg = good ? page : 0, tk = good ? at : 0;
-                const unsigned long long k_at = pg * (unsigned long long)p.c.k_page + tk * (unsigned long long)p.c.k_token;
-                const unsigned long long v_at = pg * (unsigned long long)p.c.v_page + tk * (unsigned long long)p.c.v_token;
-                if (u + 1 < take) look_up(u + 1, page, at, in);
+            for (int u = 0; ok && u < take + K::kAhead; ++u) {
+                unsigned long long k_off = 0;
+                uint32_t k_rows = 0, bad = 0;
+                if (u < take) {
+                    const bool good = in && page >= 0 && page < p.c.pages;
+                    bad = __ballot_sync(0xffffffffu, in && !good);
+                    if (bad && in && !good) atomicExch(p.err, (unsigned int)W4A16_ERR_INVALID_ARG);
+                    k_rows = __ballot_sync(0xffffffffu, good);
+                    const unsigned long long pg = good ? page : 0, tk = good ? at : 0;
+                    k_off = pg * (unsigned long long)p.c.k_page + tk * (unsigned long long)p.c.k_token;
+                    v_off[K::kAhead] = pg * (unsigned long long)p.c.v_page + tk * (unsigned long long)p.c.v_token;
+                    v_rows[K::kAhead] = k_rows;
+                    if (u + 1 < take) look_up(u + 1, page, at, in);
+                }
 #pragma unroll 1
-                for (int side = 0; side < 2; ++side) {
+                for (int side = 0; side < 2; ++side) {  // keys of unit u, values of unit u - kAhead
+                    if (side ? u < K::kAhead : u >= take) continue;
                     if (!wait(&sh.empty[stage], ring_phase)) break;
-                    if (side == 0 && lane == 0) {
-                        if (kMine == 32) sh.bad[unit_n & 7][w] = bad;
-                        else sh.bad[unit_n & 7][w] = bad & 0xffffu;
+                    if (side == 0) {
+                        if (lane == 0) sh.bad[unit_n & 15][w] = kMine == 32 ? bad : bad & 0xffffu;
+                        ++unit_n;
                     }
+                    const uint32_t good_rows = side ? v_rows[0] : k_rows;
                     const C *pool = static_cast<const C *>(side ? p.c.v : p.c.k) + kvh * (side ? p.c.v_head : p.c.k_head);
-                    const unsigned long long off = side ? v_at : k_at;
+                    const unsigned long long off = side ? v_off[0] : k_off;
                     const uint32_t dst = ring + stage * K::kStageBytes;
                     if constexpr (!K::k8) {
                         constexpr int kChunks = DT / 8, kLanes = kChunks < 32 ? kChunks : 32, kAt = 32 / kLanes;
@@ -620,16 +649,23 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                         const C *from = pool + c * 8;
                         const uint32_t to = dst + (c >> 3) * (kKeys * 128) + (w * kMine + r0) * 128;
                         const uint32_t all = kMine == 32 ? 0xffffffffu : 0xffffu;
-                        if ((real & all) == all && D == DT) {  // as a rule
-#pragma unroll 8
-                            for (int i = 0; i < kMine; i += kAt)
-                                copy16_all(to + i * 128 + (((c & 7) ^ ((i + r0) & 7)) << 4),
-                                           from + __shfl_sync(0xffffffffu, off, i + r0));
+                        if ((good_rows & all) == all && blocks) {  // as a rule
+                            const unsigned long long token = side ? p.c.v_token : p.c.k_token;
+                            const C *row = from + r0 * token;
+#pragma unroll 1
+                            for (int i0 = 0; i0 < kMine; i0 += 16) {
+                                const C *at_row = row + __shfl_sync(0xffffffffu, off, i0);
+#pragma unroll
+                                for (int i = 0; i < 16; i += kAt) {
+                                    copy16_all(to + (i0 + i) * 128 + (((c & 7) ^ ((i + r0) & 7)) << 4), at_row);
+                                    at_row += kAt * token;
+                                }
+                            }
                         } else {
 #pragma unroll 1
                             for (int i = 0; i < kMine; i += kAt) {
                                 const unsigned long long src = __shfl_sync(0xffffffffu, off, i + r0);
-                                const bool there = ((real >> (i + r0)) & 1u) && c * 8 < D;
+                                const bool there = ((good_rows >> (i + r0)) & 1u) && c * 8 < D;
                                 if (c * 8 < 16 * k_steps)
                                     copy16(to + i * 128 + (((c & 7) ^ ((i + r0) & 7)) << 4), there ? from + src : pool, there);
                             }
@@ -641,15 +677,37 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                         const C *from = pool + c * 16;
                         const uint32_t to = dst + (c >> 2) * (kKeys * 128) + (w * kMine + r0) * 128;
                         const int c0 = (2 * c) & 7;
+                        const unsigned long long token = side ? p.c.v_token : p.c.k_token;
+                        const bool quick = (kMine == 32 ? good_rows == 0xffffffffu : (good_rows & 0xffffu) == 0xffffu) && blocks;
 #pragma unroll 1
                         for (int i0 = 0; i0 < kSteps; i0 += kOnce) {
                             uint4 y[kOnce];
+                            if (quick) {
+                                // 16 keys, or fewer where kOnce steps bring fewer, lie in one page
+                                const C *at_row = from + r0 * token;
+                                if constexpr (kOnce * kAt <= 16) {
+                                    at_row += __shfl_sync(0xffffffffu, off, i0 * kAt);
 #pragma unroll
-                            for (int i = 0; i < kOnce; ++i) {
-                                const int r = (i0 + i) * kAt + r0;
-                                const unsigned long long src = __shfl_sync(0xffffffffu, off, r);
-                                const bool there = ((real >> r) & 1u) && c * 16 < D;
-                                y[i] = there ? __ldg(reinterpret_cast<const uint4 *>(from + src)) : make_uint4(0, 0, 0, 0);
+                                    for (int i = 0; i < kOnce; ++i) {
+                                        y[i] = __ldg(reinterpret_cast<const uint4 *>(at_row));
+                                        at_row += kAt * token;
+                                    }
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < kOnce; ++i) {
+                                        constexpr int kIn = kAt < 16 ? 16 / kAt : 1;  // steps in a block of 16
+                                        const unsigned long long src = __shfl_sync(0xffffffffu, off, (i0 + i) / kIn * kIn * kAt);
+                                        y[i] = __ldg(reinterpret_cast<const uint4 *>(at_row + src + (i0 + i) % kIn * kAt * token));
+                                    }
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < kOnce; ++i) {
+                                    const int r = (i0 + i) * kAt + r0;
+                                    const unsigned long long src = __shfl_sync(0xffffffffu, off, r);
+                                    const bool there = ((good_rows >> r) & 1u) && c * 16 < D;
+                                    y[i] = there ? __ldg(reinterpret_cast<const uint4 *>(from + src)) : make_uint4(0, 0, 0, 0);
+                                }
                             }
 #pragma unroll
                             for (int i = 0; i < kOnce; ++i) {
@@ -673,8 +731,8 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                     }
                     if (++stage == kStages) stage = 0, ring_phase ^= 1u;
                 }
-                if (!ok) break;
-                ++unit_n;
+#pragma unroll
+                for (int i = 0; i < K::kAhead; ++i) v_off[i] = v_off[i + 1], v_rows[i] = v_rows[i + 1];
             }
             if (!ok) break;
             __syncwarp();
@@ -690,50 +748,16 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             if (lane == 0 && p.cuts) p.cuts[cta].parts = 0;
             int s = sh.start_s, t = sh.start_t, hd = sh.start_hd, x = t_begin, base = sh.start_base;
 #pragma unroll 1
-            for (int n = 0; has_work && x < t_end; ++n) {
+            for (int n = 0; has_work && x < t_end;) {
                 const Seq seq = seq_of(s, false);
                 const Tile tile = tile_of<K>(p, seq, p.starts ? 0 : sh.least[s], tt, t);
-                const int from = x - base, take = min(tile.count - from, t_end - x);
+                const int end = base + over + tile.count;  // of the tile in the line
+                const int from = max(x - base - over, 0), take = min(end, t_end) - (base + over) - from;
                 const int kvh = hd / head_blocks, h0 = kvh * p.group + hd % head_blocks * gb;
                 const bool begins = from == 0, ends = from + take == tile.count;
-                const int qi = n % kQueue;
-                if (!wait_on(&sh.seg_empty[qi], (uint32_t)(n / kQueue + 1) & 1u, abort_flag, p.err, p.wait_ns)) break;
-                int *members = sh.members[qi];
-                if (!p.starts) {  // the requests of these ranks
-                    int rank = 0;
-#pragma unroll 1
-                    for (int b0 = 0; b0 < p.batch && rank < tile.tok0 + tile.toks; b0 += 32) {
-                        const int b = b0 + lane;
-                        const bool in = b < p.batch && behind(p, b, s);
-                        const uint32_t mask = __ballot_sync(0xffffffffu, in);
-                        const int r = rank + __popc(mask & ((1u << lane) - 1u)) - tile.tok0;
-                        if (in && r >= 0 && r < tile.toks) members[r] = b;
-                        rank += __popc(mask);
-                    }
-                    __syncwarp();
-                }
-                int parts = 1;
-                if (begins && !ends) parts = (int)(((long long)(base + tile.count) * active - 1) / total_units) - cta + 1;
-                if (!p.starts && begins)
-#pragma unroll 1
-                    for (int i = lane; i < tile.toks; i += 32)
-                        p.found[(long long)hd * p.batch + members[i]] = Found{ends ? -1 : cta, parts, i * gb, 0};
-                if (lane == 0) {
-                    Segment &g = sh.segs[qi];
-                    g.rows = tile.toks * gb, g.heads = min(gb, (kvh + 1) * p.group - h0);
-                    g.q0 = seq.q0 + tile.tok0, g.first = tile.first, g.total = seq.total;
-                    g.kvh = kvh, g.h0 = h0, g.key0 = tile.key0 + from * kKeys, g.count = take;
-                    g.lo = tile.lo, g.hi = tile.hi, g.own0 = p.starts ? seq.own0 : seq.total;
-                    g.own_pages = p.table + (p.starts ? s * p.table_stride : 0);
-                    g.pre_pages = p.ptable + (seq.pre >= 0 ? seq.pre * p.ptable_stride : 0);
-                    g.slot = begins && ends ? -1 : begins ? 2 * cta + 1 : 2 * cta;
-                    g.last = x + take >= t_end;
-                    if (p.cuts && begins && !ends) p.cuts[cta] = Cut{parts, g.rows, g.q0, h0, kvh, g.heads, s, tile.first};
-                }
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&sh.seg_full[qi]);
-                x += take;
+                x = min(end, t_end);
                 base = x;
+                const int s_now = s, hd_now = hd;
                 if (x < t_end && ++t >= (seq.n + tt - 1) / tt) {
                     t = 0;
 #pragma unroll 1
@@ -749,6 +773,44 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                         s += 31;
                     }
                 }
+                if (take <= 0) continue;  // only what the line counts besides
+                const int qi = n % kQueue;
+                if (!wait_on(&sh.seg_empty[qi], (uint32_t)(n / kQueue + 1) & 1u, abort_flag, p.err, p.wait_ns)) break;
+                ++n;
+                int *members = sh.members[qi];
+                if (!p.starts) {  // the requests of these ranks
+                    int rank = 0;
+#pragma unroll 1
+                    for (int b0 = 0; b0 < p.batch && rank < tile.tok0 + tile.toks; b0 += 32) {
+                        const int b = b0 + lane;
+                        const bool in = b < p.batch && behind(p, b, s_now);
+                        const uint32_t mask = __ballot_sync(0xffffffffu, in);
+                        const int r = rank + __popc(mask & ((1u << lane) - 1u)) - tile.tok0;
+                        if (in && r >= 0 && r < tile.toks) members[r] = b;
+                        rank += __popc(mask);
+                    }
+                    __syncwarp();
+                }
+                int parts = 1;
+                if (begins && !ends) parts = (int)(((long long)end * active - 1) / total_units) - cta + 1;
+                if (!p.starts && begins)
+#pragma unroll 1
+                    for (int i = lane; i < tile.toks; i += 32)
+                        p.found[(long long)hd_now * p.batch + members[i]] = Found{ends ? -1 : cta, parts, i * gb, 0};
+                if (lane == 0) {
+                    Segment &g = sh.segs[qi];
+                    g.rows = tile.toks * gb, g.heads = min(gb, (kvh + 1) * p.group - h0);
+                    g.q0 = seq.q0 + tile.tok0, g.first = tile.first, g.total = seq.total;
+                    g.kvh = kvh, g.h0 = h0, g.key0 = tile.key0 + from * kKeys, g.count = take;
+                    g.lo = tile.lo, g.hi = tile.hi, g.own0 = p.starts ? seq.own0 : seq.total;
+                    g.own_pages = p.table + (p.starts ? s_now * p.table_stride : 0);
+                    g.pre_pages = p.ptable + (seq.pre >= 0 ? seq.pre * p.ptable_stride : 0);
+                    g.slot = begins && ends ? -1 : begins ? 2 * cta + 1 : 2 * cta;
+                    g.last = end > t_end || t_end - end <= over;
+                    if (p.cuts && begins && !ends) p.cuts[cta] = Cut{parts, g.rows, g.q0, h0, kvh, g.heads, s_now, tile.first};
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&sh.seg_full[qi]);
             }
         }
         if (warp == K::kMma && has_work) {
@@ -758,10 +820,10 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             const uint64_t q_desc = tc5::desc_sw128(q_base, 16, 1024), k_desc = tc5::desc_sw128(ring, 16, 1024),
                            v_desc = tc5::desc_sw128(ring, kKeys * 128, 1024);
             int stage = 0;
-            uint32_t phase = 0, p_phase = 0;
+            uint32_t phase = 0, step_a = 0, step_b = 0;
             bool ok = true, last = false;
             auto wait = [&](uint64_t *bar, uint32_t parity) {
-                if (!__all_sync(0xffffffffu, mbar_test(bar, parity))) ok = wait_on(bar, parity, abort_flag, p.err, p.wait_ns);
+                ok = wait_on(bar, parity, abort_flag, p.err, p.wait_ns);
                 return ok;
             };
 #pragma unroll 1
@@ -773,11 +835,16 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&sh.seg_empty[qi]);
                 if (!wait(&sh.q_full, (uint32_t)n & 1u)) break;
-                // Step j: the values of unit j, then the keys of the next one, group after group.
+                // Step j: the values of unit j, then the keys of unit j + kAhead, group after group.
 #pragma unroll 1
-                for (int j = -1; ok && j < count; ++j) {
-                    const bool values = j >= 0, keys = j + 1 < count;
+                for (int j = -K::kAhead; ok && j < count; ++j) {
+                    const bool values = j >= 0, keys = j + K::kAhead < count;
                     int v_at = 0, k_at = 0;
+                    if (keys) {
+                        k_at = stage;
+                        if (!wait(&sh.full[stage], phase)) break;
+                        if (++stage == kStages) stage = 0, phase ^= 1u;
+                    }
                     if (values) {
                         v_at = stage;
                         if (!wait(&sh.full[stage], phase)) break;
@@ -786,51 +853,56 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
 #pragma unroll 1
                     for (int x = 0; x < groups; ++x) {
                         const bool final = x == groups - 1;
+                        const uint32_t step = x ? step_b : step_a;  // of the group, over all segments
+                        const uint32_t at = step % K::kAhead, turn = step / K::kAhead & 1u;  // the scores' place, and its phase
+                        const uint32_t s = tmem + x * K::kSStep + at * K::kSBuffer;
                         if (values) {
-                            if (!wait(&sh.p_half[x], (p_phase >> x) & 1u)) break;
-                            tc5::fence_after();
-                            const uint32_t d = tmem + K::kO + x * K::kOStep, a = tmem + x * K::kSStep;
+                            const uint32_t d = tmem + K::kO + x * K::kOStep;
                             const uint64_t b = v_desc + (uint32_t)(v_at * (K::kStageBytes >> 4));
-                            if (elect()) {
+                            // With 128 keys a unit, the first 64 weights' products do not wait for the others.
+                            constexpr int kFirst = kKeys == 128 ? 4 : 0;
+                            if constexpr (kFirst > 0) {
+                                if (!wait(&sh.p_half[x], step & 1u)) break;
+                                tc5::fence_after();
+                                if (elect())
 #pragma unroll
-                                for (int ks = 0; ks < kKeys / 32; ++ks)
-                                    tc5::mma_ts(d, a + ks * 8, b + (uint32_t)(ks * (2048 >> 4)), id_pv, j > 0 || ks > 0);
+                                    for (int ks = 0; ks < kFirst; ++ks)
+                                        tc5::mma_ts(d, s + ks * 8, b + (uint32_t)(ks * (2048 >> 4)), id_pv, j > 0 || ks > 0);
                             }
-                            __syncwarp();
-                            if (!wait(&sh.p_full[x], (p_phase >> x) & 1u)) break;
-                            p_phase ^= 1u << x;
+                            if (!wait(&sh.p_full[x][at], turn)) break;
                             tc5::fence_after();
                             if (elect()) {
 #pragma unroll
-                                for (int ks = kKeys / 32; ks < kKeys / 16; ++ks)
-                                    tc5::mma_ts(d, a + ks * 8, b + (uint32_t)(ks * (2048 >> 4)), id_pv, 1u);
+                                for (int ks = kFirst; ks < kKeys / 16; ++ks)
+                                    tc5::mma_ts(d, s + ks * 8, b + (uint32_t)(ks * (2048 >> 4)), id_pv, j > 0 || ks > 0);
+                                tc5::commit(j == count - 1 ? &sh.o_full[x] : &sh.o_step[x]);
                                 if (final) tc5::commit(&sh.empty[v_at]);
-                                if (!keys) tc5::commit(&sh.o_full[x]);
                             }
                             __syncwarp();
                         }
                         if (keys) {
-                            if (x == 0) {
-                                k_at = stage;
-                                if (!wait(&sh.full[stage], phase)) break;
-                                if (++stage == kStages) stage = 0, phase ^= 1u;
-                                tc5::fence_after();
-                            }
-                            const uint32_t d = tmem + x * K::kSStep;
+                            // These scores go where this step's weights have been or, at the beginning, to the first places.
+                            const uint32_t to = (values ? step : step + (uint32_t)(j + K::kAhead)) % K::kAhead;
+                            const uint32_t d = tmem + x * K::kSStep + to * K::kSBuffer;
                             const uint64_t a = q_desc + (uint32_t)(x * (K::kQBytes >> 4)), b = k_desc + (uint32_t)(k_at * (K::kStageBytes >> 4));
+                            tc5::fence_after();
                             if (elect()) {
 #pragma unroll
                                 for (int ks = 0; ks < DT / 16; ++ks)
                                     if (ks < k_steps)
                                         tc5::mma_ss(d, a + (uint32_t)((ks >> 2) * (16384 >> 4) + (ks & 3) * 2),
                                                     b + (uint32_t)((ks >> 2) * (kKeys * 128 >> 4) + (ks & 3) * 2), id_qk, ks > 0);
-                                tc5::commit(&sh.s_full[x]);
+                                tc5::commit(&sh.s_full[x][to]);
                                 if (final) {
                                     tc5::commit(&sh.empty[k_at]);
-                                    if (j + 2 == count) tc5::commit(&sh.q_empty);
+                                    if (j + K::kAhead + 1 == count) tc5::commit(&sh.q_empty);
                                 }
                             }
                             __syncwarp();
+                        }
+                        if (values) {
+                            if (x) ++step_b;
+                            else ++step_a;
                         }
                     }
                 }
@@ -848,12 +920,12 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
         const int x = warp >> 2;                                   // group
         const int row = x * 128 + (warp & 3) * 32 + lane;          // of the tile
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;  // tensor memory lanes of this warp
-        const uint32_t t_s = tmem + lanes + x * K::kSStep, t_o = tmem + lanes + K::kO + x * K::kOStep;
-        uint32_t s_phase = 0, o_phase = 0;
+        const uint32_t t_s0 = tmem + lanes + x * K::kSStep, t_o = tmem + lanes + K::kO + x * K::kOStep;
+        uint32_t step = 0, segs_had = 0;  // units and segments that the group has had
         int unit_n = 0;
         bool last = !has_work, ok = true, odd = false;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            if (!__all_sync(0xffffffffu, mbar_test(bar, parity))) ok = wait_on(bar, parity, abort_flag, p.err, p.wait_ns);
+            ok = wait_on(bar, parity, abort_flag, p.err, p.wait_ns);
             return ok;
         };
 #pragma unroll 1
@@ -863,7 +935,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             const Segment &g = sh.segs[qi];
             last = g.last;
             const int count = g.count, key_first = g.key0, slot = g.slot, kvh = g.kvh;
-            const int tk = row / gb, hh = row - tk * gb, head = g.h0 + hh;
+            const int tk = row * gb_inv >> 16, hh = row - tk * gb, head = g.h0 + hh;
             const bool in = row < g.rows && hh < g.heads;
             const bool some = x * 128 + (warp & 3) * 32 < g.rows;  // the warp has a row
             const bool idle = x * 128 >= g.rows;                     // so has none of the group
@@ -894,9 +966,9 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             bool far = false;
             float2 l = make_float2(0.f, 0.f), lr = make_float2(0.f, 0.f);
 #pragma unroll 1
-            for (int j = 0; j < count; ++j, ++unit_n) {
-                if (!wait(&sh.s_full[x], s_phase)) break;
-                s_phase ^= 1u;
+            for (int j = 0; j < count; ++j, ++unit_n, ++step) {
+                const uint32_t at = step % K::kAhead, t_s = t_s0 + at * K::kSBuffer;
+                if (!wait(&sh.s_full[x][at], step / K::kAhead & 1u)) break;
                 tc5::fence_after();
                 if (j == 0) {
                     if constexpr (K::kOwnPower) k_scale *= sh.powers[qi][row];
@@ -906,7 +978,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                 }
                 if (some) {
                     const int key0 = key_first + j * kKeys;
-                    const uint32_t *bad = sh.bad[unit_n & 7];
+                    const uint32_t *bad = sh.bad[unit_n & 15];
                     const bool masked = __any_sync(0xffffffffu, lo > key0 || hi - kKeys < key0) || (bad[0] | bad[1] | bad[2] | bad[3]);
                     if (masked || p.softcap > 0.f) {  // what is not a plain product goes back to where the products were
                         const Scores sc(p, k_scale);
@@ -929,67 +1001,19 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                         tc5::wait_st();
                     }
                     uint32_t v[kKeys / 32][32];
-                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    auto tops = [&](int c) {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2)
-                            top[i / 2 & 3] = fmaxf(top[i / 2 & 3], fmaxf(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1])));
-                    };
-                    constexpr int kHalf = kKeys / 64;
+                    constexpr int kHalf = kKeys / 64;  // chunks of 32 scores
 #pragma unroll
                     for (int c = 0; c < kHalf; ++c) tc5::ld32(t_s + c * 32, v[c]);
                     tc5::wait_ld();
 #pragma unroll
                     for (int c = kHalf; c < 2 * kHalf; ++c) tc5::ld32(t_s + c * 32, v[c]);
-#pragma unroll
-                    for (int c = 0; c < kHalf; ++c) tops(c);
-                    tc5::wait_ld();
-#pragma unroll
-                    for (int c = kHalf; c < 2 * kHalf; ++c) tops(c);
-                    const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                    if (__any_sync(0xffffffffu, mx > limit)) {
-                        const float y = fmaxf(m, mx), far_y = y * unit, up = fmaf(-y, unit, K::kUp);
-                        far = __any_sync(0xffffffffu, fabsf(far_y) >= 1024.f && y > kLowest);
-                        const float keep = far ? ex2((m - y) * unit) : ex2(up - shift);
-                        if (j > 0) {
-#pragma unroll 1
-                            for (int c = 0; c < (D + 15) / 16; ++c) {
-                                uint32_t o[16];
-                                tc5::ld16(t_o + c * 16, o);
-                                tc5::wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-                                tc5::st16(t_o + c * 16, o);
-                            }
-                        }
-                        l.x *= keep, l.y *= keep, lr.x *= keep, lr.y *= keep;
-                        m = y, limit = y + slack, shift = up;
-                    }
                     // Weights are 2^(s unit + shift), 2^kUp at the reference; the shift's rounding is in all of them alike and in
-                    // the shift that is kept. Where scores are so large that it could be seen, differences are taken first.
-                    float by = unit, up = shift;
-                    if (far) {
-#pragma unroll 1
-                        for (int c = 0; c < kKeys / 32; ++c) {
-                            uint32_t z[32];
-                            tc5::ld32(t_s + c * 32, z);
-                            tc5::wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) z[i] = __float_as_uint((__uint_as_float(z[i]) - m) * unit);
-                            tc5::st32(t_s + c * 32, z);
-                        }
-                        tc5::wait_st();
-#pragma unroll
-                        for (int c = 0; c < 2 * kHalf; ++c) tc5::ld32(t_s + c * 32, v[c]);
-                        tc5::wait_ld();
-                        by = 1.f, up = K::kUp;
-                    }
-                    // Rounded to the operands' type; outputs are divided by the sum of the rounded ones, so that they are a mean of
-                    // the values.
-                    const float2 by2 = make_float2(by, by), up2 = make_float2(up, up);
-#pragma unroll
-                    for (int c = 0; c < kKeys / 32; ++c) {
+                    // the shift that is kept. They are rounded to the operands' type, and outputs are divided by the sum of the
+                    // rounded ones, so that they are a mean of the values.
+                    float by = far ? 1.f : unit, up = far ? K::kUp : shift;
+                    auto weights = [&](int c) {
                         uint32_t h[16];
+                        const float2 by2 = make_float2(by, by), up2 = make_float2(up, up);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             float2 s = make_float2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1]));
@@ -1000,24 +1024,79 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                             add_pair<K::kB16>(lr, h[i]);
                         }
                         tc5::st16(t_s + c * 16, h);
-                        if (c == kHalf - 1) {  // the first half of the product with the values can begin
+                    };
+                    // As a rule no score passes the reference by much, so the first half's weights are computed while the maximum
+                    // is; where one does, they are computed again. Not so in a segment's first unit, nor where scores are so
+                    // large that the shift's rounding could be seen: there differences to the reference are taken first.
+                    const float2 l0 = l, lr0 = lr;
+                    bool known = false;
+                    const bool guess = j > 0 && !far;
+#pragma unroll 1
+                    for (;;) {
+                        if (guess || known)
+#pragma unroll
+                            for (int c = 0; c < kHalf; ++c) weights(c);
+                        if (known) break;
+                        known = true;
+                        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        tc5::wait_ld();
+#pragma unroll
+                        for (int c = 0; c < kKeys / 32; ++c)
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2)
+                                top[i / 2 & 3] = fmaxf(top[i / 2 & 3], fmaxf(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1])));
+                        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                        if (__any_sync(0xffffffffu, mx > limit)) {
+                            const float y = fmaxf(m, mx), far_y = y * unit, at_y = y > kLowest ? fmaf(-y, unit, K::kUp) : 0.f;
+                            far = __any_sync(0xffffffffu, fabsf(far_y) >= 1024.f && y > kLowest);
+                            const float keep = m == kLowest ? 0.f : far ? ex2((m - y) * unit) : ex2(at_y - shift);  // nothing so far: nothing is kept
+                            if (j > 0) {  // once the last product has been added to the outputs
+                                if (!wait(&sh.o_step[x], (step - segs_had - 1) & 1u)) break;
+                                tc5::fence_after();
+#pragma unroll 1
+                                for (int c = 0; c < (D + 15) / 16; ++c) {
+                                    uint32_t o[16];
+                                    tc5::ld16(t_o + c * 16, o);
+                                    tc5::wait_ld();
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                                    tc5::st16(t_o + c * 16, o);
+                                }
+                            }
+                            l = make_float2(l0.x * keep, l0.y * keep), lr = make_float2(lr0.x * keep, lr0.y * keep);
+                            m = y, limit = y + slack, shift = at_y;
+                            by = far ? 1.f : unit, up = far ? K::kUp : shift;
+                        } else if (guess) {
+                            break;
+                        }
+                        if (far)
+#pragma unroll
+                            for (int c = 0; c < kKeys / 32; ++c)
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) v[c][i] = __float_as_uint((__uint_as_float(v[c][i]) - m) * unit);
+                    }
+                    if (!ok) break;
+#pragma unroll
+                    for (int c = kHalf; c < 2 * kHalf; ++c) {
+                        if (c == kHalf && kKeys == 128) {  // the first half of the product with the values can begin
                             tc5::wait_st();
                             tc5::fence_before();
                             __syncwarp();
                             if (lane == 0) ptx::mbar_arrive(&sh.p_half[x]);
                         }
+                        weights(c);
                     }
                     tc5::wait_st();
-                } else if (lane == 0) {
+                } else if (lane == 0 && kKeys == 128) {
                     ptx::mbar_arrive(&sh.p_half[x]);
                 }
                 tc5::fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&sh.p_full[x]);
+                if (lane == 0) ptx::mbar_arrive(&sh.p_full[x][at]);
             }
             if (!ok) break;
-            if (!wait(&sh.o_full[x], o_phase)) break;
-            o_phase ^= 1u;
+            if (!wait(&sh.o_full[x], segs_had & 1u)) break;
+            ++segs_had;
             tc5::fence_after();
             if (!some) continue;
             const float v_scale = K::k8 && p.c.v_scale ? p.c.v_scale[kvh] : 1.f;
@@ -1040,17 +1119,26 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = any ? __uint_as_float(v[i]) * f : 0.f;
                 if (direct) {
+                    uint32_t h[16];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        if (c * 32 + i < D) {
+                    for (int i = 0; i < 32; ++i)
+                        if (c * 32 + (i & ~7) < D) check = fmaf(o[i], 0.f, check);
 #pragma unroll
-                            for (int z = 0; z < 8; ++z) check = fmaf(o[i + z], 0.f, check);
-                            if (in)
-                                *reinterpret_cast<uint4 *>(out + c * 32 + i) =
-                                    make_uint4(elem::pair_from_f32<T>(o[i], o[i + 1]), elem::pair_from_f32<T>(o[i + 2], o[i + 3]),
-                                               elem::pair_from_f32<T>(o[i + 4], o[i + 5]), elem::pair_from_f32<T>(o[i + 6], o[i + 7]));
+                    for (int i = 0; i < 16; ++i) h[i] = elem::pair_from_f32<T>(o[2 * i], o[2 * i + 1]);
+                    if (in)
+#pragma unroll
+                        for (int i = 0; i < 16; i += 8) {
+                            T *to = out + c * 32 + 2 * i;
+                            if (p.wide_out && c * 32 + 2 * i + 16 <= D) {
+                                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(h[i]), "r"(h[i + 1]),
+                                             "r"(h[i + 2]), "r"(h[i + 3]), "r"(h[i + 4]), "r"(h[i + 5]), "r"(h[i + 6]), "r"(h[i + 7])
+                                             : "memory");
+                            } else {
+                                if (c * 32 + 2 * i < D) *reinterpret_cast<uint4 *>(to) = make_uint4(h[i], h[i + 1], h[i + 2], h[i + 3]);
+                                if (c * 32 + 2 * i + 8 < D)
+                                    *reinterpret_cast<uint4 *>(to + 8) = make_uint4(h[i + 4], h[i + 5], h[i + 6], h[i + 7]);
+                            }
                         }
-                    }
                 } else if (in) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 8)
