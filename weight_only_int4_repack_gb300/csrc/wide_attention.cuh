@@ -494,11 +494,48 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
         bool ok = true, last = !has_work;
         int stage = 0, unit_n = 0;
         uint32_t ring_phase = 1;  // of the empty barriers
+        constexpr int kMine = kKeys / 4;  // rows of a warp
+        // e4m3 to fp16, a few rows at a time: what lies in their own place is read before it is overwritten.
+        [[maybe_unused]] auto widen = [&](uint32_t at) {
+            constexpr int kChunks = DT / 16, kAt = 32 / kChunks, kOnce = kMine / kAt < 4 ? kMine / kAt : 4;
+            const int c = lane % kChunks, r0 = lane / kChunks, c0 = (2 * c) & 7;
+            const uint32_t row = at + (w * kMine + r0) * 128;
+            const uint32_t from = row + (DT / 64 - (kChunks + 7) / 8 + (c >> 3)) * (kKeys * 128) + ((c & 7) << 4);
+            const uint32_t to = row + (c >> 2) * (kKeys * 128);
+            __syncwarp();
+#pragma unroll 1
+            for (int i0 = 0; i0 < kMine / kAt; i0 += kOnce) {
+                uint4 y[kOnce];
+#pragma unroll
+                for (int i = 0; i < kOnce; ++i)
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(y[i].x), "=r"(y[i].y), "=r"(y[i].z), "=r"(y[i].w)
+                                 : "r"(from + (i0 + i) * kAt * 128) : "memory");
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < kOnce; ++i) {
+                    const int turn = ((i0 + i) * kAt + r0) & 7;
+                    uint32_t h[8];
+                    elem::e4m3x4_to_half2(y[i].x, h[0], h[1]);
+                    elem::e4m3x4_to_half2(y[i].y, h[2], h[3]);
+                    elem::e4m3x4_to_half2(y[i].z, h[4], h[5]);
+                    elem::e4m3x4_to_half2(y[i].w, h[6], h[7]);
+                    const uint32_t row_to = to + (i0 + i) * kAt * 128;
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_to + ((c0 ^ turn) << 4)), "r"(h[0]), "r"(h[1]),
+                                 "r"(h[2]), "r"(h[3])
+                                 : "memory");
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_to + (((c0 + 1) ^ turn) << 4)), "r"(h[4]), "r"(h[5]),
+                                 "r"(h[6]), "r"(h[7])
+                                 : "memory");
+                }
+            }
+        };
         // Copies on their way, oldest first: the barriers that wait for them.
         constexpr int kLag = 2;
         uint64_t *pend[kLag + 1];
         int pending = 0;
         auto signal = [&](uint64_t *bar) {
+            if constexpr (K::k8)
+                if (bar != &sh.q_full) widen(ring + (uint32_t)(bar - sh.full) * K::kStageBytes);
             fence_async();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar);
@@ -595,7 +632,6 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                 else queue(&sh.q_full);
             }
             // Keys and values, unit after unit.
-            constexpr int kMine = kKeys / 4;  // rows of a warp
             const int take = g.count, kvh = g.kvh;
             const bool blocks = p.c.page_size % 16 == 0 && g.own0 % 16 == 0 && D == DT;  // 16 keys lie in one page
             auto look_up = [&](int u, int &page, int &at, bool &in) {
@@ -643,92 +679,34 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                     const C *pool = static_cast<const C *>(side ? p.c.v : p.c.k) + kvh * (side ? p.c.v_head : p.c.k_head);
                     const unsigned long long off = side ? v_off[0] : k_off;
                     const uint32_t dst = ring + stage * K::kStageBytes;
-                    if constexpr (!K::k8) {
-                        constexpr int kChunks = DT / 8, kLanes = kChunks < 32 ? kChunks : 32, kAt = 32 / kLanes;
-                        const int c = lane % kLanes, r0 = lane / kLanes;
-                        const C *from = pool + c * 8;
-                        const uint32_t to = dst + (c >> 3) * (kKeys * 128) + (w * kMine + r0) * 128;
-                        const uint32_t all = kMine == 32 ? 0xffffffffu : 0xffffu;
-                        if ((good_rows & all) == all && blocks) {  // as a rule
-                            const unsigned long long token = side ? p.c.v_token : p.c.k_token;
-                            const C *row = from + r0 * token;
-#pragma unroll 1
-                            for (int i0 = 0; i0 < kMine; i0 += 16) {
-                                const C *at_row = row + __shfl_sync(0xffffffffu, off, i0);
-#pragma unroll
-                                for (int i = 0; i < 16; i += kAt) {
-                                    copy16_all(to + (i0 + i) * 128 + (((c & 7) ^ ((i + r0) & 7)) << 4), at_row);
-                                    at_row += kAt * token;
-                                }
-                            }
-                        } else {
-#pragma unroll 1
-                            for (int i = 0; i < kMine; i += kAt) {
-                                const unsigned long long src = __shfl_sync(0xffffffffu, off, i + r0);
-                                const bool there = ((good_rows >> (i + r0)) & 1u) && c * 8 < D;
-                                if (c * 8 < 16 * k_steps)
-                                    copy16(to + i * 128 + (((c & 7) ^ ((i + r0) & 7)) << 4), there ? from + src : pool, there);
-                            }
-                        }
-                        queue(&sh.full[stage]);
-                    } else {
-                        constexpr int kChunks = DT / 16, kAt = 32 / kChunks, kSteps = kMine / kAt, kOnce = kSteps < 4 ? kSteps : 4;
-                        const int c = lane % kChunks, r0 = lane / kChunks;
-                        const C *from = pool + c * 16;
-                        const uint32_t to = dst + (c >> 2) * (kKeys * 128) + (w * kMine + r0) * 128;
-                        const int c0 = (2 * c) & 7;
+                    // A chunk is 16 bytes of a row. 8-bit rows wait in the last blocks of their own place until they are widened.
+                    constexpr int kChunks = DT * (int)sizeof(C) / 16, kLanes = kChunks < 32 ? kChunks : 32, kAt = 32 / kLanes;
+                    const int c = lane % kLanes, r0 = lane / kLanes;
+                    const C *from = pool + c * (16 / (int)sizeof(C));
+                    const uint32_t to = dst + ((c >> 3) + (K::k8 ? DT / 64 - (kChunks + 7) / 8 : 0)) * (kKeys * 128) + (w * kMine + r0) * 128;
+                    auto turned = [&](int i) { return (uint32_t)((c & 7) ^ (K::k8 ? 0 : (i + r0) & 7)) << 4; };
+                    const uint32_t all = kMine == 32 ? 0xffffffffu : 0xffffu;
+                    if ((good_rows & all) == all && blocks) {  // as a rule
                         const unsigned long long token = side ? p.c.v_token : p.c.k_token;
-                        const bool quick = (kMine == 32 ? good_rows == 0xffffffffu : (good_rows & 0xffffu) == 0xffffu) && blocks;
+                        const C *row = from + r0 * token;
 #pragma unroll 1
-                        for (int i0 = 0; i0 < kSteps; i0 += kOnce) {
-                            uint4 y[kOnce];
-                            if (quick) {
-                                // 16 keys, or fewer where kOnce steps bring fewer, lie in one page
-                                const C *at_row = from + r0 * token;
-                                if constexpr (kOnce * kAt <= 16) {
-                                    at_row += __shfl_sync(0xffffffffu, off, i0 * kAt);
+                        for (int i0 = 0; i0 < kMine; i0 += 16) {
+                            const C *at_row = row + __shfl_sync(0xffffffffu, off, i0);
 #pragma unroll
-                                    for (int i = 0; i < kOnce; ++i) {
-                                        y[i] = __ldg(reinterpret_cast<const uint4 *>(at_row));
-                                        at_row += kAt * token;
-                                    }
-                                } else {
-#pragma unroll
-                                    for (int i = 0; i < kOnce; ++i) {
-                                        constexpr int kIn = kAt < 16 ? 16 / kAt : 1;  // steps in a block of 16
-                                        const unsigned long long src = __shfl_sync(0xffffffffu, off, (i0 + i) / kIn * kIn * kAt);
-                                        y[i] = __ldg(reinterpret_cast<const uint4 *>(at_row + src + (i0 + i) % kIn * kAt * token));
-                                    }
-                                }
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < kOnce; ++i) {
-                                    const int r = (i0 + i) * kAt + r0;
-                                    const unsigned long long src = __shfl_sync(0xffffffffu, off, r);
-                                    const bool there = ((good_rows >> r) & 1u) && c * 16 < D;
-                                    y[i] = there ? __ldg(reinterpret_cast<const uint4 *>(from + src)) : make_uint4(0, 0, 0, 0);
-                                }
-                            }
-#pragma unroll
-                            for (int i = 0; i < kOnce; ++i) {
-                                const int at_row = (i0 + i) * kAt, turn = (at_row + r0) & 7;
-                                uint32_t h[8];
-                                elem::e4m3x4_to_half2(y[i].x, h[0], h[1]);
-                                elem::e4m3x4_to_half2(y[i].y, h[2], h[3]);
-                                elem::e4m3x4_to_half2(y[i].z, h[4], h[5]);
-                                elem::e4m3x4_to_half2(y[i].w, h[6], h[7]);
-                                const uint32_t row_to = to + at_row * 128;
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_to + ((c0 ^ turn) << 4)), "r"(h[0]),
-                                             "r"(h[1]), "r"(h[2]), "r"(h[3])
-                                             : "memory");
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_to + (((c0 + 1) ^ turn) << 4)), "r"(h[4]),
-                                             "r"(h[5]), "r"(h[6]), "r"(h[7])
-                                             : "memory");
+                            for (int i = 0; i < 16; i += kAt) {
+                                copy16_all(to + (i0 + i) * 128 + turned(i), at_row);
+                                at_row += kAt * token;
                             }
                         }
-                        if (!K::kOwnPower) drain();  // the queries
-                        signal(&sh.full[stage]);
+                    } else {
+#pragma unroll 1
+                        for (int i = 0; i < kMine; i += kAt) {
+                            const unsigned long long src = __shfl_sync(0xffffffffu, off, i + r0);
+                            const bool there = ((good_rows >> (i + r0)) & 1u) && c * (16 / (int)sizeof(C)) < D;
+                            if (c * (16 / (int)sizeof(C)) < 16 * k_steps) copy16(to + i * 128 + turned(i), there ? from + src : pool, there);
+                        }
                     }
+                    queue(&sh.full[stage]);
                     if (++stage == kStages) stage = 0, ring_phase ^= 1u;
                 }
 #pragma unroll
@@ -1175,42 +1153,44 @@ struct Sums {
 // Joins a row's parts, which lie with the CTAs from `first` on.
 template <typename K>
 __device__ __forceinline__ Sums<K::kDim> join_parts(const Params &p, int first, int parts, int row, int D) {
-    constexpr int DT = K::kDim;
+    constexpr int DT = K::kDim, kOnce = 4;
     Sums<DT> r;
     const int lane = threadIdx.x & 31;
-    auto part = [&](int i) { return p.slots + (long long)(2 * (first + i) + (i == 0)) * K::kSlot + row * K::kPitch; };
 #pragma unroll
     for (int e = 0; e < r.kEach; ++e) r.o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int i = lane; i < parts; i += 32) r.m = fmaxf(r.m, __ldcg(part(i) + DT));
+    for (int i0 = 0; i0 < parts; i0 += kOnce) {  // all that some parts have is asked for at once
+        float4 s[kOnce], y[kOnce][r.kEach];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) r.m = fmaxf(r.m, __shfl_xor_sync(0xffffffffu, r.m, o));
-    const float top = r.m == -INFINITY ? 0.f : r.m;
-#pragma unroll 1
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-        float4 s = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-        if (i0 + lane < parts) s = __ldcg(reinterpret_cast<const float4 *>(part(i0 + lane) + DT));
-        const float f = ex2(s.x - top);
-        r.l += f * s.y, r.lr += f * s.z;
-        const int here = min(32, parts - i0);
-#pragma unroll 4
-        for (int i = 0; i < here; ++i) {
-            const float g = __shfl_sync(0xffffffffu, f, i);
-            const float *from = part(i0 + i);
+        for (int i = 0; i < kOnce; ++i) {
+            const int part = min(i0 + i, parts - 1);
+            const float *from = p.slots + (long long)(2 * (first + part) + (part == 0)) * K::kSlot + row * K::kPitch;
+            s[i] = __ldcg(reinterpret_cast<const float4 *>(from + DT));
 #pragma unroll
             for (int e = 0; e < r.kEach; ++e) {
                 const int d = 4 * (lane + 32 * e);
-                if (d < D) {
-                    const float4 y = __ldcg(reinterpret_cast<const float4 *>(from + d));
-                    r.o[e].x += g * y.x, r.o[e].y += g * y.y, r.o[e].z += g * y.z, r.o[e].w += g * y.w;
-                }
+                y[i][e] = d < D ? __ldcg(reinterpret_cast<const float4 *>(from + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            if (i0 + i >= parts) s[i] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        }
+        float top = r.m;
+#pragma unroll
+        for (int i = 0; i < kOnce; ++i) top = fmaxf(top, s[i].x);
+        const float base = top == -INFINITY ? 0.f : top, keep = ex2(r.m - base);
+        r.m = top, r.l *= keep, r.lr *= keep;
+#pragma unroll
+        for (int e = 0; e < r.kEach; ++e) r.o[e].x *= keep, r.o[e].y *= keep, r.o[e].z *= keep, r.o[e].w *= keep;
+#pragma unroll
+        for (int i = 0; i < kOnce; ++i) {
+            const float f = ex2(s[i].x - base);
+            if (f == 0.f) continue;  // nothing there, or nothing that would count
+            r.l = fmaf(f, s[i].y, r.l), r.lr = fmaf(f, s[i].z, r.lr);
+#pragma unroll
+            for (int e = 0; e < r.kEach; ++e) {
+                r.o[e].x = fmaf(f, y[i][e].x, r.o[e].x), r.o[e].y = fmaf(f, y[i][e].y, r.o[e].y);
+                r.o[e].z = fmaf(f, y[i][e].z, r.o[e].z), r.o[e].w = fmaf(f, y[i][e].w, r.o[e].w);
             }
         }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        r.l += __shfl_xor_sync(0xffffffffu, r.l, o);
-        r.lr += __shfl_xor_sync(0xffffffffu, r.lr, o);
     }
     return r;
 }
