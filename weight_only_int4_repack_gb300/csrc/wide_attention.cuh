@@ -102,14 +102,10 @@ struct Config {
     static constexpr int kSlot = kRows * kPitch;
     // Tensor memory: kAhead units' scores of each group (weights take their place), and its outputs.
     static constexpr int kO = 256, kOStep = 128, kSStep = 128, kSBuffer = 64;
+    static constexpr int kWeights = kKeys == 128 ? 64 : 0;  // where weights begin in their scores' place
     static_assert(kAhead * kKeys <= kSStep, "scores lie in front of the outputs");
     static constexpr int kWarps = 4 * kTiles + 8, kThreads = 32 * kWarps;
     static constexpr int kLoader = 4 * kTiles, kMma = kLoader + 4;  // first warps of the roles
-    // Registers: where a row's 128 scores are in them, the loaders and the issuing warps leave some of theirs to the rows'
-    // warps (256 threads at 184 and 256 at 72 are the 65536 that 512 threads get at 128).
-    static constexpr bool kSplit = kTiles == 2;
-    static constexpr int kMore = 184, kLess = 72;
-    static_assert(kMore + kLess == 256, "as many registers as there are");
 };
 
 constexpr int kQueue = 4;
@@ -489,7 +485,6 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
 
     if (warp >= K::kLoader && warp < K::kMma) {
         // ------------------------------------------------------------ loaders
-        if constexpr (K::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(K::kLess));
         const int w = warp - K::kLoader;
         bool ok = true, last = !has_work;
         int stage = 0, unit_n = 0;
@@ -720,7 +715,6 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp >= K::kMma) {
         // ------------------------------------------------------------ segments and matrix products
-        if constexpr (K::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(K::kLess));
         if (warp == K::kMma + 1) {
             // -------------------------------------------------------- segments
             if (lane == 0 && p.cuts) p.cuts[cta].parts = 0;
@@ -838,21 +832,21 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                             const uint32_t d = tmem + K::kO + x * K::kOStep;
                             const uint64_t b = v_desc + (uint32_t)(v_at * (K::kStageBytes >> 4));
                             // With 128 keys a unit, the first 64 weights' products do not wait for the others.
-                            constexpr int kFirst = kKeys == 128 ? 4 : 0;
+                            constexpr int kFirst = kKeys == 128 ? 4 : 0, kTurn = kKeys == 128 ? 4 : 0;  // keys 64 to 127 come first
                             if constexpr (kFirst > 0) {
                                 if (!wait(&sh.p_half[x], step & 1u)) break;
                                 tc5::fence_after();
                                 if (elect())
 #pragma unroll
                                     for (int ks = 0; ks < kFirst; ++ks)
-                                        tc5::mma_ts(d, s + ks * 8, b + (uint32_t)(ks * (2048 >> 4)), id_pv, j > 0 || ks > 0);
+                                        tc5::mma_ts(d, s + K::kWeights + ks * 8, b + (uint32_t)((ks ^ kTurn) * (2048 >> 4)), id_pv, j > 0 || ks > 0);
                             }
                             if (!wait(&sh.p_full[x][at], turn)) break;
                             tc5::fence_after();
                             if (elect()) {
 #pragma unroll
                                 for (int ks = kFirst; ks < kKeys / 16; ++ks)
-                                    tc5::mma_ts(d, s + ks * 8, b + (uint32_t)(ks * (2048 >> 4)), id_pv, j > 0 || ks > 0);
+                                    tc5::mma_ts(d, s + K::kWeights + ks * 8, b + (uint32_t)((ks ^ kTurn) * (2048 >> 4)), id_pv, j > 0 || ks > 0);
                                 tc5::commit(j == count - 1 ? &sh.o_full[x] : &sh.o_step[x]);
                                 if (final) tc5::commit(&sh.empty[v_at]);
                             }
@@ -894,7 +888,6 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax and output
-        if constexpr (K::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(K::kMore));
         const int x = warp >> 2;                                   // group
         const int row = x * 128 + (warp & 3) * 32 + lane;          // of the tile
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;  // tensor memory lanes of this warp
@@ -978,91 +971,84 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                         }
                         tc5::wait_st();
                     }
-                    uint32_t v[kKeys / 32][32];
-                    constexpr int kHalf = kKeys / 64;  // chunks of 32 scores
+                    // The maximum, 32 scores at a time, the next ones on their way. The code is kept small: all roles' together has
+                    // to fit the instruction caches (a loop over 128 scores in registers, 14 KB, was slower).
+                    uint32_t v[2][32];
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    auto tops = [&](const uint32_t (&z)[32]) {
 #pragma unroll
-                    for (int c = 0; c < kHalf; ++c) tc5::ld32(t_s + c * 32, v[c]);
-                    tc5::wait_ld();
+                        for (int i = 0; i < 32; i += 2)
+                            top[i / 2 & 3] = fmaxf(top[i / 2 & 3], fmaxf(__uint_as_float(z[i]), __uint_as_float(z[i + 1])));
+                    };
+                    tc5::ld32(t_s, v[0]);
+#pragma unroll 1
+                    for (int c = 0; c < kKeys / 32; c += 2) {
+                        tc5::wait_ld();
+                        tc5::ld32(t_s + c * 32 + 32, v[1]);
+                        tops(v[0]);
+                        tc5::wait_ld();
+                        if (c + 2 < kKeys / 32) tc5::ld32(t_s + c * 32 + 64, v[0]);
+                        tops(v[1]);
+                    }
+                    const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    if (__any_sync(0xffffffffu, mx > limit)) {
+                        const float y = fmaxf(m, mx), far_y = y * unit, at_y = y > kLowest ? fmaf(-y, unit, K::kUp) : 0.f;
+                        far = __any_sync(0xffffffffu, fabsf(far_y) >= 1024.f && y > kLowest);
+                        const float keep = m == kLowest ? 0.f : far ? ex2((m - y) * unit) : ex2(at_y - shift);  // nothing so far: nothing is kept
+                        if (j > 0) {  // once the last product has been added to the outputs
+                            if (!wait(&sh.o_step[x], (step - segs_had - 1) & 1u)) break;
+                            tc5::fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < (D + 15) / 16; ++c) {
+                                uint32_t o[16];
+                                tc5::ld16(t_o + c * 16, o);
+                                tc5::wait_ld();
 #pragma unroll
-                    for (int c = kHalf; c < 2 * kHalf; ++c) tc5::ld32(t_s + c * 32, v[c]);
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                                tc5::st16(t_o + c * 16, o);
+                            }
+                        }
+                        l.x *= keep, l.y *= keep, lr.x *= keep, lr.y *= keep;
+                        m = y, limit = y + slack, shift = at_y;
+                    }
                     // Weights are 2^(s unit + shift), 2^kUp at the reference; the shift's rounding is in all of them alike and in
-                    // the shift that is kept. They are rounded to the operands' type, and outputs are divided by the sum of the
-                    // rounded ones, so that they are a mean of the values.
-                    float by = far ? 1.f : unit, up = far ? K::kUp : shift;
-                    auto weights = [&](int c) {
+                    // the shift that is kept. Where scores are so large that it could be seen, differences to the reference are
+                    // taken first. Weights are rounded to the operands' type, and outputs are divided by the sum of the rounded
+                    // ones, so that they are a mean of the values.
+                    const float2 by2 = far ? make_float2(1.f, 1.f) : make_float2(unit, unit);
+                    const float2 up2 = far ? make_float2(K::kUp, K::kUp) : make_float2(shift, shift);
+                    auto weights = [&](uint32_t (&z)[32], uint32_t to) {
+                        if (far)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) z[i] = __float_as_uint((__uint_as_float(z[i]) - m) * unit);
                         uint32_t h[16];
-                        const float2 by2 = make_float2(by, by), up2 = make_float2(up, up);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            float2 s = make_float2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1]));
+                            float2 s = make_float2(__uint_as_float(z[2 * i]), __uint_as_float(z[2 * i + 1]));
                             s = fma2(s, by2, up2);
                             s.x = ex2(s.x), s.y = ex2(s.y);
                             l = add2(l, s);
                             h[i] = elem::pair_from_f32<typename K::M>(s.x, s.y);
                             add_pair<K::kB16>(lr, h[i]);
                         }
-                        tc5::st16(t_s + c * 16, h);
+                        tc5::st16(to, h);
                     };
-                    // As a rule no score passes the reference by much, so the first half's weights are computed while the maximum
-                    // is; where one does, they are computed again. Not so in a segment's first unit, nor where scores are so
-                    // large that the shift's rounding could be seen: there differences to the reference are taken first.
-                    const float2 l0 = l, lr0 = lr;
-                    bool known = false;
-                    const bool guess = j > 0 && !far;
+                    // The last 64 scores are still there. Of 128, their weights go where they have been, those of the first 64
+                    // behind them, and the product with the values begins with them.
+                    uint32_t to = t_s + K::kWeights;
 #pragma unroll 1
-                    for (;;) {
-                        if (guess || known)
-#pragma unroll
-                            for (int c = 0; c < kHalf; ++c) weights(c);
-                        if (known) break;
-                        known = true;
-                        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                        tc5::wait_ld();
-#pragma unroll
-                        for (int c = 0; c < kKeys / 32; ++c)
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2)
-                                top[i / 2 & 3] = fmaxf(top[i / 2 & 3], fmaxf(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1])));
-                        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                        if (__any_sync(0xffffffffu, mx > limit)) {
-                            const float y = fmaxf(m, mx), far_y = y * unit, at_y = y > kLowest ? fmaf(-y, unit, K::kUp) : 0.f;
-                            far = __any_sync(0xffffffffu, fabsf(far_y) >= 1024.f && y > kLowest);
-                            const float keep = m == kLowest ? 0.f : far ? ex2((m - y) * unit) : ex2(at_y - shift);  // nothing so far: nothing is kept
-                            if (j > 0) {  // once the last product has been added to the outputs
-                                if (!wait(&sh.o_step[x], (step - segs_had - 1) & 1u)) break;
-                                tc5::fence_after();
-#pragma unroll 1
-                                for (int c = 0; c < (D + 15) / 16; ++c) {
-                                    uint32_t o[16];
-                                    tc5::ld16(t_o + c * 16, o);
-                                    tc5::wait_ld();
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-                                    tc5::st16(t_o + c * 16, o);
-                                }
-                            }
-                            l = make_float2(l0.x * keep, l0.y * keep), lr = make_float2(lr0.x * keep, lr0.y * keep);
-                            m = y, limit = y + slack, shift = at_y;
-                            by = far ? 1.f : unit, up = far ? K::kUp : shift;
-                        } else if (guess) {
-                            break;
-                        }
-                        if (far)
-#pragma unroll
-                            for (int c = 0; c < kKeys / 32; ++c)
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) v[c][i] = __float_as_uint((__uint_as_float(v[c][i]) - m) * unit);
-                    }
-                    if (!ok) break;
-#pragma unroll
-                    for (int c = kHalf; c < 2 * kHalf; ++c) {
-                        if (c == kHalf && kKeys == 128) {  // the first half of the product with the values can begin
+                    for (int c = kKeys / 64 - 1; c >= 0; --c, to += 32) {
+                        weights(v[0], to);
+                        if (c > 0) tc5::ld32(t_s, v[0]);
+                        weights(v[1], to + 16);
+                        if (c > 0) {
+                            tc5::ld32(t_s + 32, v[1]);
+                            tc5::wait_ld();
                             tc5::wait_st();
                             tc5::fence_before();
                             __syncwarp();
                             if (lane == 0) ptx::mbar_arrive(&sh.p_half[x]);
                         }
-                        weights(c);
                     }
                     tc5::wait_st();
                 } else if (lane == 0 && kKeys == 128) {
