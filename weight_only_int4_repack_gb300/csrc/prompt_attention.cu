@@ -82,6 +82,22 @@ w4a16_status check(const void *q, w4a16_type type, long long q_row, long long q_
     return W4A16_OK;
 }
 
+// Tensor maps, where rows and pages allow them: without one the kernels copy 16 bytes at a time.
+void maps(wide::Params &p) {
+    const w4a16_kv_cache &c = p.c;
+    const int most = wide::rows_of(c.head_dim), gb = p.group < most ? p.group : most;
+    p.q_tma = p.starts && p.scale != 0.f && c.type != W4A16_TYPE_E4M3 &&
+              wide::tensor_map(&p.q_map, p.q, {c.head_dim, p.heads, p.rows, 1}, {p.q_head, p.q_row, 0}, {64, gb, most / gb, 1});
+    // Boxes of whole groups of 8 keys (the swizzle's rows), at most those that one warp brings.
+    int rows = wide::keys_of(c.head_dim) / 4;
+    while (rows >= 8 && c.page_size % rows) rows /= 2;
+    p.kv_rows = 0;
+    if (rows >= 8 && c.type != W4A16_TYPE_E4M3 &&
+        wide::tensor_map(&p.k_map, c.k, {c.head_dim, c.page_size, c.kv_heads, c.pages}, {c.k_token, c.k_head, c.k_page}, {64, rows, 1, 1}) &&
+        wide::tensor_map(&p.v_map, c.v, {c.head_dim, c.page_size, c.kv_heads, c.pages}, {c.v_token, c.v_head, c.v_page}, {64, rows, 1, 1}))
+        p.kv_rows = rows;
+}
+
 }  // namespace
 
 extern "C" {
@@ -121,6 +137,7 @@ w4a16_status w4a16_prompt_attention(const void *q, w4a16_type type, long long q_
     p.wide_out = aligned(out, 32) && o_row % 16 == 0 && o_head % 16 == 0;
     p.ctas = ctas(), p.err = device_error_ptr(), p.wait_ns = wait_limit_ns();
     if (!p.err) return W4A16_ERR_CUDA;
+    maps(p);
     cudaStream_t s = (cudaStream_t)stream;
     const auto launch = type == W4A16_TYPE_F16 ? wide::launch_f16 : wide::launch_bf16;
     const cudaError_t e = launch(wide::kWide, p, s);
@@ -165,6 +182,7 @@ w4a16_status w4a16_prefix_attention(const void *q, w4a16_type type, long long q_
     p.wide_out = aligned(out, 32) && o_row % 16 == 0 && o_head % 16 == 0;
     p.ctas = ctas(), p.err = device_error_ptr(), p.wait_ns = wait_limit_ns();
     if (!p.err) return W4A16_ERR_CUDA;
+    maps(p);
     // The requests' own tokens: paged attention, whose sums go into the workspace.
     attn::Params o{};
     st = attn::fill(o, q, type, q_row, q_head, cache, table, table_stride, max_pages, lens, batch, heads, scale, window, softcap,

@@ -24,6 +24,9 @@
 // wider than 128 leave tensor memory for one group.
 #pragma once
 
+#include <cuda.h>
+
+#include <array>
 #include <cmath>
 #include <type_traits>
 
@@ -53,6 +56,9 @@ struct Found {
 };
 
 struct Params {
+    CUtensorMap q_map, k_map, v_map;  // where q_tma, kv_rows say that they are used
+    int q_tma;           // queries of a tile come in one box for each 64 elements (requests)
+    int kv_rows;         // keys of a box: they lie in one page; 0: none
     const void *q;
     void *out;
     long long q_row, q_head, o_row, o_head;
@@ -136,7 +142,7 @@ struct Shared {
     int sums[32];
     int start_s, start_t, start_hd, start_base, tiles, work;
     uint32_t tmem;
-    int abort, odd;
+    int abort, odd, begun[2];
 };
 
 // ------------------------------------------------------------------ sequences and tiles
@@ -281,6 +287,14 @@ __device__ __forceinline__ bool elect() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(x));
     return x != 0;
 }
+// A box of a tensor map into shared memory.
+__device__ __forceinline__ void load_box(void *dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+            ptx::smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(ptx::smem_u32(bar))
+        : "memory");
+}
 // 32 bytes, 32-byte aligned.
 __device__ __forceinline__ void store8(float *to, const float *x) {
     asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "f"(x[0]), "f"(x[1]), "f"(x[2]),
@@ -369,7 +383,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) ptx::mbar_init(&sh.s_full[i >> 1][i & 1], 1), ptx::mbar_init(&sh.p_full[i >> 1][i & 1], 4);
         ptx::mbar_init(&sh.q_full, 4), ptx::mbar_init(&sh.q_empty, 1), ptx::mbar_init(&sh.drain, 1);
-        sh.abort = 0, sh.odd = 0, sh.work = 0;
+        sh.abort = 0, sh.odd = 0, sh.work = 0, sh.begun[0] = sh.begun[1] = 0;
         ptx::mbar_init_fence();
     }
     if (warp == K::kMma) tc5::alloc(&sh.tmem, 512);
@@ -487,7 +501,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
         // ------------------------------------------------------------ loaders
         const int w = warp - K::kLoader;
         bool ok = true, last = !has_work;
-        int stage = 0, unit_n = 0;
+        int stage = 0, unit_n = 0, tiles_n = 0, queries_n = 0;  // tiles of the ring and of queries that are on their way or there
         uint32_t ring_phase = 1;  // of the empty barriers
         constexpr int kMine = kKeys / 4;  // rows of a warp
         // e4m3 to fp16, a few rows at a time: what lies in their own place is read before it is overwritten.
@@ -571,7 +585,18 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             last = g.last;
             // Queries, in the order of the rows.
             if (!wait(&sh.q_empty, (uint32_t)(n + 1) & 1u)) break;
-            {
+            if (!K::kOwnPower && p.q_tma) {
+                // A box holds the tile's rows in their order: heads of a token, token after token. Rows behind the request's last
+                // one are others' or zero, and nobody looks at them.
+                if (w == 0 && elect()) {
+                    ptx::mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(tt * gb * DT * 2));
+                    for (int i = 0; i < DT / 64; ++i)
+                        load_box(smem + i * (K::kRows * 128), &p.q_map, i * 64, g.h0, g.q0, 0, &sh.q_full);
+                } else if (w > 0 && lane == 0) {
+                    ptx::mbar_arrive(&sh.q_full);
+                }
+                __syncwarp();
+            } else {
                 constexpr int kChunks = DT / 8, kLanes = kChunks < 32 ? kChunks : 32, kAt = 32 / kLanes;
                 const int c = lane % kLanes, rows = g.rows;
 #pragma unroll 1
@@ -591,7 +616,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                         const long long src = srcs[z];
                         const bool real = src >= 0 && c * 8 < D;
                         const T *from = static_cast<const T *>(p.q) + (real ? src + c * 8 : 0);
-                        const uint32_t to = q_base + (rr >> 7) * K::kQBytes + (c >> 3) * 16384 + (rr & 127) * 128 + (((c & 7) ^ (rr & 7)) << 4);
+                        const uint32_t to = q_base + (c >> 3) * (K::kRows * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
                         if constexpr (!K::kOwnPower) {
                             if (c * 8 < 16 * k_steps) copy16(to, from, real);
                         } else {
@@ -626,9 +651,11 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                 if constexpr (K::kOwnPower) signal(&sh.q_full);
                 else queue(&sh.q_full);
             }
+            ++queries_n;
             // Keys and values, unit after unit.
             const int take = g.count, kvh = g.kvh;
-            const bool blocks = p.c.page_size % 16 == 0 && g.own0 % 16 == 0 && D == DT;  // 16 keys lie in one page
+            const bool boxes = p.kv_rows > 0 && (!p.starts || g.own0 % p.kv_rows == 0);  // a box's keys lie in one page
+            const bool blocks = p.c.page_size % 16 == 0 && (!p.starts || g.own0 % 16 == 0) && D == DT;  // 16 keys lie in one page
             auto look_up = [&](int u, int &page, int &at, bool &in) {
                 const int j = g.key0 + u * kKeys + w * kMine + lane % kMine, own0 = g.own0;
                 in = j >= g.lo && j < g.hi;
@@ -645,21 +672,17 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             int page, at;
             bool in;
             look_up(0, page, at, in);
-            unsigned long long v_off[K::kAhead + 1] = {};
+            int v_page[K::kAhead + 1] = {}, v_at[K::kAhead + 1] = {};
             uint32_t v_rows[K::kAhead + 1] = {};
 #pragma unroll 1
             for (int u = 0; ok && u < take + K::kAhead; ++u) {
-                unsigned long long k_off = 0;
-                uint32_t k_rows = 0, bad = 0;
+                uint32_t bad = 0;
                 if (u < take) {
                     const bool good = in && page >= 0 && page < p.c.pages;
                     bad = __ballot_sync(0xffffffffu, in && !good);
                     if (bad && in && !good) atomicExch(p.err, (unsigned int)W4A16_ERR_INVALID_ARG);
-                    k_rows = __ballot_sync(0xffffffffu, good);
-                    const unsigned long long pg = good ? page : 0, tk = good ? at : 0;
-                    k_off = pg * (unsigned long long)p.c.k_page + tk * (unsigned long long)p.c.k_token;
-                    v_off[K::kAhead] = pg * (unsigned long long)p.c.v_page + tk * (unsigned long long)p.c.v_token;
-                    v_rows[K::kAhead] = k_rows;
+                    v_rows[K::kAhead] = __ballot_sync(0xffffffffu, good);
+                    v_page[K::kAhead] = good ? page : 0, v_at[K::kAhead] = good ? at : 0;
                     if (u + 1 < take) look_up(u + 1, page, at, in);
                 }
 #pragma unroll 1
@@ -670,17 +693,34 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                         if (lane == 0) sh.bad[unit_n & 15][w] = kMine == 32 ? bad : bad & 0xffffu;
                         ++unit_n;
                     }
-                    const uint32_t good_rows = side ? v_rows[0] : k_rows;
-                    const C *pool = static_cast<const C *>(side ? p.c.v : p.c.k) + kvh * (side ? p.c.v_head : p.c.k_head);
-                    const unsigned long long off = side ? v_off[0] : k_off;
+                    const uint32_t good_rows = side ? v_rows[0] : v_rows[K::kAhead];
+                    const int my_page = side ? v_page[0] : v_page[K::kAhead], my_at = side ? v_at[0] : v_at[K::kAhead];
+                    const uint32_t all = kMine == 32 ? 0xffffffffu : 0xffffu;
                     const uint32_t dst = ring + stage * K::kStageBytes;
+                    if (!K::k8 && boxes && (good_rows & all) == all) {  // as a rule
+                        if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.full[stage], (uint32_t)(kMine * DT * 2));
+                        __syncwarp();
+#pragma unroll 1
+                        for (int i = 0; i < kMine; i += p.kv_rows) {
+                            const int box_page = __shfl_sync(0xffffffffu, my_page, i), box_at = __shfl_sync(0xffffffffu, my_at, i);
+                            if (elect()) {
+                                unsigned char *to = smem + K::kRing + stage * K::kStageBytes + (w * kMine + i) * 128;
+#pragma unroll
+                                for (int z = 0; z < DT / 64; ++z)
+                                    load_box(to + z * (kKeys * 128), side ? &p.v_map : &p.k_map, z * 64, box_at, kvh, box_page, &sh.full[stage]);
+                            }
+                        }
+                        __syncwarp();
+                    } else {
+                    const C *pool = static_cast<const C *>(side ? p.c.v : p.c.k) + kvh * (side ? p.c.v_head : p.c.k_head);
+                    const unsigned long long off = my_page * (unsigned long long)(side ? p.c.v_page : p.c.k_page) +
+                                                   my_at * (unsigned long long)(side ? p.c.v_token : p.c.k_token);
                     // A chunk is 16 bytes of a row. 8-bit rows wait in the last blocks of their own place until they are widened.
                     constexpr int kChunks = DT * (int)sizeof(C) / 16, kLanes = kChunks < 32 ? kChunks : 32, kAt = 32 / kLanes;
                     const int c = lane % kLanes, r0 = lane / kLanes;
                     const C *from = pool + c * (16 / (int)sizeof(C));
                     const uint32_t to = dst + ((c >> 3) + (K::k8 ? DT / 64 - (kChunks + 7) / 8 : 0)) * (kKeys * 128) + (w * kMine + r0) * 128;
                     auto turned = [&](int i) { return (uint32_t)((c & 7) ^ (K::k8 ? 0 : (i + r0) & 7)) << 4; };
-                    const uint32_t all = kMine == 32 ? 0xffffffffu : 0xffffu;
                     if ((good_rows & all) == all && blocks) {  // as a rule
                         const unsigned long long token = side ? p.c.v_token : p.c.k_token;
                         const C *row = from + r0 * token;
@@ -702,10 +742,12 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                         }
                     }
                     queue(&sh.full[stage]);
+                    }
+                    ++tiles_n;
                     if (++stage == kStages) stage = 0, ring_phase ^= 1u;
                 }
 #pragma unroll
-                for (int i = 0; i < K::kAhead; ++i) v_off[i] = v_off[i + 1], v_rows[i] = v_rows[i + 1];
+                for (int i = 0; i < K::kAhead; ++i) v_page[i] = v_page[i + 1], v_at[i] = v_at[i + 1], v_rows[i] = v_rows[i + 1];
             }
             if (!ok) break;
             __syncwarp();
@@ -713,6 +755,22 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
         }
         drain();
         asm volatile("cp.async.wait_all;" ::: "memory");
+        // Nothing may be on its way when the CTA ends. After a wait that ran out the warps may have stopped at different
+        // tiles: each one arrives for those that others have begun, so that what is on its way for them can be waited for.
+        if (lane == 0) atomicMax(&sh.begun[0], tiles_n), atomicMax(&sh.begun[1], queries_n);
+        ptx::named_bar_sync(1, 128);
+        const int tiles_all = *(volatile int *)&sh.begun[0], queries_all = *(volatile int *)&sh.begun[1];
+        if (lane == 0) {
+            volatile int no_abort = 0;
+#pragma unroll 1
+            for (int i = tiles_n; i < tiles_all; ++i) ptx::mbar_arrive(&sh.full[i % kStages]);
+            if (queries_n < queries_all) ptx::mbar_arrive(&sh.q_full);
+#pragma unroll 1
+            for (int i = max(tiles_all - kStages, 0); i < tiles_all; ++i)
+                ptx::mbar_wait(&sh.full[i % kStages], (uint32_t)(i / kStages) & 1u, &no_abort, nullptr, 200000000ull);
+            if (queries_all > 0) ptx::mbar_wait(&sh.q_full, (uint32_t)(queries_all - 1) & 1u, &no_abort, nullptr, 200000000ull);
+        }
+        __syncwarp();
     } else if (warp >= K::kMma) {
         // ------------------------------------------------------------ segments and matrix products
         if (warp == K::kMma + 1) {
@@ -856,13 +914,13 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                             // These scores go where this step's weights have been or, at the beginning, to the first places.
                             const uint32_t to = (values ? step : step + (uint32_t)(j + K::kAhead)) % K::kAhead;
                             const uint32_t d = tmem + x * K::kSStep + to * K::kSBuffer;
-                            const uint64_t a = q_desc + (uint32_t)(x * (K::kQBytes >> 4)), b = k_desc + (uint32_t)(k_at * (K::kStageBytes >> 4));
+                            const uint64_t a = q_desc + (uint32_t)(x * (16384 >> 4)), b = k_desc + (uint32_t)(k_at * (K::kStageBytes >> 4));
                             tc5::fence_after();
                             if (elect()) {
 #pragma unroll
                                 for (int ks = 0; ks < DT / 16; ++ks)
                                     if (ks < k_steps)
-                                        tc5::mma_ss(d, a + (uint32_t)((ks >> 2) * (16384 >> 4) + (ks & 3) * 2),
+                                        tc5::mma_ss(d, a + (uint32_t)((ks >> 2) * (K::kRows * 128 >> 4) + (ks & 3) * 2),
                                                     b + (uint32_t)((ks >> 2) * (kKeys * 128 >> 4) + (ks & 3) * 2), id_qk, ks > 0);
                                 tc5::commit(&sh.s_full[x][to]);
                                 if (final) {
@@ -1442,6 +1500,10 @@ cudaError_t launch_dims(Which which, const Params &p, cudaStream_t s) {
     if (p.c.head_dim <= 128) return launch<T, C, 128>(which, p, s);
     return launch<T, C, 256>(which, p, s);
 }
+
+// Defined in wide_tmap.cu.
+bool tensor_map(CUtensorMap *out, const void *base, const std::array<long long, 4> &dims, const std::array<long long, 3> &strides,
+                const std::array<int, 4> &box);
 
 // A head's width as the kernels have it, the rows of a tile, the keys of a unit.
 inline int dim_of(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
