@@ -69,7 +69,7 @@ w4a16_status check(const void *q, w4a16_type type, long long q_row, long long q_
     const int group = heads / cache->kv_heads, most = wide::rows_of(cache->head_dim), block = group < most ? group : most;
     const long long seqs = prefixes_only ? prefixes : batch;
     const long long tiles = rows / (most / block) + seqs, hds = (long long)(group + block - 1) / block * cache->kv_heads;
-    if (tiles * hds > INT_MAX / (keys / wide::keys_of(cache->head_dim) + 2 + wide::kOver)) return W4A16_ERR_UNSUPPORTED;
+    if (tiles * hds > INT_MAX / (keys / wide::keys_of(cache->head_dim) + 3 + wide::kOver)) return W4A16_ERR_UNSUPPORTED;
     *nothing = rows == 0 || batch == 0;
     if (*nothing) return W4A16_OK;
     if (!q || !out || !table || !lens || (prefixes > 0 && (!ptable || !plens || !pof))) return W4A16_ERR_INVALID_ARG;

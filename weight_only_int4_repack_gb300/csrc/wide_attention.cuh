@@ -125,7 +125,7 @@ struct Segment {
     int kvh, h0;         // kv head, first query head
     int key0, count;     // first key, units
     int lo, hi;          // keys that some row sees
-    int own0;            // keys of the prefix in front of the request's own
+    int own0, gap;       // keys of the prefix in front of the request's own; numbers between them that are no keys
     const int32_t *own_pages, *pre_pages;
     int slot;            // where the sums go; -1: the tile is whole
     int last;            // no segment follows
@@ -187,7 +187,16 @@ __device__ __forceinline__ bool behind(const Params &p, int b, int prefix) {
     return p.pof[b] == prefix && p.lens[b] > 0;
 }
 
-// A tile of a sequence: its tokens, the keys that any of them sees, its units.
+// Keys are numbered with a gap between a request's prefix and its own, up to the next unit's first one: so that units, and
+// the blocks of keys in them, begin where pages do.
+template <typename K>
+__device__ __forceinline__ int gap_of(int own0) {
+    return -own0 & (K::kKeys - 1);
+}
+__device__ __forceinline__ int placed_from(int j, int own0, int gap) { return j >= own0 ? j + gap : j; }
+__device__ __forceinline__ int placed_to(int j, int own0, int gap) { return j > own0 ? j + gap : j; }
+
+// A tile of a sequence: its tokens, the keys that any of them sees (as numbered with the gap), its units.
 struct Tile {
     int tok0, toks, first, lo, hi, key0, count;
 };
@@ -200,6 +209,8 @@ __device__ __noinline__ Tile tile_of(const Params &p, const Seq &s, int least, i
         x.first = s.total - s.n + x.tok0 + 1;
         x.hi = max(x.first + x.toks - 1, 0);
         x.lo = p.window > 0 ? max(0, x.first - p.window) : 0;
+        const int gap = gap_of<K>(s.own0);
+        x.hi = placed_to(x.hi, s.own0, gap), x.lo = placed_from(x.lo, s.own0, gap);
     } else {
         x.first = 0;
         x.hi = s.total;
@@ -393,7 +404,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
     const int gb = min(p.group, K::kRows), head_blocks = (p.group + gb - 1) / gb, tt = K::kRows / gb;
     const int hds = p.c.kv_heads * head_blocks;
     const int seqs = p.starts ? p.batch : p.prefixes;
-    int *plan_off = reinterpret_cast<int *>(smem), *plan_n = plan_off + seqs + 1, *plan_total = plan_n + seqs;
+    int *plan_off = reinterpret_cast<int *>(smem), *plan_n = plan_off + seqs + 1, *plan_total = plan_n + seqs, *plan_own = plan_total + seqs;
     if (!p.starts) {
 #pragma unroll 1
         for (int i = tid; i < seqs; i += K::kThreads) sh.counts[i] = 0, sh.least[i] = 0x7fffffff;
@@ -419,7 +430,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
 #pragma unroll 1
         for (int i = s0; i < s1; ++i) {
             const Seq s = seq_of(i, cta == 0);
-            plan_n[i] = s.n, plan_total[i] = s.total;
+            plan_n[i] = s.n, plan_total[i] = s.total, plan_own[i] = s.own0;
             mine += (s.n + tt - 1) / tt;
         }
         int at = scan<K::kWarps>(mine, sh.sums, &all);
@@ -448,7 +459,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             s_first = lo;
         }
         auto units_of = [&](int s, int i) {
-            const Seq q{plan_n[s], plan_total[s], 0, 0, 0};
+            const Seq q{plan_n[s], plan_total[s], 0, plan_own[s], 0};
             return tile_of<K>(p, q, p.starts ? 0 : sh.least[s], tt, i - plan_off[s]).count;
         };
         int mine = 0, per_hd = 0;
@@ -654,15 +665,17 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             ++queries_n;
             // Keys and values, unit after unit.
             const int take = g.count, kvh = g.kvh;
-            const bool boxes = p.kv_rows > 0 && (!p.starts || g.own0 % p.kv_rows == 0);  // a box's keys lie in one page
-            const bool blocks = p.c.page_size % 16 == 0 && (!p.starts || g.own0 % 16 == 0) && D == DT;  // 16 keys lie in one page
-            auto look_up = [&](int u, int &page, int &at, bool &in) {
+            const bool boxes = p.kv_rows > 0;  // a box's keys lie in one page
+            const bool blocks = p.c.page_size % 16 == 0 && D == DT;  // 16 keys lie in one page
+            auto look_up = [&](int u, int &page, int &at, bool &in, bool &none) {
                 const int j = g.key0 + u * kKeys + w * kMine + lane % kMine, own0 = g.own0;
                 in = j >= g.lo && j < g.hi;
+                none = j >= own0 && j < own0 + g.gap;
+                in = in && !none;
                 page = -1, at = 0;
                 if (in) {
                     const bool pre = j < own0;
-                    const unsigned int y = pre ? j : j - own0, n = y / (unsigned int)p.c.page_size;
+                    const unsigned int y = pre ? j : j - own0 - g.gap, n = y / (unsigned int)p.c.page_size;
                     at = (int)(y - n * (unsigned int)p.c.page_size);
                     page = __ldg((pre ? g.pre_pages : g.own_pages) + n);
                 }
@@ -670,8 +683,8 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             // Keys run kAhead units ahead of the values, as the products that need them do. A unit's places are looked up when its
             // keys are brought, and kept for its values.
             int page, at;
-            bool in;
-            look_up(0, page, at, in);
+            bool in, none;
+            look_up(0, page, at, in, none);
             int v_page[K::kAhead + 1] = {}, v_at[K::kAhead + 1] = {};
             uint32_t v_rows[K::kAhead + 1] = {};
 #pragma unroll 1
@@ -679,11 +692,11 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                 uint32_t bad = 0;
                 if (u < take) {
                     const bool good = in && page >= 0 && page < p.c.pages;
-                    bad = __ballot_sync(0xffffffffu, in && !good);
-                    if (bad && in && !good) atomicExch(p.err, (unsigned int)W4A16_ERR_INVALID_ARG);
+                    bad = __ballot_sync(0xffffffffu, none || (in && !good));
+                    if (in && !good) atomicExch(p.err, (unsigned int)W4A16_ERR_INVALID_ARG);
                     v_rows[K::kAhead] = __ballot_sync(0xffffffffu, good);
                     v_page[K::kAhead] = good ? page : 0, v_at[K::kAhead] = good ? at : 0;
-                    if (u + 1 < take) look_up(u + 1, page, at, in);
+                    if (u + 1 < take) look_up(u + 1, page, at, in, none);
                 }
 #pragma unroll 1
                 for (int side = 0; side < 2; ++side) {  // keys of unit u, values of unit u - kAhead
@@ -832,7 +845,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                     g.rows = tile.toks * gb, g.heads = min(gb, (kvh + 1) * p.group - h0);
                     g.q0 = seq.q0 + tile.tok0, g.first = tile.first, g.total = seq.total;
                     g.kvh = kvh, g.h0 = h0, g.key0 = tile.key0 + from * kKeys, g.count = take;
-                    g.lo = tile.lo, g.hi = tile.hi, g.own0 = p.starts ? seq.own0 : seq.total;
+                    g.lo = tile.lo, g.hi = tile.hi, g.own0 = p.starts ? seq.own0 : seq.total, g.gap = p.starts ? gap_of<K>(seq.own0) : 0;
                     g.own_pages = p.table + (p.starts ? s_now * p.table_stride : 0);
                     g.pre_pages = p.ptable + (seq.pre >= 0 ? seq.pre * p.ptable_stride : 0);
                     g.slot = begins && ends ? -1 : begins ? 2 * cta + 1 : 2 * cta;
@@ -973,7 +986,8 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                 if (p.starts) {
                     b = g.q0 + tk;
                     hi = max(g.first + tk, 0);
-                    lo = p.window > 0 ? max(0, hi - p.window) : 0;
+                    lo = placed_from(p.window > 0 ? max(0, hi - p.window) : 0, g.own0, g.gap);
+                    hi = placed_to(hi, g.own0, g.gap);
                 } else {
                     b = sh.members[qi][tk];
                     hi = g.total;
@@ -1478,7 +1492,7 @@ cudaError_t launch(Which which, const Params &p, cudaStream_t s) {
     using K = Config<T, C, DT>;
     constexpr int kSmem = K::kAfter + (int)sizeof(Shared<K::kRows>) + 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
-    static_assert((3 * kMaxSeqs + 1) * 4 <= K::kAfter, "the plan lies where queries, keys and values come later");
+    static_assert((4 * kMaxSeqs + 1) * 4 <= K::kAfter, "the plan lies where queries, keys and values come later");
     static_assert(K::kAfter % 1024 == 0, "alignment");
     if (which == kWide) {
         auto kernel = wide_kernel<T, C, DT>;
