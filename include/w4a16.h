@@ -725,6 +725,46 @@ typedef struct {
 w4a16_status w4a16_prompt_attention_block(const w4a16_prompt_attention_args *args);
 w4a16_status w4a16_prefix_attention_block(const w4a16_prefix_attention_args *args);
 
+/*
+ * The next token of each row of logits. With max the row's largest logit, T its
+ * temperature and w_i = exp((x_i - max) / T), in this order:
+ *   top-k   of the tokens in the order of falling logits (equal ones by number) the first k
+ *   top-p   of these the fewest first ones whose weights' sum reaches p times the sum of
+ *           all that top-k left; one at least
+ *   min-p   of these the ones with w_i >= min_p
+ *   draw    of what is kept, in the order of their numbers, the first token at which the
+ *           running sum of the weights exceeds u times their sum (u = 1: the last one)
+ *   logits  device, `type` (F16, BF16 or F32), [rows][vocab], rows `row` elements apart
+ *   uniform device fp32 [rows]: u, from 0 to 1
+ *   temperature, top_p, min_p  device fp32 [rows], top_k device int32 [rows]; any may be
+ *           NULL. T = 0: the largest logit, the first of equal ones; top_k <= 0, top_p >= 1,
+ *           min_p <= 0: not wanted (NULL: T = 1, none wanted)
+ *   out     device int64 [rows]: the token, or -1 in a row without a logit above minus
+ *           infinity. NaN counts as minus infinity, and beside plus infinity nothing else
+ *           is drawn
+ * Weights are 64-bit fixed-point numbers off by less than 2^-31 of themselves; their sums
+ * are exact, so that a row's token depends on nothing but the row. Weights below 2^-44
+ * of the largest are 0.
+ * In the device error word: a temperature below 0 or NaN (taken as 0), NaN as top_p or
+ * min_p (not wanted), u outside of [0, 1] or NaN (taken as the nearest, NaN as 0).
+ * Refused as unsupported: vocab above 2^18, rows above 2^20.
+ */
+w4a16_status w4a16_sample(const void *logits, w4a16_type type, long long row, int rows, int vocab,
+                          const float *uniform, const float *temperature, const int32_t *top_k,
+                          const float *top_p, const float *min_p, int64_t *out, void *stream);
+typedef struct {
+    const void *logits;
+    int type;
+    long long row;
+    int rows, vocab;
+    const float *uniform, *temperature;
+    const int32_t *top_k;
+    const float *top_p, *min_p;
+    int64_t *out;
+    void *stream;
+} w4a16_sample_args;
+w4a16_status w4a16_sample_block(const w4a16_sample_args *args);
+
 #ifdef __cplusplus
 }
 #endif

@@ -59,6 +59,7 @@ EXPORTS = (
     "w4a16_residual_rmsnorm_block",
     "w4a16_prompt_attention_workspace_bytes", "w4a16_prompt_attention", "w4a16_prompt_attention_block",
     "w4a16_prefix_attention_workspace_bytes", "w4a16_prefix_attention", "w4a16_prefix_attention_block",
+    "w4a16_sample", "w4a16_sample_block",
 )
 
 _vp, _ci, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
@@ -165,10 +166,11 @@ _blocks = {
     "w4a16_paged_attention": "PiqqPPqiPiififPqqPPNP",
     "w4a16_residual_rmsnorm": "PiqPiqPPqfPfPqPqiiP",
 }
-# Those of the attention of many rows.
+# Those of the attention of many rows, and of sampling.
 _wide_blocks = {
     "w4a16_prompt_attention": "PiqqPPqiPPiiiPqiPPififPqqPPNP",
     "w4a16_prefix_attention": "PiqqPPqiPiiPqiPPififPqqPPNP",
+    "w4a16_sample": "PiqiiPPPPPPP",
 }
 _sig.update({
     "w4a16_prompt_attention_workspace_bytes": (_sz, [_ci, _ci, _ci, _ci]),
@@ -177,6 +179,7 @@ _sig.update({
     "w4a16_prefix_attention_workspace_bytes": (_sz, [_ci, _ci, _ci, _ci]),
     "w4a16_prefix_attention": (_ci, [_vp, _ci, _ll, _ll, _kv, _vp, _ll, _ci, _vp, _ci, _ci, _vp, _ll, _ci, _vp, _vp, _ci,
                                      _cf, _ci, _cf, _vp, _ll, _ll, _vp, _vp, _sz, _vp]),
+    "w4a16_sample": (_ci, [_vp, _ci, _ll, _ci, _ci, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
 })
 _sig.update({_name + "_block": (_ci, [ctypes.c_char_p]) for _name in (*_blocks, *_wide_blocks)})
 for _name, (_res, _args) in _sig.items():
@@ -185,8 +188,8 @@ for _name, (_res, _args) in _sig.items():
     _f.argtypes = _args
 _pack_extend, _pack_rope, _pack_attention, _pack_norm = (struct.Struct(_blocks[_name]).pack for _name in _blocks)
 _extend, _rope, _attention, _norm = (getattr(lib, _name + "_block") for _name in _blocks)
-_pack_prompt, _pack_prefix = (struct.Struct(_wide_blocks[_name]).pack for _name in _wide_blocks)
-_prompt, _prefix = (getattr(lib, _name + "_block") for _name in _wide_blocks)
+_pack_prompt, _pack_prefix, _pack_sample = (struct.Struct(_wide_blocks[_name]).pack for _name in _wide_blocks)
+_prompt, _prefix, _sample = (getattr(lib, _name + "_block") for _name in _wide_blocks)
 
 
 class W4A16Error(RuntimeError):
@@ -663,6 +666,35 @@ def w4a16_residual_rmsnorm(h, y, gamma=None, eps: float = 1e-5, post_gamma=None,
     if status:
         raise W4A16Error(status, "w4a16_residual_rmsnorm")
     return h_out, n_out
+
+
+def w4a16_sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None, out=None, stream=None):
+    """The next token of each row of logits [rows, vocab] (float16, bfloat16 or float32) for the random numbers uniform
+    (float32 [rows], from 0 to 1): int64 [rows], -1 where every logit is minus infinity. temperature, top_p, min_p
+    (float32 [rows]) and top_k (int32 [rows]) may be None; temperature 0 takes the largest logit, top_k <= 0, top_p >= 1
+    and min_p <= 0 leave a row alone. See include/w4a16.h."""
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("w4a16_sample: logits [rows, vocab], rows contiguous")
+    rows, vocab = logits.shape
+    if out is None:
+        out = _new((rows,), _int64, logits, stream)
+    _expect(uniform, _float32, "uniform")
+    _expect(out, _int64, "out")
+    for t, kind, name in ((temperature, _float32, "temperature"), (top_k, _int32, "top_k"), (top_p, _float32, "top_p"),
+                          (min_p, _float32, "min_p")):
+        if t is not None:
+            _expect(t, kind, name)
+            if t.numel() != rows:
+                raise ValueError(f"{name}: one entry for each row")
+    if uniform.numel() != rows or out.numel() != rows:
+        raise ValueError("w4a16_sample: uniform, out: one entry for each row")
+    status = _sample(_pack_sample(
+        logits.data_ptr(), _TYPES.get(logits.dtype, -1), logits.stride(0) if rows > 1 else vocab, rows, vocab,
+        uniform.data_ptr(), 0 if temperature is None else temperature.data_ptr(), 0 if top_k is None else top_k.data_ptr(),
+        0 if top_p is None else top_p.data_ptr(), 0 if min_p is None else min_p.data_ptr(), out.data_ptr(), _stream(stream)))
+    if status:
+        raise W4A16Error(status, "w4a16_sample")
+    return out
 
 
 def w4a16_set_tuning(smallm_max: int) -> None:
