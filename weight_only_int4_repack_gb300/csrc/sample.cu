@@ -9,10 +9,11 @@
 // exact and so do not depend on any order, and a border between two tokens moves by less than 2^-31 of the sum, about what
 // it would take for a 32-bit random number to show it. A weight below 2^-44 of the largest is 0.
 //
-// The border of top-k and top-p is found by a histogram over 32 bins for each factor of two of the weight (counts, and for
-// top-p sums): the bin that holds it, then in that bin. Where few tokens lie above the border (as a rule) they are gathered,
-// and one CTA ranks them against each other and draws; otherwise the border's bin is resolved (by ranking its tokens, or, when
-// it holds many, by halving the range of its values) and a second pass over shared memory sums and draws.
+// The border of top-k and top-p is found by a histogram of counts over 32 bins for each factor of two of the weight. It
+// names the bin of the k-th token, and a few bins that hold the border of top-p (a bin's weights are alike to 2%); a second
+// pass adds up exactly what lies in front of these, and in each of them. Where few tokens lie above the border (as a rule)
+// they are gathered, and one CTA ranks them against each other and draws; otherwise the border's bin is resolved (by ranking
+// its tokens, or, when it holds many, by halving the range of its values) and one more pass sums and draws.
 #include <climits>
 #include <cmath>
 
@@ -66,20 +67,19 @@ struct Heat {
     }
     __device__ __forceinline__ uint64_t weight(float x, const uint32_t *powers) const {
         const float d = down(x), t = d * c;
-        if (!(t < 64.f)) return 0;
-        // The difference's rounding and the product's, and the factor's second part.
-        const float rest = x == top ? 0.f : (top - d) - x;
-        const float low = fmaf(d, c, -t) + fmaf(d, c_low, rest * c);
-        const float whole = floorf(t);
-        const uint64_t fixed = ((uint64_t)(uint32_t)whole << 32) + (uint64_t)((t - whole) * 4294967296.f) + (uint64_t)(int64_t)(low * 4294967296.f);
-        if ((int64_t)fixed <= 0) return (uint64_t)powers[0] << 12;
-        const uint32_t n = (uint32_t)(fixed >> 32), f = (uint32_t)fixed;
-        // 2^-f: a table for the first 8 bits, three terms of 1 - 2^-y for the others (y < 2^-8, the next term is below 2^-37).
-        const float y = (float)(f & 0xffffffu) * (0.693147180559945f / 4294967296.f);
+        if (!(t < 44.f)) return 0;
+        // In 256th factors of two: the nearest whole number (the bits of a sum with 1.5 * 2^15), and the rest, with the
+        // roundings of the difference and the product and the factor's second part.
+        const float z = t + 49152.f, back = x == top ? 0.f : (top - d) - x;
+        const float low = fmaf(d, c, -t) + fmaf(d, c_low, back * c);
+        const float y = ((t - (z - 49152.f)) + low) * 0.693147180559945f;
+        const uint32_t k = __float_as_uint(z) - 0x47400000u;
+        // 1 - 2^-y in three terms (|y| < 2^-9.4: the next is below 2^-42), as a whole number of 2^-31.
         const float e = y * fmaf(y, fmaf(y, 1.f / 6, -0.5f), 1.f);
-        const uint32_t p = powers[f >> 24];
-        const uint32_t w = p - __umulhi(p, (uint32_t)(e * 4294967296.f));
-        return n < 44 ? ((uint64_t)w << 12) >> n : 0;
+        const int32_t cut = (int32_t)(__float_as_uint(fmaf(e, 2147483648.f, 12582912.f)) - 0x4b400000u);
+        const uint32_t p = powers[k & 255u];
+        const uint64_t w = p - (((int64_t)p * cut) >> 31);
+        return (w << 12) >> (k >> 8);
     }
 };
 
@@ -141,29 +141,39 @@ __device__ __forceinline__ uint64_t part_of(uint64_t w, float f, bool up) {
     return q + (up && rest);
 }
 
-struct Pair {
-    uint64_t mass;
+// What is added up over the cluster.
+struct Sums {
+    uint64_t mass, front;
     uint32_t count;
+};
+// A bin: tokens in front of it and in it, and bounds of their weights.
+struct Found {
+    uint32_t bin, before, in;
+    uint64_t most_before, least_before, most_in, least_in;
 };
 
 template <typename T>
 struct alignas(16) Shared {
-    uint32_t counts[kBins], low[kBins], high[kBins];  // the CTA's histogram: tokens, and sums of weights in two halves
-    uint64_t slice_mass[kBins];   // of this CTA's share of the bins, over the cluster
-    uint32_t slice_count[kBins];
-    uint64_t list[kMost];         // this CTA's gathered tokens: key, then number counted down
-    uint32_t listed;
-    uint64_t all[kMost], weights[kMost];  // the cluster's
+    uint32_t counts[kBins];       // the CTA's histogram
+    union {
+        uint32_t parts[2][kBins]; // sums of weights of some bins, in two halves
+        struct {
+            uint64_t all[kMost], weights[kMost];  // gathered tokens of the whole cluster: key, then number counted down
+        };
+    };
+    uint64_t list[kMost];         // this CTA's
+    uint32_t slice[kBins];        // counts of this CTA's share of the bins, over the cluster
+    uint32_t listed, key_low, key_high;
     uint32_t powers[256];
-    uint64_t mass_slot[4];        // what a step adds up over the cluster
+    uint64_t mass_slot[4][2];     // what a step adds up over the cluster
     uint32_t count_slot[4];
     float max_slot;
     uint32_t number_slot;
-    uint64_t sums[kWarps];
+    uint64_t sums[2][kWarps];
     uint32_t sums32[kWarps];
     uint64_t scan_mass[kWarps];
     uint64_t found_mass, found_border;
-    uint32_t found_bin, found_count, found_rank;
+    Found found;
     long long token;
 };
 
@@ -249,28 +259,30 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
 
     // A step's sums over the cluster: every thread's part in, all of it out, the same everywhere.
     int step = 0;
-    auto add_up = [&](uint64_t mass, uint32_t count) {
-        mass = warp_sum(mass);
+    auto add_up = [&](uint64_t mass, uint64_t front, uint32_t count) {
+        mass = warp_sum(mass), front = warp_sum(front);
         count = __reduce_add_sync(0xffffffffu, count);
         __syncthreads();
-        if (lane == 0) sh.sums[warp] = mass, sh.sums32[warp] = count;
+        if (lane == 0) sh.sums[0][warp] = mass, sh.sums[1][warp] = front, sh.sums32[warp] = count;
         __syncthreads();
         const int slot = step++ & 3;
         if (warp == 0) {
-            mass = warp_sum(lane < kWarps ? sh.sums[lane] : 0);
+            mass = warp_sum(lane < kWarps ? sh.sums[0][lane] : 0), front = warp_sum(lane < kWarps ? sh.sums[1][lane] : 0);
             count = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.sums32[lane] : 0u);
-            if (lane == 0) sh.mass_slot[slot] = mass, sh.count_slot[slot] = count;
+            if (lane == 0) sh.mass_slot[slot][0] = mass, sh.mass_slot[slot][1] = front, sh.count_slot[slot] = count;
         }
         ptx::cluster_sync();
-        Pair all{0, 0};
-        for (int r = 0; r < cluster; ++r) all.mass += ld64(&sh.mass_slot[slot], r), all.count += ld32(&sh.count_slot[slot], r);
+        Sums all{0, 0, 0};
+        for (int r = 0; r < cluster; ++r)
+            all.mass += ld64(&sh.mass_slot[slot][0], r), all.front += ld64(&sh.mass_slot[slot][1], r), all.count += ld32(&sh.count_slot[slot], r);
         return all;
     };
-    // The first token, by number, at which the running sum of `what` over the row exceeds `target` (which is below the
-    // whole sum). A warp has consecutive tokens.
+    // The first token, by number, at which the running sum of `what` over the row exceeds target(the whole sum), which is
+    // below it. A warp has consecutive tokens.
     const int seg = p.chunk / kWarps, s0 = min(warp * seg, n), s1 = min(s0 + seg, n);
-    auto locate = [&](auto what, uint64_t target) -> long long {
+    auto locate = [&](auto what, auto target_of) -> long long {
         uint64_t sum = 0;
+#pragma unroll 4
         for (int i = s0 + lane; i < s1; i += 32) sum += what(i);
         sum = warp_sum(sum);
         __syncthreads();
@@ -278,15 +290,18 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         if (tid == 0) sh.token = -1;
         __syncthreads();
         const int slot = step++ & 3;
-        if (tid == 0) {
-            uint64_t all = 0;
-            for (int w = 0; w < kWarps; ++w) all += sh.scan_mass[w];
-            sh.mass_slot[slot] = all;
+        if (warp == 0) {
+            const uint64_t all = warp_sum(lane < kWarps ? sh.scan_mass[lane] : 0);
+            if (lane == 0) sh.mass_slot[slot][0] = all;
         }
         ptx::cluster_sync();
-        uint64_t before = 0;
-        for (int r = 0; r < rank; ++r) before += ld64(&sh.mass_slot[slot], r);
+        uint64_t before = 0, whole = 0;
+        for (int r = 0; r < cluster; ++r) {
+            const uint64_t x = ld64(&sh.mass_slot[slot][0], r);
+            before += r < rank ? x : 0, whole += x;
+        }
         for (int w = 0; w < warp; ++w) before += sh.scan_mass[w];
+        const uint64_t target = target_of(whole);
         if (before <= target && target < before + sum) {  // in this warp's tokens
             for (int i0 = s0; i0 < s1; i0 += 32) {
                 const uint64_t w = i0 + lane < s1 ? what(i0 + lane) : 0;
@@ -308,6 +323,15 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         long long token = -1;
         for (int r = 0; r < cluster; ++r) token = max(token, (long long)ld64(reinterpret_cast<const uint64_t *>(&sh.token), r));
         return token;
+    };
+    auto block_sum = [&](uint64_t v) {
+        v = warp_sum(v);
+        __syncthreads();
+        if (lane == 0) sh.sums[0][warp] = v;
+        __syncthreads();
+        v = 0;
+        for (int w = 0; w < kWarps; ++w) v += sh.sums[0][w];
+        return v;
     };
 
     const bool nothing = top == -INFINITY;                                     // no token may be drawn
@@ -362,277 +386,278 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
     auto place = [&](uint32_t key, int number) { return (uint64_t)key << 32 | (uint32_t)~number; };
     uint64_t border = 0;  // everything
     const bool need_k = top_k < p.vocab, need_p = top_p < 1.f;
+    auto value_of = [&](uint64_t at) {  // the logit at a place
+        const uint32_t key = (uint32_t)(at >> 32);
+        if constexpr (sizeof(Raw) == 4) return L::value(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+        else return L::value((Raw)(key & 0x8000u ? key & 0x7fffu : ~key));
+    };
+    auto in_front_of_border = [&](int i, uint32_t key) {
+        const uint32_t k = (uint32_t)(border >> 32);
+        return key > k || (key == k && (uint32_t)~(c0 + i) >= (uint32_t)border);
+    };
+    // Tokens of the bins from `from` to `to`, gathered by each CTA and then brought together in every one: sh.all, by their
+    // places. Returns how many (above kMost: not all are there).
+    auto gather = [&](int from, int to) {
+        ptx::cluster_sync();  // the last gathering's lists, and what lies where they come together, have been read
+        if (tid == 0) sh.listed = 0;
+        __syncthreads();
+        for (int i = tid; i < n; i += kThreads) {
+            const int b = bin_of(i);
+            if (b < from || b > to) continue;
+            const uint32_t at = atomicAdd(&sh.listed, 1u);
+            if (at < kMost) sh.list[at] = place(key_of(i), c0 + i);
+        }
+        ptx::cluster_sync();
+        int at = 0;
+        for (int r = 0; r < cluster; ++r) {
+            const int m = (int)ld32(&sh.listed, r);
+            for (int i = tid; i < m && at + i < kMost; i += kThreads) sh.all[at + i] = ld64(&sh.list[i], r);
+            at += m;
+        }
+        __syncthreads();
+        return at;
+    };
+    // The last place that is kept of bin `b`: the one with `k` of the bin's tokens up to it, or the first at which the weights
+    // up to it reach `target`.
+    auto resolve = [&](int b, bool by_mass, uint32_t k, uint64_t target) -> uint64_t {
+        const int m = gather(b, b);
+        if (m <= kMost) {
+            for (int i = tid; i < m; i += kThreads) sh.weights[i] = h.weight(value_of(sh.all[i]), sh.powers);
+            __syncthreads();
+            for (int i = tid; i < m; i += kThreads) {
+                const uint64_t at = sh.all[i];
+                uint64_t in_front = 0;
+                uint32_t ranked = 0;
+#pragma unroll 4
+                for (int j = 0; j < m; ++j)
+                    if (sh.all[j] > at) in_front += sh.weights[j], ++ranked;
+                if (by_mass ? in_front < target && in_front + sh.weights[i] >= target : ranked + 1 == k) sh.found_border = at;
+            }
+            __syncthreads();
+            return sh.found_border;
+        }
+        // Many tokens: the largest key at which what has a larger or equal one is enough, by halving the range of keys.
+        if (tid == 0) sh.key_low = 0xffffffffu, sh.key_high = 0;
+        __syncthreads();
+        uint32_t least = 0xffffffffu, most = 0;
+        for (int i = tid; i < n; i += kThreads)
+            if (bin_of(i) == b) least = min(least, key_of(i)), most = max(most, key_of(i));
+        least = __reduce_min_sync(0xffffffffu, least), most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) atomicMin(&sh.key_low, least), atomicMax(&sh.key_high, most);
+        ptx::cluster_sync();
+        for (int r = 0; r < cluster; ++r) least = min(least, ld32(&sh.key_low, r)), most = max(most, ld32(&sh.key_high, r));
+        uint64_t low = least, high = (uint64_t)most + 1;  // enough at low, not at high
+        uint64_t above_mass = 0;
+        uint32_t above_count = 0;
+        while (high - low > 1) {
+            const uint64_t mid = low + (high - low) / 2;
+            uint64_t sum = 0;
+            uint32_t count = 0;
+            for (int i = tid; i < n; i += kThreads)
+                if (key_of(i) >= mid && bin_of(i) == b) sum += by_mass ? h.weight(L::value(mine[i]), sh.powers) : 0, ++count;
+            const Sums s = add_up(sum, 0, count);
+            if (by_mass ? s.mass >= target : s.count >= k) low = mid;
+            else high = mid, above_mass = s.mass, above_count = s.count;
+        }
+        // Of the tokens with this key, all of one weight, the first ones.
+        const uint32_t key = (uint32_t)low;
+        const uint64_t each = h.weight(value_of((uint64_t)key << 32), sh.powers);
+        const uint64_t wanted = by_mass ? (target - above_mass + each - 1) / each : k - above_count;
+        const long long number = locate([&](int i) { return (uint64_t)(key_of(i) == key); }, [&](uint64_t) { return wanted - 1; });
+        return place(key, (int)number);
+    };
+    // Draws from the tokens of the bins up to `last`, which hold all that is kept, ranked against each other in one CTA.
+    // whole: what top-p is a part of; 0: the sum of the first k, which are all among them.
+    auto draw_from_few = [&](int last, uint64_t whole) {
+        const int m = gather(0, last);
+        if (rank == 0) {
+            for (int i = tid; i < m; i += kThreads) sh.weights[i] = h.weight(value_of(sh.all[i]), sh.powers);
+            __syncthreads();
+            constexpr int kMine = kMost / kThreads;
+            uint64_t in_front[kMine], sum = 0;
+            uint32_t ranked[kMine];
+#pragma unroll
+            for (int e = 0; e < kMine; ++e) {
+                const int i = tid + e * kThreads;
+                in_front[e] = 0, ranked[e] = 0;
+                if (i >= m) continue;
+                const uint64_t at = sh.all[i];
+#pragma unroll 4
+                for (int j = 0; j < m; ++j)
+                    if (sh.all[j] > at) in_front[e] += sh.weights[j], ++ranked[e];
+                if (ranked[e] < (uint32_t)top_k) sum += sh.weights[i];
+            }
+            if (whole == 0) whole = block_sum(sum);
+            const uint64_t target = need_p ? part_of(whole, top_p, true) : ~0ull;
+            sum = 0;
+            bool kept[kMine];
+#pragma unroll
+            for (int e = 0; e < kMine; ++e) {
+                const int i = tid + e * kThreads;
+                kept[e] = i < m && ranked[e] < (uint32_t)top_k && (ranked[e] == 0 || in_front[e] < target) &&
+                          value_of(sh.all[i]) >= floor_x;
+                if (kept[e]) sum += sh.weights[i];
+            }
+            sum = block_sum(sum);
+#pragma unroll
+            for (int e = 0; e < kMine; ++e) {
+                const int i = tid + e * kThreads;
+                if (i < m && !kept[e]) sh.weights[i] = 0;
+            }
+            __syncthreads();
+            const uint64_t drawn = u < 1.f ? part_of(sum, u, false) : sum - 1;
+#pragma unroll
+            for (int e = 0; e < kMine; ++e) {
+                const int i = tid + e * kThreads;
+                if (i >= m || sh.weights[i] == 0) continue;
+                const uint32_t number = ~(uint32_t)sh.all[i];
+                uint64_t before = 0;
+#pragma unroll 4
+                for (int j = 0; j < m; ++j)
+                    if (~(uint32_t)sh.all[j] < number) before += sh.weights[j];
+                if (before <= drawn && drawn < before + sh.weights[i]) p.out[row] = number;
+            }
+        }
+        ptx::cluster_sync();
+    };
+
     if (need_k || need_p) {
         const int share = kBins / cluster;  // bins that this CTA adds up
-        bool with_mass = !need_k;
-        for (;;) {
-            for (int i = tid; i < kBins; i += kThreads) sh.counts[i] = sh.low[i] = sh.high[i] = 0;
-            if (tid == 0) sh.listed = 0;
+        for (int i = tid; i < kBins; i += kThreads) sh.counts[i] = 0;
+        __syncthreads();
+#pragma unroll 4
+        for (int i = tid; i < n; i += kThreads) {
+            const int b = bin_of(i);
+            if (b < kBins) atomicAdd(&sh.counts[b], 1u);
+        }
+        ptx::cluster_sync();
+        for (int i = tid; i < share; i += kThreads) {
+            uint32_t count = 0;
+            for (int r = 0; r < cluster; ++r) count += ld32(&sh.counts[rank * share + i], r);
+            sh.slice[i] = count;
+        }
+        ptx::cluster_sync();
+        // All bins, in every CTA: a thread has kEach of them, in their order. With bounds of their weights, wide enough for
+        // the bins' own rounding.
+        constexpr int kEach = kBins / kThreads;
+        uint64_t most[kEach], least[kEach], my_most = 0, my_least = 0;
+        uint32_t count[kEach], my_count = 0;
+        auto edge = [&](int b) { return b >> 5 < 44 ? ((uint64_t)sh.powers[(b & 31) * 8] << 12) >> (b >> 5) : 0; };
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int b = tid * kEach + e;
+            count[e] = ld32(&sh.slice[b % share], b / share);
+            const uint64_t up = edge(b), down = edge(b + 1);
+            most[e] = count[e] * (up + (up >> 16) + 1), least[e] = count[e] * (down - (down >> 16) - (down > 0));
+            my_count += count[e], my_most += most[e], my_least += least[e];
+        }
+        // Sums of two such sets over the bins in front of the thread's, and over all.
+        auto in_front = [&](uint64_t a, uint64_t b, uint64_t *a_all, uint64_t *b_all, uint64_t *b_front) {
+            uint64_t x = a, y = b;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint64_t v = __shfl_up_sync(0xffffffffu, x, o), w = __shfl_up_sync(0xffffffffu, y, o);
+                if (lane >= o) x += v, y += w;
+            }
             __syncthreads();
+            if (lane == 31) sh.sums[0][warp] = x, sh.sums[1][warp] = y;
+            __syncthreads();
+            x -= a, y -= b, *a_all = 0, *b_all = 0;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) x += sh.sums[0][w], y += sh.sums[1][w];
+                *a_all += sh.sums[0][w], *b_all += sh.sums[1][w];
+            }
+            *b_front = y;
+            return x;
+        };
+        uint64_t all_most, all_least, all_count, none, before_least, none2;
+        const uint64_t before_most = in_front(my_most, my_least, &all_most, &all_least, &before_least);
+        const uint64_t before_count = in_front(my_count, 0, &all_count, &none, &none2);
+        // The first bin at which the running sum of `each` (from `before` at the thread's first bin) reaches `target`; kBins: none.
+        auto find = [&](uint64_t before, auto each, uint64_t target) {
+            __syncthreads();
+            if (tid == 0) sh.found.bin = kBins;
+            __syncthreads();
+            uint64_t x = before, c = before_count, m = before_most, l = before_least;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                if (x < target && x + each(e) >= target)
+                    sh.found = Found{(uint32_t)(tid * kEach + e), (uint32_t)c, count[e], m, l, most[e], least[e]}, sh.found_mass = x;
+                x += each(e), c += count[e], m += most[e], l += least[e];
+            }
+            __syncthreads();
+            return sh.found;
+        };
+        int bin_k = kBins;
+        uint64_t whole_least = all_least, whole_most = all_most;
+        if (need_k && (uint64_t)top_k < all_count) {
+            const Found f = find(before_count, [&](int e) { return (uint64_t)count[e]; }, (uint64_t)top_k);
+            bin_k = (int)f.bin;
+            if (f.before + f.in <= kMost) {
+                draw_from_few(bin_k, 0);
+                return;
+            }
+            whole_least = f.least_before, whole_most = f.most_before + f.most_in;
+            border = resolve(bin_k, false, (uint32_t)top_k - f.before, 0);
+        } else if (all_count <= kMost) {
+            draw_from_few(kBins - 1, 0);
+            return;
+        }
+        if (need_p) {
+            // The border lies in one of these bins.
+            const Found first = find(before_most, [&](int e) { return most[e]; }, max(part_of(whole_least, top_p, true), (uint64_t)1));
+            const Found last = find(before_least, [&](int e) { return least[e]; }, part_of(whole_most, top_p, true));
+            const int from = min((int)first.bin, kBins - 1), to = max(from, min((int)last.bin, min(bin_k, kBins - 1)));
+            ptx::cluster_sync();  // nobody looks at gathered tokens any more
+            for (int b = from + tid; b <= to; b += kThreads) sh.parts[0][b] = sh.parts[1][b] = 0;
+            __syncthreads();
+            uint64_t sum = 0, front = 0;
+#pragma unroll 4
             for (int i = tid; i < n; i += kThreads) {
+                const float v = L::value(mine[i]);
+                if (border != 0 && !in_front_of_border(i, key_of(i))) continue;
+                const uint64_t w = h.weight(v, sh.powers);
                 const int b = bin_of(i);
-                if (b >= kBins) continue;
-                atomicAdd(&sh.counts[b], 1u);
-                if (with_mass) {
-                    const uint64_t w = h.weight(L::value(mine[i]), sh.powers);
-                    const uint32_t old = atomicAdd(&sh.low[b], (uint32_t)w);
-                    const uint32_t up = (uint32_t)(w >> 32) + (old + (uint32_t)w < old);
-                    if (up) atomicAdd(&sh.high[b], up);
+                sum += w;
+                if (b < from) {
+                    front += w;
+                } else if (b <= to) {
+                    const uint32_t old = atomicAdd(&sh.parts[0][b], (uint32_t)w), up = (uint32_t)(w >> 32) + (old + (uint32_t)w < old);
+                    if (up) atomicAdd(&sh.parts[1][b], up);
                 }
             }
-            ptx::cluster_sync();
-            for (int i = tid; i < share; i += kThreads) {
-                uint64_t mass = 0;
-                uint32_t count = 0;
-                for (int r = 0; r < cluster; ++r) {
-                    count += ld32(&sh.counts[rank * share + i], r);
-                    if (with_mass) mass += (uint64_t)ld32(&sh.high[rank * share + i], r) << 32 | 0, mass += ld32(&sh.low[rank * share + i], r);
-                }
-                sh.slice_mass[i] = mass, sh.slice_count[i] = count;
-            }
-            ptx::cluster_sync();
-            // All bins' sums, in every CTA: a thread has kBins / kThreads of them, in their order.
-            constexpr int kEach = kBins / kThreads;
-            uint64_t mass[kEach];
-            uint32_t count[kEach];
-            uint64_t my_mass = 0;
-            uint32_t my_count = 0;
+            const Sums s = add_up(sum, front, 0);
+            uint64_t mass[kEach], my_mass = 0, all_mass;
 #pragma unroll
             for (int e = 0; e < kEach; ++e) {
                 const int b = tid * kEach + e;
-                count[e] = ld32(&sh.slice_count[b % share], b / share);
-                mass[e] = with_mass ? ld64(&sh.slice_mass[b % share], b / share) : 0;
-                my_mass += mass[e], my_count += count[e];
+                mass[e] = 0;
+                if (b >= from && b <= to)
+                    for (int r = 0; r < cluster; ++r) mass[e] += ((uint64_t)ld32(&sh.parts[1][b], r) << 32) + ld32(&sh.parts[0][b], r);
+                my_mass += mass[e];
             }
-            uint64_t upto_mass = my_mass;
-            uint32_t upto_count = my_count;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint64_t a = __shfl_up_sync(0xffffffffu, upto_mass, o);
-                const uint32_t b = __shfl_up_sync(0xffffffffu, upto_count, o);
-                if (lane >= o) upto_mass += a, upto_count += b;
-            }
-            if (lane == 31) sh.sums[warp] = upto_mass, sh.sums32[warp] = upto_count;
-            __syncthreads();
-            uint64_t all_mass = 0, before_mass = upto_mass - my_mass;
-            uint32_t all_count = 0, before_count = upto_count - my_count;
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < warp) before_mass += sh.sums[w], before_count += sh.sums32[w];
-                all_mass += sh.sums[w], all_count += sh.sums32[w];
-            }
-            // The bin in which the count reaches `k`, or the mass `target`: found_bin, and what lies in front of it.
-            auto find = [&](bool by_mass, uint32_t k, uint64_t target) {
-                __syncthreads();
-                if (tid == 0) sh.found_bin = kBins;
-                __syncthreads();
-                uint64_t m = before_mass;
-                uint32_t c = before_count;
-#pragma unroll
-                for (int e = 0; e < kEach; ++e) {
-                    const bool in_front = by_mass ? m < target : c < k;
-                    const bool reached = by_mass ? m + mass[e] >= target : c + count[e] >= k;
-                    if (in_front && reached) sh.found_bin = tid * kEach + e, sh.found_mass = m, sh.found_count = c, sh.found_rank = count[e];
-                    m += mass[e], c += count[e];
+            const uint64_t before_mass = s.front + in_front(my_mass, 0, &all_mass, &none, &none2);
+            const uint64_t target = part_of(s.mass, top_p, true);
+            // (The bins in front of these have no mass here: what is in them is in s.front.)
+            const Found f = find(before_mass, [&](int e) { return mass[e]; }, target);
+            const uint64_t reached = sh.found_mass;
+            if (f.bin < kBins) {
+                if (border == 0 && f.before + f.in <= kMost) {
+                    draw_from_few((int)f.bin, s.mass);
+                    return;
                 }
-                __syncthreads();
-            };
-            // Tokens of the bins from `from` to `to`, gathered by each CTA and then brought together in every one: sh.all,
-            // by their places. Returns how many (above kMost: none gathered).
-            auto gather = [&](int from, int to) {
-                ptx::cluster_sync();  // the last gathering's lists have been read
-                if (tid == 0) sh.listed = 0;
-                __syncthreads();
-                for (int i = tid; i < n; i += kThreads) {
-                    const int b = bin_of(i);
-                    if (b < from || b > to) continue;
-                    const uint32_t at = atomicAdd(&sh.listed, 1u);
-                    if (at < kMost) sh.list[at] = place(key_of(i), c0 + i);
-                }
-                ptx::cluster_sync();
-                int at = 0;
-                for (int r = 0; r < cluster; ++r) {
-                    const int m = (int)ld32(&sh.listed, r);
-                    for (int i = tid; i < m && at + i < kMost; i += kThreads) sh.all[at + i] = ld64(&sh.list[i], r);
-                    at += m;
-                }
-                __syncthreads();
-                return at;
-            };
-            auto value_of = [&](uint64_t at) {  // the logit at a place
-                const uint32_t key = (uint32_t)(at >> 32);
-                if constexpr (sizeof(Raw) == 4) return L::value(key & 0x80000000u ? key & 0x7fffffffu : ~key);
-                else return L::value((Raw)(key & 0x8000u ? key & 0x7fffu : ~key));
-            };
-
-            uint32_t before_k = 0, in_k = 0;
-            int bin_k = kBins;
-            if (need_k && (uint32_t)top_k < all_count) {
-                find(false, (uint32_t)top_k, 0);
-                bin_k = (int)sh.found_bin, before_k = sh.found_count, in_k = sh.found_rank;
+                const uint64_t at = resolve((int)f.bin, true, 0, target - reached);
+                border = border > at ? border : at;
             }
-            // The last bin of interest and the tokens up to it.
-            int bin_last = bin_k;
-            uint32_t tokens = bin_k < kBins ? before_k + in_k : all_count;
-            if (!need_k) {  // all_mass is the whole
-                find(true, 0, part_of(all_mass, top_p, true));
-                if (sh.found_bin < kBins) bin_last = (int)sh.found_bin, tokens = sh.found_count + sh.found_rank;
-            }
-            if (tokens <= kMost) {
-                // ------------------------------------------------ few: ranked against each other
-                const int m = gather(0, min(bin_last, kBins - 1));
-                if (rank == 0) {
-                    for (int i = tid; i < m; i += kThreads) sh.weights[i] = h.weight(value_of(sh.all[i]), sh.powers);
-                    __syncthreads();
-                    constexpr int kMine = kMost / kThreads;
-                    uint64_t in_front[kMine];
-                    uint32_t ranked[kMine];
-                    uint64_t sum = 0;
-#pragma unroll
-                    for (int e = 0; e < kMine; ++e) {
-                        const int i = tid + e * kThreads;
-                        in_front[e] = 0, ranked[e] = 0;
-                        if (i >= m) continue;
-                        const uint64_t at = sh.all[i];
-#pragma unroll 4
-                        for (int j = 0; j < m; ++j)
-                            if (sh.all[j] > at) in_front[e] += sh.weights[j], ++ranked[e];
-                        if (ranked[e] < (uint32_t)top_k) sum += sh.weights[i];
-                    }
-                    auto block_sum = [&](uint64_t v) {
-                        v = warp_sum(v);
-                        __syncthreads();
-                        if (lane == 0) sh.sums[warp] = v;
-                        __syncthreads();
-                        v = 0;
-                        for (int w = 0; w < kWarps; ++w) v += sh.sums[w];
-                        return v;
-                    };
-                    // Of the first k the whole is their sum; without top-k it is that of all tokens.
-                    const uint64_t whole = need_k ? block_sum(sum) : all_mass;
-                    const uint64_t target = need_p ? part_of(whole, top_p, true) : ~0ull;
-                    sum = 0;
-                    bool kept[kMine];
-#pragma unroll
-                    for (int e = 0; e < kMine; ++e) {
-                        const int i = tid + e * kThreads;
-                        kept[e] = i < m && ranked[e] < (uint32_t)top_k && (ranked[e] == 0 || in_front[e] < target) &&
-                                  value_of(sh.all[i]) >= floor_x;
-                        if (kept[e]) sum += sh.weights[i];
-                    }
-                    sum = block_sum(sum);
-#pragma unroll
-                    for (int e = 0; e < kMine; ++e) {
-                        const int i = tid + e * kThreads;
-                        if (i < m && !kept[e]) sh.weights[i] = 0;
-                    }
-                    __syncthreads();
-                    const uint64_t drawn = u < 1.f ? part_of(sum, u, false) : sum - 1;
-#pragma unroll
-                    for (int e = 0; e < kMine; ++e) {
-                        const int i = tid + e * kThreads;
-                        if (i >= m || sh.weights[i] == 0) continue;
-                        const uint32_t number = ~(uint32_t)sh.all[i];
-                        uint64_t before = 0;
-#pragma unroll 4
-                        for (int j = 0; j < m; ++j)
-                            if (~(uint32_t)sh.all[j] < number) before += sh.weights[j];
-                        if (before <= drawn && drawn < before + sh.weights[i]) p.out[row] = number;
-                    }
-                }
-                ptx::cluster_sync();
-                return;
-            }
-            if (need_p && !with_mass) {  // again, with sums of weights
-                with_mass = true;
-                ptx::cluster_sync();
-                continue;
-            }
-            // ---------------------------------------------------- many: the border in its bin
-            // Finds in bin `b` the last place that is kept: the one with `k` tokens of the bin in front of and including it, or
-            // the first at which the mass in the bin reaches `target`. Returns its place and the bin's mass up to it.
-            auto resolve = [&](int b, bool by_mass, uint32_t k, uint64_t target, uint64_t *upto) -> uint64_t {
-                const int m = gather(b, b);
-                if (m <= kMost) {
-                    for (int i = tid; i < m; i += kThreads) sh.weights[i] = h.weight(value_of(sh.all[i]), sh.powers);
-                    __syncthreads();
-                    for (int i = tid; i < m; i += kThreads) {
-                        const uint64_t at = sh.all[i];
-                        uint64_t in_front = 0;
-                        uint32_t ranked = 0;
-                        for (int j = 0; j < m; ++j)
-                            if (sh.all[j] > at) in_front += sh.weights[j], ++ranked;
-                        const bool last = by_mass ? in_front < target && in_front + sh.weights[i] >= target : ranked + 1 == k;
-                        if (last) sh.found_border = at, sh.found_mass = in_front + sh.weights[i];
-                    }
-                    __syncthreads();
-                    *upto = sh.found_mass;
-                    const uint64_t at = sh.found_border;
-                    __syncthreads();
-                    return at;
-                }
-                // Many tokens in the bin: the largest key at which what has a larger or equal one is enough, by halving.
-                uint64_t low = 0, high = 1ull << L::kBits;  // enough at low, not at high
-                uint64_t above_mass = 0;
-                uint32_t above_count = 0;
-                while (high - low > 1) {
-                    const uint64_t mid = low + (high - low) / 2;
-                    uint64_t sum = 0;
-                    uint32_t count_here = 0;
-                    for (int i = tid; i < n; i += kThreads)
-                        if (bin_of(i) == b && key_of(i) >= mid) sum += by_mass ? h.weight(L::value(mine[i]), sh.powers) : 0, ++count_here;
-                    const Pair s = add_up(sum, count_here);
-                    if (by_mass ? s.mass >= target : s.count >= k) low = mid;
-                    else high = mid, above_mass = s.mass, above_count = s.count;
-                }
-                // Of the tokens with this key, all of one weight, the first ones.
-                const uint32_t key = (uint32_t)low;
-                const uint64_t each = h.weight(value_of((uint64_t)key << 32), sh.powers);
-                const uint64_t wanted = by_mass ? (target - above_mass + each - 1) / each : k - above_count;
-                const long long number = locate([&](int i) { return (uint64_t)(key_of(i) == key); }, wanted - 1);
-                if (!by_mass) {  // the sum of what lies above was not asked for
-                    uint64_t sum = 0;
-                    for (int i = tid; i < n; i += kThreads)
-                        if (bin_of(i) == b && key_of(i) > key) sum += h.weight(L::value(mine[i]), sh.powers);
-                    above_mass = add_up(sum, 0).mass;
-                }
-                *upto = above_mass + wanted * each;
-                return place(key, (int)number);
-            };
-            uint64_t whole = all_mass, in_bin = 0;
-            if (bin_k < kBins) {
-                find(false, (uint32_t)top_k, 0);
-                const uint64_t in_front = sh.found_mass;
-                const uint32_t first = sh.found_count;
-                border = resolve(bin_k, false, (uint32_t)top_k - first, 0, &in_bin);
-                whole = in_front + in_bin;  // with need_p the histogram has sums
-            }
-            if (need_p) {
-                const uint64_t target = part_of(whole, top_p, true);
-                find(true, 0, target);
-                if (sh.found_bin < kBins) {
-                    const int b = (int)sh.found_bin;
-                    const uint64_t in_front = sh.found_mass;
-                    const uint64_t at = resolve(b, true, 0, target - in_front, &in_bin);
-                    border = border > at ? border : at;
-                }
-            }
-            break;
         }
     }
 
     // ---------------------------------------------------------------- the sum of what is kept, and the token
-    const uint32_t border_key = (uint32_t)(border >> 32);
     auto kept = [&](int i) -> uint64_t {
         const float v = L::value(mine[i]);
-        if (!(v >= floor_x)) return 0;
-        const uint32_t key = key_of(i);
-        if (key < border_key || (key == border_key && (uint32_t)~(c0 + i) < (uint32_t)border)) return 0;
-        return h.weight(v, sh.powers);
+        return v >= floor_x && (border == 0 || in_front_of_border(i, key_of(i))) ? h.weight(v, sh.powers) : 0;
     };
-    uint64_t sum = 0;
-    for (int i = tid; i < n; i += kThreads) sum += kept(i);
-    sum = add_up(sum, 0).mass;
-    const long long token = locate(kept, u < 1.f ? part_of(sum, u, false) : sum - 1);
+    const long long token = locate(kept, [&](uint64_t whole) { return u < 1.f ? part_of(whole, u, false) : whole - 1; });
     if (rank == 0 && tid == 0) p.out[row] = token;
     ptx::cluster_sync();
 }
@@ -642,7 +667,7 @@ cudaError_t launch(SampleParams p, int rows, int sms, cudaStream_t s) {
     // CTAs of a row: as many as its tokens need room, and as many as there are SMs for.
     const int room = (int)((size_t)96 * 1024 / sizeof(T));
     int cluster = 1;
-    while (cluster < kMaxCluster && ((p.vocab + cluster - 1) / cluster > room || (rows * cluster * 2 <= 2 * sms && p.vocab > 4096 * cluster)))
+    while (cluster < kMaxCluster && ((p.vocab + cluster - 1) / cluster > room || (rows * cluster <= 2 * sms && p.vocab > 4096 * cluster)))
         cluster *= 2;
     p.chunk = ((p.vocab + cluster - 1) / cluster + kThreads - 1) / kThreads * kThreads;
     const int smem = (int)sizeof(Shared<T>) + (p.chunk + 16) * (int)sizeof(T);
