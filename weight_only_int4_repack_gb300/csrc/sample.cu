@@ -35,7 +35,7 @@ struct SampleParams {
     const float *u, *temperature, *top_p, *min_p;
     const int32_t *top_k;
     int64_t *out;
-    int vocab, chunk;  // tokens of a CTA, a multiple of kThreads
+    int vocab, chunk;  // tokens of a CTA
     unsigned int *err;
 };
 
@@ -58,19 +58,18 @@ __constant__ Table kPowers = make_table();
 
 // A row's weights.
 struct Heat {
-    float top, c, c_low;  // largest logit; log2(e) / temperature in two parts
-    __device__ __forceinline__ float down(float x) const { return x == top ? 0.f : top - x; }
-    // How far below the largest, in factors of two; NaN and what is far below: 64 and more.
-    __device__ __forceinline__ float octaves(float x) const {
-        const float t = down(x) * c;
-        return t < 64.f ? t : 64.f;
+    float top, c, c_low;  // largest logit (finite); log2(e) / temperature in two parts
+    // 32 bins for each factor of two below the largest, to the nearest; kBins: NaN, and what is 64 factors below or more.
+    __device__ __forceinline__ int bin(float x) const {
+        const float t = fminf((top - x) * (c * kPerOctave), (float)kBins);
+        return (int)(__float_as_uint(t + 12582912.f) - 0x4b400000u);
     }
     __device__ __forceinline__ uint64_t weight(float x, const uint32_t *powers) const {
-        const float d = down(x), t = d * c;
+        const float d = top - x, t = d * c;
         if (!(t < 44.f)) return 0;
         // In 256th factors of two: the nearest whole number (the bits of a sum with 1.5 * 2^15), and the rest, with the
         // roundings of the difference and the product and the factor's second part.
-        const float z = t + 49152.f, back = x == top ? 0.f : (top - d) - x;
+        const float z = t + 49152.f, back = (top - d) - x;
         const float low = fmaf(d, c, -t) + fmaf(d, c_low, back * c);
         const float y = ((t - (z - 49152.f)) + low) * 0.693147180559945f;
         const uint32_t k = __float_as_uint(z) - 0x47400000u;
@@ -88,7 +87,6 @@ template <typename T>
 struct Logit;
 template <>
 struct Logit<float> {
-    static constexpr int kBits = 32;
     using Raw = uint32_t;
     static __device__ __forceinline__ float value(Raw r) { return __uint_as_float(r); }
     static __device__ __forceinline__ uint32_t key(Raw r) {
@@ -98,7 +96,6 @@ struct Logit<float> {
 };
 template <typename H>
 struct Logit16 {
-    static constexpr int kBits = 16;
     using Raw = uint16_t;
     static __device__ __forceinline__ float value(Raw r) { return elem::pair_to_f32<H>(r).x; }
     static __device__ __forceinline__ uint32_t key(Raw r) {
@@ -154,14 +151,16 @@ struct Found {
 
 template <typename T>
 struct alignas(16) Shared {
-    uint32_t counts[kBins];       // the CTA's histogram
+    union {
+        uint32_t counts[kBins];   // the CTA's histogram
+        uint64_t list[kMost];     // its gathered tokens
+    };
     union {
         uint32_t parts[2][kBins]; // sums of weights of some bins, in two halves
         struct {
             uint64_t all[kMost], weights[kMost];  // gathered tokens of the whole cluster: key, then number counted down
         };
     };
-    uint64_t list[kMost];         // this CTA's
     uint32_t slice[kBins];        // counts of this CTA's share of the bins, over the cluster
     uint32_t listed, key_low, key_high;
     uint32_t powers[256];
@@ -171,14 +170,15 @@ struct alignas(16) Shared {
     uint32_t number_slot;
     uint64_t sums[2][kWarps];
     uint32_t sums32[kWarps];
-    uint64_t scan_mass[kWarps];
+    int owner;                    // a thread, and what lies in front of its tokens
+    uint64_t owner_before;
     uint64_t found_mass, found_border;
     Found found;
     long long token;
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
     using L = Logit<T>;
     using Raw = typename L::Raw;
     extern __shared__ __align__(16) unsigned char raw_smem[];
@@ -191,8 +191,25 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
     const int c0 = min(rank * p.chunk, p.vocab), n = min(p.chunk, p.vocab - c0);  // this CTA's tokens
     const Raw *x = static_cast<const Raw *>(p.x) + row * p.row + c0;
     constexpr int kVec = 16 / sizeof(Raw);
-    const int skew = (int)((uintptr_t)x % 16 / sizeof(Raw));
-    Raw *mine = reinterpret_cast<Raw *>(raw_smem + sizeof(Shared<T>)) + skew;  // token c0 + i at mine[i]
+    // Shared memory is skewed as the row is, so that both are read 16 bytes at a time: token c0 + i at mine[i], its vectors from
+    // mine[-skew] on. What the first and the last vector have besides is NaN, which is nothing to all that follows.
+    const int skew = (int)((uintptr_t)x % 16 / sizeof(Raw)), vectors = n > 0 ? (skew + n + kVec - 1) / kVec : 0;
+    Raw *mine = reinterpret_cast<Raw *>(raw_smem + sizeof(Shared<T>)) + skew;
+    uint4 *const packed = reinterpret_cast<uint4 *>(raw_smem + sizeof(Shared<T>));
+    constexpr Raw kNone = sizeof(Raw) == 4 ? (Raw)0x7fffffffu : (Raw)0x7fffu;
+    auto unpacked = [&](const uint4 &v, int z) -> Raw {
+        const uint32_t w = z * sizeof(Raw) / 4 == 0 ? v.x : z * sizeof(Raw) / 4 == 1 ? v.y : z * sizeof(Raw) / 4 == 2 ? v.z : v.w;
+        return sizeof(Raw) == 4 ? (Raw)w : (Raw)(z & 1 ? w >> 16 : w);
+    };
+    // f(i, raw) for this CTA's tokens.
+    auto each_token = [&](auto f) {
+#pragma unroll 1
+        for (int v = tid; v < vectors; v += kThreads) {
+            const uint4 q = packed[v];
+#pragma unroll
+            for (int z = 0; z < kVec; ++z) f(v * kVec - skew + z, unpacked(q, z));
+        }
+    };
 
     // What the row asks for.
     float heat = p.temperature ? p.temperature[row] : 1.f, top_p = p.top_p ? p.top_p[row] : 1.f, min_p = p.min_p ? p.min_p[row] : 0.f;
@@ -210,30 +227,19 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
     if (tid < 256) sh.powers[tid] = kPowers.v[tid];
     float top = -INFINITY;
     {
-        const int blocks = (skew + n + kVec - 1) / kVec;
 #pragma unroll 4
-        for (int b = tid; b < blocks; b += kThreads) {
-            const int i = b * kVec - skew;
+        for (int v = tid; v < vectors; v += kThreads) {
+            const int i = v * kVec - skew;
+            uint4 q;
             if (i >= 0 && i + kVec <= n) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(x + i);
-                *reinterpret_cast<uint4 *>(mine + i) = v;
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    if constexpr (sizeof(Raw) == 4) {
-                        top = fmaxf(top, __uint_as_float(w[z]));
-                    } else {
-                        const float2 f = elem::pair_to_f32<T>(w[z]);
-                        top = fmaxf(top, fmaxf(f.x, f.y));
-                    }
-                }
+                q = *reinterpret_cast<const uint4 *>(x + i);
+                packed[v] = q;
             } else {
-                for (int j = max(i, 0); j < min(i + kVec, n); ++j) {
-                    const Raw r = x[j];
-                    mine[j] = r;
-                    top = fmaxf(top, L::value(r));
-                }
+                for (int j = i; j < i + kVec; ++j) mine[j] = j >= 0 && j < n ? x[j] : kNone;
+                q = packed[v];
             }
+#pragma unroll
+            for (int z = 0; z < kVec; ++z) top = fmaxf(top, L::value(unpacked(q, z)));
         }
     }
     auto warp_max = [](float v) {
@@ -277,46 +283,62 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
             all.mass += ld64(&sh.mass_slot[slot][0], r), all.front += ld64(&sh.mass_slot[slot][1], r), all.count += ld32(&sh.count_slot[slot], r);
         return all;
     };
-    // The first token, by number, at which the running sum of `what` over the row exceeds target(the whole sum), which is
-    // below it. A warp has consecutive tokens.
-    const int seg = p.chunk / kWarps, s0 = min(warp * seg, n), s1 = min(s0 + seg, n);
+    // The first token, by number, at which the running sum of what(i, raw) over the row exceeds target(the whole sum), which is
+    // below it. A thread has consecutive tokens (an odd number of vectors: no bank conflicts).
+    const int per = ((vectors + kThreads - 1) / kThreads) | 1, v0 = min(tid * per, vectors), v1 = min(v0 + per, vectors);
     auto locate = [&](auto what, auto target_of) -> long long {
         uint64_t sum = 0;
-#pragma unroll 4
-        for (int i = s0 + lane; i < s1; i += 32) sum += what(i);
-        sum = warp_sum(sum);
+#pragma unroll 1
+        for (int v = v0; v < v1; ++v) {
+            const uint4 q = packed[v];
+#pragma unroll
+            for (int z = 0; z < kVec; ++z) sum += what(v * kVec - skew + z, unpacked(q, z));
+        }
+        uint64_t upto = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
         __syncthreads();
-        if (lane == 0) sh.scan_mass[warp] = sum;
-        if (tid == 0) sh.token = -1;
+        if (lane == 31) sh.sums[0][warp] = upto;
+        if (tid == 0) sh.token = -1, sh.owner = -1;
         __syncthreads();
         const int slot = step++ & 3;
-        if (warp == 0) {
-            const uint64_t all = warp_sum(lane < kWarps ? sh.scan_mass[lane] : 0);
-            if (lane == 0) sh.mass_slot[slot][0] = all;
+        uint64_t mine_all = 0, before = upto - sum;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const uint64_t y = sh.sums[0][w];
+            before += w < warp ? y : 0, mine_all += y;
         }
+        if (tid == 0) sh.mass_slot[slot][0] = mine_all;
         ptx::cluster_sync();
-        uint64_t before = 0, whole = 0;
+        uint64_t whole = 0;
         for (int r = 0; r < cluster; ++r) {
-            const uint64_t x = ld64(&sh.mass_slot[slot][0], r);
-            before += r < rank ? x : 0, whole += x;
+            const uint64_t y = ld64(&sh.mass_slot[slot][0], r);
+            before += r < rank ? y : 0, whole += y;
         }
-        for (int w = 0; w < warp; ++w) before += sh.scan_mass[w];
         const uint64_t target = target_of(whole);
-        if (before <= target && target < before + sum) {  // in this warp's tokens
-            for (int i0 = s0; i0 < s1; i0 += 32) {
-                const uint64_t w = i0 + lane < s1 ? what(i0 + lane) : 0;
-                uint64_t upto = w;
+        if (before <= target && target < before + sum) sh.owner = tid, sh.owner_before = before;
+        __syncthreads();
+        if (warp == 0 && sh.owner >= 0) {  // a strip of 32 tokens at a time
+            uint64_t front = sh.owner_before;
+            const int first = sh.owner * per * kVec - skew, last = min(first + per * kVec, n);
+            for (int i0 = first; i0 < last; i0 += 32) {
+                const int i = i0 + lane;
+                const uint64_t w = i >= 0 && i < last ? what(i, mine[i]) : 0;
+                uint64_t run = w;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const uint64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-                    if (lane >= o) upto += y;
+                    const uint64_t y = __shfl_up_sync(0xffffffffu, run, o);
+                    if (lane >= o) run += y;
                 }
-                const uint32_t mask = __ballot_sync(0xffffffffu, before + upto > target);
+                const uint32_t mask = __ballot_sync(0xffffffffu, front + run > target);
                 if (mask) {
                     if (lane == 0) sh.token = c0 + i0 + __ffs(mask) - 1;
                     break;
                 }
-                before += __shfl_sync(0xffffffffu, upto, 31);
+                front += __shfl_sync(0xffffffffu, run, 31);
             }
         }
         ptx::cluster_sync();
@@ -324,26 +346,14 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         for (int r = 0; r < cluster; ++r) token = max(token, (long long)ld64(reinterpret_cast<const uint64_t *>(&sh.token), r));
         return token;
     };
-    auto block_sum = [&](uint64_t v) {
-        v = warp_sum(v);
-        __syncthreads();
-        if (lane == 0) sh.sums[0][warp] = v;
-        __syncthreads();
-        v = 0;
-        for (int w = 0; w < kWarps; ++w) v += sh.sums[0][w];
-        return v;
-    };
-
     const bool nothing = top == -INFINITY;                                     // no token may be drawn
     const bool greedy = heat == 0.f || top_k == 1 || top_p <= 0.f || min_p > 1.f;  // the largest logit, the first of equal ones
     if (nothing || greedy) {
         uint32_t first = 0xffffffffu;
         if (!nothing)
-            for (int i = tid; i < n; i += kThreads)
-                if (L::value(mine[i]) == top) {
-                    first = c0 + i;
-                    break;
-                }
+            each_token([&](int i, Raw r) {
+                if (L::value(r) == top) first = min(first, (uint32_t)(c0 + i));
+            });
         first = __reduce_min_sync(0xffffffffu, first);
         __syncthreads();
         if (lane == 0) sh.sums32[warp] = first;
@@ -361,25 +371,24 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         return;
     }
 
+    if (top == INFINITY) {  // these alone, all alike
+        for (int i = tid; i < n; i += kThreads) mine[i] = L::value(mine[i]) == INFINITY ? (Raw)0 : kNone;
+        top = 0.f;
+        __syncthreads();
+    }
     Heat h;
     {
         const double c = 1.4426950408889634 / (double)heat;
         h.top = top;
-        h.c = c < 3e38 ? (float)c : 3e38f;
-        h.c_low = c < 3e38 ? (float)(c - (double)h.c) : 0.f;
+        h.c = c < 1e37 ? (float)c : 1e37f;  // (32 times that is still a number)
+        h.c_low = c < 1e37 ? (float)(c - (double)h.c) : 0.f;
     }
     // The smallest logit that min-p leaves, rounded up.
     float floor_x = -INFINITY;
-    if (min_p > 0.f && top < INFINITY) {
+    if (min_p > 0.f) {
         const double cut = (double)top + (double)heat * log((double)min_p);
         if (cut == cut) floor_x = __double2float_ru(cut);
     }
-    auto key_of = [&](int i) { return L::key(mine[i]); };
-    auto bin_of = [&](int i) {
-        const float t = h.octaves(L::value(mine[i]));
-        return t < 64.f ? (int)(t * kPerOctave) : kBins;
-    };
-
     // ---------------------------------------------------------------- the border of top-k and top-p
     // Kept is what lies in front of the border in the order of falling keys, equal ones by number, the border included:
     // a 64-bit number, larger for what comes first.
@@ -395,18 +404,21 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         const uint32_t k = (uint32_t)(border >> 32);
         return key > k || (key == k && (uint32_t)~(c0 + i) >= (uint32_t)border);
     };
+    uint32_t key_least = 0, key_most = 0;  // of the tokens that this thread has gathered
     // Tokens of the bins from `from` to `to`, gathered by each CTA and then brought together in every one: sh.all, by their
     // places. Returns how many (above kMost: not all are there).
     auto gather = [&](int from, int to) {
         ptx::cluster_sync();  // the last gathering's lists, and what lies where they come together, have been read
         if (tid == 0) sh.listed = 0;
         __syncthreads();
-        for (int i = tid; i < n; i += kThreads) {
-            const int b = bin_of(i);
-            if (b < from || b > to) continue;
-            const uint32_t at = atomicAdd(&sh.listed, 1u);
-            if (at < kMost) sh.list[at] = place(key_of(i), c0 + i);
-        }
+        key_least = 0xffffffffu, key_most = 0;
+        each_token([&](int i, Raw r) {
+            const int b = h.bin(L::value(r));
+            if (b < from || b > to) return;
+            const uint32_t key = L::key(r), at = atomicAdd(&sh.listed, 1u);
+            key_least = min(key_least, key), key_most = max(key_most, key);
+            if (at < kMost) sh.list[at] = place(key, c0 + i);
+        });
         ptx::cluster_sync();
         int at = 0;
         for (int r = 0; r < cluster; ++r) {
@@ -417,32 +429,62 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         __syncthreads();
         return at;
     };
+    // sh.all[0 .. m) in falling order (by pairs of elements, a pair to a thread).
+    auto sort = [&](int m) {
+        int padded = 2;
+        while (padded < m) padded *= 2;
+        for (int i = m + tid; i < padded; i += kThreads) sh.all[i] = 0;
+        __syncthreads();
+        for (int run = 2; run <= padded; run *= 2)
+            for (int apart = run / 2; apart > 0; apart /= 2) {
+                if (tid < padded / 2) {
+                    const int i = 2 * tid - (tid & (apart - 1)), j = i + apart;
+                    const uint64_t x = sh.all[i], y = sh.all[j];
+                    if ((x < y) == ((i & run) == 0)) sh.all[i] = y, sh.all[j] = x;
+                }
+                __syncthreads();
+            }
+    };
+    auto weight_at = [&](int i, int m) { return i < m ? h.weight(value_of(sh.all[i]), sh.powers) : 0; };
+    // Running sums of two elements of each thread, over the CTA. Returns the whole sum.
+    auto scan = [&](const uint64_t (&w)[2], uint64_t (&upto)[2]) {
+        uint64_t x = w[0] + w[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) sh.sums[0][warp] = x;
+        __syncthreads();
+        uint64_t all = 0;
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) {
+            x += v < warp ? sh.sums[0][v] : 0;
+            all += sh.sums[0][v];
+        }
+        upto[1] = x, upto[0] = x - w[1];
+        return all;
+    };
     // The last place that is kept of bin `b`: the one with `k` of the bin's tokens up to it, or the first at which the weights
     // up to it reach `target`.
     auto resolve = [&](int b, bool by_mass, uint32_t k, uint64_t target) -> uint64_t {
         const int m = gather(b, b);
         if (m <= kMost) {
-            for (int i = tid; i < m; i += kThreads) sh.weights[i] = h.weight(value_of(sh.all[i]), sh.powers);
-            __syncthreads();
-            for (int i = tid; i < m; i += kThreads) {
-                const uint64_t at = sh.all[i];
-                uint64_t in_front = 0;
-                uint32_t ranked = 0;
-#pragma unroll 4
-                for (int j = 0; j < m; ++j)
-                    if (sh.all[j] > at) in_front += sh.weights[j], ++ranked;
-                if (by_mass ? in_front < target && in_front + sh.weights[i] >= target : ranked + 1 == k) sh.found_border = at;
-            }
+            sort(m);
+            if (!by_mass) return sh.all[k - 1];
+            uint64_t w[2] = {weight_at(2 * tid, m), weight_at(2 * tid + 1, m)}, upto[2];
+            scan(w, upto);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (upto[e] - w[e] < target && upto[e] >= target) sh.found_border = sh.all[2 * tid + e];
             __syncthreads();
             return sh.found_border;
         }
         // Many tokens: the largest key at which what has a larger or equal one is enough, by halving the range of keys.
         if (tid == 0) sh.key_low = 0xffffffffu, sh.key_high = 0;
         __syncthreads();
-        uint32_t least = 0xffffffffu, most = 0;
-        for (int i = tid; i < n; i += kThreads)
-            if (bin_of(i) == b) least = min(least, key_of(i)), most = max(most, key_of(i));
-        least = __reduce_min_sync(0xffffffffu, least), most = __reduce_max_sync(0xffffffffu, most);
+        uint32_t least = __reduce_min_sync(0xffffffffu, key_least), most = __reduce_max_sync(0xffffffffu, key_most);
         if (lane == 0) atomicMin(&sh.key_low, least), atomicMax(&sh.key_high, most);
         ptx::cluster_sync();
         for (int r = 0; r < cluster; ++r) least = min(least, ld32(&sh.key_low, r)), most = max(most, ld32(&sh.key_high, r));
@@ -453,8 +495,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
             const uint64_t mid = low + (high - low) / 2;
             uint64_t sum = 0;
             uint32_t count = 0;
-            for (int i = tid; i < n; i += kThreads)
-                if (key_of(i) >= mid && bin_of(i) == b) sum += by_mass ? h.weight(L::value(mine[i]), sh.powers) : 0, ++count;
+            each_token([&](int, Raw r) {
+                if (L::key(r) >= mid && h.bin(L::value(r)) == b) sum += by_mass ? h.weight(L::value(r), sh.powers) : 0, ++count;
+            });
             const Sums s = add_up(sum, 0, count);
             if (by_mass ? s.mass >= target : s.count >= k) low = mid;
             else high = mid, above_mass = s.mass, above_count = s.count;
@@ -463,7 +506,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         const uint32_t key = (uint32_t)low;
         const uint64_t each = h.weight(value_of((uint64_t)key << 32), sh.powers);
         const uint64_t wanted = by_mass ? (target - above_mass + each - 1) / each : k - above_count;
-        const long long number = locate([&](int i) { return (uint64_t)(key_of(i) == key); }, [&](uint64_t) { return wanted - 1; });
+        const long long number = locate([&](int, Raw r) { return (uint64_t)(L::key(r) == key); }, [&](uint64_t) { return wanted - 1; });
         return place(key, (int)number);
     };
     // Draws from the tokens of the bins up to `last`, which hold all that is kept, ranked against each other in one CTA.
@@ -471,52 +514,36 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
     auto draw_from_few = [&](int last, uint64_t whole) {
         const int m = gather(0, last);
         if (rank == 0) {
-            for (int i = tid; i < m; i += kThreads) sh.weights[i] = h.weight(value_of(sh.all[i]), sh.powers);
-            __syncthreads();
-            constexpr int kMine = kMost / kThreads;
-            uint64_t in_front[kMine], sum = 0;
-            uint32_t ranked[kMine];
+            static_assert(kMost == 2 * kThreads, "two tokens to a thread");
+            sort(m);
+            uint64_t w[2], upto[2];
 #pragma unroll
-            for (int e = 0; e < kMine; ++e) {
-                const int i = tid + e * kThreads;
-                in_front[e] = 0, ranked[e] = 0;
-                if (i >= m) continue;
-                const uint64_t at = sh.all[i];
-#pragma unroll 4
-                for (int j = 0; j < m; ++j)
-                    if (sh.all[j] > at) in_front[e] += sh.weights[j], ++ranked[e];
-                if (ranked[e] < (uint32_t)top_k) sum += sh.weights[i];
+            for (int e = 0; e < 2; ++e) w[e] = 2 * tid + e < top_k ? weight_at(2 * tid + e, m) : 0;
+            const uint64_t sum_k = scan(w, upto), target = need_p ? part_of(whole ? whole : sum_k, top_p, true) : ~0ull;
+            // What is kept is a run from the first one on.
+            bool kept[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * tid + e;
+                kept[e] = w[e] > 0 && (i == 0 || upto[e] - w[e] < target) && value_of(sh.all[i]) >= floor_x;
             }
-            if (whole == 0) whole = block_sum(sum);
-            const uint64_t target = need_p ? part_of(whole, top_p, true) : ~0ull;
-            sum = 0;
-            bool kept[kMine];
+            const int count = __syncthreads_count(kept[0]) + __syncthreads_count(kept[1]);
+            // The same by their numbers, first ones first.
 #pragma unroll
-            for (int e = 0; e < kMine; ++e) {
-                const int i = tid + e * kThreads;
-                kept[e] = i < m && ranked[e] < (uint32_t)top_k && (ranked[e] == 0 || in_front[e] < target) &&
-                          value_of(sh.all[i]) >= floor_x;
-                if (kept[e]) sum += sh.weights[i];
-            }
-            sum = block_sum(sum);
-#pragma unroll
-            for (int e = 0; e < kMine; ++e) {
-                const int i = tid + e * kThreads;
-                if (i < m && !kept[e]) sh.weights[i] = 0;
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * tid + e;
+                if (!kept[e]) continue;
+                sh.weights[i] = w[e];
+                sh.all[i] = sh.all[i] << 32 | (uint32_t)i;
             }
             __syncthreads();
-            const uint64_t drawn = u < 1.f ? part_of(sum, u, false) : sum - 1;
+            sort(count);
 #pragma unroll
-            for (int e = 0; e < kMine; ++e) {
-                const int i = tid + e * kThreads;
-                if (i >= m || sh.weights[i] == 0) continue;
-                const uint32_t number = ~(uint32_t)sh.all[i];
-                uint64_t before = 0;
-#pragma unroll 4
-                for (int j = 0; j < m; ++j)
-                    if (~(uint32_t)sh.all[j] < number) before += sh.weights[j];
-                if (before <= drawn && drawn < before + sh.weights[i]) p.out[row] = number;
-            }
+            for (int e = 0; e < 2; ++e) w[e] = 2 * tid + e < count ? sh.weights[(uint32_t)sh.all[2 * tid + e]] : 0;
+            const uint64_t sum = scan(w, upto), drawn = u < 1.f ? part_of(sum, u, false) : sum - 1;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (upto[e] > drawn && upto[e] - w[e] <= drawn) p.out[row] = (uint32_t)~(sh.all[2 * tid + e] >> 32);
         }
         ptx::cluster_sync();
     };
@@ -525,11 +552,10 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         const int share = kBins / cluster;  // bins that this CTA adds up
         for (int i = tid; i < kBins; i += kThreads) sh.counts[i] = 0;
         __syncthreads();
-#pragma unroll 4
-        for (int i = tid; i < n; i += kThreads) {
-            const int b = bin_of(i);
+        each_token([&](int, Raw r) {
+            const int b = h.bin(L::value(r));
             if (b < kBins) atomicAdd(&sh.counts[b], 1u);
-        }
+        });
         ptx::cluster_sync();
         for (int i = tid; i < share; i += kThreads) {
             uint32_t count = 0;
@@ -542,7 +568,10 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         constexpr int kEach = kBins / kThreads;
         uint64_t most[kEach], least[kEach], my_most = 0, my_least = 0;
         uint32_t count[kEach], my_count = 0;
-        auto edge = [&](int b) { return b >> 5 < 44 ? ((uint64_t)sh.powers[(b & 31) * 8] << 12) >> (b >> 5) : 0; };
+        auto edge = [&](int b) -> uint64_t {  // the largest weight of bin b, the smallest of b - 1: half a bin above its middle
+            const int x = max(8 * b - 4, 0);
+            return x >> 8 < 44 ? ((uint64_t)sh.powers[x & 255] << 12) >> (x >> 8) : 0;
+        };
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
             const int b = tid * kEach + e;
@@ -612,12 +641,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
             for (int b = from + tid; b <= to; b += kThreads) sh.parts[0][b] = sh.parts[1][b] = 0;
             __syncthreads();
             uint64_t sum = 0, front = 0;
-#pragma unroll 4
-            for (int i = tid; i < n; i += kThreads) {
-                const float v = L::value(mine[i]);
-                if (border != 0 && !in_front_of_border(i, key_of(i))) continue;
+            each_token([&](int i, Raw r) {
+                if (border != 0 && !in_front_of_border(i, L::key(r))) return;
+                const float v = L::value(r);
                 const uint64_t w = h.weight(v, sh.powers);
-                const int b = bin_of(i);
+                const int b = h.bin(v);
                 sum += w;
                 if (b < from) {
                     front += w;
@@ -625,7 +653,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
                     const uint32_t old = atomicAdd(&sh.parts[0][b], (uint32_t)w), up = (uint32_t)(w >> 32) + (old + (uint32_t)w < old);
                     if (up) atomicAdd(&sh.parts[1][b], up);
                 }
-            }
+            });
             const Sums s = add_up(sum, front, 0);
             uint64_t mass[kEach], my_mass = 0, all_mass;
 #pragma unroll
@@ -653,9 +681,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
     }
 
     // ---------------------------------------------------------------- the sum of what is kept, and the token
-    auto kept = [&](int i) -> uint64_t {
-        const float v = L::value(mine[i]);
-        return v >= floor_x && (border == 0 || in_front_of_border(i, key_of(i))) ? h.weight(v, sh.powers) : 0;
+    auto kept = [&](int i, Raw r) -> uint64_t {
+        const float v = L::value(r);
+        return v >= floor_x && (border == 0 || in_front_of_border(i, L::key(r))) ? h.weight(v, sh.powers) : 0;
     };
     const long long token = locate(kept, [&](uint64_t whole) { return u < 1.f ? part_of(whole, u, false) : whole - 1; });
     if (rank == 0 && tid == 0) p.out[row] = token;
@@ -665,12 +693,12 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
 template <typename T>
 cudaError_t launch(SampleParams p, int rows, int sms, cudaStream_t s) {
     // CTAs of a row: as many as its tokens need room, and as many as there are SMs for.
-    const int room = (int)((size_t)96 * 1024 / sizeof(T));
+    const int room = (int)((size_t)64 * 1024 / sizeof(T));
     int cluster = 1;
     while (cluster < kMaxCluster && ((p.vocab + cluster - 1) / cluster > room || (rows * cluster <= 2 * sms && p.vocab > 4096 * cluster)))
         cluster *= 2;
-    p.chunk = ((p.vocab + cluster - 1) / cluster + kThreads - 1) / kThreads * kThreads;
-    const int smem = (int)sizeof(Shared<T>) + (p.chunk + 16) * (int)sizeof(T);
+    p.chunk = (p.vocab + cluster - 1) / cluster;
+    const int smem = (int)sizeof(Shared<T>) + (p.chunk + 16) * (int)sizeof(T) + 16;
     auto kernel = sample_kernel<T>;
     cudaError_t e = ensure_max_dyn_smem((const void *)kernel, 227 * 1024);
     if (e != cudaSuccess) return e;
