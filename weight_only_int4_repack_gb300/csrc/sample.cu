@@ -162,6 +162,7 @@ struct alignas(16) Shared {
         };
     };
     uint32_t slice[kBins];        // counts of this CTA's share of the bins, over the cluster
+    uint32_t bins[kBins];         // all of them
     uint32_t listed, key_low, key_high;
     uint32_t powers[256];
     uint64_t mass_slot[4][2];     // what a step adds up over the cluster
@@ -564,21 +565,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         }
         ptx::cluster_sync();
         // All bins, in every CTA: a thread has kEach of them, in their order. With bounds of their weights, wide enough for
-        // the bins' own rounding.
+        // the bins' own rounding. (Counts stay in shared memory, so that no registers are taken through the pass below.)
         constexpr int kEach = kBins / kThreads;
-        uint64_t most[kEach], least[kEach], my_most = 0, my_least = 0;
-        uint32_t count[kEach], my_count = 0;
         auto edge = [&](int b) -> uint64_t {  // the largest weight of bin b, the smallest of b - 1: half a bin above its middle
             const int x = max(8 * b - 4, 0);
             return x >> 8 < 44 ? ((uint64_t)sh.powers[x & 255] << 12) >> (x >> 8) : 0;
         };
+        auto count_of = [&](int e) -> uint64_t { return sh.bins[tid * kEach + e]; };
+        auto most_of = [&](int e) -> uint64_t {
+            const uint64_t up = edge(tid * kEach + e);
+            return count_of(e) * (up + (up >> 16) + 1);
+        };
+        auto least_of = [&](int e) -> uint64_t {
+            const uint64_t down = edge(tid * kEach + e + 1);
+            return count_of(e) * (down - (down >> 16) - (down > 0));
+        };
+        uint64_t my_most = 0, my_least = 0, my_count = 0;
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
             const int b = tid * kEach + e;
-            count[e] = ld32(&sh.slice[b % share], b / share);
-            const uint64_t up = edge(b), down = edge(b + 1);
-            most[e] = count[e] * (up + (up >> 16) + 1), least[e] = count[e] * (down - (down >> 16) - (down > 0));
-            my_count += count[e], my_most += most[e], my_least += least[e];
+            sh.bins[b] = ld32(&sh.slice[b % share], b / share);
+            my_count += count_of(e), my_most += most_of(e), my_least += least_of(e);
         }
         // Sums of two such sets over the bins in front of the thread's, and over all.
         auto in_front = [&](uint64_t a, uint64_t b, uint64_t *a_all, uint64_t *b_all, uint64_t *b_front) {
@@ -610,9 +617,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             uint64_t x = before, c = before_count, m = before_most, l = before_least;
 #pragma unroll
             for (int e = 0; e < kEach; ++e) {
-                if (x < target && x + each(e) >= target)
-                    sh.found = Found{(uint32_t)(tid * kEach + e), (uint32_t)c, count[e], m, l, most[e], least[e]}, sh.found_mass = x;
-                x += each(e), c += count[e], m += most[e], l += least[e];
+                const uint64_t y = each(e);
+                if (x < target && x + y >= target)
+                    sh.found = Found{(uint32_t)(tid * kEach + e), (uint32_t)c, (uint32_t)count_of(e), m, l, most_of(e), least_of(e)}, sh.found_mass = x;
+                x += y, c += count_of(e), m += most_of(e), l += least_of(e);
             }
             __syncthreads();
             return sh.found;
@@ -620,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         int bin_k = kBins;
         uint64_t whole_least = all_least, whole_most = all_most;
         if (need_k && (uint64_t)top_k < all_count) {
-            const Found f = find(before_count, [&](int e) { return (uint64_t)count[e]; }, (uint64_t)top_k);
+            const Found f = find(before_count, count_of, (uint64_t)top_k);
             bin_k = (int)f.bin;
             if (f.before + f.in <= kMost) {
                 draw_from_few(bin_k, 0);
@@ -634,8 +642,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         }
         if (need_p) {
             // The border lies in one of these bins.
-            const Found first = find(before_most, [&](int e) { return most[e]; }, max(part_of(whole_least, top_p, true), (uint64_t)1));
-            const Found last = find(before_least, [&](int e) { return least[e]; }, part_of(whole_most, top_p, true));
+            const Found first = find(before_most, most_of, max(part_of(whole_least, top_p, true), (uint64_t)1));
+            const Found last = find(before_least, least_of, part_of(whole_most, top_p, true));
             const int from = min((int)first.bin, kBins - 1), to = max(from, min((int)last.bin, min(bin_k, kBins - 1)));
             ptx::cluster_sync();  // nobody looks at gathered tokens any more
             for (int b = from + tid; b <= to; b += kThreads) sh.parts[0][b] = sh.parts[1][b] = 0;
