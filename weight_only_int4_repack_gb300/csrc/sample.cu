@@ -160,8 +160,8 @@ struct alignas(16) Shared {
         struct {
             uint64_t all[kMost], weights[kMost];  // gathered tokens of the whole cluster: key, then number counted down
         };
+        uint32_t slice[kBins];    // counts of this CTA's share of the bins, over the cluster
     };
-    uint32_t slice[kBins];        // counts of this CTA's share of the bins, over the cluster
     uint32_t bins[kBins];         // all of them
     uint32_t listed, key_low, key_high;
     uint32_t powers[256];
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         return key > k || (key == k && (uint32_t)~(c0 + i) >= (uint32_t)border);
     };
     uint32_t key_least = 0, key_most = 0;  // of the tokens that this thread has gathered
-    // Tokens of the bins from `from` to `to`, gathered by each CTA and then brought together in every one: sh.all, by their
+    // Tokens of the bins from `from` to `to`, gathered by each CTA and then brought together in the first: sh.all, by their
     // places. Returns how many (above kMost: not all are there).
     auto gather = [&](int from, int to) {
         ptx::cluster_sync();  // the last gathering's lists, and what lies where they come together, have been read
@@ -424,7 +424,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         int at = 0;
         for (int r = 0; r < cluster; ++r) {
             const int m = (int)ld32(&sh.listed, r);
-            for (int i = tid; i < m && at + i < kMost; i += kThreads) sh.all[at + i] = ld64(&sh.list[i], r);
+            if (rank == 0)
+                for (int i = tid; i < m && at + i < kMost; i += kThreads) sh.all[at + i] = ld64(&sh.list[i], r);
             at += m;
         }
         __syncthreads();
@@ -472,15 +473,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     auto resolve = [&](int b, bool by_mass, uint32_t k, uint64_t target) -> uint64_t {
         const int m = gather(b, b);
         if (m <= kMost) {
-            sort(m);
-            if (!by_mass) return sh.all[k - 1];
-            uint64_t w[2] = {weight_at(2 * tid, m), weight_at(2 * tid + 1, m)}, upto[2];
-            scan(w, upto);
+            if (rank == 0) {
+                sort(m);
+                uint64_t w[2] = {weight_at(2 * tid, m), weight_at(2 * tid + 1, m)}, upto[2];
+                if (by_mass) scan(w, upto);
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if (upto[e] - w[e] < target && upto[e] >= target) sh.found_border = sh.all[2 * tid + e];
-            __syncthreads();
-            return sh.found_border;
+                for (int e = 0; e < 2; ++e)
+                    if (by_mass ? upto[e] - w[e] < target && upto[e] >= target : 2 * tid + e == (int)k - 1) sh.found_border = sh.all[2 * tid + e];
+            }
+            ptx::cluster_sync();
+            return ld64(&sh.found_border, 0);
         }
         // Many tokens: the largest key at which what has a larger or equal one is enough, by halving the range of keys.
         if (tid == 0) sh.key_low = 0xffffffffu, sh.key_high = 0;
@@ -701,7 +703,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 template <typename T>
 cudaError_t launch(SampleParams p, int rows, int sms, cudaStream_t s) {
     // CTAs of a row: as many as its tokens need room, and as many as there are SMs for.
-    const int room = (int)((size_t)64 * 1024 / sizeof(T));
+    // (Two CTAs share an SM's 228 KB, of which each leaves 1 KB to the system.)
+    const int room = (int)((113 * 1024 - sizeof(Shared<T>) - 64) / sizeof(T));
     int cluster = 1;
     while (cluster < kMaxCluster && ((p.vocab + cluster - 1) / cluster > room || (rows * cluster <= 2 * sms && p.vocab > 4096 * cluster)))
         cluster *= 2;
