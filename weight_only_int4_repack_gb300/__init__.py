@@ -234,6 +234,16 @@ def _new(shape, dtype, like, stream, make=torch.empty):
         return make(shape, dtype=dtype, device=like.device)
 
 
+def _placed(where, *tensors):
+    """Refuses tensors that the call's kernels, which run on the current device, cannot be given."""
+    device = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{where}: tensors on different devices")
+    if device < 0 or device != (torch.cuda.current_device() if _current_device is None else _current_device()):
+        raise ValueError(f"{where}: tensors on the current CUDA device expected")
+
+
 def _expect_half(*tensors):
     """The projections read and write contiguous float16 and are handed addresses only."""
     for t in tensors:
@@ -586,6 +596,8 @@ def w4a16_prompt_attention(q, cache, table, starts, lens, scale: Optional[float]
     prefixes = _prefixes("w4a16_prompt_attention", batch, prefix_table, prefix_lens, prefix_of)
     if workspace is None:
         workspace = _new(w4a16_prompt_attention_workspace_bytes(rows, heads, cache.kv_heads, D), torch.uint8, q, stream)
+    _placed("w4a16_prompt_attention", q, out, table, starts, lens, lse, workspace, prefix_table, prefix_lens, prefix_of,
+            *cache.tensors)
     status = _prompt(_pack_prompt(
         q.data_ptr(), _TYPES.get(q.dtype, -1), q_row, q_head, cache.address, table.data_ptr(),
         table.stride(0) if batch > 1 else max_pages, max_pages, starts.data_ptr(), lens.data_ptr(), rows, batch, heads,
@@ -619,6 +631,8 @@ def w4a16_prefix_attention(q, cache, table, lens, prefix_table, prefix_lens, pre
     if workspace is None:
         workspace = _new(w4a16_prefix_attention_workspace_bytes(batch, heads, cache.kv_heads, D), torch.uint8, q, stream,
                          torch.zeros)
+    _placed("w4a16_prefix_attention", q, out, table, lens, lse, workspace, prefix_table, prefix_lens, prefix_of,
+            *cache.tensors)
     status = _prefix(_pack_prefix(
         q.data_ptr(), _TYPES.get(q.dtype, -1), q_row, q_head, cache.address, table.data_ptr(),
         table.stride(0) if batch > 1 else max_pages, max_pages, lens.data_ptr(), batch, heads, *prefixes,
@@ -688,6 +702,7 @@ def w4a16_sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_
                 raise ValueError(f"{name}: one entry for each row")
     if uniform.numel() != rows or out.numel() != rows:
         raise ValueError("w4a16_sample: uniform, out: one entry for each row")
+    _placed("w4a16_sample", logits, uniform, temperature, top_k, top_p, min_p, out)
     status = _sample(_pack_sample(
         logits.data_ptr(), _TYPES.get(logits.dtype, -1), logits.stride(0) if rows > 1 else vocab, rows, vocab,
         uniform.data_ptr(), 0 if temperature is None else temperature.data_ptr(), 0 if top_k is None else top_k.data_ptr(),

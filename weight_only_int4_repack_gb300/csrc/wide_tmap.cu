@@ -1,11 +1,8 @@
-// Tensor maps of queries and of a cache's pages for the attention of many rows, kept from call to call: they depend on
-// addresses, shapes and strides only.
+// Tensor maps of queries and of a cache's pages for the attention of many rows, made by each call.
 #include <cudaTypedefs.h>
 
 #include <array>
 #include <cstring>
-#include <map>
-#include <mutex>
 
 #include "wide_attention.cuh"
 
@@ -30,20 +27,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // 128-byte swizzle. Strides in elements; that of a dimension of one entry says nothing.
 bool tensor_map(CUtensorMap *out, const void *base, const std::array<long long, 4> &dims, const std::array<long long, 3> &strides,
                 const std::array<int, 4> &box) {
-    using Key = std::array<long long, 12>;
-    Key key{(long long)(uintptr_t)base};
-    for (int i = 0; i < 4; ++i) key[1 + i] = dims[i], key[5 + i] = box[i];
-    for (int i = 0; i < 3; ++i) key[9 + i] = strides[i];
-    static std::mutex mu;
-    static std::map<Key, CUtensorMap> cache;
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        const auto it = cache.find(key);
-        if (it != cache.end()) {
-            *out = it->second;
-            return true;
-        }
-    }
     const auto fn = encode_fn();
     if (!fn) return false;
     cuuint64_t d[4], s[3];
@@ -55,16 +38,9 @@ bool tensor_map(CUtensorMap *out, const void *base, const std::array<long long, 
     for (int i = 0; i < 3; ++i) s[i] = dims[i + 1] > 1 ? (cuuint64_t)strides[i] * 2 : 16;
     for (int i = 0; i < 3; ++i)
         if (s[i] == 0 || s[i] % 16) return false;
-    CUtensorMap map;
-    std::memset(&map, 0, sizeof(map));
-    if (fn(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(base), d, s, b, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
-           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return false;
-    std::lock_guard<std::mutex> lock(mu);
-    if (cache.size() >= 1024) cache.clear();  // bounded: buffers come and go
-    cache[key] = map;
-    *out = map;
-    return true;
+    std::memset(out, 0, sizeof(*out));
+    return fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(base), d, s, b, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace wide
