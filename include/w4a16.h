@@ -622,7 +622,8 @@ w4a16_status w4a16_residual_rmsnorm_block(const w4a16_residual_rmsnorm_args *arg
  *             aligned; nothing is kept in it from call to call. Calls that can overlap
  *             on the GPU need one each
  * Errors in the device error word: a pair of starts that falls or leaves [0, rows] (the
- * request has no rows), a length below the request's rows or beyond its table row (it
+ * request has no rows; where the others overlap so that there is more to do than `rows`
+ * rows could need, nothing is done), a length below the request's rows or beyond its table row (it
  * counts as its row), a prefix number of `prefixes` or more (no prefix) and a prefix length
  * beyond its row; a page number out of range, whose tokens are left out. A row that sees
  * no key gets out = 0 and lse = -inf.
@@ -655,8 +656,8 @@ w4a16_status w4a16_prompt_attention(const void *q, w4a16_type type, long long q_
  * without a token of its own (lens[b] <= 0) gets out = 0 and lse = -inf; one without a
  * prefix is as in w4a16_paged_attention. A window counts over prefix and own tokens.
  *   ws        of w4a16_prefix_attention_workspace_bytes(), 256-byte aligned. It has to be
- *             zero before its first use; every call leaves it ready for the next of the
- *             same heads, kv_heads and head_dim and no larger a batch
+ *             zero before its first use; every call leaves it ready for the next, of
+ *             whatever shape it is large enough for
  * Numerics: the prefix's part as in w4a16_prompt_attention, the own tokens' part as in
  * w4a16_paged_attention; the two are joined in fp32 and rounded once.
  */

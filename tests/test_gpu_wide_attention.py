@@ -415,3 +415,51 @@ def test_offsets_beyond_32_bits(w4):
     k = [f64(torch.stack([pool[3], pool[1], pool[2]])).reshape(48, 1, 64) for pool in (s.k, s.v)]
     want, lse, mag, _ = rows_attention(f64(s.q), k[0], k[1], 28, 0.125)
     assert np.abs(f64(s.out) - want).max() <= 4 * 2.0**-11 * mag.max() and np.abs(f64(s.lse) - lse).max() < 1e-4
+
+
+def test_starts_that_fall_again_and_again(w4):
+    # Requests that all have all rows would be more work than the rows could need: nothing is done.
+    n = 600
+    s = Setup(w4, [1] * n, [30] * n, heads=256, kv=1, dim=16)  # a tile has one token
+    s.starts = i32([0, n] * (n // 2) + [0])
+    s.prompt()
+    torch.cuda.synchronize()
+    assert w4.w4a16_device_error() == w4.W4A16_ERR_INVALID_ARG
+    assert bool((s.out == 77).all()) and bool((s.lse == 55).all())
+
+
+def test_tiny_softcap(w4):
+    s = Setup(w4, [20], [60], heads=4, kv=2, dim=64)
+    s.q[:, 0] = 0.0  # scores of 0 stay 0, all others are the cap, which is as good as 0
+    s.prompt(softcap=1e-40)
+    s.check(softcap=1e-40)
+
+
+def test_workspace_of_a_larger_batch_serves_smaller_ones_in_between(w4):
+    big = Setup(w4, [1] * 40, [50] * 40, [300], [0] * 40, heads=8, kv=2, dim=64)
+    small = Setup(w4, [1] * 3, [700, 5, 90], [20], [0, -1, 0], heads=4, kv=4, dim=256, seed=1)
+    ws = torch.zeros(max(w4.w4a16_prefix_attention_workspace_bytes(40, 8, 2, 64), w4.w4a16_prefix_attention_workspace_bytes(3, 4, 4, 256)),
+                     dtype=torch.uint8, device="cuda")
+    for s in (big, small, big, small):
+        s.prefix(workspace=ws)
+        s.check()
+
+
+def test_two_calls_at_once(w4):
+    a = Setup(w4, [700, 90], [1500, 90], [200], [0, 0], heads=8, kv=2, dim=128)
+    b = Setup(w4, [1] * 50, [40 + i for i in range(50)], [2000], [0] * 50, heads=8, kv=2, dim=128, dtype=BF16, seed=1)
+    logits = torch.randn(70, 50257, device="cuda")
+    u, p = torch.rand(70, device="cuda"), torch.full((70,), 0.9, device="cuda")
+    a.prompt(), b.prefix()
+    first = (a.out.clone(), b.out.clone(), w4.w4a16_sample(logits, u, top_p=p))
+    a.check(), b.check()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(5):
+        outs = []
+        torch.cuda.synchronize()
+        for stream, call in zip(streams, (a.prompt, b.prefix, lambda: w4.w4a16_sample(logits, u, top_p=p))):
+            with torch.cuda.stream(stream):
+                outs.append(call())
+        torch.cuda.synchronize()
+        for x, y in zip(first, outs):
+            assert torch.equal(x, y)

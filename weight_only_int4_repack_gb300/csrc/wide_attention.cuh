@@ -359,7 +359,7 @@ struct Scores {
         const float to_score = (p.scale != 0.f ? fabsf(p.scale) : 1.f) * k_scale;
         unit = unit_of(p, k_scale);
         capped = p.softcap > 0.f;
-        in = capped ? 2.f * kLog2e * to_score / p.softcap : 0.f;
+        in = capped ? fminf(2.f * kLog2e * to_score / p.softcap, 3e38f) : 0.f;  // (0 times it is 0)
         cap = p.softcap * kLog2e;
         slack = kSlack / unit;
     }
@@ -439,7 +439,10 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             plan_off[i] = at;
             at += (plan_n[i] + tt - 1) / tt;
         }
-        if (tid == 0) plan_off[seqs] = all, sh.tiles = all;
+        // Requests whose rows overlap (starts that fall) may have more tiles than the host has counted with: nothing is done.
+        const bool many = all > p.rows / tt + seqs;
+        if (many && cta == 0 && tid == 0) atomicExch(p.err, (unsigned int)W4A16_ERR_INVALID_ARG);
+        if (tid == 0) plan_off[seqs] = all, sh.tiles = many ? 0 : all;
     }
     __syncthreads();
     int total_units = 0, t_begin = 0, t_end = 0;  // below 2^31: the host has seen to that
@@ -618,11 +621,11 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                     const long long at = in ? row * p.q_row + (g.h0 + hh) * p.q_head : -1;
 #pragma unroll 1
                     for (int i0 = 0; i0 < 32; i0 += 4 * kAt) {
-                      long long srcs[4];  // the rows' places first: copies and shuffles stay in their order
+                        long long srcs[4];  // the rows' places first: copies and shuffles stay in their order
 #pragma unroll
-                      for (int z = 0; z < 4; ++z) srcs[z] = __shfl_sync(0xffffffffu, at, i0 + z * kAt + lane / kLanes);
+                        for (int z = 0; z < 4; ++z) srcs[z] = __shfl_sync(0xffffffffu, at, i0 + z * kAt + lane / kLanes);
 #pragma unroll
-                      for (int z = 0; z < 4; ++z) {
+                        for (int z = 0; z < 4; ++z) {
                         const int rr = r0 + i0 + z * kAt + lane / kLanes;
                         const long long src = srcs[z];
                         const bool real = src >= 0 && c * 8 < D;
@@ -656,7 +659,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                                 asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
                                              : "memory");
                         }
-                      }
+                        }
                     }
                 }
                 if constexpr (K::kOwnPower) signal(&sh.q_full);
@@ -725,36 +728,36 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                         }
                         __syncwarp();
                     } else {
-                    const C *pool = static_cast<const C *>(side ? p.c.v : p.c.k) + kvh * (side ? p.c.v_head : p.c.k_head);
-                    const unsigned long long off = my_page * (unsigned long long)(side ? p.c.v_page : p.c.k_page) +
-                                                   my_at * (unsigned long long)(side ? p.c.v_token : p.c.k_token);
-                    // A chunk is 16 bytes of a row. 8-bit rows wait in the last blocks of their own place until they are widened.
-                    constexpr int kChunks = DT * (int)sizeof(C) / 16, kLanes = kChunks < 32 ? kChunks : 32, kAt = 32 / kLanes;
-                    const int c = lane % kLanes, r0 = lane / kLanes;
-                    const C *from = pool + c * (16 / (int)sizeof(C));
-                    const uint32_t to = dst + ((c >> 3) + (K::k8 ? DT / 64 - (kChunks + 7) / 8 : 0)) * (kKeys * 128) + (w * kMine + r0) * 128;
-                    auto turned = [&](int i) { return (uint32_t)((c & 7) ^ (K::k8 ? 0 : (i + r0) & 7)) << 4; };
-                    if ((good_rows & all) == all && blocks) {  // as a rule
-                        const unsigned long long token = side ? p.c.v_token : p.c.k_token;
-                        const C *row = from + r0 * token;
-#pragma unroll 1
-                        for (int i0 = 0; i0 < kMine; i0 += 16) {
-                            const C *at_row = row + __shfl_sync(0xffffffffu, off, i0);
-#pragma unroll
-                            for (int i = 0; i < 16; i += kAt) {
-                                copy16_all(to + (i0 + i) * 128 + turned(i), at_row);
-                                at_row += kAt * token;
+                        const C *pool = static_cast<const C *>(side ? p.c.v : p.c.k) + kvh * (side ? p.c.v_head : p.c.k_head);
+                        const unsigned long long off = my_page * (unsigned long long)(side ? p.c.v_page : p.c.k_page) +
+                                                       my_at * (unsigned long long)(side ? p.c.v_token : p.c.k_token);
+                        // A chunk is 16 bytes of a row. 8-bit rows wait in the last blocks of their own place until they are widened.
+                        constexpr int kChunks = DT * (int)sizeof(C) / 16, kLanes = kChunks < 32 ? kChunks : 32, kAt = 32 / kLanes;
+                        const int c = lane % kLanes, r0 = lane / kLanes;
+                        const C *from = pool + c * (16 / (int)sizeof(C));
+                        const uint32_t to = dst + ((c >> 3) + (K::k8 ? DT / 64 - (kChunks + 7) / 8 : 0)) * (kKeys * 128) + (w * kMine + r0) * 128;
+                        auto turned = [&](int i) { return (uint32_t)((c & 7) ^ (K::k8 ? 0 : (i + r0) & 7)) << 4; };
+                        if ((good_rows & all) == all && blocks) {  // as a rule
+                            const unsigned long long token = side ? p.c.v_token : p.c.k_token;
+                            const C *row = from + r0 * token;
+    #pragma unroll 1
+                            for (int i0 = 0; i0 < kMine; i0 += 16) {
+                                const C *at_row = row + __shfl_sync(0xffffffffu, off, i0);
+    #pragma unroll
+                                for (int i = 0; i < 16; i += kAt) {
+                                    copy16_all(to + (i0 + i) * 128 + turned(i), at_row);
+                                    at_row += kAt * token;
+                                }
+                            }
+                        } else {
+    #pragma unroll 1
+                            for (int i = 0; i < kMine; i += kAt) {
+                                const unsigned long long src = __shfl_sync(0xffffffffu, off, i + r0);
+                                const bool there = ((good_rows >> (i + r0)) & 1u) && c * (16 / (int)sizeof(C)) < D;
+                                if (c * (16 / (int)sizeof(C)) < 16 * k_steps) copy16(to + i * 128 + turned(i), there ? from + src : pool, there);
                             }
                         }
-                    } else {
-#pragma unroll 1
-                        for (int i = 0; i < kMine; i += kAt) {
-                            const unsigned long long src = __shfl_sync(0xffffffffu, off, i + r0);
-                            const bool there = ((good_rows >> (i + r0)) & 1u) && c * (16 / (int)sizeof(C)) < D;
-                            if (c * (16 / (int)sizeof(C)) < 16 * k_steps) copy16(to + i * 128 + turned(i), there ? from + src : pool, there);
-                        }
-                    }
-                    queue(&sh.full[stage]);
+                        queue(&sh.full[stage]);
                     }
                     ++tiles_n;
                     if (++stage == kStages) stage = 0, ring_phase ^= 1u;
