@@ -629,8 +629,8 @@ w4a16_status w4a16_residual_rmsnorm_block(const w4a16_residual_rmsnorm_args *arg
  * no key gets out = 0 and lse = -inf.
  * The result does not depend on timing. Scores, their maximum and the sums are fp32.
  * Weights are rounded once to `type`, as operands (2^-11 of a weight in fp16, down to
- * 2^-25 of the largest; 2^-8 in bf16), and outputs are divided by the sum of the rounded
- * ones; lse is that of the unrounded ones. Values that a row does not see do not reach it,
+ * 2^-25 of the largest; 2^-8 in bf16); their sum, which outputs are divided by and lse
+ * comes from, is that of the unrounded ones. Values that a row does not see do not reach it,
  * whatever they are.
  * Refused as unsupported: rows * heads above 2^24, batch above 8192, prefixes above 2048,
  * table rows of 2^31 tokens together.

@@ -104,7 +104,7 @@ struct Config {
     static constexpr int kQBytes = 128 * DT * 2;          // queries of a group
     static constexpr int kRing = kTiles * kQBytes;        // offset of the ring
     static constexpr int kAfter = kRing + kStages * kStageBytes;
-    static constexpr int kPitch = DT + 8;                 // floats of a row of sums: outputs, then m, l, l as rounded
+    static constexpr int kPitch = DT + 8;                 // floats of a row of sums: outputs, then m, l
     static constexpr int kSlot = kRows * kPitch;
     // Tensor memory: kAhead units' scores of each group (weights take their place), and its outputs.
     static constexpr int kO = 256, kOStep = 128, kSStep = 128, kSBuffer = 64;
@@ -328,19 +328,6 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
         : "=f"(r.x), "=f"(r.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return r;
-}
-
-// The two halves of a pair of operands added to a pair of sums.
-template <bool kB16>
-__device__ __forceinline__ void add_pair(float2 &sum, uint32_t pair) {
-    if constexpr (kB16)
-        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.rn.f32.bf16 %0, a, %0;\n\tadd.rn.f32.bf16 %1, b, %1;\n\t}"
-            : "+f"(sum.x), "+f"(sum.y)
-            : "r"(pair));
-    else
-        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.rn.f32.f16 %0, a, %0;\n\tadd.rn.f32.f16 %1, b, %1;\n\t}"
-            : "+f"(sum.x), "+f"(sum.y)
-            : "r"(pair));
 }
 
 // A score in units of log2 is a raw product times this. A scale of 0 or below is in the queries (none, or negated); a unit
@@ -1010,7 +997,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             float k_scale = K::k8 && p.c.k_scale ? p.c.k_scale[kvh] : 1.f, unit = 1.f, slack = 0.f;
             float m = kLowest, limit = kLowest, shift = 0.f;
             bool far = false;
-            float2 l = make_float2(0.f, 0.f), lr = make_float2(0.f, 0.f);
+            float2 l = make_float2(0.f, 0.f);
 #pragma unroll 1
             for (int j = 0; j < count; ++j, ++unit_n, ++step) {
                 const uint32_t at = step % K::kAhead, t_s = t_s0 + at * K::kSBuffer;
@@ -1083,13 +1070,14 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                                 tc5::st16(t_o + c * 16, o);
                             }
                         }
-                        l.x *= keep, l.y *= keep, lr.x *= keep, lr.y *= keep;
+                        l.x *= keep, l.y *= keep;
                         m = y, limit = y + slack, shift = at_y;
                     }
                     // Weights are 2^(s unit + shift), 2^kUp at the reference; the shift's rounding is in all of them alike and in
                     // the shift that is kept. Where scores are so large that it could be seen, differences to the reference are
-                    // taken first. Weights are rounded to the operands' type, and outputs are divided by the sum of the rounded
-                    // ones, so that they are a mean of the values.
+                    // taken first. Weights are rounded to the operands' type, half a step at most each; the sum that outputs are
+                    // divided by is that of the unrounded ones (that of the rounded ones, as costly as all other sums and maxima
+                    // together, would leave the errors' bound as it is).
                     const float2 by2 = far ? make_float2(1.f, 1.f) : make_float2(unit, unit);
                     const float2 up2 = far ? make_float2(K::kUp, K::kUp) : make_float2(shift, shift);
                     auto weights = [&](uint32_t (&z)[32], uint32_t to) {
@@ -1104,7 +1092,6 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                             s.x = ex2(s.x), s.y = ex2(s.y);
                             l = add2(l, s);
                             h[i] = elem::pair_from_f32<typename K::M>(s.x, s.y);
-                            add_pair<K::kB16>(lr, h[i]);
                         }
                         tc5::st16(to, h);
                     };
@@ -1139,10 +1126,10 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             tc5::fence_after();
             if (!some) continue;
             const float v_scale = K::k8 && p.c.v_scale ? p.c.v_scale[kvh] : 1.f;
-            const float sum = l.x + l.y, cut = lr.x + lr.y;
+            const float sum = l.x + l.y;
             const bool any = sum > 0.f || sum != sum;
             const bool direct = slot < 0 && p.starts;
-            const float f = !direct ? 1.f : any ? v_scale / cut : 0.f;
+            const float f = !direct ? 1.f : any ? v_scale / sum : 0.f;
             float *sums = nullptr;
             if (!direct)
                 sums = slot >= 0 ? p.slots + (long long)slot * K::kSlot + row * K::kPitch
@@ -1190,7 +1177,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                     if (p.lse)
                         p.lse[(long long)b * p.heads + head] = any ? (log2f(sum) - shift) / kLog2e : -INFINITY;
                 } else {
-                    *reinterpret_cast<float4 *>(sums + DT) = make_float4(any ? -shift : -INFINITY, sum, cut, 0.f);
+                    *reinterpret_cast<float4 *>(sums + DT) = make_float4(any ? -shift : -INFINITY, sum, 0.f, 0.f);
                 }
             }
         }
@@ -1208,7 +1195,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
 template <int DT>
 struct Sums {
     static constexpr int kEach = DT > 128 ? 2 : 1;
-    float m = -INFINITY, l = 0.f, lr = 0.f;
+    float m = -INFINITY, l = 0.f;
     float4 o[kEach];
 };
 // Joins a row's parts, which lie with the CTAs from `first` on.
@@ -1238,14 +1225,14 @@ __device__ __forceinline__ Sums<K::kDim> join_parts(const Params &p, int first, 
 #pragma unroll
         for (int i = 0; i < kOnce; ++i) top = fmaxf(top, s[i].x);
         const float base = top == -INFINITY ? 0.f : top, keep = ex2(r.m - base);
-        r.m = top, r.l *= keep, r.lr *= keep;
+        r.m = top, r.l *= keep;
 #pragma unroll
         for (int e = 0; e < r.kEach; ++e) r.o[e].x *= keep, r.o[e].y *= keep, r.o[e].z *= keep, r.o[e].w *= keep;
 #pragma unroll
         for (int i = 0; i < kOnce; ++i) {
             const float f = ex2(s[i].x - base);
             if (f == 0.f) continue;  // nothing there, or nothing that would count
-            r.l = fmaf(f, s[i].y, r.l), r.lr = fmaf(f, s[i].z, r.lr);
+            r.l = fmaf(f, s[i].y, r.l);
 #pragma unroll
             for (int e = 0; e < r.kEach; ++e) {
                 r.o[e].x = fmaf(f, y[i][e].x, r.o[e].x), r.o[e].y = fmaf(f, y[i][e].y, r.o[e].y);
@@ -1366,7 +1353,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) finish_kernel(const __grid_co
             if (r >= c.rows || hh >= c.heads) continue;
             const Sums<DT> x = join_parts<K>(p, cta, c.parts, r, D);
             const bool any = x.l > 0.f || x.l != x.l;
-            const float f = any ? (K::k8 && p.c.v_scale ? p.c.v_scale[c.kvh] : 1.f) / x.lr : 0.f;
+            const float f = any ? (K::k8 && p.c.v_scale ? p.c.v_scale[c.kvh] : 1.f) / x.l : 0.f;
             const int row = c.q0 + tk, head = c.h0 + hh;
             T *out = static_cast<T *>(p.out) + (long long)row * p.o_row + head * p.o_head;
             float check = 0.f;
@@ -1432,7 +1419,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
         if (f.first < 0) {
             const float *from = p.whole + i * K::kPitch;
             const float4 s = __ldcg(reinterpret_cast<const float4 *>(from + DT));
-            x.m = s.x, x.l = s.y, x.lr = s.z;
+            x.m = s.x, x.l = s.y;
 #pragma unroll
             for (int e = 0; e < x.kEach; ++e) {
                 const int d = 4 * (lane + 32 * e);
@@ -1447,7 +1434,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefix_join_kernel(const __gr
     const float a = any ? x.m + log2f(x.l) : -INFINITY;
     const float top = fmaxf(a, own_lse), from = top == -INFINITY ? 0.f : top;
     const float wa = any ? ex2(a - from) : 0.f, wo = any_own ? ex2(own_lse - from) : 0.f;
-    const float sum = wa + wo, f = any ? wa / sum * (K::k8 && p.c.v_scale ? p.c.v_scale[kvh] : 1.f) / x.lr : 0.f;
+    const float sum = wa + wo, f = any ? wa / sum * (K::k8 && p.c.v_scale ? p.c.v_scale[kvh] : 1.f) / x.l : 0.f;
     const float fo = any_own ? wo / sum : 0.f;
     float check = 0.f;
 #pragma unroll
