@@ -274,19 +274,23 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-// ptx::mbar_wait in fewer instructions, for all lanes of a warp alike.
-__device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *abort_flag, unsigned int *err, uint64_t limit_ns) {
-    uint64_t since = 0;
+// ptx::mbar_wait for all lanes of a warp alike. What comes after the first try is kept out of the way of the instruction
+// caches, once for all calls.
+static __device__ __noinline__ bool wait_longer(uint64_t *bar, uint32_t parity, volatile int *abort_flag, unsigned int *err,
+                                                uint64_t limit_ns) {
+    const uint64_t since = ptx::globaltimer();
+    bool over = limit_ns == 0;
 #pragma unroll 1
-    while (!__all_sync(0xffffffffu, ptx::mbar_try_wait_sleep(bar, parity, 20000u))) {
-        const uint64_t now = ptx::globaltimer();
-        if (since == 0) since = now;
-        const bool over = now - since >= limit_ns;
+    for (;;) {
         if (over && err) atomicExch(err, (unsigned int)W4A16_ERR_TIMEOUT);
         if (over) *abort_flag = 1;
         if (__any_sync(0xffffffffu, over || *abort_flag)) return false;
+        if (__all_sync(0xffffffffu, ptx::mbar_try_wait_sleep(bar, parity, 20000u))) return true;
+        over = ptx::globaltimer() - since >= limit_ns;
     }
-    return true;
+}
+__device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *abort_flag, unsigned int *err, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, ptx::mbar_try_wait_sleep(bar, parity, 20000u)) || wait_longer(bar, parity, abort_flag, err, limit_ns);
 }
 
 // The same value in all lanes, so that the compiler knows it.
@@ -621,7 +625,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                         if constexpr (!K::kOwnPower) {
                             if (c * 8 < 16 * k_steps) copy16(to, from, real);
                         } else {
-                            // To fp16, after a power of two that brings the row's largest below 2: what that loses is 2^-25
+                            // To fp16, after a power of two that brings the row's largest below 4: what that loses is 2^-25
                             // of the largest.
                             const uint4 y = real ? *reinterpret_cast<const uint4 *>(from) : make_uint4(0, 0, 0, 0);
                             const uint32_t w4[4] = {y.x, y.y, y.z, y.w};
@@ -633,15 +637,15 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                             }
 #pragma unroll
                             for (int o = 1; o < kLanes; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-                            const int e2 = big > 0.f && big < INFINITY ? max(ilogbf(big), -120) : 0;
-                            const float down = ldexpf(1.f, -e2);
+                            const int e2 = big > 0.f && big < INFINITY ? min(max((int)(__float_as_uint(big) >> 23) - 127, -120), 126) : 0;
+                            const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
                             uint32_t h[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const float2 f = elem::pair_to_f32<T>(w4[e]);
                                 h[e] = elem::pair_from_f32<__half>(f.x * down, f.y * down);
                             }
-                            if (c == 0) sh.powers[qi][rr] = ldexpf(1.f, e2);
+                            if (c == 0) sh.powers[qi][rr] = __uint_as_float((uint32_t)(127 + e2) << 23);
                             if (c * 8 < 16 * k_steps)
                                 asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
                                              : "memory");
@@ -1015,20 +1019,25 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                     const bool masked = __any_sync(0xffffffffu, lo > key0 || hi - kKeys < key0) || (bad[0] | bad[1] | bad[2] | bad[3]);
                     if (masked || p.softcap > 0.f) {  // what is not a plain product goes back to where the products were
                         const Scores sc(p, k_scale);
-                        const unsigned int rel = (unsigned int)(key0 - lo), span = (unsigned int)max(hi - lo, 0);
 #pragma unroll 1
                         for (int c = 0; c < kKeys / 32; ++c) {
+                            // Which of these 32 the row sees, as bits; where all rows see all of them the products stay.
+                            const int from = lo - (key0 + c * 32), to = hi - (key0 + c * 32);
+                            uint32_t seen = ~(kKeys == 128 ? bad[c] : bad[2 * c] | (bad[2 * c + 1] << 16));
+                            seen &= from <= 0 ? ~0u : from < 32 ? ~0u << from : 0u;
+                            seen &= to >= 32 ? ~0u : to > 0 ? ~(~0u << to) : 0u;
+                            const bool whole = __all_sync(0xffffffffu, seen == ~0u);
+                            if (whole && !sc.capped) continue;
                             uint32_t v[32];
                             tc5::ld32(t_s + c * 32, v);
-                            const uint32_t none = kKeys == 128 ? bad[c] : bad[2 * c] | (bad[2 * c + 1] << 16);
                             tc5::wait_ld();
                             if (sc.capped)
 #pragma unroll
                                 for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(sc.squeezed(__uint_as_float(v[i])));
-                            if (masked)
+                            if (!whole)
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
-                                    if (rel + (unsigned int)(c * 32 + i) >= span || ((none >> i) & 1u)) v[i] = 0xff800000u;
+                                    if (!(seen & 1u << i)) v[i] = 0xff800000u;
                             tc5::st32(t_s + c * 32, v);
                         }
                         tc5::wait_st();
@@ -1135,7 +1144,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                 sums = slot >= 0 ? p.slots + (long long)slot * K::kSlot + row * K::kPitch
                                    : p.whole + ((long long)b * p.heads + head) * K::kPitch;
             T *out = static_cast<T *>(p.out) + (long long)b * p.o_row + head * p.o_head;
-            float check = 0.f;
+            float check[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
             for (int c = 0; c < (D + 31) / 32; ++c) {
                 uint32_t v[32];
@@ -1143,12 +1152,12 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                 tc5::ld32(t_o + c * 32, v);
                 tc5::wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = any ? __uint_as_float(v[i]) * f : 0.f;
+                for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(v[i]) * f;  // (0 of weights of 0)
                 if (direct) {
                     uint32_t h[16];
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (c * 32 + (i & ~7) < D) check = fmaf(o[i], 0.f, check);
+                        if (c * 32 + (i & ~7) < D) check[i & 3] = fmaf(o[i], 0.f, check[i & 3]);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) h[i] = elem::pair_from_f32<T>(o[2 * i], o[2 * i + 1]);
                     if (in)
@@ -1173,7 +1182,8 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             }
             if (in) {
                 if (direct) {
-                    odd |= check != check;
+                    const float all = (check[0] + check[1]) + (check[2] + check[3]);
+                    odd |= all != all;
                     if (p.lse)
                         p.lse[(long long)b * p.heads + head] = any ? (log2f(sum) - shift) / kLog2e : -INFINITY;
                 } else {
