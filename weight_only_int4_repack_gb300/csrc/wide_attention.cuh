@@ -610,46 +610,51 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                     const bool in = r < rows && hh < g.heads && p.scale != 0.f;
                     const long long row = !in ? 0 : p.starts ? g.q0 + tk : sh.members[qi][tk];
                     const long long at = in ? row * p.q_row + (g.h0 + hh) * p.q_head : -1;
+                    // Several rows at a time: their places and, where they pass through registers, all their loads come first.
+                    constexpr int kOnce = K::kOwnPower && 8 * kAt <= 32 ? 8 : 4;
 #pragma unroll 1
-                    for (int i0 = 0; i0 < 32; i0 += 4 * kAt) {
-                        long long srcs[4];  // the rows' places first: copies and shuffles stay in their order
+                    for (int i0 = 0; i0 < 32; i0 += kOnce * kAt) {
+                        long long srcs[kOnce];
+                        [[maybe_unused]] uint4 ys[kOnce];
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) srcs[z] = __shfl_sync(0xffffffffu, at, i0 + z * kAt + lane / kLanes);
+                        for (int z = 0; z < kOnce; ++z) srcs[z] = __shfl_sync(0xffffffffu, at, i0 + z * kAt + lane / kLanes);
+                        if constexpr (K::kOwnPower)
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) {
-                        const int rr = r0 + i0 + z * kAt + lane / kLanes;
-                        const long long src = srcs[z];
-                        const bool real = src >= 0 && c * 8 < D;
-                        const T *from = static_cast<const T *>(p.q) + (real ? src + c * 8 : 0);
-                        const uint32_t to = q_base + (c >> 3) * (K::kRows * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
-                        if constexpr (!K::kOwnPower) {
-                            if (c * 8 < 16 * k_steps) copy16(to, from, real);
-                        } else {
-                            // To fp16, after a power of two that brings the row's largest below 4: what that loses is 2^-25
-                            // of the largest.
-                            const uint4 y = real ? *reinterpret_cast<const uint4 *>(from) : make_uint4(0, 0, 0, 0);
-                            const uint32_t w4[4] = {y.x, y.y, y.z, y.w};
-                            float big = 0.f;
+                            for (int z = 0; z < kOnce; ++z)
+                                ys[z] = srcs[z] >= 0 && c * 8 < D ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) + srcs[z] + c * 8))
+                                                                  : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float2 f = elem::pair_to_f32<T>(w4[e]);
-                                big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+                        for (int z = 0; z < kOnce; ++z) {
+                            const int rr = r0 + i0 + z * kAt + lane / kLanes;
+                            const uint32_t to = q_base + (c >> 3) * (K::kRows * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
+                            if constexpr (!K::kOwnPower) {
+                                const bool real = srcs[z] >= 0 && c * 8 < D;
+                                if (c * 8 < 16 * k_steps) copy16(to, static_cast<const T *>(p.q) + (real ? srcs[z] + c * 8 : 0), real);
+                            } else {
+                                // To fp16, after a power of two that brings the row's largest below 2 (of the largest numbers:
+                                // below 4): what that loses is 2^-25 of the largest.
+                                const uint32_t w4[4] = {ys[z].x, ys[z].y, ys[z].z, ys[z].w};
+                                float big = 0.f;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float2 f = elem::pair_to_f32<T>(w4[e]);
+                                    big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+                                }
+#pragma unroll
+                                for (int o = 1; o < kLanes; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+                                const int e2 = big > 0.f && big < INFINITY ? min(max((int)(__float_as_uint(big) >> 23) - 127, -120), 126) : 0;
+                                const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
+                                uint32_t h[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float2 f = elem::pair_to_f32<T>(w4[e]);
+                                    h[e] = elem::pair_from_f32<__half>(f.x * down, f.y * down);
+                                }
+                                if (c == 0) sh.powers[qi][rr] = __uint_as_float((uint32_t)(127 + e2) << 23);
+                                if (c * 8 < 16 * k_steps)
+                                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                                                 : "memory");
                             }
-#pragma unroll
-                            for (int o = 1; o < kLanes; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-                            const int e2 = big > 0.f && big < INFINITY ? min(max((int)(__float_as_uint(big) >> 23) - 127, -120), 126) : 0;
-                            const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
-                            uint32_t h[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float2 f = elem::pair_to_f32<T>(w4[e]);
-                                h[e] = elem::pair_from_f32<__half>(f.x * down, f.y * down);
-                            }
-                            if (c == 0) sh.powers[qi][rr] = __uint_as_float((uint32_t)(127 + e2) << 23);
-                            if (c * 8 < 16 * k_steps)
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
-                                             : "memory");
-                        }
                         }
                     }
                 }
