@@ -2,18 +2,24 @@
 //     w_i = 2^(-(max - x_i) log2(e) / T); of the tokens in the order of falling x (equal ones by number) the first k, of
 //     these the fewest whose weights reach p of theirs, of these the ones with w_i >= min_p; the token drawn is the first, by
 //     number, at which the kept weights' running sum exceeds u times their sum
-// Bound by HBM at best (each logit is read once), in practice by the steps' latencies: a row is one cluster of CTAs, which
-// keeps its logits in shared memory, and every step that all of them have to agree on is a cluster barrier.
 //
-// Weights are fixed-point numbers of 44 binary places in 64-bit integers, off by less than 2^-31 of themselves: sums are
-// exact and so do not depend on any order, and a border between two tokens moves by less than 2^-31 of the sum, about what
-// it would take for a 32-bit random number to show it. A weight below 2^-44 of the largest is 0.
+// Weights are fixed-point numbers of 44 binary places in 64-bit integers, off by less than 2^-30 of themselves (2^-32 each
+// from the table, the rest's whole number and the product, as much from the rest's roundings): sums are exact and so do not
+// depend on any order, and a border between two tokens, a quotient of two sums, moves by less than 2^-31, about what it would
+// take for a 32-bit random number to show it. A weight below 2^-44 of the largest is 0.
 //
-// The border of top-k and top-p is found by a histogram of counts over 32 bins for each factor of two of the weight. It
+// A row is one cluster of CTAs, which keeps its logits in shared memory, so that each is read from memory once. The border of
+// top-k and top-p is found by a histogram of counts over 32 bins for each factor of two of the weight. It
 // names the bin of the k-th token, and a few bins that hold the border of top-p (a bin's weights are alike to 2%); a second
 // pass adds up exactly what lies in front of these, and in each of them. Where few tokens lie above the border (as a rule)
-// they are gathered, and one CTA ranks them against each other and draws; otherwise the border's bin is resolved (by ranking
-// its tokens, or, when it holds many, by halving the range of its values) and one more pass sums and draws.
+// they are gathered, and one CTA sorts them and draws; otherwise the border's bin is resolved (by sorting its tokens or, when
+// it holds many, by halving the range of its values) and one more pass sums and draws.
+//
+// What bounds it: instructions and barriers, not HBM. Cycles of a CTA of 37500 bf16 logits, two CTAs to an SM (256 rows of
+// 150001, top-p alone, 336 us, 11 of them the bytes): logits and maximum 10000 to 22000, counts 14000, bounds and searches
+// 15000, exact sums 30000 to 55000, the border's bin 25000, the last sums and the draw 50000. A single row of 32001 takes 18
+// us: launch 3, and a dozen steps of a barrier of the cluster and some dependent reads each. Sums of weights in the histogram
+// in place of counts (two shared atomics a logit) made 64 rows of 131072 128 us; with counts they are 85.
 #include <climits>
 #include <cmath>
 
@@ -39,18 +45,17 @@ struct SampleParams {
     unsigned int *err;
 };
 
-// 2^(-i/256) with 32 binary places: from the series of exp, the first entry one unit short of 1.
+// 2^(-(i + 1)/256) with 32 binary places, from the series of exp.
 struct Table {
     uint32_t v[256];
 };
 constexpr Table make_table() {
     Table t{};
     for (int i = 0; i < 256; ++i) {
-        const double y = -0.69314718055994530942 * i / 256;
+        const double y = -0.69314718055994530942 * (i + 1) / 256;
         double term = 1, sum = 1;
         for (int k = 1; k < 30; ++k) term *= y / k, sum += term;
-        const double scaled = sum * 4294967296.0 + 0.5;
-        t.v[i] = scaled >= 4294967295.0 ? 0xffffffffu : (uint32_t)scaled;
+        t.v[i] = (uint32_t)(sum * 4294967296.0 + 0.5);
     }
     return t;
 }
@@ -64,21 +69,26 @@ struct Heat {
         const float t = fminf((top - x) * (c * kPerOctave), (float)kBins);
         return (int)(__float_as_uint(t + 12582912.f) - 0x4b400000u);
     }
-    __device__ __forceinline__ uint64_t weight(float x, const uint32_t *powers) const {
-        const float d = top - x, t = d * c;
-        if (!(t < 44.f)) return 0;
+    // As a product of two 32-bit numbers, which sums take up in one instruction. (Of what is far below the largest, infinities
+    // and NaN the first is 0: all of it is shifted out.)
+    struct Weight {
+        uint32_t part, up;
+        __device__ __forceinline__ uint64_t whole() const { return (uint64_t)part * up; }
+    };
+    __device__ __forceinline__ Weight weight(float x, const uint32_t *powers) const {
+        const float d = top - x, t = fminf(d * c, 64.f);
         // In 256th factors of two: the nearest whole number (the bits of a sum with 1.5 * 2^15), and the rest, with the
         // roundings of the difference and the product and the factor's second part.
         const float z = t + 49152.f, back = (top - d) - x;
         const float low = fmaf(d, c, -t) + fmaf(d, c_low, back * c);
         const float y = ((t - (z - 49152.f)) + low) * 0.693147180559945f;
-        const uint32_t k = __float_as_uint(z) - 0x47400000u;
+        const int k = (int)(__float_as_uint(z) - 0x47400001u);  // one less: an entry of the table, from 2^-(1/256) on, times 2^-y is below 1
         // 1 - 2^-y in three terms (|y| < 2^-9.4: the next is below 2^-42), as a whole number of 2^-31.
         const float e = y * fmaf(y, fmaf(y, 1.f / 6, -0.5f), 1.f);
         const int32_t cut = (int32_t)(__float_as_uint(fmaf(e, 2147483648.f, 12582912.f)) - 0x4b400000u);
-        const uint32_t p = powers[k & 255u];
-        const uint64_t w = p - (((int64_t)p * cut) >> 31);
-        return (w << 12) >> (k >> 8);
+        const uint32_t p = powers[k & 255], w = p - __umulhi(p, 2 * (uint32_t)cut + 1u) + (p & (uint32_t)(cut >> 31));  // (the 1: to the nearest, about)
+        const int octave = k >> 8;  // 44 binary places: 12 more than w has, less these (-1 beside the largest)
+        return Weight{__funnelshift_rc(w, 0, (uint32_t)max(octave - 12, 0)), 1u << max(12 - octave, 0)};
     }
 };
 
@@ -447,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 __syncthreads();
             }
     };
-    auto weight_at = [&](int i, int m) { return i < m ? h.weight(value_of(sh.all[i]), sh.powers) : 0; };
+    auto weight_at = [&](int i, int m) { return i < m ? h.weight(value_of(sh.all[i]), sh.powers).whole() : 0; };
     // Running sums of two elements of each thread, over the CTA. Returns the whole sum.
     auto scan = [&](const uint64_t (&w)[2], uint64_t (&upto)[2]) {
         uint64_t x = w[0] + w[1];
@@ -499,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             uint64_t sum = 0;
             uint32_t count = 0;
             each_token([&](int, Raw r) {
-                if (L::key(r) >= mid && h.bin(L::value(r)) == b) sum += by_mass ? h.weight(L::value(r), sh.powers) : 0, ++count;
+                if (L::key(r) >= mid && h.bin(L::value(r)) == b) sum += by_mass ? h.weight(L::value(r), sh.powers).whole() : 0, ++count;
             });
             const Sums s = add_up(sum, 0, count);
             if (by_mass ? s.mass >= target : s.count >= k) low = mid;
@@ -507,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         }
         // Of the tokens with this key, all of one weight, the first ones.
         const uint32_t key = (uint32_t)low;
-        const uint64_t each = h.weight(value_of((uint64_t)key << 32), sh.powers);
+        const uint64_t each = h.weight(value_of((uint64_t)key << 32), sh.powers).whole();
         const uint64_t wanted = by_mass ? (target - above_mass + each - 1) / each : k - above_count;
         const long long number = locate([&](int, Raw r) { return (uint64_t)(L::key(r) == key); }, [&](uint64_t) { return wanted - 1; });
         return place(key, (int)number);
@@ -570,8 +580,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         // the bins' own rounding. (Counts stay in shared memory, so that no registers are taken through the pass below.)
         constexpr int kEach = kBins / kThreads;
         auto edge = [&](int b) -> uint64_t {  // the largest weight of bin b, the smallest of b - 1: half a bin above its middle
-            const int x = max(8 * b - 4, 0);
-            return x >> 8 < 44 ? ((uint64_t)sh.powers[x & 255] << 12) >> (x >> 8) : 0;
+            const int x = max(8 * b - 4, 0) - 1;
+            return x >> 8 < 44 ? ((uint64_t)sh.powers[x & 255] << 13) >> ((x >> 8) + 1) : 0;
         };
         auto count_of = [&](int e) -> uint64_t { return sh.bins[tid * kEach + e]; };
         auto most_of = [&](int e) -> uint64_t {
@@ -650,21 +660,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             ptx::cluster_sync();  // nobody looks at gathered tokens any more
             for (int b = from + tid; b <= to; b += kThreads) sh.parts[0][b] = sh.parts[1][b] = 0;
             __syncthreads();
-            uint64_t sum = 0, front = 0;
+            uint64_t behind = 0, front = 0;
             each_token([&](int i, Raw r) {
                 if (border != 0 && !in_front_of_border(i, L::key(r))) return;
                 const float v = L::value(r);
-                const uint64_t w = h.weight(v, sh.powers);
+                const typename Heat::Weight y = h.weight(v, sh.powers);
                 const int b = h.bin(v);
-                sum += w;
-                if (b < from) {
-                    front += w;
-                } else if (b <= to) {
+                (b < from ? front : behind) += y.whole();
+                if (b >= from && b <= to) {
+                    const uint64_t w = y.whole();
                     const uint32_t old = atomicAdd(&sh.parts[0][b], (uint32_t)w), up = (uint32_t)(w >> 32) + (old + (uint32_t)w < old);
                     if (up) atomicAdd(&sh.parts[1][b], up);
                 }
             });
-            const Sums s = add_up(sum, front, 0);
+            const Sums s = add_up(front + behind, front, 0);
             uint64_t mass[kEach], my_mass = 0, all_mass;
 #pragma unroll
             for (int e = 0; e < kEach; ++e) {
@@ -693,7 +702,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     // ---------------------------------------------------------------- the sum of what is kept, and the token
     auto kept = [&](int i, Raw r) -> uint64_t {
         const float v = L::value(r);
-        return v >= floor_x && (border == 0 || in_front_of_border(i, L::key(r))) ? h.weight(v, sh.powers) : 0;
+        const typename Heat::Weight w = h.weight(v, sh.powers);
+        return (uint64_t)w.part * (v >= floor_x && (border == 0 || in_front_of_border(i, L::key(r))) ? w.up : 0u);
     };
     const long long token = locate(kept, [&](uint64_t whole) { return u < 1.f ? part_of(whole, u, false) : whole - 1; });
     if (rank == 0 && tid == 0) p.out[row] = token;
@@ -702,7 +712,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 
 template <typename T>
 cudaError_t launch(SampleParams p, int rows, int sms, cudaStream_t s) {
-    // CTAs of a row: as many as its tokens need room, and as many as there are SMs for.
+    // CTAs of a row: as many as its tokens need room, and as many as there are SMs for (what a CTA does whatever it has costs
+    // as much as a pass over 10000 logits: 256 rows of 150001 take 342 us with 4 CTAs to a row, 463 with 8).
     // (Two CTAs share an SM's 228 KB, of which each leaves 1 KB to the system.)
     const int room = (int)((113 * 1024 - sizeof(Shared<T>) - 64) / sizeof(T));
     int cluster = 1;
