@@ -179,3 +179,9 @@ def test_draws_have_their_probabilities(w4):
     got = torch.bincount(w4.w4a16_sample(x, u), minlength=40).double() / 2000
     want = torch.softmax(x[0].double(), 0)
     assert float((got - want).abs().max()) <= 1 / 2000 + 1e-6
+
+
+def test_more_rows_than_fit_the_gpu_at_once(w4):
+    r = np.random.RandomState(5)
+    x = torch.from_numpy(r.randn(3001, 700).astype(np.float32) * 3).cuda()
+    check(w4, x.half(), spread(3001, 6), top_p=[float(v) for v in r.rand(3001)], top_k=[int(v) for v in r.randint(0, 300, 3001)])

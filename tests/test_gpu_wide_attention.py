@@ -463,3 +463,15 @@ def test_two_calls_at_once(w4):
         torch.cuda.synchronize()
         for x, y in zip(first, outs):
             assert torch.equal(x, y)
+
+
+def test_most_requests_and_prefixes(w4):
+    r = np.random.RandomState(3)
+    n = 8192
+    s = Setup(w4, [1] * n, [int(x) for x in r.randint(1, 6, n)], heads=2, kv=1, dim=16, page=8)
+    s.prompt()
+    s.check()
+    of = [int(x) for x in r.randint(-1, 2048, n)]
+    s = Setup(w4, [1] * n, [int(x) for x in r.randint(1, 4, n)], [int(x) for x in r.randint(1, 20, 2048)], of, heads=2, kv=1, dim=16, page=8)
+    s.prefix()
+    s.check()

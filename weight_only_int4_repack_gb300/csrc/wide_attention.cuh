@@ -37,8 +37,8 @@
 // the output, 1500 more in a unit with masks. Code is kept small (rolled loops, waits out of
 // line): the roles together do not fit the first instruction caches, and what is rarely run
 // is fetched anew (an output's first time costs 7500 cycles).
-// 4099 rows of 40 heads over 8 kv heads of 128, bf16: 202 us, 0.85 PFLOP/s, 44% of a large
-// library product. 13 packed prompts behind prefixes, e4m3, 16 heads to a kv head: 337 us,
+// 4099 rows of 40 heads over 8 kv heads of 128, bf16: 201 us, 0.86 PFLOP/s, 45% of a large
+// library product; 16 of it join the tiles that were cut (42 MB of sums, written and read). 13 packed prompts behind prefixes, e4m3, 16 heads to a kv head: 337 us,
 // 46%. 4 prompts of heads of 256 with a window and a cap: 124 us, 21% (each score passes the
 // exponential unit three times). 64 requests behind 16001 tokens: 97 us, of which 43 are the
 // requests' own tokens, 8 the join.
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                         if constexpr (K::kOwnPower)
 #pragma unroll
                             for (int z = 0; z < kOnce; ++z)
-                                ys[z] = srcs[z] >= 0 && c * 8 < D ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) + srcs[z] + c * 8))
+                                ys[z] = srcs[z] >= 0 && c * 8 < D ? __ldcg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) + srcs[z] + c * 8))
                                                                   : make_uint4(0, 0, 0, 0);
 #pragma unroll
                         for (int z = 0; z < kOnce; ++z) {
@@ -699,7 +699,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                     const bool pre = j < own0;
                     const unsigned int y = pre ? j : j - own0 - g.gap, n = y / (unsigned int)p.c.page_size;
                     at = (int)(y - n * (unsigned int)p.c.page_size);
-                    page = __ldg((pre ? g.pre_pages : g.own_pages) + n);
+                    page = __ldcg((pre ? g.pre_pages : g.own_pages) + n);  // (written by the kernel in front, as a rule: not through the read-only path)
                 }
             };
             // Keys run kAhead units ahead of the values, as the products that need them do. A unit's places are looked up when its
@@ -1249,15 +1249,15 @@ __device__ __forceinline__ Sums<K::kDim> join_parts(const Params &p, int first, 
         float4 s[kOnce], y[kOnce][r.kEach];
 #pragma unroll
         for (int i = 0; i < kOnce; ++i) {
-            const int part = min(i0 + i, parts - 1);
+            const int part = i0 + i;
+            const bool there = part < parts;
             const float *from = p.slots + (long long)(2 * (first + part) + (part == 0)) * K::kSlot + row * K::kPitch;
-            s[i] = __ldcg(reinterpret_cast<const float4 *>(from + DT));
+            s[i] = there ? __ldcg(reinterpret_cast<const float4 *>(from + DT)) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < r.kEach; ++e) {
                 const int d = 4 * (lane + 32 * e);
-                y[i][e] = d < D ? __ldcg(reinterpret_cast<const float4 *>(from + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                y[i][e] = there && d < D ? __ldcg(reinterpret_cast<const float4 *>(from + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            if (i0 + i >= parts) s[i] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
         }
         float top = r.m;
 #pragma unroll
@@ -1365,7 +1365,8 @@ __device__ __forceinline__ void store4(T *to, const float4 &y, float *check) {
     *reinterpret_cast<uint2 *>(to) = make_uint2(elem::pair_from_f32<T>(y.x, y.y), elem::pair_from_f32<T>(y.z, y.w));
 }
 
-constexpr int kJoinWarps = 8, kJoinRows = 16;  // of a block
+// Of a block. (8 rows to a block: 17 us to join 4099 rows' tiles and 6 for drafts, 32: 15.6 and 6, 16: 16 and 4.7.)
+constexpr int kJoinWarps = 8, kJoinRows = 16;
 
 // Requests: the tiles that were cut are joined, and rows that are no finite numbers looked at again.
 template <typename T, typename C, int DT>
