@@ -39,8 +39,8 @@
 // is fetched anew (an output's first time costs 7500 cycles).
 // 4099 rows of 40 heads over 8 kv heads of 128, bf16: 201 us, 0.86 PFLOP/s, 45% of a large
 // library product; 16 of it join the tiles that were cut (42 MB of sums, written and read). 13 packed prompts behind prefixes, e4m3, 16 heads to a kv head: 337 us,
-// 46%. 4 prompts of heads of 256 with a window and a cap: 124 us, 21% (each score passes the
-// exponential unit three times). 64 requests behind 16001 tokens: 97 us, of which 43 are the
+// 46%. 4 prompts of heads of 256 with a window and a cap: 119 us, 22% (the cap takes 2000 of
+// the 3900 cycles of a unit of 128 rows and 64 keys). 64 requests behind 16001 tokens: 97 us, of which 43 are the
 // requests' own tokens, 8 the join.
 #pragma once
 
@@ -1026,7 +1026,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                 unit_n += count;
                 continue;
             }
-            float k_scale = K::k8 && p.c.k_scale ? p.c.k_scale[kvh] : 1.f, unit = 1.f, slack = 0.f;
+            float k_scale = K::k8 && p.c.k_scale ? p.c.k_scale[kvh] : 1.f, unit = 1.f, slack = 0.f, in2 = 0.f, cap = 0.f;
             float m = kLowest, limit = kLowest, shift = 0.f;
             bool far = false;
             float2 l = make_float2(0.f, 0.f);
@@ -1037,7 +1037,11 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                 tc5::fence_after();
                 if (j == 0) {
                     if constexpr (K::kOwnPower) k_scale *= sh.powers[qi][row];
-                    unit = p.softcap > 0.f ? 1.f : unit_of(p, k_scale);
+                    unit = unit_of(p, k_scale);
+                    if (p.softcap > 0.f) {
+                        const Scores sc(p, k_scale);
+                        unit = 1.f, in2 = sc.in, cap = sc.cap;
+                    }
                     slack = kSlack / unit;
                     done();
                 }
@@ -1045,8 +1049,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                     const int key0 = key_first + j * kKeys;
                     const uint32_t *bad = sh.bad[unit_n & 15];
                     const bool masked = __any_sync(0xffffffffu, lo > key0 || hi - kKeys < key0) || (bad[0] | bad[1] | bad[2] | bad[3]);
-                    if (masked || p.softcap > 0.f) {  // what is not a plain product goes back to where the products were
-                        const Scores sc(p, k_scale);
+                    if (masked || cap != 0.f) {  // what is not a plain product goes back to where the products were
 #pragma unroll 1
                         for (int c = 0; c < kKeys / 32; ++c) {
                             // Which of these 32 the row sees, as bits; where all rows see all of them the products stay.
@@ -1055,13 +1058,23 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                             seen &= from <= 0 ? ~0u : from < 32 ? ~0u << from : 0u;
                             seen &= to >= 32 ? ~0u : to > 0 ? ~(~0u << to) : 0u;
                             const bool whole = __all_sync(0xffffffffu, seen == ~0u);
-                            if (whole && !sc.capped) continue;
+                            if (whole && cap == 0.f) continue;
                             uint32_t v[32];
                             tc5::ld32(t_s + c * 32, v);
                             tc5::wait_ld();
-                            if (sc.capped)
+                            if (cap != 0.f) {  // Scores::squeezed, step by step for all 32
+                                auto all = [&](auto f) {
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(sc.squeezed(__uint_as_float(v[i])));
+                                    for (int i = 0; i < 32; i += 2) {
+                                        const float2 y = f(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+                                        v[i] = __float_as_uint(y.x), v[i + 1] = __float_as_uint(y.y);
+                                    }
+                                };
+                                const float2 by = make_float2(in2, in2), two = make_float2(-2.f * cap, -2.f * cap), one = make_float2(cap, cap);
+                                all([&](float2 x) { x = fma2(x, by, make_float2(0.f, 0.f)); return make_float2(ex2(x.x), ex2(x.y)); });
+                                all([&](float2 x) { x = add2(x, make_float2(1.f, 1.f)); return make_float2(rcp(x.x), rcp(x.y)); });
+                                all([&](float2 x) { return fma2(x, two, one); });
+                            }
                             if (!whole)
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
@@ -1097,14 +1110,19 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                         if (j > 0) {  // once the last product has been added to the outputs
                             if (!wait(&sh.o_step[x], (step - segs_had - 1) & 1u)) break;
                             tc5::fence_after();
+                            constexpr int kBoth = DT > 128 ? 2 : 1;  // (with 128 registers a thread two spill)
 #pragma unroll 1
-                            for (int c = 0; c < (D + 15) / 16; ++c) {
-                                uint32_t o[16];
-                                tc5::ld16(t_o + c * 16, o);
+                            for (int c = 0; c < (D + 16 * kBoth - 1) / (16 * kBoth); ++c) {
+                                uint32_t o[kBoth][16];
+#pragma unroll
+                                for (int z = 0; z < kBoth; ++z) tc5::ld16(t_o + (c * kBoth + z) * 16, o[z]);
                                 tc5::wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-                                tc5::st16(t_o + c * 16, o);
+                                for (int z = 0; z < kBoth; ++z) {
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) o[z][i] = __float_as_uint(__uint_as_float(o[z][i]) * keep);
+                                    tc5::st16(t_o + (c * kBoth + z) * 16, o[z]);
+                                }
                             }
                         }
                         l.x *= keep, l.y *= keep;
