@@ -133,6 +133,7 @@ class Decoder:
             torch.argmax(logits, 1, out=out)
         else:
             w4.w4a16_sample(logits, uniform, **sampling, out=out)
+            out.clamp_(min=0)  # -1: logits that are none, from which nothing can be drawn
 
     def many(self, tokens, positions, slots, table, starts, lens, **prefix):
         """The layers over many tokens of some requests; returns the rows that the head reads."""

@@ -192,6 +192,9 @@ def test_binding_refusals(w4):
     no(ValueError, run, q, c, table, starts, lens, prefix_table=table, prefix_lens=i32(2), prefix_of=lens, **kw)
     no(TypeError, run, q, c, table, starts, lens, prefix_table=table, prefix_lens=lens.long(), prefix_of=lens, **kw)
     no(ValueError, run, q, c, table, starts, lens, **kw)                    # not on a GPU
+    for broadcast in (half(1, 4, 64).expand(5, 4, 64), half(5, 1, 64).expand(5, 4, 64)):
+        with pytest.raises(ValueError, match="one place"):
+            run(q, c, table, starts, lens, out=broadcast, workspace=ws, stream=0)
     one = q[:3]
     kw = dict(out=torch.zeros_like(one), workspace=ws)
     no(ValueError, shared, one, c, table, i32(2), table, lens, lens, **kw)

@@ -570,6 +570,8 @@ def _attention_tensors(where, q, cache, table, out, lse, *ints):
         if lse.numel() != q.shape[0] * q.shape[1]:
             raise ValueError("lse: [rows, heads]")
     rows, heads = q.shape[0] > 1, q.shape[1] > 1  # strides over one entry say nothing
+    if (rows and so[0] == 0) or (heads and so[1] == 0):
+        raise ValueError(f"{where}: rows of out lie in one place")
     return sq[0] if rows else 0, sq[1] if heads else 0, so[0] if rows else 0, so[1] if heads else 0
 
 
