@@ -70,12 +70,12 @@ struct Heat {
         return (int)(__float_as_uint(t + 12582912.f) - 0x4b400000u);
     }
     // As a product of two 32-bit numbers, which sums take up in one instruction. (Of what is far below the largest, infinities
-    // and NaN the first is 0: all of it is shifted out.)
+    // and NaN the second is 0.)
     struct Weight {
         uint32_t part, up;
         __device__ __forceinline__ uint64_t whole() const { return (uint64_t)part * up; }
     };
-    __device__ __forceinline__ Weight weight(float x, const uint32_t *powers) const {
+    __device__ __forceinline__ Weight weight(float x, const uint32_t *powers, const uint2 *octaves) const {
         const float d = top - x, t = fminf(d * c, 64.f);
         // In 256th factors of two: the nearest whole number (the bits of a sum with 1.5 * 2^15), and the rest, with the
         // roundings of the difference and the product and the factor's second part.
@@ -85,10 +85,11 @@ struct Heat {
         const int k = (int)(__float_as_uint(z) - 0x47400001u);  // one less: an entry of the table, from 2^-(1/256) on, times 2^-y is below 1
         // 1 - 2^-y in three terms (|y| < 2^-9.4: the next is below 2^-42), as a whole number of 2^-31.
         const float e = y * fmaf(y, fmaf(y, 1.f / 6, -0.5f), 1.f);
-        const int32_t cut = (int32_t)(__float_as_uint(fmaf(e, 2147483648.f, 12582912.f)) - 0x4b400000u);
-        const uint32_t p = powers[k & 255], w = p - __umulhi(p, 2 * (uint32_t)cut + 1u) + (p & (uint32_t)(cut >> 31));  // (the 1: to the nearest, about)
-        const int octave = k >> 8;  // 44 binary places: 12 more than w has, less these (-1 beside the largest)
-        return Weight{__funnelshift_rc(w, 0, (uint32_t)max(octave - 12, 0)), 1u << max(12 - octave, 0)};
+        const int32_t cut = (int32_t)(2 * __float_as_uint(fmaf(e, 2147483648.f, 12582912.f)) - 0x967fffffu);  // twice, and 1: to the nearest, about
+        // p - (p cut >> 32), p taken as the signed number that is 2^32 less.
+        const uint32_t p = powers[k & 255], w = p - (uint32_t)__mulhi((int)p, cut) - (uint32_t)cut;
+        const uint2 places = octaves[k >> 8];  // (-1 beside the largest)
+        return Weight{w >> places.x, places.y};
     }
 };
 
@@ -175,6 +176,7 @@ struct alignas(16) Shared {
     uint32_t bins[kBins];         // all of them
     uint32_t listed, key_low, key_high;
     uint32_t powers[256];
+    uint2 octaves[66];            // of octave o - 1: 44 binary places, 12 more than an entry of powers has, less o - 1
     uint64_t mass_slot[4][2];     // what a step adds up over the cluster
     uint32_t count_slot[4];
     float max_slot;
@@ -236,6 +238,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 
     // ---------------------------------------------------------------- logits into shared memory, and their maximum
     if (tid < 256) sh.powers[tid] = kPowers.v[tid];
+    else if (tid < 256 + 66) {
+        const int o = tid - 257;
+        sh.octaves[o + 1] = make_uint2((unsigned)min(max(o - 12, 0), 31), o < 44 ? 1u << max(12 - o, 0) : 0u);
+    }
     float top = -INFINITY;
     {
 #pragma unroll 4
@@ -411,10 +417,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         if constexpr (sizeof(Raw) == 4) return L::value(key & 0x80000000u ? key & 0x7fffffffu : ~key);
         else return L::value((Raw)(key & 0x8000u ? key & 0x7fffu : ~key));
     };
-    auto in_front_of_border = [&](int i, uint32_t key) {
-        const uint32_t k = (uint32_t)(border >> 32);
-        return key > k || (key == k && (uint32_t)~(c0 + i) >= (uint32_t)border);
+    // The same as a logit and the last of this CTA's tokens that is kept with that logit.
+    float border_x = -INFINITY;
+    int border_i = INT_MAX;
+    auto set_border = [&](uint64_t at) {
+        border = at, border_x = value_of(at), border_i = (int)~(uint32_t)at - c0;
     };
+    auto in_front_of_border = [&](int i, float v) { return v > border_x || (v == border_x && i <= border_i); };
     uint32_t key_least = 0, key_most = 0;  // of the tokens that this thread has gathered
     // Tokens of the bins from `from` to `to`, gathered by each CTA and then brought together in the first: sh.all, by their
     // places. Returns how many (above kMost: not all are there).
@@ -457,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 __syncthreads();
             }
     };
-    auto weight_at = [&](int i, int m) { return i < m ? h.weight(value_of(sh.all[i]), sh.powers).whole() : 0; };
+    auto weight_at = [&](int i, int m) { return i < m ? h.weight(value_of(sh.all[i]), sh.powers, sh.octaves + 1).whole() : 0; };
     // Running sums of two elements of each thread, over the CTA. Returns the whole sum.
     auto scan = [&](const uint64_t (&w)[2], uint64_t (&upto)[2]) {
         uint64_t x = w[0] + w[1];
@@ -509,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             uint64_t sum = 0;
             uint32_t count = 0;
             each_token([&](int, Raw r) {
-                if (L::key(r) >= mid && h.bin(L::value(r)) == b) sum += by_mass ? h.weight(L::value(r), sh.powers).whole() : 0, ++count;
+                if (L::key(r) >= mid && h.bin(L::value(r)) == b) sum += by_mass ? h.weight(L::value(r), sh.powers, sh.octaves + 1).whole() : 0, ++count;
             });
             const Sums s = add_up(sum, 0, count);
             if (by_mass ? s.mass >= target : s.count >= k) low = mid;
@@ -517,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         }
         // Of the tokens with this key, all of one weight, the first ones.
         const uint32_t key = (uint32_t)low;
-        const uint64_t each = h.weight(value_of((uint64_t)key << 32), sh.powers).whole();
+        const uint64_t each = h.weight(value_of((uint64_t)key << 32), sh.powers, sh.octaves + 1).whole();
         const uint64_t wanted = by_mass ? (target - above_mass + each - 1) / each : k - above_count;
         const long long number = locate([&](int, Raw r) { return (uint64_t)(L::key(r) == key); }, [&](uint64_t) { return wanted - 1; });
         return place(key, (int)number);
@@ -647,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 return;
             }
             whole_least = f.least_before, whole_most = f.most_before + f.most_in;
-            border = resolve(bin_k, false, (uint32_t)top_k - f.before, 0);
+            set_border(resolve(bin_k, false, (uint32_t)top_k - f.before, 0));
         } else if (all_count <= kMost) {
             draw_from_few(kBins - 1, 0);
             return;
@@ -662,9 +671,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             __syncthreads();
             uint64_t behind = 0, front = 0;
             each_token([&](int i, Raw r) {
-                if (border != 0 && !in_front_of_border(i, L::key(r))) return;
                 const float v = L::value(r);
-                const typename Heat::Weight y = h.weight(v, sh.powers);
+                if (border != 0 && !in_front_of_border(i, v)) return;
+                const typename Heat::Weight y = h.weight(v, sh.powers, sh.octaves + 1);
                 const int b = h.bin(v);
                 (b < from ? front : behind) += y.whole();
                 if (b >= from && b <= to) {
@@ -694,16 +703,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                     return;
                 }
                 const uint64_t at = resolve((int)f.bin, true, 0, target - reached);
-                border = border > at ? border : at;
+                if (at > border) set_border(at);
             }
         }
     }
 
     // ---------------------------------------------------------------- the sum of what is kept, and the token
+    if (floor_x > border_x) border_x = floor_x, border_i = INT_MAX;
     auto kept = [&](int i, Raw r) -> uint64_t {
         const float v = L::value(r);
-        const typename Heat::Weight w = h.weight(v, sh.powers);
-        return (uint64_t)w.part * (v >= floor_x && (border == 0 || in_front_of_border(i, L::key(r))) ? w.up : 0u);
+        const typename Heat::Weight w = h.weight(v, sh.powers, sh.octaves + 1);
+        return (uint64_t)w.part * (in_front_of_border(i, v) ? w.up : 0u);
     };
     const long long token = locate(kept, [&](uint64_t whole) { return u < 1.f ? part_of(whole, u, false) : whole - 1; });
     if (rank == 0 && tid == 0) p.out[row] = token;
