@@ -1,7 +1,8 @@
 """GPU parity of w4a16_sample with its float64 statement: the same token, unless the random number or top-p is nearer to a
 border between two tokens than the weights' precision.
 
-A weight is off by less than 2^-31 of itself, a sum by as much, the float64 statement by n 2^-53: answers may differ where
+A weight is off by less than 2^-30 of itself. A border F is a quotient of two sums, which errors e and f of what is in front
+of it and behind move by F (1 - F) |e - f|, less than 2^-31; the float64 statement is off by n 2^-53: answers may differ where
 a border is nearer than 2^-30 of the sum. Rows where one is (none of the seeds here) would be left out, not accepted.
 """
 import math
