@@ -188,7 +188,7 @@ struct alignas(16) Shared {
     uint64_t owner_before;
     uint64_t found_mass, found_border;
     Found found;
-    long long token;
+    long long token[4];           // what a step has found, read by the whole cluster after its last barrier: a place for each of four steps
 };
 
 template <typename T>
@@ -320,9 +320,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         }
         __syncthreads();
         if (lane == 31) sh.sums[0][warp] = upto;
-        if (tid == 0) sh.token = -1, sh.owner = -1;
-        __syncthreads();
         const int slot = step++ & 3;
+        if (tid == 0) sh.token[slot] = -1, sh.owner = -1;  // (others may still read the last step's)
+        __syncthreads();
         uint64_t mine_all = 0, before = upto - sum;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 }
                 const uint32_t mask = __ballot_sync(0xffffffffu, front + run > target);
                 if (mask) {
-                    if (lane == 0) sh.token = c0 + i0 + __ffs(mask) - 1;
+                    if (lane == 0) sh.token[slot] = c0 + i0 + __ffs(mask) - 1;
                     break;
                 }
                 front += __shfl_sync(0xffffffffu, run, 31);
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         }
         ptx::cluster_sync();
         long long token = -1;
-        for (int r = 0; r < cluster; ++r) token = max(token, (long long)ld64(reinterpret_cast<const uint64_t *>(&sh.token), r));
+        for (int r = 0; r < cluster; ++r) token = max(token, (long long)ld64(reinterpret_cast<const uint64_t *>(&sh.token[slot]), r));
         return token;
     };
     const bool nothing = top == -INFINITY;                                     // no token may be drawn
