@@ -743,9 +743,10 @@ w4a16_status w4a16_prefix_attention_block(const w4a16_prefix_attention_args *arg
  *   out     device int64 [rows]: the token, or -1 in a row without a logit above minus
  *           infinity. NaN counts as minus infinity, and beside plus infinity nothing else
  *           is drawn
- * Weights are 64-bit fixed-point numbers off by less than 2^-30 of themselves; their sums
- * are exact, so that a row's token depends on nothing but the row. Weights below 2^-44
- * of the largest are 0.
+ * Weights are 64-bit fixed-point numbers, off by less than 2^-30 of themselves and 2^-44
+ * of the largest; their sums are exact, so that a row's token depends on nothing but the
+ * row. Borders between two tokens, as parts of the sum, are off by less than 2^-31 and
+ * 2^-44 for each token. Weights below 2^-44 of the largest are 0.
  * In the device error word: a temperature below 0 or NaN (taken as 0), NaN as top_p or
  * min_p (not wanted), u outside of [0, 1] or NaN (taken as the nearest, NaN as 0).
  * Refused as unsupported: vocab above 2^18, rows above 2^20.

@@ -1,5 +1,6 @@
 """Sampling where it is hardest to get right: steps of a cluster that follow each other closely, weights that are taken by
 differences of logits of any size, random numbers next to a border between two tokens."""
+import numpy as np
 import pytest
 import torch
 
@@ -31,3 +32,73 @@ def test_a_border_among_equal_logits_again_and_again(w4, dtype, vocab):
     for i in range(400):
         w4.w4a16_sample(x, u, top_k=k, top_p=p, out=out[i])
     assert bool((out == torch.tensor(want, device="cuda")).all())
+
+
+# A weight is off by less than 2^-30 of itself and 2^-44 of the largest. A border F between two tokens is a quotient of two
+# sums, which errors of e and f of what is in front of it and behind move by F (1 - F) |e - f| < 2^-31; the second part adds
+# 2^-44 for each token, the sum being the largest weight at least. The float64 statement is off by n 2^-53.
+def bound(n):
+    return 2.0**-31 + n * (2.0**-44 + 2.0**-53)
+
+
+def next_to_a_border(upto):
+    """The float32 number that is nearest to one of the borders `upto` (float64, from 0 to 1), but not nearer than twice the
+    bound; None if there is none within 2^-28."""
+    near = upto[:-1].astype(np.float32)
+    u = np.stack([near, np.nextafter(near, np.float32(0)), np.nextafter(near, np.float32(1))])
+    far = np.abs(u.astype(np.float64) - upto[:-1])
+    far[(far <= 2 * bound(len(upto))) | (u <= 0) | (u >= 1)] = 1
+    at = np.unravel_index(far.argmin(), far.shape)
+    return float(u[at]) if far[at] < 2.0**-28 else None
+
+
+def rows_of(kind, n, dtype, g):
+    """Logits whose largest is smaller than the others' magnitudes, so that differences to it need more bits than 32."""
+    x = -torch.rand(n, generator=g) * 6 - 0.3
+    if kind == "negative":       # all but the largest a little beyond a power of two
+        x = -4.0 - torch.rand(n, generator=g) * 1e-2
+        x[int(torch.randint(0, n, (1,), generator=g))] = -1.0 - float(torch.rand(1, generator=g)) * 0.7
+    elif kind == "tiny largest":
+        x[int(torch.randint(0, n, (1,), generator=g))] = 2.0**-24 * float(torch.randint(1, 512, (1,), generator=g))
+    else:
+        x = torch.log_softmax(x, 0)
+    return x.to(dtype)
+
+
+@pytest.mark.parametrize("kind,dtype", [("log-probabilities", F32), ("tiny largest", F32), ("tiny largest", F16), ("negative", F32),
+                                        ("log-probabilities", BF16)])
+@pytest.mark.parametrize("n", [7, 60, 2500])
+def test_next_to_a_border(w4, kind, dtype, n):
+    g = torch.Generator().manual_seed(n)
+    rows, us, ps = [], [], []
+    while len(rows) < 48:
+        x = rows_of(kind, n, dtype, g)
+        v = x.double().numpy()
+        if len(rows) % 2:  # a border of the draw
+            w = np.exp(v - v.max())
+            u, p = next_to_a_border(np.cumsum(w) / w.sum()), 1.0
+        else:              # of top-p: the last random number that is not 1 draws the last token that is left, or one near it
+            w = np.sort(np.exp(v - v.max()))[::-1]
+            u, p = 1.0, next_to_a_border(np.cumsum(w) / w.sum())
+        if u is not None and p is not None:
+            rows.append(x), us.append(u), ps.append(p)
+    x = torch.stack(rows)
+    got = w4.w4a16_sample(x.cuda(), torch.tensor(us, device="cuda"), top_p=torch.tensor(ps, device="cuda")).tolist()
+    for r in range(len(rows)):
+        assert got[r] == sample(x[r].double().numpy(), us[r], 1.0, 0, ps[r])[0], f"row {r}, u {us[r]}, top-p {ps[r]}"
+
+
+@pytest.mark.parametrize("down", [20.0, 26.0, 29.5])
+def test_many_small_weights(w4, down):
+    # One token of weight 1 and 200000 far below it: whichever of these is drawn, its borders are next to u.
+    n, rows = 200001, 16
+    g = torch.Generator().manual_seed(1)
+    x = -down - torch.rand(n, generator=g)
+    x[77] = 0.0
+    w = np.exp(x.double().numpy())
+    upto = np.cumsum(w)
+    u = torch.from_numpy(np.float32(1) - np.float32(2.0**-24) * np.arange(rows, dtype=np.float32))
+    got = w4.w4a16_sample(x.expand(rows, n).contiguous().cuda(), u.cuda()).tolist()
+    for token, at in zip(got, u.double().tolist()):
+        before = upto[token - 1] if token else 0.0
+        assert before / upto[-1] - bound(n) <= at <= upto[token] / upto[-1] + bound(n), (token, at)

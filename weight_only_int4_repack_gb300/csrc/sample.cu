@@ -4,9 +4,11 @@
 //     number, at which the kept weights' running sum exceeds u times their sum
 //
 // Weights are fixed-point numbers of 44 binary places in 64-bit integers, off by less than 2^-30 of themselves (2^-32 each
-// from the table, the rest's whole number and the product, as much from the rest's roundings): sums are exact and so do not
-// depend on any order, and a border between two tokens, a quotient of two sums, moves by less than 2^-31, about what it would
-// take for a 32-bit random number to show it. A weight below 2^-44 of the largest is 0.
+// from the table, the rest's whole number and the product, as much from the rest's roundings) and, below 2^-12 of the largest,
+// by what is cut off below 2^-44 of it. Sums are exact and so do not depend on any order. A border between two tokens, a
+// quotient of two sums, moves by less than 2^-31, about what it would take for a 32-bit random number to show it, and by less
+// than 2^-44 for each token (where 2^18 tokens are all that far below the largest, 2^-26: a few of them). A weight below 2^-44
+// of the largest is 0.
 //
 // A row is one cluster of CTAs, which keeps its logits in shared memory, so that each is read from memory once. The border of
 // top-k and top-p is found by a histogram of counts over 32 bins for each factor of two of the weight. It
@@ -80,7 +82,8 @@ struct Heat {
         const float d = top - x, t = fminf(d * c, 64.f);
         // In 256th factors of two: the nearest whole number (the bits of a sum with 1.5 * 2^15), and the rest, with the
         // roundings of the difference and the product and the factor's second part.
-        const float z = t + 49152.f, back = (top - d) - x;
+        // (What the difference's rounding took is taken back by the sum of two numbers of any magnitudes: `x` may be the larger.)
+        const float z = t + 49152.f, over = d - top, back = (top - (d - over)) - (x + over);
         const float low = fmaf(d, c, -t) + fmaf(d, c_low, back * c);
         const float y = ((t - (z - 49152.f)) + low) * 0.693147180559945f;
         const int k = (int)(__float_as_uint(z) - 0x47400001u);  // one less: an entry of the table, from 2^-(1/256) on, times 2^-y is below 1
