@@ -516,6 +516,8 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             }
         }
     }
+    // The plan has been written and read by ordinary accesses where boxes of tensor maps are written next.
+    fence_async();
     tc5::fence_before();
     __syncthreads();
     tc5::fence_after();
