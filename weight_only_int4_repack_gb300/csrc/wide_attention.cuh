@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
             if (!wait(&sh.q_empty, (uint32_t)(n + 1) & 1u)) break;
             if (!K::kOwnPower && p.q_tma) {
                 // A box holds the tile's rows in their order: heads of a token, token after token. Rows behind the request's last
-                // one are others' or zero, and nobody looks at them.
+                // one are others' or zero, or what lay there before: they have no part in what the tile's own rows get.
                 if (w == 0 && elect()) {
                     ptx::mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(tt * gb * DT * 2));
                     for (int i = 0; i < DT / 64; ++i)
@@ -1105,9 +1105,10 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                         tops(v[1]);
                     }
                     const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                    if (__any_sync(0xffffffffu, mx > limit)) {
+                    // Rows that are none have no vote here: what is in them is other requests' or an earlier kernel's.
+                    if (__any_sync(0xffffffffu, in && mx > limit)) {
                         const float y = fmaxf(m, mx), far_y = y * unit, at_y = y > kLowest ? fmaf(-y, unit, K::kUp) : 0.f;
-                        far = __any_sync(0xffffffffu, fabsf(far_y) >= 1024.f && y > kLowest);
+                        far = __any_sync(0xffffffffu, in && fabsf(far_y) >= 1024.f && y > kLowest);
                         const float keep = m == kLowest ? 0.f : far ? ex2((m - y) * unit) : ex2(at_y - shift);  // nothing so far: nothing is kept
                         if (j > 0) {  // once the last product has been added to the outputs
                             if (!wait(&sh.o_step[x], (step - segs_had - 1) & 1u)) break;
