@@ -627,8 +627,9 @@ w4a16_status w4a16_residual_rmsnorm_block(const w4a16_residual_rmsnorm_args *arg
  * counts as its row), a prefix number of `prefixes` or more (no prefix) and a prefix length
  * beyond its row; a page number out of range, whose tokens are left out. A row that sees
  * no key gets out = 0 and lse = -inf.
- * The result does not depend on timing. Scores, their maximum and the sums are fp32.
- * Weights are rounded once to `type`, as operands (2^-11 of a weight in fp16, down to
+ * The result does not depend on timing. Scores, their maximum and the sums are fp32; a
+ * softcap up to 128 leaves scores off by 2^-22 of it, a larger one by a few roundings of
+ * themselves. Weights are rounded once to `type`, as operands (2^-11 of a weight in fp16, down to
  * 2^-25 of the largest; 2^-8 in bf16); their sum, which outputs are divided by and lse
  * comes from, is that of the unrounded ones. Values that a row does not see do not reach it,
  * whatever they are.

@@ -1,8 +1,9 @@
 """Attention of many rows at its limits: what lies in shared memory where a call begins, rows of a tile that are nobody's."""
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_wide_attention import BF16, F16, Setup, w4  # noqa: F401
+from test_gpu_wide_attention import BF16, E, E4M3, F16, Setup, U, f64, w4  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +40,26 @@ def test_rows_that_are_nobody_s_change_nothing(w4, dim, dtype, new, pad):  # noq
         s.prompt()
         same = torch.equal(s.out[mine], first[0]), torch.equal(s.lse[mine], first[1])
         assert same == (True, True), level
+
+
+def check_scores_to_their_own_size(s, softcap):
+    """As Setup.check, for a cap that costs each score a few roundings of itself and nothing that goes by the cap."""
+    torch.cuda.synchronize()
+    u, out, lse = U[s.dtype], f64(s.out), f64(s.lse)
+    for at, (want, want_lse, mag, top), n in s.want(s.dim**-0.5, 0, softcap):
+        # products' sum, then scale, quotient by the cap, tanh (2), product with the cap, difference, exponential
+        eps = (s.dim + 24) * E * top + (n + 8) * E + 2.0**-22
+        bound = u * np.abs(want) + 2 * (u + eps)[..., None] * mag + n * 2.0**-36 * (mag.max() + 1) + 2.0**-24
+        assert (np.abs(out[at] - want) <= bound).all() and (np.abs(lse[at] - want_lse) <= eps + 2 * E * np.abs(want_lse)).all()
+
+
+@pytest.mark.parametrize("dim,dtype,cache", [(64, F16, F16), (128, BF16, BF16), (128, BF16, E4M3), (256, F16, F16)])
+@pytest.mark.parametrize("softcap", [129.0, 1000.0, 1e4, 1e6, 1e20, 3e38])
+def test_large_caps(w4, softcap, dim, dtype, cache):  # noqa: F811
+    s = Setup(w4, [3, 70], [200, 300], [100], [0, -1], heads=6, kv=2, dim=dim, dtype=dtype, cache=cache)
+    s.prompt(softcap=softcap)
+    check_scores_to_their_own_size(s, softcap)
+    s = Setup(w4, [1] * 20, [1 + 7 * i for i in range(20)], [400], [-(i % 2) for i in range(20)], heads=6, kv=2, dim=dim, dtype=dtype,
+              cache=cache)
+    s.prefix(softcap=softcap)
+    check_scores_to_their_own_size(s, softcap)

@@ -792,7 +792,8 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
                 }
             }
             if (p.softcap > 0.f) {
-                const float in = to_score / p.softcap, out = p.softcap * kLog2e;
+                const float most = fminf(p.softcap, 1e30f);  // (its product stays finite; what it takes off lower scores is not seen)
+                const float in = to_score / most, out = most * kLog2e;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll

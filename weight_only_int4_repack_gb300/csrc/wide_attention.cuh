@@ -366,22 +366,39 @@ __device__ __forceinline__ float unit_of(const Params &p, float k_scale) {
 // How a raw product becomes a score, in units of log2.
 struct Scores {
     float unit;            // without a cap: score * log2(e) of a product
-    float in, cap;         // with one: 2 * log2(e) / softcap * scale, softcap * log2(e)
+    float in, cap;         // with one: 2 * log2(e) / softcap * scale, softcap * log2(e) (no more than 1e30: sums and products of it
+                           // stay finite, and what it would take off lower scores is not seen)
     float slack;           // kSlack powers of two, as a difference of products
     bool capped;
     __device__ __forceinline__ Scores(const Params &p, float k_scale) {
         const float to_score = (p.scale != 0.f ? fabsf(p.scale) : 1.f) * k_scale;
         unit = unit_of(p, k_scale);
         capped = p.softcap > 0.f;
-        in = capped ? fminf(2.f * kLog2e * to_score / p.softcap, 3e38f) : 0.f;  // (0 times it is 0)
-        cap = p.softcap * kLog2e;
+        const float most = fminf(p.softcap, 1e30f);
+        in = capped ? fminf(2.f * kLog2e * to_score / most, 3e38f) : 0.f;  // (0 times it is 0)
+        cap = most * kLog2e;
         slack = kSlack / unit;
     }
-    // cap * tanh(x): 1 - 2 / (1 + e^2x), off by a few 2^-24 of the cap.
-    __device__ __forceinline__ float squeezed(float s) const { return fmaf(rcp(1.f + ex2(s * in)), -2.f * cap, cap); }
+    // cap * tanh(x), 2x the exponent of e that `in` gives as one of 2.
+    static __device__ __forceinline__ float squeezed(float s, float in, float cap) { return cap * tanhf(s * (in * 0.34657359f)); }
+    __device__ __forceinline__ float squeezed(float s) const { return squeezed(s, in, cap); }
     // What a reference m is as a score.
     __device__ __forceinline__ float of(float m) const { return capped ? squeezed(m) : m * unit; }
 };
+
+// A cap up to here is taken by 1 - 2 / (1 + e^2x), which is off by 2^-22 of the cap: less than 2^-15 in a score, where an
+// operand's weight has 2^-11. Above it that would be seen, and scores that a large cap leaves as they are would be lost in it.
+constexpr float kQuickCap = 128.f * kLog2e;
+// 32 columns of scores with a larger cap, in their place. (Out of line: caps are smaller, as a rule.)
+static __device__ __noinline__ void squeeze_in_place(uint32_t at, float in, float cap) {
+    uint32_t v[32];
+    tc5::ld32(at, v);
+    tc5::wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(Scores::squeezed(__uint_as_float(v[i]), in, cap));
+    tc5::st32(at, v);
+    tc5::wait_st();
+}
 
 // ------------------------------------------------------------------ the kernel
 template <typename T, typename C, int DT>
@@ -1060,11 +1077,13 @@ __global__ void __launch_bounds__(Config<T, C, DT>::kThreads, 1) wide_kernel(con
                             seen &= from <= 0 ? ~0u : from < 32 ? ~0u << from : 0u;
                             seen &= to >= 32 ? ~0u : to > 0 ? ~(~0u << to) : 0u;
                             const bool whole = __all_sync(0xffffffffu, seen == ~0u);
-                            if (whole && cap == 0.f) continue;
+                            const bool quick = cap != 0.f && cap <= kQuickCap;
+                            if (cap > kQuickCap) squeeze_in_place(t_s + c * 32, in2, cap);
+                            if (whole && !quick) continue;
                             uint32_t v[32];
                             tc5::ld32(t_s + c * 32, v);
                             tc5::wait_ld();
-                            if (cap != 0.f) {  // Scores::squeezed, step by step for all 32
+                            if (quick) {  // cap * (1 - 2 / (1 + e^2x)), step by step for all 32
                                 auto all = [&](auto f) {
 #pragma unroll
                                     for (int i = 0; i < 32; i += 2) {
