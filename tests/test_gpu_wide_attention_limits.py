@@ -63,3 +63,16 @@ def test_large_caps(w4, softcap, dim, dtype, cache):  # noqa: F811
               cache=cache)
     s.prefix(softcap=softcap)
     check_scores_to_their_own_size(s, softcap)
+
+
+def test_the_largest_window_of_rows_in_front_of_the_first_token(w4):  # noqa: F811
+    # A length below a request's rows: the first ones see nothing, the others what there is, with any window.
+    s = Setup(w4, [9, 4], [9, 4], heads=4, kv=2, dim=64)
+    s.len_t = torch.tensor([2, 4], dtype=torch.int32, device="cuda")
+    s.prompt()
+    assert w4.w4a16_device_error() == w4.W4A16_ERR_INVALID_ARG
+    assert bool((s.out[:7] == 0).all()) and bool((s.out[7:] != 0).all())
+    want = s.out.clone(), s.lse.clone()
+    s.prompt(window=2**31 - 1)
+    assert w4.w4a16_device_error() == w4.W4A16_ERR_INVALID_ARG
+    assert torch.equal(s.out, want[0]) and torch.equal(s.lse, want[1])

@@ -231,7 +231,7 @@ __device__ __noinline__ Tile tile_of(const Params &p, const Seq &s, int least, i
     if (p.starts) {
         x.first = s.total - s.n + x.tok0 + 1;
         x.hi = max(x.first + x.toks - 1, 0);
-        x.lo = p.window > 0 ? max(0, x.first - p.window) : 0;
+        x.lo = p.window > 0 ? max(0, max(x.first, 0) - p.window) : 0;  // (rows in front of the first token see none: below 0)
         const int gap = gap_of<K>(s.own0);
         x.hi = placed_to(x.hi, s.own0, gap), x.lo = placed_from(x.lo, s.own0, gap);
     } else {
