@@ -102,3 +102,25 @@ def test_many_small_weights(w4, down):
     for token, at in zip(got, u.double().tolist()):
         before = upto[token - 1] if token else 0.0
         assert before / upto[-1] - bound(n) <= at <= upto[token] / upto[-1] + bound(n), (token, at)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,n", [(12, 50), (12, 3000)])
+def test_logits_further_apart_than_the_largest_float(w4, dtype, rows, n):
+    # With temperatures of their size they have weights all the same: e^-2 for the lowest at 3e38, all alike at infinity.
+    g = torch.Generator().manual_seed(n)
+    x = ((torch.rand(rows, n, generator=g) * 2 - 1) * 3.3e38).to(dtype)
+    x[:, 5] = 3.3e38
+    x[:, n - 3] = -3.3e38
+    heat = torch.tensor([3e38, float("inf"), 1e38, 3e37] * 3)
+    k = torch.tensor([0] * 8 + [n // 2] * 4, dtype=torch.int32)
+    p = torch.tensor([1.0] * 4 + [0.9] * 8)
+    m = torch.tensor([0.0] * 11 + [0.05])
+    u = (torch.arange(rows) + 0.4) / rows
+    got = w4.w4a16_sample(x.cuda(), u.cuda(), heat.cuda(), k.cuda(), p.cuda(), m.cuda()).tolist()
+    for r in range(rows):
+        want, near = sample(x[r].double().numpy(), float(u[r]), float(heat[r]), int(k[r]), float(p[r]), float(m[r]))
+        # At infinity every weight is the same number, so that sums are whole multiples of it on both sides (the product of u,
+        # 24 bits, and n is exact in 64): a border may be as near as it likes.
+        assert near > 2 * bound(n) or heat[r] == float("inf")
+        assert got[r] == want, r

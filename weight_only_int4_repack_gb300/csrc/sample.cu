@@ -104,6 +104,7 @@ template <>
 struct Logit<float> {
     using Raw = uint32_t;
     static __device__ __forceinline__ float value(Raw r) { return __uint_as_float(r); }
+    static __device__ __forceinline__ Raw half(Raw r) { return __float_as_uint(value(r) * 0.5f); }
     static __device__ __forceinline__ uint32_t key(Raw r) {
         if (r == 0x80000000u) r = 0;
         return r & 0x80000000u ? ~r : r | 0x80000000u;
@@ -113,6 +114,7 @@ template <typename H>
 struct Logit16 {
     using Raw = uint16_t;
     static __device__ __forceinline__ float value(Raw r) { return elem::pair_to_f32<H>(r).x; }
+    static __device__ __forceinline__ Raw half(Raw r) { return (Raw)elem::pair_from_f32<H>(value(r) * 0.5f, 0.f); }
     static __device__ __forceinline__ uint32_t key(Raw r) {
         if (r == 0x8000u) r = 0;
         return r & 0x8000u ? (uint32_t)(uint16_t)~r : r | 0x8000u;
@@ -395,6 +397,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     if (top == INFINITY) {  // these alone, all alike
         for (int i = tid; i < n; i += kThreads) mine[i] = L::value(mine[i]) == INFINITY ? (Raw)0 : kNone;
         top = 0.f;
+        __syncthreads();
+    }
+    // Differences to a largest logit beyond 2^100 may be no floats: such a row is halved, and its temperature. (Nothing that this
+    // rounds, below 2^-125, is told apart by a weight; fp16 has none of it.)
+    if (top > 0x1p100f) {
+        for (int i = tid; i < n; i += kThreads) mine[i] = L::half(mine[i]);
+        top *= 0.5f, heat *= 0.5f;
         __syncthreads();
     }
     Heat h;
