@@ -83,8 +83,9 @@ class Decoder:
         # What sampling goes by (its random numbers are the caller's, anew before each step).
         kinds = dict(temperature=torch.float32, top_k=i32, top_p=torch.float32, min_p=torch.float32)
         self.sampling = sampling and {n: torch.full((batch,), x, dtype=kinds[n], device="cuda") for n, x in sampling.items()}
-        # The step's buffers.
-        self.tokens = torch.randint(0, vocab, (batch,), device="cuda", generator=g)
+        # The step's buffers. tokens: what each request goes on with; -1 where logits that are none left nothing to draw
+        # (the request goes on with token 0 unless the caller ends it).
+        self.tokens, self.words = torch.randint(0, vocab, (batch,), device="cuda", generator=g), new(batch, dtype=torch.int64)
         self.uniform = torch.rand(batch, device="cuda", generator=g)
         self.zero, self.h = new(batch, width, dtype=torch.float32), new(batch, width, dtype=torch.float32)
         self.x, self.n, self.y = new(batch, width), new(batch, width), new(batch, width)
@@ -98,7 +99,8 @@ class Decoder:
         w4.w4a16_kv_extend(self.lens, self.new, self.table, self.free, self.free_count, PAGE, self.slots, self.positions,
                            self.refused, spacing=1)  # row b of everything stays request b's
         places = torch.add(self.positions, self.behind, out=self.places) if self.shared else self.positions
-        torch.index_select(self.embedding, 0, self.tokens, out=self.x)
+        words = self.tokens if self.sampling is None else torch.clamp(self.tokens, min=0, out=self.words)
+        torch.index_select(self.embedding, 0, words, out=self.x)
         self.rows(self.__dict__, places, self.slots, self.attend)
         w4.w4a16_gemm(self.n, *self.head, GROUP, out=self.logits)
         self.pick(self.logits, self.uniform, self.sampling, self.tokens)
@@ -133,7 +135,6 @@ class Decoder:
             torch.argmax(logits, 1, out=out)
         else:
             w4.w4a16_sample(logits, uniform, **sampling, out=out)
-            out.clamp_(min=0)  # -1: logits that are none, from which nothing can be drawn
 
     def many(self, tokens, positions, slots, table, starts, lens, **prefix):
         """The layers over many tokens of some requests; returns the rows that the head reads."""
@@ -235,7 +236,7 @@ def main():
     graph = model.capture()
     print(f"graph with launch overlap: {timed(graph.replay, n):.1f} us a step")
     w4.w4a16_set_launch_overlap(False)
-    assert w4.w4a16_device_error() == w4.W4A16_OK
+    assert w4.w4a16_device_error() == w4.W4A16_OK and int(model.tokens.min()) >= 0
     print(f"{a['batch']} requests of {int(model.lens[0])} tokens, {int(model.free_count)} pages free; "
           f"next tokens {model.tokens.tolist()}")
 
