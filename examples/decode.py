@@ -80,7 +80,7 @@ class Decoder:
         self.prefix_lens = new(prefixes, dtype=i32)
         self.prefix_of = torch.full((batch,), -1, dtype=i32, device="cuda")
         self.behind, self.places = new(batch, dtype=i32), new(batch, dtype=i32)
-        # What sampling goes by (its random numbers are the caller's, anew before each step).
+        # What sampling goes by (its random numbers are the caller's, anew before each step and each prompt).
         kinds = dict(temperature=torch.float32, top_k=i32, top_p=torch.float32, min_p=torch.float32)
         self.sampling = sampling and {n: torch.full((batch,), x, dtype=kinds[n], device="cuda") for n, x in sampling.items()}
         # The step's buffers. tokens: what each request goes on with; -1 where logits that are none left nothing to draw
@@ -227,6 +227,7 @@ def main():
         model.behind.fill_(prefix)
     if prompt:
         model.prompt({b: some(prompt) for b in range(a["batch"])})
+        model.uniform.uniform_()  # the prompts' draws have had theirs
     model.step()
     n = min(steps, (a["context"] - prompt) // 4)
     print(f"eager: {timed(model.step, n):.1f} us a step")
