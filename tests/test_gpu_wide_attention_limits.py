@@ -1,4 +1,6 @@
 """Attention of many rows at its limits: what lies in shared memory where a call begins, rows of a tile that are nobody's."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -42,15 +44,18 @@ def test_rows_that_are_nobody_s_change_nothing(w4, dim, dtype, new, pad):  # noq
         assert same == (True, True), level
 
 
-def check_scores_to_their_own_size(s, softcap):
-    """As Setup.check, for a cap that costs each score a few roundings of itself and nothing that goes by the cap."""
+def check_scores_to_their_own_size(s, expected, rows=None):
+    """As Setup.check, for scores that are off by a few roundings of themselves and nothing that goes by a cap: of all rows, or
+    of those named for each request (from its first one on)."""
     torch.cuda.synchronize()
     u, out, lse = U[s.dtype], f64(s.out), f64(s.lse)
-    for at, (want, want_lse, mag, top), n in s.want(s.dim**-0.5, 0, softcap):
+    for i, (at, (want, want_lse, mag, top), n) in enumerate(expected):
         # products' sum, then scale, quotient by the cap, tanh (2), product with the cap, difference, exponential
         eps = (s.dim + 24) * E * top + (n + 8) * E + 2.0**-22
         bound = u * np.abs(want) + 2 * (u + eps)[..., None] * mag + n * 2.0**-36 * (mag.max() + 1) + 2.0**-24
-        assert (np.abs(out[at] - want) <= bound).all() and (np.abs(lse[at] - want_lse) <= eps + 2 * E * np.abs(want_lse)).all()
+        some = slice(0, rows[i]) if rows else slice(None)
+        assert (np.abs(out[at] - want) <= bound)[some].all()
+        assert (np.abs(lse[at] - want_lse) <= eps + 2 * E * np.abs(want_lse))[some].all()
 
 
 @pytest.mark.parametrize("dim,dtype,cache", [(64, F16, F16), (128, BF16, BF16), (128, BF16, E4M3), (256, F16, F16)])
@@ -58,11 +63,11 @@ def check_scores_to_their_own_size(s, softcap):
 def test_large_caps(w4, softcap, dim, dtype, cache):  # noqa: F811
     s = Setup(w4, [3, 70], [200, 300], [100], [0, -1], heads=6, kv=2, dim=dim, dtype=dtype, cache=cache)
     s.prompt(softcap=softcap)
-    check_scores_to_their_own_size(s, softcap)
+    check_scores_to_their_own_size(s, s.want(dim**-0.5, 0, softcap))
     s = Setup(w4, [1] * 20, [1 + 7 * i for i in range(20)], [400], [-(i % 2) for i in range(20)], heads=6, kv=2, dim=dim, dtype=dtype,
               cache=cache)
     s.prefix(softcap=softcap)
-    check_scores_to_their_own_size(s, softcap)
+    check_scores_to_their_own_size(s, s.want(dim**-0.5, 0, softcap))
 
 
 def test_the_largest_window_of_rows_in_front_of_the_first_token(w4):  # noqa: F811
@@ -76,3 +81,22 @@ def test_the_largest_window_of_rows_in_front_of_the_first_token(w4):  # noqa: F8
     s.prompt(window=2**31 - 1)
     assert w4.w4a16_device_error() == w4.W4A16_ERR_INVALID_ARG
     assert torch.equal(s.out, want[0]) and torch.equal(s.lse, want[1])
+
+
+@pytest.mark.parametrize("cache,junk", [(F16, math.nan), (F16, math.inf), (F16, -math.inf), (F16, 65504.0), (F16, -65504.0),
+                                        (BF16, math.nan), (BF16, -math.inf), (E4M3, math.nan), (E4M3, -448.0)])
+@pytest.mark.parametrize("dim", [128, 256])
+def test_what_only_other_rows_see_is_not_seen(w4, cache, junk, dim):  # noqa: F811
+    # As test_what_is_not_visible, every set of it with something to find, and no error named.
+    s = Setup(w4, [40, 7], [300, 130], [70], [0, -1], heads=10, kv=2, dim=dim, dtype=BF16 if cache == BF16 else F16, cache=cache)
+    expected = s.want(dim**-0.5)
+    hidden = torch.ones(s.pages, s.page, dtype=torch.bool)
+    for row, n in ((s.table[0], 297), (s.table[1], 129), (s.ptable[0], 70)):  # all but the last 3 and the last 1 tokens
+        for j in range(n):
+            hidden[int(row[j // 16]), j % 16] = False
+    for pool in (s.k, s.v):
+        x = pool.float()
+        x[hidden.cuda()] = junk
+        pool.copy_(x.to(cache))
+    s.prompt()
+    check_scores_to_their_own_size(s, expected, rows=(37, 6))
