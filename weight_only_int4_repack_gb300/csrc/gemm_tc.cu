@@ -40,6 +40,7 @@
 #include <tuple>
 
 #include "ptx.cuh"
+#include "tc5.cuh"
 #include "w4a16_internal.h"
 
 namespace w4a16 {
@@ -65,92 +66,12 @@ struct TcShape {
     static_assert(STAGES == ASTAGES, "one barrier frees a shared-memory stage and its tensor-memory A stage");
 };
 
-// ------------------------------------------------------------------ tcgen05
-__device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t ncols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(ptx::smem_u32(slot)),
-                 "r"(ncols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// D[tmem] (+)= A[tmem] * B[smem desc]^T, kind::f16, one CTA.
-__device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// Arrive on `bar` once every tcgen05 operation this thread issued so far is complete.
-__device__ __forceinline__ void tc_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     ptx::smem_u32(bar))
-                 : "memory");
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
 template <int N>
 __device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[N]) {
     static_assert(N == 8 || N == 16 || N == 32, "8, 16 or 32 columns");
-    if constexpr (N == 32) tmem_st32(taddr, r);
-    else if constexpr (N == 16) tmem_st16(taddr, r);
-    else tmem_st8(taddr, r);
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
-// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups 1024 B apart.
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);          // start address
-    d |= (uint64_t)1u << 16;                           // leading byte offset (unused for this layout)
-    d |= (uint64_t)(1024u >> 4) << 32;                 // stride byte offset: 8 rows x 128 B
-    d |= (uint64_t)1u << 46;                           // descriptor version for tcgen05
-    d |= (uint64_t)2u << 61;                           // layout: 128-byte swizzle
-    return d;
-}
-
-// Instruction descriptor, kind::f16: fp16 A and B (K-major), fp32 D, M = 128, N = n.
-__host__ __device__ constexpr uint32_t idesc_f16(int n) {
-    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+    if constexpr (N == 32) tc5::st32(taddr, r);
+    else if constexpr (N == 16) tc5::st16(taddr, r);
+    else tc5::st8(taddr, r);
 }
 
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
@@ -254,10 +175,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 0;
         ptx::mbar_init_fence();
     }
-    if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
-    tc_fence_before();
+    if (warp == 1) tc5::alloc(tmem_slot, kTmemCols);
+    tc5::fence_before();
     __syncthreads();
-    tc_fence_after();
+    tc5::fence_after();
     const uint32_t tmem = *tmem_slot;
     // Tensor-memory columns: accumulators (T per set), then ASTAGES x NS x 32 A columns.
     const uint32_t acc_col = 0;
@@ -304,11 +225,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // period: descriptors and tensor-memory addresses advance by constant steps
         // and the stage counters run without divisions.
         if (lane == 0) {
-            const uint32_t idesc = idesc_f16(T);
+            const uint32_t idesc = tc5::idesc(false, T, false, false);
             // Start-address field of the descriptor in 16-byte units: +b_stage/16 per
             // stage, +2 per k16 step (32 bytes); shared addresses stay below 2^18, so
             // the 14-bit field never carries.
-            const uint64_t bdesc0 = smem_desc_sw128(ptx::smem_u32(smem));
+            const uint64_t bdesc0 = tc5::desc_sw128(ptx::smem_u32(smem), 16, 1024);
             const uint32_t bstage = (uint32_t)(L.b_stage >> 4);
             const uint32_t d_acc = tmem + acc_col, a_base0 = tmem + a_col0;
             int kb = 0, s = 0;  // stage of both rings
@@ -318,26 +239,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // this stage's copies (weights and activations alike), so a completed
                 // afull phase implies a completed full phase: no second wait here.
                 if (!ptx::mbar_wait(&afull[s], ph, abort_flag, p.err, p.wait_ns)) break;
-                tc_fence_after();
+                tc5::fence_after();
                 const uint64_t bdesc = bdesc0 + (uint64_t)((uint32_t)s * bstage);
                 const uint32_t a_base = a_base0 + (uint32_t)(s * NS * 32);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
 #pragma unroll
                     for (int w = 0; w < NS; ++w)
-                        tc_mma(d_acc + (uint32_t)(w * T), a_base + (uint32_t)(w * 32 + 8 * j), bdesc + 2u * j, idesc,
+                        tc5::mma_ts(d_acc + (uint32_t)(w * T), a_base + (uint32_t)(w * 32 + 8 * j), bdesc + 2u * j, idesc,
                                (kb > 0 || j > 0) ? 1u : 0u);
                 }
-                tc_commit(&empty[s]);  // frees the shared-memory and tensor-memory stages
+                tc5::commit(&empty[s]);  // frees the shared-memory and tensor-memory stages
                 if (++s == STAGES) {
                     s = 0;
                     ph ^= 1u;
                 }
             }
             if (kb == nkb) {
-                tc_commit(accfull);
+                tc5::commit(accfull);
             } else {  // aborted: wait (bounded) for the MMAs already issued
-                tc_commit(drain);
+                tc5::commit(drain);
                 volatile int no_abort = 0;
                 ptx::mbar_wait(drain, 0u, &no_abort, nullptr, 200000000ull);
             }
@@ -420,8 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t ta = tmem + lane_base + a_col0 + (uint32_t)((s * NS + w) * 32);
                 tmem_st_cols(ta, col);
             }
-            tmem_wait_st();
-            tc_fence_before();
+            tc5::wait_st();
+            tc5::fence_before();
             ptx::mbar_arrive(&afull[s]);
             if (kbn < nkb) {
 #pragma unroll
@@ -438,11 +359,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool acc_ok = !aborted && ptx::mbar_wait(accfull, 0u, abort_flag, p.err, p.wait_ns);
         if constexpr (!SWIGLU) {
             if (acc_ok) {
-                tc_fence_after();
+                tc5::fence_after();
                 for (int c0 = 16 * hf; c0 < T; c0 += 16 * kDqParts) {
                     uint32_t v[16];
-                    tmem_ld16(tmem + lane_base + acc_col + (uint32_t)c0, v);
-                    tmem_wait_ld();
+                    tc5::ld16(tmem + lane_base + acc_col + (uint32_t)c0, v);
+                    tc5::wait_ld();
                     if (row_ok) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
@@ -457,12 +378,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             // output column n: exchange half of each 16-token chunk with lane r ^ 16,
             // then the gate lane finishes tokens 0-7 and the up lane tokens 8-15.
             if (acc_ok) {
-                tc_fence_after();
+                tc5::fence_after();
                 const bool gate_lane = (lane & 16) == 0;
                 for (int c0 = 16 * hf; c0 < T; c0 += 16 * kDqParts) {
                     uint32_t v[16];
-                    tmem_ld16(tmem + lane_base + acc_col + (uint32_t)c0, v);
-                    tmem_wait_ld();
+                    tc5::ld16(tmem + lane_base + acc_col + (uint32_t)c0, v);
+                    tc5::wait_ld();
                     const int mb = m0 + c0 + (gate_lane ? 0 : 8);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -476,11 +397,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
-    tc_fence_before();
+    tc5::fence_before();
     __syncthreads();
     if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        tc5::fence_after();
+        tc5::dealloc(tmem, kTmemCols);
     }
 }
 

@@ -87,14 +87,14 @@ void maps(wide::Params &p) {
     const w4a16_kv_cache &c = p.c;
     const int most = wide::rows_of(c.head_dim), gb = p.group < most ? p.group : most;
     p.q_tma = p.starts && p.scale != 0.f && c.type != W4A16_TYPE_E4M3 &&
-              wide::tensor_map(&p.q_map, p.q, {c.head_dim, p.heads, p.rows, 1}, {p.q_head, p.q_row, 0}, {64, gb, most / gb, 1});
+              tmap_boxes(&p.q_map, p.q, {c.head_dim, p.heads, p.rows, 1}, {p.q_head, p.q_row, 0}, {64, gb, most / gb, 1});
     // Boxes of whole groups of 8 keys (the swizzle's rows), at most those that one warp brings.
     int rows = wide::keys_of(c.head_dim) / 4;
     while (rows >= 8 && c.page_size % rows) rows /= 2;
     p.kv_rows = 0;
     if (rows >= 8 && c.type != W4A16_TYPE_E4M3 &&
-        wide::tensor_map(&p.k_map, c.k, {c.head_dim, c.page_size, c.kv_heads, c.pages}, {c.k_token, c.k_head, c.k_page}, {64, rows, 1, 1}) &&
-        wide::tensor_map(&p.v_map, c.v, {c.head_dim, c.page_size, c.kv_heads, c.pages}, {c.v_token, c.v_head, c.v_page}, {64, rows, 1, 1}))
+        tmap_boxes(&p.k_map, c.k, {c.head_dim, c.page_size, c.kv_heads, c.pages}, {c.k_token, c.k_head, c.k_page}, {64, rows, 1, 1}) &&
+        tmap_boxes(&p.v_map, c.v, {c.head_dim, c.page_size, c.kv_heads, c.pages}, {c.v_token, c.v_head, c.v_page}, {64, rows, 1, 1}))
         p.kv_rows = rows;
 }
 

@@ -1,5 +1,5 @@
-// tcgen05 and tensor memory for the attention of many rows (wide_attention.cuh):
-// inline PTX, written from the PTX ISA. One CTA issues (cta_group::1), kind::f16,
+// tcgen05 and tensor memory for the projections of many tokens (gemm_tc.cu) and the
+// attention of many rows (wide_attention.cuh): inline PTX, written from the PTX ISA. One CTA issues (cta_group::1), kind::f16,
 // M = 128, accumulators in fp32.
 #pragma once
 
@@ -80,6 +80,11 @@ __device__ __forceinline__ void st16(uint32_t at, const uint32_t (&r)[16]) {
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+__device__ __forceinline__ void st8(uint32_t at, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 // Matrix in shared memory with the 128-byte swizzle, as atoms of 8 rows of 128 bytes

@@ -1,6 +1,7 @@
-// Tensor-map (TMA descriptor) encoding with a per-process cache.
+// Tensor-map (TMA descriptor) encoding: of the projections' operands with a
+// per-process cache, of attention's queries and pages for each call anew.
 //
-// A call's tensor maps depend only on the buffer address, its shape and the
+// A projection's tensor maps depend only on the buffer address, its shape and the
 // box the kernel copies, so they are encoded once and reused: repeated calls on
 // the same buffers (the common case: weights and activation buffers reused
 // every step) cost a hash lookup instead of a driver call.
@@ -117,6 +118,24 @@ bool tmap_activations_kblocks(CUtensorMap *out, const __half *A, int M, int K, i
     d.box[2] = (uint32_t)kblocks_box;
     d.swizzle128 = 1;
     return encode_tmap(out, d);
+}
+
+bool tmap_boxes(CUtensorMap *out, const void *base, const std::array<long long, 4> &dims, const std::array<long long, 3> &strides,
+                const std::array<int, 4> &box) {
+    const auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t d[4], s[3];
+    cuuint32_t b[4], each[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 4; ++i) {
+        if (dims[i] <= 0 || box[i] <= 0 || box[i] > 256) return false;
+        d[i] = (cuuint64_t)dims[i], b[i] = (cuuint32_t)box[i];
+    }
+    for (int i = 0; i < 3; ++i) s[i] = dims[i + 1] > 1 ? (cuuint64_t)strides[i] * 2 : 16;
+    for (int i = 0; i < 3; ++i)
+        if (s[i] == 0 || s[i] % 16) return false;
+    std::memset(out, 0, sizeof(*out));
+    return fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(base), d, s, b, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace w4a16

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <array>
+
 #include "../../include/w4a16.h"
 
 namespace w4a16 {
@@ -56,7 +58,8 @@ struct TcParams {
 };
 
 // ---------------------------------------------------------------------------
-// Tensor maps (TMA descriptors), encoded once per buffer and shape and cached.
+// Tensor maps (TMA descriptors): those of TmapDesc are encoded once per buffer and
+// shape and cached.
 // ---------------------------------------------------------------------------
 struct TmapDesc {
     const void *ptr;
@@ -77,6 +80,12 @@ bool tmap_activations(CUtensorMap *out, const __half *A, int M, int K, int rows_
 // The same activations as (64 k, token, k-block): one box brings `kblocks_box`
 // consecutive k-blocks of rows_box tokens, laid out k-block after k-block.
 bool tmap_activations_kblocks(CUtensorMap *out, const __half *A, int M, int K, int rows_box, int kblocks_box);
+// Boxes of box[0] x box[1] x box[2] x box[3] of a tensor of 16-bit elements whose
+// innermost dimension is contiguous, 128-byte swizzle; not cached. Strides in
+// elements; that of a dimension of one entry says nothing. False where the tensor
+// or the box allows none.
+bool tmap_boxes(CUtensorMap *out, const void *base, const std::array<long long, 4> &dims,
+                const std::array<long long, 3> &strides, const std::array<int, 4> &box);
 
 // Number of SMs of the current device (cached per device, thread-safe).
 int sm_count();

@@ -46,7 +46,6 @@
 
 #include <cuda.h>
 
-#include <array>
 #include <cmath>
 #include <type_traits>
 
@@ -1583,10 +1582,6 @@ cudaError_t launch_dims(Which which, const Params &p, cudaStream_t s) {
     if (p.c.head_dim <= 128) return launch<T, C, 128>(which, p, s);
     return launch<T, C, 256>(which, p, s);
 }
-
-// Defined in wide_tmap.cu.
-bool tensor_map(CUtensorMap *out, const void *base, const std::array<long long, 4> &dims, const std::array<long long, 3> &strides,
-                const std::array<int, 4> &box);
 
 // A head's width as the kernels have it, the rows of a tile, the keys of a unit.
 inline int dim_of(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
