@@ -56,8 +56,8 @@ struct Params {
     float *lse;
     unsigned int *counters;  // [3][kMaxCtas], zero between calls
     float *partial;          // [CTAs][2][kMaxPartial]
-    // Where another kernel joins the results with more tokens of the requests (prefix attention): outputs in fp32,
-    // [batch * heads][head_dim], and log2 of the sums of weights, in place of out and lse; nullptr otherwise.
+    // Of kernels for sums: outputs in fp32, [batch * heads][head_dim], and log2 of the sums of weights, in place of out
+    // and lse.
     float *raw, *raw_lse;
     int max_pages, batch, heads, group, head_blocks, window;
     int one_page;  // page_size is a multiple of 16
@@ -80,8 +80,12 @@ constexpr float kSlack = 4.f, kLowest = -3.402823466e38f;
 template <typename M>
 constexpr float kUpOf = std::is_same<M, __half>::value ? 11.f : -kSlack;
 
-template <typename T, typename C, int DT, int NT>
+// kRaw: for sums, which another kernel joins with more tokens of the requests (prefix attention). Kernels of their own: where
+// it was asked in one kernel, the others' calls took 1 to 2% longer (one request of 1000 tokens 8.04 -> 8.20 us, 121 over an
+// 8-bit cache 107.3 -> 108.5).
+template <typename T, typename C, int DT, int NT, bool R>
 struct Config {
+    static constexpr bool kRaw = R;
     using M = typename std::conditional<sizeof(C) == 1, __half, T>::type;  // operand type
     static constexpr float kUp = kUpOf<M>;
     static constexpr int kDim = DT;                        // head_dim, rounded up
@@ -305,17 +309,17 @@ struct Ends {
         constexpr float kLn2 = 0.6931471805599453f;
         const bool any = j.l > 0.f || j.l != j.l;
         const float f = any ? v_scale / j.l : 0.f;
-        if (p.raw) {
+        if constexpr (K::kRaw) {
             const long long at = (long long)seg.b * p.heads + seg.h0 + row;
             *reinterpret_cast<float4 *>(p.raw + at * p.c.head_dim + d) = make_float4(j.o.x * f, j.o.y * f, j.o.z * f, j.o.w * f);
             if (d == 0) p.raw_lse[at] = any ? j.m + log2f(j.l) - K::kUp : -INFINITY;
-            return;
+        } else {
+            T *out = static_cast<T *>(p.out) + seg.b * p.o_row + (seg.h0 + row) * p.o_head + d;
+            *reinterpret_cast<uint2 *>(out) =
+                make_uint2(elem::pair_from_f32<T>(j.o.x * f, j.o.y * f), elem::pair_from_f32<T>(j.o.z * f, j.o.w * f));
+            if (p.lse && d == 0)
+                p.lse[(long long)seg.b * p.heads + seg.h0 + row] = any ? (j.m + log2f(j.l) - K::kUp) * kLn2 : -INFINITY;
         }
-        T *out = static_cast<T *>(p.out) + seg.b * p.o_row + (seg.h0 + row) * p.o_head + d;
-        *reinterpret_cast<uint2 *>(out) =
-            make_uint2(elem::pair_from_f32<T>(j.o.x * f, j.o.y * f), elem::pair_from_f32<T>(j.o.z * f, j.o.w * f));
-        if (p.lse && d == 0)
-            p.lse[(long long)seg.b * p.heads + seg.h0 + row] = any ? (j.m + log2f(j.l) - K::kUp) * kLn2 : -INFINITY;
     }
     // The place of the i-th partial result of these heads.
     __device__ __forceinline__ float *part(int i) const {
@@ -459,9 +463,10 @@ __device__ __forceinline__ void join_parts(const Params &p, const Segment *open,
     }
 }
 
-template <typename T, typename C, int DT, int NT>
-__global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, DT, NT>::kPerSm) paged_attention_kernel(const __grid_constant__ Params p) {
-    using K = Config<T, C, DT, NT>;
+template <typename T, typename C, int DT, int NT, bool R>
+__global__ void __launch_bounds__(Config<T, C, DT, NT, R>::kThreads, Config<T, C, DT, NT, R>::kPerSm)
+    paged_attention_kernel(const __grid_constant__ Params p) {
+    using K = Config<T, C, DT, NT, R>;
     constexpr bool k8 = sizeof(C) == 1;
     using M = typename K::M;
     constexpr float kUp = K::kUp;
@@ -534,14 +539,12 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
         if (tid == 0 && (p.lens[b] < 0 || p.lens[b] > (long long)p.max_pages * p.c.page_size))
             atomicExch(p.err, (unsigned int)W4A16_ERR_INVALID_ARG);
         if (r.hi > r.lo) continue;
-        if (p.raw) {
-            for (int i = tid; i < p.heads; i += K::kThreads) p.raw_lse[(long long)b * p.heads + i] = -INFINITY;
-            continue;
-        }
-        for (int i = tid; i < p.heads * D; i += K::kThreads)
-            static_cast<T *>(p.out)[b * p.o_row + (i / D) * p.o_head + i % D] = T(0.f);
-        if (p.lse)
-            for (int i = tid; i < p.heads; i += K::kThreads) p.lse[(long long)b * p.heads + i] = -INFINITY;
+        if constexpr (!K::kRaw)
+            for (int i = tid; i < p.heads * D; i += K::kThreads)
+                static_cast<T *>(p.out)[b * p.o_row + (i / D) * p.o_head + i % D] = T(0.f);
+        float *lse = K::kRaw ? p.raw_lse : p.lse;
+        if (lse)
+            for (int i = tid; i < p.heads; i += K::kThreads) lse[(long long)b * p.heads + i] = -INFINITY;
     }
     if (D < DT)  // the ring's columns beyond head_dim stay zero
         for (int i = tid; i < K::kWarps * K::kRing / 16; i += K::kThreads)
@@ -979,10 +982,10 @@ __global__ void __launch_bounds__(Config<T, C, DT, NT>::kThreads, Config<T, C, D
     join_parts<K, T>(p, open, arrived, k8, reinterpret_cast<float *>(smem), meet[0], last);
 }
 
-template <typename T, typename C, int DT, int NT>
+template <typename T, typename C, int DT, int NT, bool R>
 cudaError_t launch(Params p, int sms, cudaStream_t s) {
-    using K = Config<T, C, DT, NT>;
-    auto kernel = paged_attention_kernel<T, C, DT, NT>;
+    using K = Config<T, C, DT, NT, R>;
+    auto kernel = paged_attention_kernel<T, C, DT, NT, R>;
     cudaError_t e = ensure_max_dyn_smem((const void *)kernel, K::kSmem);
     if (e != cudaSuccess) return e;
     p.k_page = (unsigned int)p.c.k_page, p.k_token = (unsigned int)p.c.k_token;
@@ -1004,12 +1007,16 @@ cudaError_t launch(Params p, int sms, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <typename T, typename C>
+template <bool R, typename T, typename C>
 cudaError_t launch_dims(const Params &p, int sms, cudaStream_t s) {
     const bool two = p.group > 8;
-    if (p.c.head_dim <= 64) return two ? launch<T, C, 64, 2>(p, sms, s) : launch<T, C, 64, 1>(p, sms, s);
-    if (p.c.head_dim <= 128) return two ? launch<T, C, 128, 2>(p, sms, s) : launch<T, C, 128, 1>(p, sms, s);
-    return launch<T, C, 256, 1>(p, sms, s);
+    if (p.c.head_dim <= 64) return two ? launch<T, C, 64, 2, R>(p, sms, s) : launch<T, C, 64, 1, R>(p, sms, s);
+    if (p.c.head_dim <= 128) return two ? launch<T, C, 128, 2, R>(p, sms, s) : launch<T, C, 128, 1, R>(p, sms, s);
+    return launch<T, C, 256, 1, R>(p, sms, s);
+}
+template <bool R, typename T>
+cudaError_t launch_caches(const Params &p, int sms, cudaStream_t s) {
+    return p.c.type == W4A16_TYPE_E4M3 ? launch_dims<R, T, E4M3>(p, sms, s) : launch_dims<R, T, T>(p, sms, s);
 }
 
 // Checks a call's arguments as w4a16_paged_attention does, and fills `p` with them. Defined in paged_attention.cu.
@@ -1018,9 +1025,11 @@ w4a16_status fill(Params &p, const void *q, w4a16_type type, long long q_row, lo
                   float scale, int window, float softcap, void *out, long long o_row, long long o_head, float *lse, void *ws,
                   size_t ws_bytes);
 
-// Defined in paged_attention_f16.cu and paged_attention_bf16.cu.
+// Defined in paged_attention_f16.cu, paged_attention_bf16.cu and, for sums, paged_attention_sums_f16.cu and _bf16.cu.
 cudaError_t launch_f16(const Params &p, int sms, cudaStream_t s);
 cudaError_t launch_bf16(const Params &p, int sms, cudaStream_t s);
+cudaError_t launch_sums_f16(const Params &p, int sms, cudaStream_t s);
+cudaError_t launch_sums_bf16(const Params &p, int sms, cudaStream_t s);
 
 }  // namespace attn
 }  // namespace w4a16

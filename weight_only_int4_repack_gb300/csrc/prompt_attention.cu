@@ -192,7 +192,7 @@ w4a16_status w4a16_prefix_attention(const void *q, w4a16_type type, long long q_
     cudaStream_t s = (cudaStream_t)stream;
     const auto launch = type == W4A16_TYPE_F16 ? wide::launch_f16 : wide::launch_bf16;
     cudaError_t e = launch(wide::kWide, p, s);
-    if (e == cudaSuccess) e = type == W4A16_TYPE_F16 ? attn::launch_f16(o, sm_count(), s) : attn::launch_bf16(o, sm_count(), s);
+    if (e == cudaSuccess) e = type == W4A16_TYPE_F16 ? attn::launch_sums_f16(o, sm_count(), s) : attn::launch_sums_bf16(o, sm_count(), s);
     return from_cuda(e != cudaSuccess ? e : launch(wide::kPrefixJoin, p, s));
 }
 
