@@ -652,7 +652,7 @@ w4a16_status w4a16_prompt_attention(const void *q, w4a16_type type, long long q_
  * requests share prefixes: request b sees the tokens of prefix prefix_of[b] and then its
  * own lens[b] (the new one counted). What the requests of a prefix see of it is computed
  * for all of them together, so a prefix's keys and values are read once for up to 256
- * query heads that share them, not once a request.
+ * query heads that share them (128 where heads are wider than 128), not once a request.
  * Arguments as above, with one row of q and out for each request; prefixes > 0. A request
  * without a token of its own (lens[b] <= 0) gets out = 0 and lse = -inf; one without a
  * prefix is as in w4a16_paged_attention. A window counts over prefix and own tokens.
@@ -739,8 +739,8 @@ w4a16_status w4a16_prefix_attention_block(const w4a16_prefix_attention_args *arg
  *   logits  device, `type` (F16, BF16 or F32), [rows][vocab], rows `row` elements apart
  *   uniform device fp32 [rows]: u, from 0 to 1
  *   temperature, top_p, min_p  device fp32 [rows], top_k device int32 [rows]; any may be
- *           NULL. T = 0: the largest logit, the first of equal ones; top_k <= 0, top_p >= 1,
- *           min_p <= 0: not wanted (NULL: T = 1, none wanted)
+ *           NULL. T = 0, top_p <= 0 or min_p > 1: the largest logit, the first of equal
+ *           ones; top_k <= 0, top_p >= 1, min_p <= 0: not wanted (NULL: T = 1, none wanted)
  *   out     device int64 [rows]: the token, or -1 in a row without a logit above minus
  *           infinity. NaN counts as minus infinity, and beside plus infinity nothing else
  *           is drawn

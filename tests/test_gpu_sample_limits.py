@@ -124,3 +124,13 @@ def test_logits_further_apart_than_the_largest_float(w4, dtype, rows, n):
         # 24 bits, and n is exact in 64): a border may be as near as it likes.
         assert near > 2 * bound(n) or heat[r] == float("inf")
         assert got[r] == want, r
+
+
+def test_settings_that_leave_the_largest_logit_only(w4):
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(6, 5000, generator=g)
+    x[:, 4321] = x[:, 1234] = 9.0
+    f = lambda *v: torch.tensor(v, dtype=F32, device="cuda")  # noqa: E731
+    got = w4.w4a16_sample(x.cuda(), f(*[0.99] * 6), f(0, 1, 1, 1, 1, 1), torch.tensor([0, 1, 0, 0, 0, 0], dtype=torch.int32, device="cuda"),
+                          f(1, 1, 0, -2, 1, 1), f(0, 0, 0, 0, 1.5, 1))
+    assert got.tolist() == [1234] * 5 + [4321]  # of weights of 1 the second one, too, is at least 1

@@ -687,8 +687,8 @@ def w4a16_residual_rmsnorm(h, y, gamma=None, eps: float = 1e-5, post_gamma=None,
 def w4a16_sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None, out=None, stream=None):
     """The next token of each row of logits [rows, vocab] (float16, bfloat16 or float32) for the random numbers uniform
     (float32 [rows], from 0 to 1): int64 [rows], -1 where every logit is minus infinity. temperature, top_p, min_p
-    (float32 [rows]) and top_k (int32 [rows]) may be None; temperature 0 takes the largest logit, top_k <= 0, top_p >= 1
-    and min_p <= 0 leave a row alone. See include/w4a16.h."""
+    (float32 [rows]) and top_k (int32 [rows]) may be None; temperature 0, top_p <= 0 and min_p > 1 take the largest logit,
+    top_k <= 0, top_p >= 1 and min_p <= 0 leave a row alone. See include/w4a16.h."""
     if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError("w4a16_sample: logits [rows, vocab], rows contiguous")
     rows, vocab = logits.shape

@@ -17,12 +17,12 @@
 // they are gathered, and one CTA sorts them and draws; otherwise the border's bin is resolved (by sorting its tokens or, when
 // it holds many, by halving the range of its values) and one more pass sums and draws.
 //
-// What bounds it: instructions and barriers, not HBM. Cycles of a CTA of 37500 bf16 logits, two CTAs to an SM (256 rows of
-// 150001, top-p alone, 308 us, 11 of them the bytes; before weights took their present form, 336): logits and maximum 10000
-// to 22000, counts 14000, bounds and searches 15000, exact sums 30000 to 55000, the border's bin 25000, the last sums and the
-// draw 50000. Integer instructions, of which half as many are issued a cycle, set the pace of the passes. A single row of 32001 takes 18
-// us: launch 3, and a dozen steps of a barrier of the cluster and some dependent reads each. Sums of weights in the histogram
-// in place of counts (two shared atomics a logit) made 64 rows of 131072 128 us; with counts they are 85.
+// What bounds it: instructions and barriers, not HBM. Mean cycles of a CTA of 37500 bf16 logits, two CTAs to an SM (256 rows of
+// 150001, top-p alone, 315 us, 11 of them the bytes): logits and maximum 11000, counts 17000, bounds and searches 19000, exact
+// sums 47000, the search in them 7000, the border's bin 30000, the last sums and the draw 33000. 61% of all issue slots are
+// used, the rest is barriers' above all. A single row of 32001 takes 18 us: launch 3, and a dozen steps of a barrier of the
+// cluster and some dependent reads each. Sums of weights in the histogram in place of counts (two shared atomics a logit) made
+// 64 rows of 131072 128 us; with counts they are 82.
 #include <climits>
 #include <cmath>
 
@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 template <typename T>
 cudaError_t launch(SampleParams p, int rows, int sms, cudaStream_t s) {
     // CTAs of a row: as many as its tokens need room, and as many as there are SMs for (what a CTA does whatever it has costs
-    // as much as a pass over 10000 logits: 256 rows of 150001 took 342 us with 4 CTAs to a row, 463 with 8).
+    // as much as a pass over 10000 logits: 256 rows of 150001 took 342 us with 4 CTAs to a row, 463 with 8, in an earlier form).
     // (Two CTAs share an SM's 228 KB, of which each leaves 1 KB to the system.)
     const int room = (int)((113 * 1024 - sizeof(Shared<T>) - 64) / sizeof(T));
     int cluster = 1;

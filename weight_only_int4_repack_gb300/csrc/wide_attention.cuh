@@ -37,10 +37,11 @@
 // the output, 1500 more in a unit with masks. Code is kept small (rolled loops, waits out of
 // line): the roles together do not fit the first instruction caches, and what is rarely run
 // is fetched anew (an output's first time costs 7500 cycles).
-// 4099 rows of 40 heads over 8 kv heads of 128, bf16: 201 us, 0.86 PFLOP/s, 45% of a large
-// library product; 16 of it join the tiles that were cut (42 MB of sums, written and read). 13 packed prompts behind prefixes, e4m3, 16 heads to a kv head: 337 us,
-// 46%. 4 prompts of heads of 256 with a window and a cap: 119 us, 22% (the cap takes 2000 of
-// the 3900 cycles of a unit of 128 rows and 64 keys). 64 requests behind 16001 tokens: 97 us, of which 43 are the
+// 4099 rows of 40 heads over 8 kv heads of 128, bf16: 200 us, 0.86 PFLOP/s, 45% of a large
+// library product; 16 of it join the tiles that were cut (42 MB of sums, written and read).
+// 13 packed prompts behind prefixes, e4m3, 16 heads to a kv head: 333 us, 46%. 4 prompts of
+// heads of 256 with a window and a cap: 120 us, 22% (the cap takes 2000 of the 3900 cycles of
+// a unit of 128 rows and 64 keys). 64 requests behind 16001 tokens: 97 us, of which 43 are the
 // requests' own tokens, 8 the join.
 #pragma once
 
