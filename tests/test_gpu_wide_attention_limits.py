@@ -1,10 +1,12 @@
-"""Attention of many rows at its limits: what lies in shared memory where a call begins, rows of a tile that are nobody's."""
+"""Attention of many rows at its limits: what lies in shared memory where a call begins, rows of a tile that are nobody's,
+what only other rows see, large caps and windows, prompts of many thousand tokens."""
 import math
 
 import numpy as np
 import pytest
 import torch
 
+from oracle.wide_ops import rows_attention
 from test_gpu_wide_attention import BF16, E, E4M3, F16, Setup, U, f64, w4  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -100,3 +102,18 @@ def test_what_only_other_rows_see_is_not_seen(w4, cache, junk, dim):  # noqa: F8
         pool.copy_(x.to(cache))
     s.prompt()
     check_scores_to_their_own_size(s, expected, rows=(37, 6))
+
+
+@pytest.mark.parametrize("dim,dtype,cache,window", [(64, F16, F16, 0), (128, BF16, BF16, 0), (128, BF16, E4M3, 5000), (256, F16, F16, 0)])
+def test_prompts_of_many_thousand_tokens(w4, dim, dtype, cache, window):  # noqa: F811
+    n, before = 20011, 3000
+    s = Setup(w4, [n], [n + before], heads=4, kv=2, dim=dim, dtype=dtype, cache=cache, page=32)
+    s.prompt(window=window)
+    k, v = s.tokens(0)
+    rows = [0, 1, 127, 128, n - 2, n - 1, *np.random.RandomState(dim).randint(0, n, 60).tolist()]
+    got = s.out, s.lse, s.q
+    s.out, s.lse, s.q = (x[rows] for x in got)
+    check_scores_to_their_own_size(s, [
+        (slice(i, i + 1), rows_attention(f64(s.q[i:i + 1]), k[:before + r + 1], v[:before + r + 1], before + r, dim**-0.5, window),
+         before + r + 1) for i, r in enumerate(rows)])
+    assert bool((got[0] != 77.0).any(2).all()) and bool((got[1] != 55.0).all())
